@@ -1,0 +1,170 @@
+// Shared by the paged-cache kernels: arguments, visibility, page lookup, TMA box
+// loads from the pools and the 16-bit helpers of both data types.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "dkv_internal.cuh"
+
+namespace dkv {
+
+// What every paged kernel knows of the cache (passed by value).
+struct PagedArgs {
+  int B, Hq, Hkv, G, page_shift, page_mask, n_pages, max_pages, cap;  // cap: tokens a page-table row reaches
+  int window, sinks;
+  float scale_log2;  // log2(e) / sqrt(d)
+  int64_t stride_page, stride_head, stride_token;  // elements
+  const int32_t* __restrict__ table;
+  const int32_t* __restrict__ lens;
+  uint32_t* err;
+};
+
+// tokens of sequence b, brought into [0, cap]
+__device__ inline int paged_len(const PagedArgs& a, int b) {
+  const int n = __ldg(a.lens + b);
+  if (n < 0 || n > a.cap) raise_error(a.err, DKV_DEVERR_INDEX);
+  return min(max(n, 0), a.cap);
+}
+
+// first token of the sliding window of a query at position p (0 without a window)
+__device__ inline int paged_window_lo(const PagedArgs& a, int p) {
+  return a.window > 0 ? max(0, p - a.window + 1) : 0;
+}
+
+// Page of token t of sequence b; n_pages (a box outside the pool, which a TMA load
+// fills with zeros) for a page index that is out of range.
+__device__ inline int paged_page(const PagedArgs& a, int b, int t) {
+  const int page = __ldg(a.table + (size_t)b * a.max_pages + (t >> a.page_shift));
+  if (page >= 0 && page < a.n_pages) return page;
+  raise_error(a.err, DKV_DEVERR_INDEX);
+  return a.n_pages;
+}
+
+// ---------------------------------------------------------------------------
+// Tiles in shared memory: per 64 channels a sub-tile of `rows` rows x 128 bytes,
+// written by TMA boxes under the 128-byte swizzle (16-byte chunk index XOR row % 8;
+// sub-tiles start on 1024-byte boundaries), so that eight rows of one chunk lie in
+// eight different bank groups for ldmatrix and tcgen05.mma alike.
+// ---------------------------------------------------------------------------
+__device__ inline uint32_t sw128(uint32_t rows, uint32_t row, uint32_t chunk) {  // chunk: 8 channels
+  return (chunk >> 3) * rows * 128u + row * 128u + (((chunk & 7u) ^ (row & 7u)) << 4);
+}
+
+// one box {64 channels, box rows} of head h of a pool: x = first channel (0 or 64), y = slot
+__device__ inline void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int h, int page, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(h), "r"(page), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ inline void tma_prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// fp16 / bf16
+// ---------------------------------------------------------------------------
+template <typename T>
+struct Num;
+template <>
+struct Num<__half> {
+  static constexpr uint32_t kUmma = 0;  // operand format field of the tcgen05 instruction descriptor
+  static __device__ inline float to_float(__half x) { return __half2float(x); }
+  static __device__ inline __half from_float(float x) { return __float2half_rn(x); }
+  static __device__ inline uint32_t pack(float lo, float hi) { return pack_half2(lo, hi); }
+  static __device__ inline void split(float x, float y, uint32_t& hi, uint32_t& lo) { split_half2(x, y, hi, lo); }
+  static __device__ inline void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    mma16816(c, a0, a1, a2, a3, b0, b1);
+  }
+};
+template <>
+struct Num<__nv_bfloat16> {
+  static constexpr uint32_t kUmma = 1;
+  static __device__ inline float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+  static __device__ inline __nv_bfloat16 from_float(float x) { return __float2bfloat16_rn(x); }
+  static __device__ inline uint32_t pack(float lo, float hi) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+  // hi + lo carries 16 bits of each value
+  static __device__ inline void split(float x, float y, uint32_t& hi, uint32_t& lo) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    const float2 f = __bfloat1622float2(h);
+    hi = *reinterpret_cast<uint32_t*>(&h);
+    lo = pack(x - f.x, y - f.y);
+  }
+  static __device__ inline void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
+};
+
+__device__ inline uint4 ldsm_x4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ inline uint4 ldsm_x4_trans(uint32_t addr) {
+  uint4 v;
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ inline void sts128(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// launchers
+// ---------------------------------------------------------------------------
+struct PagedMaps {  // tensor maps of the pools: boxes of 64 channels x min(page_size, 64) slots
+  CUtensorMap k, v;
+};
+
+// decode: workspace [header][records: two per CTA, fp32 m[8] l[8] o[d][8]][scores fp32 [units][cap][8]]
+size_t paged_decode_ws_bytes(const PagedArgs& a, int d, bool with_weights);
+cudaError_t launch_paged_decode(const PagedArgs& a, int d, int dtype, const PagedMaps& m, const void* q,
+                                const dkv_strides& qs, void* out, float* lse, float* weights, uint8_t* ws,
+                                cudaStream_t s);
+cudaError_t launch_paged_append(const PagedArgs& a, int d, const void* K, const void* V, const dkv_strides& ns,
+                                int n_new, const int32_t* pos, const int32_t* counts, void* k_pool, void* v_pool,
+                                cudaStream_t s);
+// prefill and weights: qmap boxes of 64 channels x 128 tokens of q (weights: x paged_weights_rows(Tq))
+struct PagedQuery {
+  const void* q;
+  dkv_strides qs;
+  int Tq;
+  const int32_t* q_lens;
+};
+cudaError_t launch_paged_prefill(const PagedArgs& a, int d, int dtype, const PagedMaps& m, const CUtensorMap& qmap,
+                                 const PagedQuery& q, const void* v_pool, const void* k_pool, void* out,
+                                 const dkv_strides& os, float* lse, cudaStream_t s);
+int paged_weights_rows(int Tq);
+cudaError_t launch_paged_weights(const PagedArgs& a, int d, int dtype, const CUtensorMap& kmap, const CUtensorMap& qmap,
+                                 const PagedQuery& q, const float* lse, float* weights, cudaStream_t s);
+// evict: workspace [header][kept counts int32 [B]]
+size_t paged_evict_ws_bytes(const PagedArgs& a);
+struct PagedEvict {
+  int budget, first, recent, new_max_pages;
+  const float* weights;
+  const int32_t* new_table;
+  int32_t* kept;
+  int32_t* new_lens;
+  float* new_weights;
+};
+cudaError_t launch_paged_evict(const PagedArgs& a, int d, const PagedEvict& e, void* k_pool, void* v_pool, uint8_t* ws,
+                               cudaStream_t s);
+
+}  // namespace dkv

@@ -1,0 +1,411 @@
+// dkv_paged_prefill: causal attention of the last tokens of each sequence over a paged cache,
+// with an optional sliding window and sinks, on the tcgen05 tensor cores.
+//
+// A CTA owns two groups of 128 query rows that share every K and V tile: two heads of one
+// KV head at the same tokens where the group size is even, else 256 tokens of one head.  Per
+// 128-key tile j and group g
+//   S_g = Q_g K_j^T   M = 128 queries, N = 128 keys       (128 TMEM columns)
+//   O_g += P_g V_j    M = 128, N = d, P from TMEM (16-bit, over the first 64 columns of S_g)
+// One row per softmax thread (warps 0-3 group A, 4-7 group B); the tiles come through a ring of
+// 128-row slots (K_0, V_0, K_1, ...) filled with TMA boxes by warp 8, one box per page and 64
+// channels; lane 0 of warps 9 and 10 issue the products of groups A and B.  While one group's
+// rows turn S into P, the tensor cores run the other group's products.  P is handed over in two
+// halves of 64 keys, so that half of its product runs under the other half's exponentials.
+// S_{j+1} overwrites P_j, so it is issued once O_j is done; the arrival on S_{j+1} then also
+// says that O may be rescaled.  The row maximum moves only when a score exceeds it by kPfSlack
+// (base 2), and only then is O rescaled in tensor memory.
+//
+// P is rounded once to the type of V.  The output is rounded to that type too, and the error of
+// p enters it with about the same size: sqrt(2) of the unavoidable error instead of twice the
+// work for P V.  For fp16 p is scaled by 2^7 first, which keeps weights down to e^-14 of the
+// largest normal; the scale cancels in the division.
+//
+// Tiles in which some row sees a key that another does not (the diagonal, the window's edge, the
+// sinks' end) go past warp 11 first: it zeroes the V rows that no row of the CTA sees, and, since
+// a masked weight of 0 would still carry a NaN or infinity of V into the sum, the rows that are
+// not finite; those are kept in a bit set, and the rows that do see them add them at the end.
+//
+// Bound by the tensor cores and the exponentials alike: a pair of 128 x 128 tiles at d 128 is
+// 2048 cycles of products and 2048 of ex2.
+#include "paged_tc.cuh"
+
+namespace dkv {
+namespace {
+
+constexpr int kPfThreads = 384, kPfM = 128, kPfN = 128;
+constexpr float kPfSlack = 8.f;
+constexpr int kPfEdges = 8;  // edge tiles of a CTA: 3 on the diagonal, 3 at the window's edge, 1 at the sinks' end
+
+template <typename T>
+constexpr float kPfShift = 0.f;
+template <>
+constexpr float kPfShift<__half> = 7.f;
+
+template <int D>
+struct PfSmem {
+  static constexpr int kSlots = 5;
+  static constexpr uint32_t kTile = kPfN * D * 2;  // one K or V tile, or one group's Q
+  static constexpr uint32_t kOffRing = 2 * kTile;
+  static constexpr uint32_t kOffBar = kOffRing + kSlots * kTile;
+  static constexpr uint32_t kBytes = kOffBar + 512;
+};
+
+struct PfKernelArgs {
+  PagedArgs a;
+  PagedQuery q;
+  const void* k_pool;
+  const void* v_pool;
+  void* out;
+  dkv_strides os;
+  float* lse;
+  int by_heads;  // the groups are two heads (else two 128-token tiles of one head)
+};
+
+// The keys that the queries at positions [p_lo, p_hi] see between them, in 128-key tiles.
+struct KeySpan {
+  int lo, hi, st, wt0, n;  // window start, end, sink tiles, first window tile, tiles
+  __device__ int key(int j) const { return (j < st ? j : wt0 + j - st) * kPfN; }
+};
+__device__ inline KeySpan key_span(const PagedArgs& a, int p_lo, int p_hi) {
+  KeySpan s;
+  s.hi = max(0, p_hi + 1);
+  s.lo = min(paged_window_lo(a, max(p_lo, 0)), s.hi);
+  s.wt0 = s.lo / kPfN;
+  s.st = min((min(a.sinks, s.hi) + kPfN - 1) / kPfN, s.wt0);
+  s.n = s.st + (s.hi + kPfN - 1) / kPfN - s.wt0;
+  return s;
+}
+
+// every query at positions [p_lo, p_hi] sees every key of [k0, k0 + kPfN)
+__device__ inline bool all_seen(const PagedArgs& a, int k0, int p_lo, int p_hi) {
+  return k0 + kPfN - 1 <= p_lo && (a.window == 0 || k0 > p_hi - a.window || k0 + kPfN <= a.sinks);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kPfThreads, 1)
+    paged_prefill_kernel(PfKernelArgs p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                         const __grid_constant__ CUtensorMap vmap) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  using S = PfSmem<D>;
+  constexpr int NS = S::kSlots;
+  const PagedArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.z;
+  const QuerySpan qs = query_span(a, p.q.q_lens, p.q.Tq, b);
+  // the groups: head and first query row (later rows, with more keys, first)
+  const int tile = (int)gridDim.x - 1 - (int)blockIdx.x;
+  const int row0 = tile * (p.by_heads ? kPfM : 2 * kPfM);
+  if (row0 >= qs.n) return;
+  const int h0 = p.by_heads ? 2 * (int)blockIdx.y : (int)blockIdx.y, kvh = h0 / a.G;
+  const int rowsA = min(kPfM, qs.n - row0), rowsB = p.by_heads ? rowsA : min(kPfM, max(0, qs.n - row0 - kPfM));
+  const int p_lo = qs.off + row0, p_hi = p_lo + (p.by_heads ? rowsA : rowsA + rowsB) - 1;
+  const KeySpan ks = key_span(a, p_lo, p_hi);
+  // group A's keys may end a tile or two before B's
+  const int nA = min(ks.n, max(0, ks.st + (max(0, p_lo + rowsA) + kPfN - 1) / kPfN - ks.wt0)), nB = rowsB > 0 ? ks.n : 0;
+  const int nt = max(nA, nB);
+
+  const uint32_t sb = smem_u32(smem);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kOffBar);  // [slot]
+  uint64_t* empty = full + NS;                                       // [slot]
+  uint64_t* landed = empty + NS;                                     // [edge tile] its V landed, for warp 11 (used once)
+  uint64_t* q_full = landed + kPfEdges;
+  uint64_t* s_full = q_full + 1;   // [group]
+  uint64_t* p_half = s_full + 2;   // [group][half]
+  uint64_t* o_done = p_half + 4;   // [group]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 2);
+  int* n_bad = reinterpret_cast<int*>(tmem_slot + 1);
+  int* bad_key = n_bad + 1;                                          // [edge] first key of an edge tile with bad rows
+  uint32_t* bad_bits = reinterpret_cast<uint32_t*>(bad_key + kPfEdges);  // [edge][4]
+
+  if (threadIdx.x == 0) {
+    tma_prefetch_map(&qmap);
+    tma_prefetch_map(&kmap);
+    tma_prefetch_map(&vmap);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 2);  // one commit per group
+    }
+    for (int i = 0; i < kPfEdges; ++i) mbar_init(&landed[i], 1);
+    mbar_init(q_full, 1);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&s_full[g], 1);
+      mbar_init(&p_half[2 * g], kPfM);
+      mbar_init(&p_half[2 * g + 1], kPfM);
+      mbar_init(&o_done[g], 1);
+    }
+    *n_bad = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) tc_alloc<512>(tmem_slot);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  bool ok = true;
+
+  if (warp == 8) {
+    // =========================== loads
+    if (lane == 0 && nt > 0) {
+      mbar_arrive_expect_tx(q_full, (rowsB > 0 ? 2 : 1) * S::kTile);
+      for (int g = 0; g < (rowsB > 0 ? 2 : 1); ++g)
+        for (int hf = 0; hf < D / 64; ++hf)
+          tma_load_4d(sb + g * S::kTile + hf * kPfM * 128, &qmap, hf * 64, p.by_heads ? row0 : row0 + g * kPfM,
+                      p.by_heads ? h0 + g : h0, b, q_full);
+    }
+    __syncwarp();
+    const int rows = min(a.page_mask + 1, 64), per = kPfN / rows, nbox = per * (D / 64);
+    const int pi = lane % per, hf = lane / per;
+    int i = 0, edges = 0;  // ring position: K of tile j at 2j, V at 2j + 1
+    for (int j = 0; j < nt && ok; ++j) {
+      const int first = ks.key(j) + pi * rows;
+      int page = a.n_pages;  // boxes without a visible key: zeros, wherever the table points
+      if (lane < nbox && first < ks.hi && (first + rows > ks.lo || first < a.sinks)) page = paged_page(a, b, first);
+      for (int kv = 0; kv < 2; ++kv, ++i) {
+        const int sl = i % NS;
+        if (i >= NS) ok = mbar_wait(&empty[sl], (uint32_t)((i / NS - 1) & 1), a.err);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        // V of an edge tile lands for warp 11, whose arrival then fills the slot
+        uint64_t* bar = kv && !all_seen(a, ks.key(j), p_lo, p_hi) ? &landed[edges++] : &full[sl];
+        if (lane == 0) mbar_arrive_expect_tx(bar, S::kTile);
+        __syncwarp();
+        if (lane < nbox)
+          tma_load_4d(sb + S::kOffRing + sl * S::kTile + hf * kPfN * 128 + pi * rows * 128, kv ? &vmap : &kmap, hf * 64,
+                      first & a.page_mask, kvh, page, bar);
+      }
+    }
+    // every copy has landed before the CTA may end (also after a wait that gave up)
+    if (nt > 0) mbar_wait(q_full, 0, a.err);
+    for (int x = max(0, i - NS); x < i; ++x) mbar_wait(&full[x % NS], (uint32_t)((x / NS) & 1), a.err);
+  } else if (warp == 9 || warp == 10) {
+    // =========================== products of group g
+    const int g = warp - 9, n = g ? nB : nA, n_other = g ? nA : nB;
+    if (lane == 0 && n > 0) {
+      const uint32_t ts = tmem + 256u * g, to = ts + 128u;
+      constexpr uint32_t id_s = tc_idesc(Num<T>::kUmma, false, kPfN), id_o = tc_idesc(Num<T>::kUmma, true, D);
+      const uint64_t qd = tc_desc(sb + g * S::kTile, 16, 1024);
+      auto release = [&](int sl, int j) {  // once for this group, once more where the other has no tile j
+        tc_commit(&empty[sl]);
+        if (j >= n_other) tc_commit(&empty[sl]);
+      };
+      auto scores = [&](int j) {
+        const int sl = 2 * j % NS;
+        ok = ok && mbar_wait(&full[sl], (uint32_t)((2 * j / NS) & 1), a.err);
+        if (j > 0) ok = ok && mbar_wait(&o_done[g], (uint32_t)((j - 1) & 1), a.err);
+        tc_fence_after();
+        if (!ok) return;
+        const uint64_t kd = tc_desc(sb + S::kOffRing + sl * S::kTile, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {  // 16 channels: 32 bytes of a 128-byte row, then the next 64 channels
+          const uint64_t step = (uint64_t)(((k >> 2) * kPfN * 128 + (k & 3) * 32) >> 4);
+          tc_mma(ts, qd + step, kd + step, id_s, k > 0);
+        }
+        tc_commit(&s_full[g]);
+        release(sl, j);
+      };
+      ok = mbar_wait(q_full, 0, a.err);
+      scores(0);
+      for (int j = 0; j < n && ok; ++j) {
+        const int i = 2 * j + 1, sl = i % NS;
+        ok = mbar_wait(&full[sl], (uint32_t)((i / NS) & 1), a.err);
+        const uint64_t vd = tc_desc(sb + S::kOffRing + sl * S::kTile, kPfN * 128, 1024);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          ok = ok && mbar_wait(&p_half[2 * g + half], (uint32_t)(j & 1), a.err);
+          tc_fence_after();
+          if (!ok) break;
+#pragma unroll
+          for (int k = 4 * half; k < 4 * half + 4; ++k)  // 16 keys: 16 rows of 128 bytes
+            tc_mma_ta(to, ts + 8u * k, vd + (uint64_t)(k * 16 * 128 >> 4), id_o, (j > 0 || k > 0) ? 1u : 0u);
+        }
+        if (!ok) break;
+        release(sl, j);
+        tc_commit(&o_done[g]);
+        if (j + 1 < n) scores(j + 1);
+      }
+    }
+  } else if (warp == 11) {
+    // =========================== V rows of edge tiles
+    int edges = 0;
+    for (int j = 0; j < nt && ok; ++j) {
+      const int k0 = ks.key(j), i = 2 * j + 1, sl = i % NS;
+      if (!all_seen(a, k0, p_lo, p_hi)) {
+        ok = mbar_wait(&landed[edges++], 0, a.err);
+        const uint32_t vb = sb + S::kOffRing + sl * S::kTile;
+        uint32_t bad = 0;  // rows lane, lane + 32, ... with a value that is not finite
+        for (int x = 0; x < 4; ++x) {
+          const int r = 32 * x + lane, t = k0 + r;
+          const bool some = t < ks.hi && (t >= ks.lo || t < a.sinks);  // a row of the CTA sees it
+          bool odd = false;
+          if (some) {
+            constexpr uint32_t kExp = Num<T>::kUmma ? 0x7f80u : 0x7c00u;
+#pragma unroll 4
+            for (int ch = 0; ch < D / 8; ++ch) {
+              const uint4 v = lds128(vb + sw128(kPfN, r, ch));
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int y = 0; y < 4; ++y) odd |= (w[y] & kExp) == kExp || ((w[y] >> 16) & kExp) == kExp;
+            }
+          }
+          if (!some || odd)
+            for (int ch = 0; ch < D / 8; ++ch) sts128(vb + sw128(kPfN, r, ch), make_uint4(0, 0, 0, 0));
+          const uint32_t bits = __ballot_sync(0xffffffffu, odd);
+          if (lane == x) bad = bits;
+        }
+        if (__any_sync(0xffffffffu, lane < 4 && bad)) {
+          const int at = *n_bad;
+          __syncwarp();
+          if (at < kPfEdges) {
+            if (lane < 4) bad_bits[4 * at + lane] = bad;
+            if (lane == 0) { bad_key[at] = k0; *n_bad = at + 1; }
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[sl]);
+      }
+    }
+  } else {
+    // =========================== softmax: one query row per thread
+    const int g = warp >> 2, rw = warp & 3, row = 32 * rw + lane;
+    const int n = g ? nB : nA, rows = g ? rowsB : rowsA;
+    const int qrow = p.by_heads ? row0 + row : row0 + g * kPfM + row, pos = qs.off + qrow;
+    const int head = p.by_heads ? h0 + g : h0;
+    // positions of the group's rows (the tile is unmasked when all of them see all of it)
+    const int g_lo = p.by_heads ? p_lo : p_lo + g * kPfM, g_hi = g_lo + rows - 1;
+    const uint32_t ts = tmem + ((uint32_t)(32 * rw) << 16) + 256u * g, to = ts + 128u;
+    const float slog2 = a.scale_log2;
+    float m = -INFINITY, l = 0.f;
+    for (int j = 0; j < n; ++j) {
+      if (ok) ok = mbar_wait(&s_full[g], (uint32_t)(j & 1), a.err);
+      tc_fence_after();
+      uint32_t s[kPfN];
+#pragma unroll
+      for (int c = 0; c < kPfN / 32; ++c) tc_ld32(ts + 32 * c, s + 32 * c);
+      tc_ld_wait();
+      const int k0 = ks.key(j);
+      if (!all_seen(a, k0, g_lo, g_hi)) {
+        const int hi = pos - k0, lo = a.window ? pos - a.window + 1 - k0 : 0, sk = a.sinks - k0;
+#pragma unroll
+        for (int c = 0; c < kPfN; ++c)
+          if (c > hi || (c < lo && c >= sk)) s[c] = 0xff800000u;
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int c = 0; c < kPfN; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * slog2;
+      const bool up = top > m + kPfSlack || (m == -INFINITY && top > m);
+      const float al = up ? fast_exp2(m - top) : 1.f;
+      if (up) m = top;
+      if (j > 0 && __any_sync(0xffffffffu, up)) {  // O_{j-1} is done: rescale it
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tc_ld32(to + 32 * c, o);
+          tc_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+          tc_st32(to + 32 * c, o);
+        }
+      }
+      const float ms = (m == -INFINITY ? 0.f : m) - kPfShift<T>;
+      float lp[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t w[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const int c = 64 * half + 2 * e;
+          const float p0 = fast_exp2(fmaf(__uint_as_float(s[c]), slog2, -ms));
+          const float p1 = fast_exp2(fmaf(__uint_as_float(s[c + 1]), slog2, -ms));
+          lp[e & 3] += p0 + p1;
+          w[e] = Num<T>::pack(p0, p1);
+        }
+        tc_st32(ts + 32 * half, w);
+        tc_st_wait();
+        tc_fence_before();
+        mbar_arrive(&p_half[2 * g + half]);
+      }
+      l = fmaf(l, al, (lp[0] + lp[1]) + (lp[2] + lp[3]));
+    }
+    if (n > 0 && ok) ok = mbar_wait(&o_done[g], (uint32_t)((n - 1) & 1), a.err);
+    tc_fence_after();
+    const bool live = row < rows;
+    const float il = n == 0 || l == 0.f ? 0.f : 1.f / l;  // a row that sees no key: zeros
+    T* orow = static_cast<T*>(p.out) + (int64_t)b * p.os.batch + (int64_t)head * p.os.head + (int64_t)(live ? qrow : 0) * p.os.token;
+    // (every edge tile's product, and so warp 11's work on it, is behind o_done)
+    const int bads = n > 0 ? *reinterpret_cast<volatile int*>(n_bad) : 0;
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t o[32];
+      if (n > 0) {
+        tc_ld32(to + 32 * c, o);
+        tc_ld_wait();
+      }
+      float f[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) f[e] = n > 0 && l != 0.f ? __uint_as_float(o[e]) * il : 0.f;
+      if (bads && live) {
+        // V rows that are not finite, and that this row sees: p v in fp32 (rare, so in plain loops)
+        const T* qr = static_cast<const T*>(p.q.q) + (int64_t)b * p.q.qs.batch + (int64_t)head * p.q.qs.head + (int64_t)qrow * p.q.qs.token;
+        for (int x = 0; x < bads * kPfN; ++x) {
+          const int t = bad_key[x / kPfN] + x % kPfN;
+          if (!((bad_bits[x / 32] >> (x % 32)) & 1u)) continue;
+          if (t > pos || (a.window && t <= pos - a.window && t >= a.sinks)) continue;
+          const int page = paged_page(a, b, t);
+          if (page >= a.n_pages) continue;
+          const int64_t at = page * a.stride_page + kvh * a.stride_head + (t & a.page_mask) * a.stride_token;
+          const T* kr = static_cast<const T*>(p.k_pool) + at;
+          const T* vr = static_cast<const T*>(p.v_pool) + at + 32 * c;
+          float dot = 0.f;
+          for (int e = 0; e < D; ++e) dot = fmaf(Num<T>::to_float(qr[e]), Num<T>::to_float(kr[e]), dot);
+          const float w = fast_exp2(fmaf(dot, slog2, kPfShift<T> - m)) * il;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) f[e] += w * Num<T>::to_float(vr[e]);
+        }
+      }
+      if (live)
+#pragma unroll
+        for (int e = 0; e < 32; e += 8)
+          *reinterpret_cast<uint4*>(orow + 32 * c + e) =
+              make_uint4(Num<T>::pack(f[e], f[e + 1]), Num<T>::pack(f[e + 2], f[e + 3]), Num<T>::pack(f[e + 4], f[e + 5]),
+                         Num<T>::pack(f[e + 6], f[e + 7]));
+    }
+    if (live && p.lse)
+      p.lse[((int64_t)b * a.Hq + head) * p.q.Tq + qrow] =
+          n == 0 ? -INFINITY : (m - kPfShift<T> + log2f(l)) * 0.6931471805599453f;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tc_free<512>(tmem);
+}
+
+template <typename T, int D>
+cudaError_t launch_td(const PfKernelArgs& p, const PagedMaps& m, const CUtensorMap& qmap, cudaStream_t s) {
+  constexpr uint32_t smem = PfSmem<D>::kBytes;
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(paged_prefill_kernel<T, D>), smem);
+  if (e != cudaSuccess) return e;
+  const int per = p.by_heads ? kPfM : 2 * kPfM;
+  const dim3 grid((p.q.Tq + per - 1) / per, p.by_heads ? p.a.Hq / 2 : p.a.Hq, p.a.B);
+  paged_prefill_kernel<T, D><<<grid, kPfThreads, smem, s>>>(p, qmap, m.k, m.v);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_prefill(const PagedArgs& a, int d, int dtype, const PagedMaps& m, const CUtensorMap& qmap,
+                                 const PagedQuery& q, const void* v_pool, const void* k_pool, void* out,
+                                 const dkv_strides& os, float* lse, cudaStream_t s) {
+  PfKernelArgs p;
+  p.a = a;
+  p.q = q;
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.out = out;
+  p.os = os;
+  p.lse = lse;
+  p.by_heads = a.G % 2 == 0;
+  if (dtype == DKV_BF16)
+    return d == 128 ? launch_td<__nv_bfloat16, 128>(p, m, qmap, s) : launch_td<__nv_bfloat16, 64>(p, m, qmap, s);
+  return d == 128 ? launch_td<__half, 128>(p, m, qmap, s) : launch_td<__half, 64>(p, m, qmap, s);
+}
+
+}  // namespace dkv

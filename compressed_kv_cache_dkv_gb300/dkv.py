@@ -33,6 +33,8 @@ DKV_DEVERR_RANGE = 0x4
 BLOCK_SIZE = 256
 DKV_LAYOUT_FRAGMENT = 0
 DKV_LAYOUT_TC = 1
+DKV_FP16 = 0
+DKV_BF16 = 1
 
 EXPORTED = (
     "dkv_version", "dkv_status_string", "dkv_layout", "dkv_layout_bytes",
@@ -42,6 +44,8 @@ EXPORTED = (
     "dkv_dense_workspace_bytes", "dkv_dense_decode", "dkv_get_error", "dkv_decode_attend_noalloc",
     "dkv_append_workspace_bytes", "dkv_append", "dkv_debug_set_limits", "dkv_debug_set_launch", "dkv_prefill_routed_slots",
     "dkv_prefill_workspace_bytes", "dkv_prefill_attend",
+    "dkv_paged_check", "dkv_paged_workspace_bytes", "dkv_paged_append", "dkv_paged_decode", "dkv_paged_prefill",
+    "dkv_paged_weights", "dkv_paged_evict",
 )
 
 
@@ -70,6 +74,16 @@ class dkv_desc(ctypes.Structure):
 class dkv_factors(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "a_k", "a_v", "U", "V_K", "V_V", "res_pos", "K_res", "V_res", "kmin", "kmax", "win_K", "win_V")]
+
+
+class dkv_paged(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "n_q_heads", "n_kv_heads", "head_dim", "page_size", "n_pages", "max_pages", "dtype", "window", "sinks")] + [
+        (n, ctypes.c_int64) for n in ("stride_page", "stride_head", "stride_token")]
+
+
+class dkv_strides(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "head", "token")]
 
 
 _lib = None
@@ -117,6 +131,15 @@ def lib() -> ctypes.CDLL:
         L.dkv_prefill_workspace_bytes.restype = sz
         L.dkv_prefill_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
         L.dkv_prefill_attend.argtypes = [i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        ppaged, pstr = ctypes.POINTER(dkv_paged), ctypes.POINTER(dkv_strides)
+        L.dkv_paged_check.argtypes = [ppaged]
+        L.dkv_paged_workspace_bytes.restype = sz
+        L.dkv_paged_workspace_bytes.argtypes = [ppaged, i32]
+        L.dkv_paged_append.argtypes = [ppaged, vp, vp, pstr, i32] + [vp] * 6 + [sz, vp]
+        L.dkv_paged_decode.argtypes = [ppaged, vp, pstr] + [vp] * 8 + [sz, vp]
+        L.dkv_paged_prefill.argtypes = [ppaged, vp, pstr, i32] + [vp] * 6 + [pstr, vp, vp, sz, vp]
+        L.dkv_paged_weights.argtypes = [ppaged, vp, pstr, i32] + [vp] * 7 + [sz, vp]
+        L.dkv_paged_evict.argtypes = [ppaged] + [vp] * 5 + [i32] * 3 + [vp, i32] + [vp] * 4 + [sz, vp]
         _lib = L
     return _lib
 
@@ -338,6 +361,207 @@ def dkv_prefill_attend(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, top_k:
                                     _ptr(routed_t) if routed_t is not None else None, _ptr(workspace),
                                     workspace.numel(), _stream(stream)), "dkv_prefill_attend")
     return out, lse_t, routed_t
+
+
+# ---------------------------------------------------------------- paged cache
+
+_PAGED_DTYPES = {torch.float16: DKV_FP16, torch.bfloat16: DKV_BF16}
+
+
+def _typed(t: torch.Tensor, dtype: torch.dtype, shape: tuple, what: str) -> int:
+    """Address of a contiguous device tensor of this type and shape."""
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{what}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+    return _ptr(t)
+
+
+def _rows(t: torch.Tensor, dtype: torch.dtype, shape: tuple, what: str) -> dkv_strides:
+    """Strides of a device tensor [batch][head][token][head_dim] whose channels are adjacent."""
+    if not t.is_cuda:
+        raise ValueError("device tensor expected")
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{what}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+    s = t.stride()
+    if s[-1] != 1:
+        raise ValueError(f"{what}: adjacent channels expected")
+    return dkv_strides(s[0], s[1], s[2] if len(s) == 4 else 0)
+
+
+def _pools(p: dkv_paged, *pools: torch.Tensor) -> list:
+    shape = (p.n_pages, p.n_kv_heads, p.page_size, p.head_dim)
+    want = (p.stride_page, p.stride_head, p.stride_token, 1)
+    for t in pools:
+        if not t.is_cuda:
+            raise ValueError("device tensor expected")
+        if tuple(t.shape) != shape or _PAGED_DTYPES.get(t.dtype) != p.dtype:
+            raise ValueError(f"pool: expected {shape} of the descriptor's type, got {t.dtype} {tuple(t.shape)}")
+        if any(n > 1 and a != b for n, a, b in zip(shape, t.stride(), want)):
+            raise ValueError(f"pool: strides {t.stride()} are not the descriptor's {want}")
+    return [t.data_ptr() for t in pools]
+
+
+def _paged_dtype(p: dkv_paged) -> torch.dtype:
+    return torch.bfloat16 if p.dtype == DKV_BF16 else torch.float16
+
+
+def _on(device):
+    """The CUDA calls of a paged operator go to its tensors' device."""
+    return torch.cuda.device(device)
+
+
+def dkv_paged_layout(k_pages: torch.Tensor, batch: int, n_q_heads: int, max_pages: int, window: int = 0,
+                     sinks: int = 0) -> dkv_paged:
+    """Descriptor of a paged cache from one of its pools, fp16 or bf16 [n_pages, Hkv, page_size, d]
+    under any strides with adjacent channels (a transposed [n_pages, page_size, Hkv, d], a half of a
+    pool that interleaves K and V).  `max_pages`: entries of a page-table row; `window`, `sinks`: a
+    query at position p sees token t when t <= p and (window == 0 or t > p - window or t < sinks)."""
+    if k_pages.dim() != 4 or k_pages.dtype not in _PAGED_DTYPES or k_pages.stride(3) != 1:
+        raise DkvError(DKV_ERR_ARG, "dkv_paged_layout")
+    n_pages, hkv, page, d = k_pages.shape
+    sp, sh, st, _ = k_pages.stride()
+    p = dkv_paged(batch, n_q_heads, hkv, d, page, n_pages, max_pages, _PAGED_DTYPES[k_pages.dtype], window, sinks, sp, sh, st)
+    _check(lib().dkv_paged_check(ctypes.byref(p)), "dkv_paged_layout")
+    return p
+
+
+def dkv_paged_workspace_bytes(p: dkv_paged, with_weights: bool = False) -> int:
+    return int(lib().dkv_paged_workspace_bytes(ctypes.byref(p), int(with_weights)))
+
+
+def _paged_ws(p: dkv_paged, workspace, device, with_weights: bool = False) -> torch.Tensor:
+    if workspace is not None:
+        return workspace
+    ws = torch.empty(dkv_paged_workspace_bytes(p, with_weights), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def dkv_paged_append(p: dkv_paged, K_new: torch.Tensor, V_new: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                     page_table: torch.Tensor, pos: torch.Tensor, counts: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Write K_new, V_new [B, Hkv, n_new, d] (any strides with adjacent channels, both alike) into their
+    pages: token i < counts[b] of sequence b at position pos[b] + i (counts None: all n_new)."""
+    B, n = p.batch, K_new.shape[2]
+    shape = (B, p.n_kv_heads, n, p.head_dim)
+    ns, vs = (_rows(t, _paged_dtype(p), shape, "K_new, V_new") for t in (K_new, V_new))
+    if any(m > 1 and getattr(ns, f) != getattr(vs, f) for f, m in zip(("batch", "head", "token"), shape)):
+        V_new = V_new.contiguous()
+        K_new = K_new.contiguous()
+        ns = _rows(K_new, _paged_dtype(p), shape, "K_new")
+    kp, vp = _pools(p, k_pages, v_pages)
+    with _on(K_new.device):
+        ws = _paged_ws(p, workspace, K_new.device)
+        _check(lib().dkv_paged_append(
+            p, K_new.data_ptr(), V_new.data_ptr(), ns, n, _typed(pos, torch.int32, (B,), "pos"),
+            None if counts is None else _typed(counts, torch.int32, (B,), "counts"), kp, vp,
+            _typed(page_table, torch.int32, (B, p.max_pages), "page_table"), _ptr(ws), ws.numel(), _stream(stream)),
+            "dkv_paged_append")
+
+
+def dkv_paged_decode(p: dkv_paged, q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                     lens: torch.Tensor, out: torch.Tensor | None = None, lse: torch.Tensor | bool | None = True,
+                     weights: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """One new token per sequence: q [B, Hq, d] at position lens[b] - 1 -> (out [B, Hq, d] in q's type,
+    lse fp32 [B, Hq] or None).  `weights` fp32 [B, Hkv, max_pages * page_size]: every visible token's
+    softmax weight, summed over its KV head's query heads, is added."""
+    B, Hq, d = p.batch, p.n_q_heads, p.head_dim
+    dt = _paged_dtype(p)
+    qs = _rows(q, dt, (B, Hq, d), "q")
+    kp, vp = _pools(p, k_pages, v_pages)
+    with _on(q.device):
+        if out is None:
+            out = torch.empty(B, Hq, d, dtype=dt, device=q.device)
+        if lse is True:
+            lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
+        elif lse is False:
+            lse = None
+        ws = _paged_ws(p, workspace, q.device, weights is not None)
+        _check(lib().dkv_paged_decode(
+            p, q.data_ptr(), qs, kp, vp, _typed(page_table, torch.int32, (B, p.max_pages), "page_table"),
+            _typed(lens, torch.int32, (B,), "lens"), _typed(out, dt, (B, Hq, d), "out"),
+            None if lse is None else _typed(lse, torch.float32, (B, Hq), "lse"),
+            None if weights is None else _typed(weights, torch.float32, (B, p.n_kv_heads, p.max_pages * p.page_size), "weights"),
+            _ptr(ws), ws.numel(), _stream(stream)), "dkv_paged_decode")
+    return out, lse
+
+
+def dkv_paged_prefill(p: dkv_paged, q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                      lens: torch.Tensor, q_lens: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                      lse: torch.Tensor | bool | None = True, workspace: torch.Tensor | None = None, stream=None):
+    """The last tokens of each sequence: q [B, Hq, Tq, d], query i < q_lens[b] (None: Tq) at position
+    lens[b] - q_lens[b] + i -> (out [B, Hq, Tq, d] in q's type, lse fp32 [B, Hq, Tq] or None).  Rows from
+    q_lens[b] on are left as they were (zeros in outputs allocated here)."""
+    B, Hq, d = p.batch, p.n_q_heads, p.head_dim
+    dt, Tq = _paged_dtype(p), q.shape[2]
+    qs = _rows(q, dt, (B, Hq, Tq, d), "q")
+    kp, vp = _pools(p, k_pages, v_pages)
+    with _on(q.device):
+        new = torch.empty if q_lens is None else torch.zeros
+        if out is None:
+            out = new(B, Hq, Tq, d, dtype=dt, device=q.device)
+        if lse is True:
+            lse = new(B, Hq, Tq, dtype=torch.float32, device=q.device)
+        elif lse is False:
+            lse = None
+        ws = _paged_ws(p, workspace, q.device)
+        _check(lib().dkv_paged_prefill(
+            p, q.data_ptr(), qs, Tq, kp, vp, _typed(page_table, torch.int32, (B, p.max_pages), "page_table"),
+            _typed(lens, torch.int32, (B,), "lens"),
+            None if q_lens is None else _typed(q_lens, torch.int32, (B,), "q_lens"), out.data_ptr(),
+            _rows(out, dt, (B, Hq, Tq, d), "out"),
+            None if lse is None else _typed(lse, torch.float32, (B, Hq, Tq), "lse"), _ptr(ws), ws.numel(), _stream(stream)),
+            "dkv_paged_prefill")
+    return out, lse
+
+
+def dkv_paged_weights(p: dkv_paged, q: torch.Tensor, lse: torch.Tensor, k_pages: torch.Tensor, page_table: torch.Tensor,
+                      lens: torch.Tensor, weights: torch.Tensor, q_lens: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Add the softmax weights that the queries (as in dkv_paged_prefill, with the lse it gave) give every
+    token, summed over queries and a KV head's query heads, to weights fp32 [B, Hkv, max_pages * page_size]."""
+    B, Hq, d = p.batch, p.n_q_heads, p.head_dim
+    Tq = q.shape[2]
+    qs = _rows(q, _paged_dtype(p), (B, Hq, Tq, d), "q")
+    kp, = _pools(p, k_pages)
+    with _on(q.device):
+        ws = _paged_ws(p, workspace, q.device)
+        _check(lib().dkv_paged_weights(
+            p, q.data_ptr(), qs, Tq, _typed(lse, torch.float32, (B, Hq, Tq), "lse"), kp,
+            _typed(page_table, torch.int32, (B, p.max_pages), "page_table"), _typed(lens, torch.int32, (B,), "lens"),
+            None if q_lens is None else _typed(q_lens, torch.int32, (B,), "q_lens"),
+            _typed(weights, torch.float32, (B, p.n_kv_heads, p.max_pages * p.page_size), "weights"), _ptr(ws), ws.numel(),
+            _stream(stream)), "dkv_paged_weights")
+    return weights
+
+
+def dkv_paged_evict(p: dkv_paged, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
+                    weights: torch.Tensor, budget: int, first: int, recent: int, new_table: torch.Tensor,
+                    kept: torch.Tensor | None = None, new_lens: torch.Tensor | None = None,
+                    new_weights: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Cut every sequence to `budget` tokens: the first `first`, the last `recent` and the heaviest between
+    them, in order, moved to new_table's pages (int32 [B, n]; page_table itself compacts in place) ->
+    (kept int32 [B, Hkv, budget], new_lens int32 [B], new_weights like weights)."""
+    B, shape = p.batch, (p.batch, p.n_kv_heads, p.max_pages * p.page_size)
+    kp, vp = _pools(p, k_pages, v_pages)
+    if new_table.dim() != 2:
+        raise ValueError("new_table: expected [B, pages]")
+    dev = k_pages.device
+    with _on(dev):
+        if kept is None:
+            kept = torch.empty(B, p.n_kv_heads, budget, dtype=torch.int32, device=dev)
+        if new_lens is None:
+            new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+        if new_weights is None:
+            new_weights = torch.empty(shape, dtype=torch.float32, device=dev)
+        ws = _paged_ws(p, workspace, dev)
+        _check(lib().dkv_paged_evict(
+            p, kp, vp, _typed(page_table, torch.int32, (B, p.max_pages), "page_table"), _typed(lens, torch.int32, (B,), "lens"),
+            _typed(weights, torch.float32, shape, "weights"), int(budget), int(first), int(recent),
+            _typed(new_table, torch.int32, (B, new_table.shape[1]), "new_table"), new_table.shape[1],
+            _typed(kept, torch.int32, (B, p.n_kv_heads, budget), "kept"), _typed(new_lens, torch.int32, (B,), "new_lens"),
+            _typed(new_weights, torch.float32, shape, "new_weights"), _ptr(ws), ws.numel(), _stream(stream)),
+            "dkv_paged_evict")
+    return kept, new_lens, new_weights
 
 
 def dkv_debug_set_limits(stop_after_chunks: int = -1, wait_polls: int = 0) -> None:

@@ -386,6 +386,169 @@ DKV_API int dkv_prefill_attend(int32_t batch, int32_t n_q_heads, int32_t n_kv_he
                                int32_t* routed, void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * Paged cache of exact keys and values, and the operators on it.
+ *
+ * Each sequence's tokens lie in pages of page_size tokens that are taken from
+ * a pool in any order: token t of sequence b in page
+ * page_table[b * max_pages + t / page_size], slot t % page_size, of both the
+ * key pool and the value pool.  Element (page, head, slot, channel) of a pool
+ * is at page * stride_page + head * stride_head + slot * stride_token +
+ * channel, so that [page][head][slot][d], [page][slot][head][d] and pools that
+ * interleave keys and values are all taken as they are.
+ *
+ * Which tokens a query sees: a query at position p of its sequence (p counts
+ * the sequence's tokens from 0) sees token t when
+ *     t <= p  and  (window == 0 or t > p - window or t < sinks):
+ * causal, the last `window` tokens, and the first `sinks` tokens whatever the
+ * window.  Scores are c q.k with c = 1/sqrt(head_dim).  A query that sees no
+ * token gets zeros and a log-sum-exp of -infinity.  What lies in slots that no
+ * query of a sequence sees (behind its last token, or before its window) has no
+ * influence, whatever its bits are, and pages that hold only such slots are not
+ * read: their page-table entries may be anything.
+ *
+ * Data types: dtype DKV_FP16 or DKV_BF16 for the pools, the new rows, the
+ * queries and the outputs alike; scores, softmax statistics, sums and weights
+ * are held in fp32, and an output is rounded once.
+ *
+ * Faults that only the device can see raise DKV_DEVERR_INDEX in the error word
+ * of the workspace (dkv_get_error): a page index outside [0, n_pages) of a page
+ * that is needed is read as a page of zeros and not written; a length outside
+ * [0, max_pages * page_size] is taken as the nearest bound.
+ *
+ * Supported: head_dim 64 or 128; 1 <= n_q_heads / n_kv_heads <= 8; page_size
+ * 16, 32, 64, 128 or 256; batch <= 4096, batch * n_kv_heads <= 65535;
+ * max_pages * page_size <= 1048576; strides multiples of 8 elements below 2^38.
+ */
+#define DKV_FP16 0
+#define DKV_BF16 1
+
+typedef struct dkv_paged {
+  int32_t batch;         /* sequences B */
+  int32_t n_q_heads;     /* query heads Hq */
+  int32_t n_kv_heads;    /* KV heads Hkv (Hq % Hkv == 0) */
+  int32_t head_dim;      /* d */
+  int32_t page_size;     /* tokens of a page */
+  int32_t n_pages;       /* pages of each pool */
+  int32_t max_pages;     /* entries of a page-table row: the capacity is max_pages * page_size tokens */
+  int32_t dtype;         /* DKV_FP16 or DKV_BF16 */
+  int32_t window;        /* 0: every earlier token; > 0: the last `window` tokens */
+  int32_t sinks;         /* first tokens that stay visible beside the window */
+  int64_t stride_page;   /* pool strides in elements (channels are adjacent) */
+  int64_t stride_head;
+  int64_t stride_token;
+} dkv_paged;
+
+/* Strides in elements of a [batch][head][token][head_dim] tensor (channels are adjacent). */
+typedef struct dkv_strides {
+  int64_t batch, head, token;
+} dkv_strides;
+
+/* Check a descriptor: DKV_OK, DKV_ERR_ARG, DKV_ERR_SHAPE, DKV_ERR_ALIGN or DKV_ERR_UNSUPPORTED.  Host only. */
+DKV_API int dkv_paged_check(const dkv_paged* p);
+
+/*
+ * Bytes of the workspace that every call below takes (0 for a bad descriptor).
+ * with_weights: room for dkv_paged_decode with weights as well.  Its 256-byte
+ * header holds the device error word; zero-fill the header once before the
+ * first use.  Nothing else in it is kept from call to call; calls that may
+ * overlap on the GPU need a workspace each.
+ */
+DKV_API size_t dkv_paged_workspace_bytes(const dkv_paged* p, int32_t with_weights);
+
+/*
+ * Write new tokens into their pages: token i of sequence b, i < counts[b], to
+ * position pos[b] + i.  Everything else in the pools stays as it is.
+ *   K_new, V_new  device [B][Hkv][n_new][head_dim] under strides `ns` (both alike)
+ *   pos           device int32 [B]: position of each sequence's first new token
+ *   counts        optional device int32 [B]: new tokens of each sequence, at
+ *                 most n_new (NULL: n_new); rows behind them are not read
+ * A token whose position lies outside the capacity, or on a bad page, is
+ * skipped and DKV_DEVERR_INDEX raised.  Two new tokens never meet in one slot
+ * unless two sequences share a page there.
+ */
+DKV_API int dkv_paged_append(const dkv_paged* p, const void* K_new, const void* V_new, const dkv_strides* ns,
+                             int32_t n_new, const int32_t* pos, const int32_t* counts, void* k_pool, void* v_pool,
+                             const int32_t* page_table, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Attention of one new token per sequence, at position lens[b] - 1, over the
+ * sequence's tokens (its own among them: append it first).
+ *   q        device [B][Hq][head_dim] under strides `qs` (token stride unused)
+ *   lens     device int32 [B]: tokens of each sequence; 0 gives zeros and -inf
+ *   out      device [B][Hq][head_dim], contiguous, in the pools' type
+ *   lse      device fp32 [B][Hq]: natural-log log-sum-exp of the scores
+ *            (optional without weights)
+ *   weights  optional device fp32 [B][Hkv][max_pages * page_size]: each visible
+ *            token's softmax weight, summed over the query heads of its KV head,
+ *            is added to its entry; the other entries stay
+ * The cache's tokens are dealt out evenly to all multiprocessors, across and
+ * within sequences, and the parts joined in fp32 in a fixed order.
+ */
+DKV_API int dkv_paged_decode(const dkv_paged* p, const void* q, const dkv_strides* qs, const void* k_pool,
+                             const void* v_pool, const int32_t* page_table, const int32_t* lens, void* out,
+                             float* lse, float* weights, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Attention of the last tokens of each sequence: query i < q_lens[b] is at
+ * position lens[b] - q_lens[b] + i (a whole prompt, a chunk of one, or a few
+ * drafted tokens; append them first).
+ *   q        device [B][Hq][Tq][head_dim] under strides `qs`
+ *   lens     device int32 [B]: tokens of each sequence, the new ones included
+ *   q_lens   optional device int32 [B]: queries of each sequence, 0 to Tq
+ *            (NULL: Tq); rows from q_lens[b] on are left as they were.  Where
+ *            q_lens[b] > lens[b] the first queries have negative positions and
+ *            see no token.
+ *   out      device [B][Hq][Tq][head_dim] under strides `os`, in the pools' type
+ *   lse      optional device fp32 [B][Hq][Tq]
+ */
+DKV_API int dkv_paged_prefill(const dkv_paged* p, const void* q, const dkv_strides* qs, int32_t Tq,
+                              const void* k_pool, const void* v_pool, const int32_t* page_table, const int32_t* lens,
+                              const int32_t* q_lens, void* out, const dkv_strides* os, float* lse, void* workspace,
+                              size_t ws_bytes, void* stream);
+
+/*
+ * Attention weights by key: for every token t, the softmax weights that the
+ * queries give it (the same queries as dkv_paged_prefill's; pass the last
+ * tokens only to weigh the cache by them), summed over the queries and the
+ * query heads of its KV head, are added to weights[b][h][t].
+ *   lse      device fp32 [B][Hq][Tq]: the queries' log-sum-exps (as
+ *            dkv_paged_prefill gives them); a query whose value is -inf adds nothing
+ *   weights  device fp32 [B][Hkv][max_pages * page_size]; entries of tokens that
+ *            no query sees stay
+ */
+DKV_API int dkv_paged_weights(const dkv_paged* p, const void* q, const dkv_strides* qs, int32_t Tq, const float* lse,
+                              const void* k_pool, const int32_t* page_table, const int32_t* lens,
+                              const int32_t* q_lens, float* weights, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Eviction by accumulated weight.  Every sequence with more than `budget`
+ * tokens is cut to `budget`: each KV head keeps its first `first` tokens, its
+ * last `recent` ones and, of those between, the ones with the largest weights
+ * (equal weights: the lower token first; NaN counts as -infinity).  Kept tokens
+ * keep their order and move to positions 0 .. budget - 1 of new_table's pages;
+ * shorter sequences move whole.  Heads of one sequence may keep different
+ * tokens, their count is the same.
+ *   weights      device fp32 [B][Hkv][max_pages * page_size] (dkv_paged_decode,
+ *                dkv_paged_weights)
+ *   new_table    device int32 [B][new_max_pages]: pages to move to, with
+ *                new_max_pages * page_size >= budget.  A sequence's row names
+ *                pages that hold none of the tokens being kept, or begins with
+ *                the very pages of its page_table row (page_table itself with
+ *                new_max_pages = max_pages, for instance): then the sequence is
+ *                compacted in place
+ *   kept         device int32 [B][Hkv][budget]: the positions kept, ascending,
+ *                -1 behind the last
+ *   new_lens     device int32 [B]: min(lens, budget); may be lens itself
+ *   new_weights  device fp32 like weights, and may be weights itself: the kept
+ *                tokens' weights at their new positions, zero from there on
+ * 1 <= budget <= max_pages * page_size; first + recent <= budget.
+ */
+DKV_API int dkv_paged_evict(const dkv_paged* p, void* k_pool, void* v_pool, const int32_t* page_table,
+                            const int32_t* lens, const float* weights, int32_t budget, int32_t first, int32_t recent,
+                            const int32_t* new_table, int32_t new_max_pages, int32_t* kept, int32_t* new_lens,
+                            float* new_weights, void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Diagnostics for the failure path (no counterpart in the pages): from the
  * next launch on, the producer of every attention CTA of the fragment layout
  * issues at most `stop_after_chunks` chunks (negative: all of them) and every

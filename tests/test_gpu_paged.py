@@ -1,0 +1,508 @@
+"""The paged-cache operators against their definitions in 64 bits: head layouts, types, page sizes and
+orders, lengths from none on, windows, sinks, ragged batches; slots that nothing may look at hold NaN
+and infinities, unneeded page-table entries numbers out of range."""
+import math
+
+import pytest
+import torch
+
+from compressed_kv_cache_dkv_gb300 import dkv
+from tests import paged_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+def no_fault(ws):
+    assert dkv.dkv_get_error(ws) == (dkv.DKV_OK, 0)
+
+
+def workspace(p, weights=False):
+    ws = torch.full((dkv.dkv_paged_workspace_bytes(p, weights),), 0xFF, dtype=torch.uint8, device="cuda")
+    ws[:256] = 0  # only the header has to be zero
+    return ws
+
+
+def queries(shape, dt, seed, scale=2.0):
+    return (torch.randn(*shape, generator=torch.Generator().manual_seed(seed)) * scale).to(dt)
+
+
+# ---------------------------------------------------------------- append
+
+@pytest.mark.parametrize("dtype,d,hkv,page,order,lens,news", [
+    ("fp16", 128, 2, 16, "head", [1], [1]),
+    ("bf16", 64, 1, 32, "token", [5, 33, 64], [5, 1, 0]),
+    ("fp16", 64, 3, 256, "token", [700, 256, 257], [700, 256, 1]),
+    ("bf16", 128, 8, 64, "head", [1000, 1, 63], [999, 0, 63]),
+])
+def test_append_writes_its_tokens_only(dtype, d, hkv, page, order, lens, news):
+    c = R.Cache(lens, hkv, d, page, dtype, order, seed=3)
+    p, ws = c.layout(hkv), None
+    ws = workspace(p)
+    n = max(max(news), 1)
+    K, V = (queries((c.B, n, hkv, d), c.dt, s).cuda().transpose(1, 2) for s in (1, 2))
+    want = [x.clone() for x in (c.k, c.v)]
+    for b in range(c.B):
+        t = torch.arange(lens[b] - news[b], lens[b])
+        for x, new in zip(want, (K, V)):
+            x[c.table[b].long()[t // page].cuda(), :, (t % page).cuda()] = new[b, :, :news[b]].transpose(0, 1)
+    dkv.dkv_paged_append(p, K, V, c.k, c.v, c.table.cuda(), c.dev([a - x for a, x in zip(lens, news)]), c.dev(news), workspace=ws)
+    no_fault(ws)
+    for x, y in zip((c.k, c.v), want):
+        assert torch.equal(x.contiguous().view(torch.int16), y.contiguous().view(torch.int16))
+
+
+def test_append_takes_differing_strides_and_skips_bad_places():
+    c = R.Cache([40, 20], 2, 64, 16, seed=4)
+    p = c.layout(2)
+    ws = workspace(p)
+    K = queries((2, 2, 8, 64), c.dt, 1).cuda()
+    V = queries((2, 8, 2, 64), c.dt, 2).cuda().transpose(1, 2)
+    table = c.table.clone()
+    table[0, 1] = c.n_pages      # tokens 16..31 of sequence 0 lie on a page that is not there
+    before = c.k.clone()
+    dkv.dkv_paged_append(p, K, V, c.k, c.v, table.cuda(), c.dev([12, 45]), workspace=ws)  # 48 tokens of room
+    assert dkv.dkv_get_error(ws) == (dkv.DKV_ERR_DEVICE, dkv.DKV_DEVERR_INDEX)
+    t = torch.arange(12, 16)
+    assert torch.equal(c.row(c.k, 0, 1, t), K[0, 1, :4].double().cpu())
+    assert torch.equal(c.row(c.v, 0, 1, t), V[0, 1, :4].double().cpu())
+    changed = (c.k.view(torch.int16) != before.view(torch.int16)).any(-1).sum()  # rows: 4 tokens x 2 heads ...
+    # ... and positions 45..47 of sequence 1, whose third table entry is out of range: skipped
+    assert int(changed) == 8
+
+
+# ---------------------------------------------------------------- decode
+
+DECODE = [
+    # dtype, d, hq, hkv, page, order, lens, window, sinks
+    ("fp16", 128, 12, 2, 64, "head", [1000], 0, 0),
+    ("fp16", 64, 1, 1, 16, "token", [1], 0, 0),
+    ("bf16", 128, 8, 1, 16, "token", [1, 2, 63, 64, 65, 127, 128, 129, 0], 0, 0),
+    ("bf16", 64, 9, 3, 32, "head", [0, 300, 0, 17, 555], 0, 0),
+    ("fp16", 128, 7, 7, 256, "token", [5, 2049], 0, 0),
+    ("bf16", 128, 5, 1, 128, "head", [777, 1300], 100, 0),
+    ("fp16", 128, 12, 4, 16, "token", [50, 64, 65, 500, 1999], 64, 4),
+    ("bf16", 64, 16, 2, 64, "head", [3000, 1, 70, 71], 70, 1),
+    ("fp16", 64, 4, 2, 32, "token", [900, 130], 1, 0),
+    ("fp16", 128, 6, 2, 64, "head", [1500, 333], 200, 130),
+    ("bf16", 128, 2, 1, 32, "token", [400, 90], 1000, 5),
+]
+
+
+@pytest.mark.parametrize("dtype,d,hq,hkv,page,order,lens,window,sinks", DECODE)
+@pytest.mark.parametrize("weighed", [False, True])
+def test_decode(dtype, d, hq, hkv, page, order, lens, window, sinks, weighed):
+    c = R.Cache(lens, hkv, d, page, dtype, order, seed=len(lens))
+    p = c.layout(hq, window, sinks)
+    ws = workspace(p, weighed)
+    q = queries((c.B, hq, d), c.dt, 7)
+    weights = torch.rand(c.B, hkv, c.width * page, generator=torch.Generator().manual_seed(1)) if weighed else None
+    got = weights.cuda() if weighed else None
+    table = c.hidden_table([n - 1 for n in lens], window, sinks)
+    out, lse = dkv.dkv_paged_decode(p, q.cuda(), c.k, c.v, table, c.dev(lens), weights=got, workspace=ws)
+    no_fault(ws)
+    p_eps = 2.0 ** -16 if dtype == "bf16" else 2.0 ** -21  # p as two halves of its type
+    for b in range(c.B):
+        for h in range(hkv):
+            added = torch.zeros(c.width * page, dtype=torch.float64)
+            big = 0.0
+            for j in range(h * hq // hkv, (h + 1) * hq // hkv):
+                ref = R.attend(q[b, j:j + 1].double(), c.K[b][h], c.V[b][h], torch.tensor([lens[b] - 1]), window, sinks)
+                R.check_rows(out[b, j:j + 1], lse[b, j:j + 1], ref, d, c.dt, p_eps, f"sequence {b} head {j}")
+                added[:lens[b]] += ref[2][0]
+                big = max(big, ref[4])
+            if weighed:
+                want = weights[b, h].double() + added
+                # each weight is off by its score's and the lse's errors; fp32 adds the heads and the old value
+                tol = (2 * R.score_error(d, big) + 2.0 ** -20 * (1 + math.log(max(2, lens[b])))) * added + 2.0 ** -22 * want
+                assert bool(((got[b, h].double().cpu() - want).abs() <= tol).all()), f"weights of sequence {b} head {h}"
+
+
+def test_decode_takes_strided_queries_and_own_buffers():
+    c = R.Cache([130, 70], 2, 128, 64, seed=5)
+    p = c.layout(4)
+    qkv = queries((2, 8, 128), c.dt, 8).cuda()      # q heads first, K and V heads behind them
+    q = qkv[:, :4]
+    out = torch.empty(2, 4, 128, dtype=c.dt, device="cuda")
+    o, lse = dkv.dkv_paged_decode(p, q, c.k, c.v, c.table.cuda(), c.dev([130, 70]), out=out, lse=False)
+    assert o is out and lse is None
+    want, _ = dkv.dkv_paged_decode(p, q.contiguous(), c.k, c.v, c.table.cuda(), c.dev([130, 70]))
+    assert torch.equal(out, want)
+
+
+def test_decode_of_many_sequences_covers_every_deal():
+    """Units of every length dealt to the multiprocessors: some runs hold many units, some a part of one."""
+    lens = [(i * 37) % 400 for i in range(700)]
+    c = R.Cache(lens, 1, 64, 32, "bf16", seed=6)
+    p = c.layout(2)
+    ws = workspace(p)
+    q = queries((c.B, 2, 64), c.dt, 9)
+    out, lse = dkv.dkv_paged_decode(p, q.cuda(), c.k, c.v, c.table.cuda(), c.dev(lens), workspace=ws)
+    no_fault(ws)
+    out, lse = out.cpu(), lse.cpu()
+    for b in range(c.B):
+        ref = R.attend(q[b].double(), c.K[b][0], c.V[b][0], torch.full((2,), lens[b] - 1), 0, 0)
+        R.check_rows(out[b], lse[b], ref, 64, c.dt, 2.0 ** -16, f"sequence {b}")
+
+
+@pytest.mark.parametrize("dtype,hkv,hq,lens,window,sinks", [
+    ("fp16", 2, 12, [60000, 20000], 0, 0), ("bf16", 8, 8, [30001], 0, 0), ("fp16", 4, 8, [25000, 9000, 31000], 20000, 100)])
+@pytest.mark.parametrize("weighed", [False, True])
+def test_decode_of_long_sequences(dtype, hkv, hq, lens, window, sinks, weighed):
+    """Many tiles in a row on every multiprocessor: the ring of tiles goes round several times."""
+    c = R.Cache(lens, hkv, 128, 256, dtype, seed=8)
+    p = c.layout(hq, window, sinks)
+    ws = workspace(p, weighed)
+    q = queries((c.B, hq, 128), c.dt, 10)
+    weights = torch.zeros(c.B, hkv, c.width * 256, device="cuda") if weighed else None
+    out, lse = dkv.dkv_paged_decode(p, q.cuda(), c.k, c.v, c.table.cuda(), c.dev(lens), weights=weights, workspace=ws)
+    no_fault(ws)
+    for b in range(c.B):
+        for h in range(hkv):
+            added, big = torch.zeros(lens[b], dtype=torch.float64), 0.0
+            for j in range(h * hq // hkv, (h + 1) * hq // hkv):
+                ref = R.attend(q[b, j:j + 1].double(), c.K[b][h], c.V[b][h], torch.tensor([lens[b] - 1]), window, sinks)
+                R.check_rows(out[b, j:j + 1], lse[b, j:j + 1], ref, 128, c.dt, 2.0 ** -16 if dtype == "bf16" else 2.0 ** -21)
+                added += ref[2][0]
+                big = max(big, ref[4])
+            if weighed:
+                tol = (2 * R.score_error(128, big) + 2.0 ** -20 * (1 + math.log(lens[b]))) * added + 2.0 ** -40
+                assert bool(((weights[b, h, :lens[b]].double().cpu() - added).abs() <= tol).all())
+
+
+def test_lengths_and_pages_out_of_range_are_reported():
+    c = R.Cache([100, 50], 1, 64, 16, seed=7)
+    p = c.layout(1)
+    ws = workspace(p)
+    q = queries((2, 1, 64), c.dt, 3)
+    for lens in ([100, -5], [c.width * 16 + 9, 50]):
+        table = c.table.clone()
+        table[table < 0] = 0
+        out, lse = dkv.dkv_paged_decode(p, q.cuda(), c.k, c.v, table.cuda(), c.dev(lens), workspace=ws)
+        assert dkv.dkv_get_error(ws) == (dkv.DKV_ERR_DEVICE, dkv.DKV_DEVERR_INDEX)
+        good = 0 if lens[1] < 0 else 1
+        ref = R.attend(q[good].double(), c.K[good][0], c.V[good][0], torch.tensor([c.lens[good] - 1]), 0, 0)
+        R.check_rows(out[good], lse[good], ref, 64, c.dt, 2.0 ** -21)
+        if lens[1] < 0:
+            assert float(out[1].abs().max()) == 0 and bool(torch.isneginf(lse[1]).all())
+    table = c.table.clone()
+    table[0, 2] = c.n_pages + 1  # read as a page of zeros: scores 0, values 0
+    out, lse = dkv.dkv_paged_decode(p, q.cuda(), c.k, c.v, table.cuda(), c.dev([100, 50]), workspace=ws)
+    assert dkv.dkv_get_error(ws) == (dkv.DKV_ERR_DEVICE, dkv.DKV_DEVERR_INDEX)
+    K, V = c.K[0][0].clone(), c.V[0][0].clone()
+    K[32:48] = V[32:48] = 0
+    R.check_rows(out[0], lse[0], R.attend(q[0].double(), K, V, torch.tensor([99]), 0, 0), 64, c.dt, 2.0 ** -21)
+
+
+# ---------------------------------------------------------------- prefill and weights
+
+PREFILL = [
+    # dtype, d, hq, hkv, page, order, lens, q_lens (None: all Tq), Tq, window, sinks
+    ("fp16", 128, 2, 1, 64, "head", [128], None, 128, 0, 0),
+    ("bf16", 128, 2, 1, 64, "head", [300], None, 300, 0, 0),
+    ("fp16", 64, 1, 1, 16, "token", [1], None, 1, 0, 0),
+    ("fp16", 128, 3, 1, 32, "token", [513], None, 513, 0, 0),
+    ("bf16", 64, 12, 2, 128, "head", [700, 129, 64], [300, 129, 1], 300, 0, 0),
+    ("fp16", 64, 5, 1, 256, "token", [1000, 0, 40], [17, 0, 33], 33, 0, 0),
+    ("bf16", 128, 8, 8, 16, "token", [600], None, 600, 128, 0),
+    ("fp16", 128, 12, 2, 64, "head", [900, 500], [900, 257], 900, 100, 4),
+    ("bf16", 64, 7, 1, 32, "head", [777], None, 400, 33, 130),
+    ("fp16", 128, 4, 1, 16, "head", [1200], None, 260, 1, 1),
+    ("bf16", 128, 2, 2, 64, "token", [640], None, 640, 300, 300),
+    ("fp16", 64, 6, 3, 32, "token", [20, 300], [50, 50], 50, 40, 2),   # sequence 0: 30 queries before its first token
+]
+
+
+@pytest.mark.parametrize("dtype,d,hq,hkv,page,order,lens,q_lens,Tq,window,sinks", PREFILL)
+def test_prefill_and_weights(dtype, d, hq, hkv, page, order, lens, q_lens, Tq, window, sinks):
+    c = R.Cache(lens, hkv, d, page, dtype, order, seed=Tq)
+    p = c.layout(hq, window, sinks)
+    ws = workspace(p)
+    n_q = q_lens or [Tq] * c.B
+    q = queries((c.B, Tq, hq, d), c.dt, 11).transpose(1, 2)
+    for b, n in enumerate(n_q):
+        q[b, :, n:] = float("nan")  # rows of padding
+    out = torch.full((c.B, Tq, hq, d), 7.0, dtype=c.dt, device="cuda").transpose(1, 2)
+    lse = torch.full((c.B, hq, Tq), 7.0, device="cuda")
+    table = c.hidden_table([n - m for n, m in zip(lens, n_q)], window, sinks)
+    ql = None if q_lens is None else c.dev(q_lens)
+    qd = q.cuda()
+    dkv.dkv_paged_prefill(p, qd, c.k, c.v, table, c.dev(lens), q_lens=ql, out=out, lse=lse, workspace=ws)
+    no_fault(ws)
+    old = torch.rand(c.B, hkv, c.width * page, generator=torch.Generator().manual_seed(1))
+    weights = old.cuda()
+    dkv.dkv_paged_weights(p, qd, lse, c.k, table, c.dev(lens), weights, q_lens=ql, workspace=ws)
+    no_fault(ws)
+    for b in range(c.B):
+        pos = torch.arange(n_q[b]) + lens[b] - n_q[b]
+        assert bool((out[b, :, n_q[b]:] == 7).all()) and bool((lse[b, :, n_q[b]:] == 7).all())
+        for h in range(hkv):
+            added, big, lse_off = torch.zeros(c.width * page, dtype=torch.float64), 0.0, 0.0
+            for j in range(h * hq // hkv, (h + 1) * hq // hkv):
+                ref = R.attend(q[b, j, :n_q[b]].double(), c.K[b][h], c.V[b][h], pos, window, sinks)
+                R.check_rows(out[b, j, :n_q[b]], lse[b, j, :n_q[b]], ref, d, c.dt, torch.finfo(c.dt).eps / 2,
+                             f"sequence {b} head {j}")
+                added[:lens[b]] += ref[2].sum(0)
+                big = max(big, ref[4])
+            want = old[b, h].double() + added
+            rows = n_q[b] * hq // hkv
+            # each weight: its score's and the lse's errors; fp32 adds `rows` weights in 8 partial sums
+            tol = (2 * R.score_error(d, big) + 2.0 ** -20 * (1 + math.log(max(2, lens[b]))) + 2.0 ** -23 * (rows / 8 + 8)) * added + 2.0 ** -22 * want
+            err = (weights[b, h].double().cpu() - want).abs()
+            assert bool((err <= tol).all()), f"weights of sequence {b} head {h}: {float((err - tol).max())}"
+
+
+@pytest.mark.parametrize("dtype,d,hq,window,sinks", [("fp16", 128, 2, 0, 0), ("bf16", 64, 1, 90, 3), ("bf16", 128, 4, 200, 20)])
+def test_prefill_rows_are_not_touched_by_keys_they_do_not_see(dtype, d, hq, window, sinks):
+    """NaN and infinities in the values (and keys) of some tokens reach the rows that see them, and no other."""
+    n, bad = 500, [3, 130, 260, 261, 444]
+    c = R.Cache([n], 1, d, 64, dtype, seed=2)
+    p = c.layout(hq, window, sinks)
+    q = queries((1, hq, n, d), c.dt, 5).cuda()
+    clean, clean_lse = dkv.dkv_paged_prefill(p, q, c.k, c.v, c.table.cuda(), c.dev([n]))
+    k, v = c.k.clone(), c.v.clone()
+    for i, t in enumerate(bad):
+        where = (int(c.table[0, t // 64]), 0, t % 64)
+        if i % 2 == 0:
+            v[where] = torch.tensor([float("nan"), float("inf")], dtype=c.dt).repeat(d // 2)
+        else:
+            k[where] = float("nan")
+    out, lse = dkv.dkv_paged_prefill(p, q, k, v, c.table.cuda(), c.dev([n]))
+    m = R.seen(torch.arange(n), n, window, sinks)
+    sees_v = m[:, [t for i, t in enumerate(bad) if i % 2 == 0]].any(1)
+    sees_k = m[:, [t for i, t in enumerate(bad) if i % 2 == 1]].any(1)
+    good = (~sees_v & ~sees_k).cuda()
+    assert torch.equal(out[0][:, good], clean[0][:, good])
+    assert torch.equal(lse[0][:, good], clean_lse[0][:, good])
+    assert bool(torch.isnan(out[0][:, sees_k.cuda()]).all()) and bool(torch.isnan(lse[0][:, sees_k.cuda()]).all())
+    # the values reach the rows that see them: NaN stays NaN (channels 0, 2, ...), +inf stays +inf unless a NaN joins
+    only_v = (sees_v & ~sees_k).cuda()
+    assert bool(torch.isnan(out[0][:, only_v][..., 0::2]).all())
+    assert not bool(torch.isfinite(out[0][:, only_v][..., 1::2]).any())
+    assert bool(torch.isfinite(lse[0][:, only_v]).all())
+
+
+def test_prefill_adds_large_values_of_edge_tiles_exactly():
+    """A row that sees one infinite channel keeps its other channels."""
+    n, d = 140, 64
+    c = R.Cache([n], 1, d, 32, "fp16", seed=12)
+    p = c.layout(1)
+    q = queries((1, 1, n, d), c.dt, 5)
+    v = c.v.clone()
+    t = 100
+    v[int(c.table[0, t // 32]), 0, t % 32, 5] = float("-inf")
+    out, lse = dkv.dkv_paged_prefill(p, q.cuda(), c.k, v, c.table.cuda(), c.dev([n]))
+    assert bool((out[0, 0, t:, 5] == float("-inf")).all())
+    ref = R.attend(q[0, 0].double(), c.K[0][0], c.V[0][0], torch.arange(n), 0, 0)
+    keep = [i for i in range(d) if i != 5]
+    sub = (ref[0][:, keep], ref[1], ref[2], ref[3][:, keep], ref[4])
+    R.check_rows(out[0, 0][:, keep], lse[0, 0], sub, d, c.dt, torch.finfo(c.dt).eps / 2)
+
+
+# ---------------------------------------------------------------- evict
+
+def _evict_check(c, p, weights, budget, first, recent, kept, new_lens, new_weights, table, k, v):
+    """k, v: the pools before; the kept rows lie at positions 0.. of `table`."""
+    for b, n in enumerate(c.lens):
+        m = min(n, budget)
+        assert int(new_lens[b]) == m
+        for h in range(c.hkv):
+            want = R.evict(weights[b, h, :n].tolist(), n, budget, first, recent)
+            assert kept[b, h, :m].tolist() == want, f"sequence {b} head {h}"
+            assert bool((kept[b, h, m:] == -1).all())
+            t, j = torch.tensor(want, dtype=torch.long), torch.arange(m)
+            for pool, before in ((c.k, k), (c.v, v)):
+                now = pool.cpu()[table[b].long()[j // c.page], h, j % c.page]
+                assert torch.equal(now.view(torch.int16), before.cpu()[c.table[b].long()[t // c.page], h, t % c.page].view(torch.int16))
+            got = new_weights[b, h].cpu()
+            w = weights[b, h][t]
+            assert torch.equal(got[:m].nan_to_num(-1.0), w.nan_to_num(-1.0)) and bool((got[m:] == 0).all())
+
+
+@pytest.mark.parametrize("dtype,d,hkv,page,order,lens,budget,first,recent", [
+    ("fp16", 128, 2, 64, "head", [300, 200, 0, 128, 129], 128, 4, 16),
+    ("bf16", 64, 1, 16, "token", [1000], 17, 0, 0),
+    ("fp16", 64, 3, 32, "token", [65, 64, 40], 64, 32, 32),       # no room for a candidate
+    ("bf16", 128, 1, 256, "head", [5000, 2100], 2047, 1, 700),
+    ("fp16", 128, 2, 16, "head", [33, 2], 1, 0, 1),
+    ("bf16", 64, 2, 64, "head", [700], 500, 0, 0),
+])
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("kind", ["spread", "ties"])
+def test_evict(dtype, d, hkv, page, order, lens, budget, first, recent, in_place, kind):
+    keep_pages = -(-budget // page)
+    width = max(max(-(-n // page) for n in lens), keep_pages)
+    c = R.Cache(lens, hkv, d, page, dtype, order, seed=budget, spare=len(lens) * keep_pages, width=width)
+    p = c.layout(hkv)
+    ws = workspace(p)
+    g = torch.Generator().manual_seed(5)
+    weights = torch.rand(c.B, hkv, width * page, generator=g) ** 8
+    if kind == "ties":  # few values, zeros of both signs, infinities, NaN, negative ones
+        weights = torch.tensor([0.0, -0.0, 1.0, 2.0, math.inf, -math.inf, math.nan, -1.0, 1e-40])[
+            torch.randint(0, 9, weights.shape, generator=g)]
+    lens_d, w_d, k, v = c.dev(lens), weights.cuda(), c.k.clone(), c.v.clone()
+    table = c.table.cuda()
+    if in_place:
+        kept, new_lens, new_weights = dkv.dkv_paged_evict(p, c.k, c.v, table, lens_d, w_d, budget, first, recent, table,
+                                                          new_lens=lens_d, new_weights=w_d, workspace=ws)
+        assert new_lens is lens_d and new_weights is w_d
+        to = c.table
+    else:
+        to = c.free[:c.B * keep_pages].view(c.B, keep_pages)
+        kept, new_lens, new_weights = dkv.dkv_paged_evict(p, c.k, c.v, table, lens_d, w_d, budget, first, recent, to.cuda(),
+                                                          workspace=ws)
+    no_fault(ws)
+    _evict_check(c, p, weights, budget, first, recent, kept.cpu(), new_lens.cpu(), new_weights, to, k, v)
+
+
+# ---------------------------------------------------------------- together
+
+def test_a_serving_run():
+    """Prompts enter in two chunks, their last tokens weigh the cache, it is cut down in place, and tokens
+    follow one by one with their weights, through a second eviction: every step against 64 bits."""
+    B, hq, hkv, d, page, budget, first, recent = 3, 6, 2, 128, 32, 160, 4, 32
+    dt = torch.bfloat16
+    lens0, width = [300, 170, 90], 12
+    g = torch.Generator().manual_seed(77)
+    table = torch.randperm(B * width, generator=g).int().view(B, width).cuda()
+    k, v = (torch.full((B * width, hkv, page, d), float("nan"), dtype=dt, device="cuda") for _ in range(2))
+    p = dkv.dkv_paged_layout(k, B, hq, width, window=150, sinks=first)
+    ws = workspace(p, True)
+    weights = torch.zeros(B, hkv, width * page, device="cuda")
+    K = [[torch.empty(0, d, dtype=torch.float64) for _ in range(hkv)] for _ in range(B)]
+    V = [[torch.empty(0, d, dtype=torch.float64) for _ in range(hkv)] for _ in range(B)]
+    W = [[torch.empty(0, dtype=torch.float64) for _ in range(hkv)] for _ in range(B)]
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    u = torch.finfo(dt).eps / 2
+
+    def add(counts):
+        n = max(counts)
+        kn, vn = (torch.randn(B, n, hkv, d, generator=g).to(dt).transpose(1, 2) for _ in range(2))
+        cn = torch.tensor(counts, dtype=torch.int32, device="cuda")
+        dkv.dkv_paged_append(p, kn.cuda(), vn.cuda(), k, v, table, lens, counts=cn, workspace=ws)
+        lens.add_(cn)
+        for b in range(B):
+            for h in range(hkv):
+                K[b][h] = torch.cat([K[b][h], kn[b, h, :counts[b]].double()])
+                V[b][h] = torch.cat([V[b][h], vn[b, h, :counts[b]].double()])
+                W[b][h] = torch.cat([W[b][h], torch.zeros(counts[b], dtype=torch.float64)])
+        return cn
+
+    def cut():
+        kept, _, _ = dkv.dkv_paged_evict(p, k, v, table, lens, weights, budget, first, recent, table, new_lens=lens,
+                                         new_weights=weights, workspace=ws)
+        kept = kept.cpu()
+        for b in range(B):
+            for h in range(hkv):
+                n = W[b][h].numel()
+                m = min(n, budget)
+                t = kept[b, h, :m].long()
+                # the choice is made by the fp32 weights: against the 64-bit ones it may differ among near equals only
+                order = W[b][h].clone()
+                order[:first], order[n - recent:] = math.inf, math.inf
+                assert float(order[t].min()) >= float(order.sort(descending=True).values[m - 1]) - 1e-3
+                assert bool((t[1:] > t[:-1]).all())
+                K[b][h], V[b][h], W[b][h] = K[b][h][t], V[b][h][t], W[b][h][t]
+
+    for part in range(2):
+        counts = [n // 2 if part == 0 else n - n // 2 for n in lens0]
+        cn = add(counts)
+        q = (torch.randn(B, hq, max(counts), d, generator=g) * 2).to(dt)
+        out, lse = dkv.dkv_paged_prefill(p, q.cuda(), k, v, table, lens, q_lens=cn, workspace=ws)
+        if part == 1:
+            dkv.dkv_paged_weights(p, q.cuda(), lse, k, table, lens, weights, q_lens=cn, workspace=ws)
+        for b in range(B):
+            n = K[b][0].shape[0]
+            for j in range(hq):
+                h = j // 3
+                ref = R.attend(q[b, j, :counts[b]].double(), K[b][h], V[b][h], torch.arange(n - counts[b], n), 150, first)
+                R.check_rows(out[b, j, :counts[b]], lse[b, j, :counts[b]], ref, d, dt, u, f"chunk {part} {b} {j}")
+                if part == 1:
+                    W[b][h] += ref[2].sum(0)
+    cut()
+    for step in range(40):
+        add([1] * B)
+        q = (torch.randn(B, hq, d, generator=g) * 2).to(dt)
+        out, lse = dkv.dkv_paged_decode(p, q.cuda(), k, v, table, lens, weights=weights, workspace=ws)
+        for b in range(B):
+            n = K[b][0].shape[0]
+            for j in range(hq):
+                h = j // 3
+                ref = R.attend(q[b, j:j + 1].double(), K[b][h], V[b][h], torch.tensor([n - 1]), 150, first)
+                R.check_rows(out[b, j:j + 1], lse[b, j:j + 1], ref, d, dt, 2.0 ** -16, f"step {step} {b} {j}")
+                W[b][h] += ref[2][0]
+        if step == 30:
+            cut()
+    no_fault(ws)
+    assert lens.tolist() == [169, 169, 130] or lens.tolist() == [n.numel() for n in (W[0][0], W[1][0], W[2][0])]
+    for b in range(B):
+        for h in range(hkv):
+            n = W[b][h].numel()
+            assert float((weights[b, h, :n].double().cpu() - W[b][h]).abs().max()) < 1e-3
+            assert bool((weights[b, h, n:] == 0).all())
+
+
+def test_calls_in_a_graph_and_on_a_stream_of_their_own():
+    c = R.Cache([400, 90], 2, 128, 64, "fp16", seed=9)
+    p = c.layout(4, window=128, sinks=4)
+    table, lens = c.table.cuda(), c.dev(c.lens)
+    ws = workspace(p, True)
+    q = queries((2, 4, 128), c.dt, 1).cuda()
+    qp = queries((2, 4, 40, 128), c.dt, 2).cuda()
+    ql = c.dev([40, 33])
+    weights = torch.zeros(2, 2, c.width * 64, device="cuda")
+    out, lse = torch.zeros_like(q), torch.zeros(2, 4, device="cuda")
+    po, pl = torch.zeros_like(qp), torch.zeros(2, 4, 40, device="cuda")
+
+    def step():
+        dkv.dkv_paged_decode(p, q, c.k, c.v, table, lens, out=out, lse=lse, weights=weights, workspace=ws)
+        dkv.dkv_paged_prefill(p, qp, c.k, c.v, table, lens, q_lens=ql, out=po, lse=pl, workspace=ws)
+        dkv.dkv_paged_weights(p, qp, pl, c.k, table, lens, weights, q_lens=ql, workspace=ws)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    want = [x.clone() for x in (out, lse, po, pl, weights)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for x in (out, lse, po, pl, weights):
+        x.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    for x, y in zip((out, lse, po, pl, weights), want):
+        assert torch.equal(x, y)
+    # new contents of the same buffers are taken up by the next replay
+    lens.copy_(c.dev([399, 1]))
+    graph.replay()
+    torch.cuda.synchronize()
+    fresh, _ = dkv.dkv_paged_decode(p, q, c.k, c.v, table, lens)
+    assert torch.equal(out, fresh) and not torch.equal(out, want[0])
+    no_fault(ws)
+
+
+def test_pools_past_two_to_the_31_elements():
+    """Offsets inside a pool that do not fit 32 bits: a sequence on the first and last pages."""
+    page, hkv, d = 256, 8, 128
+    n_pages = 2 ** 31 // (page * hkv * d) + 40
+    k, v = (torch.empty(n_pages, hkv, page, d, dtype=torch.float16, device="cuda") for _ in range(2))
+    lens, B = [700, 300], 2
+    table = torch.tensor([[n_pages - 1, 0, n_pages - 7], [n_pages - 3, 5, -1]], dtype=torch.int32, device="cuda")
+    p = dkv.dkv_paged_layout(k, B, hkv, 3)
+    ws = workspace(p)
+    kn, vn = (queries((B, hkv, 700, d), torch.float16, s, 1.0) for s in (1, 2))
+    counts = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    dkv.dkv_paged_append(p, kn.cuda(), vn.cuda(), k, v, table, torch.zeros_like(counts), counts=counts, workspace=ws)
+    q = queries((B, hkv, d), torch.float16, 3)
+    out, lse = dkv.dkv_paged_decode(p, q.cuda(), k, v, table, counts, workspace=ws)
+    qp = queries((B, hkv, 5, d), torch.float16, 4)
+    po, pl = dkv.dkv_paged_prefill(p, qp.cuda(), k, v, table, counts, workspace=ws)
+    no_fault(ws)
+    for b in range(B):
+        for h in range(hkv):
+            K, V = kn[b, h, :lens[b]].double(), vn[b, h, :lens[b]].double()
+            R.check_rows(out[b, h:h + 1], lse[b, h:h + 1], R.attend(q[b, h:h + 1].double(), K, V, torch.tensor([lens[b] - 1]), 0, 0),
+                         d, torch.float16, 2.0 ** -21)
+            R.check_rows(po[b, h], pl[b, h], R.attend(qp[b, h].double(), K, V, torch.arange(lens[b] - 5, lens[b]), 0, 0),
+                         d, torch.float16, 2.0 ** -11)
