@@ -129,6 +129,23 @@ __device__ inline void sts128(uint32_t addr, uint4 v) {
 // ---------------------------------------------------------------------------
 // launchers
 // ---------------------------------------------------------------------------
+// a grid that may start before the one in front of it on the stream has finished, and calls
+// griddep_wait() before it reads what that one wrote
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = programmatic_launch() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 struct PagedMaps {  // tensor maps of the pools: boxes of 64 channels x min(page_size, 64) slots
   CUtensorMap k, v;
 };
@@ -154,8 +171,7 @@ cudaError_t launch_paged_prefill(const PagedArgs& a, int d, int dtype, const Pag
 int paged_weights_rows(int Tq);
 cudaError_t launch_paged_weights(const PagedArgs& a, int d, int dtype, const CUtensorMap& kmap, const CUtensorMap& qmap,
                                  const PagedQuery& q, const float* lse, float* weights, cudaStream_t s);
-// evict: workspace [header][kept counts int32 [B]]
-size_t paged_evict_ws_bytes(const PagedArgs& a);
+size_t paged_evict_ws_bytes(const PagedArgs& a, int d);
 struct PagedEvict {
   int budget, first, recent, new_max_pages;
   const float* weights;

@@ -417,21 +417,6 @@ __global__ void __launch_bounds__(kScoreThreads) paged_score_kernel(DecArgs p, f
 
 size_t off_scores(int d) { return round_up(kWsHeader + (size_t)2 * sm_count() * (16 + 8 * d) * 4, 256); }
 
-template <typename K, typename... A>
-cudaError_t launch_pdl(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = programmatic_launch() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <typename T, int D>
 cudaError_t launch_decode_td(const DecArgs& p, const PagedMaps& m, float* weights, cudaStream_t s) {
   const int ncta = sm_count();
@@ -441,11 +426,11 @@ cudaError_t launch_decode_td(const DecArgs& p, const PagedMaps& m, float* weight
   if (e != cudaSuccess) return e;
   paged_decode_kernel<T, D><<<ncta, kDecThreads, smem, s>>>(p, m.k, m.v);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  e = launch_pdl(paged_combine_kernel<T, D>, dim3(ncta, D / kCombCols), kCombThreads,
+  e = launch_dependent(paged_combine_kernel<T, D>, dim3(ncta, D / kCombCols), kCombThreads,
                  ((size_t)p.a.B + 1 + 8 * ncta + 16) * 4, s, p, ncta);
   if (e != cudaSuccess || !weights) return e;
   const int per = kScoreThreads * kScorePer;
-  return launch_pdl(paged_score_kernel, dim3((p.a.cap + per - 1) / per, p.a.B * p.a.Hkv), kScoreThreads, 0, s, p, weights);
+  return launch_dependent(paged_score_kernel, dim3((p.a.cap + per - 1) / per, p.a.B * p.a.Hkv), kScoreThreads, 0, s, p, weights);
 }
 
 }  // namespace

@@ -1,20 +1,31 @@
 // dkv_paged_evict: keep the heaviest tokens of every (sequence, KV head) and move them
 // together.
 //
-// select: the k-th largest weight of a unit by radix selection over an order-preserving
-// integer image of the weights (three passes of 11, 11 and 10 bits, a histogram in shared
-// memory each), then one ordered pass that writes the kept positions, ascending.
-// compact: kept rows to positions 0, 1, ...  Position j is filled from a position >= j, so
-// a CTA that walks its rows in order, reading a batch before it writes it, can compact in
-// place; the CTAs of a unit split the row's bytes, never its tokens.
+// select: one CTA per unit brings the weights' order-preserving integer images into shared
+// memory, finds the smallest image that stays by radix selection (three passes of 11, 11 and 10
+// bits over a histogram), then writes the kept positions, ascending, from one scan that counts
+// certain and equal images side by side.  Bound by the latency of its passes.
+//
+// move: a gather of budget rows of K and V per unit, bound by memory (each kept row read and
+// written once).  A CTA moves one chunk of kMoveBytes of K and as much of V, whole rows, all of
+// it in flight at once.  Position j is filled from a position >= j, so that a sequence compacted
+// in place needs an order only between a chunk's write and the reads of the chunks before it:
+// CTAs take their chunks from a counter, unit by unit and upwards, read, raise the chunk's flag,
+// wait for the flags of those earlier chunks of the unit whose rows come from where this one
+// writes, and write.  A CTA waits only for CTAs that started before it and that read without
+// waiting, so every wait ends.
 #include "paged.cuh"
 
 namespace dkv {
 namespace {
 
 constexpr int kSelThreads = 1024, kSelBins = 2048;
-constexpr int kMoveThreads = 256, kMoveRows = 8;  // rows in flight per thread
-constexpr int kMovePiece = 64;                    // bytes of a row one CTA moves
+constexpr int kSelPer = 8;                        // consecutive tokens of a thread in the ordered pass
+constexpr int kSelStage = 24 * 1024;              // images held in shared memory (two CTAs fit a multiprocessor)
+constexpr int kMoveThreads = 256, kMoveVec = 4;   // 16-byte pieces of K, and as many of V, per thread
+constexpr int kMoveBytes = kMoveThreads * kMoveVec * 16;
+constexpr int kZeroChunk = 8192;                  // weights zeroed by one CTA
+constexpr int kPollLimit = 1 << 22;               // polls of a flag before a wait gives up
 
 // a < b as floats iff image(a) < image(b); -0 is 0, NaN is -infinity
 __device__ inline uint32_t weight_image(float w) {
@@ -24,14 +35,37 @@ __device__ inline uint32_t weight_image(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(PagedArgs a, PagedEvict e, int32_t* __restrict__ counts) {
+// Workspace: [header][counts int32 [B]][ticket][flags [unit][chunk]]
+struct EvictPlan {
+  int rows, chunks, zeros;  // rows of a chunk, chunks of a unit's rows, chunks of its weights' tail
+  size_t off_ticket, off_flags, bytes;
+};
+__host__ __device__ inline EvictPlan evict_plan(int B, int Hkv, int cap, int d, int budget) {
+  EvictPlan p;
+  p.rows = kMoveBytes / (2 * d);
+  p.chunks = (budget + p.rows - 1) / p.rows;
+  p.zeros = (cap + kZeroChunk - 1) / kZeroChunk;
+  p.off_ticket = round_up(kWsHeader + (size_t)B * 4, 16);
+  p.off_flags = p.off_ticket + 16;
+  p.bytes = p.off_flags + (size_t)B * Hkv * p.chunks * 4;
+  return p;
+}
+
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(PagedArgs a, PagedEvict e, EvictPlan plan,
+                                                                  uint8_t* __restrict__ ws) {
+  extern __shared__ __align__(16) uint32_t img[];  // images of the unit's weights (when they fit)
   __shared__ int hist[kSelBins];
   __shared__ int wsum[32];
   __shared__ int sh_digit, sh_above;
   const int u = blockIdx.x, b = u / a.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  griddep_launch();
   const int len = paged_len(a, b), n = min(len, e.budget);
   int32_t* kept = e.kept + (size_t)u * e.budget;
-  if (u % a.Hkv == 0 && tid == 0) counts[b] = n;
+  // what the move kernel starts from
+  if (u % a.Hkv == 0 && tid == 0) reinterpret_cast<int32_t*>(ws + kWsHeader)[b] = n;
+  if (u == 0 && tid == 0) *reinterpret_cast<uint32_t*>(ws + plan.off_ticket) = 0;
+  uint32_t* flags = reinterpret_cast<uint32_t*>(ws + plan.off_flags) + (size_t)u * plan.chunks;
+  for (int i = tid; i < plan.chunks; i += kSelThreads) flags[i] = 0;
   for (int j = n + tid; j < e.budget; j += kSelThreads) kept[j] = -1;
   if (len <= e.budget) {
     for (int j = tid; j < n; j += kSelThreads) kept[j] = j;
@@ -40,24 +74,32 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(PagedArgs a, 
   // candidates [c0, c1); the tokens around them stay whatever they weigh
   const int c0 = e.first, c1 = len - e.recent;
   const float* w = e.weights + (size_t)u * a.cap;
+  const bool staged = len <= kSelStage;
+  if (staged) {
+    for (int t = tid; t < len; t += kSelThreads) img[t] = weight_image(__ldg(w + t));
+    __syncthreads();
+  }
+  auto image = [&](int t) { return staged ? img[t] : weight_image(__ldg(w + t)); };
   int k = e.budget - e.first - e.recent;  // candidates to keep: 0 <= k < c1 - c0
-  uint32_t thr = 0, mask = 0;             // the k-th largest image, found from its high bits down
+  uint32_t thr = 0xffffffffu, mask = 0;   // the smallest image that stays (none above it when k is 0)
   if (k > 0) {
+    thr = 0;
     const int shift[3] = {21, 10, 0}, bits[3] = {11, 11, 10};
+#pragma unroll
     for (int p = 0; p < 3; ++p) {
       const int bins = 1 << bits[p];
       for (int i = tid; i < bins; i += kSelThreads) hist[i] = 0;
       __syncthreads();
       for (int t = c0 + tid; t < c1; t += kSelThreads) {
-        const uint32_t x = weight_image(__ldg(w + t));
+        const uint32_t x = image(t);
         if ((x & mask) == thr) atomicAdd(&hist[(x >> shift[p]) & (bins - 1)], 1);
       }
       __syncthreads();
-      // the digit with fewer than k images above it and at least k down to it: thread i takes
-      // bins - 1 - (per i), ... downwards
-      const int per = (bins + kSelThreads - 1) / kSelThreads, top = bins - 1 - tid * per;
+      // the digit with fewer than k images above it and at least k down to it: thread i takes the
+      // i-th group of bins from the top
+      const int per = bins / kSelThreads, top = bins - 1 - tid * per;
       int sum = 0;
-      for (int i = 0; i < per && top - i >= 0; ++i) sum += hist[top - i];
+      for (int i = 0; i < per; ++i) sum += hist[top - i];
       int scan = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -66,8 +108,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(PagedArgs a, 
       }
       if (lane == 31) wsum[warp] = scan;
       __syncthreads();
-      int above = scan - sum;
-      for (int i = 0; i < warp; ++i) above += wsum[i];
+      int before = lane < warp ? wsum[lane] : 0;
+      int above = scan - sum + __reduce_add_sync(0xffffffffu, before);
       if (above < k && above + sum >= k) {
         int i = 0;
         while (above + hist[top - i] < k) above += hist[top - i++];
@@ -81,120 +123,152 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(PagedArgs a, 
       __syncthreads();
     }
   }
-  // every image above thr stays, and the first k that equal it (none when no candidate stays)
-  const bool any = e.budget > e.first + e.recent;
-  int out = 0, ties = 0;  // kept positions and equal images of the chunks before
-  for (int base = 0; base < len; base += kSelThreads) {
-    const int t = base + tid;
-    int keep = 0, tie = 0;
-    if (t < len) {
-      if (t < c0 || t >= c1) keep = 1;
-      else if (any) {
-        const uint32_t x = weight_image(__ldg(w + t));
-        keep = x > thr;
-        tie = x == thr;
+  // every image above thr stays, and the first k that equal it
+  int out = 0, ties = 0;  // certain and equal images of the chunks before
+  for (int base = 0; base < len; base += kSelThreads * kSelPer) {
+    const int t0 = base + tid * kSelPer;
+    uint32_t keep = 0, tie = 0;  // bits of this thread's tokens
+#pragma unroll
+    for (int i = 0; i < kSelPer; ++i) {
+      const int t = t0 + i;
+      if (t >= len) continue;
+      if (t < c0 || t >= c1) keep |= 1u << i;
+      else {
+        const uint32_t x = image(t);
+        keep |= (x > thr ? 1u : 0u) << i;
+        tie |= (x == thr ? 1u : 0u) << i;
       }
     }
-    // both counts at once: ties of the chunk before this token, then kept ones
-    auto scan_excl = [&](int v, int* total) {
-      int s = v;
+    // both counts in one scan (a chunk has kSelThreads * kSelPer = 2^13 tokens at most)
+    const int v = __popc(keep) | __popc(tie) << 16;
+    int s = v;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += y;
-      }
-      __syncthreads();
-      if (lane == 31) wsum[warp] = s;
-      __syncthreads();
-      int before = s - v, all = 0;
-      for (int i = 0; i < 32; ++i) {
-        if (i < warp) before += wsum[i];
-        all += wsum[i];
-      }
-      *total = all;
-      return before;
-    };
-    int nt, nk;
-    const int tb = scan_excl(tie, &nt);
-    if (tie && ties + tb < k) keep = 1;
-    const int kb = scan_excl(keep, &nk);
-    if (keep) kept[out + kb] = t;
-    ties += nt;
-    out += nk;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    if (lane == 31) wsum[warp] = s;
+    __syncthreads();
+    const int part = wsum[lane];
+    const int all = __reduce_add_sync(0xffffffffu, part);
+    const int before = s - v + __reduce_add_sync(0xffffffffu, lane < warp ? part : 0);
+    int nk = out + (before & 0xffff), nt = ties + (before >> 16);
+#pragma unroll
+    for (int i = 0; i < kSelPer; ++i) {
+      const bool kp = keep >> i & 1u, te = tie >> i & 1u;
+      if (kp || (te && nt < k)) kept[nk + min(nt, k)] = t0 + i;
+      nk += kp;
+      nt += te;
+    }
+    out += all & 0xffff;
+    ties += all >> 16;
+    __syncthreads();
   }
 }
 
-// grid (units, 2 * row bytes / kMovePiece + 1): K pieces, V pieces, the weights
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(PagedArgs a, PagedEvict e, int pieces,
-                                                                 uint8_t* __restrict__ kp, uint8_t* __restrict__ vp,
-                                                                 const int32_t* __restrict__ counts) {
-  const int u = blockIdx.x, b = u / a.Hkv, h = u % a.Hkv, tid = threadIdx.x;
-  const int n = __ldg(counts + b);
+template <int D>
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(PagedArgs a, PagedEvict e, EvictPlan plan,
+                                                                 uint4* __restrict__ kp, uint4* __restrict__ vp,
+                                                                 uint8_t* __restrict__ ws) {
+  constexpr int R = D / 8, kRows = kMoveThreads / R;  // pieces of a row, rows of one access
+  __shared__ uint32_t sh_ticket;
+  const int tid = threadIdx.x;
+  griddep_wait();
+  if (tid == 0) sh_ticket = atomicAdd(reinterpret_cast<uint32_t*>(ws + plan.off_ticket), 1u);
+  __syncthreads();
+  const int per = plan.chunks + plan.zeros;
+  const int u = (int)(sh_ticket / (uint32_t)per), c = (int)(sh_ticket % (uint32_t)per), b = u / a.Hkv, h = u % a.Hkv;
+  const int n = __ldg(reinterpret_cast<const int32_t*>(ws + kWsHeader) + b);
   const int32_t* kept = e.kept + (size_t)u * e.budget;
-  if ((int)blockIdx.y == 2 * pieces) {
-    const float* w = e.weights + (size_t)u * a.cap;
-    float* nw = e.new_weights + (size_t)u * a.cap;
-    for (int j0 = 0; j0 < n; j0 += kMoveThreads * kMoveRows) {
-      float v[kMoveRows];
-#pragma unroll
-      for (int x = 0; x < kMoveRows; ++x) {
-        const int j = j0 + x * kMoveThreads + tid;
-        if (j < n) v[x] = __ldcg(w + __ldg(kept + j));
+  const float* w = e.weights + (size_t)u * a.cap;
+  float* nw = e.new_weights + (size_t)u * a.cap;
+  uint32_t* flags = reinterpret_cast<uint32_t*>(ws + plan.off_flags) + (size_t)u * plan.chunks;
+  // the chunks of the unit before chunk `to` with a row from position j0 or behind (a run of chunks, since
+  // kept is ascending) have read their rows; false when a wait gave up
+  auto wait_for = [&](int to, int j0) {
+    bool ok = true;
+    for (int i = to - 1 - tid; i >= 0 && ok; i -= kMoveThreads) {
+      if (__ldg(kept + min((i + 1) * plan.rows, n) - 1) < j0) break;
+      uint32_t f = 0;
+      for (int x = 0; x < kPollLimit && !f; ++x) {
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(f) : "l"(flags + i) : "memory");
+        if (!f) __nanosleep(100);
       }
-      __syncthreads();
-#pragma unroll
-      for (int x = 0; x < kMoveRows; ++x) {
-        const int j = j0 + x * kMoveThreads + tid;
-        if (j < n) nw[j] = v[x];
+      if (!f) {
+        raise_error(a.err, DKV_DEVERR_TIMEOUT);
+        ok = false;
       }
     }
-    for (int j = n + tid; j < a.cap; j += kMoveThreads) nw[j] = 0.f;
-    if (h == 0 && tid == 0) e.new_lens[b] = n;
+    return __syncthreads_and(ok);
+  };
+  if (c >= plan.chunks) {  // zeros behind the kept tokens' weights
+    const int z0 = max(n, (c - plan.chunks) * kZeroChunk), z1 = min(a.cap, (c - plan.chunks + 1) * kZeroChunk);
+    if (z0 >= z1) return;
+    if (nw == w && !wait_for((n + plan.rows - 1) / plan.rows, z0)) return;
+    for (int j = z0 + tid; j < z1; j += kMoveThreads) nw[j] = 0.f;
     return;
   }
-  uint8_t* pool = (int)blockIdx.y < pieces ? kp : vp;
-  constexpr int kLanes = kMovePiece / 16, kRows = kMoveThreads / kLanes;  // rows of one access
-  const int64_t col = (int64_t)(blockIdx.y % pieces) * kMovePiece + (tid % kLanes) * 16 + h * a.stride_head * 2;
-  for (int j0 = 0; j0 < n; j0 += kRows * kMoveRows) {
-    uint4 v[kMoveRows];
-    uint8_t* to[kMoveRows];
+  const int j0 = c * plan.rows;
+  if (c == 0 && h == 0 && tid == 0) e.new_lens[b] = n;
+  if (j0 >= n) return;
+  uint4 v[2 * kMoveVec];
+  int64_t to[kMoveVec];
 #pragma unroll
-    for (int x = 0; x < kMoveRows; ++x) {
-      const int j = j0 + x * kRows + tid / kLanes;
-      to[x] = nullptr;
-      if (j >= n) continue;
-      const int t = __ldg(kept + j), sp = paged_page(a, b, t);
-      const int dp = __ldg(e.new_table + (size_t)b * e.new_max_pages + (j >> a.page_shift));
-      if (dp < 0 || dp >= a.n_pages) {
-        raise_error(a.err, DKV_DEVERR_INDEX);
-        continue;
-      }
-      v[x] = make_uint4(0, 0, 0, 0);
-      if (sp < a.n_pages)
-        v[x] = __ldcg(reinterpret_cast<const uint4*>(pool + col + (sp * a.stride_page + (t & a.page_mask) * a.stride_token) * 2));
-      to[x] = pool + col + (dp * a.stride_page + (j & a.page_mask) * a.stride_token) * 2;
+  for (int x = 0; x < kMoveVec; ++x) {
+    const int j = j0 + x * kRows + tid / R;
+    to[x] = -1;
+    if (j >= n) continue;
+    const int t = __ldg(kept + j), sp = paged_page(a, b, t);
+    const int dp = __ldg(e.new_table + (size_t)b * e.new_max_pages + (j >> a.page_shift));
+    if (dp < 0 || dp >= a.n_pages) {
+      raise_error(a.err, DKV_DEVERR_INDEX);
+      continue;
     }
-    __syncthreads();  // the batch is read: its positions may be written
-#pragma unroll
-    for (int x = 0; x < kMoveRows; ++x)
-      if (to[x]) *reinterpret_cast<uint4*>(to[x]) = v[x];
+    v[x] = v[x + kMoveVec] = make_uint4(0, 0, 0, 0);
+    if (sp < a.n_pages) {
+      const int64_t from = (sp * a.stride_page + h * a.stride_head + (t & a.page_mask) * a.stride_token) / 8 + tid % R;
+      v[x] = __ldcg(kp + from);
+      v[x + kMoveVec] = __ldcg(vp + from);
+    }
+    to[x] = (dp * a.stride_page + h * a.stride_head + (j & a.page_mask) * a.stride_token) / 8 + tid % R;
   }
+  const int jw = j0 + tid;
+  const bool weighs = tid < plan.rows && jw < n;
+  float wt = 0.f;
+  if (weighs) wt = __ldcg(w + __ldg(kept + jw));
+  // a sequence whose first page stays is compacted in place
+  const bool in_place = __ldg(a.table + (size_t)b * a.max_pages) == __ldg(e.new_table + (size_t)b * e.new_max_pages);
+  if (in_place || nw == w) {
+    __threadfence();  // this thread's reads are done
+    __syncthreads();
+    if (tid == 0) asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(flags + c), "r"(1u) : "memory");
+    if (!wait_for(c, j0)) return;
+  }
+#pragma unroll
+  for (int x = 0; x < kMoveVec; ++x)
+    if (to[x] >= 0) {
+      kp[to[x]] = v[x];
+      vp[to[x]] = v[x + kMoveVec];
+    }
+  if (weighs) nw[jw] = wt;
 }
 
 }  // namespace
 
-size_t paged_evict_ws_bytes(const PagedArgs& a) { return kWsHeader + (size_t)a.B * 4; }
+size_t paged_evict_ws_bytes(const PagedArgs& a, int d) { return evict_plan(a.B, a.Hkv, a.cap, d, a.cap).bytes; }
 
 cudaError_t launch_paged_evict(const PagedArgs& a, int d, const PagedEvict& e, void* k_pool, void* v_pool, uint8_t* ws,
                                cudaStream_t s) {
-  int32_t* counts = reinterpret_cast<int32_t*>(ws + kWsHeader);
-  const int units = a.B * a.Hkv, pieces = d * 2 / kMovePiece;
-  evict_select_kernel<<<units, kSelThreads, 0, s>>>(a, e, counts);
-  cudaError_t err = cudaGetLastError();
+  const int units = a.B * a.Hkv;
+  const EvictPlan plan = evict_plan(a.B, a.Hkv, a.cap, d, e.budget);
+  const size_t smem = (size_t)(a.cap < kSelStage ? a.cap : kSelStage) * 4;
+  cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(evict_select_kernel), smem);
   if (err != cudaSuccess) return err;
-  evict_move_kernel<<<dim3(units, 2 * pieces + 1), kMoveThreads, 0, s>>>(a, e, pieces, static_cast<uint8_t*>(k_pool),
-                                                                         static_cast<uint8_t*>(v_pool), counts);
-  return cudaGetLastError();
+  evict_select_kernel<<<units, kSelThreads, smem, s>>>(a, e, plan, ws);
+  if ((err = cudaGetLastError()) != cudaSuccess) return err;
+  return launch_dependent(d == 128 ? evict_move_kernel<128> : evict_move_kernel<64>,
+                          dim3((unsigned)units * (plan.chunks + plan.zeros)), kMoveThreads, 0, s, a, e, plan,
+                          static_cast<uint4*>(k_pool), static_cast<uint4*>(v_pool), ws);
 }
 
 }  // namespace dkv

@@ -92,7 +92,7 @@ PagedArgs make_args(const dkv_paged* p, const int32_t* table, const int32_t* len
 
 size_t ws_need(const dkv_paged* p, bool with_weights) {
   const PagedArgs a = make_args(p, nullptr, nullptr, nullptr);
-  const size_t dec = paged_decode_ws_bytes(a, p->head_dim, with_weights), ev = paged_evict_ws_bytes(a);
+  const size_t dec = paged_decode_ws_bytes(a, p->head_dim, with_weights), ev = paged_evict_ws_bytes(a, p->head_dim);
   return dec > ev ? dec : ev;
 }
 

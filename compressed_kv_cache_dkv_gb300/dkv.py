@@ -11,6 +11,7 @@ There is no CPU fallback: when libdkv.so is missing every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -366,47 +367,83 @@ def dkv_prefill_attend(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, top_k:
 # ---------------------------------------------------------------- paged cache
 
 _PAGED_DTYPES = {torch.float16: DKV_FP16, torch.bfloat16: DKV_BF16}
+_I32, _F32 = torch.int32, torch.float32
 
 
-def _typed(t: torch.Tensor, dtype: torch.dtype, shape: tuple, what: str) -> int:
-    """Address of a contiguous device tensor of this type and shape."""
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise ValueError(f"{what}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
-    return _ptr(t)
+class _Geometry:
+    """What the calls compare their tensors with, from a descriptor's bytes."""
+
+    __slots__ = ("key", "ref", "dtype", "pool", "strides", "batch", "heads", "kv_heads", "d", "table", "weights")
+
+    def __init__(self, p: dkv_paged, key: bytes):
+        self.key, self.ref = key, ctypes.byref(p)
+        self.dtype = torch.bfloat16 if p.dtype == DKV_BF16 else torch.float16
+        self.batch, self.heads, self.kv_heads, self.d = p.batch, p.n_q_heads, p.n_kv_heads, p.head_dim
+        self.pool = (p.n_pages, p.n_kv_heads, p.page_size, p.head_dim)
+        self.strides = (p.stride_page, p.stride_head, p.stride_token, 1)
+        self.table = (p.batch, p.max_pages)
+        self.weights = (p.batch, p.n_kv_heads, p.max_pages * p.page_size)
 
 
-def _rows(t: torch.Tensor, dtype: torch.dtype, shape: tuple, what: str) -> dkv_strides:
-    """Strides of a device tensor [batch][head][token][head_dim] whose channels are adjacent."""
-    if not t.is_cuda:
-        raise ValueError("device tensor expected")
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise ValueError(f"{what}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+def _geometry(p: dkv_paged) -> _Geometry:
+    key = bytes(p)
+    g = p.__dict__.get("_geometry")
+    if g is None or g.key != key:
+        g = p._geometry = _Geometry(p, key)
+    return g
+
+
+def _typed(t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev: int, what: str) -> int:
+    """Address of a contiguous tensor of this type and shape on this device."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{what}: expected contiguous {dtype} {shape} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} "
+                         f"with strides {t.stride()} on {t.device}")
+    return t.data_ptr()
+
+
+@functools.lru_cache(maxsize=1024)
+def _strides(batch: int, head: int, token: int):
+    s = dkv_strides(batch, head, token)
+    return ctypes.byref(s)
+
+
+def _rows(t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev: int, what: str):
+    """Strides of a tensor [batch][head][(token)][head_dim] whose channels are adjacent."""
     s = t.stride()
-    if s[-1] != 1:
-        raise ValueError(f"{what}: adjacent channels expected")
-    return dkv_strides(s[0], s[1], s[2] if len(s) == 4 else 0)
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or s[-1] != 1:
+        raise ValueError(f"{what}: expected {dtype} {shape} with adjacent channels on cuda:{dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} with strides {s} on {t.device}")
+    return _strides(s[0], s[1], s[2] if len(s) == 4 else 0)
 
 
-def _pools(p: dkv_paged, *pools: torch.Tensor) -> list:
-    shape = (p.n_pages, p.n_kv_heads, p.page_size, p.head_dim)
-    want = (p.stride_page, p.stride_head, p.stride_token, 1)
-    for t in pools:
-        if not t.is_cuda:
-            raise ValueError("device tensor expected")
-        if tuple(t.shape) != shape or _PAGED_DTYPES.get(t.dtype) != p.dtype:
-            raise ValueError(f"pool: expected {shape} of the descriptor's type, got {t.dtype} {tuple(t.shape)}")
-        if any(n > 1 and a != b for n, a, b in zip(shape, t.stride(), want)):
-            raise ValueError(f"pool: strides {t.stride()} are not the descriptor's {want}")
-    return [t.data_ptr() for t in pools]
+def _pool(g: _Geometry, t: torch.Tensor, dev: int) -> int:
+    if t.dtype is not g.dtype or t.shape != g.pool or t.get_device() != dev:
+        raise ValueError(f"pool: expected {g.dtype} {g.pool} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.stride() != g.strides and any(n > 1 and a != b for n, a, b in zip(g.pool, t.stride(), g.strides)):
+        raise ValueError(f"pool: strides {t.stride()} are not the descriptor's {g.strides}")
+    return t.data_ptr()
 
 
-def _paged_dtype(p: dkv_paged) -> torch.dtype:
-    return torch.bfloat16 if p.dtype == DKV_BF16 else torch.float16
+def _paged_device(t: torch.Tensor) -> int:
+    """Index of the tensor's device, -1 where it is not the current one (the call goes there then)."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("device tensor expected")
+    return dev if dev == torch._C._cuda_getDevice() else -1
 
 
-def _on(device):
-    """The CUDA calls of a paged operator go to its tensors' device."""
-    return torch.cuda.device(device)
+def _paged_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _paged_ws(p: dkv_paged, workspace, dev: int, with_weights: bool = False) -> torch.Tensor:
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous() or workspace.element_size() != 1:
+            raise ValueError("workspace: expected contiguous bytes on the tensors' device")
+        return workspace
+    ws = torch.empty(dkv_paged_workspace_bytes(p, with_weights), dtype=torch.uint8, device=dev)
+    ws[:256].zero_()
+    return ws
 
 
 def dkv_paged_layout(k_pages: torch.Tensor, batch: int, n_q_heads: int, max_pages: int, window: int = 0,
@@ -428,34 +465,27 @@ def dkv_paged_workspace_bytes(p: dkv_paged, with_weights: bool = False) -> int:
     return int(lib().dkv_paged_workspace_bytes(ctypes.byref(p), int(with_weights)))
 
 
-def _paged_ws(p: dkv_paged, workspace, device, with_weights: bool = False) -> torch.Tensor:
-    if workspace is not None:
-        return workspace
-    ws = torch.empty(dkv_paged_workspace_bytes(p, with_weights), dtype=torch.uint8, device=device)
-    ws[:256].zero_()
-    return ws
-
-
 def dkv_paged_append(p: dkv_paged, K_new: torch.Tensor, V_new: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
                      page_table: torch.Tensor, pos: torch.Tensor, counts: torch.Tensor | None = None,
                      workspace: torch.Tensor | None = None, stream=None) -> None:
-    """Write K_new, V_new [B, Hkv, n_new, d] (any strides with adjacent channels, both alike) into their
-    pages: token i < counts[b] of sequence b at position pos[b] + i (counts None: all n_new)."""
-    B, n = p.batch, K_new.shape[2]
-    shape = (B, p.n_kv_heads, n, p.head_dim)
-    ns, vs = (_rows(t, _paged_dtype(p), shape, "K_new, V_new") for t in (K_new, V_new))
-    if any(m > 1 and getattr(ns, f) != getattr(vs, f) for f, m in zip(("batch", "head", "token"), shape)):
-        V_new = V_new.contiguous()
-        K_new = K_new.contiguous()
-        ns = _rows(K_new, _paged_dtype(p), shape, "K_new")
-    kp, vp = _pools(p, k_pages, v_pages)
-    with _on(K_new.device):
-        ws = _paged_ws(p, workspace, K_new.device)
-        _check(lib().dkv_paged_append(
-            p, K_new.data_ptr(), V_new.data_ptr(), ns, n, _typed(pos, torch.int32, (B,), "pos"),
-            None if counts is None else _typed(counts, torch.int32, (B,), "counts"), kp, vp,
-            _typed(page_table, torch.int32, (B, p.max_pages), "page_table"), _ptr(ws), ws.numel(), _stream(stream)),
-            "dkv_paged_append")
+    """Write K_new, V_new [B, Hkv, n_new, d] (any strides with adjacent channels) into their pages: token
+    i < counts[b] of sequence b at position pos[b] + i (counts None: all n_new)."""
+    dev = _paged_device(K_new)
+    if dev < 0:
+        with torch.cuda.device(K_new.device):
+            return dkv_paged_append(p, K_new, V_new, k_pages, v_pages, page_table, pos, counts, workspace, stream)
+    g, n = _geometry(p), K_new.shape[2]
+    if K_new.stride() != V_new.stride():
+        K_new, V_new = K_new.contiguous(), V_new.contiguous()
+    shape = (g.batch, g.kv_heads, n, g.d)
+    ns = _rows(K_new, g.dtype, shape, dev, "K_new")
+    _rows(V_new, g.dtype, shape, dev, "V_new")
+    ws = _paged_ws(p, workspace, dev)
+    _check(lib().dkv_paged_append(
+        g.ref, K_new.data_ptr(), V_new.data_ptr(), ns, n, _typed(pos, _I32, (g.batch,), dev, "pos"),
+        None if counts is None else _typed(counts, _I32, (g.batch,), dev, "counts"), _pool(g, k_pages, dev),
+        _pool(g, v_pages, dev), _typed(page_table, _I32, g.table, dev, "page_table"), ws.data_ptr(), ws.numel(),
+        _paged_stream(stream, dev)), "dkv_paged_append")
 
 
 def dkv_paged_decode(p: dkv_paged, q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
@@ -464,24 +494,27 @@ def dkv_paged_decode(p: dkv_paged, q: torch.Tensor, k_pages: torch.Tensor, v_pag
     """One new token per sequence: q [B, Hq, d] at position lens[b] - 1 -> (out [B, Hq, d] in q's type,
     lse fp32 [B, Hq] or None).  `weights` fp32 [B, Hkv, max_pages * page_size]: every visible token's
     softmax weight, summed over its KV head's query heads, is added."""
-    B, Hq, d = p.batch, p.n_q_heads, p.head_dim
-    dt = _paged_dtype(p)
-    qs = _rows(q, dt, (B, Hq, d), "q")
-    kp, vp = _pools(p, k_pages, v_pages)
-    with _on(q.device):
-        if out is None:
-            out = torch.empty(B, Hq, d, dtype=dt, device=q.device)
-        if lse is True:
-            lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
-        elif lse is False:
-            lse = None
-        ws = _paged_ws(p, workspace, q.device, weights is not None)
-        _check(lib().dkv_paged_decode(
-            p, q.data_ptr(), qs, kp, vp, _typed(page_table, torch.int32, (B, p.max_pages), "page_table"),
-            _typed(lens, torch.int32, (B,), "lens"), _typed(out, dt, (B, Hq, d), "out"),
-            None if lse is None else _typed(lse, torch.float32, (B, Hq), "lse"),
-            None if weights is None else _typed(weights, torch.float32, (B, p.n_kv_heads, p.max_pages * p.page_size), "weights"),
-            _ptr(ws), ws.numel(), _stream(stream)), "dkv_paged_decode")
+    dev = _paged_device(q)
+    if dev < 0:
+        with torch.cuda.device(q.device):
+            return dkv_paged_decode(p, q, k_pages, v_pages, page_table, lens, out, lse, weights, workspace, stream)
+    g = _geometry(p)
+    shape = (g.batch, g.heads, g.d)
+    qs = _rows(q, g.dtype, shape, dev, "q")
+    if out is None:
+        out = torch.empty(shape, dtype=g.dtype, device=dev)
+    if lse is True:
+        lse = torch.empty(g.batch, g.heads, dtype=_F32, device=dev)
+    elif lse is False:
+        lse = None
+    ws = _paged_ws(p, workspace, dev, weights is not None)
+    _check(lib().dkv_paged_decode(
+        g.ref, q.data_ptr(), qs, _pool(g, k_pages, dev), _pool(g, v_pages, dev),
+        _typed(page_table, _I32, g.table, dev, "page_table"), _typed(lens, _I32, (g.batch,), dev, "lens"),
+        _typed(out, g.dtype, shape, dev, "out"),
+        None if lse is None else _typed(lse, _F32, (g.batch, g.heads), dev, "lse"),
+        None if weights is None else _typed(weights, _F32, g.weights, dev, "weights"), ws.data_ptr(), ws.numel(),
+        _paged_stream(stream, dev)), "dkv_paged_decode")
     return out, lse
 
 
@@ -491,26 +524,27 @@ def dkv_paged_prefill(p: dkv_paged, q: torch.Tensor, k_pages: torch.Tensor, v_pa
     """The last tokens of each sequence: q [B, Hq, Tq, d], query i < q_lens[b] (None: Tq) at position
     lens[b] - q_lens[b] + i -> (out [B, Hq, Tq, d] in q's type, lse fp32 [B, Hq, Tq] or None).  Rows from
     q_lens[b] on are left as they were (zeros in outputs allocated here)."""
-    B, Hq, d = p.batch, p.n_q_heads, p.head_dim
-    dt, Tq = _paged_dtype(p), q.shape[2]
-    qs = _rows(q, dt, (B, Hq, Tq, d), "q")
-    kp, vp = _pools(p, k_pages, v_pages)
-    with _on(q.device):
-        new = torch.empty if q_lens is None else torch.zeros
-        if out is None:
-            out = new(B, Hq, Tq, d, dtype=dt, device=q.device)
-        if lse is True:
-            lse = new(B, Hq, Tq, dtype=torch.float32, device=q.device)
-        elif lse is False:
-            lse = None
-        ws = _paged_ws(p, workspace, q.device)
-        _check(lib().dkv_paged_prefill(
-            p, q.data_ptr(), qs, Tq, kp, vp, _typed(page_table, torch.int32, (B, p.max_pages), "page_table"),
-            _typed(lens, torch.int32, (B,), "lens"),
-            None if q_lens is None else _typed(q_lens, torch.int32, (B,), "q_lens"), out.data_ptr(),
-            _rows(out, dt, (B, Hq, Tq, d), "out"),
-            None if lse is None else _typed(lse, torch.float32, (B, Hq, Tq), "lse"), _ptr(ws), ws.numel(), _stream(stream)),
-            "dkv_paged_prefill")
+    dev = _paged_device(q)
+    if dev < 0:
+        with torch.cuda.device(q.device):
+            return dkv_paged_prefill(p, q, k_pages, v_pages, page_table, lens, q_lens, out, lse, workspace, stream)
+    g, Tq = _geometry(p), q.shape[2]
+    shape = (g.batch, g.heads, Tq, g.d)
+    qs = _rows(q, g.dtype, shape, dev, "q")
+    new = torch.empty if q_lens is None else torch.zeros
+    if out is None:
+        out = new(shape, dtype=g.dtype, device=dev)
+    if lse is True:
+        lse = new(shape[:3], dtype=_F32, device=dev)
+    elif lse is False:
+        lse = None
+    ws = _paged_ws(p, workspace, dev)
+    _check(lib().dkv_paged_prefill(
+        g.ref, q.data_ptr(), qs, Tq, _pool(g, k_pages, dev), _pool(g, v_pages, dev),
+        _typed(page_table, _I32, g.table, dev, "page_table"), _typed(lens, _I32, (g.batch,), dev, "lens"),
+        None if q_lens is None else _typed(q_lens, _I32, (g.batch,), dev, "q_lens"), out.data_ptr(),
+        _rows(out, g.dtype, shape, dev, "out"), None if lse is None else _typed(lse, _F32, shape[:3], dev, "lse"),
+        ws.data_ptr(), ws.numel(), _paged_stream(stream, dev)), "dkv_paged_prefill")
     return out, lse
 
 
@@ -519,18 +553,20 @@ def dkv_paged_weights(p: dkv_paged, q: torch.Tensor, lse: torch.Tensor, k_pages:
                       workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Add the softmax weights that the queries (as in dkv_paged_prefill, with the lse it gave) give every
     token, summed over queries and a KV head's query heads, to weights fp32 [B, Hkv, max_pages * page_size]."""
-    B, Hq, d = p.batch, p.n_q_heads, p.head_dim
-    Tq = q.shape[2]
-    qs = _rows(q, _paged_dtype(p), (B, Hq, Tq, d), "q")
-    kp, = _pools(p, k_pages)
-    with _on(q.device):
-        ws = _paged_ws(p, workspace, q.device)
-        _check(lib().dkv_paged_weights(
-            p, q.data_ptr(), qs, Tq, _typed(lse, torch.float32, (B, Hq, Tq), "lse"), kp,
-            _typed(page_table, torch.int32, (B, p.max_pages), "page_table"), _typed(lens, torch.int32, (B,), "lens"),
-            None if q_lens is None else _typed(q_lens, torch.int32, (B,), "q_lens"),
-            _typed(weights, torch.float32, (B, p.n_kv_heads, p.max_pages * p.page_size), "weights"), _ptr(ws), ws.numel(),
-            _stream(stream)), "dkv_paged_weights")
+    dev = _paged_device(q)
+    if dev < 0:
+        with torch.cuda.device(q.device):
+            return dkv_paged_weights(p, q, lse, k_pages, page_table, lens, weights, q_lens, workspace, stream)
+    g, Tq = _geometry(p), q.shape[2]
+    shape = (g.batch, g.heads, Tq, g.d)
+    qs = _rows(q, g.dtype, shape, dev, "q")
+    ws = _paged_ws(p, workspace, dev)
+    _check(lib().dkv_paged_weights(
+        g.ref, q.data_ptr(), qs, Tq, _typed(lse, _F32, shape[:3], dev, "lse"), _pool(g, k_pages, dev),
+        _typed(page_table, _I32, g.table, dev, "page_table"), _typed(lens, _I32, (g.batch,), dev, "lens"),
+        None if q_lens is None else _typed(q_lens, _I32, (g.batch,), dev, "q_lens"),
+        _typed(weights, _F32, g.weights, dev, "weights"), ws.data_ptr(), ws.numel(), _paged_stream(stream, dev)),
+        "dkv_paged_weights")
     return weights
 
 
@@ -541,26 +577,27 @@ def dkv_paged_evict(p: dkv_paged, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     """Cut every sequence to `budget` tokens: the first `first`, the last `recent` and the heaviest between
     them, in order, moved to new_table's pages (int32 [B, n]; page_table itself compacts in place) ->
     (kept int32 [B, Hkv, budget], new_lens int32 [B], new_weights like weights)."""
-    B, shape = p.batch, (p.batch, p.n_kv_heads, p.max_pages * p.page_size)
-    kp, vp = _pools(p, k_pages, v_pages)
-    if new_table.dim() != 2:
-        raise ValueError("new_table: expected [B, pages]")
-    dev = k_pages.device
-    with _on(dev):
-        if kept is None:
-            kept = torch.empty(B, p.n_kv_heads, budget, dtype=torch.int32, device=dev)
-        if new_lens is None:
-            new_lens = torch.empty(B, dtype=torch.int32, device=dev)
-        if new_weights is None:
-            new_weights = torch.empty(shape, dtype=torch.float32, device=dev)
-        ws = _paged_ws(p, workspace, dev)
-        _check(lib().dkv_paged_evict(
-            p, kp, vp, _typed(page_table, torch.int32, (B, p.max_pages), "page_table"), _typed(lens, torch.int32, (B,), "lens"),
-            _typed(weights, torch.float32, shape, "weights"), int(budget), int(first), int(recent),
-            _typed(new_table, torch.int32, (B, new_table.shape[1]), "new_table"), new_table.shape[1],
-            _typed(kept, torch.int32, (B, p.n_kv_heads, budget), "kept"), _typed(new_lens, torch.int32, (B,), "new_lens"),
-            _typed(new_weights, torch.float32, shape, "new_weights"), _ptr(ws), ws.numel(), _stream(stream)),
-            "dkv_paged_evict")
+    dev = _paged_device(k_pages)
+    if dev < 0:
+        with torch.cuda.device(k_pages.device):
+            return dkv_paged_evict(p, k_pages, v_pages, page_table, lens, weights, budget, first, recent, new_table, kept,
+                                   new_lens, new_weights, workspace, stream)
+    g = _geometry(p)
+    width = new_table.shape[-1]
+    if kept is None:
+        kept = torch.empty(g.batch, g.kv_heads, max(budget, 0), dtype=_I32, device=dev)
+    if new_lens is None:
+        new_lens = torch.empty(g.batch, dtype=_I32, device=dev)
+    if new_weights is None:
+        new_weights = torch.empty(g.weights, dtype=_F32, device=dev)
+    ws = _paged_ws(p, workspace, dev)
+    _check(lib().dkv_paged_evict(
+        g.ref, _pool(g, k_pages, dev), _pool(g, v_pages, dev), _typed(page_table, _I32, g.table, dev, "page_table"),
+        _typed(lens, _I32, (g.batch,), dev, "lens"), _typed(weights, _F32, g.weights, dev, "weights"), budget, first, recent,
+        _typed(new_table, _I32, (g.batch, width), dev, "new_table"), width,
+        _typed(kept, _I32, (g.batch, g.kv_heads, max(budget, 0)), dev, "kept"),
+        _typed(new_lens, _I32, (g.batch,), dev, "new_lens"), _typed(new_weights, _F32, g.weights, dev, "new_weights"),
+        ws.data_ptr(), ws.numel(), _paged_stream(stream, dev)), "dkv_paged_evict")
     return kept, new_lens, new_weights
 
 
