@@ -8,9 +8,11 @@
 //   O_g += P_g V_j    M = 128, N = d, P from TMEM (16-bit, over the first 64 columns of S_g)
 // One row per softmax thread (warps 0-3 group A, 4-7 group B); the tiles come through a ring of
 // 128-row slots (K_0, V_0, K_1, ...) filled with TMA boxes by warp 8, one box per page and 64
-// channels; lane 0 of warps 9 and 10 issue the products of groups A and B.  While one group's
-// rows turn S into P, the tensor cores run the other group's products.  P is handed over in two
-// halves of 64 keys, so that half of its product runs under the other half's exponentials.
+// channels; one lane of warp 9 issues the products, each block of eight or four in one go for
+// whichever group is ready, so that while one group's rows turn S into P the tensor cores run the
+// other's products (with a thread for each group their products mixed, both fell into step and
+// idled together).  P is handed over in two halves of 64 keys, so that half of its product runs
+// under the other half's exponentials.
 // S_{j+1} overwrites P_j, so it is issued once O_j is done; the arrival on S_{j+1} then also
 // says that O may be rescaled.  The row maximum moves only when a score exceeds it by kPfSlack
 // (base 2), and only then is O rescaled in tensor memory.
@@ -34,6 +36,7 @@ namespace {
 
 constexpr int kPfThreads = 384, kPfM = 128, kPfN = 128;
 constexpr float kPfSlack = 8.f;
+constexpr int kPfIdle = 1 << 24;  // polls without a product before the issuing thread gives up
 constexpr int kPfEdges = 8;  // edge tiles of a CTA: 3 on the diagonal, 3 at the window's edge, 1 at the sinks' end
 
 template <typename T>
@@ -89,13 +92,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   using S = PfSmem<D>;
   constexpr int NS = S::kSlots;
   const PagedArgs& a = p.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
   const QuerySpan qs = query_span(a, p.q.q_lens, p.q.Tq, b);
-  // the groups: head and first query row (later rows, with more keys, first)
-  const int tile = (int)gridDim.x - 1 - (int)blockIdx.x;
+  // the groups: head and first query row (of all heads the later rows, with more keys, first)
+  const int tile = (int)gridDim.z - 1 - (int)blockIdx.z;
   const int row0 = tile * (p.by_heads ? kPfM : 2 * kPfM);
   if (row0 >= qs.n) return;
-  const int h0 = p.by_heads ? 2 * (int)blockIdx.y : (int)blockIdx.y, kvh = h0 / a.G;
+  const int h0 = p.by_heads ? 2 * (int)blockIdx.x : (int)blockIdx.x, kvh = h0 / a.G;
   const int rowsA = min(kPfM, qs.n - row0), rowsB = p.by_heads ? rowsA : min(kPfM, max(0, qs.n - row0 - kPfM));
   const int p_lo = qs.off + row0, p_hi = p_lo + (p.by_heads ? rowsA : rowsA + rowsB) - 1;
   const KeySpan ks = key_span(a, p_lo, p_hi);
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     tma_prefetch_map(&vmap);
     for (int i = 0; i < NS; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 2);  // one commit per group
+      mbar_init(&empty[i], 1);  // the commit behind the last product of the tile
     }
     for (int i = 0; i < kPfEdges; ++i) mbar_init(&landed[i], 1);
     mbar_init(q_full, 1);
@@ -175,51 +178,72 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     // every copy has landed before the CTA may end (also after a wait that gave up)
     if (nt > 0) mbar_wait(q_full, 0, a.err);
     for (int x = max(0, i - NS); x < i; ++x) mbar_wait(&full[x % NS], (uint32_t)((x / NS) & 1), a.err);
-  } else if (warp == 9 || warp == 10) {
-    // =========================== products of group g
-    const int g = warp - 9, n = g ? nB : nA, n_other = g ? nA : nB;
-    if (lane == 0 && n > 0) {
-      const uint32_t ts = tmem + 256u * g, to = ts + 128u;
-      constexpr uint32_t id_s = tc_idesc(Num<T>::kUmma, false, kPfN), id_o = tc_idesc(Num<T>::kUmma, true, D);
-      const uint64_t qd = tc_desc(sb + g * S::kTile, 16, 1024);
-      auto release = [&](int sl, int j) {  // once for this group, once more where the other has no tile j
-        tc_commit(&empty[sl]);
-        if (j >= n_other) tc_commit(&empty[sl]);
-      };
-      auto scores = [&](int j) {
-        const int sl = 2 * j % NS;
-        ok = ok && mbar_wait(&full[sl], (uint32_t)((2 * j / NS) & 1), a.err);
-        if (j > 0) ok = ok && mbar_wait(&o_done[g], (uint32_t)((j - 1) & 1), a.err);
-        tc_fence_after();
-        if (!ok) return;
-        const uint64_t kd = tc_desc(sb + S::kOffRing + sl * S::kTile, 16, 1024);
+  } else if (warp == 9) {
+    // =========================== products: whichever of the two groups has one ready
+    // The whole warp walks through here and one elected lane issues: in code that one lane runs
+    // alone the operands are not known to be uniform, and an issue took 150 cycles instead of the 64
+    // that a product needs.
+    constexpr uint32_t id_s = tc_idesc(Num<T>::kUmma, false, kPfN), id_o = tc_idesc(Num<T>::kUmma, true, D);
+    const uint32_t el = elect_one();
+    const int n[2] = {nA, nB};
+    int js[2] = {0, 0}, jv[2] = {0, 0};  // tiles of which S_g, and O_g, have been issued
+    int half[2] = {0, 0};                // halves of P_g taken of the tile at hand
+    int landed_k = 0, landed_v = 0;      // tiles known to have landed
+    int idle = 0;
+    auto over = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, mbar_test(bar, (uint32_t)parity)) != 0; };
+    if (nt > 0) ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, a.err));
+    while (ok && (jv[0] < n[0] || jv[1] < n[1])) {
+      bool any = false;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {  // 16 channels: 32 bytes of a 128-byte row, then the next 64 channels
-          const uint64_t step = (uint64_t)(((k >> 2) * kPfN * 128 + (k & 3) * 32) >> 4);
-          tc_mma(ts, qd + step, kd + step, id_s, k > 0);
-        }
-        tc_commit(&s_full[g]);
-        release(sl, j);
-      };
-      ok = mbar_wait(q_full, 0, a.err);
-      scores(0);
-      for (int j = 0; j < n && ok; ++j) {
-        const int i = 2 * j + 1, sl = i % NS;
-        ok = mbar_wait(&full[sl], (uint32_t)((i / NS) & 1), a.err);
-        const uint64_t vd = tc_desc(sb + S::kOffRing + sl * S::kTile, kPfN * 128, 1024);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          ok = ok && mbar_wait(&p_half[2 * g + half], (uint32_t)(j & 1), a.err);
+      for (int g = 0; g < 2; ++g) {
+        const int o = 1 - g;
+        const uint32_t ts = tmem + 256u * g;
+        if (js[g] == jv[g]) {  // the next product is S_g of tile j, once O_g of tile j - 1 is done
+          const int j = js[g], sl = 2 * j % NS;
+          if (j >= n[g] || (j > 0 && !over(&o_done[g], (j - 1) & 1))) continue;
+          if (landed_k <= j) {
+            if (!over(&full[sl], (2 * j / NS) & 1)) continue;
+            landed_k = j + 1;
+          }
           tc_fence_after();
-          if (!ok) break;
+          const uint64_t qd = tc_desc(sb + g * S::kTile, 16, 1024), kd = tc_desc(sb + S::kOffRing + sl * S::kTile, 16, 1024);
 #pragma unroll
-          for (int k = 4 * half; k < 4 * half + 4; ++k)  // 16 keys: 16 rows of 128 bytes
-            tc_mma_ta(to, ts + 8u * k, vd + (uint64_t)(k * 16 * 128 >> 4), id_o, (j > 0 || k > 0) ? 1u : 0u);
+          for (int k = 0; k < D / 16; ++k) {  // 16 channels: 32 bytes of a 128-byte row, then the next 64 channels
+            const uint64_t step = (uint64_t)(((k >> 2) * kPfN * 128 + (k & 3) * 32) >> 4);
+            tc_mma(ts, qd + step, kd + step, id_s, k > 0, el);
+          }
+          tc_commit(&s_full[g], el);
+          js[g] = j + 1;
+          if (js[o] > j || n[o] <= j) tc_commit(&empty[sl], el);  // the other group is past this tile
+        } else {  // a half of O_g of tile j
+          const int j = jv[g], i = 2 * j + 1, sl = i % NS;
+          if (!over(&p_half[2 * g + half[g]], j & 1)) continue;
+          if (landed_v <= j) {
+            if (!over(&full[sl], (i / NS) & 1)) continue;
+            landed_v = j + 1;
+          }
+          tc_fence_after();
+          const uint64_t vd = tc_desc(sb + S::kOffRing + sl * S::kTile, kPfN * 128, 1024);
+          if (half[g] == 0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)  // 16 keys: 16 rows of 128 bytes
+              tc_mma_ta(ts + 128u, ts + 8u * k, vd + (uint64_t)(k * 16 * 128 >> 4), id_o, k > 0 ? 1u : (j > 0 ? 1u : 0u), el);
+            half[g] = 1;
+          } else {
+#pragma unroll
+            for (int k = 4; k < 8; ++k) tc_mma_ta(ts + 128u, ts + 8u * k, vd + (uint64_t)(k * 16 * 128 >> 4), id_o, 1u, el);
+            tc_commit(&o_done[g], el);
+            half[g] = 0;
+            jv[g] = j + 1;
+            if (jv[o] > j || n[o] <= j) tc_commit(&empty[sl], el);
+          }
         }
-        if (!ok) break;
-        release(sl, j);
-        tc_commit(&o_done[g]);
-        if (j + 1 < n) scores(j + 1);
+        any = true;
+      }
+      idle = any ? 0 : idle + 1;
+      if (idle > kPfIdle) {
+        if (el) raise_error(a.err, DKV_DEVERR_TIMEOUT);
+        ok = false;
       }
     }
   } else if (warp == 11) {
@@ -263,7 +287,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (lane == 0) mbar_arrive(&full[sl]);
       }
     }
-  } else {
+  } else if (warp < 8) {  // (warp 10 has no work)
     // =========================== softmax: one query row per thread
     const int g = warp >> 2, rw = warp & 3, row = 32 * rw + lane;
     const int n = g ? nB : nA, rows = g ? rowsB : rowsA;
@@ -307,24 +331,25 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
       }
       const float ms = (m == -INFINITY ? 0.f : m) - kPfShift<T>;
-      float lp[4] = {0.f, 0.f, 0.f, 0.f};
+      const float2 scale2 = make_float2(slog2, slog2), shift2 = make_float2(-ms, -ms);
+      float2 lp[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t w[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           const int c = 64 * half + 2 * e;
-          const float p0 = fast_exp2(fmaf(__uint_as_float(s[c]), slog2, -ms));
-          const float p1 = fast_exp2(fmaf(__uint_as_float(s[c + 1]), slog2, -ms));
-          lp[e & 3] += p0 + p1;
-          w[e] = Num<T>::pack(p0, p1);
+          const float2 x = fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, shift2);
+          const float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+          lp[e & 1] = add2(lp[e & 1], y);
+          w[e] = Num<T>::pack(y.x, y.y);
         }
         tc_st32(ts + 32 * half, w);
         tc_st_wait();
         tc_fence_before();
         mbar_arrive(&p_half[2 * g + half]);
       }
-      l = fmaf(l, al, (lp[0] + lp[1]) + (lp[2] + lp[3]));
+      l = fmaf(l, al, (lp[0].x + lp[1].x) + (lp[0].y + lp[1].y));
     }
     if (n > 0 && ok) ok = mbar_wait(&o_done[g], (uint32_t)((n - 1) & 1), a.err);
     tc_fence_after();
@@ -384,7 +409,7 @@ cudaError_t launch_td(const PfKernelArgs& p, const PagedMaps& m, const CUtensorM
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(paged_prefill_kernel<T, D>), smem);
   if (e != cudaSuccess) return e;
   const int per = p.by_heads ? kPfM : 2 * kPfM;
-  const dim3 grid((p.q.Tq + per - 1) / per, p.by_heads ? p.a.Hq / 2 : p.a.Hq, p.a.B);
+  const dim3 grid(p.by_heads ? p.a.Hq / 2 : p.a.Hq, p.a.B, (p.q.Tq + per - 1) / per);
   paged_prefill_kernel<T, D><<<grid, kPfThreads, smem, s>>>(p, qmap, m.k, m.v);
   return cudaGetLastError();
 }

@@ -17,26 +17,36 @@ __device__ inline uint64_t tc_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
 __device__ constexpr uint32_t tc_idesc(uint32_t fmt, bool b_mn, uint32_t n) {
   return (1u << 4) | (fmt << 7) | (fmt << 10) | ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
+// one lane of a converged warp (1 in it, 0 in the others)
+__device__ inline uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
+// The lane with `el` issues; the whole warp calls these with the same operands.
 // A and B from shared memory
-__device__ inline void tc_mma(uint32_t dt, uint64_t ad, uint64_t bd, uint32_t id, uint32_t acc) {
+__device__ inline void tc_mma(uint32_t dt, uint64_t ad, uint64_t bd, uint32_t id, uint32_t acc, uint32_t el) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(dt),
-      "l"(ad), "l"(bd), "r"(id), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(dt),
+      "l"(ad), "l"(bd), "r"(id), "r"(acc), "r"(el)
       : "memory");
 }
 // A from tensor memory (row = lane, two elements of k a column)
-__device__ inline void tc_mma_ta(uint32_t dt, uint32_t at, uint64_t bd, uint32_t id, uint32_t acc) {
+__device__ inline void tc_mma_ta(uint32_t dt, uint32_t at, uint64_t bd, uint32_t id, uint32_t acc, uint32_t el) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(dt),
-      "r"(at), "l"(bd), "r"(id), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(dt),
+      "r"(at), "l"(bd), "r"(id), "r"(acc), "r"(el)
       : "memory");
 }
-// arrive on `bar` when every product this thread has issued is done
-__device__ inline void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
+// arrive on `bar` when every product that lane has issued is done
+__device__ inline void tc_commit(uint64_t* bar, uint32_t el) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(el)
+      : "memory");
 }
 __device__ inline void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ inline void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -74,6 +84,30 @@ __device__ inline void tc_st32(uint32_t ta, const uint32_t* r) {
   tc_st16(ta + 16, r + 16);
 }
 __device__ inline void tc_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// whether the phase of this parity is over (no waiting)
+__device__ inline bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// two fp32 operations in one instruction (sm_100 and up)
+__device__ inline uint64_t f2_bits(float2 x) { return *reinterpret_cast<uint64_t*>(&x); }
+__device__ inline float2 fma2(float2 x, float2 y, float2 z) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(f2_bits(x)), "l"(f2_bits(y)), "l"(f2_bits(z)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ inline float2 add2(float2 x, float2 y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(x)), "l"(f2_bits(y)));
+  return *reinterpret_cast<float2*>(&r);
+}
 
 // The queries of one sequence.
 struct QuerySpan {

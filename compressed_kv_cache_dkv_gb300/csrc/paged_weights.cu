@@ -5,7 +5,7 @@
 // them, head by head: S^T = K Q^T puts one key into each TMEM lane, so a thread sums its key's
 // weights over the columns in registers and every key has one owner (no atomics, a fixed order).
 // Two warpgroups take query tiles in turn, each with its own 128 TMEM columns; warp 8 streams
-// the query tiles with TMA through two slots, lane 0 of warp 9 issues the products.  Two CTAs
+// the query tiles with TMA through two slots, one lane of warp 9 issues the products.  Two CTAs
 // share a multiprocessor.  Bound by the exponentials (one per visible pair: twice the cycles of
 // its product at d 128) for whole prompts, by the read of K for a few queries; the query tile is
 // cut to 32 or 64 rows when there are no more queries, since a product's time goes with its rows.
@@ -32,7 +32,8 @@ __global__ void __launch_bounds__(kWtThreads, 2)
   extern __shared__ __align__(1024) uint8_t smem[];
   using S = WtSmem<D>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int u = blockIdx.y, b = u / a.Hkv, h = u % a.Hkv, k0 = blockIdx.x * kWtM;
+  // of all units the earlier keys, which more queries see, first
+  const int u = blockIdx.x, b = u / a.Hkv, h = u % a.Hkv, k0 = blockIdx.y * kWtM;
   const QuerySpan qs = query_span(a, q.q_lens, q.Tq, b);
   // query rows that see a key of the tile
   const int r_lo = max(0, k0 - qs.off);
@@ -97,24 +98,23 @@ __global__ void __launch_bounds__(kWtThreads, 2)
     for (int x = max(0, i - 2); x < i; ++x) mbar_wait(&q_full[x & 1], (uint32_t)((x / 2) & 1), a.err);
   } else if (warp == 9) {
     // =========================== products
-    if (lane == 0) {
-      const uint32_t id = tc_idesc(Num<T>::kUmma, false, (uint32_t)qn);
-      const uint64_t kd = tc_desc(sb, 16, 1024);
-      ok = mbar_wait(k_full, 0, a.err);
-      for (int i = 0; i < nq && ok; ++i) {
-        const int w = i & 1;
-        ok = mbar_wait(&q_full[w], (uint32_t)((i / 2) & 1), a.err);
-        if (i >= 2) ok = ok && mbar_wait(&s_empty[w], (uint32_t)((i / 2 - 1) & 1), a.err);
-        tc_fence_after();
-        if (!ok) break;
-        const uint64_t qd = tc_desc(sb + S::kOffQ + w * S::kTile, 16, 1024);
+    // (the whole warp, one elected lane issuing: see the prefill kernel)
+    const uint32_t el = elect_one(), id = tc_idesc(Num<T>::kUmma, false, (uint32_t)qn);
+    const uint64_t kd = tc_desc(sb, 16, 1024);
+    ok = mbar_wait(k_full, 0, a.err);
+    for (int i = 0; i < nq; ++i) {
+      const int w = i & 1;
+      ok = ok && mbar_wait(&q_full[w], (uint32_t)((i / 2) & 1), a.err);
+      if (i >= 2) ok = ok && mbar_wait(&s_empty[w], (uint32_t)((i / 2 - 1) & 1), a.err);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint64_t qd = tc_desc(sb + S::kOffQ + w * S::kTile, 16, 1024);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc_mma(tmem + 128u * w, kd + (uint64_t)(((k >> 2) * kWtM * 128 + (k & 3) * 32) >> 4),
-                 qd + (uint64_t)(((k >> 2) * qn * 128 + (k & 3) * 32) >> 4), id, k > 0);
-        tc_commit(&q_empty[w]);
-        tc_commit(&s_full[w]);
-      }
+      for (int k = 0; k < D / 16; ++k)
+        tc_mma(tmem + 128u * w, kd + (uint64_t)(((k >> 2) * kWtM * 128 + (k & 3) * 32) >> 4),
+               qd + (uint64_t)(((k >> 2) * qn * 128 + (k & 3) * 32) >> 4), id, k > 0, el);
+      tc_commit(&q_empty[w], el);
+      tc_commit(&s_full[w], el);
     }
   } else {
     // =========================== sums: one key per thread and warpgroup
@@ -177,7 +177,7 @@ cudaError_t launch_td(const PagedArgs& a, const CUtensorMap& kmap, const CUtenso
   constexpr uint32_t smem = WtSmem<D>::kBytes;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(paged_weights_kernel<T, D>), smem);
   if (e != cudaSuccess) return e;
-  const dim3 grid((a.cap + kWtM - 1) / kWtM, a.B * a.Hkv);
+  const dim3 grid(a.B * a.Hkv, (a.cap + kWtM - 1) / kWtM);
   paged_weights_kernel<T, D><<<grid, kWtThreads, smem, s>>>(a, q, lse, weights, paged_weights_rows(q.Tq), kmap, qmap);
   return cudaGetLastError();
 }
