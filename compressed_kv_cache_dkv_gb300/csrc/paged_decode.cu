@@ -9,7 +9,7 @@
 //
 // One producer warp streams tiles of K and V with TMA boxes (one per page, 64
 // channels wide, 128-byte swizzle) into a ring of kDecStages stages; its lanes look up
-// the tile's pages.  Eight consumer warps in two teams take tiles in turn, warp w of
+// the tile's pages, one elected lane issues.  Eight consumer warps in two teams take tiles in turn, warp w of
 // a team 16 tokens:
 //   S = K q      ldmatrix K fragments, mma.sync m16n8k16, tokens in M, heads in N
 //   o += V^T p   ldmatrix.trans V^T fragments, p as hi + lo 16-bit halves
@@ -155,25 +155,30 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 
   if (warp == kDecConsumers) {
     // =========================== producer
-    const int rows = min(a.page_mask + 1, kDecTile), ppt = kDecTile / rows;  // boxes of `rows` slots, boxes per tile
-    const int nbox = ppt * 2 * (D / 64);
-    const int pi = lane % ppt, hf = (lane / ppt) % (D / 64), kv = lane / (ppt * (D / 64));
+    const uint32_t el = elect_one();
+    const int rows = min(a.page_mask + 1, kDecTile), ppt = kDecTile / rows;  // boxes of `rows` slots, runs per tile
     bool ok = true;
     int it = 0;
     for (int x = x0; x < x1 && ok;) {
       const Seg g = dec_seg(prefix, a.B, a.Hkv, x, x1);
       const Span s = dec_span(a, g.b);
       for (int j = g.j0; j < g.j1; ++j, ++it) {
-        const int st = it % kDecStages, first = s.token(j) + pi * rows;
-        int page = a.n_pages;  // boxes without a visible token: zeros, wherever the table points
-        if (lane < nbox && first < s.len && (first + rows > s.lo || first < a.sinks)) page = paged_page(a, g.b, first);
+        const int st = it % kDecStages, y = s.token(j) & a.page_mask, first = s.token(j) + lane * rows;
+        int page = a.n_pages;  // runs without a visible token: zeros, wherever the table points
+        if (lane < ppt && first < s.len && (first + rows > s.lo || first < a.sinks)) page = paged_page(a, g.b, first);
         if (it >= kDecStages) ok = mbar_wait(&empty[st], (uint32_t)((it / kDecStages - 1) & 1), a.err);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], 2 * TILE);
-        __syncwarp();
-        if (lane < nbox)
-          tma_load_4d(sb + (uint32_t)(2 * st + kv) * TILE + (uint32_t)hf * kDecTile * 128u + (uint32_t)(pi * rows) * 128u,
-                      kv ? &vmap : &kmap, hf * 64, first & a.page_mask, g.h, page, &full[st]);
+        if (el) mbar_arrive_expect_tx(&full[st], 2 * TILE);
+        const uint32_t dst = sb + (uint32_t)(2 * st) * TILE;
+        for (int i = 0; i < ppt; ++i) {
+          const int pg = __shfl_sync(0xffffffffu, page, i);
+#pragma unroll
+          for (int hf = 0; hf < D / 64; ++hf) {
+            const uint32_t at = dst + (uint32_t)hf * kDecTile * 128u + (uint32_t)(i * rows) * 128u;
+            tma_load_4d(at, &kmap, hf * 64, y, g.h, pg, &full[st], el);
+            tma_load_4d(at + TILE, &vmap, hf * 64, y, g.h, pg, &full[st], el);
+          }
+        }
       }
       x += g.j1 - g.j0;
     }

@@ -210,7 +210,7 @@ int dkv_paged_weights(const dkv_paged* p, const void* q, const dkv_strides* qs, 
     return DKV_ERR_ALIGN;
   const PagedArgs a = make_args(p, page_table, lens, workspace);
   CUtensorMap km, qm;
-  if (!encode_pool(&km, p, k_pool) || !encode_query(&qm, p, q, *qs, Tq, paged_weights_rows(Tq))) return DKV_ERR_CUDA;
+  if (!encode_pool(&km, p, k_pool) || !encode_query(&qm, p, q, *qs, Tq, paged_weights_rows(p->n_q_heads / p->n_kv_heads, Tq))) return DKV_ERR_CUDA;
   const PagedQuery pq = {q, *qs, Tq, q_lens};
   return done(launch_paged_weights(a, p->head_dim, p->dtype, km, qm, pq, lse, weights,
                                    static_cast<cudaStream_t>(stream)));

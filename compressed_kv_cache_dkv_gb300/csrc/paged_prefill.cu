@@ -3,19 +3,17 @@
 //
 // A CTA owns two groups of 128 query rows that share every K and V tile: two heads of one
 // KV head at the same tokens where the group size is even, else 256 tokens of one head.  Per
-// 128-key tile j and group g
-//   S_g = Q_g K_j^T   M = 128 queries, N = 128 keys       (128 TMEM columns)
-//   O_g += P_g V_j    M = 128, N = d, P from TMEM (16-bit, over the first 64 columns of S_g)
-// One row per softmax thread (warps 0-3 group A, 4-7 group B); the tiles come through a ring of
-// 128-row slots (K_0, V_0, K_1, ...) filled with TMA boxes by warp 8, one box per page and 64
-// channels; one lane of warp 9 issues the products, each block of eight or four in one go for
-// whichever group is ready, so that while one group's rows turn S into P the tensor cores run the
-// other's products (with a thread for each group their products mixed, both fell into step and
-// idled together).  P is handed over in two halves of 64 keys, so that half of its product runs
-// under the other half's exponentials.
-// S_{j+1} overwrites P_j, so it is issued once O_j is done; the arrival on S_{j+1} then also
-// says that O may be rescaled.  The row maximum moves only when a score exceeds it by kPfSlack
-// (base 2), and only then is O rescaled in tensor memory.
+// 64-key tile j and group g
+//   S_g = Q_g K_j^T   M = 128 queries, N = 64 keys   (64 TMEM columns, two buffers a group)
+//   O_g += P_g V_j    M = 128, N = d, P from TMEM (16-bit, over the first 32 columns of its S)
+// One row per softmax thread (warps 0-3 group A, 4-7 group B).  Warp 8 streams the tiles with TMA
+// boxes, one per page and 64 channels, into six slots for K and four for V; warps 9 and 10 issue
+// the products of groups A and B: S of tile j + 1 goes out while the rows still turn S_j into P,
+// so that neither the rows nor the tensor cores wait for the other's latency.  (With 128-key
+// tiles, which read Q half as often from shared memory, there is room for one S only, and the
+// chain S - P - O - next S of a group takes 3700 cycles per 128 keys, of which 1024 products.)
+// S_{j+2} overwrites P_j, so it is issued once O_j is done.  The row maximum moves only when a
+// score exceeds it by kPfSlack (base 2), and only then is O rescaled in tensor memory.
 //
 // P is rounded once to the type of V.  The output is rounded to that type too, and the error of
 // p enters it with about the same size: sqrt(2) of the unavoidable error instead of twice the
@@ -27,17 +25,17 @@
 // a masked weight of 0 would still carry a NaN or infinity of V into the sum, the rows that are
 // not finite; those are kept in a bit set, and the rows that do see them add them at the end.
 //
-// Bound by the tensor cores and the exponentials alike: a pair of 128 x 128 tiles at d 128 is
-// 2048 cycles of products and 2048 of ex2.
+// Bound by the tensor cores: a 128 x 64 tile at d 128 takes 8 x 50 cycles for S (6 KB of shared
+// memory a product) and 4 x 64 for P V.
 #include "paged_tc.cuh"
 
 namespace dkv {
 namespace {
 
-constexpr int kPfThreads = 384, kPfM = 128, kPfN = 128;
+constexpr int kPfThreads = 384, kPfM = 128, kPfN = 64;
 constexpr float kPfSlack = 8.f;
 constexpr int kPfIdle = 1 << 24;  // polls without a product before the issuing thread gives up
-constexpr int kPfEdges = 8;  // edge tiles of a CTA: 3 on the diagonal, 3 at the window's edge, 1 at the sinks' end
+constexpr int kPfEdges = 12;  // edge tiles of a CTA (255 positions): 5 on the diagonal, 5 at the window's edge, 1 at the sinks' end
 
 template <typename T>
 constexpr float kPfShift = 0.f;
@@ -46,10 +44,12 @@ constexpr float kPfShift<__half> = 7.f;
 
 template <int D>
 struct PfSmem {
-  static constexpr int kSlots = 5;
-  static constexpr uint32_t kTile = kPfN * D * 2;  // one K or V tile, or one group's Q
-  static constexpr uint32_t kOffRing = 2 * kTile;
-  static constexpr uint32_t kOffBar = kOffRing + kSlots * kTile;
+  static constexpr int kK = 6, kV = 4;                  // slots
+  static constexpr uint32_t kQ = kPfM * D * 2;          // one group's Q
+  static constexpr uint32_t kTile = kPfN * D * 2;       // one K or V tile
+  static constexpr uint32_t kOffK = 2 * kQ;
+  static constexpr uint32_t kOffV = kOffK + kK * kTile;
+  static constexpr uint32_t kOffBar = kOffV + kV * kTile;
   static constexpr uint32_t kBytes = kOffBar + 512;
 };
 
@@ -64,7 +64,7 @@ struct PfKernelArgs {
   int by_heads;  // the groups are two heads (else two 128-token tiles of one head)
 };
 
-// The keys that the queries at positions [p_lo, p_hi] see between them, in 128-key tiles.
+// The keys that the queries at positions [p_lo, p_hi] see between them, in tiles.
 struct KeySpan {
   int lo, hi, st, wt0, n;  // window start, end, sink tiles, first window tile, tiles
   __device__ int key(int j) const { return (j < st ? j : wt0 + j - st) * kPfN; }
@@ -90,7 +90,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                          const __grid_constant__ CUtensorMap vmap) {
   extern __shared__ __align__(1024) uint8_t smem[];
   using S = PfSmem<D>;
-  constexpr int NS = S::kSlots;
   const PagedArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
   const QuerySpan qs = query_span(a, p.q.q_lens, p.q.Tq, b);
@@ -107,33 +106,34 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   const int nt = max(nA, nB);
 
   const uint32_t sb = smem_u32(smem);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kOffBar);  // [slot]
-  uint64_t* empty = full + NS;                                       // [slot]
-  uint64_t* landed = empty + NS;                                     // [edge tile] its V landed, for warp 11 (used once)
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + S::kOffBar);  // [slot]
+  uint64_t* v_full = k_full + S::kK;   // [slot]
+  uint64_t* empty = v_full + S::kV;    // [V slot] O_j, and so S_{j+1}, of both groups are done
+  uint64_t* landed = empty + S::kV;    // [edge tile] its V landed, for warp 11 (used once)
   uint64_t* q_full = landed + kPfEdges;
-  uint64_t* s_full = q_full + 1;   // [group]
-  uint64_t* p_half = s_full + 2;   // [group][half]
-  uint64_t* o_done = p_half + 4;   // [group]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 2);
+  uint64_t* s_full = q_full + 1;       // [group][buffer]
+  uint64_t* p_full = s_full + 4;       // [group][buffer]
+  uint64_t* o_done = p_full + 4;       // [group][buffer]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 4);
   int* n_bad = reinterpret_cast<int*>(tmem_slot + 1);
-  int* bad_key = n_bad + 1;                                          // [edge] first key of an edge tile with bad rows
-  uint32_t* bad_bits = reinterpret_cast<uint32_t*>(bad_key + kPfEdges);  // [edge][4]
+  int* bad_key = n_bad + 1;                                              // [edge] first key of an edge tile with bad rows
+  uint32_t* bad_bits = reinterpret_cast<uint32_t*>(bad_key + kPfEdges);  // [edge][2]
 
   if (threadIdx.x == 0) {
     tma_prefetch_map(&qmap);
     tma_prefetch_map(&kmap);
     tma_prefetch_map(&vmap);
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);  // the commit behind the last product of the tile
+    for (int i = 0; i < S::kK; ++i) mbar_init(&k_full[i], 1);
+    for (int i = 0; i < S::kV; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&empty[i], 2);  // one commit per group
     }
     for (int i = 0; i < kPfEdges; ++i) mbar_init(&landed[i], 1);
     mbar_init(q_full, 1);
-    for (int g = 0; g < 2; ++g) {
-      mbar_init(&s_full[g], 1);
-      mbar_init(&p_half[2 * g], kPfM);
-      mbar_init(&p_half[2 * g + 1], kPfM);
-      mbar_init(&o_done[g], 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], kPfM);
+      mbar_init(&o_done[i], 1);
     }
     *n_bad = 0;
     fence_mbar_init();
@@ -146,148 +146,136 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   bool ok = true;
 
   if (warp == 8) {
-    // =========================== loads
-    if (lane == 0 && nt > 0) {
-      mbar_arrive_expect_tx(q_full, (rowsB > 0 ? 2 : 1) * S::kTile);
+    // =========================== loads: Q, K_0, then V_j and K_{j+1}
+    const uint32_t el = elect_one();
+    if (nt > 0) {
+      if (el) mbar_arrive_expect_tx(q_full, (rowsB > 0 ? 2 : 1) * S::kQ);
       for (int g = 0; g < (rowsB > 0 ? 2 : 1); ++g)
         for (int hf = 0; hf < D / 64; ++hf)
-          tma_load_4d(sb + g * S::kTile + hf * kPfM * 128, &qmap, hf * 64, p.by_heads ? row0 : row0 + g * kPfM,
-                      p.by_heads ? h0 + g : h0, b, q_full);
+          tma_load_4d(sb + g * S::kQ + hf * kPfM * 128, &qmap, hf * 64, p.by_heads ? row0 : row0 + g * kPfM,
+                      p.by_heads ? h0 + g : h0, b, q_full, el);
     }
-    __syncwarp();
-    const int rows = min(a.page_mask + 1, 64), per = kPfN / rows, nbox = per * (D / 64);
-    const int pi = lane % per, hf = lane / per;
-    int i = 0, edges = 0;  // ring position: K of tile j at 2j, V at 2j + 1
-    for (int j = 0; j < nt && ok; ++j) {
-      const int first = ks.key(j) + pi * rows;
-      int page = a.n_pages;  // boxes without a visible key: zeros, wherever the table points
-      if (lane < nbox && first < ks.hi && (first + rows > ks.lo || first < a.sinks)) page = paged_page(a, b, first);
-      for (int kv = 0; kv < 2; ++kv, ++i) {
-        const int sl = i % NS;
-        if (i >= NS) ok = mbar_wait(&empty[sl], (uint32_t)((i / NS - 1) & 1), a.err);
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        // V of an edge tile lands for warp 11, whose arrival then fills the slot
-        uint64_t* bar = kv && !all_seen(a, ks.key(j), p_lo, p_hi) ? &landed[edges++] : &full[sl];
-        if (lane == 0) mbar_arrive_expect_tx(bar, S::kTile);
-        __syncwarp();
-        if (lane < nbox)
-          tma_load_4d(sb + S::kOffRing + sl * S::kTile + hf * kPfN * 128 + pi * rows * 128, kv ? &vmap : &kmap, hf * 64,
-                      first & a.page_mask, kvh, page, bar);
+    const int rows = min(a.page_mask + 1, kPfN), per = kPfN / rows;
+    auto page_of = [&](int j) {  // lane i < per: the page of the tile's i-th run of `rows` keys
+      const int first = ks.key(j) + lane * rows;
+      // runs without a visible key: zeros, wherever the table points
+      return j < nt && lane < per && first < ks.hi && (first + rows > ks.lo || first < a.sinks) ? paged_page(a, b, first)
+                                                                                              : a.n_pages;
+    };
+    auto load = [&](const CUtensorMap* map, uint32_t at, int j, int page, uint64_t* bar) {
+      if (el) mbar_arrive_expect_tx(bar, S::kTile);
+      const int y = ks.key(j) & a.page_mask;
+      for (int i = 0; i < per; ++i) {
+        const int pg = __shfl_sync(0xffffffffu, page, i);
+#pragma unroll
+        for (int hf = 0; hf < D / 64; ++hf)
+          tma_load_4d(sb + at + hf * kPfN * 128 + i * rows * 128, map, hf * 64, y, kvh, pg, bar, el);
       }
+    };
+    int page = page_of(0), next = page_of(1), edges = 0, j = 0;
+    if (nt > 0) load(&kmap, S::kOffK, 0, page, &k_full[0]);
+    for (; j < nt && ok; ++j) {
+      const int after = page_of(j + 2);  // looked up a tile ahead of its use
+      // V_{j-4} is read, and K_{j-5} was before it
+      if (j >= S::kV) ok = mbar_wait(&empty[j % S::kV], (uint32_t)((j / S::kV - 1) & 1), a.err);
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      // V of an edge tile lands for warp 11, whose arrival then fills the slot
+      const bool edge = !all_seen(a, ks.key(j), p_lo, p_hi);
+      load(&vmap, S::kOffV + (j % S::kV) * S::kTile, j, page, edge ? &landed[edges++] : &v_full[j % S::kV]);
+      if (j + 1 < nt) load(&kmap, S::kOffK + ((j + 1) % S::kK) * S::kTile, j + 1, next, &k_full[(j + 1) % S::kK]);
+      page = next;
+      next = after;
     }
     // every copy has landed before the CTA may end (also after a wait that gave up)
     if (nt > 0) mbar_wait(q_full, 0, a.err);
-    for (int x = max(0, i - NS); x < i; ++x) mbar_wait(&full[x % NS], (uint32_t)((x / NS) & 1), a.err);
-  } else if (warp == 9) {
-    // =========================== products: whichever of the two groups has one ready
+    for (int x = max(0, j - S::kV); x < j; ++x) mbar_wait(&v_full[x % S::kV], (uint32_t)((x / S::kV) & 1), a.err);
+    for (int x = max(0, min(j, nt - 1) + 1 - S::kK); x <= min(j, nt - 1); ++x)
+      mbar_wait(&k_full[x % S::kK], (uint32_t)((x / S::kK) & 1), a.err);
+  } else if (warp == 9 || warp == 10) {
+    // =========================== products of group g
     // The whole warp walks through here and one elected lane issues: in code that one lane runs
-    // alone the operands are not known to be uniform, and an issue took 150 cycles instead of the 64
-    // that a product needs.
+    // alone the operands are not known to be uniform, and an issue took 75 to 150 cycles.
     constexpr uint32_t id_s = tc_idesc(Num<T>::kUmma, false, kPfN), id_o = tc_idesc(Num<T>::kUmma, true, D);
     const uint32_t el = elect_one();
-    const int n[2] = {nA, nB};
-    int js[2] = {0, 0}, jv[2] = {0, 0};  // tiles of which S_g, and O_g, have been issued
-    int half[2] = {0, 0};                // halves of P_g taken of the tile at hand
-    int landed_k = 0, landed_v = 0;      // tiles known to have landed
-    int idle = 0;
-    auto over = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, mbar_test(bar, (uint32_t)parity)) != 0; };
-    if (nt > 0) ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, a.err));
-    while (ok && (jv[0] < n[0] || jv[1] < n[1])) {
-      bool any = false;
+    const int g = warp - 9, n = g ? nB : nA, n_other = g ? nA : nB;
+    const uint32_t tg = tmem + 256u * g;
+    const uint64_t qd = tc_desc(sb + g * S::kQ, 16, 1024);
+    auto wait = [&](uint64_t* bar, int parity) { ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, (uint32_t)parity, a.err)); };
+    auto scores = [&](int j) {
+      const int sl = j % S::kK, buf = j & 1;
+      wait(&k_full[sl], (j / S::kK) & 1);
+      if (j >= 2) wait(&o_done[2 * g + buf], ((j - 2) >> 1) & 1);  // the buffer holds P_{j-2}
+      if (!ok) return;
+      tc_fence_after();
+      const uint64_t kd = tc_desc(sb + S::kOffK + sl * S::kTile, 16, 1024);
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const int o = 1 - g;
-        const uint32_t ts = tmem + 256u * g;
-        if (js[g] == jv[g]) {  // the next product is S_g of tile j, once O_g of tile j - 1 is done
-          const int j = js[g], sl = 2 * j % NS;
-          if (j >= n[g] || (j > 0 && !over(&o_done[g], (j - 1) & 1))) continue;
-          if (landed_k <= j) {
-            if (!over(&full[sl], (2 * j / NS) & 1)) continue;
-            landed_k = j + 1;
-          }
-          tc_fence_after();
-          const uint64_t qd = tc_desc(sb + g * S::kTile, 16, 1024), kd = tc_desc(sb + S::kOffRing + sl * S::kTile, 16, 1024);
+      for (int k = 0; k < D / 16; ++k)  // 16 channels: 32 bytes of a 128-byte row, then the next 64 channels
+        tc_mma(tg + kPfN * buf, qd + (uint64_t)(((k >> 2) * kPfM * 128 + (k & 3) * 32) >> 4),
+               kd + (uint64_t)(((k >> 2) * kPfN * 128 + (k & 3) * 32) >> 4), id_s, k > 0, el);
+      tc_commit(&s_full[2 * g + buf], el);
+    };
+    if (n > 0) {
+      wait(q_full, 0);
+      scores(0);
+      for (int j = 0; j < n && ok; ++j) {
+        if (j + 1 < n) scores(j + 1);
+        const int sl = j % S::kV, buf = j & 1;
+        wait(&v_full[sl], (j / S::kV) & 1);
+        wait(&p_full[2 * g + buf], (j >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t vd = tc_desc(sb + S::kOffV + sl * S::kTile, kPfN * 128, 1024);
+        const uint32_t ts = tg + kPfN * buf;
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {  // 16 channels: 32 bytes of a 128-byte row, then the next 64 channels
-            const uint64_t step = (uint64_t)(((k >> 2) * kPfN * 128 + (k & 3) * 32) >> 4);
-            tc_mma(ts, qd + step, kd + step, id_s, k > 0, el);
-          }
-          tc_commit(&s_full[g], el);
-          js[g] = j + 1;
-          if (js[o] > j || n[o] <= j) tc_commit(&empty[sl], el);  // the other group is past this tile
-        } else {  // a half of O_g of tile j
-          const int j = jv[g], i = 2 * j + 1, sl = i % NS;
-          if (!over(&p_half[2 * g + half[g]], j & 1)) continue;
-          if (landed_v <= j) {
-            if (!over(&full[sl], (i / NS) & 1)) continue;
-            landed_v = j + 1;
-          }
-          tc_fence_after();
-          const uint64_t vd = tc_desc(sb + S::kOffRing + sl * S::kTile, kPfN * 128, 1024);
-          if (half[g] == 0) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)  // 16 keys: 16 rows of 128 bytes
-              tc_mma_ta(ts + 128u, ts + 8u * k, vd + (uint64_t)(k * 16 * 128 >> 4), id_o, k > 0 ? 1u : (j > 0 ? 1u : 0u), el);
-            half[g] = 1;
-          } else {
-#pragma unroll
-            for (int k = 4; k < 8; ++k) tc_mma_ta(ts + 128u, ts + 8u * k, vd + (uint64_t)(k * 16 * 128 >> 4), id_o, 1u, el);
-            tc_commit(&o_done[g], el);
-            half[g] = 0;
-            jv[g] = j + 1;
-            if (jv[o] > j || n[o] <= j) tc_commit(&empty[sl], el);
-          }
-        }
-        any = true;
-      }
-      idle = any ? 0 : idle + 1;
-      if (idle > kPfIdle) {
-        if (el) raise_error(a.err, DKV_DEVERR_TIMEOUT);
-        ok = false;
+        for (int k = 0; k < kPfN / 16; ++k)  // 16 keys: 16 rows of 128 bytes
+          tc_mma_ta(tg + 128u, ts + 8u * k, vd + (uint64_t)(k * 16 * 128 >> 4), id_o, k > 0 ? 1u : (j > 0 ? 1u : 0u), el);
+        tc_commit(&o_done[2 * g + buf], el);
+        // once for this group, once more where the other has no tile j
+        tc_commit(&empty[sl], el);
+        if (j >= n_other) tc_commit(&empty[sl], el);
       }
     }
   } else if (warp == 11) {
     // =========================== V rows of edge tiles
     int edges = 0;
     for (int j = 0; j < nt && ok; ++j) {
-      const int k0 = ks.key(j), i = 2 * j + 1, sl = i % NS;
-      if (!all_seen(a, k0, p_lo, p_hi)) {
-        ok = mbar_wait(&landed[edges++], 0, a.err);
-        const uint32_t vb = sb + S::kOffRing + sl * S::kTile;
-        uint32_t bad = 0;  // rows lane, lane + 32, ... with a value that is not finite
-        for (int x = 0; x < 4; ++x) {
-          const int r = 32 * x + lane, t = k0 + r;
-          const bool some = t < ks.hi && (t >= ks.lo || t < a.sinks);  // a row of the CTA sees it
-          bool odd = false;
-          if (some) {
-            constexpr uint32_t kExp = Num<T>::kUmma ? 0x7f80u : 0x7c00u;
+      const int k0 = ks.key(j), sl = j % S::kV;
+      if (all_seen(a, k0, p_lo, p_hi)) continue;
+      ok = mbar_wait(&landed[edges++], 0, a.err);
+      const uint32_t vb = sb + S::kOffV + sl * S::kTile;
+      uint32_t bad = 0;  // rows lane, lane + 32 with a value that is not finite
+      for (int x = 0; x < kPfN / 32; ++x) {
+        const int r = 32 * x + lane, t = k0 + r;
+        const bool some = t < ks.hi && (t >= ks.lo || t < a.sinks);  // a row of the CTA sees it
+        bool odd = false;
+        if (some) {
+          constexpr uint32_t kExp = Num<T>::kUmma ? 0x7f80u : 0x7c00u;
 #pragma unroll 4
-            for (int ch = 0; ch < D / 8; ++ch) {
-              const uint4 v = lds128(vb + sw128(kPfN, r, ch));
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          for (int ch = 0; ch < D / 8; ++ch) {
+            const uint4 v = lds128(vb + sw128(kPfN, r, ch));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-              for (int y = 0; y < 4; ++y) odd |= (w[y] & kExp) == kExp || ((w[y] >> 16) & kExp) == kExp;
-            }
-          }
-          if (!some || odd)
-            for (int ch = 0; ch < D / 8; ++ch) sts128(vb + sw128(kPfN, r, ch), make_uint4(0, 0, 0, 0));
-          const uint32_t bits = __ballot_sync(0xffffffffu, odd);
-          if (lane == x) bad = bits;
-        }
-        if (__any_sync(0xffffffffu, lane < 4 && bad)) {
-          const int at = *n_bad;
-          __syncwarp();
-          if (at < kPfEdges) {
-            if (lane < 4) bad_bits[4 * at + lane] = bad;
-            if (lane == 0) { bad_key[at] = k0; *n_bad = at + 1; }
+            for (int y = 0; y < 4; ++y) odd |= (w[y] & kExp) == kExp || ((w[y] >> 16) & kExp) == kExp;
           }
         }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[sl]);
+        if (!some || odd)
+          for (int ch = 0; ch < D / 8; ++ch) sts128(vb + sw128(kPfN, r, ch), make_uint4(0, 0, 0, 0));
+        const uint32_t bits = __ballot_sync(0xffffffffu, odd);
+        if (lane == x) bad = bits;
       }
+      if (__any_sync(0xffffffffu, bad)) {
+        const int at = *n_bad;
+        __syncwarp();
+        if (at < kPfEdges) {
+          if (lane < kPfN / 32) bad_bits[kPfN / 32 * at + lane] = bad;
+          if (lane == 0) { bad_key[at] = k0; *n_bad = at + 1; }
+        }
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&v_full[sl]);
     }
-  } else if (warp < 8) {  // (warp 10 has no work)
+  } else if (warp < 8) {
     // =========================== softmax: one query row per thread
     const int g = warp >> 2, rw = warp & 3, row = 32 * rw + lane;
     const int n = g ? nB : nA, rows = g ? rowsB : rowsA;
@@ -295,11 +283,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const int head = p.by_heads ? h0 + g : h0;
     // positions of the group's rows (the tile is unmasked when all of them see all of it)
     const int g_lo = p.by_heads ? p_lo : p_lo + g * kPfM, g_hi = g_lo + rows - 1;
-    const uint32_t ts = tmem + ((uint32_t)(32 * rw) << 16) + 256u * g, to = ts + 128u;
+    const uint32_t tg = tmem + ((uint32_t)(32 * rw) << 16) + 256u * g, to = tg + 128u;
     const float slog2 = a.scale_log2;
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < n; ++j) {
-      if (ok) ok = mbar_wait(&s_full[g], (uint32_t)(j & 1), a.err);
+      const int buf = j & 1;
+      const uint32_t ts = tg + kPfN * buf;
+      if (ok) ok = mbar_wait(&s_full[2 * g + buf], (uint32_t)((j >> 1) & 1), a.err);
       tc_fence_after();
       uint32_t s[kPfN];
 #pragma unroll
@@ -312,14 +302,18 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         for (int c = 0; c < kPfN; ++c)
           if (c > hi || (c < lo && c >= sk)) s[c] = 0xff800000u;
       }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      float mx[8];
 #pragma unroll
-      for (int c = 0; c < kPfN; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * slog2;
-      const bool up = top > m + kPfSlack || (m == -INFINITY && top > m);
+      for (int c = 0; c < 8; ++c) mx[c] = __uint_as_float(s[c]);
+#pragma unroll
+      for (int c = 8; c < kPfN; ++c) mx[c & 7] = fmaxf(mx[c & 7], __uint_as_float(s[c]));
+      const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * slog2;
+      const bool up = top > m + kPfSlack;
       const float al = up ? fast_exp2(m - top) : 1.f;
       if (up) m = top;
-      if (j > 0 && __any_sync(0xffffffffu, up)) {  // O_{j-1} is done: rescale it
+      if (j > 0 && __any_sync(0xffffffffu, up)) {  // rescale O once O_{j-1} is done
+        if (ok) ok = mbar_wait(&o_done[2 * g + (buf ^ 1)], (uint32_t)(((j - 1) >> 1) & 1), a.err);
+        tc_fence_after();
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -333,25 +327,21 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const float ms = (m == -INFINITY ? 0.f : m) - kPfShift<T>;
       const float2 scale2 = make_float2(slog2, slog2), shift2 = make_float2(-ms, -ms);
       float2 lp[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      uint32_t w[kPfN / 2];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t w[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int c = 64 * half + 2 * e;
-          const float2 x = fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, shift2);
-          const float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-          lp[e & 1] = add2(lp[e & 1], y);
-          w[e] = Num<T>::pack(y.x, y.y);
-        }
-        tc_st32(ts + 32 * half, w);
-        tc_st_wait();
-        tc_fence_before();
-        mbar_arrive(&p_half[2 * g + half]);
+      for (int e = 0; e < kPfN / 2; ++e) {
+        const float2 x = fma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), scale2, shift2);
+        const float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+        lp[e & 1] = add2(lp[e & 1], y);
+        w[e] = Num<T>::pack(y.x, y.y);
       }
+      tc_st32(ts, w);
       l = fmaf(l, al, (lp[0].x + lp[1].x) + (lp[0].y + lp[1].y));
+      tc_st_wait();
+      tc_fence_before();
+      mbar_arrive(&p_full[2 * g + buf]);
     }
-    if (n > 0 && ok) ok = mbar_wait(&o_done[g], (uint32_t)((n - 1) & 1), a.err);
+    if (n > 0 && ok) ok = mbar_wait(&o_done[2 * g + ((n - 1) & 1)], (uint32_t)(((n - 1) >> 1) & 1), a.err);
     tc_fence_after();
     const bool live = row < rows;
     const float il = n == 0 || l == 0.f ? 0.f : 1.f / l;  // a row that sees no key: zeros

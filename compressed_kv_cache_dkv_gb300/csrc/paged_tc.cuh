@@ -17,12 +17,6 @@ __device__ inline uint64_t tc_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
 __device__ constexpr uint32_t tc_idesc(uint32_t fmt, bool b_mn, uint32_t n) {
   return (1u << 4) | (fmt << 7) | (fmt << 10) | ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
-// one lane of a converged warp (1 in it, 0 in the others)
-__device__ inline uint32_t elect_one() {
-  uint32_t e;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
-  return e;
-}
 // The lane with `el` issues; the whole warp calls these with the same operands.
 // A and B from shared memory
 __device__ inline void tc_mma(uint32_t dt, uint64_t ad, uint64_t bd, uint32_t id, uint32_t acc, uint32_t el) {

@@ -1,198 +1,343 @@
 // dkv_paged_weights: softmax weights summed by key, weights[t] += sum over queries of
 // 2^(c q.k_t - lse), on the tcgen05 tensor cores.
 //
-// A CTA owns 128 keys of one (sequence, KV head) and goes through every query row that can see
-// them, head by head: S^T = K Q^T puts one key into each TMEM lane, so a thread sums its key's
-// weights over the columns in registers and every key has one owner (no atomics, a fixed order).
-// Two warpgroups take query tiles in turn, each with its own 128 TMEM columns; warp 8 streams
-// the query tiles with TMA through two slots, one lane of warp 9 issues the products.  Two CTAs
-// share a multiprocessor.  Bound by the exponentials (one per visible pair: twice the cycles of
-// its product at d 128) for whole prompts, by the read of K for a few queries; the query tile is
-// cut to 32 or 64 rows when there are no more queries, since a product's time goes with its rows.
+// S^T = K Q^T for 128 keys and up to 128 query columns puts one key into each TMEM lane: a thread
+// sums its key's weights over the columns in registers, every key has one owner, and the order is
+// fixed (no atomics).  Two warpgroups take column tiles in turn, each with its own 128 TMEM columns;
+// warp 8 streams operands with TMA through three slots, warp 9 issues the products; two CTAs share
+// a multiprocessor.
+//
+// Few queries (those of all heads of a group fit 128 columns, padded to 16, 32, 64 or 128 a head):
+// the column tile stays, two slots stream the keys, a CTA walks kRun key tiles.  Bound by the read
+// of K.
+// Many queries: the keys stay, two slots stream the query tiles of one head after the other; a
+// cluster of kCluster CTAs shares the queries of its keys and adds the parts in rank order, since
+// the first keys of a prompt are seen by all its queries and would take many times the average.
+// Bound by the products (8 x 64 cycles a tile at d 128) and, close behind, their exponentials.
 #include "paged_tc.cuh"
 
 namespace dkv {
 namespace {
 
-constexpr int kWtThreads = 320, kWtM = 128, kWtN = 128;  // keys, query rows of a tile at most
+constexpr int kWtThreads = 320, kWtM = 128, kWtN = 128;  // keys, query columns of a tile at most
+constexpr int kRun = 8;       // key tiles of a CTA when the queries stay
+constexpr int kCluster = 8;   // CTAs that share the queries when the keys stay
 
 template <int D>
 struct WtSmem {
-  static constexpr uint32_t kTile = 128 * D * 2;  // K tile, or a slot of query rows
-  static constexpr uint32_t kOffQ = kTile;
-  static constexpr uint32_t kOffLse = kOffQ + 2 * kTile;  // [warpgroup][128] base-2 lse
-  static constexpr uint32_t kOffBar = kOffLse + 2 * kWtN * 4;
+  static constexpr uint32_t kTile = 128 * D * 2;          // a slot: 128 keys or query rows
+  static constexpr uint32_t kOffLse = 3 * kTile;          // [warpgroup][128] base-2 lse
+  static constexpr uint32_t kOffPart = kOffLse + 2 * kWtN * 4;  // [warpgroup][128] sums
+  static constexpr uint32_t kOffRank = kOffPart + 2 * kWtM * 4;  // [rank][128] sums of the cluster
+  static constexpr uint32_t kOffBar = kOffRank + kCluster * kWtM * 4;
   static constexpr uint32_t kBytes = kOffBar + 128;
+};
+
+struct WtArgs {
+  PagedArgs a;
+  PagedQuery q;
+  const float* lse;
+  float* weights;
+  int stay;  // the queries stay: `rows` columns a head, all heads of a group in one tile
+  int rows;  // query rows of a box
 };
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kWtThreads, 2)
-    paged_weights_kernel(PagedArgs a, PagedQuery q, const float* __restrict__ lse, float* __restrict__ weights, int qn,
-                         const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap) {
+    paged_weights_kernel(WtArgs p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap) {
   extern __shared__ __align__(1024) uint8_t smem[];
   using S = WtSmem<D>;
+  const PagedArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool stay = p.stay != 0;
   // of all units the earlier keys, which more queries see, first
-  const int u = blockIdx.x, b = u / a.Hkv, h = u % a.Hkv, k0 = blockIdx.y * kWtM;
-  const QuerySpan qs = query_span(a, q.q_lens, q.Tq, b);
-  // query rows that see a key of the tile
-  const int r_lo = max(0, k0 - qs.off);
-  int r_hi = qs.n - 1;
-  if (a.window > 0 && k0 >= a.sinks) r_hi = (int)min((int64_t)r_hi, (int64_t)k0 + kWtM - 2 + a.window - qs.off);
-  if (k0 >= qs.len || r_lo > r_hi) return;
-  const int t_lo = r_lo / qn, per = r_hi / qn - t_lo + 1, nq = per * a.G;  // query tiles, those of a head side by side
+  const int ncl = stay ? 1 : kCluster, rank = stay ? 0 : (int)cluster_ctarank();
+  const int u = (int)blockIdx.x / ncl, b = u / a.Hkv, h = u % a.Hkv, qn = p.rows;
+  const QuerySpan qs = query_span(a, p.q.q_lens, p.q.Tq, b);
+  const int kt0 = (int)blockIdx.y * (stay ? kRun : 1), kt1 = min(kt0 + (stay ? kRun : 1), (qs.len + kWtM - 1) / kWtM);
+  // query rows [lo, hi] that see a key of tile kt
+  auto rows_of = [&](int kt, int& lo, int& hi) {
+    const int k0 = kt * kWtM;
+    lo = max(0, k0 - qs.off);
+    hi = qs.n - 1;
+    if (a.window > 0 && k0 >= a.sinks) hi = (int)min((int64_t)hi, (int64_t)k0 + kWtM - 2 + a.window - qs.off);
+  };
+  // column tiles of key tile kt: [c0, c0 + n) of the head-by-head list (this CTA's share of it)
+  struct Cols { int per, t_lo, c0, n; };
+  auto cols_of = [&](int kt) {
+    Cols c = {0, 0, 0, 0};
+    int lo, hi;
+    rows_of(kt, lo, hi);
+    if (lo > hi) return c;
+    if (stay) { c.n = c.per = 1; return c; }
+    c.t_lo = lo / qn;
+    c.per = hi / qn - c.t_lo + 1;
+    const int all = c.per * a.G;
+    c.c0 = all * rank / ncl;
+    c.n = all * (rank + 1) / ncl - c.c0;
+    return c;
+  };
+  {
+    bool any = false;  // the same answer in every CTA of a cluster
+    for (int kt = kt0; kt < kt1; ++kt) {
+      int lo, hi;
+      rows_of(kt, lo, hi);
+      any |= lo <= hi;
+    }
+    if (!any) return;
+  }
 
   const uint32_t sb = smem_u32(smem);
   float* lse2 = reinterpret_cast<float*>(smem + S::kOffLse);
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + S::kOffBar);
-  uint64_t* q_full = k_full + 1;   // [slot]
-  uint64_t* q_empty = q_full + 2;  // [slot]
-  uint64_t* s_full = q_empty + 2;  // [warpgroup]
+  float* part = reinterpret_cast<float*>(smem + S::kOffPart);
+  float* ranks = reinterpret_cast<float*>(smem + S::kOffRank);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kOffBar);  // [slot]: the operand that stays is in slot 2
+  uint64_t* empty = full + 3;     // [slot]
+  uint64_t* s_full = empty + 2;   // [warpgroup]
   uint64_t* s_empty = s_full + 2;  // [warpgroup]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_empty + 2);
   if (threadIdx.x == 0) {
     tma_prefetch_map(&kmap);
     tma_prefetch_map(&qmap);
-    mbar_init(k_full, 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&full[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], 1);
+      mbar_init(&empty[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], 128);
     }
     fence_mbar_init();
   }
+  if (!stay) cluster_arrive_relaxed();  // the CTAs that rank 0 hears from may find it not yet started
   if (warp == 0) tc_alloc<256>(tmem_slot);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (!stay) cluster_wait();
   const uint32_t tmem = *tmem_slot;
   bool ok = true;
 
   if (warp == 8) {
     // =========================== loads
-    const int rows = min(a.page_mask + 1, 64), pk = kWtM / rows, nbox = pk * (D / 64);
-    const int pi = lane % pk, hf = lane / pk, first = k0 + pi * rows;
+    const uint32_t el = elect_one();
+    const int rows = min(a.page_mask + 1, 64), pk = kWtM / rows;  // runs of `rows` keys
     const int lo = paged_window_lo(a, max(qs.off, 0));
-    const bool need = first < qs.len && (first + rows > lo || first < a.sinks);  // else zeros, wherever the table points
-    if (lane == 0) mbar_arrive_expect_tx(k_full, S::kTile);
-    __syncwarp();
-    if (lane < nbox)
-      tma_load_4d(sb + hf * kWtM * 128 + pi * rows * 128, &kmap, hf * 64, first & a.page_mask, h,
-                  need ? paged_page(a, b, first) : a.n_pages, k_full);
-    int i = 0;
-    for (; i < nq && ok; ++i) {
-      const int sl = i & 1;
-      if (i >= 2) ok = mbar_wait(&q_empty[sl], (uint32_t)((i / 2 - 1) & 1), a.err);
-      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&q_full[sl], (uint32_t)qn * D * 2);
-        for (int x = 0; x < D / 64; ++x)
-          tma_load_4d(sb + S::kOffQ + sl * S::kTile + x * qn * 128, &qmap, x * 64, (t_lo + i % per) * qn, h * a.G + i / per, b,
-                      &q_full[sl]);
+    auto load_k = [&](int kt, int sl) {
+      const int k0 = kt * kWtM, first = k0 + lane * rows;
+      // runs without a visible key: zeros, wherever the table points
+      const int page = lane < pk && first < qs.len && (first + rows > lo || first < a.sinks) ? paged_page(a, b, first) : a.n_pages;
+      if (el) mbar_arrive_expect_tx(&full[sl], S::kTile);
+      for (int i = 0; i < pk; ++i) {
+        const int pg = __shfl_sync(0xffffffffu, page, i);
+#pragma unroll
+        for (int hf = 0; hf < D / 64; ++hf)
+          tma_load_4d(sb + sl * S::kTile + hf * kWtM * 128 + i * rows * 128, &kmap, hf * 64, (k0 + i * rows) & a.page_mask, h, pg,
+                      &full[sl], el);
       }
-      __syncwarp();
+    };
+    // `n` heads' boxes of qn rows, side by side in column tiles of `ncol`
+    auto load_q = [&](int head, int n, int row, int sl) {
+      if (el) mbar_arrive_expect_tx(&full[sl], (uint32_t)(n * qn) * D * 2);
+      for (int x = 0; x < n; ++x)
+#pragma unroll
+        for (int hf = 0; hf < D / 64; ++hf)
+          tma_load_4d(sb + sl * S::kTile + hf * n * qn * 128 + x * qn * 128, &qmap, hf * 64, row, head + x, b, &full[sl], el);
+    };
+    int i = 0;
+    if (stay) load_q(h * a.G, a.G, 0, 2);
+    else load_k(kt0, 2);
+    for (int kt = kt0; kt < kt1 && ok; ++kt) {
+      const Cols c = cols_of(kt);
+      for (int x = 0; x < c.n; ++x, ++i) {
+        const int sl = i & 1;
+        if (i >= 2) ok = mbar_wait(&empty[sl], (uint32_t)((i / 2 - 1) & 1), a.err);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        if (stay) load_k(kt, sl);
+        else load_q(h * a.G + (c.c0 + x) / c.per, 1, (c.t_lo + (c.c0 + x) % c.per) * qn, sl);
+      }
     }
     // every copy has landed before the CTA may end (also after a wait that gave up)
-    mbar_wait(k_full, 0, a.err);
-    for (int x = max(0, i - 2); x < i; ++x) mbar_wait(&q_full[x & 1], (uint32_t)((x / 2) & 1), a.err);
+    mbar_wait(&full[2], 0, a.err);
+    for (int x = max(0, i - 2); x < i; ++x) mbar_wait(&full[x & 1], (uint32_t)((x / 2) & 1), a.err);
   } else if (warp == 9) {
     // =========================== products
-    // (the whole warp, one elected lane issuing: see the prefill kernel)
-    const uint32_t el = elect_one(), id = tc_idesc(Num<T>::kUmma, false, (uint32_t)qn);
-    const uint64_t kd = tc_desc(sb, 16, 1024);
-    ok = mbar_wait(k_full, 0, a.err);
-    for (int i = 0; i < nq; ++i) {
-      const int w = i & 1;
-      ok = ok && mbar_wait(&q_full[w], (uint32_t)((i / 2) & 1), a.err);
-      if (i >= 2) ok = ok && mbar_wait(&s_empty[w], (uint32_t)((i / 2 - 1) & 1), a.err);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
-      const uint64_t qd = tc_desc(sb + S::kOffQ + w * S::kTile, 16, 1024);
+    const uint32_t el = elect_one();
+    const int ncol = stay ? a.G * qn : qn;
+    const uint32_t id = tc_idesc(Num<T>::kUmma, false, (uint32_t)ncol);
+    ok = __all_sync(0xffffffffu, mbar_wait(&full[2], 0, a.err));
+    int i = 0;
+    for (int kt = kt0; kt < kt1 && ok; ++kt) {
+      const Cols c = cols_of(kt);
+      for (int x = 0; x < c.n; ++x, ++i) {
+        const int w = i & 1;
+        ok = ok && mbar_wait(&full[w], (uint32_t)((i / 2) & 1), a.err);
+        if (i >= 2) ok = ok && mbar_wait(&s_empty[w], (uint32_t)((i / 2 - 1) & 1), a.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t kd = tc_desc(sb + (stay ? w : 2) * S::kTile, 16, 1024), qd = tc_desc(sb + (stay ? 2 : w) * S::kTile, 16, 1024);
+        const uint64_t half = (uint64_t)(ncol * 128 >> 4);  // the query tile's second 64 channels
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        tc_mma(tmem + 128u * w, kd + (uint64_t)(((k >> 2) * kWtM * 128 + (k & 3) * 32) >> 4),
-               qd + (uint64_t)(((k >> 2) * qn * 128 + (k & 3) * 32) >> 4), id, k > 0, el);
-      tc_commit(&q_empty[w], el);
-      tc_commit(&s_full[w], el);
+        for (int k = 0; k < D / 16; ++k)
+          tc_mma(tmem + 128u * w, kd + (uint64_t)(((k >> 2) * kWtM * 128 + (k & 3) * 32) >> 4),
+                 qd + (k >> 2) * half + (uint64_t)((k & 3) * 32 >> 4), id, k > 0, el);
+        tc_commit(&s_full[w], el);
+        tc_commit(&empty[w], el);
+      }
     }
   } else {
     // =========================== sums: one key per thread and warpgroup
-    const int w = warp >> 2, row = threadIdx.x & 127, t = k0 + row;
+    const int w = warp >> 2, row = threadIdx.x & 127;
     const uint32_t ts = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 128u * w;
     float* l2 = lse2 + kWtN * w;
-    const float slog2 = a.scale_log2;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int i = w; i < nq; i += 2) {
-      const int r0 = (t_lo + i % per) * qn, head = h * a.G + i / per;
-      if (row < qn) {
-        const float v = r0 + row < qs.n ? __ldg(lse + ((int64_t)b * a.Hq + head) * q.Tq + r0 + row) : -INFINITY;
-        l2[row] = v == -INFINITY ? INFINITY : v * 1.4426950408889634f;
-      }
-      named_bar_sync(1 + w, 128);
-      if (ok) ok = mbar_wait(&s_full[w], (uint32_t)((i / 2) & 1), a.err);
-      tc_fence_after();
-      // columns [c_lo, c_hi] see this key; the warp's keys bound the columns worth loading
-      const int c_lo = t - qs.off - r0;
-      const int c_end = min(qn, qs.n - r0);
-      const int64_t c_win = a.window > 0 && t >= a.sinks ? (int64_t)t + a.window - 1 - qs.off - r0 : c_end - 1;
-      const int c_hi = (int)min((int64_t)c_end - 1, c_win);
-      const int w_lo = __reduce_min_sync(0xffffffffu, c_lo), w_hi = __reduce_max_sync(0xffffffffu, c_hi);
-      const bool whole = __all_sync(0xffffffffu, c_lo <= 0 && c_hi >= c_end - 1);
+    const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
+    auto sync_group = [&]() { if (w == 0) named_bar_sync(1, 128); else named_bar_sync(2, 128); };
+    // minus the base-2 lse of column `row` of a tile (-inf for a column without a query, so that it adds 0)
+    auto column = [&](int head, int r, bool live) {
+      if (!live || r >= qs.n) return -INFINITY;
+      const float v = __ldg(p.lse + ((int64_t)b * a.Hq + head) * p.q.Tq + r);
+      return v == -INFINITY ? -INFINITY : v * -1.4426950408889634f;
+    };
+    if (stay) {
+      l2[row] = column(h * a.G + row / qn, row % qn, row < a.G * qn);
+      sync_group();
+    }
+    int i = 0;
+    for (int kt = kt0; kt < kt1; ++kt) {
+      const Cols c = cols_of(kt);
+      const int t = kt * kWtM + row;
+      float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      float next = 0.f;
+      auto fetch = [&](int x) { return column(h * a.G + (c.c0 + x) / c.per, (c.t_lo + (c.c0 + x) % c.per) * qn + row, row < qn); };
+      const int x0 = (w ^ i) & 1;  // this warpgroup's first column tile
+      if (!stay && x0 < c.n) next = fetch(x0);
+      for (int x = x0; x < c.n; x += 2) {
+        const int at = (i + x) / 2;  // tiles of this warpgroup so far
+        const int r0 = stay ? 0 : (c.t_lo + (c.c0 + x) % c.per) * qn;
+        if (!stay) {
+          l2[row] = next;
+          if (x + 2 < c.n) next = fetch(x + 2);
+          sync_group();
+        }
+        if (ok) ok = mbar_wait(&s_full[w], (uint32_t)(at & 1), a.err);
+        tc_fence_after();
+        // rows [v_lo, v_hi) of the tile see this key
+        const int v_lo = max(t - qs.off - r0, 0);
+        int v_hi = min(qn, qs.n - r0);
+        const bool bound = a.window > 0 && t >= a.sinks;
+        if (bound) v_hi = (int)max((int64_t)0, min((int64_t)v_hi, (int64_t)t + a.window - qs.off - r0));
+        const int ncol = stay ? a.G * qn : qn;
+        if (__all_sync(0xffffffffu, v_lo == 0 && v_hi == qn)) {
 #pragma unroll
-      for (int c = 0; c < kWtN / 32; ++c) {
-        if (32 * c + 31 < w_lo || 32 * c > w_hi) continue;
-        uint32_t s[32];
-        tc_ld32(ts + 32 * c, s);
-        tc_ld_wait();
-        if (whole && 32 * c + 31 < c_end) {
+          for (int ch = 0; ch < kWtN / 32; ++ch) {
+            if (32 * ch >= ncol) break;
+            uint32_t s[32];
+            tc_ld32(ts + 32 * ch, s);
+            tc_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) acc[e & 3] += fast_exp2(fmaf(__uint_as_float(s[e]), slog2, -l2[32 * c + e]));
+            for (int e = 0; e < 32; e += 4) {
+              if (32 * ch + e >= ncol) break;  // (columns come in sixteens)
+              const float4 m = *reinterpret_cast<const float4*>(l2 + 32 * ch + e);
+              const float2 y0 = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale2, make_float2(m.x, m.y));
+              const float2 y1 = fma2(make_float2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), scale2, make_float2(m.z, m.w));
+              acc[0] = add2(acc[0], make_float2(fast_exp2(y0.x), fast_exp2(y0.y)));
+              acc[1] = add2(acc[1], make_float2(fast_exp2(y1.x), fast_exp2(y1.y)));
+            }
+          }
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float x = fast_exp2(fmaf(__uint_as_float(s[e]), slog2, -l2[32 * c + e]));
-            acc[e & 3] += 32 * c + e >= c_lo && 32 * c + e <= c_hi ? x : 0.f;
+          for (int ch = 0; ch < kWtN / 32; ++ch) {
+            if (32 * ch >= ncol) break;
+            uint32_t s[32];
+            tc_ld32(ts + 32 * ch, s);
+            tc_ld_wait();
+            if (!stay && !__any_sync(0xffffffffu, v_lo < 32 * ch + 32 && v_hi > 32 * ch)) continue;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int r = stay ? (32 * ch + e) & (qn - 1) : 32 * ch + e;
+              const float x2 = fast_exp2(fmaf(__uint_as_float(s[e]), a.scale_log2, l2[32 * ch + e]));
+              // (what lies in a hidden column, or beyond the last, is not looked at)
+              acc[e & 1].x += r >= v_lo && r < v_hi && 32 * ch + e < ncol ? x2 : 0.f;
+            }
           }
         }
+        tc_fence_before();
+        mbar_arrive(&s_empty[w]);
+        if (!stay) sync_group();  // l2 is read
       }
-      tc_fence_before();
-      mbar_arrive(&s_empty[w]);
-      named_bar_sync(1 + w, 128);  // l2 is read
+      i += c.n;
+      const float sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+      if (stay) {  // a key tile is one column tile, and so one warpgroup's
+        if (c.n > 0 && x0 == 0 && t < qs.len) p.weights[(size_t)u * a.cap + t] += sum;
+      } else {
+        part[w * kWtM + row] = sum;
+        named_bar_sync(3, 256);
+        if (w == 0) st_cluster_f32(ranks + rank * kWtM + row, 0, part[row] + part[kWtM + row]);
+      }
     }
-    const float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-    if (w == 1) lse2[kWtN + row] = sum;
-    named_bar_sync(3, 256);
-    if (w == 0 && t < qs.len) weights[(size_t)u * a.cap + t] += sum + lse2[kWtN + row];
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 0) tc_free<256>(tmem);
+  if (!stay) {
+    cluster_sync();
+    const int t = kt0 * kWtM + (int)threadIdx.x;
+    if (rank == 0 && threadIdx.x < kWtM && t < qs.len) {
+      float sum = 0.f;
+#pragma unroll
+      for (int r = 0; r < kCluster; ++r) sum += ranks[r * kWtM + threadIdx.x];
+      p.weights[(size_t)u * a.cap + t] += sum;
+    }
+  }
+}
+
+// Columns of a head when the queries of all heads of a group fit one tile (0: they do not).
+int stay_rows(int G, int Tq) {
+  for (int r = 16; r <= 128; r *= 2)
+    if (Tq <= r) return G * r <= kWtN ? r : 0;
+  return 0;
 }
 
 template <typename T, int D>
-cudaError_t launch_td(const PagedArgs& a, const CUtensorMap& kmap, const CUtensorMap& qmap, const PagedQuery& q,
-                      const float* lse, float* weights, cudaStream_t s) {
+cudaError_t launch_td(const WtArgs& p, const CUtensorMap& kmap, const CUtensorMap& qmap, cudaStream_t s) {
+  const void* kernel = reinterpret_cast<const void*>(paged_weights_kernel<T, D>);
   constexpr uint32_t smem = WtSmem<D>::kBytes;
-  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(paged_weights_kernel<T, D>), smem);
+  cudaError_t e = ensure_smem_limit(kernel, smem);
   if (e != cudaSuccess) return e;
-  const dim3 grid(a.B * a.Hkv, (a.cap + kWtM - 1) / kWtM);
-  paged_weights_kernel<T, D><<<grid, kWtThreads, smem, s>>>(a, q, lse, weights, paged_weights_rows(q.Tq), kmap, qmap);
-  return cudaGetLastError();
+  const int units = p.a.B * p.a.Hkv, tiles = (p.a.cap + kWtM - 1) / kWtM;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = p.stay ? dim3(units, (tiles + kRun - 1) / kRun) : dim3(units * kCluster, tiles);
+  cfg.blockDim = dim3(kWtThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.stay ? 0 : 1;
+  return cudaLaunchKernelEx(&cfg, paged_weights_kernel<T, D>, p, kmap, qmap);
 }
 
 }  // namespace
 
-int paged_weights_rows(int Tq) { return Tq <= 32 ? 32 : Tq <= 64 ? 64 : 128; }
+int paged_weights_rows(int G, int Tq) {
+  const int r = stay_rows(G, Tq);
+  return r ? r : Tq <= 32 ? 32 : Tq <= 64 ? 64 : kWtN;
+}
 
 cudaError_t launch_paged_weights(const PagedArgs& a, int d, int dtype, const CUtensorMap& kmap, const CUtensorMap& qmap,
                                  const PagedQuery& q, const float* lse, float* weights, cudaStream_t s) {
+  WtArgs p;
+  p.a = a;
+  p.q = q;
+  p.lse = lse;
+  p.weights = weights;
+  p.stay = stay_rows(a.G, q.Tq) > 0;
+  p.rows = paged_weights_rows(a.G, q.Tq);
   if (dtype == DKV_BF16)
-    return d == 128 ? launch_td<__nv_bfloat16, 128>(a, kmap, qmap, q, lse, weights, s)
-                    : launch_td<__nv_bfloat16, 64>(a, kmap, qmap, q, lse, weights, s);
-  return d == 128 ? launch_td<__half, 128>(a, kmap, qmap, q, lse, weights, s)
-                  : launch_td<__half, 64>(a, kmap, qmap, q, lse, weights, s);
+    return d == 128 ? launch_td<__nv_bfloat16, 128>(p, kmap, qmap, s) : launch_td<__nv_bfloat16, 64>(p, kmap, qmap, s);
+  return d == 128 ? launch_td<__half, 128>(p, kmap, qmap, s) : launch_td<__half, 64>(p, kmap, qmap, s);
 }
 
 }  // namespace dkv
