@@ -43,6 +43,64 @@ __device__ inline int paged_page(const PagedArgs& a, int b, int t) {
 }
 
 // ---------------------------------------------------------------------------
+// Dealing tiles to CTAs: the tiles of all (sequence, KV head) units in a row, sequence by sequence
+// and head by head, are cut into equal runs, one for each CTA.
+// ---------------------------------------------------------------------------
+// prefix[b] = tiles (of one head) of the sequences before b; every thread of the CTA calls it
+template <typename F>
+__device__ inline void deal_prefix(int B, int* prefix, F tiles_of) {
+  __shared__ int wsum[32];
+  __shared__ int carry;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+  if (tid == 0) { carry = 0; prefix[0] = 0; }
+  __syncthreads();
+  for (int b0 = 0; b0 < B; b0 += blockDim.x) {
+    const int b = b0 + tid;
+    int v = b < B ? tiles_of(b) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    if (lane == 31) wsum[warp] = v;
+    __syncthreads();
+    int add = carry, all = carry;
+    for (int w = 0; w < nw; ++w) {
+      if (w < warp) add += wsum[w];
+      all += wsum[w];
+    }
+    if (b < B) prefix[b + 1] = v + add;
+    __syncthreads();
+    if (tid == 0) carry = all;
+    __syncthreads();
+  }
+}
+// The run of CTA c of n: tiles [deal_bound(c), deal_bound(c + 1)) of total.
+__device__ inline int deal_bound(int total, int n, int c) { return (int)((int64_t)total * c / n); }
+// The CTA whose run holds tile x.
+__device__ inline int deal_owner(int total, int n, int x) { return (int)((((int64_t)x + 1) * n - 1) / total); }
+// The unit of tile x, and its tiles up to x1.
+struct DealSeg {
+  int b, h, j0, j1, n;  // tiles [j0, j1) of the unit's n
+};
+__device__ inline DealSeg deal_seg(const int* prefix, int B, int Hkv, int x, int x1) {
+  int lo = 0, hi = B - 1;  // the first b whose tiles end behind x
+  while (lo < hi) {
+    const int m = (lo + hi) >> 1;
+    if (prefix[m + 1] * Hkv > x) hi = m;
+    else lo = m + 1;
+  }
+  DealSeg s;
+  s.b = lo;
+  s.n = prefix[lo + 1] - prefix[lo];
+  const int rem = x - prefix[lo] * Hkv;
+  s.h = rem / s.n;
+  s.j0 = rem - s.h * s.n;
+  s.j1 = min(s.n, s.j0 + x1 - x);
+  return s;
+}
+
+// ---------------------------------------------------------------------------
 // Tiles in shared memory: per 64 channels a sub-tile of `rows` rows x 128 bytes,
 // written by TMA boxes under the 128-byte swizzle (16-byte chunk index XOR row % 8;
 // sub-tiles start on 1024-byte boundaries), so that eight rows of one chunk lie in

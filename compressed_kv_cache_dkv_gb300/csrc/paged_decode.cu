@@ -49,61 +49,6 @@ __device__ inline Span dec_span(const PagedArgs& a, int b) {
   return s;
 }
 
-// prefix[b] = tiles (of one head) of the sequences before b; every thread of the CTA calls it
-__device__ inline void dec_prefix(const PagedArgs& a, int* prefix) {
-  __shared__ int wsum[32];
-  __shared__ int carry;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
-  if (tid == 0) { carry = 0; prefix[0] = 0; }
-  __syncthreads();
-  for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
-    const int b = b0 + tid;
-    int v = b < a.B ? dec_span(a, b).n : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += y;
-    }
-    if (lane == 31) wsum[warp] = v;
-    __syncthreads();
-    int add = carry, all = carry;
-    for (int w = 0; w < nw; ++w) {
-      if (w < warp) add += wsum[w];
-      all += wsum[w];
-    }
-    if (b < a.B) prefix[b + 1] = v + add;
-    __syncthreads();
-    if (tid == 0) carry = all;
-    __syncthreads();
-  }
-}
-
-// The run of tiles of CTA c: [x0, x1) of total, dealt to n CTAs.
-__device__ inline int dec_bound(int total, int n, int c) { return (int)((int64_t)total * c / n); }
-// The CTA whose run holds tile x.
-__device__ inline int dec_owner(int total, int n, int x) { return (int)((((int64_t)x + 1) * n - 1) / total); }
-
-// The unit of tile x.
-struct Seg {
-  int b, h, j0, j1, n;  // tiles [j0, j1) of the unit's n
-};
-__device__ inline Seg dec_seg(const int* prefix, int B, int Hkv, int x, int x1) {
-  int lo = 0, hi = B - 1;  // the first b whose tiles end behind x
-  while (lo < hi) {
-    const int m = (lo + hi) >> 1;
-    if (prefix[m + 1] * Hkv > x) hi = m;
-    else lo = m + 1;
-  }
-  Seg s;
-  s.b = lo;
-  s.n = prefix[lo + 1] - prefix[lo];
-  const int rem = x - prefix[lo] * Hkv;
-  s.h = rem / s.n;
-  s.j0 = rem - s.h * s.n;
-  s.j1 = min(s.n, s.j0 + x1 - x);
-  return s;
-}
-
 struct DecArgs {
   PagedArgs a;
   const void* q;
@@ -138,7 +83,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
     fence_mbar_init();
   }
-  dec_prefix(a, prefix);
+  deal_prefix(a.B, prefix, [&](int b) { return dec_span(a, b).n; });
   __syncthreads();
   griddep_launch();
   // sequences without a token: zeros and -inf
@@ -151,7 +96,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
   const int total = prefix[a.B] * a.Hkv, nc = min((int)gridDim.x, total), c = blockIdx.x;
   if (c >= nc) return;
-  const int x0 = dec_bound(total, nc, c), x1 = dec_bound(total, nc, c + 1);
+  const int x0 = deal_bound(total, nc, c), x1 = deal_bound(total, nc, c + 1);
 
   if (warp == kDecConsumers) {
     // =========================== producer
@@ -160,7 +105,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     bool ok = true;
     int it = 0;
     for (int x = x0; x < x1 && ok;) {
-      const Seg g = dec_seg(prefix, a.B, a.Hkv, x, x1);
+      const DealSeg g = deal_seg(prefix, a.B, a.Hkv, x, x1);
       const Span s = dec_span(a, g.b);
       for (int j = g.j0; j < g.j1; ++j, ++it) {
         const int st = it % kDecStages, y = s.token(j) & a.page_mask, first = s.token(j) + lane * rows;
@@ -194,7 +139,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   bool ok = true;
   int it = 0;
   for (int x = x0; x < x1;) {
-    const Seg g = dec_seg(prefix, a.B, a.Hkv, x, x1);
+    const DealSeg g = deal_seg(prefix, a.B, a.Hkv, x, x1);
     const Span s = dec_span(a, g.b);
     const int u = g.b * a.Hkv + g.h;
     // q as B fragments (k = channels, n = heads of the group; heads past the group read zeros)
@@ -348,16 +293,16 @@ __global__ void __launch_bounds__(kCombThreads) paged_combine_kernel(DecArgs p, 
   int* prefix = reinterpret_cast<int*>(csm);
   float* fac = csm + a.B + 1;  // [record][8]
   float* red = fac + 8 * ncta;  // M, L [8] each
-  dec_prefix(a, prefix);
+  deal_prefix(a.B, prefix, [&](int b) { return dec_span(a, b).n; });
   __syncthreads();
   griddep_wait();
   const int total = prefix[a.B] * a.Hkv, nc = min(ncta, total), c = blockIdx.x;
   if (c >= nc) return;
-  const int x0 = dec_bound(total, nc, c), x1 = dec_bound(total, nc, c + 1);
-  const Seg g = dec_seg(prefix, a.B, a.Hkv, x1 - 1, x1);  // the last tile's unit
+  const int x0 = deal_bound(total, nc, c), x1 = deal_bound(total, nc, c + 1);
+  const DealSeg g = deal_seg(prefix, a.B, a.Hkv, x1 - 1, x1);  // the last tile's unit
   const int begin = x1 - 1 - g.j0;                        // its first tile
   if (begin < x0 || g.j0 + 1 == g.n) return;
-  const int nrec = dec_owner(total, nc, begin + g.n - 1) - c + 1;
+  const int nrec = deal_owner(total, nc, begin + g.n - 1) - c + 1;
   auto rec = [&](int i) { return p.records + (size_t)(2 * (c + i) + (i == 0 ? 1 : 0)) * rec_floats<D>(); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp < 8) {

@@ -64,21 +64,6 @@ struct PfKernelArgs {
   int by_heads;  // the groups are two heads (else two 128-token tiles of one head)
 };
 
-// The keys that the queries at positions [p_lo, p_hi] see between them, in tiles.
-struct KeySpan {
-  int lo, hi, st, wt0, n;  // window start, end, sink tiles, first window tile, tiles
-  __device__ int key(int j) const { return (j < st ? j : wt0 + j - st) * kPfN; }
-};
-__device__ inline KeySpan key_span(const PagedArgs& a, int p_lo, int p_hi) {
-  KeySpan s;
-  s.hi = max(0, p_hi + 1);
-  s.lo = min(paged_window_lo(a, max(p_lo, 0)), s.hi);
-  s.wt0 = s.lo / kPfN;
-  s.st = min((min(a.sinks, s.hi) + kPfN - 1) / kPfN, s.wt0);
-  s.n = s.st + (s.hi + kPfN - 1) / kPfN - s.wt0;
-  return s;
-}
-
 // every query at positions [p_lo, p_hi] sees every key of [k0, k0 + kPfN)
 __device__ inline bool all_seen(const PagedArgs& a, int k0, int p_lo, int p_hi) {
   return k0 + kPfN - 1 <= p_lo && (a.window == 0 || k0 > p_hi - a.window || k0 + kPfN <= a.sinks);
@@ -100,7 +85,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   const int h0 = p.by_heads ? 2 * (int)blockIdx.x : (int)blockIdx.x, kvh = h0 / a.G;
   const int rowsA = min(kPfM, qs.n - row0), rowsB = p.by_heads ? rowsA : min(kPfM, max(0, qs.n - row0 - kPfM));
   const int p_lo = qs.off + row0, p_hi = p_lo + (p.by_heads ? rowsA : rowsA + rowsB) - 1;
-  const KeySpan ks = key_span(a, p_lo, p_hi);
+  const KeySpan<kPfN> ks = key_span<kPfN>(a, p_lo, p_hi);
   // group A's keys may end a tile or two before B's
   const int nA = min(ks.n, max(0, ks.st + (max(0, p_lo + rowsA) + kPfN - 1) / kPfN - ks.wt0)), nB = rowsB > 0 ? ks.n : 0;
   const int nt = max(nA, nB);

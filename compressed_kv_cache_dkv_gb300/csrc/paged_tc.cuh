@@ -65,6 +65,13 @@ __device__ inline void tc_ld32(uint32_t ta, uint32_t* r) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(ta));
 }
+__device__ inline void tc_ld16(uint32_t ta, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(ta));
+}
 __device__ inline void tc_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ inline void tc_st16(uint32_t ta, const uint32_t* r) {
   asm volatile(
@@ -119,6 +126,23 @@ __device__ inline QuerySpan query_span(const PagedArgs& a, const int32_t* q_lens
     }
   }
   s.off = s.len - s.n;
+  return s;
+}
+
+// The keys that the queries at positions [p_lo, p_hi] see between them, in tiles of N.
+template <int N>
+struct KeySpan {
+  int lo, hi, st, wt0, n;  // window start, end, sink tiles, first window tile, tiles
+  __device__ int key(int j) const { return (j < st ? j : wt0 + j - st) * N; }
+};
+template <int N>
+__device__ inline KeySpan<N> key_span(const PagedArgs& a, int p_lo, int p_hi) {
+  KeySpan<N> s;
+  s.hi = max(0, p_hi + 1);
+  s.lo = min(paged_window_lo(a, max(p_lo, 0)), s.hi);
+  s.wt0 = s.lo / N;
+  s.st = min((min(a.sinks, s.hi) + N - 1) / N, s.wt0);
+  s.n = s.st + (s.hi + N - 1) / N - s.wt0;
   return s;
 }
 
