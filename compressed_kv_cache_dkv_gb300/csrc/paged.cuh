@@ -145,6 +145,12 @@ struct Num<__half> {
   static __device__ inline __half from_float(float x) { return __float2half_rn(x); }
   static __device__ inline uint32_t pack(float lo, float hi) { return pack_half2(lo, hi); }
   static __device__ inline void split(float x, float y, uint32_t& hi, uint32_t& lo) { split_half2(x, y, hi, lo); }
+  // 0 x + z, two values
+  static __device__ inline uint32_t zero_times(uint32_t x, uint32_t z) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(z));
+    return r;
+  }
   static __device__ inline void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
     mma16816(c, a0, a1, a2, a3, b0, b1);
@@ -158,6 +164,11 @@ struct Num<__nv_bfloat16> {
   static __device__ inline uint32_t pack(float lo, float hi) {
     __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&h);
+  }
+  static __device__ inline uint32_t zero_times(uint32_t x, uint32_t z) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(z));
+    return r;
   }
   // hi + lo carries 16 bits of each value
   static __device__ inline void split(float x, float y, uint32_t& hi, uint32_t& lo) {

@@ -22,7 +22,7 @@ namespace {
 constexpr int kSelThreads = 1024, kSelBins = 2048;
 constexpr int kSelPer = 8;                        // consecutive tokens of a thread in the ordered pass
 constexpr int kSelStage = 24 * 1024;              // images held in shared memory (two CTAs fit a multiprocessor)
-constexpr int kMoveThreads = 256, kMoveVec = 4;   // 16-byte pieces of K, and as many of V, per thread
+constexpr int kMoveThreads = 256, kMoveVec = 2;   // 16-byte pieces of K, and as many of V, per thread
 constexpr int kMoveBytes = kMoveThreads * kMoveVec * 16;
 constexpr int kZeroChunk = 8192;                  // weights zeroed by one CTA
 constexpr int kPollLimit = 1 << 22;               // polls of a flag before a wait gives up
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(PagedArgs a, 
 }
 
 template <int D>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(PagedArgs a, PagedEvict e, EvictPlan plan,
+__global__ void __launch_bounds__(kMoveThreads, 8) evict_move_kernel(PagedArgs a, PagedEvict e, EvictPlan plan,
                                                                  uint4* __restrict__ kp, uint4* __restrict__ vp,
                                                                  uint8_t* __restrict__ ws) {
   constexpr int R = D / 8, kRows = kMoveThreads / R;  // pieces of a row, rows of one access

@@ -6,8 +6,8 @@
 // 64-key tile j and group g
 //   S_g = Q_g K_j^T   M = 128 queries, N = 64 keys   (64 TMEM columns, two buffers a group)
 //   O_g += P_g V_j    M = 128, N = d, P from TMEM (16-bit, over the first 32 columns of its S)
-// One row per softmax thread (warps 0-3 group A, 4-7 group B).  Warp 8 streams the tiles with TMA
-// boxes, one per page and 64 channels, into six slots for K and four for V; warps 9 and 10 issue
+// One row per softmax thread (warps 0-3 group A, 4-7 group B).  Warps 8 and 11 stream K and V
+// with TMA boxes, one per page and 64 channels, into five slots each; warps 9 and 10 issue
 // the products of groups A and B: S of tile j + 1 goes out while the rows still turn S_j into P,
 // so that neither the rows nor the tensor cores wait for the other's latency.  (With 128-key
 // tiles, which read Q half as often from shared memory, there is room for one S only, and the
@@ -44,12 +44,12 @@ constexpr float kPfShift<__half> = 7.f;
 
 template <int D>
 struct PfSmem {
-  static constexpr int kK = 6, kV = 4;                  // slots
+  static constexpr int kR = 5;                          // slots for K, and for V
   static constexpr uint32_t kQ = kPfM * D * 2;          // one group's Q
   static constexpr uint32_t kTile = kPfN * D * 2;       // one K or V tile
   static constexpr uint32_t kOffK = 2 * kQ;
-  static constexpr uint32_t kOffV = kOffK + kK * kTile;
-  static constexpr uint32_t kOffBar = kOffV + kV * kTile;
+  static constexpr uint32_t kOffV = kOffK + kR * kTile;
+  static constexpr uint32_t kOffBar = kOffV + kR * kTile;
   static constexpr uint32_t kBytes = kOffBar + 512;
 };
 
@@ -67,6 +67,29 @@ struct PfKernelArgs {
 // every query at positions [p_lo, p_hi] sees every key of [k0, k0 + kPfN)
 __device__ inline bool all_seen(const PagedArgs& a, int k0, int p_lo, int p_hi) {
   return k0 + kPfN - 1 <= p_lo && (a.window == 0 || k0 > p_hi - a.window || k0 + kPfN <= a.sinks);
+}
+
+// V rows that are not finite, and that this row sees: p v in fp32, for channels c0 .. c0 + 31 (rare, so in
+// plain loops)
+template <typename T, int D>
+__device__ __noinline__ void add_bad_rows(const PfKernelArgs& p, const PagedArgs& a, int b, int head, int kvh, int qrow, int pos,
+                                          int bads, const int* bad_key, const uint32_t* bad_bits, int c0, float m, float il,
+                                          float* f) {
+  const T* qr = static_cast<const T*>(p.q.q) + (int64_t)b * p.q.qs.batch + (int64_t)head * p.q.qs.head + (int64_t)qrow * p.q.qs.token;
+  for (int x = 0; x < bads * kPfN; ++x) {
+    const int t = bad_key[x / kPfN] + x % kPfN;
+    if (!((bad_bits[x / 32] >> (x % 32)) & 1u)) continue;
+    if (t > pos || (a.window && t <= pos - a.window && t >= a.sinks)) continue;
+    const int page = paged_page(a, b, t);
+    if (page >= a.n_pages) continue;
+    const int64_t at = page * a.stride_page + kvh * a.stride_head + (t & a.page_mask) * a.stride_token;
+    const T* kr = static_cast<const T*>(p.k_pool) + at;
+    const T* vr = static_cast<const T*>(p.v_pool) + at + c0;
+    float dot = 0.f;
+    for (int e = 0; e < D; ++e) dot = fmaf(Num<T>::to_float(qr[e]), Num<T>::to_float(kr[e]), dot);
+    const float w = fast_exp2(fmaf(dot, a.scale_log2, kPfShift<T> - m)) * il;
+    for (int e = 0; e < 32; ++e) f[e] += w * Num<T>::to_float(vr[e]);
+  }
 }
 
 template <typename T, int D>
@@ -92,9 +115,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 
   const uint32_t sb = smem_u32(smem);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + S::kOffBar);  // [slot]
-  uint64_t* v_full = k_full + S::kK;   // [slot]
-  uint64_t* empty = v_full + S::kV;    // [V slot] O_j, and so S_{j+1}, of both groups are done
-  uint64_t* landed = empty + S::kV;    // [edge tile] its V landed, for warp 11 (used once)
+  uint64_t* v_full = k_full + S::kR;   // [slot]
+  uint64_t* empty = v_full + S::kR;    // [slot] O_j, and so S_j, of both groups are done
+  uint64_t* landed = empty + S::kR;    // [edge tile] its V landed, for warp 11 (used once)
   uint64_t* q_full = landed + kPfEdges;
   uint64_t* s_full = q_full + 1;       // [group][buffer]
   uint64_t* p_full = s_full + 4;       // [group][buffer]
@@ -108,8 +131,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     tma_prefetch_map(&qmap);
     tma_prefetch_map(&kmap);
     tma_prefetch_map(&vmap);
-    for (int i = 0; i < S::kK; ++i) mbar_init(&k_full[i], 1);
-    for (int i = 0; i < S::kV; ++i) {
+    for (int i = 0; i < S::kR; ++i) {
+      mbar_init(&k_full[i], 1);
       mbar_init(&v_full[i], 1);
       mbar_init(&empty[i], 2);  // one commit per group
     }
@@ -130,9 +153,33 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   const uint32_t tmem = *tmem_slot;
   bool ok = true;
 
+  // K or V tiles; whole warp
+  const int rows = min(a.page_mask + 1, kPfN), runs = kPfN / rows;
+  auto page_of = [&](int j) {  // lane i < runs: the page of the tile's i-th run of `rows` keys
+    const int first = ks.key(j) + lane * rows;
+    // runs without a visible key: zeros, wherever the table points
+    return j < nt && lane < runs && first < ks.hi && (first + rows > ks.lo || first < a.sinks) ? paged_page(a, b, first) : a.n_pages;
+  };
+  auto load = [&](const CUtensorMap* map, uint32_t to, int j, int page, uint64_t* bar, uint32_t el) {
+    if (el) mbar_arrive_expect_tx(bar, S::kTile);
+    const int y = ks.key(j) & a.page_mask;
+#pragma unroll 2
+    for (int i = 0; i < runs; ++i) {
+      const int pg = __shfl_sync(0xffffffffu, page, i);
+#pragma unroll
+      for (int hf = 0; hf < D / 64; ++hf)
+        tma_load_4d(sb + to + hf * kPfN * 128 + i * rows * 128, map, hf * 64, y, kvh, pg, bar, el);
+    }
+  };
+  auto slot_free = [&](int j) {  // the slots of tile j - kR
+    if (j >= S::kR) ok = mbar_wait(&empty[j % S::kR], (uint32_t)((j / S::kR - 1) & 1), a.err);
+    return ok = __all_sync(0xffffffffu, ok);
+  };
+
   if (warp == 8) {
-    // =========================== loads: Q, K_0, then V_j and K_{j+1}
+    // =========================== Q and K
     const uint32_t el = elect_one();
+    int j = 0;
     if (nt > 0) {
       if (el) mbar_arrive_expect_tx(q_full, (rowsB > 0 ? 2 : 1) * S::kQ);
       for (int g = 0; g < (rowsB > 0 ? 2 : 1); ++g)
@@ -140,42 +187,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           tma_load_4d(sb + g * S::kQ + hf * kPfM * 128, &qmap, hf * 64, p.by_heads ? row0 : row0 + g * kPfM,
                       p.by_heads ? h0 + g : h0, b, q_full, el);
     }
-    const int rows = min(a.page_mask + 1, kPfN), per = kPfN / rows;
-    auto page_of = [&](int j) {  // lane i < per: the page of the tile's i-th run of `rows` keys
-      const int first = ks.key(j) + lane * rows;
-      // runs without a visible key: zeros, wherever the table points
-      return j < nt && lane < per && first < ks.hi && (first + rows > ks.lo || first < a.sinks) ? paged_page(a, b, first)
-                                                                                              : a.n_pages;
-    };
-    auto load = [&](const CUtensorMap* map, uint32_t at, int j, int page, uint64_t* bar) {
-      if (el) mbar_arrive_expect_tx(bar, S::kTile);
-      const int y = ks.key(j) & a.page_mask;
-      for (int i = 0; i < per; ++i) {
-        const int pg = __shfl_sync(0xffffffffu, page, i);
-#pragma unroll
-        for (int hf = 0; hf < D / 64; ++hf)
-          tma_load_4d(sb + at + hf * kPfN * 128 + i * rows * 128, map, hf * 64, y, kvh, pg, bar, el);
-      }
-    };
-    int page = page_of(0), next = page_of(1), edges = 0, j = 0;
-    if (nt > 0) load(&kmap, S::kOffK, 0, page, &k_full[0]);
-    for (; j < nt && ok; ++j) {
-      const int after = page_of(j + 2);  // looked up a tile ahead of its use
-      // V_{j-4} is read, and K_{j-5} was before it
-      if (j >= S::kV) ok = mbar_wait(&empty[j % S::kV], (uint32_t)((j / S::kV - 1) & 1), a.err);
-      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-      // V of an edge tile lands for warp 11, whose arrival then fills the slot
-      const bool edge = !all_seen(a, ks.key(j), p_lo, p_hi);
-      load(&vmap, S::kOffV + (j % S::kV) * S::kTile, j, page, edge ? &landed[edges++] : &v_full[j % S::kV]);
-      if (j + 1 < nt) load(&kmap, S::kOffK + ((j + 1) % S::kK) * S::kTile, j + 1, next, &k_full[(j + 1) % S::kK]);
+    for (int page = page_of(0); j < nt; ++j) {
+      const int next = page_of(j + 1);  // looked up a tile ahead of its use
+      if (!slot_free(j)) break;
+      load(&kmap, S::kOffK + (j % S::kR) * S::kTile, j, page, &k_full[j % S::kR], el);
       page = next;
-      next = after;
     }
     // every copy has landed before the CTA may end (also after a wait that gave up)
     if (nt > 0) mbar_wait(q_full, 0, a.err);
-    for (int x = max(0, j - S::kV); x < j; ++x) mbar_wait(&v_full[x % S::kV], (uint32_t)((x / S::kV) & 1), a.err);
-    for (int x = max(0, min(j, nt - 1) + 1 - S::kK); x <= min(j, nt - 1); ++x)
-      mbar_wait(&k_full[x % S::kK], (uint32_t)((x / S::kK) & 1), a.err);
+    for (int x = max(0, j - S::kR); x < j; ++x) mbar_wait(&k_full[x % S::kR], (uint32_t)((x / S::kR) & 1), a.err);
   } else if (warp == 9 || warp == 10) {
     // =========================== products of group g
     // The whole warp walks through here and one elected lane issues: in code that one lane runs
@@ -187,8 +207,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const uint64_t qd = tc_desc(sb + g * S::kQ, 16, 1024);
     auto wait = [&](uint64_t* bar, int parity) { ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, (uint32_t)parity, a.err)); };
     auto scores = [&](int j) {
-      const int sl = j % S::kK, buf = j & 1;
-      wait(&k_full[sl], (j / S::kK) & 1);
+      const int sl = j % S::kR, buf = j & 1;
+      wait(&k_full[sl], (j / S::kR) & 1);
       if (j >= 2) wait(&o_done[2 * g + buf], ((j - 2) >> 1) & 1);  // the buffer holds P_{j-2}
       if (!ok) return;
       tc_fence_after();
@@ -204,8 +224,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       scores(0);
       for (int j = 0; j < n && ok; ++j) {
         if (j + 1 < n) scores(j + 1);
-        const int sl = j % S::kV, buf = j & 1;
-        wait(&v_full[sl], (j / S::kV) & 1);
+        const int sl = j % S::kR, buf = j & 1;
+        wait(&v_full[sl], (j / S::kR) & 1);
         wait(&p_full[2 * g + buf], (j >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
@@ -221,27 +241,28 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       }
     }
   } else if (warp == 11) {
-    // =========================== V rows of edge tiles
-    int edges = 0;
-    for (int j = 0; j < nt && ok; ++j) {
-      const int k0 = ks.key(j), sl = j % S::kV;
-      if (all_seen(a, k0, p_lo, p_hi)) continue;
-      ok = mbar_wait(&landed[edges++], 0, a.err);
+    // =========================== V, and the rows of its edge tiles
+    const uint32_t el = elect_one();
+    auto clean = [&](int j, int edge) {
+      const int k0 = ks.key(j), sl = j % S::kR;
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(&landed[edge], 0, a.err));
       const uint32_t vb = sb + S::kOffV + sl * S::kTile;
       uint32_t bad = 0;  // rows lane, lane + 32 with a value that is not finite
       for (int x = 0; x < kPfN / 32; ++x) {
         const int r = 32 * x + lane, t = k0 + r;
         const bool some = t < ks.hi && (t >= ks.lo || t < a.sinks);  // a row of the CTA sees it
         bool odd = false;
-        if (some) {
-          constexpr uint32_t kExp = Num<T>::kUmma ? 0x7f80u : 0x7c00u;
-#pragma unroll 4
+        if (some) {  // 0 x is NaN for every x that is not finite, and stays one in the sum
+          uint32_t z[2] = {0u, 0u};
+#pragma unroll
           for (int ch = 0; ch < D / 8; ++ch) {
             const uint4 v = lds128(vb + sw128(kPfN, r, ch));
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int y = 0; y < 4; ++y) odd |= (w[y] & kExp) == kExp || ((w[y] >> 16) & kExp) == kExp;
+            z[0] = Num<T>::zero_times(v.x, z[0]);
+            z[1] = Num<T>::zero_times(v.y, z[1]);
+            z[0] = Num<T>::zero_times(v.z, z[0]);
+            z[1] = Num<T>::zero_times(v.w, z[1]);
           }
+          odd = ((z[0] | z[1]) & 0x7fff7fffu) != 0u;
         }
         if (!some || odd)
           for (int ch = 0; ch < D / 8; ++ch) sts128(vb + sw128(kPfN, r, ch), make_uint4(0, 0, 0, 0));
@@ -259,7 +280,30 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&v_full[sl]);
+    };
+    // V of an edge tile lands on a barrier of its own, and fills its slot once it has been looked over.
+    // That is done up to two tiles later, so that the loads behind it go out meanwhile (the slot of tile
+    // j is waited for only by tile j + kR).
+    int edges = 0, j = 0, todo[2] = {-1, -1}, first = 0, cleaned = 0;  // edge tiles loaded and not yet clean
+    auto clean_next = [&]() {
+      clean(todo[first], cleaned++);
+      todo[first] = -1;
+      first ^= 1;
+    };
+    for (int page = page_of(0); j < nt; ++j) {
+      const int next = page_of(j + 1);
+      if (!slot_free(j)) break;
+      const bool edge = !all_seen(a, ks.key(j), p_lo, p_hi);
+      load(&vmap, S::kOffV + (j % S::kR) * S::kTile, j, page, edge ? &landed[edges] : &v_full[j % S::kR], el);
+      page = next;
+      if (todo[first] >= 0 && (todo[first] <= j - 2 || todo[first ^ 1] >= 0)) clean_next();
+      if (edge) {
+        todo[todo[first] < 0 ? first : first ^ 1] = j;
+        ++edges;
+      }
     }
+    while (todo[first] >= 0) clean_next();
+    for (int x = max(0, j - S::kR); x < j; ++x) mbar_wait(&v_full[x % S::kR], (uint32_t)((x / S::kR) & 1), a.err);
   } else if (warp < 8) {
     // =========================== softmax: one query row per thread
     const int g = warp >> 2, rw = warp & 3, row = 32 * rw + lane;
@@ -282,10 +326,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       tc_ld_wait();
       const int k0 = ks.key(j);
       if (!all_seen(a, k0, g_lo, g_hi)) {
+        // bit c: this row sees key k0 + c
         const int hi = pos - k0, lo = a.window ? pos - a.window + 1 - k0 : 0, sk = a.sinks - k0;
+        auto below = [](int n) { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1; };
+        const unsigned long long sees = below(hi + 1) & (~below(lo) | below(sk));
+        if (__any_sync(0xffffffffu, sees != ~0ull)) {
+          const uint32_t half[2] = {(uint32_t)sees, (uint32_t)(sees >> 32)};
 #pragma unroll
-        for (int c = 0; c < kPfN; ++c)
-          if (c > hi || (c < lo && c >= sk)) s[c] = 0xff800000u;
+          for (int c = 0; c < kPfN; ++c) s[c] = half[c >> 5] >> (c & 31) & 1u ? s[c] : 0xff800000u;
+        }
       }
       float mx[8];
 #pragma unroll
@@ -330,9 +379,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     tc_fence_after();
     const bool live = row < rows;
     const float il = n == 0 || l == 0.f ? 0.f : 1.f / l;  // a row that sees no key: zeros
-    T* orow = static_cast<T*>(p.out) + (int64_t)b * p.os.batch + (int64_t)head * p.os.head + (int64_t)(live ? qrow : 0) * p.os.token;
     // (every edge tile's product, and so warp 11's work on it, is behind o_done)
     const int bads = n > 0 ? *reinterpret_cast<volatile int*>(n_bad) : 0;
+    // The rows go through the group's Q, which no product reads any more, so that a warp then writes
+    // whole rows of the output.
+    const uint32_t stage = sb + g * S::kQ;
+#pragma unroll
     for (int c = 0; c < D / 32; ++c) {
       uint32_t o[32];
       if (n > 0) {
@@ -342,31 +394,21 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       float f[32];
 #pragma unroll
       for (int e = 0; e < 32; ++e) f[e] = n > 0 && l != 0.f ? __uint_as_float(o[e]) * il : 0.f;
-      if (bads && live) {
-        // V rows that are not finite, and that this row sees: p v in fp32 (rare, so in plain loops)
-        const T* qr = static_cast<const T*>(p.q.q) + (int64_t)b * p.q.qs.batch + (int64_t)head * p.q.qs.head + (int64_t)qrow * p.q.qs.token;
-        for (int x = 0; x < bads * kPfN; ++x) {
-          const int t = bad_key[x / kPfN] + x % kPfN;
-          if (!((bad_bits[x / 32] >> (x % 32)) & 1u)) continue;
-          if (t > pos || (a.window && t <= pos - a.window && t >= a.sinks)) continue;
-          const int page = paged_page(a, b, t);
-          if (page >= a.n_pages) continue;
-          const int64_t at = page * a.stride_page + kvh * a.stride_head + (t & a.page_mask) * a.stride_token;
-          const T* kr = static_cast<const T*>(p.k_pool) + at;
-          const T* vr = static_cast<const T*>(p.v_pool) + at + 32 * c;
-          float dot = 0.f;
-          for (int e = 0; e < D; ++e) dot = fmaf(Num<T>::to_float(qr[e]), Num<T>::to_float(kr[e]), dot);
-          const float w = fast_exp2(fmaf(dot, slog2, kPfShift<T> - m)) * il;
+      if (bads && live) add_bad_rows<T, D>(p, a, b, head, kvh, qrow, pos, bads, bad_key, bad_bits, 32 * c, m, il, f);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) f[e] += w * Num<T>::to_float(vr[e]);
-        }
-      }
-      if (live)
-#pragma unroll
-        for (int e = 0; e < 32; e += 8)
-          *reinterpret_cast<uint4*>(orow + 32 * c + e) =
-              make_uint4(Num<T>::pack(f[e], f[e + 1]), Num<T>::pack(f[e + 2], f[e + 3]), Num<T>::pack(f[e + 4], f[e + 5]),
-                         Num<T>::pack(f[e + 6], f[e + 7]));
+      for (int e = 0; e < 32; e += 8)
+        sts128(stage + sw128(kPfM, row, (32 * c + e) / 8),
+               make_uint4(Num<T>::pack(f[e], f[e + 1]), Num<T>::pack(f[e + 2], f[e + 3]), Num<T>::pack(f[e + 4], f[e + 5]),
+                          Num<T>::pack(f[e + 6], f[e + 7])));
+    }
+    __syncwarp();
+    {
+      T* out = static_cast<T*>(p.out) + (int64_t)b * p.os.batch + (int64_t)head * p.os.head;
+      const int q0 = qrow - lane, ch = lane % (D / 8);  // a row's piece; D / 8 lanes a row
+#pragma unroll 4
+      for (int r = lane / (D / 8); r < 32; r += 256 / D)
+        if (32 * rw + r < rows)
+          *reinterpret_cast<uint4*>(out + (int64_t)(q0 + r) * p.os.token + 8 * ch) = lds128(stage + sw128(kPfM, 32 * rw + r, ch));
     }
     if (live && p.lse)
       p.lse[((int64_t)b * a.Hq + head) * p.q.Tq + qrow] =
