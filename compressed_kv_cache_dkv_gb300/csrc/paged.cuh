@@ -230,15 +230,16 @@ struct PagedMaps {  // tensor maps of the pools: boxes of 64 channels x min(page
   CUtensorMap k, v;
 };
 
-// decode: workspace [header][records: two per CTA, fp32 m[8] l[8] o[d][8]][scores fp32 [units][cap][8]]
-size_t paged_decode_ws_bytes(const PagedArgs& a, int d, bool with_weights);
+// decode: workspace [header][records: two per CTA, fp32 m[8] l[8] o[d][8]]; scores fp32 [units][cap][8]
+size_t paged_decode_ws_bytes(int d);
 cudaError_t launch_paged_decode(const PagedArgs& a, int d, int dtype, const PagedMaps& m, const void* q,
-                                const dkv_strides& qs, void* out, float* lse, float* weights, uint8_t* ws,
+                                const dkv_strides& qs, void* out, float* lse, float* weights, float* scores, uint8_t* ws,
                                 cudaStream_t s);
 cudaError_t launch_paged_append(const PagedArgs& a, int d, const void* K, const void* V, const dkv_strides& ns,
                                 int n_new, const int32_t* pos, const int32_t* counts, void* k_pool, void* v_pool,
                                 cudaStream_t s);
-// prefill and weights: qmap boxes of 64 channels x 128 tokens of q (weights: x paged_weights_rows(G, Tq))
+// prefill and weights: qmap boxes of 64 channels x paged_prefill_rows(Tq) tokens of q (weights: x
+// paged_weights_rows(G, Tq))
 struct PagedQuery {
   const void* q;
   dkv_strides qs;
@@ -247,7 +248,9 @@ struct PagedQuery {
 };
 cudaError_t launch_paged_prefill(const PagedArgs& a, int d, int dtype, const PagedMaps& m, const CUtensorMap& qmap,
                                  const PagedQuery& q, const void* v_pool, const void* k_pool, void* out,
-                                 const dkv_strides& os, float* lse, cudaStream_t s);
+                                 const dkv_strides& os, float* lse, uint8_t* ws, cudaStream_t s);
+int paged_prefill_rows(int Tq);
+size_t paged_prefill_ws_bytes(int d);
 int paged_weights_rows(int G, int Tq);
 cudaError_t launch_paged_weights(const PagedArgs& a, int d, int dtype, const CUtensorMap& kmap, const CUtensorMap& qmap,
                                  const PagedQuery& q, const float* lse, float* weights, cudaStream_t s);

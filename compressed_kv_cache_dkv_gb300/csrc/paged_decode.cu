@@ -365,8 +365,6 @@ __global__ void __launch_bounds__(kScoreThreads) paged_score_kernel(DecArgs p, f
   }
 }
 
-size_t off_scores(int d) { return round_up(kWsHeader + (size_t)2 * sm_count() * (16 + 8 * d) * 4, 256); }
-
 template <typename T, int D>
 cudaError_t launch_decode_td(const DecArgs& p, const PagedMaps& m, float* weights, cudaStream_t s) {
   const int ncta = sm_count();
@@ -385,12 +383,10 @@ cudaError_t launch_decode_td(const DecArgs& p, const PagedMaps& m, float* weight
 
 }  // namespace
 
-size_t paged_decode_ws_bytes(const PagedArgs& a, int d, bool with_weights) {
-  return off_scores(d) + (with_weights ? (size_t)a.B * a.Hkv * a.cap * 32 : 0);
-}
+size_t paged_decode_ws_bytes(int d) { return kWsHeader + (size_t)2 * sm_count() * (16 + 8 * d) * 4; }
 
 cudaError_t launch_paged_decode(const PagedArgs& a, int d, int dtype, const PagedMaps& m, const void* q,
-                                const dkv_strides& qs, void* out, float* lse, float* weights, uint8_t* ws,
+                                const dkv_strides& qs, void* out, float* lse, float* weights, float* scores, uint8_t* ws,
                                 cudaStream_t s) {
   DecArgs p;
   p.a = a;
@@ -400,7 +396,7 @@ cudaError_t launch_paged_decode(const PagedArgs& a, int d, int dtype, const Page
   p.out = out;
   p.lse = lse;
   p.records = reinterpret_cast<float*>(ws + kWsHeader);
-  p.scores = weights ? reinterpret_cast<float*>(ws + off_scores(d)) : nullptr;
+  p.scores = weights ? scores : nullptr;
   if (dtype == DKV_BF16)
     return d == 128 ? launch_decode_td<__nv_bfloat16, 128>(p, m, weights, s) : launch_decode_td<__nv_bfloat16, 64>(p, m, weights, s);
   return d == 128 ? launch_decode_td<__half, 128>(p, m, weights, s) : launch_decode_td<__half, 64>(p, m, weights, s);

@@ -90,10 +90,15 @@ PagedArgs make_args(const dkv_paged* p, const int32_t* table, const int32_t* len
   return a;
 }
 
-size_t ws_need(const dkv_paged* p, bool with_weights) {
+// [what one call keeps in it, and behind the largest such part the scores of decode with weights]
+size_t ws_base(const dkv_paged* p) {
   const PagedArgs a = make_args(p, nullptr, nullptr, nullptr);
-  const size_t dec = paged_decode_ws_bytes(a, p->head_dim, with_weights), ev = paged_evict_ws_bytes(a, p->head_dim);
-  return dec > ev ? dec : ev;
+  const size_t dec = paged_decode_ws_bytes(p->head_dim), pre = paged_prefill_ws_bytes(p->head_dim);
+  const size_t ev = paged_evict_ws_bytes(a, p->head_dim), most = dec > pre ? dec : pre;
+  return round_up(most > ev ? most : ev, 256);
+}
+size_t ws_need(const dkv_paged* p, bool with_weights) {
+  return ws_base(p) + (with_weights ? (size_t)p->batch * p->n_kv_heads * p->max_pages * p->page_size * 32 : 0);
 }
 
 // what all calls check alike
@@ -166,8 +171,9 @@ int dkv_paged_decode(const dkv_paged* p, const void* q, const dkv_strides* qs, c
   const PagedArgs a = make_args(p, page_table, lens, workspace);
   PagedMaps m;
   if (!encode_pool(&m.k, p, k_pool) || !encode_pool(&m.v, p, v_pool)) return DKV_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   return done(launch_paged_decode(a, p->head_dim, p->dtype, m, q, *qs, out, lse, weights,
-                                  static_cast<uint8_t*>(workspace), static_cast<cudaStream_t>(stream)));
+                                  reinterpret_cast<float*>(ws + ws_base(p)), ws, static_cast<cudaStream_t>(stream)));
 }
 
 int dkv_paged_prefill(const dkv_paged* p, const void* q, const dkv_strides* qs, int32_t Tq, const void* k_pool,
@@ -188,11 +194,11 @@ int dkv_paged_prefill(const dkv_paged* p, const void* q, const dkv_strides* qs, 
   const PagedArgs a = make_args(p, page_table, lens, workspace);
   PagedMaps m;
   CUtensorMap qm;
-  if (!encode_pool(&m.k, p, k_pool) || !encode_pool(&m.v, p, v_pool) || !encode_query(&qm, p, q, *qs, Tq, 128))
+  if (!encode_pool(&m.k, p, k_pool) || !encode_pool(&m.v, p, v_pool) || !encode_query(&qm, p, q, *qs, Tq, paged_prefill_rows(Tq)))
     return DKV_ERR_CUDA;
   const PagedQuery pq = {q, *qs, Tq, q_lens};
   return done(launch_paged_prefill(a, p->head_dim, p->dtype, m, qm, pq, v_pool, k_pool, out, *os, lse,
-                                   static_cast<cudaStream_t>(stream)));
+                                   static_cast<uint8_t*>(workspace), static_cast<cudaStream_t>(stream)));
 }
 
 int dkv_paged_weights(const dkv_paged* p, const void* q, const dkv_strides* qs, int32_t Tq, const float* lse,

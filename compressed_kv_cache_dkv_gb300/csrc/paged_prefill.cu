@@ -2,8 +2,11 @@
 // with an optional sliding window and sinks, on the tcgen05 tensor cores.
 //
 // A CTA owns two groups of 128 query rows that share every K and V tile: two heads of one
-// KV head at the same tokens where the group size is even, else 256 tokens of one head.  Per
-// 64-key tile j and group g
+// KV head at the same tokens where the group size is even, else 256 tokens of one head; up to 64
+// queries stand in rows of 8, 16, 32 or 64 a head, so that a group holds several heads.  A grid
+// that would leave half of the multiprocessors idle is multiplied by cutting the key tiles of
+// each CTA into parts, which a second grid joins by their log-sum-exps.  Per 64-key tile j and
+// group g
 //   S_g = Q_g K_j^T   M = 128 queries, N = 64 keys   (64 TMEM columns, two buffers a group)
 //   O_g += P_g V_j    M = 128, N = d, P from TMEM (16-bit, over the first 32 columns of its S)
 // One row per softmax thread (warps 0-3 group A, 4-7 group B).  Warps 8 and 11 stream K and V
@@ -61,20 +64,41 @@ struct PfKernelArgs {
   void* out;
   dkv_strides os;
   float* lse;
-  int by_heads;  // the groups are two heads (else two 128-token tiles of one head)
+  int rows;      // query rows of a head in a group: 128, or 8, 16, 32, 64 with 128 / rows heads a group
+  int by_heads;  // the groups hold different heads (else two 128-token tiles of one head)
+  int heads;     // heads of a CTA
+  int per_kv;    // CTAs that share the heads of a KV head
+  int parts;     // parts of each CTA's key tiles
+  float* part_o;    // [CTA][part][256 rows][d] and
+  float* part_lse;  // [CTA][part][256 rows] base-2, when parts > 1
 };
+
+// Row `row` of group g of a CTA's 256: its head and token.
+struct PfRow {
+  int head, token;
+  bool live;
+};
+__device__ inline PfRow pf_row(const PfKernelArgs& p, int kvh, int h0, int row0, int n, int g, int row) {
+  PfRow r;
+  const int h = h0 + (p.by_heads ? g * (kPfM / p.rows) + row / p.rows : 0);  // within the KV head's group
+  r.head = kvh * p.a.G + h;
+  r.token = row0 + (p.by_heads ? row & (p.rows - 1) : g * kPfM + row);
+  r.live = h < p.a.G && r.token < n;
+  return r;
+}
 
 // every query at positions [p_lo, p_hi] sees every key of [k0, k0 + kPfN)
 __device__ inline bool all_seen(const PagedArgs& a, int k0, int p_lo, int p_hi) {
   return k0 + kPfN - 1 <= p_lo && (a.window == 0 || k0 > p_hi - a.window || k0 + kPfN <= a.sinks);
 }
 
-// V rows that are not finite, and that this row sees: p v in fp32, for channels c0 .. c0 + 31 (rare, so in
-// plain loops)
+// f = the sum of p v in fp32 over the V rows that are not finite and that this row sees, for channels
+// c0 .. c0 + 31 (rare, so in plain loops)
 template <typename T, int D>
 __device__ __noinline__ void add_bad_rows(const PfKernelArgs& p, const PagedArgs& a, int b, int head, int kvh, int qrow, int pos,
                                           int bads, const int* bad_key, const uint32_t* bad_bits, int c0, float m, float il,
                                           float* f) {
+  for (int e = 0; e < 32; ++e) f[e] = 0.f;
   const T* qr = static_cast<const T*>(p.q.q) + (int64_t)b * p.q.qs.batch + (int64_t)head * p.q.qs.head + (int64_t)qrow * p.q.qs.token;
   for (int x = 0; x < bads * kPfN; ++x) {
     const int t = bad_key[x / kPfN] + x % kPfN;
@@ -103,15 +127,23 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   const QuerySpan qs = query_span(a, p.q.q_lens, p.q.Tq, b);
   // the groups: head and first query row (of all heads the later rows, with more keys, first)
   const int tile = (int)gridDim.z - 1 - (int)blockIdx.z;
-  const int row0 = tile * (p.by_heads ? kPfM : 2 * kPfM);
+  const int row0 = tile * (p.by_heads ? p.rows : 2 * kPfM);
+  griddep_launch();
   if (row0 >= qs.n) return;
-  const int h0 = p.by_heads ? 2 * (int)blockIdx.x : (int)blockIdx.x, kvh = h0 / a.G;
-  const int rowsA = min(kPfM, qs.n - row0), rowsB = p.by_heads ? rowsA : min(kPfM, max(0, qs.n - row0 - kPfM));
-  const int p_lo = qs.off + row0, p_hi = p_lo + (p.by_heads ? rowsA : rowsA + rowsB) - 1;
+  const int part = (int)blockIdx.x % p.parts, hg = (int)blockIdx.x / p.parts;
+  const int kvh = hg / p.per_kv, h0 = hg % p.per_kv * p.heads;  // h0: within the KV head's group
+  // tokens of the groups, heads of each (0: an empty group)
+  const int tokA = min(p.by_heads ? p.rows : kPfM, qs.n - row0), tokB = p.by_heads ? tokA : max(0, min(kPfM, qs.n - row0 - kPfM));
+  const int hdA = p.by_heads ? min(kPfM / p.rows, a.G - h0) : 1;
+  const int hdB = p.by_heads ? max(0, min(kPfM / p.rows, a.G - h0 - kPfM / p.rows)) : (tokB > 0 ? 1 : 0);
+  const int p_lo = qs.off + row0, p_hi = p_lo + (p.by_heads ? tokA : tokA + tokB) - 1;
   const KeySpan<kPfN> ks = key_span<kPfN>(a, p_lo, p_hi);
-  // group A's keys may end a tile or two before B's
-  const int nA = min(ks.n, max(0, ks.st + (max(0, p_lo + rowsA) + kPfN - 1) / kPfN - ks.wt0)), nB = rowsB > 0 ? ks.n : 0;
+  // this part's key tiles; group A's may end a tile or two before B's
+  const int t0 = (int)((int64_t)ks.n * part / p.parts), t1 = (int)((int64_t)ks.n * (part + 1) / p.parts);
+  const int endA = p.by_heads ? ks.n : min(ks.n, max(0, ks.st + (max(0, p_lo + tokA) + kPfN - 1) / kPfN - ks.wt0));
+  const int nA = max(0, min(endA, t1) - t0), nB = hdB > 0 ? t1 - t0 : 0;
   const int nt = max(nA, nB);
+  auto key_of = [&](int j) { return ks.key(t0 + j); };  // first key of tile j
 
   const uint32_t sb = smem_u32(smem);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + S::kOffBar);  // [slot]
@@ -156,13 +188,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   // K or V tiles; whole warp
   const int rows = min(a.page_mask + 1, kPfN), runs = kPfN / rows;
   auto page_of = [&](int j) {  // lane i < runs: the page of the tile's i-th run of `rows` keys
-    const int first = ks.key(j) + lane * rows;
+    const int first = key_of(j) + lane * rows;
     // runs without a visible key: zeros, wherever the table points
     return j < nt && lane < runs && first < ks.hi && (first + rows > ks.lo || first < a.sinks) ? paged_page(a, b, first) : a.n_pages;
   };
   auto load = [&](const CUtensorMap* map, uint32_t to, int j, int page, uint64_t* bar, uint32_t el) {
     if (el) mbar_arrive_expect_tx(bar, S::kTile);
-    const int y = ks.key(j) & a.page_mask;
+    const int y = key_of(j) & a.page_mask;
 #pragma unroll 2
     for (int i = 0; i < runs; ++i) {
       const int pg = __shfl_sync(0xffffffffu, page, i);
@@ -181,11 +213,14 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const uint32_t el = elect_one();
     int j = 0;
     if (nt > 0) {
-      if (el) mbar_arrive_expect_tx(q_full, (rowsB > 0 ? 2 : 1) * S::kQ);
-      for (int g = 0; g < (rowsB > 0 ? 2 : 1); ++g)
+      if (el) mbar_arrive_expect_tx(q_full, (uint32_t)((hdA + hdB) * p.rows) * D * 2);
+      for (int x = 0; x < hdA + hdB; ++x) {  // a box of p.rows rows for each head (or 128-token tile)
+        const int g = x < hdA ? 0 : 1, slot = x - g * hdA;
+#pragma unroll
         for (int hf = 0; hf < D / 64; ++hf)
-          tma_load_4d(sb + g * S::kQ + hf * kPfM * 128, &qmap, hf * 64, p.by_heads ? row0 : row0 + g * kPfM,
-                      p.by_heads ? h0 + g : h0, b, q_full, el);
+          tma_load_4d(sb + g * S::kQ + hf * kPfM * 128 + slot * p.rows * 128, &qmap, hf * 64, p.by_heads ? row0 : row0 + g * kPfM,
+                      kvh * a.G + h0 + (p.by_heads ? x : 0), b, q_full, el);
+      }
     }
     for (int page = page_of(0); j < nt; ++j) {
       const int next = page_of(j + 1);  // looked up a tile ahead of its use
@@ -244,7 +279,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     // =========================== V, and the rows of its edge tiles
     const uint32_t el = elect_one();
     auto clean = [&](int j, int edge) {
-      const int k0 = ks.key(j), sl = j % S::kR;
+      const int k0 = key_of(j), sl = j % S::kR;
       ok = __all_sync(0xffffffffu, ok && mbar_wait(&landed[edge], 0, a.err));
       const uint32_t vb = sb + S::kOffV + sl * S::kTile;
       uint32_t bad = 0;  // rows lane, lane + 32 with a value that is not finite
@@ -293,7 +328,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     for (int page = page_of(0); j < nt; ++j) {
       const int next = page_of(j + 1);
       if (!slot_free(j)) break;
-      const bool edge = !all_seen(a, ks.key(j), p_lo, p_hi);
+      const bool edge = !all_seen(a, key_of(j), p_lo, p_hi);
       load(&vmap, S::kOffV + (j % S::kR) * S::kTile, j, page, edge ? &landed[edges] : &v_full[j % S::kR], el);
       page = next;
       if (todo[first] >= 0 && (todo[first] <= j - 2 || todo[first ^ 1] >= 0)) clean_next();
@@ -307,11 +342,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   } else if (warp < 8) {
     // =========================== softmax: one query row per thread
     const int g = warp >> 2, rw = warp & 3, row = 32 * rw + lane;
-    const int n = g ? nB : nA, rows = g ? rowsB : rowsA;
-    const int qrow = p.by_heads ? row0 + row : row0 + g * kPfM + row, pos = qs.off + qrow;
-    const int head = p.by_heads ? h0 + g : h0;
+    const int n = g ? nB : nA;
+    const PfRow me = pf_row(p, kvh, h0, row0, qs.n, g, row);
+    const int pos = qs.off + me.token;
     // positions of the group's rows (the tile is unmasked when all of them see all of it)
-    const int g_lo = p.by_heads ? p_lo : p_lo + g * kPfM, g_hi = g_lo + rows - 1;
+    const int g_lo = p.by_heads ? p_lo : p_lo + g * kPfM, g_hi = g_lo + (g ? tokB : tokA) - 1;
     const uint32_t tg = tmem + ((uint32_t)(32 * rw) << 16) + 256u * g, to = tg + 128u;
     const float slog2 = a.scale_log2;
     float m = -INFINITY, l = 0.f;
@@ -324,7 +359,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
       for (int c = 0; c < kPfN / 32; ++c) tc_ld32(ts + 32 * c, s + 32 * c);
       tc_ld_wait();
-      const int k0 = ks.key(j);
+      const int k0 = key_of(j);
       if (!all_seen(a, k0, g_lo, g_hi)) {
         // bit c: this row sees key k0 + c
         const int hi = pos - k0, lo = a.window ? pos - a.window + 1 - k0 : 0, sk = a.sinks - k0;
@@ -377,13 +412,14 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     }
     if (n > 0 && ok) ok = mbar_wait(&o_done[2 * g + ((n - 1) & 1)], (uint32_t)(((n - 1) >> 1) & 1), a.err);
     tc_fence_after();
-    const bool live = row < rows;
+    const bool live = me.live;
     const float il = n == 0 || l == 0.f ? 0.f : 1.f / l;  // a row that sees no key: zeros
     // (every edge tile's product, and so warp 11's work on it, is behind o_done)
     const int bads = n > 0 ? *reinterpret_cast<volatile int*>(n_bad) : 0;
     // The rows go through the group's Q, which no product reads any more, so that a warp then writes
     // whole rows of the output.
     const uint32_t stage = sb + g * S::kQ;
+    const int64_t rec = (((int64_t)b * gridDim.z + tile) * (gridDim.x / p.parts) + hg) * p.parts + part;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
       uint32_t o[32];
@@ -394,25 +430,41 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       float f[32];
 #pragma unroll
       for (int e = 0; e < 32; ++e) f[e] = n > 0 && l != 0.f ? __uint_as_float(o[e]) * il : 0.f;
-      if (bads && live) add_bad_rows<T, D>(p, a, b, head, kvh, qrow, pos, bads, bad_key, bad_bits, 32 * c, m, il, f);
+      if (bads && live) {
+        float more[32];
+        add_bad_rows<T, D>(p, a, b, me.head, kvh, me.token, pos, bads, bad_key, bad_bits, 32 * c, m, il, more);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) f[e] += more[e];
+      }
+      if (p.parts > 1) {
+        if (live) {
+          float* o32 = p.part_o + (rec * 2 * kPfM + g * kPfM + row) * D + 32 * c;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(o32 + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+        }
+        continue;
+      }
 #pragma unroll
       for (int e = 0; e < 32; e += 8)
         sts128(stage + sw128(kPfM, row, (32 * c + e) / 8),
                make_uint4(Num<T>::pack(f[e], f[e + 1]), Num<T>::pack(f[e + 2], f[e + 3]), Num<T>::pack(f[e + 4], f[e + 5]),
                           Num<T>::pack(f[e + 6], f[e + 7])));
     }
-    __syncwarp();
-    {
-      T* out = static_cast<T*>(p.out) + (int64_t)b * p.os.batch + (int64_t)head * p.os.head;
-      const int q0 = qrow - lane, ch = lane % (D / 8);  // a row's piece; D / 8 lanes a row
+    const float lse2 = n == 0 ? -INFINITY : m - kPfShift<T> + log2f(l);
+    if (p.parts > 1) {
+      if (live) p.part_lse[rec * 2 * kPfM + g * kPfM + row] = lse2;
+    } else {
+      __syncwarp();
+      const int ch = lane % (D / 8);  // a row's piece; D / 8 lanes a row
 #pragma unroll 4
-      for (int r = lane / (D / 8); r < 32; r += 256 / D)
-        if (32 * rw + r < rows)
-          *reinterpret_cast<uint4*>(out + (int64_t)(q0 + r) * p.os.token + 8 * ch) = lds128(stage + sw128(kPfM, 32 * rw + r, ch));
+      for (int r = 32 * rw + lane / (D / 8); r < 32 * rw + 32; r += 256 / D) {
+        const PfRow to_row = pf_row(p, kvh, h0, row0, qs.n, g, r);
+        if (to_row.live)
+          *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (int64_t)b * p.os.batch + (int64_t)to_row.head * p.os.head +
+                                    (int64_t)to_row.token * p.os.token + 8 * ch) = lds128(stage + sw128(kPfM, r, ch));
+      }
+      if (live && p.lse) p.lse[((int64_t)b * a.Hq + me.head) * p.q.Tq + me.token] = lse2 * 0.6931471805599453f;
     }
-    if (live && p.lse)
-      p.lse[((int64_t)b * a.Hq + head) * p.q.Tq + qrow] =
-          n == 0 ? -INFINITY : (m - kPfShift<T> + log2f(l)) * 0.6931471805599453f;
   }
   tc_fence_before();
   __syncthreads();
@@ -420,22 +472,70 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   if (warp == 0) tc_free<512>(tmem);
 }
 
+// The parts of a row joined: weights 2^(lse_part - M), in part order.  A warp per row.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) paged_prefill_join_kernel(PfKernelArgs p, int tiles, int hgs) {
+  constexpr int V = D / 32;  // channels of a lane
+  const PagedArgs& a = p.a;
+  griddep_wait();
+  const int b = blockIdx.z, tile = (int)blockIdx.y / hgs, hg = (int)blockIdx.y % hgs, lane = threadIdx.x & 31;
+  const int row = (int)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const QuerySpan qs = query_span(a, p.q.q_lens, p.q.Tq, b);
+  const PfRow me = pf_row(p, hg / p.per_kv, hg % p.per_kv * p.heads, tile * (p.by_heads ? p.rows : 2 * kPfM), qs.n, row / kPfM, row % kPfM);
+  if (!me.live) return;
+  const int64_t rec = (((int64_t)b * tiles + tile) * hgs + hg) * p.parts;
+  auto at = [&](int i) { return (rec + i) * 2 * kPfM + row; };
+  float M = -INFINITY;
+  for (int i = lane; i < p.parts; i += 32) M = fmaxf(M, __ldcg(p.part_lse + at(i)));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float f[V] = {}, L = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < p.parts; ++i) {
+    const float lse = __ldcg(p.part_lse + at(i));
+    if (lse == -INFINITY) continue;  // (a NaN goes on)
+    const float w = fast_exp2(lse - M);
+    L += w;
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+      const float2 o = __ldcg(reinterpret_cast<const float2*>(p.part_o + at(i) * D + V * lane + e));
+      f[e] = fmaf(w, o.x, f[e]);
+      f[e + 1] = fmaf(w, o.y, f[e + 1]);
+    }
+  }
+  const float il = L == 0.f ? 0.f : 1.f / L;
+  T* out = static_cast<T*>(p.out) + (int64_t)b * p.os.batch + (int64_t)me.head * p.os.head + (int64_t)me.token * p.os.token + V * lane;
+#pragma unroll
+  for (int e = 0; e < V; e += 2) *reinterpret_cast<uint32_t*>(out + e) = Num<T>::pack(f[e] * il, f[e + 1] * il);
+  if (p.lse && lane == 0) p.lse[((int64_t)b * a.Hq + me.head) * p.q.Tq + me.token] = (M + log2f(L)) * 0.6931471805599453f;
+}
+
 template <typename T, int D>
 cudaError_t launch_td(const PfKernelArgs& p, const PagedMaps& m, const CUtensorMap& qmap, cudaStream_t s) {
   constexpr uint32_t smem = PfSmem<D>::kBytes;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(paged_prefill_kernel<T, D>), smem);
   if (e != cudaSuccess) return e;
-  const int per = p.by_heads ? kPfM : 2 * kPfM;
-  const dim3 grid(p.by_heads ? p.a.Hq / 2 : p.a.Hq, p.a.B, (p.q.Tq + per - 1) / per);
-  paged_prefill_kernel<T, D><<<grid, kPfThreads, smem, s>>>(p, qmap, m.k, m.v);
-  return cudaGetLastError();
+  const int tiles = (p.q.Tq + (p.by_heads ? p.rows : 2 * kPfM) - 1) / (p.by_heads ? p.rows : 2 * kPfM);
+  const int hgs = p.a.Hkv * p.per_kv;
+  paged_prefill_kernel<T, D><<<dim3(hgs * p.parts, p.a.B, tiles), kPfThreads, smem, s>>>(p, qmap, m.k, m.v);
+  if ((e = cudaGetLastError()) != cudaSuccess || p.parts == 1) return e;
+  return launch_dependent(paged_prefill_join_kernel<T, D>, dim3(2 * kPfM / 8, tiles * hgs, p.a.B), 256, 0, s, p, tiles, hgs);
 }
 
 }  // namespace
 
+// Rows of a head in a group.  Up to 64 queries: a power of two, so that a group holds several heads.
+int paged_prefill_rows(int Tq) {
+  int r = 8;
+  while (r < Tq && r < kPfM) r *= 2;
+  return r;
+}
+
+size_t paged_prefill_ws_bytes(int d) { return kWsHeader + (size_t)sm_count() * 2 * kPfM * (d + 1) * 4; }
+
 cudaError_t launch_paged_prefill(const PagedArgs& a, int d, int dtype, const PagedMaps& m, const CUtensorMap& qmap,
                                  const PagedQuery& q, const void* v_pool, const void* k_pool, void* out,
-                                 const dkv_strides& os, float* lse, cudaStream_t s) {
+                                 const dkv_strides& os, float* lse, uint8_t* ws, cudaStream_t s) {
   PfKernelArgs p;
   p.a = a;
   p.q = q;
@@ -444,7 +544,20 @@ cudaError_t launch_paged_prefill(const PagedArgs& a, int d, int dtype, const Pag
   p.out = out;
   p.os = os;
   p.lse = lse;
-  p.by_heads = a.G % 2 == 0;
+  p.rows = paged_prefill_rows(q.Tq);
+  p.by_heads = a.G % 2 == 0 || p.rows < kPfM;
+  p.heads = p.by_heads ? 2 * kPfM / p.rows : 1;
+  p.per_kv = (a.G + p.heads - 1) / p.heads;
+  // Parts: when the grid would fill at most half of the multiprocessors (records for one grid of them
+  // are what the workspace holds), at least four tiles each by the longest sequence the table allows.
+  const int tokens = p.by_heads ? p.rows : 2 * kPfM;
+  const int64_t ctas = (int64_t)a.Hkv * p.per_kv * a.B * ((q.Tq + tokens - 1) / tokens);
+  const int64_t keys = a.window > 0 && (int64_t)a.window + a.sinks + tokens < a.cap ? (int64_t)a.window + a.sinks + tokens : a.cap;
+  const int64_t most = keys / (4 * kPfN), fit = sm_count() / ctas;
+  p.parts = (int)(fit < most ? fit : most);
+  if (p.parts < 2) p.parts = 1;
+  p.part_o = reinterpret_cast<float*>(ws + kWsHeader);
+  p.part_lse = p.part_o + (size_t)sm_count() * 2 * kPfM * d;
   if (dtype == DKV_BF16)
     return d == 128 ? launch_td<__nv_bfloat16, 128>(p, m, qmap, s) : launch_td<__nv_bfloat16, 64>(p, m, qmap, s);
   return d == 128 ? launch_td<__half, 128>(p, m, qmap, s) : launch_td<__half, 64>(p, m, qmap, s);
