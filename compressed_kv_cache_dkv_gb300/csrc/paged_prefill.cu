@@ -65,6 +65,7 @@ struct PfKernelArgs {
   dkv_strides os;
   float* lse;
   int rows;      // query rows of a head in a group: 128, or 8, 16, 32, 64 with 128 / rows heads a group
+  int rows_shift;
   int by_heads;  // the groups hold different heads (else two 128-token tiles of one head)
   int heads;     // heads of a CTA
   int per_kv;    // CTAs that share the heads of a KV head
@@ -80,7 +81,7 @@ struct PfRow {
 };
 __device__ inline PfRow pf_row(const PfKernelArgs& p, int kvh, int h0, int row0, int n, int g, int row) {
   PfRow r;
-  const int h = h0 + (p.by_heads ? g * (kPfM / p.rows) + row / p.rows : 0);  // within the KV head's group
+  const int h = h0 + (p.by_heads ? (g * kPfM + row) >> p.rows_shift : 0);  // within the KV head's group
   r.head = kvh * p.a.G + h;
   r.token = row0 + (p.by_heads ? row & (p.rows - 1) : g * kPfM + row);
   r.live = h < p.a.G && r.token < n;
@@ -456,13 +457,17 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     } else {
       __syncwarp();
       const int ch = lane % (D / 8);  // a row's piece; D / 8 lanes a row
+      T* out = static_cast<T*>(p.out) + (int64_t)b * p.os.batch + 8 * ch;
+      auto store = [&](const PfRow& first, int r0, int n_rows) {  // rows r0 .. r0 + n_rows - 1, of one head
+        if (!first.live) return;
+        T* at = out + (int64_t)first.head * p.os.head + (int64_t)first.token * p.os.token;
+        const int live_rows = min(n_rows, qs.n - first.token);
 #pragma unroll 4
-      for (int r = 32 * rw + lane / (D / 8); r < 32 * rw + 32; r += 256 / D) {
-        const PfRow to_row = pf_row(p, kvh, h0, row0, qs.n, g, r);
-        if (to_row.live)
-          *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (int64_t)b * p.os.batch + (int64_t)to_row.head * p.os.head +
-                                    (int64_t)to_row.token * p.os.token + 8 * ch) = lds128(stage + sw128(kPfM, r, ch));
-      }
+        for (int r = lane / (D / 8); r < live_rows; r += 256 / D)
+          *reinterpret_cast<uint4*>(at + (int64_t)r * p.os.token) = lds128(stage + sw128(kPfM, r0 + r, ch));
+      };
+      const int step = min(p.rows, 32);
+      for (int r = 32 * rw; r < 32 * rw + 32; r += step) store(pf_row(p, kvh, h0, row0, qs.n, g, r), r, step);
       if (live && p.lse) p.lse[((int64_t)b * a.Hq + me.head) * p.q.Tq + me.token] = lse2 * 0.6931471805599453f;
     }
   }
@@ -545,6 +550,8 @@ cudaError_t launch_paged_prefill(const PagedArgs& a, int d, int dtype, const Pag
   p.os = os;
   p.lse = lse;
   p.rows = paged_prefill_rows(q.Tq);
+  p.rows_shift = 0;
+  while ((1 << p.rows_shift) < p.rows) ++p.rows_shift;
   p.by_heads = a.G % 2 == 0 || p.rows < kPfM;
   p.heads = p.by_heads ? 2 * kPfM / p.rows : 1;
   p.per_kv = (a.G + p.heads - 1) / p.heads;
