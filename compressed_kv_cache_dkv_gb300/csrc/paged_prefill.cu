@@ -235,45 +235,55 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   } else if (warp == 9 || warp == 10) {
     // =========================== products of group g
     // The whole warp walks through here and one elected lane issues: in code that one lane runs
-    // alone the operands are not known to be uniform, and an issue took 75 to 150 cycles.
+    // alone the operands are not known to be uniform, and an issue took 75 to 150 cycles.  The code
+    // is kept short: between two tiles the other warps' code has taken its place in the
+    // instruction cache.
     constexpr uint32_t id_s = tc_idesc(Num<T>::kUmma, false, kPfN), id_o = tc_idesc(Num<T>::kUmma, true, D);
     const uint32_t el = elect_one();
     const int g = warp - 9, n = g ? nB : nA, n_other = g ? nA : nB;
     const uint32_t tg = tmem + 256u * g;
     const uint64_t qd = tc_desc(sb + g * S::kQ, 16, 1024);
-    auto wait = [&](uint64_t* bar, int parity) { ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, (uint32_t)parity, a.err)); };
+    uint64_t* const sf = s_full + 2 * g;
+    uint64_t* const pf = p_full + 2 * g;
+    uint64_t* const od = o_done + 2 * g;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok) ok = mbar_wait(bar, parity, a.err);
+      __syncwarp();
+    };
+    int k_sl = 0, v_sl = 0;             // slots of the next K and V tile
+    uint32_t k_ph = 0, v_ph = 0;        // and their phases
     auto scores = [&](int j) {
-      const int sl = j % S::kR, buf = j & 1;
-      wait(&k_full[sl], (j / S::kR) & 1);
-      if (j >= 2) wait(&o_done[2 * g + buf], ((j - 2) >> 1) & 1);  // the buffer holds P_{j-2}
-      if (!ok) return;
+      const int buf = j & 1;
+      wait(&k_full[k_sl], k_ph);
+      if (j >= 2) wait(&od[buf], (uint32_t)((j - 2) >> 1) & 1u);  // the buffer holds P_{j-2}
       tc_fence_after();
-      const uint64_t kd = tc_desc(sb + S::kOffK + sl * S::kTile, 16, 1024);
+      const uint64_t kd = tc_desc(sb + S::kOffK + k_sl * S::kTile, 16, 1024);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)  // 16 channels: 32 bytes of a 128-byte row, then the next 64 channels
         tc_mma(tg + kPfN * buf, qd + (uint64_t)(((k >> 2) * kPfM * 128 + (k & 3) * 32) >> 4),
                kd + (uint64_t)(((k >> 2) * kPfN * 128 + (k & 3) * 32) >> 4), id_s, k > 0, el);
-      tc_commit(&s_full[2 * g + buf], el);
+      tc_commit(&sf[buf], el);
+      if (++k_sl == S::kR) { k_sl = 0; k_ph ^= 1u; }
     };
     if (n > 0) {
       wait(q_full, 0);
       scores(0);
-      for (int j = 0; j < n && ok; ++j) {
+      for (int j = 0; j < n; ++j) {
         if (j + 1 < n) scores(j + 1);
-        const int sl = j % S::kR, buf = j & 1;
-        wait(&v_full[sl], (j / S::kR) & 1);
-        wait(&p_full[2 * g + buf], (j >> 1) & 1);
-        if (!ok) break;
+        const int buf = j & 1;
+        wait(&v_full[v_sl], v_ph);
+        wait(&pf[buf], (uint32_t)(j >> 1) & 1u);
         tc_fence_after();
-        const uint64_t vd = tc_desc(sb + S::kOffV + sl * S::kTile, kPfN * 128, 1024);
+        const uint64_t vd = tc_desc(sb + S::kOffV + v_sl * S::kTile, kPfN * 128, 1024);
         const uint32_t ts = tg + kPfN * buf;
 #pragma unroll
         for (int k = 0; k < kPfN / 16; ++k)  // 16 keys: 16 rows of 128 bytes
           tc_mma_ta(tg + 128u, ts + 8u * k, vd + (uint64_t)(k * 16 * 128 >> 4), id_o, k > 0 ? 1u : (j > 0 ? 1u : 0u), el);
-        tc_commit(&o_done[2 * g + buf], el);
+        tc_commit(&od[buf], el);
         // once for this group, once more where the other has no tile j
-        tc_commit(&empty[sl], el);
-        if (j >= n_other) tc_commit(&empty[sl], el);
+        tc_commit(&empty[v_sl], el);
+        if (j >= n_other) tc_commit(&empty[v_sl], el);
+        if (++v_sl == S::kR) { v_sl = 0; v_ph ^= 1u; }
       }
     }
   } else if (warp == 11) {
