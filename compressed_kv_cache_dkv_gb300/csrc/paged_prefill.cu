@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   auto load = [&](const CUtensorMap* map, uint32_t to, int j, int page, uint64_t* bar, uint32_t el) {
     if (el) mbar_arrive_expect_tx(bar, S::kTile);
     const int y = key_of(j) & a.page_mask;
-#pragma unroll 2
+#pragma unroll 1  // (here as below: what is short stays in the instruction cache)
     for (int i = 0; i < runs; ++i) {
       const int pg = __shfl_sync(0xffffffffu, page, i);
 #pragma unroll
