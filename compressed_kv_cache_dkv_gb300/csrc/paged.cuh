@@ -129,6 +129,16 @@ __device__ inline void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, 
       "l"(map), "r"(x), "r"(y), "r"(h), "r"(page), "r"(smem_u32(bar)), "r"(el)
       : "memory");
 }
+// the same under an L2 policy
+__device__ inline void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int h, int page, uint64_t* bar,
+                                   uint32_t el, uint64_t policy) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %7, 0;\n\t"
+      "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+      "[%1, {%2, %3, %4, %5}], [%6], %8;\n\t}" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(h), "r"(page), "r"(smem_u32(bar)), "r"(el), "l"(policy)
+      : "memory");
+}
 __device__ inline void tma_prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }

@@ -29,7 +29,7 @@ constexpr int kDecTile = 64, kDecStages = 4, kDecConsumers = 8;
 static_assert(kDecStages % 2 == 0, "two teams take the stages in turn");
 constexpr int kDecThreads = 32 * (kDecConsumers + 1);
 constexpr int kCombThreads = 512, kCombCols = 32;  // combine: channels per CTA
-constexpr int kScoreThreads = 256, kScorePer = 4;
+constexpr int kScoreThreads = 256, kScorePer = 8;
 
 template <int D>
 constexpr int rec_floats() { return 16 + 8 * D; }
@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   if (warp == kDecConsumers) {
     // =========================== producer
     const uint32_t el = elect_one();
+    const uint64_t policy = policy_evict_first();  // a cache is read once a step
     const int rows = min(a.page_mask + 1, kDecTile), ppt = kDecTile / rows;  // boxes of `rows` slots, runs per tile
     bool ok = true;
     int it = 0;
@@ -115,13 +116,14 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         if (el) mbar_arrive_expect_tx(&full[st], 2 * TILE);
         const uint32_t dst = sb + (uint32_t)(2 * st) * TILE;
+#pragma unroll 1
         for (int i = 0; i < ppt; ++i) {
           const int pg = __shfl_sync(0xffffffffu, page, i);
 #pragma unroll
           for (int hf = 0; hf < D / 64; ++hf) {
             const uint32_t at = dst + (uint32_t)hf * kDecTile * 128u + (uint32_t)(i * rows) * 128u;
-            tma_load_4d(at, &kmap, hf * 64, y, g.h, pg, &full[st], el);
-            tma_load_4d(at + TILE, &vmap, hf * 64, y, g.h, pg, &full[st], el);
+            tma_load_4d(at, &kmap, hf * 64, y, g.h, pg, &full[st], el, policy);
+            tma_load_4d(at + TILE, &vmap, hf * 64, y, g.h, pg, &full[st], el, policy);
           }
         }
       }
