@@ -373,7 +373,8 @@ _I32, _F32 = torch.int32, torch.float32
 class _Geometry:
     """What the calls compare their tensors with, from a descriptor's bytes."""
 
-    __slots__ = ("key", "ref", "dtype", "pool", "strides", "batch", "heads", "kv_heads", "d", "table", "weights")
+    __slots__ = ("key", "ref", "dtype", "pool", "strides", "batch", "heads", "kv_heads", "d", "each", "table", "q1", "lse1",
+                 "weights", "lib")
 
     def __init__(self, p: dkv_paged, key: bytes):
         self.key, self.ref = key, ctypes.byref(p)
@@ -381,8 +382,10 @@ class _Geometry:
         self.batch, self.heads, self.kv_heads, self.d = p.batch, p.n_q_heads, p.n_kv_heads, p.head_dim
         self.pool = (p.n_pages, p.n_kv_heads, p.page_size, p.head_dim)
         self.strides = (p.stride_page, p.stride_head, p.stride_token, 1)
-        self.table = (p.batch, p.max_pages)
+        self.each, self.table = (p.batch,), (p.batch, p.max_pages)
+        self.q1, self.lse1 = (p.batch, p.n_q_heads, p.head_dim), (p.batch, p.n_q_heads)
         self.weights = (p.batch, p.n_kv_heads, p.max_pages * p.page_size)
+        self.lib = lib()
 
 
 def _geometry(p: dkv_paged) -> _Geometry:
@@ -393,12 +396,17 @@ def _geometry(p: dkv_paged) -> _Geometry:
     return g
 
 
-def _typed(t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev: int, what: str) -> int:
-    """Address of a contiguous tensor of this type and shape on this device."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{what}: expected contiguous {dtype} {shape} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} "
-                         f"with strides {t.stride()} on {t.device}")
-    return t.data_ptr()
+# The checks below stand in the calls themselves as one expression per tensor (a call into a helper
+# costs as much as a check); these say what was wrong.
+
+def _wrong(what: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev: int):
+    raise ValueError(f"{what}: expected contiguous {dtype} {tuple(shape)} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} "
+                     f"with strides {t.stride()} on {t.device}")
+
+
+def _wrong_rows(what: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev: int):
+    raise ValueError(f"{what}: expected {dtype} {tuple(shape)} with adjacent channels on cuda:{dev}, got {t.dtype} "
+                     f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
 @functools.lru_cache(maxsize=1024)
@@ -407,33 +415,18 @@ def _strides(batch: int, head: int, token: int):
     return ctypes.byref(s)
 
 
-def _rows(t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev: int, what: str):
-    """Strides of a tensor [batch][head][(token)][head_dim] whose channels are adjacent."""
-    s = t.stride()
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or s[-1] != 1:
-        raise ValueError(f"{what}: expected {dtype} {shape} with adjacent channels on cuda:{dev}, got {t.dtype} "
-                         f"{tuple(t.shape)} with strides {s} on {t.device}")
-    return _strides(s[0], s[1], s[2] if len(s) == 4 else 0)
-
-
-def _pool(g: _Geometry, t: torch.Tensor, dev: int) -> int:
+def _check_pool(g: _Geometry, t: torch.Tensor, dev: int) -> None:
     if t.dtype is not g.dtype or t.shape != g.pool or t.get_device() != dev:
         raise ValueError(f"pool: expected {g.dtype} {g.pool} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     if t.stride() != g.strides and any(n > 1 and a != b for n, a, b in zip(g.pool, t.stride(), g.strides)):
         raise ValueError(f"pool: strides {t.stride()} are not the descriptor's {g.strides}")
-    return t.data_ptr()
 
 
-def _paged_device(t: torch.Tensor) -> int:
-    """Index of the tensor's device, -1 where it is not the current one (the call goes there then)."""
-    dev = t.get_device()
+def _elsewhere(t: torch.Tensor, dev: int) -> bool:
+    """Whether the call has to be made on another device than the current one (its tensors' own)."""
     if dev < 0:
         raise ValueError("device tensor expected")
-    return dev if dev == torch._C._cuda_getDevice() else -1
-
-
-def _paged_stream(stream, dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    return dev != torch._C._cuda_getDevice()
 
 
 def _paged_ws(p: dkv_paged, workspace, dev: int, with_weights: bool = False) -> torch.Tensor:
@@ -470,22 +463,37 @@ def dkv_paged_append(p: dkv_paged, K_new: torch.Tensor, V_new: torch.Tensor, k_p
                      workspace: torch.Tensor | None = None, stream=None) -> None:
     """Write K_new, V_new [B, Hkv, n_new, d] (any strides with adjacent channels) into their pages: token
     i < counts[b] of sequence b at position pos[b] + i (counts None: all n_new)."""
-    dev = _paged_device(K_new)
-    if dev < 0:
-        with torch.cuda.device(K_new.device):
+    dev = K_new.get_device()
+    if _elsewhere(K_new, dev):
+        with torch.cuda.device(dev):
             return dkv_paged_append(p, K_new, V_new, k_pages, v_pages, page_table, pos, counts, workspace, stream)
-    g, n = _geometry(p), K_new.shape[2]
+    g = _geometry(p)
     if K_new.stride() != V_new.stride():
         K_new, V_new = K_new.contiguous(), V_new.contiguous()
+    n = K_new.shape[2]
     shape = (g.batch, g.kv_heads, n, g.d)
-    ns = _rows(K_new, g.dtype, shape, dev, "K_new")
-    _rows(V_new, g.dtype, shape, dev, "V_new")
+    s = K_new.stride()
+    if K_new.dtype is not g.dtype or K_new.shape != shape or K_new.get_device() != dev or s[-1] != 1:
+        _wrong_rows("K_new", K_new, g.dtype, shape, dev)
+    if V_new.dtype is not g.dtype or V_new.shape != shape or V_new.get_device() != dev:
+        _wrong_rows("V_new", V_new, g.dtype, shape, dev)
+    if pos.dtype is not _I32 or pos.shape != g.each or pos.get_device() != dev or not pos.is_contiguous():
+        _wrong("pos", pos, _I32, g.each, dev)
+    if counts is not None and (counts.dtype is not _I32 or counts.shape != g.each or counts.get_device() != dev or not counts.is_contiguous()):
+        _wrong("counts", counts, _I32, g.each, dev)
+    if k_pages.dtype is not g.dtype or k_pages.stride() != g.strides or k_pages.shape != g.pool or k_pages.get_device() != dev:
+        _check_pool(g, k_pages, dev)
+    if v_pages.dtype is not g.dtype or v_pages.stride() != g.strides or v_pages.shape != g.pool or v_pages.get_device() != dev:
+        _check_pool(g, v_pages, dev)
+    if page_table.dtype is not _I32 or page_table.shape != g.table or page_table.get_device() != dev or not page_table.is_contiguous():
+        _wrong("page_table", page_table, _I32, g.table, dev)
     ws = _paged_ws(p, workspace, dev)
-    _check(lib().dkv_paged_append(
-        g.ref, K_new.data_ptr(), V_new.data_ptr(), ns, n, _typed(pos, _I32, (g.batch,), dev, "pos"),
-        None if counts is None else _typed(counts, _I32, (g.batch,), dev, "counts"), _pool(g, k_pages, dev),
-        _pool(g, v_pages, dev), _typed(page_table, _I32, g.table, dev, "page_table"), ws.data_ptr(), ws.numel(),
-        _paged_stream(stream, dev)), "dkv_paged_append")
+    st = g.lib.dkv_paged_append(
+        g.ref, K_new.data_ptr(), V_new.data_ptr(), _strides(s[0], s[1], s[2]), n, pos.data_ptr(),
+        None if counts is None else counts.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+        ws.data_ptr(), ws.numel(), torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st, "dkv_paged_append")
 
 
 def dkv_paged_decode(p: dkv_paged, q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
@@ -494,27 +502,42 @@ def dkv_paged_decode(p: dkv_paged, q: torch.Tensor, k_pages: torch.Tensor, v_pag
     """One new token per sequence: q [B, Hq, d] at position lens[b] - 1 -> (out [B, Hq, d] in q's type,
     lse fp32 [B, Hq] or None).  `weights` fp32 [B, Hkv, max_pages * page_size]: every visible token's
     softmax weight, summed over its KV head's query heads, is added."""
-    dev = _paged_device(q)
-    if dev < 0:
-        with torch.cuda.device(q.device):
+    dev = q.get_device()
+    if _elsewhere(q, dev):
+        with torch.cuda.device(dev):
             return dkv_paged_decode(p, q, k_pages, v_pages, page_table, lens, out, lse, weights, workspace, stream)
     g = _geometry(p)
-    shape = (g.batch, g.heads, g.d)
-    qs = _rows(q, g.dtype, shape, dev, "q")
+    s = q.stride()
+    if q.dtype is not g.dtype or q.shape != g.q1 or q.get_device() != dev or s[-1] != 1:
+        _wrong_rows("q", q, g.dtype, g.q1, dev)
+    if k_pages.dtype is not g.dtype or k_pages.stride() != g.strides or k_pages.shape != g.pool or k_pages.get_device() != dev:
+        _check_pool(g, k_pages, dev)
+    if v_pages.dtype is not g.dtype or v_pages.stride() != g.strides or v_pages.shape != g.pool or v_pages.get_device() != dev:
+        _check_pool(g, v_pages, dev)
+    if page_table.dtype is not _I32 or page_table.shape != g.table or page_table.get_device() != dev or not page_table.is_contiguous():
+        _wrong("page_table", page_table, _I32, g.table, dev)
+    if lens.dtype is not _I32 or lens.shape != g.each or lens.get_device() != dev or not lens.is_contiguous():
+        _wrong("lens", lens, _I32, g.each, dev)
     if out is None:
-        out = torch.empty(shape, dtype=g.dtype, device=dev)
+        out = torch.empty(g.q1, dtype=g.dtype, device=dev)
+    elif out.dtype is not g.dtype or out.shape != g.q1 or out.get_device() != dev or not out.is_contiguous():
+        _wrong("out", out, g.dtype, g.q1, dev)
     if lse is True:
-        lse = torch.empty(g.batch, g.heads, dtype=_F32, device=dev)
+        lse = torch.empty(g.lse1, dtype=_F32, device=dev)
     elif lse is False:
         lse = None
+    elif lse is not None and (lse.dtype is not _F32 or lse.shape != g.lse1 or lse.get_device() != dev or not lse.is_contiguous()):
+        _wrong("lse", lse, _F32, g.lse1, dev)
+    if weights is not None and (weights.dtype is not _F32 or weights.shape != g.weights or weights.get_device() != dev or not weights.is_contiguous()):
+        _wrong("weights", weights, _F32, g.weights, dev)
     ws = _paged_ws(p, workspace, dev, weights is not None)
-    _check(lib().dkv_paged_decode(
-        g.ref, q.data_ptr(), qs, _pool(g, k_pages, dev), _pool(g, v_pages, dev),
-        _typed(page_table, _I32, g.table, dev, "page_table"), _typed(lens, _I32, (g.batch,), dev, "lens"),
-        _typed(out, g.dtype, shape, dev, "out"),
-        None if lse is None else _typed(lse, _F32, (g.batch, g.heads), dev, "lse"),
-        None if weights is None else _typed(weights, _F32, g.weights, dev, "weights"), ws.data_ptr(), ws.numel(),
-        _paged_stream(stream, dev)), "dkv_paged_decode")
+    st = g.lib.dkv_paged_decode(
+        g.ref, q.data_ptr(), _strides(s[0], s[1], 0), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+        lens.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+        None if weights is None else weights.data_ptr(), ws.data_ptr(), ws.numel(),
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st, "dkv_paged_decode")
     return out, lse
 
 
@@ -524,27 +547,45 @@ def dkv_paged_prefill(p: dkv_paged, q: torch.Tensor, k_pages: torch.Tensor, v_pa
     """The last tokens of each sequence: q [B, Hq, Tq, d], query i < q_lens[b] (None: Tq) at position
     lens[b] - q_lens[b] + i -> (out [B, Hq, Tq, d] in q's type, lse fp32 [B, Hq, Tq] or None).  Rows from
     q_lens[b] on are left as they were (zeros in outputs allocated here)."""
-    dev = _paged_device(q)
-    if dev < 0:
-        with torch.cuda.device(q.device):
+    dev = q.get_device()
+    if _elsewhere(q, dev):
+        with torch.cuda.device(dev):
             return dkv_paged_prefill(p, q, k_pages, v_pages, page_table, lens, q_lens, out, lse, workspace, stream)
     g, Tq = _geometry(p), q.shape[2]
     shape = (g.batch, g.heads, Tq, g.d)
-    qs = _rows(q, g.dtype, shape, dev, "q")
+    s = q.stride()
+    if q.dtype is not g.dtype or q.shape != shape or q.get_device() != dev or s[-1] != 1:
+        _wrong_rows("q", q, g.dtype, shape, dev)
+    if k_pages.dtype is not g.dtype or k_pages.stride() != g.strides or k_pages.shape != g.pool or k_pages.get_device() != dev:
+        _check_pool(g, k_pages, dev)
+    if v_pages.dtype is not g.dtype or v_pages.stride() != g.strides or v_pages.shape != g.pool or v_pages.get_device() != dev:
+        _check_pool(g, v_pages, dev)
+    if page_table.dtype is not _I32 or page_table.shape != g.table or page_table.get_device() != dev or not page_table.is_contiguous():
+        _wrong("page_table", page_table, _I32, g.table, dev)
+    if lens.dtype is not _I32 or lens.shape != g.each or lens.get_device() != dev or not lens.is_contiguous():
+        _wrong("lens", lens, _I32, g.each, dev)
+    if q_lens is not None and (q_lens.dtype is not _I32 or q_lens.shape != g.each or q_lens.get_device() != dev or not q_lens.is_contiguous()):
+        _wrong("q_lens", q_lens, _I32, g.each, dev)
     new = torch.empty if q_lens is None else torch.zeros
     if out is None:
         out = new(shape, dtype=g.dtype, device=dev)
+    o = out.stride()
+    if out.dtype is not g.dtype or out.shape != shape or out.get_device() != dev or o[-1] != 1:
+        _wrong_rows("out", out, g.dtype, shape, dev)
     if lse is True:
         lse = new(shape[:3], dtype=_F32, device=dev)
     elif lse is False:
         lse = None
+    elif lse is not None and (lse.dtype is not _F32 or lse.shape != shape[:3] or lse.get_device() != dev or not lse.is_contiguous()):
+        _wrong("lse", lse, _F32, shape[:3], dev)
     ws = _paged_ws(p, workspace, dev)
-    _check(lib().dkv_paged_prefill(
-        g.ref, q.data_ptr(), qs, Tq, _pool(g, k_pages, dev), _pool(g, v_pages, dev),
-        _typed(page_table, _I32, g.table, dev, "page_table"), _typed(lens, _I32, (g.batch,), dev, "lens"),
-        None if q_lens is None else _typed(q_lens, _I32, (g.batch,), dev, "q_lens"), out.data_ptr(),
-        _rows(out, g.dtype, shape, dev, "out"), None if lse is None else _typed(lse, _F32, shape[:3], dev, "lse"),
-        ws.data_ptr(), ws.numel(), _paged_stream(stream, dev)), "dkv_paged_prefill")
+    st = g.lib.dkv_paged_prefill(
+        g.ref, q.data_ptr(), _strides(s[0], s[1], s[2]), Tq, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+        lens.data_ptr(), None if q_lens is None else q_lens.data_ptr(), out.data_ptr(), _strides(o[0], o[1], o[2]),
+        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st, "dkv_paged_prefill")
     return out, lse
 
 
@@ -553,20 +594,34 @@ def dkv_paged_weights(p: dkv_paged, q: torch.Tensor, lse: torch.Tensor, k_pages:
                       workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Add the softmax weights that the queries (as in dkv_paged_prefill, with the lse it gave) give every
     token, summed over queries and a KV head's query heads, to weights fp32 [B, Hkv, max_pages * page_size]."""
-    dev = _paged_device(q)
-    if dev < 0:
-        with torch.cuda.device(q.device):
+    dev = q.get_device()
+    if _elsewhere(q, dev):
+        with torch.cuda.device(dev):
             return dkv_paged_weights(p, q, lse, k_pages, page_table, lens, weights, q_lens, workspace, stream)
     g, Tq = _geometry(p), q.shape[2]
     shape = (g.batch, g.heads, Tq, g.d)
-    qs = _rows(q, g.dtype, shape, dev, "q")
+    s = q.stride()
+    if q.dtype is not g.dtype or q.shape != shape or q.get_device() != dev or s[-1] != 1:
+        _wrong_rows("q", q, g.dtype, shape, dev)
+    if lse.dtype is not _F32 or lse.shape != shape[:3] or lse.get_device() != dev or not lse.is_contiguous():
+        _wrong("lse", lse, _F32, shape[:3], dev)
+    if k_pages.dtype is not g.dtype or k_pages.stride() != g.strides or k_pages.shape != g.pool or k_pages.get_device() != dev:
+        _check_pool(g, k_pages, dev)
+    if page_table.dtype is not _I32 or page_table.shape != g.table or page_table.get_device() != dev or not page_table.is_contiguous():
+        _wrong("page_table", page_table, _I32, g.table, dev)
+    if lens.dtype is not _I32 or lens.shape != g.each or lens.get_device() != dev or not lens.is_contiguous():
+        _wrong("lens", lens, _I32, g.each, dev)
+    if q_lens is not None and (q_lens.dtype is not _I32 or q_lens.shape != g.each or q_lens.get_device() != dev or not q_lens.is_contiguous()):
+        _wrong("q_lens", q_lens, _I32, g.each, dev)
+    if weights.dtype is not _F32 or weights.shape != g.weights or weights.get_device() != dev or not weights.is_contiguous():
+        _wrong("weights", weights, _F32, g.weights, dev)
     ws = _paged_ws(p, workspace, dev)
-    _check(lib().dkv_paged_weights(
-        g.ref, q.data_ptr(), qs, Tq, _typed(lse, _F32, shape[:3], dev, "lse"), _pool(g, k_pages, dev),
-        _typed(page_table, _I32, g.table, dev, "page_table"), _typed(lens, _I32, (g.batch,), dev, "lens"),
-        None if q_lens is None else _typed(q_lens, _I32, (g.batch,), dev, "q_lens"),
-        _typed(weights, _F32, g.weights, dev, "weights"), ws.data_ptr(), ws.numel(), _paged_stream(stream, dev)),
-        "dkv_paged_weights")
+    st = g.lib.dkv_paged_weights(
+        g.ref, q.data_ptr(), _strides(s[0], s[1], s[2]), Tq, lse.data_ptr(), k_pages.data_ptr(), page_table.data_ptr(),
+        lens.data_ptr(), None if q_lens is None else q_lens.data_ptr(), weights.data_ptr(), ws.data_ptr(), ws.numel(),
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st, "dkv_paged_weights")
     return weights
 
 
@@ -577,27 +632,44 @@ def dkv_paged_evict(p: dkv_paged, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     """Cut every sequence to `budget` tokens: the first `first`, the last `recent` and the heaviest between
     them, in order, moved to new_table's pages (int32 [B, n]; page_table itself compacts in place) ->
     (kept int32 [B, Hkv, budget], new_lens int32 [B], new_weights like weights)."""
-    dev = _paged_device(k_pages)
-    if dev < 0:
-        with torch.cuda.device(k_pages.device):
+    dev = k_pages.get_device()
+    if _elsewhere(k_pages, dev):
+        with torch.cuda.device(dev):
             return dkv_paged_evict(p, k_pages, v_pages, page_table, lens, weights, budget, first, recent, new_table, kept,
                                    new_lens, new_weights, workspace, stream)
-    g = _geometry(p)
-    width = new_table.shape[-1]
+    g, width = _geometry(p), new_table.shape[-1]
+    k_shape, t_shape = (g.batch, g.kv_heads, max(budget, 0)), (g.batch, width)
+    if k_pages.dtype is not g.dtype or k_pages.stride() != g.strides or k_pages.shape != g.pool or k_pages.get_device() != dev:
+        _check_pool(g, k_pages, dev)
+    if v_pages.dtype is not g.dtype or v_pages.stride() != g.strides or v_pages.shape != g.pool or v_pages.get_device() != dev:
+        _check_pool(g, v_pages, dev)
+    if page_table.dtype is not _I32 or page_table.shape != g.table or page_table.get_device() != dev or not page_table.is_contiguous():
+        _wrong("page_table", page_table, _I32, g.table, dev)
+    if lens.dtype is not _I32 or lens.shape != g.each or lens.get_device() != dev or not lens.is_contiguous():
+        _wrong("lens", lens, _I32, g.each, dev)
+    if weights.dtype is not _F32 or weights.shape != g.weights or weights.get_device() != dev or not weights.is_contiguous():
+        _wrong("weights", weights, _F32, g.weights, dev)
+    if new_table.dtype is not _I32 or new_table.shape != t_shape or new_table.get_device() != dev or not new_table.is_contiguous():
+        _wrong("new_table", new_table, _I32, t_shape, dev)
     if kept is None:
-        kept = torch.empty(g.batch, g.kv_heads, max(budget, 0), dtype=_I32, device=dev)
+        kept = torch.empty(k_shape, dtype=_I32, device=dev)
+    if kept.dtype is not _I32 or kept.shape != k_shape or kept.get_device() != dev or not kept.is_contiguous():
+        _wrong("kept", kept, _I32, k_shape, dev)
     if new_lens is None:
-        new_lens = torch.empty(g.batch, dtype=_I32, device=dev)
+        new_lens = torch.empty(g.each, dtype=_I32, device=dev)
+    if new_lens.dtype is not _I32 or new_lens.shape != g.each or new_lens.get_device() != dev or not new_lens.is_contiguous():
+        _wrong("new_lens", new_lens, _I32, g.each, dev)
     if new_weights is None:
         new_weights = torch.empty(g.weights, dtype=_F32, device=dev)
+    if new_weights.dtype is not _F32 or new_weights.shape != g.weights or new_weights.get_device() != dev or not new_weights.is_contiguous():
+        _wrong("new_weights", new_weights, _F32, g.weights, dev)
     ws = _paged_ws(p, workspace, dev)
-    _check(lib().dkv_paged_evict(
-        g.ref, _pool(g, k_pages, dev), _pool(g, v_pages, dev), _typed(page_table, _I32, g.table, dev, "page_table"),
-        _typed(lens, _I32, (g.batch,), dev, "lens"), _typed(weights, _F32, g.weights, dev, "weights"), budget, first, recent,
-        _typed(new_table, _I32, (g.batch, width), dev, "new_table"), width,
-        _typed(kept, _I32, (g.batch, g.kv_heads, max(budget, 0)), dev, "kept"),
-        _typed(new_lens, _I32, (g.batch,), dev, "new_lens"), _typed(new_weights, _F32, g.weights, dev, "new_weights"),
-        ws.data_ptr(), ws.numel(), _paged_stream(stream, dev)), "dkv_paged_evict")
+    st = g.lib.dkv_paged_evict(
+        g.ref, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), lens.data_ptr(), weights.data_ptr(), budget,
+        first, recent, new_table.data_ptr(), width, kept.data_ptr(), new_lens.data_ptr(), new_weights.data_ptr(),
+        ws.data_ptr(), ws.numel(), torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st, "dkv_paged_evict")
     return kept, new_lens, new_weights
 
 
