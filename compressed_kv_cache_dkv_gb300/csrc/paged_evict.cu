@@ -1,10 +1,12 @@
 // dkv_paged_evict: keep the heaviest tokens of every (sequence, KV head) and move them
 // together.
 //
-// select: one CTA per unit brings the weights' order-preserving integer images into shared
-// memory, finds the smallest image that stays by radix selection (three passes of 11, 11 and 10
-// bits over a histogram), then writes the kept positions, ascending, from one scan that counts
-// certain and equal images side by side.  Bound by the latency of its passes.
+// select: a unit's tokens are split over a cluster of CTAs (one CTA up to kSelStage tokens of
+// capacity, kSelCluster beyond).  They bring the weights' order-preserving integer images into
+// shared memory, find the smallest image that stays by radix selection (three passes of 11, 11
+// and 10 bits over histograms that every CTA adds up from all of them through distributed shared
+// memory), then write the kept positions, ascending, from one scan that counts certain and equal
+// images side by side.  Bound by the latency of its passes.
 //
 // move: a gather of budget rows of K and V per unit, bound by memory (each kept row read and
 // written once).  A CTA moves one chunk of kMoveBytes of K and as much of V, whole rows, all of
@@ -21,7 +23,8 @@ namespace {
 
 constexpr int kSelThreads = 1024, kSelBins = 2048;
 constexpr int kSelPer = 8;                        // consecutive tokens of a thread in the ordered pass
-constexpr int kSelStage = 24 * 1024;              // images held in shared memory (two CTAs fit a multiprocessor)
+constexpr int kSelStage = 24 * 1024;              // images a CTA holds in shared memory (two CTAs fit a multiprocessor)
+constexpr int kSelCluster = 8;
 constexpr int kMoveThreads = 256, kMoveVec = 2;   // 16-byte pieces of K, and as many of V, per thread
 constexpr int kMoveBytes = kMoveThreads * kMoveVec * 16;
 constexpr int kZeroChunk = 8192;                  // weights zeroed by one CTA
@@ -51,35 +54,48 @@ __host__ __device__ inline EvictPlan evict_plan(int B, int Hkv, int cap, int d, 
   return p;
 }
 
+__device__ inline int ld_cluster_s32(const void* local, uint32_t rank) {
+  uint32_t remote;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
+  return v;
+}
+
+template <int CL>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(PagedArgs a, PagedEvict e, EvictPlan plan,
                                                                   uint8_t* __restrict__ ws) {
-  extern __shared__ __align__(16) uint32_t img[];  // images of the unit's weights (when they fit)
+  extern __shared__ __align__(16) uint32_t img[];  // images of this CTA's weights (when they fit)
   __shared__ int hist[kSelBins];
   __shared__ int wsum[32];
   __shared__ int sh_digit, sh_above;
-  const int u = blockIdx.x, b = u / a.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = CL > 1 ? (int)cluster_ctarank() : 0;
+  const int u = blockIdx.x / CL, b = u / a.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_launch();
   const int len = paged_len(a, b), n = min(len, e.budget);
   int32_t* kept = e.kept + (size_t)u * e.budget;
   // what the move kernel starts from
-  if (u % a.Hkv == 0 && tid == 0) reinterpret_cast<int32_t*>(ws + kWsHeader)[b] = n;
-  if (u == 0 && tid == 0) *reinterpret_cast<uint32_t*>(ws + plan.off_ticket) = 0;
+  if (u % a.Hkv == 0 && rank == 0 && tid == 0) reinterpret_cast<int32_t*>(ws + kWsHeader)[b] = n;
+  if (blockIdx.x == 0 && tid == 0) *reinterpret_cast<uint32_t*>(ws + plan.off_ticket) = 0;
   uint32_t* flags = reinterpret_cast<uint32_t*>(ws + plan.off_flags) + (size_t)u * plan.chunks;
-  for (int i = tid; i < plan.chunks; i += kSelThreads) flags[i] = 0;
-  for (int j = n + tid; j < e.budget; j += kSelThreads) kept[j] = -1;
-  if (len <= e.budget) {
-    for (int j = tid; j < n; j += kSelThreads) kept[j] = j;
+  const int all = CL * kSelThreads, me = rank * kSelThreads + tid;
+  for (int i = me; i < plan.chunks; i += all) flags[i] = 0;
+  for (int j = n + me; j < e.budget; j += all) kept[j] = -1;
+  if (len <= e.budget) {  // the same answer in every CTA of a cluster
+    for (int j = me; j < n; j += all) kept[j] = j;
     return;
   }
   // candidates [c0, c1); the tokens around them stay whatever they weigh
   const int c0 = e.first, c1 = len - e.recent;
+  // this CTA's tokens
+  const int share = (len + CL - 1) / CL, t0 = min(rank * share, len), t1 = min(t0 + share, len);
   const float* w = e.weights + (size_t)u * a.cap;
-  const bool staged = len <= kSelStage;
+  const bool staged = share <= kSelStage;
   if (staged) {
-    for (int t = tid; t < len; t += kSelThreads) img[t] = weight_image(__ldg(w + t));
+    for (int t = t0 + tid; t < t1; t += kSelThreads) img[t - t0] = weight_image(__ldg(w + t));
     __syncthreads();
   }
-  auto image = [&](int t) { return staged ? img[t] : weight_image(__ldg(w + t)); };
+  auto image = [&](int t) { return staged ? img[t - t0] : weight_image(__ldg(w + t)); };
   int k = e.budget - e.first - e.recent;  // candidates to keep: 0 <= k < c1 - c0
   uint32_t thr = 0xffffffffu, mask = 0;   // the smallest image that stays (none above it when k is 0)
   if (k > 0) {
@@ -90,16 +106,24 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(PagedArgs a, 
       const int bins = 1 << bits[p];
       for (int i = tid; i < bins; i += kSelThreads) hist[i] = 0;
       __syncthreads();
-      for (int t = c0 + tid; t < c1; t += kSelThreads) {
+      for (int t = max(c0, t0) + tid; t < min(c1, t1); t += kSelThreads) {
         const uint32_t x = image(t);
         if ((x & mask) == thr) atomicAdd(&hist[(x >> shift[p]) & (bins - 1)], 1);
       }
-      __syncthreads();
+      if (CL > 1) cluster_sync();
+      else __syncthreads();
       // the digit with fewer than k images above it and at least k down to it: thread i takes the
       // i-th group of bins from the top
       const int per = bins / kSelThreads, top = bins - 1 - tid * per;
-      int sum = 0;
-      for (int i = 0; i < per; ++i) sum += hist[top - i];
+      int cnt[2] = {0, 0};
+      for (int i = 0; i < per; ++i) {
+        if (CL == 1) cnt[i] = hist[top - i];
+        else {
+#pragma unroll
+          for (int r = 0; r < CL; ++r) cnt[i] += ld_cluster_s32(&hist[top - i], r);
+        }
+      }
+      const int sum = cnt[0] + cnt[1];
       int scan = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -107,14 +131,14 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(PagedArgs a, 
         if (lane >= o) scan += y;
       }
       if (lane == 31) wsum[warp] = scan;
-      __syncthreads();
-      int before = lane < warp ? wsum[lane] : 0;
-      int above = scan - sum + __reduce_add_sync(0xffffffffu, before);
+      if (CL > 1) cluster_sync();  // (the histograms are read)
+      else __syncthreads();
+      const int before = lane < warp ? wsum[lane] : 0;
+      const int above = scan - sum + __reduce_add_sync(0xffffffffu, before);
       if (above < k && above + sum >= k) {
-        int i = 0;
-        while (above + hist[top - i] < k) above += hist[top - i++];
-        sh_digit = top - i;
-        sh_above = above;
+        const int second = above + cnt[0] < k;
+        sh_digit = top - second;
+        sh_above = above + (second ? cnt[0] : 0);
       }
       __syncthreads();
       thr |= (uint32_t)sh_digit << shift[p];
@@ -123,22 +147,48 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(PagedArgs a, 
       __syncthreads();
     }
   }
-  // every image above thr stays, and the first k that equal it
-  int out = 0, ties = 0;  // certain and equal images of the chunks before
-  for (int base = 0; base < len; base += kSelThreads * kSelPer) {
-    const int t0 = base + tid * kSelPer;
-    uint32_t keep = 0, tie = 0;  // bits of this thread's tokens
+  // every image above thr stays, and the first k that equal it.  Tokens of this thread: bits of the
+  // certain ones and of the equal ones among t .. t + kSelPer - 1
+  auto look = [&](int t, uint32_t& keep, uint32_t& tie) {
+    keep = tie = 0;
 #pragma unroll
     for (int i = 0; i < kSelPer; ++i) {
-      const int t = t0 + i;
-      if (t >= len) continue;
-      if (t < c0 || t >= c1) keep |= 1u << i;
+      if (t + i >= t1) continue;
+      if (t + i < c0 || t + i >= c1) keep |= 1u << i;
       else {
-        const uint32_t x = image(t);
+        const uint32_t x = image(t + i);
         keep |= (x > thr ? 1u : 0u) << i;
         tie |= (x == thr ? 1u : 0u) << i;
       }
     }
+  };
+  int out = 0, ties = 0;  // certain and equal images before this CTA's tokens, then before the chunk
+  if (CL > 1) {
+    int mk = 0, mt = 0;
+    for (int base = t0; base < t1; base += kSelThreads * kSelPer) {
+      uint32_t keep, tie;
+      look(base + tid * kSelPer, keep, tie);
+      mk += __popc(keep);
+      mt += __popc(tie);
+    }
+    mk = __reduce_add_sync(0xffffffffu, mk);
+    mt = __reduce_add_sync(0xffffffffu, mt);
+    if (tid < 2) hist[tid] = 0;
+    __syncthreads();
+    if (lane == 0) {
+      atomicAdd(&hist[0], mk);
+      atomicAdd(&hist[1], mt);
+    }
+    cluster_sync();
+    for (int r = 0; r < rank; ++r) {
+      out += ld_cluster_s32(&hist[0], r);
+      ties += ld_cluster_s32(&hist[1], r);
+    }
+  }
+  for (int base = t0; base < t1; base += kSelThreads * kSelPer) {
+    const int t = base + tid * kSelPer;
+    uint32_t keep, tie;
+    look(t, keep, tie);
     // both counts in one scan (a chunk has kSelThreads * kSelPer = 2^13 tokens at most)
     const int v = __popc(keep) | __popc(tie) << 16;
     int s = v;
@@ -150,20 +200,21 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(PagedArgs a, 
     if (lane == 31) wsum[warp] = s;
     __syncthreads();
     const int part = wsum[lane];
-    const int all = __reduce_add_sync(0xffffffffu, part);
+    const int chunk = __reduce_add_sync(0xffffffffu, part);
     const int before = s - v + __reduce_add_sync(0xffffffffu, lane < warp ? part : 0);
     int nk = out + (before & 0xffff), nt = ties + (before >> 16);
 #pragma unroll
     for (int i = 0; i < kSelPer; ++i) {
       const bool kp = keep >> i & 1u, te = tie >> i & 1u;
-      if (kp || (te && nt < k)) kept[nk + min(nt, k)] = t0 + i;
+      if (kp || (te && nt < k)) kept[nk + min(nt, k)] = t + i;
       nk += kp;
       nt += te;
     }
-    out += all & 0xffff;
-    ties += all >> 16;
+    out += chunk & 0xffff;
+    ties += chunk >> 16;
     __syncthreads();
   }
+  if (CL > 1) cluster_sync();  // nobody leaves while another reads its counts
 }
 
 template <int D>
@@ -262,10 +313,22 @@ cudaError_t launch_paged_evict(const PagedArgs& a, int d, const PagedEvict& e, v
   const int units = a.B * a.Hkv;
   const EvictPlan plan = evict_plan(a.B, a.Hkv, a.cap, d, e.budget);
   const size_t smem = (size_t)(a.cap < kSelStage ? a.cap : kSelStage) * 4;
-  cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(evict_select_kernel), smem);
+  const bool wide = a.cap > kSelStage;
+  const auto select = wide ? evict_select_kernel<kSelCluster> : evict_select_kernel<1>;
+  cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(select), smem);
   if (err != cudaSuccess) return err;
-  evict_select_kernel<<<units, kSelThreads, smem, s>>>(a, e, plan, ws);
-  if ((err = cudaGetLastError()) != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(units * (wide ? kSelCluster : 1));
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kSelCluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = wide ? 1 : 0;
+  if ((err = cudaLaunchKernelEx(&cfg, select, a, e, plan, ws)) != cudaSuccess) return err;
   return launch_dependent(d == 128 ? evict_move_kernel<128> : evict_move_kernel<64>,
                           dim3((unsigned)units * (plan.chunks + plan.zeros)), kMoveThreads, 0, s, a, e, plan,
                           static_cast<uint4*>(k_pool), static_cast<uint4*>(v_pool), ws);

@@ -354,6 +354,26 @@ def test_evict(dtype, d, hkv, page, order, lens, budget, first, recent, in_place
     _evict_check(c, p, weights, budget, first, recent, kept.cpu(), new_lens.cpu(), new_weights, to, k, v)
 
 
+@pytest.mark.parametrize("lens,budget,kind", [([40000, 30001, 25], 20000, "spread"), ([33333], 30000, "ties"), ([24577], 3, "ties"),
+                                              ([210000], 100000, "spread")])
+def test_evict_of_long_sequences(lens, budget, kind):
+    """Capacities past what one block of threads holds; the last one past what all of them hold."""
+    page = 256
+    width = max(-(-n // page) for n in lens)
+    c = R.Cache(lens, 1, 64, page, "bf16", seed=budget, width=width)
+    p = c.layout(2)
+    ws = workspace(p)
+    g = torch.Generator().manual_seed(6)
+    weights = torch.rand(c.B, 1, width * page, generator=g)
+    if kind == "ties":
+        weights = torch.tensor([0.0, 1.0, 2.0, math.nan])[torch.randint(0, 4, weights.shape, generator=g)]
+    lens_d, w_d, k, v, table = c.dev(lens), weights.cuda(), c.k.clone(), c.v.clone(), c.table.cuda()
+    kept, new_lens, new_weights = dkv.dkv_paged_evict(p, c.k, c.v, table, lens_d, w_d, budget, 1, 1, table, new_lens=lens_d,
+                                                      new_weights=w_d, workspace=ws)
+    no_fault(ws)
+    _evict_check(c, p, weights, budget, 1, 1, kept.cpu(), new_lens.cpu(), new_weights, c.table, k, v)
+
+
 # ---------------------------------------------------------------- together
 
 def test_a_serving_run():
