@@ -209,6 +209,18 @@ PREFILL = [
     ("fp16", 128, 4, 1, 16, "head", [1200], None, 260, 1, 1),
     ("bf16", 128, 2, 2, 64, "token", [640], None, 640, 300, 300),
     ("fp16", 64, 6, 3, 32, "token", [20, 300], [50, 50], 50, 40, 2),   # sequence 0: 30 queries before its first token
+    # few queries over many keys: several heads to a row group, the keys cut into parts
+    ("bf16", 128, 8, 1, 16, "token", [5000, 1700, 0, 130], [8, 3, 0, 8], 8, 0, 0),
+    ("fp16", 64, 7, 1, 64, "head", [4000], None, 16, 300, 4),
+    ("bf16", 128, 6, 2, 32, "head", [2500, 900], [64, 40], 64, 0, 0),
+    ("fp16", 128, 3, 1, 128, "token", [1111], None, 50, 0, 0),
+    ("bf16", 64, 5, 1, 256, "head", [2049, 64], [9, 1], 9, 1000, 100),
+    ("fp16", 128, 4, 4, 64, "head", [1500], None, 1, 0, 0),
+    ("bf16", 128, 4, 1, 64, "head", [2300], None, 100, 0, 0),
+    ("fp16", 64, 16, 2, 16, "token", [700, 690], None, 33, 128, 64),
+    # many tiles: the rings go round
+    ("bf16", 64, 2, 1, 64, "head", [4500], None, 4500, 0, 0),
+    ("fp16", 128, 3, 1, 16, "token", [2600], None, 2600, 1500, 3),
 ]
 
 
@@ -279,6 +291,32 @@ def test_prefill_rows_are_not_touched_by_keys_they_do_not_see(dtype, d, hq, wind
     assert bool(torch.isnan(out[0][:, only_v][..., 0::2]).all())
     assert not bool(torch.isfinite(out[0][:, only_v][..., 1::2]).any())
     assert bool(torch.isfinite(lse[0][:, only_v]).all())
+
+
+def test_few_queries_are_not_touched_by_keys_they_do_not_see():
+    """The same where the keys are cut into parts and joined."""
+    n, Tq, d = 3001, 6, 128
+    c = R.Cache([n], 1, d, 64, "bf16", seed=21)
+    p = c.layout(4, window=2000, sinks=10)
+    q = queries((1, 4, Tq, d), c.dt, 5)
+    v = c.v.clone()
+    for t, x in ((9, "nan"), (10, "nan"), (995, "inf"), (n - 3, "nan"), (n - 1, "inf")):
+        v[int(c.table[0, t // 64]), 0, t % 64, :64] = float(x)
+    out, lse = dkv.dkv_paged_prefill(p, q.cuda(), c.k, v, c.table.cuda(), c.dev([n]))
+    pos = torch.arange(n - Tq, n)
+    m = R.seen(pos, n, 2000, 10)
+    # token 9 is a sink; the first row, at 2995, sees tokens from 2995 - 2000 + 1 = 996 on, so that none sees 995
+    assert bool(m[:, 9].all()) and not bool(m[:, 10].any()) and not bool(m[:, 995].any())
+    V = c.V[0][0].clone()
+    for j in range(4):
+        ref = R.attend(q[0, j].double(), c.K[0][0], V, pos, 2000, 10)
+        assert bool(torch.isnan(out[0, j, :, :64]).all())
+        sub = (ref[0][:, 64:], ref[1], ref[2], ref[3][:, 64:], ref[4])
+        R.check_rows(out[0, j][:, 64:], lse[0, j], sub, d, c.dt, torch.finfo(c.dt).eps / 2)
+    v[int(c.table[0, 0]), 0, 9] = 1.0  # now the first rows are free of NaN, the last three are not
+    out, _ = dkv.dkv_paged_prefill(p, q.cuda(), c.k, v, c.table.cuda(), c.dev([n]))
+    assert bool(torch.isfinite(out[0, :, :Tq - 3]).all()) and bool(torch.isnan(out[0, :, Tq - 3:, :64]).all())
+    assert bool(torch.isfinite(out[0, :, :, 64:]).all())
 
 
 def test_prefill_adds_large_values_of_edge_tiles_exactly():
@@ -500,6 +538,120 @@ def test_calls_in_a_graph_and_on_a_stream_of_their_own():
     fresh, _ = dkv.dkv_paged_decode(p, q, c.k, c.v, table, lens)
     assert torch.equal(out, fresh) and not torch.equal(out, want[0])
     no_fault(ws)
+
+
+def test_pools_that_interleave_keys_and_values():
+    c = R.Cache([333, 64], 2, 64, 32, "bf16", seed=30)
+    both = torch.empty(c.n_pages, 2, 2, 32, 64, dtype=c.dt, device="cuda")
+    both[:, 0], both[:, 1] = c.k, c.v
+    k, v = both[:, 0], both[:, 1]
+    p = dkv.dkv_paged_layout(k, 2, 6, c.width)
+    q, table, lens = queries((2, 6, 64), c.dt, 1).cuda(), c.table.cuda(), c.dev(c.lens)
+    out, lse = dkv.dkv_paged_decode(p, q, k, v, table, lens)
+    want, want_lse = dkv.dkv_paged_decode(c.layout(6), q, c.k, c.v, table, lens)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    qp = queries((2, 6, 20, 64), c.dt, 2).cuda()
+    out, _ = dkv.dkv_paged_prefill(p, qp, k, v, table, lens)
+    want, _ = dkv.dkv_paged_prefill(c.layout(6), qp, c.k, c.v, table, lens)
+    assert torch.equal(out, want)
+    new = queries((2, 2, 3, 64), c.dt, 3).cuda()
+    dkv.dkv_paged_append(p, new, new + 1, k, v, table, c.dev([40, 7]))
+    assert torch.equal(k[int(c.table[0, 1]), :, 8:11], new[0]) and torch.equal(v[int(c.table[1, 0]), :, 7:10], new[1] + 1)
+
+
+def test_runs_are_alike_and_two_streams_do_not_meet():
+    """The same bits every time; two calls at once, each with its workspace, give what they give alone."""
+    c = R.Cache([3000, 2000, 100], 2, 128, 64, "bf16", seed=31)
+    p = c.layout(8, window=1500, sinks=4)
+    table, lens = c.table.cuda(), c.dev(c.lens)
+    qs = [queries((3, 8, 128), c.dt, s).cuda() for s in (1, 2)]
+    qp = [queries((3, 8, 50, 128), c.dt, s).cuda() for s in (3, 4)]
+
+    def run(i, ws):
+        w = torch.zeros(3, 2, c.width * 64, device="cuda")
+        o, l = dkv.dkv_paged_decode(p, qs[i], c.k, c.v, table, lens, weights=w, workspace=ws)
+        po, pl = dkv.dkv_paged_prefill(p, qp[i], c.k, c.v, table, lens, workspace=ws)
+        dkv.dkv_paged_weights(p, qp[i], pl, c.k, table, lens, w, workspace=ws)
+        return o, l, po, pl, w
+
+    alone = [run(i, workspace(p, True)) for i in range(2)]
+    torch.cuda.synchronize()
+    streams, spaces = [torch.cuda.Stream() for _ in range(2)], [workspace(p, True) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [None, None]
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i] = run(i, spaces[i])
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_nothing_to_do():
+    c = R.Cache([0, 0], 1, 64, 16, seed=32, width=2)
+    p = c.layout(2)
+    q = queries((2, 2, 64), c.dt, 1).cuda()
+    table, lens = c.table.cuda(), c.dev([0, 0])
+    weights = torch.ones(2, 1, 32, device="cuda")
+    out, lse = dkv.dkv_paged_decode(p, q, c.k, c.v, table, lens, weights=weights)
+    assert bool((out == 0).all()) and bool(torch.isneginf(lse).all()) and bool((weights == 1).all())
+    qp = queries((2, 2, 5, 64), c.dt, 1).cuda()
+    out, lse = dkv.dkv_paged_prefill(p, qp, c.k, c.v, table, lens)  # five queries before the first token
+    assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+    dkv.dkv_paged_weights(p, qp, lse, c.k, table, lens, weights)
+    assert bool((weights == 1).all())
+    none = qp[:, :, :0]
+    out, lse = dkv.dkv_paged_prefill(p, none, c.k, c.v, table, lens)
+    assert out.shape == (2, 2, 0, 64) and lse.shape == (2, 2, 0)
+    dkv.dkv_paged_append(p, none[:, :1], none[:, :1], c.k, c.v, table, lens)
+    kept, new_lens, new_weights = dkv.dkv_paged_evict(p, c.k, c.v, table, lens, weights, 8, 1, 2, table)
+    assert bool((kept == -1).all()) and bool((new_lens == 0).all()) and bool((new_weights == 0).all())
+
+
+def test_tensors_that_do_not_fit_are_refused():
+    c = R.Cache([100], 2, 64, 16, seed=33)
+    p = c.layout(4)
+    table, lens = c.table.cuda(), c.dev([100])
+    q = queries((1, 4, 64), c.dt, 1).cuda()
+    ok = dict(q=q, k_pages=c.k, v_pages=c.v, page_table=table, lens=lens)
+    for change in (dict(q=q.bfloat16()), dict(q=q[:, :3]), dict(q=q.cpu()), dict(lens=lens.long()), dict(lens=lens.cpu()),
+                   dict(page_table=table[:, :-1]), dict(k_pages=c.k[:-1]), dict(v_pages=c.v.float()),
+                   dict(v_pages=c.v.transpose(1, 2).contiguous().transpose(1, 2)), dict(out=q.float()),
+                   dict(lse=torch.zeros(1, 3, device="cuda")), dict(weights=torch.zeros(1, 2, 5, device="cuda")),
+                   dict(q=queries((1, 64, 4), c.dt, 1).cuda().transpose(1, 2)),
+                   dict(workspace=torch.zeros(1 << 25, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            dkv.dkv_paged_decode(p, **(ok | change))
+    wide = queries((1, 1, 64), c.dt, 1).cuda().expand(1, 4, 64)  # one row for four heads: stride 0
+    with pytest.raises(dkv.DkvError) as e:
+        dkv.dkv_paged_decode(p, **(ok | dict(q=wide)))
+    assert e.value.status == dkv.DKV_ERR_ALIGN
+    with pytest.raises(dkv.DkvError) as e:
+        dkv.dkv_paged_decode(p, **ok, workspace=torch.zeros(512, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == dkv.DKV_ERR_WORKSPACE
+    with pytest.raises(dkv.DkvError) as e:
+        dkv.dkv_paged_evict(p, c.k, c.v, table, lens, torch.zeros(1, 2, c.width * 16, device="cuda"), 10, 6, 5, table)
+    assert e.value.status == dkv.DKV_ERR_SHAPE
+
+
+def test_eviction_to_a_page_that_is_not_there():
+    c = R.Cache([100], 1, 64, 16, seed=34, spare=3)
+    p = c.layout(1)
+    ws = workspace(p)
+    to = torch.tensor([[int(c.free[0]), c.n_pages, int(c.free[1])]], dtype=torch.int32, device="cuda")
+    w = torch.rand(1, 1, c.width * 16, device="cuda")
+    k, v = c.k.clone(), c.v.clone()
+    kept, new_lens, _ = dkv.dkv_paged_evict(p, c.k, c.v, c.table.cuda(), c.dev([100]), w, 40, 0, 0, to, workspace=ws)
+    assert dkv.dkv_get_error(ws) == (dkv.DKV_ERR_DEVICE, dkv.DKV_DEVERR_INDEX)
+    want = R.evict(w[0, 0, :100].tolist(), 100, 40, 0, 0)
+    assert kept[0, 0].tolist() == want and int(new_lens[0]) == 40
+    for j, t in enumerate(want):
+        if not 16 <= j < 32:
+            got = c.k[int(to[0, j // 16]), 0, j % 16]
+            assert torch.equal(got, k[int(c.table[0, t // 16]), 0, t % 16])
+    changed = (c.v.view(torch.int16) != v.view(torch.int16)).any(-1).any(-1).any(-1).nonzero().flatten().tolist()
+    assert sorted(changed) == sorted([int(c.free[0]), int(c.free[1])])
 
 
 def test_pools_past_two_to_the_31_elements():
