@@ -214,9 +214,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const uint32_t el = elect_one();
     int j = 0;
     if (nt > 0) {
-      if (el) mbar_arrive_expect_tx(q_full, (uint32_t)((hdA + hdB) * p.rows) * D * 2);
-      for (int x = 0; x < hdA + hdB; ++x) {  // a box of p.rows rows for each head (or 128-token tile)
-        const int g = x < hdA ? 0 : 1, slot = x - g * hdA;
+      const int boxesA = nA > 0 ? hdA : 0;  // (the rows of a group without a tile go out through its place meanwhile)
+      if (el) mbar_arrive_expect_tx(q_full, (uint32_t)((boxesA + hdB) * p.rows) * D * 2);
+      for (int x = 0; x < boxesA + hdB; ++x) {  // a box of p.rows rows for each head (or 128-token tile)
+        const int g = x < boxesA ? 0 : 1, slot = x - g * boxesA;
 #pragma unroll
         for (int hf = 0; hf < D / 64; ++hf)
           tma_load_4d(sb + g * S::kQ + hf * kPfM * 128 + slot * p.rows * 128, &qmap, hf * 64, p.by_heads ? row0 : row0 + g * kPfM,

@@ -93,7 +93,7 @@ __device__ inline int wt_page(const PagedArgs& a, int b, int len, int k_lo, int 
 template <int D>
 __device__ inline void wt_load_keys(const PagedArgs& a, const CUtensorMap* kmap, int h, int k0, int rows, int page, uint32_t to,
                                     uint64_t* bar, uint32_t el) {
-#pragma unroll 2
+#pragma unroll 4
   for (int i = 0; i < kWtM / rows; ++i) {
     const int pg = __shfl_sync(0xffffffffu, page, i);
 #pragma unroll

@@ -209,6 +209,9 @@ PREFILL = [
     ("fp16", 128, 4, 1, 16, "head", [1200], None, 260, 1, 1),
     ("bf16", 128, 2, 2, 64, "token", [640], None, 640, 300, 300),
     ("fp16", 64, 6, 3, 32, "token", [20, 300], [50, 50], 50, 40, 2),   # sequence 0: 30 queries before its first token
+    # the first 128 rows of a 256-row block lie before the first token, the others do not
+    ("bf16", 128, 1, 1, 64, "head", [100, 40, 300], [256, 200, 256], 256, 0, 0),
+    ("fp16", 64, 3, 1, 16, "token", [1], None, 600, 30, 1),
     # few queries over many keys: several heads to a row group, the keys cut into parts
     ("bf16", 128, 8, 1, 16, "token", [5000, 1700, 0, 130], [8, 3, 0, 8], 8, 0, 0),
     ("fp16", 64, 7, 1, 64, "head", [4000], None, 16, 300, 4),
