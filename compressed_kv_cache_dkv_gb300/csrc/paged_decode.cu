@@ -29,7 +29,8 @@ constexpr int kDecTile = 64, kDecStages = 4, kDecConsumers = 8;
 static_assert(kDecStages % 2 == 0, "two teams take the stages in turn");
 constexpr int kDecThreads = 32 * (kDecConsumers + 1);
 constexpr int kCombThreads = 512, kCombCols = 32;  // combine: channels per CTA
-constexpr int kScoreThreads = 256, kScorePer = 8;
+constexpr int kScoreThreads = 256, kScoreBatch = 8, kScoreTokens = 2048;
+static_assert(kScoreTokens % (kScoreBatch * kScoreThreads / 2) == 0, "whole rounds");
 
 template <int D>
 constexpr int rec_floats() { return 16 + 8 * D; }
@@ -341,29 +342,46 @@ __global__ void __launch_bounds__(kCombThreads) paged_combine_kernel(DecArgs p, 
 }
 
 // weights[unit][t] += sum over the group's heads of 2^(score - lse), from the scores the decode
-// kernel left: 32 bytes a token beside the 4 d of its key and value.
+// kernel left: 32 bytes a token beside the 4 d of its key and value.  Two neighbouring threads take
+// the two halves of a token's scores, so that a warp reads whole lines; kScoreBatch of them in flight.
 __global__ void __launch_bounds__(kScoreThreads) paged_score_kernel(DecArgs p, float* __restrict__ weights) {
   const PagedArgs& a = p.a;
   griddep_wait();
   const int u = blockIdx.y, b = u / a.Hkv, h = u % a.Hkv, len = paged_len(a, b), lo = paged_window_lo(a, len - 1);
-  const int t0 = blockIdx.x * (kScoreThreads * kScorePer) + threadIdx.x;
-  if (blockIdx.x * (kScoreThreads * kScorePer) >= len) return;
-  float l2[8];
+  const int first = blockIdx.x * kScoreTokens;
+  if (first >= len) return;
+  const int half = threadIdx.x & 1, g0 = 4 * half;
+  float l2[4];
 #pragma unroll
-  for (int g = 0; g < 8; ++g)
-    l2[g] = g < a.G ? __ldcg(p.lse + (size_t)b * a.Hq + h * a.G + g) * 1.4426950408889634f : INFINITY;
+  for (int g = 0; g < 4; ++g) {
+    const float l = g0 + g < a.G ? __ldcg(p.lse + (size_t)b * a.Hq + h * a.G + g0 + g) * 1.4426950408889634f : -INFINITY;
+    l2[g] = l == -INFINITY ? INFINITY : l;  // (a head without a weight, or none: adds 0)
+  }
+  float* wu = weights + (size_t)u * a.cap;
+#pragma unroll 1
+  for (int base = first + (threadIdx.x >> 5) * 16; base < min(first + kScoreTokens, len); base += kScoreBatch * kScoreThreads / 2) {
+    const int t0 = base + ((threadIdx.x & 31) >> 1);  // (base is the warp's: its lanes go round together)
+    float4 s[kScoreBatch];
+    float old[kScoreBatch];
+    bool sees[kScoreBatch];
 #pragma unroll
-  for (int x = 0; x < kScorePer; ++x) {
-    const int t = t0 + x * kScoreThreads;
-    if (t >= len || (t < lo && t >= a.sinks)) continue;
-    const float4* s = reinterpret_cast<const float4*>(p.scores + ((size_t)u * a.cap + t) * 8);
-    const float4 s0 = __ldcs(s), s1 = __ldcs(s + 1);
-    const float v[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-    float w = 0.f;
+    for (int x = 0; x < kScoreBatch; ++x) {
+      const int t = t0 + x * kScoreThreads / 2;
+      sees[x] = t < len && (t >= lo || t < a.sinks);
+      s[x] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (sees[x] && g0 < a.G) s[x] = __ldcs(reinterpret_cast<const float4*>(p.scores + ((size_t)u * a.cap + t) * 8 + g0));
+      old[x] = sees[x] && half == 0 ? __ldcg(wu + t) : 0.f;
+    }
 #pragma unroll
-    for (int g = 0; g < 8; ++g)
-      if (g < a.G && l2[g] != -INFINITY) w += fast_exp2(v[g] - l2[g]);
-    weights[(size_t)u * a.cap + t] += w;
+    for (int x = 0; x < kScoreBatch; ++x) {
+      const float v[4] = {s[x].x, s[x].y, s[x].z, s[x].w};
+      float w = 0.f;
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        if (g0 + g < a.G) w += fast_exp2(v[g] - l2[g]);
+      w += __shfl_xor_sync(0xffffffffu, w, 1);
+      if (sees[x] && half == 0) wu[t0 + x * kScoreThreads / 2] = old[x] + w;
+    }
   }
 }
 
@@ -379,8 +397,7 @@ cudaError_t launch_decode_td(const DecArgs& p, const PagedMaps& m, float* weight
   e = launch_dependent(paged_combine_kernel<T, D>, dim3(ncta, D / kCombCols), kCombThreads,
                  ((size_t)p.a.B + 1 + 8 * ncta + 16) * 4, s, p, ncta);
   if (e != cudaSuccess || !weights) return e;
-  const int per = kScoreThreads * kScorePer;
-  return launch_dependent(paged_score_kernel, dim3((p.a.cap + per - 1) / per, p.a.B * p.a.Hkv), kScoreThreads, 0, s, p, weights);
+  return launch_dependent(paged_score_kernel, dim3((p.a.cap + kScoreTokens - 1) / kScoreTokens, p.a.B * p.a.Hkv), kScoreThreads, 0, s, p, weights);
 }
 
 }  // namespace
