@@ -32,6 +32,14 @@ constexpr int kCombThreads = 512, kCombCols = 32;  // combine: channels per CTA
 constexpr int kScoreThreads = 256, kScoreBatch = 8, kScoreTokens = 2048;
 static_assert(kScoreTokens % (kScoreBatch * kScoreThreads / 2) == 0, "whole rounds");
 
+// p, its sums and so o carry a factor 2^kDecShift.  A fp16 value below 2^-25 would be lost, and a long
+// cache can hold tens of thousands of such weights beside one of 1: with the factor, and the low half
+// behind the high one, weights down to e^-18 of the largest keep 11 bits and those to e^-27 count.
+template <typename T>
+constexpr float kDecShift = 0.f;
+template <>
+constexpr float kDecShift<__half> = 14.f;
+
 template <int D>
 constexpr int rec_floats() { return 16 + 8 * D; }
 
@@ -206,8 +214,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       const float f0 = fast_exp2(m0 - ms0), f1 = fast_exp2(m1 - ms1);
       m0 = n0;
       m1 = n1;
-      const float p0 = fast_exp2(sc[0] - ms0), p1 = fast_exp2(sc[1] - ms1);
-      const float p2 = fast_exp2(sc[2] - ms0), p3 = fast_exp2(sc[3] - ms1);
+      const float s0 = ms0 - kDecShift<T>, s1 = ms1 - kDecShift<T>;
+      const float p0 = fast_exp2(sc[0] - s0), p1 = fast_exp2(sc[1] - s1);
+      const float p2 = fast_exp2(sc[2] - s0), p3 = fast_exp2(sc[3] - s1);
       l0 = l0 * f0 + (p0 + p2);
       l1 = l1 * f1 + (p1 + p3);
       if (__any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f)) {
@@ -276,7 +285,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           rec[gg] = M;
           rec[8 + gg] = L;
         } else if (gg < a.G && p.lse) {
-          p.lse[head] = (M + log2f(L)) * 0.6931471805599453f;
+          p.lse[head] = (M - kDecShift<T> + log2f(L)) * 0.6931471805599453f;
         }
       }
     }
@@ -337,7 +346,7 @@ __global__ void __launch_bounds__(kCombThreads) paged_combine_kernel(DecArgs p, 
     const float L = red[8 + gg], inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
     const size_t head = (size_t)g.b * a.Hq + g.h * a.G + gg;
     static_cast<T*>(p.out)[head * D + dd] = Num<T>::from_float(v * inv);
-    if (p.lse && dd == 0) p.lse[head] = (red[gg] + log2f(L)) * 0.6931471805599453f;
+    if (p.lse && dd == 0) p.lse[head] = (red[gg] - kDecShift<T> + log2f(L)) * 0.6931471805599453f;
   }
 }
 

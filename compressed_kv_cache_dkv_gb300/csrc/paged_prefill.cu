@@ -20,8 +20,10 @@
 //
 // P is rounded once to the type of V.  The output is rounded to that type too, and the error of
 // p enters it with about the same size: sqrt(2) of the unavoidable error instead of twice the
-// work for P V.  For fp16 p is scaled by 2^7 first, which keeps weights down to e^-14 of the
-// largest normal; the scale cancels in the division.
+// work for P V.  For fp16 p is scaled by 2^7 first (2^15 with the slack): weights down to e^-14 of
+// the largest keep 11 bits and smaller ones are off by 2^-32 of it at most, 2^-12 for all of the longest
+// cache's tokens together; the scale cancels in the division.  (A slack of 4 and a scale of 2^11 would
+// give them four bits more: 141 us instead of 137 for a 16k prompt under a window of 1024, 12 heads.)
 //
 // Tiles in which some row sees a key that another does not (the diagonal, the window's edge, the
 // sinks' end) go past warp 11 first: it zeroes the V rows that no row of the CTA sees, and, since

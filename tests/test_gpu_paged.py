@@ -681,3 +681,37 @@ def test_pools_past_two_to_the_31_elements():
                          d, torch.float16, 2.0 ** -21)
             R.check_rows(po[b, h], pl[b, h], R.attend(qp[b, h].double(), K, V, torch.arange(lens[b] - 5, lens[b]), 0, 0),
                          d, torch.float16, 2.0 ** -11)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_many_small_weights_beside_a_large_one_count(dtype):
+    """Token 0 scores 18, every other one 0: weights of e^-18, which a half of its own cannot hold, and
+    only they have values in the upper channels."""
+    n, d, hkv = 2048, 64, 8
+    c = R.Cache([n] * 4, hkv, d, 64, dtype, seed=2)
+    K, V = torch.zeros(n, d, dtype=torch.float64), torch.zeros(n, d, dtype=torch.float64)
+    K[0, 0] = 18.0
+    V[0, :32] = 1.0
+    V[1:, 32:] = 1000.0
+    t = torch.arange(n)
+    for b in range(c.B):
+        for pool, rows in ((c.k, K), (c.v, V)):
+            pool[c.table[b].long()[t // 64].cuda(), :, (t % 64).cuda()] = rows.to(c.dt).cuda()[:, None]
+    q = torch.zeros(c.B, hkv, n, d, dtype=c.dt)
+    q[..., 0] = 8.0  # 1 / c
+    p, lens = c.layout(hkv), c.dev([n] * 4)
+    V = V.to(c.dt).double()
+    ref = R.attend(q[0, 0].double(), K, V, t, 0, 0)
+    out, lse = dkv.dkv_paged_prefill(p, q.cuda(), c.k, c.v, c.table.cuda(), lens)
+    # p as one value of the pools' type: e^-18 is above 2^-26, and 2^7 p in fp16 off by half a subnormal
+    # step, 2^-25, at most: relative 2^-25 / 2^-19
+    p_eps = 2.0 ** -6 if dtype == "fp16" else torch.finfo(c.dt).eps / 2
+    for b, h in ((0, 0), (3, 7), (1, 4)):
+        R.check_rows(out[b, h], lse[b, h], ref, d, c.dt, p_eps, f"prefill {b} {h}")
+    out, lse = dkv.dkv_paged_decode(p, q[:, :, -1].cuda(), c.k, c.v, c.table.cuda(), lens)
+    last = tuple(x[-1:] for x in ref[:2]) + (ref[2],) + (ref[3][-1:],) + (ref[4],)
+    p_eps = 2.0 ** -16 if dtype == "bf16" else 2.0 ** -21
+    p_eps = max(p_eps, 2.0 ** -13)  # (the low half of 2^14 p > 2^-12 is in steps of 2^-24)
+    for b in range(c.B):
+        for h in range(hkv):
+            R.check_rows(out[b, h][None], lse[b, h][None], last, d, c.dt, p_eps, f"decode {b} {h}")
