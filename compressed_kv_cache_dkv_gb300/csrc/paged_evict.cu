@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(kMoveThreads, 8) evict_move_kernel(PagedArgs a
       raise_error(a.err, DKV_DEVERR_INDEX);
       continue;
     }
+    if (t == j && sp == dp) continue;  // it lies there already
     v[x] = v[x + kMoveVec] = make_uint4(0, 0, 0, 0);
     if (sp < a.n_pages) {
       const int64_t from = (sp * a.stride_page + h * a.stride_head + (t & a.page_mask) * a.stride_token) / 8 + tid % R;
