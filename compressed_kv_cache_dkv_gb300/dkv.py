@@ -429,6 +429,14 @@ def _elsewhere(t: torch.Tensor, dev: int) -> bool:
     return dev != torch._C._cuda_getDevice()
 
 
+def _place(dev: int, stream):
+    """The tensors' device, and the caller's stream as its current one: what a call allocates and fills
+    is then in that stream's order, and returns to that stream's memory."""
+    if stream is None:
+        return torch.cuda.device(dev)
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), device=dev))
+
+
 def _paged_ws(p: dkv_paged, workspace, dev: int, with_weights: bool = False) -> torch.Tensor:
     if workspace is not None:
         if workspace.get_device() != dev or not workspace.is_contiguous() or workspace.element_size() != 1:
@@ -464,9 +472,9 @@ def dkv_paged_append(p: dkv_paged, K_new: torch.Tensor, V_new: torch.Tensor, k_p
     """Write K_new, V_new [B, Hkv, n_new, d] (any strides with adjacent channels) into their pages: token
     i < counts[b] of sequence b at position pos[b] + i (counts None: all n_new)."""
     dev = K_new.get_device()
-    if _elsewhere(K_new, dev):
-        with torch.cuda.device(dev):
-            return dkv_paged_append(p, K_new, V_new, k_pages, v_pages, page_table, pos, counts, workspace, stream)
+    if _elsewhere(K_new, dev) or stream is not None:
+        with _place(dev, stream):
+            return dkv_paged_append(p, K_new, V_new, k_pages, v_pages, page_table, pos, counts, workspace)
     g = _geometry(p)
     if K_new.stride() != V_new.stride():
         K_new, V_new = K_new.contiguous(), V_new.contiguous()
@@ -491,7 +499,7 @@ def dkv_paged_append(p: dkv_paged, K_new: torch.Tensor, V_new: torch.Tensor, k_p
     st = g.lib.dkv_paged_append(
         g.ref, K_new.data_ptr(), V_new.data_ptr(), _strides(s[0], s[1], s[2]), n, pos.data_ptr(),
         None if counts is None else counts.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-        ws.data_ptr(), ws.numel(), torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+        ws.data_ptr(), ws.numel(), torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _check(st, "dkv_paged_append")
 
@@ -503,9 +511,9 @@ def dkv_paged_decode(p: dkv_paged, q: torch.Tensor, k_pages: torch.Tensor, v_pag
     lse fp32 [B, Hq] or None).  `weights` fp32 [B, Hkv, max_pages * page_size]: every visible token's
     softmax weight, summed over its KV head's query heads, is added."""
     dev = q.get_device()
-    if _elsewhere(q, dev):
-        with torch.cuda.device(dev):
-            return dkv_paged_decode(p, q, k_pages, v_pages, page_table, lens, out, lse, weights, workspace, stream)
+    if _elsewhere(q, dev) or stream is not None:
+        with _place(dev, stream):
+            return dkv_paged_decode(p, q, k_pages, v_pages, page_table, lens, out, lse, weights, workspace)
     g = _geometry(p)
     s = q.stride()
     if q.dtype is not g.dtype or q.shape != g.q1 or q.get_device() != dev or s[-1] != 1:
@@ -535,7 +543,7 @@ def dkv_paged_decode(p: dkv_paged, q: torch.Tensor, k_pages: torch.Tensor, v_pag
         g.ref, q.data_ptr(), _strides(s[0], s[1], 0), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
         lens.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
         None if weights is None else weights.data_ptr(), ws.data_ptr(), ws.numel(),
-        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+        torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _check(st, "dkv_paged_decode")
     return out, lse
@@ -548,9 +556,9 @@ def dkv_paged_prefill(p: dkv_paged, q: torch.Tensor, k_pages: torch.Tensor, v_pa
     lens[b] - q_lens[b] + i -> (out [B, Hq, Tq, d] in q's type, lse fp32 [B, Hq, Tq] or None).  Rows from
     q_lens[b] on are left as they were (zeros in outputs allocated here)."""
     dev = q.get_device()
-    if _elsewhere(q, dev):
-        with torch.cuda.device(dev):
-            return dkv_paged_prefill(p, q, k_pages, v_pages, page_table, lens, q_lens, out, lse, workspace, stream)
+    if _elsewhere(q, dev) or stream is not None:
+        with _place(dev, stream):
+            return dkv_paged_prefill(p, q, k_pages, v_pages, page_table, lens, q_lens, out, lse, workspace)
     g, Tq = _geometry(p), q.shape[2]
     shape = (g.batch, g.heads, Tq, g.d)
     s = q.stride()
@@ -583,7 +591,7 @@ def dkv_paged_prefill(p: dkv_paged, q: torch.Tensor, k_pages: torch.Tensor, v_pa
         g.ref, q.data_ptr(), _strides(s[0], s[1], s[2]), Tq, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
         lens.data_ptr(), None if q_lens is None else q_lens.data_ptr(), out.data_ptr(), _strides(o[0], o[1], o[2]),
         None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
-        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+        torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _check(st, "dkv_paged_prefill")
     return out, lse
@@ -595,9 +603,9 @@ def dkv_paged_weights(p: dkv_paged, q: torch.Tensor, lse: torch.Tensor, k_pages:
     """Add the softmax weights that the queries (as in dkv_paged_prefill, with the lse it gave) give every
     token, summed over queries and a KV head's query heads, to weights fp32 [B, Hkv, max_pages * page_size]."""
     dev = q.get_device()
-    if _elsewhere(q, dev):
-        with torch.cuda.device(dev):
-            return dkv_paged_weights(p, q, lse, k_pages, page_table, lens, weights, q_lens, workspace, stream)
+    if _elsewhere(q, dev) or stream is not None:
+        with _place(dev, stream):
+            return dkv_paged_weights(p, q, lse, k_pages, page_table, lens, weights, q_lens, workspace)
     g, Tq = _geometry(p), q.shape[2]
     shape = (g.batch, g.heads, Tq, g.d)
     s = q.stride()
@@ -619,7 +627,7 @@ def dkv_paged_weights(p: dkv_paged, q: torch.Tensor, lse: torch.Tensor, k_pages:
     st = g.lib.dkv_paged_weights(
         g.ref, q.data_ptr(), _strides(s[0], s[1], s[2]), Tq, lse.data_ptr(), k_pages.data_ptr(), page_table.data_ptr(),
         lens.data_ptr(), None if q_lens is None else q_lens.data_ptr(), weights.data_ptr(), ws.data_ptr(), ws.numel(),
-        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+        torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _check(st, "dkv_paged_weights")
     return weights
@@ -633,10 +641,10 @@ def dkv_paged_evict(p: dkv_paged, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     them, in order, moved to new_table's pages (int32 [B, n]; page_table itself compacts in place) ->
     (kept int32 [B, Hkv, budget], new_lens int32 [B], new_weights like weights)."""
     dev = k_pages.get_device()
-    if _elsewhere(k_pages, dev):
-        with torch.cuda.device(dev):
+    if _elsewhere(k_pages, dev) or stream is not None:
+        with _place(dev, stream):
             return dkv_paged_evict(p, k_pages, v_pages, page_table, lens, weights, budget, first, recent, new_table, kept,
-                                   new_lens, new_weights, workspace, stream)
+                                   new_lens, new_weights, workspace)
     g, width = _geometry(p), new_table.shape[-1]
     k_shape, t_shape = (g.batch, g.kv_heads, max(budget, 0)), (g.batch, width)
     if k_pages.dtype is not g.dtype or k_pages.stride() != g.strides or k_pages.shape != g.pool or k_pages.get_device() != dev:
@@ -667,7 +675,7 @@ def dkv_paged_evict(p: dkv_paged, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     st = g.lib.dkv_paged_evict(
         g.ref, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), lens.data_ptr(), weights.data_ptr(), budget,
         first, recent, new_table.data_ptr(), width, kept.data_ptr(), new_lens.data_ptr(), new_weights.data_ptr(),
-        ws.data_ptr(), ws.numel(), torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+        ws.data_ptr(), ws.numel(), torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _check(st, "dkv_paged_evict")
     return kept, new_lens, new_weights

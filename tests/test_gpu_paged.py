@@ -715,3 +715,27 @@ def test_many_small_weights_beside_a_large_one_count(dtype):
     for b in range(c.B):
         for h in range(hkv):
             R.check_rows(out[b, h][None], lse[b, h][None], last, d, c.dt, p_eps, f"decode {b} {h}")
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_what_a_call_allocates_is_in_its_streams_order(handle):
+    """The current stream is busy while calls on another one allocate outputs and workspaces."""
+    lens, q_lens = [150, 70], [40, 5]
+    c = R.Cache(lens, 2, 64, 16, "bf16", seed=6)
+    p = c.layout(4)
+    q, table, n, nq = queries((2, 4, 40, 64), c.dt, 3).cuda(), c.table.cuda(), c.dev(lens), c.dev(q_lens)
+    q1 = q[:, :, 0].contiguous()
+    want, wlse = dkv.dkv_paged_prefill(p, q, c.k, c.v, table, n, nq)
+    want1, wlse1 = dkv.dkv_paged_decode(p, q1, c.k, c.v, table, n)
+    side = torch.cuda.Stream()
+    x = torch.randn(8192, 8192, device="cuda", dtype=c.dt)
+    torch.cuda.synchronize()
+    for _ in range(30):
+        y = x @ x  # about 20 ms
+    stream = side.cuda_stream if handle else side
+    out, lse = dkv.dkv_paged_prefill(p, q, c.k, c.v, table, n, nq, stream=stream)
+    out1, lse1 = dkv.dkv_paged_decode(p, q1, c.k, c.v, table, n, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+    assert torch.equal(out1, want1) and torch.equal(lse1, wlse1)
+    del y
