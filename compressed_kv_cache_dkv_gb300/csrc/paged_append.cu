@@ -4,6 +4,9 @@
 // 16-byte piece per lane and access, the pieces of one token's heads side by side
 // (a projection's output order), kAppendVec independent pieces per thread in
 // flight; the page of a piece comes from the table through the read-only cache.
+//
+// Measured: prompts of 700 to 4096 tokens in 8 sequences, 8 KV heads, d 128 (166 MB read and written):
+// 29 us, 5.7 TB/s.  One token for each of 16 sequences: 2.0 us in a graph, latency.
 #include "paged.cuh"
 
 namespace dkv {

@@ -15,7 +15,14 @@
 //   o += V^T p   ldmatrix.trans V^T fragments, p as hi + lo 16-bit halves
 // with an online softmax per warp in base 2, merged over the warps at a unit's end.
 // Bound by HBM: 4 d bytes per token and KV head; the products need 2 x 8 columns of
-// which G are used, on a path that has time to spare.
+// which G are used, on a path that has time to spare.  Even runs of tiles keep all multiprocessors
+// reading to the end whatever the lengths are; two teams of consumers hide one tile's chain of products,
+// softmax and products behind the other's; four stages of 32 KB keep more bytes on their way than the
+// latency of the reads takes.
+//
+// Measured (d 128): 64 sequences of 300 to 8000 tokens, 8 KV heads, a window of 4096 and 4 sinks,
+// pages of 16 (841 MB): 138 us, 6.1 TB/s.  16 of 64k tokens, 2 KV heads, with their weights (1.09 GB):
+// 195 us, 5.6 TB/s.  One of 1000 tokens: 7.8 us in a graph, the latency of two launches.
 //
 // Rows of V that the query does not see inside a tile are zeroed in shared memory
 // before the product: their weight is 0, but 0 x NaN from a slot never written would not be.

@@ -16,6 +16,9 @@
 // wait for the flags of those earlier chunks of the unit whose rows come from where this one
 // writes, and write.  A CTA waits only for CTAs that started before it and that read without
 // waiting, so every wait ends.
+//
+// Measured (d 128): 32 sequences of 2500 to 8192 tokens, 8 KV heads, cut to 4096 (1.03 GB): 177 us,
+// of which 17 the selection; 5.8 TB/s.  30000 tokens to 15000, 8 heads: 46 us; 300 to 256: 9 us (graph).
 #include "paged.cuh"
 
 namespace dkv {

@@ -32,6 +32,11 @@
 //
 // Bound by the tensor cores: a 128 x 64 tile at d 128 takes 8 x 50 cycles for S (6 KB of shared
 // memory a product) and 4 x 64 for P V.
+//
+// Measured (d 128): a prompt of 8191, 32 query and 8 KV heads, pages of 16: 395 to 415 us, 1.3 to 1.4
+// PFLOP/s.  One of 16384 under a window of 1024, 12 heads: 136 us, 740 TFLOP/s; its 768 CTAs of 19 tiles
+// take five waves and a remainder, and the start and end of a CTA, which nothing overlaps, a fifth of the
+// time.  32 queries over 300 to 2000 keys: 16 us.
 #include "paged_tc.cuh"
 
 namespace dkv {
