@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kScoreThreads) paged_score_kernel(DecArgs p, f
       const int t = t0 + x * kScoreThreads / 2;
       sees[x] = t < len && (t >= lo || t < a.sinks);
       s[x] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (sees[x] && g0 < a.G) s[x] = __ldcs(reinterpret_cast<const float4*>(p.scores + ((size_t)u * a.cap + t) * 8 + g0));
+      if (sees[x] && g0 < a.G) s[x] = __ldcg(reinterpret_cast<const float4*>(p.scores + ((size_t)u * a.cap + t) * 8 + g0));
       old[x] = sees[x] && half == 0 ? __ldcg(wu + t) : 0.f;
     }
 #pragma unroll
