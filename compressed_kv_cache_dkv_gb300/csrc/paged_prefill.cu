@@ -573,17 +573,23 @@ cudaError_t launch_paged_prefill(const PagedArgs& a, int d, int dtype, const Pag
   p.by_heads = a.G % 2 == 0 || p.rows < kPfM;
   p.heads = p.by_heads ? 2 * kPfM / p.rows : 1;
   p.per_kv = (a.G + p.heads - 1) / p.heads;
-  // Parts: when the grid would fill at most half of the multiprocessors (records for one grid of them
-  // are what the workspace holds) and the longest sequence the table allows has more than 16 key tiles,
-  // about eight tiles each.  A tile takes 0.85 us and the join 4 to 8: 16 queries of 32 heads over
-  // 4096 keys take 23.2, 18.0, 19.9 and 21.7 us in 16, 8, 5 and 4 parts; 512 over 512 keys 22.4 in two
-  // and 14.7 in one.
+  // Parts of the key tiles, when the grid would fill at most half of the multiprocessors (records for one
+  // grid of them are what the workspace holds).  A tile takes 0.85 us; the join 2.5, 0.65 a part, and 2 ps
+  // for every value that a part leaves and the join reads.  That fits these times (us; the number of parts
+  // in front) of 32 heads at d 128 to within 1.5: 16 queries over 1024 keys 1: 17.9, 2: 15.6, 4: 13.2; over
+  // 4096 keys 4: 21.7, 8: 18.0, 16: 23.2; 128 over 1024 1: 20.7, 2: 20.9, 4: 19.3; 512 over 1024 1: 20.6,
+  // 2: 25.2.  The tiles are those of the longest sequence that the table allows.
   const int tokens = p.by_heads ? p.rows : 2 * kPfM;
   const int64_t ctas = (int64_t)a.Hkv * p.per_kv * a.B * ((q.Tq + tokens - 1) / tokens);
   const int64_t keys = a.window > 0 && (int64_t)a.window + a.sinks + tokens < a.cap ? (int64_t)a.window + a.sinks + tokens : a.cap;
-  const int64_t most = keys > 16 * kPfN ? (keys + 8 * kPfN - 1) / (8 * kPfN) : 1, fit = sm_count() / ctas;
-  p.parts = (int)(fit < most ? fit : most);
-  if (p.parts < 2) p.parts = 1;
+  const int64_t fit = sm_count() / ctas;
+  p.parts = 1;
+  if (fit > 1) {
+    const float tiles = (float)((keys + kPfN - 1) / kPfN), per_part = 0.65f + 2e-6f * (float)d * (float)a.B * (float)a.Hq * (float)q.Tq;
+    float parts = rintf(sqrtf(0.85f * tiles / per_part));
+    parts = fminf(fmaxf(parts, 1.f), fminf((float)fit, tiles));
+    if (0.85f * ceilf(tiles / parts) + 2.5f + per_part * parts < 0.85f * tiles) p.parts = (int)parts;
+  }
   p.part_o = reinterpret_cast<float*>(ws + kWsHeader);
   p.part_lse = p.part_o + (size_t)sm_count() * 2 * kPfM * d;
   if (dtype == DKV_BF16)
