@@ -37,14 +37,16 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(PagedArgs 
   if (base >= total) return;
   uint4 v[kAppendVec];
   int64_t to[kAppendVec];
+  // row = i * Hkv + h of the thread's first piece; the next one is kStep rows on
+  constexpr int kStep = kAppendThreads / R;
+  const int c = (int)(base % R);
+  int i = (int)(base / R / a.Hkv), h = (int)(base / R - (int64_t)i * a.Hkv);
+  const int di = kStep / a.Hkv, dh = kStep - di * a.Hkv;
 #pragma unroll
-  for (int x = 0; x < kAppendVec; ++x) {
-    const int64_t e = base + x * kAppendThreads;
+  for (int x = 0; x < kAppendVec; ++x, i += di, h += dh) {
+    if (h >= a.Hkv) { h -= a.Hkv; ++i; }
     to[x] = -1;
-    if (e >= total) continue;
-    const int c = (int)(e % R);
-    const int64_t row = e / R;
-    const int h = (int)(row % a.Hkv), i = (int)(row / a.Hkv);
+    if (base + x * kAppendThreads >= total) continue;
     const int64_t t = p0 + i;
     if (t < 0 || t >= a.cap) {
       raise_error(a.err, DKV_DEVERR_INDEX);
