@@ -407,8 +407,15 @@ DKV_API int dkv_prefill_attend(int32_t batch, int32_t n_q_heads, int32_t n_kv_he
  * read: their page-table entries may be anything.
  *
  * Data types: dtype DKV_FP16 or DKV_BF16 for the pools, the new rows, the
- * queries and the outputs alike; scores, softmax statistics, sums and weights
- * are held in fp32, and an output is rounded once.
+ * queries and the outputs alike; scores, softmax statistics, sums and the
+ * weights by key are held in fp32, and an output is rounded once.  In front of
+ * the product with V a softmax weight is rounded too: dkv_paged_decode keeps it
+ * as the sum of two values of the pools' type (16 bits in bf16, 22 in fp16,
+ * fewer below e^-18 of the row's largest), dkv_paged_prefill as one (8 bits in
+ * bf16, relative error at most 2^-8; 11 in fp16, 2^-11, and weights below 2^-21
+ * of the row's largest are off by up to 2^-32 of it).  So an output of decode
+ * is off by the rounding of itself, one of prefill by that and by up to the
+ * relative error just given of sum p |v|.
  *
  * Faults that only the device can see raise DKV_DEVERR_INDEX in the error word
  * of the workspace (dkv_get_error): a page index outside [0, n_pages) of a page
