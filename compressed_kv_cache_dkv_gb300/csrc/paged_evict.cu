@@ -14,8 +14,10 @@
 // in place needs an order only between a chunk's write and the reads of the chunks before it:
 // CTAs take their chunks from a counter, unit by unit and upwards, read, raise the chunk's flag,
 // wait for the flags of those earlier chunks of the unit whose rows come from where this one
-// writes, and write.  A CTA waits only for CTAs that started before it and that read without
-// waiting, so every wait ends.
+// writes, and write.  A page that is compacted in place may hold tokens of other sequences, which
+// move to pages of their own: the sequences that move come first in the counter's order, and
+// where a batch has both kinds a sequence in place writes once all rows that move have been read.
+// A CTA waits only for CTAs that started before it and that read without waiting, so every wait ends.
 //
 // Measured (d 128): 32 sequences of 2500 to 8192 tokens, 8 KV heads, cut to 4096 (1.03 GB): 177 us,
 // of which 17 the selection; 5.8 TB/s.  30000 tokens to 15000, 8 heads: 46 us; 300 to 256: 9 us (graph).
@@ -41,18 +43,28 @@ __device__ inline uint32_t weight_image(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Workspace: [header][counts int32 [B]][ticket][flags [unit][chunk]]
+// Workspace: [header][order EvictSeq [B]][EvictState][flags [unit][chunk]]
+struct EvictSeq {  // in the order in which the sequences are moved
+  int32_t b, n;    // sequence, tokens that stay
+  int32_t in_place, mixed;  // mixed: the batch has sequences in place and others
+};
+struct EvictState {
+  uint32_t ticket;   // chunks taken
+  uint32_t moved;    // of a mixed batch: chunks read of the sequences that are not in place
+  uint32_t to_move;  // and how many there are
+  uint32_t pad;
+};
 struct EvictPlan {
   int rows, chunks, zeros;  // rows of a chunk, chunks of a unit's rows, chunks of its weights' tail
-  size_t off_ticket, off_flags, bytes;
+  size_t off_state, off_flags, bytes;
 };
 __host__ __device__ inline EvictPlan evict_plan(int B, int Hkv, int cap, int d, int budget) {
   EvictPlan p;
   p.rows = kMoveBytes / (2 * d);
   p.chunks = (budget + p.rows - 1) / p.rows;
   p.zeros = (cap + kZeroChunk - 1) / kZeroChunk;
-  p.off_ticket = round_up(kWsHeader + (size_t)B * 4, 16);
-  p.off_flags = p.off_ticket + 16;
+  p.off_state = kWsHeader + (size_t)B * sizeof(EvictSeq);
+  p.off_flags = p.off_state + sizeof(EvictState);
   p.bytes = p.off_flags + (size_t)B * Hkv * p.chunks * 4;
   return p;
 }
@@ -65,6 +77,41 @@ __device__ inline int ld_cluster_s32(const void* local, uint32_t rank) {
   return v;
 }
 
+// What the move kernel starts from, written by one CTA: the sequences that move to other pages, then
+// those compacted in place (their first page stays), each kind in the batch's order.
+__device__ inline void evict_order(const PagedArgs& a, const PagedEvict& e, const EvictPlan& plan, uint8_t* ws, int* wsum) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto stays = [&](int b) { return __ldg(a.table + (size_t)b * a.max_pages) == __ldg(e.new_table + (size_t)b * e.new_max_pages); };
+  int moving = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kSelThreads) moving += __syncthreads_count(b0 + tid < a.B && !stays(b0 + tid));
+  const bool mixed = moving > 0 && moving < a.B;
+  EvictSeq* order = reinterpret_cast<EvictSeq*>(ws + kWsHeader);
+  int before = 0, to_move = 0;  // sequences that move in front of this round's; this thread's chunks
+  for (int b0 = 0; b0 < a.B; b0 += kSelThreads) {
+    const int b = b0 + tid;
+    const bool in = b < a.B, move = in && !stays(b);
+    const uint32_t bits = __ballot_sync(0xffffffffu, move);
+    if (lane == 0) wsum[warp] = __popc(bits);
+    __syncthreads();
+    const int count = wsum[lane];
+    const int at = before + __reduce_add_sync(0xffffffffu, lane < warp ? count : 0) + __popc(bits & ((1u << lane) - 1));
+    before += __reduce_add_sync(0xffffffffu, count);
+    if (in) {
+      const int n = min(paged_len(a, b), e.budget);
+      order[move ? at : moving + b - at] = {b, n, !move, mixed};
+      if (move) to_move += (n + plan.rows - 1) / plan.rows;
+    }
+    __syncthreads();
+  }
+  to_move = __reduce_add_sync(0xffffffffu, to_move);
+  if (lane == 0) wsum[warp] = to_move;
+  __syncthreads();
+  if (warp == 0) {
+    to_move = __reduce_add_sync(0xffffffffu, wsum[lane]);
+    if (lane == 0) *reinterpret_cast<EvictState*>(ws + plan.off_state) = {0u, 0u, (uint32_t)to_move * a.Hkv, 0u};
+  }
+}
+
 template <int CL>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(PagedArgs a, PagedEvict e, EvictPlan plan,
                                                                   uint8_t* __restrict__ ws) {
@@ -73,13 +120,14 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(PagedArgs a, 
   __shared__ int wsum[32];
   __shared__ int sh_digit, sh_above;
   const int rank = CL > 1 ? (int)cluster_ctarank() : 0;
-  const int u = blockIdx.x / CL, b = u / a.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int u = (int)(blockIdx.x / CL) - 1, b = u / a.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_launch();
+  if (u < 0) {  // beside the units' CTAs
+    if (rank == 0) evict_order(a, e, plan, ws, wsum);
+    return;
+  }
   const int len = paged_len(a, b), n = min(len, e.budget);
   int32_t* kept = e.kept + (size_t)u * e.budget;
-  // what the move kernel starts from
-  if (u % a.Hkv == 0 && rank == 0 && tid == 0) reinterpret_cast<int32_t*>(ws + kWsHeader)[b] = n;
-  if (blockIdx.x == 0 && tid == 0) *reinterpret_cast<uint32_t*>(ws + plan.off_ticket) = 0;
   uint32_t* flags = reinterpret_cast<uint32_t*>(ws + plan.off_flags) + (size_t)u * plan.chunks;
   const int all = CL * kSelThreads, me = rank * kSelThreads + tid;
   for (int i = me; i < plan.chunks; i += all) flags[i] = 0;
@@ -228,30 +276,37 @@ __global__ void __launch_bounds__(kMoveThreads, 8) evict_move_kernel(PagedArgs a
   __shared__ uint32_t sh_ticket;
   const int tid = threadIdx.x;
   griddep_wait();
-  if (tid == 0) sh_ticket = atomicAdd(reinterpret_cast<uint32_t*>(ws + plan.off_ticket), 1u);
+  EvictState* state = reinterpret_cast<EvictState*>(ws + plan.off_state);
+  if (tid == 0) sh_ticket = atomicAdd(&state->ticket, 1u);
   __syncthreads();
   const int per = plan.chunks + plan.zeros;
-  const int u = (int)(sh_ticket / (uint32_t)per), c = (int)(sh_ticket % (uint32_t)per), b = u / a.Hkv, h = u % a.Hkv;
-  const int n = __ldg(reinterpret_cast<const int32_t*>(ws + kWsHeader) + b);
+  const int ou = (int)(sh_ticket / (uint32_t)per), c = (int)(sh_ticket % (uint32_t)per), h = ou % a.Hkv;
+  const int4 seq = __ldg(reinterpret_cast<const int4*>(ws + kWsHeader) + ou / a.Hkv);  // EvictSeq
+  const int b = seq.x, n = seq.y, u = b * a.Hkv + h;
+  const bool in_place = seq.z != 0, mixed = seq.w != 0;
   const int32_t* kept = e.kept + (size_t)u * e.budget;
   const float* w = e.weights + (size_t)u * a.cap;
   float* nw = e.new_weights + (size_t)u * a.cap;
   uint32_t* flags = reinterpret_cast<uint32_t*>(ws + plan.off_flags) + (size_t)u * plan.chunks;
+  auto poll = [&](auto over) {  // false after kPollLimit polls
+    for (int x = 0; x < kPollLimit; ++x) {
+      if (over()) return true;
+      __nanosleep(100);
+    }
+    raise_error(a.err, DKV_DEVERR_TIMEOUT);
+    return false;
+  };
   // the chunks of the unit before chunk `to` with a row from position j0 or behind (a run of chunks, since
   // kept is ascending) have read their rows; false when a wait gave up
   auto wait_for = [&](int to, int j0) {
     bool ok = true;
     for (int i = to - 1 - tid; i >= 0 && ok; i -= kMoveThreads) {
       if (__ldg(kept + min((i + 1) * plan.rows, n) - 1) < j0) break;
-      uint32_t f = 0;
-      for (int x = 0; x < kPollLimit && !f; ++x) {
+      ok = poll([&]() {
+        uint32_t f;
         asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(f) : "l"(flags + i) : "memory");
-        if (!f) __nanosleep(100);
-      }
-      if (!f) {
-        raise_error(a.err, DKV_DEVERR_TIMEOUT);
-        ok = false;
-      }
+        return f != 0;
+      });
     }
     return __syncthreads_and(ok);
   };
@@ -291,13 +346,23 @@ __global__ void __launch_bounds__(kMoveThreads, 8) evict_move_kernel(PagedArgs a
   const bool weighs = tid < plan.rows && jw < n;
   float wt = 0.f;
   if (weighs) wt = __ldcg(w + __ldg(kept + jw));
-  // a sequence whose first page stays is compacted in place
-  const bool in_place = __ldg(a.table + (size_t)b * a.max_pages) == __ldg(e.new_table + (size_t)b * e.new_max_pages);
-  if (in_place || nw == w) {
+  if (in_place || nw == w || mixed) {
     __threadfence();  // this thread's reads are done
     __syncthreads();
-    if (tid == 0) asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(flags + c), "r"(1u) : "memory");
-    if (!wait_for(c, j0)) return;
+    if (tid == 0) {
+      asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(flags + c), "r"(1u) : "memory");
+      if (mixed && !in_place) atomicAdd(&state->moved, 1u);
+    }
+    if ((in_place || nw == w) && !wait_for(c, j0)) return;
+    if (in_place && mixed) {  // other sequences' rows may lie where this one writes
+      bool ok = true;
+      if (tid == 0) ok = poll([&]() {
+        uint32_t moved;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(moved) : "l"(&state->moved) : "memory");
+        return moved >= state->to_move;
+      });
+      if (!__syncthreads_and(ok)) return;
+    }
   }
 #pragma unroll
   for (int x = 0; x < kMoveVec; ++x)
@@ -322,7 +387,7 @@ cudaError_t launch_paged_evict(const PagedArgs& a, int d, const PagedEvict& e, v
   cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(select), smem);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(units * (wide ? kSelCluster : 1));
+  cfg.gridDim = dim3((units + 1) * (wide ? kSelCluster : 1));
   cfg.blockDim = dim3(kSelThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;

@@ -542,8 +542,11 @@ DKV_API int dkv_paged_weights(const dkv_paged* p, const void* q, const dkv_strid
  *                pages that hold none of the tokens being kept, or begins with
  *                the very pages of its page_table row (page_table itself with
  *                new_max_pages = max_pages, for instance): then the sequence is
- *                compacted in place.  Pages that two sequences share can be read
- *                from, but no page may be written for two of them
+ *                compacted in place.  Pages that several sequences share are
+ *                read from for all of them; no page may be written for two.
+ *                Where one of them is compacted in place, each other that keeps
+ *                tokens of the pages written for it has to move to other pages
+ *                (its rows are read before they are written over)
  *   kept         device int32 [B][Hkv][budget]: the positions kept, ascending,
  *                -1 behind the last
  *   new_lens     device int32 [B]: min(lens, budget); may be lens itself

@@ -415,6 +415,44 @@ def test_evict_of_long_sequences(lens, budget, kind):
     _evict_check(c, p, weights, budget, 1, 1, kept.cpu(), new_lens.cpu(), new_weights, c.table, k, v)
 
 
+def _evict_mixed(c, stays, budget, first, recent, own_weights):
+    """Sequences with stays[b] are compacted in place, the others move to free pages."""
+    keep = -(-budget // c.page)
+    to = c.free[:c.B * keep].view(c.B, keep).clone()
+    for b in range(c.B):
+        if stays[b]:
+            to[b] = c.table[b, :keep]
+    p = c.layout(c.hkv)
+    ws = workspace(p)
+    weights = torch.rand(c.B, c.hkv, c.width * c.page, generator=torch.Generator().manual_seed(5)) ** 8
+    w_d, k, v = weights.cuda(), c.k.cpu(), c.v.cpu()
+    kept, new_lens, new_weights = dkv.dkv_paged_evict(p, c.k, c.v, c.table.cuda(), c.dev(c.lens), w_d, budget, first, recent,
+                                                      to.cuda(), new_weights=w_d if own_weights else None, workspace=ws)
+    no_fault(ws)
+    c.k, c.v = c.k.cpu(), c.v.cpu()
+    _evict_check(c, p, weights, budget, first, recent, kept.cpu(), new_lens.cpu(), new_weights.cpu(), to, k, v)
+
+
+@pytest.mark.parametrize("dtype,d,hkv,page,order", [("fp16", 128, 4, 16, "head"), ("bf16", 64, 2, 64, "token")])
+@pytest.mark.parametrize("who", [0, 2, 4])
+@pytest.mark.parametrize("own_weights", [False, True])
+def test_evict_in_place_of_pages_that_others_are_moved_from(dtype, d, hkv, page, order, who, own_weights):
+    """Five sequences share their first tokens; one is compacted in place, over rows that the others keep."""
+    lens = [6000, 5000, 5500, 1200, 4800]
+    keep, shared = -(-2000 // page), 1024 // page
+    c = R.Cache(lens, hkv, d, page, dtype, order, seed=7, spare=len(lens) * keep)
+    c.table[:, :shared] = c.table[who, :shared].clone()
+    _evict_mixed(c, [b == who for b in range(len(lens))], 2000, 4, 64, own_weights)
+
+
+@pytest.mark.parametrize("own_weights", [False, True])
+def test_evict_of_many_sequences_in_place_and_not(own_weights):
+    """More sequences than one round of threads puts in order."""
+    lens = [(i * 29) % 60 for i in range(1300)]
+    c = R.Cache(lens, 1, 64, 16, "bf16", seed=8, spare=2 * 1300, width=4)
+    _evict_mixed(c, [n > 20 and b % 3 == 0 for b, n in enumerate(lens)], 20, 1, 5, own_weights)
+
+
 # ---------------------------------------------------------------- together
 
 def test_a_serving_run():
