@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   // the groups: head and first query row (of all heads the later rows, with more keys, first)
   const int tile = (int)gridDim.z - 1 - (int)blockIdx.z;
   const int row0 = tile * (p.by_heads ? p.rows : 2 * kPfM);
-  griddep_launch();
+  if (p.parts > 1) griddep_launch();  // the join; without it the next grid on the stream may be anyone's
   if (row0 >= qs.n) return;
   const int part = (int)blockIdx.x % p.parts, hg = (int)blockIdx.x / p.parts;
   const int kvh = hg / p.per_kv, h0 = hg % p.per_kv * p.heads;  // h0: within the KV head's group

@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from compressed_kv_cache_dkv_gb300 import dkv
+from compressed_kv_cache_dkv_gb300 import dkv, synth
 from tests import paged_ref as R
 
 pytestmark = pytest.mark.gpu
@@ -777,3 +777,37 @@ def test_what_a_call_allocates_is_in_its_streams_order(handle):
     assert torch.equal(out, want) and torch.equal(lse, wlse)
     assert torch.equal(out1, want1) and torch.equal(lse1, wlse1)
     del y
+
+
+def test_a_prefill_has_ended_before_what_follows_reads_its_rows():
+    """The stage calls' attention grid may start before the grid in front of it has ended, if that one allows
+    it; it reads its queries at once.  Here they are the rows that a long prefill writes last."""
+    w = synth.WORKLOADS["8k"]
+    desc = dkv.dkv_layout(1, w.n_q_heads, w.n_kv_heads, w.head_dim, w.n_blocks, w.window, w.rank(0), w.n_residual)
+    K, V = (torch.from_numpy(x[:1]).cuda() for x in synth.layer_kv(w, 0))
+    packed = dkv.dkv_compress_layout(desc, K, V)
+    Tq = 4096
+    c = R.Cache([Tq], w.n_kv_heads, w.head_dim, 64, "fp16", seed=40)
+    p, table, lens = c.layout(w.n_q_heads), c.table.cuda(), c.dev([Tq])
+    q = queries((1, w.n_q_heads, Tq, w.head_dim), c.dt, 41).cuda()
+    rows = torch.zeros(Tq, 1, w.n_q_heads, w.head_dim, dtype=c.dt, device="cuda")
+    ws, pws = torch.zeros(dkv.dkv_decode_workspace_bytes(desc, w.top_k), dtype=torch.uint8, device="cuda"), workspace(p)
+
+    def run(wait):
+        rows.zero_()
+        out = torch.full((1, w.n_q_heads, w.head_dim), float("nan"), device="cuda")
+        dkv.dkv_decode_route(desc, q[:, :, 0].contiguous(), packed, w.top_k, ws)
+        dkv.dkv_paged_prefill(p, q, c.k, c.v, table, lens, out=rows.permute(1, 2, 0, 3), lse=False, workspace=pws)
+        if wait:
+            torch.cuda.synchronize()
+        dkv.dkv_decode_blocks(desc, rows[0], packed, w.top_k, ws)
+        dkv.dkv_decode_combine(desc, w.top_k, out, ws)
+        torch.cuda.synchronize()
+        return out
+
+    want = run(True)
+    assert bool(want.isfinite().all())
+    for _ in range(5):
+        assert torch.equal(run(False), want)
+    no_fault(ws)
+    no_fault(pws)
