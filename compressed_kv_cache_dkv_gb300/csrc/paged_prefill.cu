@@ -162,7 +162,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   uint64_t* s_full = q_full + 1;       // [group][buffer]
   uint64_t* p_full = s_full + 4;       // [group][buffer]
   uint64_t* o_done = p_full + 4;       // [group][buffer]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 4);
+  uint64_t* drain = o_done + 4;        // [group] after a wait that gave up
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   int* n_bad = reinterpret_cast<int*>(tmem_slot + 1);
   int* bad_key = n_bad + 1;                                              // [edge] first key of an edge tile with bad rows
   uint32_t* bad_bits = reinterpret_cast<uint32_t*>(bad_key + kPfEdges);  // [edge][2]
@@ -183,6 +184,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       mbar_init(&p_full[i], kPfM);
       mbar_init(&o_done[i], 1);
     }
+    for (int i = 0; i < 2; ++i) mbar_init(&drain[i], 1);
     *n_bad = 0;
     fence_mbar_init();
   }
@@ -294,12 +296,17 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (++v_sl == S::kR) { v_sl = 0; v_ph ^= 1u; }
       }
     }
+    if (!__all_sync(0xffffffffu, ok)) {  // a wait gave up, and the rows may have too: no product outlives the CTA
+      tc_commit(&drain[g], el);
+      mbar_wait(&drain[g], 0, a.err);
+    }
   } else if (warp == 11) {
     // =========================== V, and the rows of its edge tiles
     const uint32_t el = elect_one();
     auto clean = [&](int j, int edge) {
       const int k0 = key_of(j), sl = j % S::kR;
-      ok = __all_sync(0xffffffffu, ok && mbar_wait(&landed[edge], 0, a.err));
+      // (waited for also when another wait has given up: the copy must not outlive the CTA)
+      if (!__all_sync(0xffffffffu, mbar_wait(&landed[edge], 0, a.err))) { ok = false; return; }
       const uint32_t vb = sb + S::kOffV + sl * S::kTile;
       uint32_t bad = 0;  // rows lane, lane + 32 with a value that is not finite
       for (int x = 0; x < kPfN / 32; ++x) {

@@ -49,6 +49,7 @@ struct WtArgs {
 
 struct WtBars {
   uint64_t *stay_full, *stay_empty, *full, *empty, *s_full, *s_empty;  // [kStay] x 2, [kSlots] x 2, [warpgroup] x 2
+  uint64_t* drain;
   uint32_t* tmem_slot;
 };
 
@@ -61,7 +62,8 @@ __device__ inline uint32_t wt_start(uint8_t* smem, WtBars& b, const CUtensorMap*
   b.empty = b.full + kSlots;
   b.s_full = b.empty + kSlots;
   b.s_empty = b.s_full + 4;
-  b.tmem_slot = reinterpret_cast<uint32_t*>(b.s_empty + 4);
+  b.drain = b.s_empty + 4;
+  b.tmem_slot = reinterpret_cast<uint32_t*>(b.drain + 1);
   if (threadIdx.x == 0) {
     tma_prefetch_map(kmap);
     tma_prefetch_map(qmap);
@@ -70,6 +72,7 @@ __device__ inline uint32_t wt_start(uint8_t* smem, WtBars& b, const CUtensorMap*
       mbar_init(&b.s_full[i], 1);
       mbar_init(&b.s_empty[i], 128);
     }
+    mbar_init(b.drain, 1);
     fence_mbar_init();
   }
   if (threadIdx.x < 32) tc_alloc<512>(b.tmem_slot);
@@ -77,6 +80,11 @@ __device__ inline uint32_t wt_start(uint8_t* smem, WtBars& b, const CUtensorMap*
   __syncthreads();
   tc_fence_after();
   return *b.tmem_slot;
+}
+// a wait of the issuing warp gave up, and the sums' may have too: no product outlives the CTA
+__device__ inline void wt_drain(const WtBars& b, uint32_t* err, uint32_t el) {
+  tc_commit(b.drain, el);
+  mbar_wait(b.drain, 0, err);
 }
 __device__ inline void wt_end(uint32_t tmem) {
   tc_fence_before();
@@ -255,6 +263,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       tc_commit(&bar.stay_empty[seg % kStay], el);
       x += g.j1 - g.j0;
     }
+    if (!ok) wt_drain(bar, a.err, el);
   } else {
     // =========================== sums: one key per thread
     const int w = warp >> 2, row = threadIdx.x & 127;
@@ -350,6 +359,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) __cluster_dims__(kCluster, 1, 1
       }
       tc_commit(&bar.empty[sl], el);
     }
+    if (!ok) wt_drain(bar, a.err, el);
   } else {
     // =========================== sums: one key per thread
     const int w = warp >> 2, row = threadIdx.x & 127, t = k0 + (w & 1) * kWtM + row;
