@@ -86,6 +86,17 @@ __device__ inline void tc_st32(uint32_t ta, const uint32_t* r) {
 }
 __device__ inline void tc_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// named_bar_sync that tells whether x holds for any of the threads
+__device__ inline bool named_bar_any(int id, int nthreads, bool x) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(nthreads), "r"((uint32_t)x)
+      : "memory");
+  return any != 0;
+}
+
 // whether the phase of this parity is over (no waiting)
 __device__ inline bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;

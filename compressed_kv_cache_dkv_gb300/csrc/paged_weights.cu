@@ -137,15 +137,16 @@ __device__ inline void wt_product(uint32_t td, uint32_t key, uint32_t query, int
 __device__ inline float wt_minus_lse2(float lse) { return lse == -INFINITY ? -INFINITY : lse * -1.4426950408889634f; }
 
 // Adds to acc the weights of this thread's key t over the columns at TMEM address ts: query rows r0 on
-// of head after head, qn columns each, with l2 their minus base-2 lse.  Waits for the scores and gives
-// the columns back.
-__device__ inline bool wt_sum(const PagedArgs& a, const QuerySpan& qs, uint32_t ts, int ncol, int qn, int r0, int t, const float* l2,
+// of head after head, qn columns each, with l2 their minus base-2 lse; `left_out`: it is -inf for some,
+// which add nothing whatever their scores are (NaN, for a row that nothing has written).  Waits for the
+// scores and gives the columns back.
+__device__ inline bool wt_sum(const PagedArgs& a, const QuerySpan& qs, uint32_t ts, int ncol, int qn, int r0, int t, const float* l2, bool left_out,
                               uint64_t* s_full, uint64_t* s_empty, uint32_t parity, float2 (&acc)[2], bool ok) {
   // rows [v_lo, v_hi) of each head see this key
   const int v_lo = max(t - qs.off - r0, 0);
   int v_hi = min(qn, qs.n - r0);
   if (a.window > 0 && t >= a.sinks) v_hi = (int)max((int64_t)0, min((int64_t)v_hi, (int64_t)t + a.window - qs.off - r0));
-  const bool all = ncol == kWtN && __all_sync(0xffffffffu, v_lo == 0 && v_hi == qn);
+  const bool all = ncol == kWtN && !left_out && __all_sync(0xffffffffu, v_lo == 0 && v_hi == qn);
   if (ok) ok = mbar_wait(s_full, parity, a.err);
   tc_fence_after();
   if (all) {  // every column counts
@@ -187,8 +188,8 @@ __device__ inline bool wt_sum(const PagedArgs& a, const QuerySpan& qs, uint32_t 
     tc_ld_wait();
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const float x = fast_exp2(fmaf(__uint_as_float(s[e]), a.scale_log2, l2[c + e]));
-      acc[e & 1].x += r1 + e >= v_lo && r1 + e < v_hi ? x : 0.f;  // (what lies in a hidden column is not looked at)
+      const float m = l2[c + e], x = fast_exp2(fmaf(__uint_as_float(s[e]), a.scale_log2, m));
+      acc[e & 1].x += r1 + e >= v_lo && r1 + e < v_hi && m != -INFINITY ? x : 0.f;  // (what lies in a hidden column is not looked at)
     }
   }
   tc_fence_before();
@@ -279,14 +280,14 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         const int head = g.h * a.G + row / qn, r = row % qn;
         l2[row] = row < ncol && r < qs.n ? wt_minus_lse2(__ldg(p.lse + ((int64_t)g.b * a.Hq + head) * p.q.Tq + r)) : -INFINITY;
       }
-      named_bar_sync(1 + w, 128);
+      const bool left_out = named_bar_any(1 + w, 128, l2[row] == -INFINITY);
       for (int j = g.j0; j < g.j1; ++j, ++i) {
         if ((i & 3) != w) continue;
         const int t = ks.key(j) + row;
         float* to = p.weights + (size_t)u * a.cap + t;
         const float old = t < qs.len ? __ldcg(to) : 0.f;  // back before the sum is
         float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        ok = wt_sum(a, qs, tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 128u * w, ncol, qn, 0, t, l2, &bar.s_full[w], &bar.s_empty[w],
+        ok = wt_sum(a, qs, tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 128u * w, ncol, qn, 0, t, l2, left_out, &bar.s_full[w], &bar.s_empty[w],
                     (uint32_t)((i >> 2) & 1), acc, ok);
         if (t < qs.len) *to = old + wt_total(acc);
       }
@@ -379,8 +380,8 @@ __global__ void __launch_bounds__(kWtThreads, 1) __cluster_dims__(kCluster, 1, 1
       tl += 2;
       while (tl >= per) { tl -= per; ++hd; }
       if (i + 2 < n) next = fetch();
-      named_bar_sync(1 + w, 128);
-      ok = wt_sum(a, qs, tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 128u * w, qn, qn, r0, t, l2, &bar.s_full[w], &bar.s_empty[w],
+      const bool left_out = named_bar_any(1 + w, 128, l2[row] == -INFINITY);
+      ok = wt_sum(a, qs, tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 128u * w, qn, qn, r0, t, l2, left_out, &bar.s_full[w], &bar.s_empty[w],
                   (uint32_t)(k & 1), acc, ok);
       named_bar_sync(1 + w, 128);  // l2 is read
     }

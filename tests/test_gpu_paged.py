@@ -811,3 +811,34 @@ def test_a_prefill_has_ended_before_what_follows_reads_its_rows():
         assert torch.equal(run(False), want)
     no_fault(ws)
     no_fault(pws)
+
+
+@pytest.mark.parametrize("dtype,d,hq,hkv,Tq", [("fp16", 128, 2, 1, 20), ("bf16", 64, 8, 2, 32), ("fp16", 64, 3, 1, 300),
+                                               ("bf16", 128, 6, 2, 256)])
+def test_a_query_whose_lse_is_minus_infinity_adds_no_weight(dtype, d, hq, hkv, Tq):
+    """Whatever its row holds: NaN and infinities, as rows that nothing has written may."""
+    n = 700
+    c = R.Cache([n], hkv, d, 64, dtype, seed=50)
+    p = c.layout(hq)
+    ws = workspace(p)
+    q = queries((1, hq, Tq, d), c.dt, 51)
+    table, lens = c.table.cuda(), c.dev([n])
+    _, lse = dkv.dkv_paged_prefill(p, q.cuda(), c.k, c.v, table, lens, workspace=ws)
+    out = torch.zeros(hq, Tq, dtype=torch.bool)
+    out[:, 3] = out[0, 7:12] = out[-1, Tq - 1] = True
+    bad = q.clone()
+    bad[0, out] = torch.tensor([float("nan"), float("inf")], dtype=c.dt).repeat(d // 2)
+    lse[0, out.cuda()] = float("-inf")
+    weights = torch.zeros(1, hkv, c.width * 64, device="cuda")
+    dkv.dkv_paged_weights(p, bad.cuda(), lse, c.k, table, lens, weights, workspace=ws)
+    no_fault(ws)
+    pos = torch.arange(n - Tq, n)
+    for h in range(hkv):
+        added, big = torch.zeros(n, dtype=torch.float64), 0.0
+        for j in range(h * hq // hkv, (h + 1) * hq // hkv):
+            ref = R.attend(q[0, j].double(), c.K[0][h], c.V[0][h], pos, 0, 0)
+            added += ref[2][~out[j]].sum(0)
+            big = max(big, ref[4])
+        rows = Tq * hq // hkv  # (as for the weights of all queries)
+        tol = (2 * R.score_error(d, big) + 2.0 ** -20 * (1 + math.log(n)) + 2.0 ** -23 * (rows / 8 + 8)) * added
+        assert bool(((weights[0, h, :n].double().cpu() - added).abs() <= tol).all())
