@@ -221,9 +221,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       const float f0 = fast_exp2(m0 - ms0), f1 = fast_exp2(m1 - ms1);
       m0 = n0;
       m1 = n1;
-      const float s0 = ms0 - kDecShift<T>, s1 = ms1 - kDecShift<T>;
-      const float p0 = fast_exp2(sc[0] - s0), p1 = fast_exp2(sc[1] - s1);
-      const float p2 = fast_exp2(sc[2] - s0), p3 = fast_exp2(sc[3] - s1);
+      // (the shift behind the difference: in front of it a large maximum would round it away)
+      const float p0 = fast_exp2((sc[0] - ms0) + kDecShift<T>), p1 = fast_exp2((sc[1] - ms1) + kDecShift<T>);
+      const float p2 = fast_exp2((sc[2] - ms0) + kDecShift<T>), p3 = fast_exp2((sc[3] - ms1) + kDecShift<T>);
       l0 = l0 * f0 + (p0 + p2);
       l1 = l1 * f1 + (p1 + p3);
       if (__any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f)) {

@@ -5,7 +5,7 @@
 // KV head at the same tokens where the group size is even, else 256 tokens of one head; up to 64
 // queries stand in rows of 8, 16, 32 or 64 a head, so that a group holds several heads.  A grid
 // that would leave half of the multiprocessors idle is multiplied by cutting the key tiles of
-// each CTA into parts, which a second grid joins by their log-sum-exps.  Per 64-key tile j and
+// each CTA into parts, which a second grid joins by their maxima and sums.  Per 64-key tile j and
 // group g
 //   S_g = Q_g K_j^T   M = 128 queries, N = 64 keys   (64 TMEM columns, two buffers a group)
 //   O_g += P_g V_j    M = 128, N = d, P from TMEM (16-bit, over the first 32 columns of its S)
@@ -44,7 +44,8 @@ namespace {
 
 constexpr int kPfThreads = 384, kPfM = 128, kPfN = 64;
 constexpr float kPfSlack = 8.f;
-constexpr int kPfIdle = 1 << 24;  // polls without a product before the issuing thread gives up
+// Rows with scores from here on (in base 2) are left to large_tiles.
+constexpr float kPfLarge = 0x1p20f;
 constexpr int kPfEdges = 12;  // edge tiles of a CTA (255 positions): 5 on the diagonal, 5 at the window's edge, 1 at the sinks' end
 
 template <typename T>
@@ -77,8 +78,9 @@ struct PfKernelArgs {
   int heads;     // heads of a CTA
   int per_kv;    // CTAs that share the heads of a KV head
   int parts;     // parts of each CTA's key tiles
-  float* part_o;    // [CTA][part][256 rows][d] and
-  float* part_lse;  // [CTA][part][256 rows] base-2, when parts > 1
+  float* part_o;     // [CTA][part][256 rows][d] and
+  float2* part_stat; // [CTA][part][256 rows] maximum and sum, when parts > 1 (a log-sum-exp would lose a sum
+                     // beside a large maximum)
 };
 
 // Row `row` of group g of a CTA's 256: its head and token.
@@ -95,9 +97,88 @@ __device__ inline PfRow pf_row(const PfKernelArgs& p, int kvh, int h0, int row0,
   return r;
 }
 
+// natural log-sum-exp of a row's maximum and sum (-inf for a row that sees no key)
+template <typename T>
+__device__ inline float lse_of(float m, float l) { return (m - kPfShift<T> + log2f(l)) * 0.6931471805599453f; }
+
 // every query at positions [p_lo, p_hi] sees every key of [k0, k0 + kPfN)
 __device__ inline bool all_seen(const PagedArgs& a, int k0, int p_lo, int p_hi) {
   return k0 + kPfN - 1 <= p_lo && (a.window == 0 || k0 > p_hi - a.window || k0 + kPfN <= a.sinks);
+}
+
+// bit c: the query at position pos sees key k0 + c
+__device__ inline unsigned long long pf_sees(const PagedArgs& a, int pos, int k0) {
+  const int hi = pos - k0, lo = a.window ? pos - a.window + 1 - k0 : 0, sk = a.sinks - k0;
+  auto below = [](int n) { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1; };
+  return below(hi + 1) & (~below(lo) | below(sk));
+}
+
+// Tiles j .. n - 1 of a row, in the softmax loop's place, where scores are large (rare, so in rolled
+// loops).  That loop's fma of score, scale and minus the maximum leaves the rounding of the maximum in the
+// exponent: 2^-4 at kPfLarge, but 1 at 2^24, which with slack and shift is past fp16, and hundreds at
+// 2^32.  Here the product is rounded as the maximum's was, and the maximum moves at once.  Returns it and
+// the sum.
+template <typename T, int D>
+__device__ __noinline__ float2 large_tiles(const PagedArgs& a, const KeySpan<kPfN>& ks, int t0, int j, int n, int pos, uint32_t tg,
+                                           uint64_t* s_full, uint64_t* p_full, uint64_t* o_done, float m, float l) {
+  bool ok = true;
+#pragma unroll 1
+  for (; j < n; ++j) {
+    const int buf = j & 1;
+    const uint32_t ts = tg + kPfN * buf, to = tg + 128u;
+    if (ok) ok = mbar_wait(&s_full[buf], (uint32_t)((j >> 1) & 1), a.err);
+    tc_fence_after();
+    const unsigned long long sees = pf_sees(a, pos, ks.key(t0 + j));
+    float top = m;
+#pragma unroll 1
+    for (int c = 0; c < kPfN; c += 16) {
+      uint32_t s[16];
+      tc_ld16(ts + c, s);
+      tc_ld_wait();
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (sees >> (c + e) & 1ull) top = fmaxf(top, __fmul_rn(__uint_as_float(s[e]), a.scale_log2));
+    }
+    const float al = top > m ? fast_exp2(m - top) : 1.f;
+    m = top;
+    if (j > 0 && __any_sync(0xffffffffu, al != 1.f)) {
+      if (ok) ok = mbar_wait(&o_done[buf ^ 1], (uint32_t)(((j - 1) >> 1) & 1), a.err);
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < D; c += 16) {
+        uint32_t o[16];
+        tc_ld16(to + c, o);
+        tc_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+        tc_st16(to + c, o);
+      }
+    }
+    const float ms = m == -INFINITY ? 0.f : m;
+    l *= al;
+#pragma unroll 1
+    for (int c = 0; c < kPfN; c += 16) {  // (P's columns c / 2 .. c / 2 + 7 lie over scores that have been read)
+      uint32_t s[16], w[8];
+      tc_ld16(ts + c, s);
+      tc_ld_wait();
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        float y[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float d = __fadd_rn(__fmul_rn(__uint_as_float(s[e + x]), a.scale_log2), -ms);
+          y[x] = sees >> (c + e + x) & 1ull ? fast_exp2(d + kPfShift<T>) : 0.f;
+          l += y[x];
+        }
+        w[e / 2] = Num<T>::pack(y[0], y[1]);
+      }
+      tc_st8(ts + c / 2, w);
+    }
+    tc_st_wait();
+    tc_fence_before();
+    mbar_arrive(&p_full[buf]);
+  }
+  return make_float2(m, l);
 }
 
 // f = the sum of p v in fp32 over the V rows that are not finite and that this row sees, for channels
@@ -119,7 +200,7 @@ __device__ __noinline__ void add_bad_rows(const PfKernelArgs& p, const PagedArgs
     const T* vr = static_cast<const T*>(p.v_pool) + at + c0;
     float dot = 0.f;
     for (int e = 0; e < D; ++e) dot = fmaf(Num<T>::to_float(qr[e]), Num<T>::to_float(kr[e]), dot);
-    const float w = fast_exp2(fmaf(dot, a.scale_log2, kPfShift<T> - m)) * il;
+    const float w = fast_exp2(__fadd_rn(__fmul_rn(dot, a.scale_log2), -m) + kPfShift<T>) * il;
     for (int e = 0; e < 32; ++e) f[e] += w * Num<T>::to_float(vr[e]);
   }
 }
@@ -387,10 +468,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       tc_ld_wait();
       const int k0 = key_of(j);
       if (!all_seen(a, k0, g_lo, g_hi)) {
-        // bit c: this row sees key k0 + c
-        const int hi = pos - k0, lo = a.window ? pos - a.window + 1 - k0 : 0, sk = a.sinks - k0;
-        auto below = [](int n) { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1; };
-        const unsigned long long sees = below(hi + 1) & (~below(lo) | below(sk));
+        const unsigned long long sees = pf_sees(a, pos, k0);
         if (__any_sync(0xffffffffu, sees != ~0ull)) {
           const uint32_t half[2] = {(uint32_t)sees, (uint32_t)(sees >> 32)};
 #pragma unroll
@@ -403,10 +481,17 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
       for (int c = 8; c < kPfN; ++c) mx[c & 7] = fmaxf(mx[c & 7], __uint_as_float(s[c]));
       const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * slog2;
-      const bool up = top > m + kPfSlack;
+      const bool up = top > m + kPfSlack, moved = __any_sync(0xffffffffu, up);
+      // (rows that are not live hold whatever was there)
+      if (moved && __any_sync(0xffffffffu, me.live && fabsf(top) >= kPfLarge && top > -INFINITY)) {
+        const float2 ml = large_tiles<T, D>(a, ks, t0, j, n, pos, tg, s_full + 2 * g, p_full + 2 * g, o_done + 2 * g, m, l);
+        m = ml.x;
+        l = ml.y;
+        break;
+      }
       const float al = up ? fast_exp2(m - top) : 1.f;
       if (up) m = top;
-      if (j > 0 && __any_sync(0xffffffffu, up)) {  // rescale O once O_{j-1} is done
+      if (j > 0 && moved) {  // rescale O once O_{j-1} is done
         if (ok) ok = mbar_wait(&o_done[2 * g + (buf ^ 1)], (uint32_t)(((j - 1) >> 1) & 1), a.err);
         tc_fence_after();
 #pragma unroll
@@ -476,9 +561,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                make_uint4(Num<T>::pack(f[e], f[e + 1]), Num<T>::pack(f[e + 2], f[e + 3]), Num<T>::pack(f[e + 4], f[e + 5]),
                           Num<T>::pack(f[e + 6], f[e + 7])));
     }
-    const float lse2 = n == 0 ? -INFINITY : m - kPfShift<T> + log2f(l);
     if (p.parts > 1) {
-      if (live) p.part_lse[rec * 2 * kPfM + g * kPfM + row] = lse2;
+      if (live) p.part_stat[rec * 2 * kPfM + g * kPfM + row] = make_float2(m, l);
     } else {
       __syncwarp();
       const int ch = lane % (D / 8);  // a row's piece; D / 8 lanes a row
@@ -493,7 +577,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       };
       const int step = min(p.rows, 32);
       for (int r = 32 * rw; r < 32 * rw + 32; r += step) store(pf_row(p, kvh, h0, row0, qs.n, g, r), r, step);
-      if (live && p.lse) p.lse[((int64_t)b * a.Hq + me.head) * p.q.Tq + me.token] = lse2 * 0.6931471805599453f;
+      if (live && p.lse) p.lse[((int64_t)b * a.Hq + me.head) * p.q.Tq + me.token] = lse_of<T>(m, l);
     }
   }
   tc_fence_before();
@@ -502,7 +586,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   if (warp == 0) tc_free<512>(tmem);
 }
 
-// The parts of a row joined: weights 2^(lse_part - M), in part order.  A warp per row.
+// The parts of a row joined: weights l_part 2^(m_part - M), in part order.  A warp per row.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) paged_prefill_join_kernel(PfKernelArgs p, int tiles, int hgs) {
   constexpr int V = D / 32;  // channels of a lane
@@ -516,15 +600,15 @@ __global__ void __launch_bounds__(256) paged_prefill_join_kernel(PfKernelArgs p,
   const int64_t rec = (((int64_t)b * tiles + tile) * hgs + hg) * p.parts;
   auto at = [&](int i) { return (rec + i) * 2 * kPfM + row; };
   float M = -INFINITY;
-  for (int i = lane; i < p.parts; i += 32) M = fmaxf(M, __ldcg(p.part_lse + at(i)));
+  for (int i = lane; i < p.parts; i += 32) M = fmaxf(M, __ldcg(p.part_stat + at(i)).x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float f[V] = {}, L = 0.f;
 #pragma unroll 4
   for (int i = 0; i < p.parts; ++i) {
-    const float lse = __ldcg(p.part_lse + at(i));
-    if (lse == -INFINITY) continue;  // (a NaN goes on)
-    const float w = fast_exp2(lse - M);
+    const float2 ml = __ldcg(p.part_stat + at(i));
+    if (ml.y == 0.f) continue;  // (a NaN goes on)
+    const float w = ml.y * fast_exp2(ml.x - M);
     L += w;
 #pragma unroll
     for (int e = 0; e < V; e += 2) {
@@ -537,7 +621,7 @@ __global__ void __launch_bounds__(256) paged_prefill_join_kernel(PfKernelArgs p,
   T* out = static_cast<T*>(p.out) + (int64_t)b * p.os.batch + (int64_t)me.head * p.os.head + (int64_t)me.token * p.os.token + V * lane;
 #pragma unroll
   for (int e = 0; e < V; e += 2) *reinterpret_cast<uint32_t*>(out + e) = Num<T>::pack(f[e] * il, f[e + 1] * il);
-  if (p.lse && lane == 0) p.lse[((int64_t)b * a.Hq + me.head) * p.q.Tq + me.token] = (M + log2f(L)) * 0.6931471805599453f;
+  if (p.lse && lane == 0) p.lse[((int64_t)b * a.Hq + me.head) * p.q.Tq + me.token] = lse_of<T>(M, L);
 }
 
 template <typename T, int D>
@@ -561,7 +645,7 @@ int paged_prefill_rows(int Tq) {
   return r;
 }
 
-size_t paged_prefill_ws_bytes(int d) { return kWsHeader + (size_t)sm_count() * 2 * kPfM * (d + 1) * 4; }
+size_t paged_prefill_ws_bytes(int d) { return kWsHeader + (size_t)sm_count() * 2 * kPfM * (d + 2) * 4; }
 
 cudaError_t launch_paged_prefill(const PagedArgs& a, int d, int dtype, const PagedMaps& m, const CUtensorMap& qmap,
                                  const PagedQuery& q, const void* v_pool, const void* k_pool, void* out,
@@ -598,7 +682,7 @@ cudaError_t launch_paged_prefill(const PagedArgs& a, int d, int dtype, const Pag
     if (0.85f * ceilf(tiles / parts) + 2.5f + per_part * parts < 0.85f * tiles) p.parts = (int)parts;
   }
   p.part_o = reinterpret_cast<float*>(ws + kWsHeader);
-  p.part_lse = p.part_o + (size_t)sm_count() * 2 * kPfM * d;
+  p.part_stat = reinterpret_cast<float2*>(p.part_o + (size_t)sm_count() * 2 * kPfM * d);
   if (dtype == DKV_BF16)
     return d == 128 ? launch_td<__nv_bfloat16, 128>(p, m, qmap, s) : launch_td<__nv_bfloat16, 64>(p, m, qmap, s);
   return d == 128 ? launch_td<__half, 128>(p, m, qmap, s) : launch_td<__half, 64>(p, m, qmap, s);

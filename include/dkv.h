@@ -487,7 +487,9 @@ DKV_API int dkv_paged_append(const dkv_paged* p, const void* K_new, const void* 
  *            (optional without weights)
  *   weights  optional device fp32 [B][Hkv][max_pages * page_size]: each visible
  *            token's softmax weight, summed over the query heads of its KV head,
- *            is added to its entry; the other entries stay
+ *            is added to its entry; the other entries stay.  A weight is taken
+ *            as exp(score - lse) in fp32: its relative error grows with the
+ *            score, by about 2^-22 |score|
  * The cache's tokens are dealt out evenly to all multiprocessors, across and
  * within sequences, and the parts joined in fp32 in a fixed order.
  */
@@ -519,7 +521,9 @@ DKV_API int dkv_paged_prefill(const dkv_paged* p, const void* q, const dkv_strid
  * tokens only to weigh the cache by them), summed over the queries and the
  * query heads of its KV head, are added to weights[b][h][t].
  *   lse      device fp32 [B][Hq][Tq]: the queries' log-sum-exps (as
- *            dkv_paged_prefill gives them); a query whose value is -inf adds nothing
+ *            dkv_paged_prefill gives them); a query whose value is -inf adds
+ *            nothing, whatever its row holds.  Their rounding goes into the
+ *            weights exp(score - lse): a relative error of about 2^-22 |score|
  *   weights  device fp32 [B][Hkv][max_pages * page_size]; entries of tokens that
  *            no query sees stay
  */

@@ -842,3 +842,51 @@ def test_a_query_whose_lse_is_minus_infinity_adds_no_weight(dtype, d, hq, hkv, T
         rows = Tq * hq // hkv  # (as for the weights of all queries)
         tol = (2 * R.score_error(d, big) + 2.0 ** -20 * (1 + math.log(n)) + 2.0 ** -23 * (rows / 8 + 8)) * added
         assert bool(((weights[0, h, :n].double().cpu() - added).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("dtype,size", [("fp16", 4e4), ("fp16", 1.5e4), ("bf16", 1e7), ("bf16", 2e4)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_scores_of_any_size(dtype, size, sign):
+    """Scores past 2^24, where neighbouring fp32 values are further apart than the exponentials reach: the
+    key with the largest one has all the weight, and keys with equal ones share it.  One channel of q and k is
+    not zero, so that the products are exact; its steps are worth more than 1000 in a score, so that every
+    other weight is below e^-1000."""
+    d, n, hq = 64, 700, 2
+    c = R.Cache([n], 1, d, 64, dtype, seed=60)
+    g = torch.Generator().manual_seed(61)
+    K = torch.zeros(n, d, dtype=torch.float64)
+    K[:, 0] = ((0.5 + 0.5 * torch.rand(n, generator=g)) * size).to(c.dt).double()
+    t = torch.arange(n)
+    c.k[c.table[0].long()[t // 64].cuda(), 0, (t % 64).cuda()] = K.to(c.dt).cuda()
+    q = torch.zeros(1, hq, n, d, dtype=c.dt)
+    q[..., 0] = sign * 0.9 * size
+    scores = q[0, 0, 0, 0].double() * K[:, 0] / math.sqrt(d)
+    table, lens, u = c.table.cuda(), c.dev([n]), torch.finfo(c.dt).eps / 2
+    apart = scores.unique().diff()
+    assert float(apart.min()) > 1000 and float(scores.abs().min()) * 1.4427 > 2 ** 23
+    p = c.layout(hq)
+    V = c.V[0][0]
+
+    def check(out, lse, pos, p_eps, what):
+        for i, at in enumerate(pos):
+            s = scores[:at + 1]
+            top = float(s.max())
+            best = s == top
+            want = V[:at + 1][best].mean(0)
+            tol = u * want.abs() + p_eps * (1 + u) * V[:at + 1][best].abs().mean(0)
+            assert bool(((out[i].double().cpu() - want).abs() <= tol).all()), f"{what}: row at {at}"
+            # the product with log2(e) / sqrt(d), the maximum's part, the logarithm of the count and the way back to base e
+            exact = top + math.log(int(best.sum()))
+            assert abs(float(lse[i]) - exact) <= 2.0 ** -21 * abs(exact), f"{what}: lse at {at}"
+
+    some = [0, 1, 2, 63, 64, 200, 511, 512, 698, 699]
+    out, lse = dkv.dkv_paged_prefill(p, q.cuda(), c.k, c.v, table, lens)
+    for j in range(hq):
+        check(out[0, j][some], lse[0, j][some], some, u, f"prefill {j}")
+    out, lse = dkv.dkv_paged_prefill(p, q[:, :, -5:].cuda(), c.k, c.v, table, lens)  # few queries, keys in parts
+    for j in range(hq):
+        check(out[0, j], lse[0, j], range(n - 5, n), u, f"few queries {j}")
+    for at in some:
+        out, lse = dkv.dkv_paged_decode(p, q[:, :, at].contiguous().cuda(), c.k, c.v, table, c.dev([at + 1]))
+        for j in range(hq):
+            check(out[:, j], lse[:, j], [at], 2.0 ** -16 if dtype == "bf16" else 2.0 ** -21, f"decode {j}")
