@@ -34,8 +34,8 @@ struct WtSmem {
   static constexpr uint32_t kTile = 128 * D * 2;                     // 128 keys or query rows
   static constexpr uint32_t kOffSlots = kStay * kTile;
   static constexpr uint32_t kOffLse = kOffSlots + kSlots * kTile;    // [warpgroup][128] minus base-2 lse
-  static constexpr uint32_t kOffRank = kOffLse + 4 * kWtN * 4;       // [rank][256] sums of the cluster
-  static constexpr uint32_t kOffBar = kOffRank + kCluster * 2 * kWtM * 4;
+  static constexpr uint32_t kOffRank = kOffLse + 4 * kWtN * 4;       // [block % 2][rank][256] sums of the cluster
+  static constexpr uint32_t kOffBar = kOffRank + 2 * kCluster * 2 * kWtM * 4;
   static constexpr uint32_t kOffPrefix = kOffBar + 256;              // [B + 1] (few queries)
 };
 
@@ -298,7 +298,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 }
 
 // ---------------------------------------------------------------- many queries
-template <typename T, int D>
+// A cluster takes 256 keys of one unit (LOOP: blocks y, y + gridDim.y, ... of them; the rings of operand
+// tiles and scores run on from block to block, and a block's keys are loaded when the last one's sums are
+// done).
+template <typename T, int D, bool LOOP>
 __global__ void __launch_bounds__(kWtThreads, 1) __cluster_dims__(kCluster, 1, 1)
     paged_weights_kernel(WtArgs p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -306,100 +309,125 @@ __global__ void __launch_bounds__(kWtThreads, 1) __cluster_dims__(kCluster, 1, 1
   const PagedArgs& a = p.a;
   const int warp = threadIdx.x >> 5, rank = (int)cluster_ctarank(), qn = p.rows;
   // of all units the earlier keys, which more queries see, first
-  const int u = (int)blockIdx.x / kCluster, b = u / a.Hkv, h = u % a.Hkv, k0 = (int)blockIdx.y * 2 * kWtM;
+  const int u = (int)blockIdx.x / kCluster, b = u / a.Hkv, h = u % a.Hkv;
   const QuerySpan qs = query_span(a, p.q.q_lens, p.q.Tq, b);
-  // query rows that see one of the keys
-  const int r_lo = max(0, k0 - qs.off);
-  int r_hi = qs.n - 1;
-  if (a.window > 0 && k0 >= a.sinks) r_hi = (int)min((int64_t)r_hi, (int64_t)k0 + 2 * kWtM - 2 + a.window - qs.off);
-  if (k0 >= qs.len || r_lo > r_hi) return;  // the same answer in every CTA of a cluster
-  // this CTA's share of the head-by-head list of query tiles
-  const int t_lo = r_lo / qn, per = r_hi / qn - t_lo + 1, all = per * a.G;
-  const int c0 = (int)((int64_t)all * rank / kCluster), n = (int)((int64_t)all * (rank + 1) / kCluster) - c0;
+  // first and last query row that sees one of the keys from k0 on
+  auto row_lo = [&](int k0) { return max(0, k0 - qs.off); };
+  auto row_hi = [&](int k0) {
+    int hi = qs.n - 1;
+    if (a.window > 0 && k0 >= a.sinks) hi = (int)min((int64_t)hi, (int64_t)k0 + 2 * kWtM - 2 + a.window - qs.off);
+    return hi;
+  };
+  // the next block from k0 on that a query sees (the same answer in every CTA of a cluster)
+  const int step = (int)gridDim.y * 2 * kWtM;
+  auto seen_from = [&](int k0) {
+    while (k0 < qs.len && row_lo(k0) > row_hi(k0)) k0 += step;
+    return k0;
+  };
+  int k0 = (int)blockIdx.y * 2 * kWtM;
+  if (LOOP) k0 = seen_from(k0);
+  if (k0 >= qs.len || (!LOOP && row_lo(k0) > row_hi(k0))) return;
   cluster_arrive_relaxed();  // the CTAs that rank 0 hears from may find it not yet started
   WtBars bar;
   const uint32_t tmem = wt_start<D>(smem, bar, &kmap, &qmap), sb = smem_u32(smem), slots = sb + S::kOffSlots;
   cluster_wait();
   float* lse2 = reinterpret_cast<float*>(smem + S::kOffLse);
-  float* ranks = reinterpret_cast<float*>(smem + S::kOffRank);
   bool ok = true;
+  int blk = 0, i0 = 0;    // blocks and steps before this block
+  int even = 0, odd = 0;  // and the steps among them of warpgroups 0 and 1, and of 2 and 3
+  do {
+    const int r_lo = row_lo(k0), r_hi = row_hi(k0);
+    // this CTA's share of the head-by-head list of query tiles
+    const int t_lo = r_lo / qn, per = r_hi / qn - t_lo + 1, all = per * a.G;
+    const int c0 = (int)((int64_t)all * rank / kCluster), n = (int)((int64_t)all * (rank + 1) / kCluster) - c0;
+    float* ranks = reinterpret_cast<float*>(smem + S::kOffRank) + (blk & 1) * kCluster * 2 * kWtM;  // (rank 0 may still read the last block's)
 
-  if (warp == 16) {
-    // =========================== loads
-    const uint32_t el = elect_one();
-    const int rows = min(a.page_mask + 1, 64), k_lo = paged_window_lo(a, max(qs.off, 0));
-    if (el) mbar_arrive_expect_tx(bar.stay_full, kStay * S::kTile);
-    for (int x = 0; x < kStay; ++x)
-      wt_load_keys<D>(a, &kmap, h, k0 + x * kWtM, rows, wt_page(a, b, qs.len, k_lo, k0 + x * kWtM, rows), sb + x * S::kTile,
-                      bar.stay_full, el);
-    int i = 0, hd = c0 / per, tl = c0 % per;
-    for (; i < n; ++i) {
-      const int sl = i % kSlots;
-      if (i >= kSlots) ok = mbar_wait(&bar.empty[sl], (uint32_t)((i / kSlots - 1) & 1), a.err);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      wt_load_queries<D>(&qmap, b, h * a.G + hd, 1, (t_lo + tl) * qn, qn, slots + sl * S::kTile, &bar.full[sl], el);
-      if (++tl == per) { tl = 0; ++hd; }
-    }
-    // every copy has landed before the CTA may end (also after a wait that gave up)
-    mbar_wait(bar.stay_full, 0, a.err);
-    for (int y = max(0, i - kSlots); y < i; ++y) mbar_wait(&bar.full[y % kSlots], (uint32_t)((y / kSlots) & 1), a.err);
-  } else if (warp == 17) {
-    // =========================== products: key tile x of step i to warpgroup 2 (i % 2) + x
-    const uint32_t el = elect_one(), id = tc_idesc(Num<T>::kUmma, false, (uint32_t)qn);
-    auto wait = [&](uint64_t* b, int parity) { return ok = __all_sync(0xffffffffu, ok && mbar_wait(b, (uint32_t)parity, a.err)); };
-    wait(bar.stay_full, 0);
-    for (int i = 0; i < n && ok; ++i) {
-      const int sl = i % kSlots;
-      if (!wait(&bar.full[sl], (i / kSlots) & 1)) break;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int w = 2 * (i & 1) + x;
-        if (i >= 2 && !wait(&bar.s_empty[w], (i / 2 - 1) & 1)) break;
-        wt_product<D>(tmem + 128u * w, sb + x * S::kTile, slots + sl * S::kTile, qn, id, el);
-        tc_commit(&bar.s_full[w], el);
+    if (warp == 16) {
+      // =========================== loads
+      const uint32_t el = elect_one();
+      const int rows = min(a.page_mask + 1, 64), k_lo = paged_window_lo(a, max(qs.off, 0));
+      if (!LOOP || ok) {
+        if (el) mbar_arrive_expect_tx(bar.stay_full, kStay * S::kTile);
+        for (int x = 0; x < kStay; ++x)
+          wt_load_keys<D>(a, &kmap, h, k0 + x * kWtM, rows, wt_page(a, b, qs.len, k_lo, k0 + x * kWtM, rows), sb + x * S::kTile,
+                          bar.stay_full, el);
+        int i = 0, hd = c0 / per, tl = c0 % per;
+        for (; i < n; ++i) {
+          const int at = i0 + i, sl = at % kSlots;
+          if (at >= kSlots) ok = mbar_wait(&bar.empty[sl], (uint32_t)((at / kSlots - 1) & 1), a.err);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          wt_load_queries<D>(&qmap, b, h * a.G + hd, 1, (t_lo + tl) * qn, qn, slots + sl * S::kTile, &bar.full[sl], el);
+          if (++tl == per) { tl = 0; ++hd; }
+        }
+        // every copy has landed before the CTA may end (also after a wait that gave up)
+        mbar_wait(bar.stay_full, (uint32_t)(blk & 1), a.err);
+        for (int y = max(0, i0 + i - kSlots); y < i0 + i; ++y) mbar_wait(&bar.full[y % kSlots], (uint32_t)((y / kSlots) & 1), a.err);
       }
-      tc_commit(&bar.empty[sl], el);
-    }
-    if (!ok) wt_drain(bar, a.err, el);
-  } else {
-    // =========================== sums: one key per thread
-    const int w = warp >> 2, row = threadIdx.x & 127, t = k0 + (w & 1) * kWtM + row;
-    float* l2 = lse2 + kWtN * w;
-    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    // this warpgroup's steps w / 2, w / 2 + 2, ...: head and query tile of each
-    int i = w >> 1, hd = (c0 + i) / per, tl = (c0 + i) % per;
-    const float* lse = p.lse + ((int64_t)b * a.Hq + h * a.G) * p.q.Tq;
-    auto fetch = [&]() {
-      const int r = (t_lo + tl) * qn + row;
-      return row < qn && r < qs.n ? __ldg(lse + (int64_t)hd * p.q.Tq + r) : -INFINITY;
-    };
-    float next = i < n ? fetch() : 0.f;
-    for (int k = 0; i < n; i += 2, ++k) {
-      const int r0 = (t_lo + tl) * qn;
-      l2[row] = wt_minus_lse2(next);
-      tl += 2;
-      while (tl >= per) { tl -= per; ++hd; }
-      if (i + 2 < n) next = fetch();
-      const bool left_out = named_bar_any(1 + w, 128, l2[row] == -INFINITY);
-      ok = wt_sum(a, qs, tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 128u * w, qn, qn, r0, t, l2, left_out, &bar.s_full[w], &bar.s_empty[w],
-                  (uint32_t)(k & 1), acc, ok);
-      named_bar_sync(1 + w, 128);  // l2 is read
-    }
-    // the two warpgroups of these keys, then the ranks, in order
-    const float sum = wt_total(acc);
-    if (w >= 2) l2[row] = sum;
-    named_bar_sync(5, 512);
-    if (w < 2) st_cluster_f32(ranks + rank * 2 * kWtM + w * kWtM + row, 0, sum + lse2[kWtN * (w + 2) + row]);
-  }
-  wt_end(tmem);
-  cluster_sync();
-  const int t = k0 + (int)threadIdx.x;
-  if (rank == 0 && threadIdx.x < 2 * kWtM && t < qs.len) {
-    float sum = 0.f;
+    } else if (warp == 17) {
+      // =========================== products: key tile x of step i to warpgroup 2 (i % 2) + x
+      const uint32_t el = elect_one(), id = tc_idesc(Num<T>::kUmma, false, (uint32_t)qn);
+      auto wait = [&](uint64_t* b, int parity) { return ok = __all_sync(0xffffffffu, ok && mbar_wait(b, (uint32_t)parity, a.err)); };
+      wait(bar.stay_full, blk & 1);
+      for (int i = 0; i < n && ok; ++i) {
+        const int at = i0 + i, sl = at % kSlots, turn = (i & 1 ? odd : even) + (i >> 1);
+        if (!wait(&bar.full[sl], (at / kSlots) & 1)) break;
 #pragma unroll
-    for (int r = 0; r < kCluster; ++r) sum += ranks[r * 2 * kWtM + threadIdx.x];
-    p.weights[(size_t)u * a.cap + t] += sum;
-  }
+        for (int x = 0; x < 2; ++x) {
+          const int w = 2 * (i & 1) + x;
+          if (turn >= 1 && !wait(&bar.s_empty[w], (turn - 1) & 1)) break;
+          wt_product<D>(tmem + 128u * w, sb + x * S::kTile, slots + sl * S::kTile, qn, id, el);
+          tc_commit(&bar.s_full[w], el);
+        }
+        tc_commit(&bar.empty[sl], el);
+      }
+      if (!ok) wt_drain(bar, a.err, el);
+    } else {
+      // =========================== sums: one key per thread
+      const int w = warp >> 2, row = threadIdx.x & 127, t = k0 + (w & 1) * kWtM + row;
+      float* l2 = lse2 + kWtN * w;
+      float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      // this warpgroup's steps w / 2, w / 2 + 2, ...: head and query tile of each
+      int i = w >> 1, hd = (c0 + i) / per, tl = (c0 + i) % per;
+      const float* lse = p.lse + ((int64_t)b * a.Hq + h * a.G) * p.q.Tq;
+      auto fetch = [&]() {
+        const int r = (t_lo + tl) * qn + row;
+        return row < qn && r < qs.n ? __ldg(lse + (int64_t)hd * p.q.Tq + r) : -INFINITY;
+      };
+      float next = i < n ? fetch() : 0.f;
+      for (int k = w >> 1 ? odd : even; i < n; i += 2, ++k) {
+        const int r0 = (t_lo + tl) * qn;
+        l2[row] = wt_minus_lse2(next);
+        tl += 2;
+        while (tl >= per) { tl -= per; ++hd; }
+        if (i + 2 < n) next = fetch();
+        const bool left_out = named_bar_any(1 + w, 128, l2[row] == -INFINITY);
+        ok = wt_sum(a, qs, tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 128u * w, qn, qn, r0, t, l2, left_out, &bar.s_full[w], &bar.s_empty[w],
+                    (uint32_t)(k & 1), acc, ok);
+        named_bar_sync(1 + w, 128);  // l2 is read
+      }
+      // the two warpgroups of these keys, then the ranks, in order
+      const float sum = wt_total(acc);
+      if (w >= 2) l2[row] = sum;
+      named_bar_sync(5, 512);
+      if (w < 2) st_cluster_f32(ranks + rank * 2 * kWtM + w * kWtM + row, 0, sum + lse2[kWtN * (w + 2) + row]);
+    }
+    if (LOOP) __syncthreads();
+    else wt_end(tmem);
+    cluster_sync();
+    const int t = k0 + (int)threadIdx.x;
+    if (rank == 0 && threadIdx.x < 2 * kWtM && t < qs.len) {
+      float sum = 0.f;
+#pragma unroll
+      for (int r = 0; r < kCluster; ++r) sum += ranks[r * 2 * kWtM + threadIdx.x];
+      p.weights[(size_t)u * a.cap + t] += sum;
+    }
+    if (!LOOP) return;
+    ++blk;
+    i0 += n;
+    even += (n + 1) >> 1;
+    odd += n >> 1;
+  } while ((k0 = seen_from(k0 + step)) < qs.len);
+  wt_end(tmem);
 }
 
 // Columns of a head when the queries of all heads of a group fit one tile (0: they do not).
@@ -411,11 +439,17 @@ int few_rows(int G, int Tq) {
 
 template <typename T, int D>
 cudaError_t launch_td(const WtArgs& p, bool few, const CUtensorMap& kmap, const CUtensorMap& qmap, cudaStream_t s) {
-  const auto kernel = few ? paged_weights_few_kernel<T, D> : paged_weights_kernel<T, D>;
+  // Many queries: a cluster for each block of keys of each unit that the table has room for, or, where that
+  // is more than four for each place (38 of four multiprocessors), so many that walk the blocks in turn: the
+  // table says nothing of the lengths, and a cluster without a block holds its place for 0.7 us.  64 prompts
+  // of 2048, 8 heads, d 128: 1464 us in turn, 1510 one by one, and 6950 one by one under a table for 131072
+  // tokens; one prompt of 8192, 2 heads: 94 us in turn, 90 one by one (64 clusters, so taken).
+  const int units = p.a.B * p.a.Hkv, blocks = (p.a.cap + 2 * kWtM - 1) / (2 * kWtM), most = (sm_count() + units - 1) / units;
+  const auto kernel = few ? paged_weights_few_kernel<T, D> : blocks <= most ? paged_weights_kernel<T, D, false> : paged_weights_kernel<T, D, true>;
+  const dim3 grid = few ? dim3(sm_count()) : dim3(units * kCluster, blocks < most ? blocks : most);
   const size_t smem = WtSmem<D>::kOffPrefix + (few ? ((size_t)p.a.B + 1) * 4 : 0);
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
-  const dim3 grid = few ? dim3(sm_count()) : dim3(p.a.B * p.a.Hkv * kCluster, (p.a.cap + 2 * kWtM - 1) / (2 * kWtM));
   kernel<<<grid, kWtThreads, smem, s>>>(p, kmap, qmap);
   return cudaGetLastError();
 }

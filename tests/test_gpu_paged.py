@@ -890,3 +890,86 @@ def test_scores_of_any_size(dtype, size, sign):
         out, lse = dkv.dkv_paged_decode(p, q[:, :, at].contiguous().cuda(), c.k, c.v, table, c.dev([at + 1]))
         for j in range(hq):
             check(out[:, j], lse[:, j], [at], 2.0 ** -16 if dtype == "bf16" else 2.0 ** -21, f"decode {j}")
+
+
+WIDE = [
+    # dtype, d, hq, hkv, page, lens, q_lens, Tq, window, sinks: tables for many times the lengths
+    ("bf16", 128, 4, 2, 64, [1024], None, 16, 0, 0),
+    ("fp16", 64, 8, 8, 16, [333, 2001, 1, 700], [32, 32, 1, 9], 32, 0, 0),
+    ("bf16", 64, 3, 1, 256, [300, 4000], [1, 100], 100, 500, 4),
+    ("fp16", 128, 6, 1, 32, [1300, 600, 700], [1300, 600, 500], 1300, 0, 0),
+    ("bf16", 64, 2, 1, 64, [700] * 40, None, 300, 256, 3),
+]
+
+
+@pytest.mark.parametrize("dtype,d,hq,hkv,page,lens,q_lens,Tq,window,sinks", WIDE)
+def test_a_wide_page_table_changes_no_result(dtype, d, hq, hkv, page, lens, q_lens, Tq, window, sinks):
+    """A table for 131072 tokens: grids that are reckoned from it find most of their work missing."""
+    c = R.Cache(lens, hkv, d, page, dtype, seed=70, width=131072 // page)
+    p = c.layout(hq, window, sinks)
+    ws = workspace(p)
+    n_q = q_lens or [Tq] * c.B
+    q = queries((c.B, hq, Tq, d), c.dt, 71)
+    ql = None if q_lens is None else c.dev(q_lens)
+    table = c.hidden_table([n - m for n, m in zip(lens, n_q)], window, sinks)
+    out, lse = dkv.dkv_paged_prefill(p, q.cuda(), c.k, c.v, table, c.dev(lens), q_lens=ql, workspace=ws)
+    no_fault(ws)
+    weights = torch.zeros(c.B, hkv, c.width * page, device="cuda")
+    dkv.dkv_paged_weights(p, q.cuda(), lse, c.k, table, c.dev(lens), weights, q_lens=ql, workspace=ws)
+    no_fault(ws)
+    for b in range(0, c.B, 7 if c.B > 10 else 1):
+        pos = torch.arange(n_q[b]) + lens[b] - n_q[b]
+        assert bool((weights[b, :, lens[b]:] == 0).all())
+        for h in range(hkv):
+            added, big = torch.zeros(lens[b], dtype=torch.float64), 0.0
+            for j in range(h * hq // hkv, (h + 1) * hq // hkv):
+                ref = R.attend(q[b, j, :n_q[b]].double(), c.K[b][h], c.V[b][h], pos, window, sinks)
+                R.check_rows(out[b, j, :n_q[b]], lse[b, j, :n_q[b]], ref, d, c.dt, torch.finfo(c.dt).eps / 2, f"sequence {b} head {j}")
+                added += ref[2].sum(0)
+                big = max(big, ref[4])
+            rows = n_q[b] * hq // hkv
+            tol = (2 * R.score_error(d, big) + 2.0 ** -20 * (1 + math.log(max(2, lens[b]))) + 2.0 ** -23 * (rows / 8 + 8)) * added
+            assert bool(((weights[b, h, :lens[b]].double().cpu() - added).abs() <= tol + 2.0 ** -40).all()), f"weights of {b} {h}"
+
+
+def _microseconds(f):
+    """The quickest of a dozen calls, each replayed from a graph."""
+    f()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(4):
+            f()
+    best = math.inf
+    for _ in range(12):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        graph.replay()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 250)
+    return best
+
+
+def _tight_and_wide(call):
+    """Times of call(width of the table in tokens) on a table of the sequences' length and on one for 131072."""
+    return _microseconds(call(1024)), _microseconds(call(131072))
+
+
+def _uniform(B, hkv, d, tokens, G):
+    n, page = 1024, 64
+    c = R.Cache([n] * B, hkv, d, page, "bf16", seed=72, width=tokens // page)
+    return c, c.layout(G * hkv), c.table.cuda(), c.dev(c.lens)
+
+
+@pytest.mark.parametrize("B,hkv,G,Tq,d", [(16, 2, 4, 1024, 64), (8, 2, 8, 32, 128)])
+def test_the_time_of_weights_goes_by_the_lengths(B, hkv, G, Tq, d):
+    """Twice the time on a table of 128 times the length would be the table's (it was 10 to 15 times)."""
+    def call(tokens):
+        c, p, table, lens = _uniform(B, hkv, d, tokens, G)
+        ws, q = workspace(p), queries((B, G * hkv, Tq, d), c.dt, 73).cuda()
+        lse, weights = torch.full((B, G * hkv, Tq), 8.0, device="cuda"), torch.zeros(B, hkv, tokens, device="cuda")
+        return lambda: dkv.dkv_paged_weights(p, q, lse, c.k, table, lens, weights, workspace=ws)
+
+    tight, wide = _tight_and_wide(call)
+    assert wide < 2 * tight, f"{wide:.1f} us, {tight:.1f} on the narrow table"
