@@ -77,11 +77,23 @@ struct PfKernelArgs {
   int by_heads;  // the groups hold different heads (else two 128-token tiles of one head)
   int heads;     // heads of a CTA
   int per_kv;    // CTAs that share the heads of a KV head
-  int parts;     // parts of each CTA's key tiles
+  int parts;     // parts of a row tile's keys at most
+  float tile_us, part_us, ratio;  // times of a key tile, and of a part; the first over the second
   float* part_o;     // [CTA][part][256 rows][d] and
   float2* part_stat; // [CTA][part][256 rows] maximum and sum, when parts > 1 (a log-sum-exp would lose a sum
                      // beside a large maximum)
 };
+
+// Parts of `tiles` key tiles: as many as take the least time by the model, with kPfJoin us for the join, one
+// where that takes no longer.  The grid and its join have to agree, so the roundings are spelled out.
+constexpr float kPfJoin = 2.5f;
+__device__ inline int pf_parts(const PfKernelArgs& p, int tiles) {
+  if (p.parts < 2) return 1;
+  const int parts = min(min((int)rintf(__fsqrt_rn(__fmul_rn(p.ratio, (float)tiles))), p.parts), tiles);
+  if (parts < 2) return 1;
+  const float whole = __fmul_rn(p.tile_us, (float)tiles), cut = __fadd_rn(__fmul_rn(p.tile_us, (float)((tiles + parts - 1) / parts)), __fadd_rn(__fmul_rn(p.part_us, (float)parts), kPfJoin));
+  return cut < whole ? parts : 1;
+}
 
 // Row `row` of group g of a CTA's 256: its head and token.
 struct PfRow {
@@ -227,8 +239,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   const int hdB = p.by_heads ? max(0, min(kPfM / p.rows, a.G - h0 - kPfM / p.rows)) : (tokB > 0 ? 1 : 0);
   const int p_lo = qs.off + row0, p_hi = p_lo + (p.by_heads ? tokA : tokA + tokB) - 1;
   const KeySpan<kPfN> ks = key_span<kPfN>(a, p_lo, p_hi);
+  const int parts = pf_parts(p, ks.n);
+  if (part >= parts) return;  // fewer than a sequence of the table's length would take
   // this part's key tiles; group A's may end a tile or two before B's
-  const int t0 = (int)((int64_t)ks.n * part / p.parts), t1 = (int)((int64_t)ks.n * (part + 1) / p.parts);
+  const int t0 = (int)((int64_t)ks.n * part / parts), t1 = (int)((int64_t)ks.n * (part + 1) / parts);
   const int endA = p.by_heads ? ks.n : min(ks.n, max(0, ks.st + (max(0, p_lo + tokA) + kPfN - 1) / kPfN - ks.wt0));
   const int nA = max(0, min(endA, t1) - t0), nB = hdB > 0 ? t1 - t0 : 0;
   const int nt = max(nA, nB);
@@ -547,7 +561,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
         for (int e = 0; e < 32; ++e) f[e] += more[e];
       }
-      if (p.parts > 1) {
+      if (parts > 1) {
         if (live) {
           float* o32 = p.part_o + (rec * 2 * kPfM + g * kPfM + row) * D + 32 * c;
 #pragma unroll
@@ -561,7 +575,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                make_uint4(Num<T>::pack(f[e], f[e + 1]), Num<T>::pack(f[e + 2], f[e + 3]), Num<T>::pack(f[e + 4], f[e + 5]),
                           Num<T>::pack(f[e + 6], f[e + 7])));
     }
-    if (p.parts > 1) {
+    if (parts > 1) {
       if (live) p.part_stat[rec * 2 * kPfM + g * kPfM + row] = make_float2(m, l);
     } else {
       __syncwarp();
@@ -595,17 +609,20 @@ __global__ void __launch_bounds__(256) paged_prefill_join_kernel(PfKernelArgs p,
   const int b = blockIdx.z, tile = (int)blockIdx.y / hgs, hg = (int)blockIdx.y % hgs, lane = threadIdx.x & 31;
   const int row = (int)blockIdx.x * 8 + (threadIdx.x >> 5);
   const QuerySpan qs = query_span(a, p.q.q_lens, p.q.Tq, b);
-  const PfRow me = pf_row(p, hg / p.per_kv, hg % p.per_kv * p.heads, tile * (p.by_heads ? p.rows : 2 * kPfM), qs.n, row / kPfM, row % kPfM);
+  const int row0 = tile * (p.by_heads ? p.rows : 2 * kPfM), p_lo = qs.off + row0;
+  const PfRow me = pf_row(p, hg / p.per_kv, hg % p.per_kv * p.heads, row0, qs.n, row / kPfM, row % kPfM);
   if (!me.live) return;
+  const int parts = pf_parts(p, key_span<kPfN>(a, p_lo, p_lo + min(p.by_heads ? p.rows : 2 * kPfM, qs.n - row0) - 1).n);
+  if (parts < 2) return;  // written by its one part
   const int64_t rec = (((int64_t)b * tiles + tile) * hgs + hg) * p.parts;
   auto at = [&](int i) { return (rec + i) * 2 * kPfM + row; };
   float M = -INFINITY;
-  for (int i = lane; i < p.parts; i += 32) M = fmaxf(M, __ldcg(p.part_stat + at(i)).x);
+  for (int i = lane; i < parts; i += 32) M = fmaxf(M, __ldcg(p.part_stat + at(i)).x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float f[V] = {}, L = 0.f;
 #pragma unroll 4
-  for (int i = 0; i < p.parts; ++i) {
+  for (int i = 0; i < parts; ++i) {
     const float2 ml = __ldcg(p.part_stat + at(i));
     if (ml.y == 0.f) continue;  // (a NaN goes on)
     const float w = ml.y * fast_exp2(ml.x - M);
@@ -669,17 +686,23 @@ cudaError_t launch_paged_prefill(const PagedArgs& a, int d, int dtype, const Pag
   // for every value that a part leaves and the join reads.  That fits these times (us; the number of parts
   // in front) of 32 heads at d 128 to within 1.5: 16 queries over 1024 keys 1: 17.9, 2: 15.6, 4: 13.2; over
   // 4096 keys 4: 21.7, 8: 18.0, 16: 23.2; 128 over 1024 1: 20.7, 2: 20.9, 4: 19.3; 512 over 1024 1: 20.6,
-  // 2: 25.2.  The tiles are those of the longest sequence that the table allows.
+  // 2: 25.2.  At d 64 a tile takes 0.6 and the rule is not refitted: 16 queries over 1024 keys 1: 15.4, 2: 13.1,
+  // 4: 10.7, 8: 10.6, the rule's 11.1; over 4096 keys 1: 44.6, 4: 18.3, 8: 14.1, 16: 14.9, the rule's 15.2.  Under
+  // a window of 1024 the same as over 1024 keys (d 128 4: 13.7, the rule's 13.9).  The grid has room for the parts
+  // of the longest sequence that the table allows; how many there are goes by the keys that are there.
   const int tokens = p.by_heads ? p.rows : 2 * kPfM;
   const int64_t ctas = (int64_t)a.Hkv * p.per_kv * a.B * ((q.Tq + tokens - 1) / tokens);
   const int64_t keys = a.window > 0 && (int64_t)a.window + a.sinks + tokens < a.cap ? (int64_t)a.window + a.sinks + tokens : a.cap;
   const int64_t fit = sm_count() / ctas;
+  p.tile_us = 0.85f;
+  p.part_us = 0.65f + 2e-6f * (float)d * (float)a.B * (float)a.Hq * (float)q.Tq;
+  p.ratio = p.tile_us / p.part_us;
   p.parts = 1;
   if (fit > 1) {
-    const float tiles = (float)((keys + kPfN - 1) / kPfN), per_part = 0.65f + 2e-6f * (float)d * (float)a.B * (float)a.Hq * (float)q.Tq;
-    float parts = rintf(sqrtf(0.85f * tiles / per_part));
+    const float tiles = (float)((keys + kPfN - 1) / kPfN);
+    float parts = rintf(sqrtf(p.ratio * tiles));
     parts = fminf(fmaxf(parts, 1.f), fminf((float)fit, tiles));
-    if (0.85f * ceilf(tiles / parts) + 2.5f + per_part * parts < 0.85f * tiles) p.parts = (int)parts;
+    if (p.tile_us * ceilf(tiles / parts) + kPfJoin + p.part_us * parts < p.tile_us * tiles) p.parts = (int)parts;
   }
   p.part_o = reinterpret_cast<float*>(ws + kWsHeader);
   p.part_stat = reinterpret_cast<float2*>(p.part_o + (size_t)sm_count() * 2 * kPfM * d);

@@ -973,3 +973,17 @@ def test_the_time_of_weights_goes_by_the_lengths(B, hkv, G, Tq, d):
 
     tight, wide = _tight_and_wide(call)
     assert wide < 2 * tight, f"{wide:.1f} us, {tight:.1f} on the narrow table"
+
+
+@pytest.mark.parametrize("B,hkv,G,Tq,d", [(1, 1, 8, 16, 128), (8, 1, 8, 8, 64)])
+def test_the_time_of_few_queries_goes_by_the_lengths(B, hkv, G, Tq, d):
+    """On a table of 128 times the length the grid is one of more parts, which return at once (it took 1.5 to
+    2 times the time, while every part left and joined its rows)."""
+    def call(tokens):
+        c, p, table, lens = _uniform(B, hkv, d, tokens, G)
+        ws, q = workspace(p), queries((B, G * hkv, Tq, d), c.dt, 74).cuda()
+        out, lse = torch.empty_like(q), torch.empty(B, G * hkv, Tq, device="cuda")
+        return lambda: dkv.dkv_paged_prefill(p, q, c.k, c.v, table, lens, out=out, lse=lse, workspace=ws)
+
+    tight, wide = _tight_and_wide(call)
+    assert wide < 1.3 * tight, f"{wide:.1f} us, {tight:.1f} on the narrow table"
