@@ -1,8 +1,8 @@
 // dkv_paged_evict: keep the heaviest tokens of every (sequence, KV head) and move them
 // together.
 //
-// select: a unit's tokens are split over a cluster of CTAs (one CTA up to kSelStage tokens of
-// capacity, kSelCluster beyond).  They bring the weights' order-preserving integer images into
+// select: a unit's tokens are split over a cluster of CTAs (kSelCluster where the table has room for
+// more than kSelStage, of which one does the work of a shorter sequence; else a CTA alone).  They bring the weights' order-preserving integer images into
 // shared memory, find the smallest image that stays by radix selection (three passes of 11, 11
 // and 10 bits over histograms that every CTA adds up from all of them through distributed shared
 // memory), then write the kept positions, ascending, from one scan that counts certain and equal
@@ -136,10 +136,16 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(PagedArgs a, 
     for (int j = me; j < n; j += all) kept[j] = j;
     return;
   }
+  const bool alone = CL == 1 || len <= kSelStage;
+  if (alone && rank > 0) return;
+  auto sync = [&]() {
+    if (alone) __syncthreads();
+    else cluster_sync();
+  };
   // candidates [c0, c1); the tokens around them stay whatever they weigh
   const int c0 = e.first, c1 = len - e.recent;
   // this CTA's tokens
-  const int share = (len + CL - 1) / CL, t0 = min(rank * share, len), t1 = min(t0 + share, len);
+  const int share = alone ? len : (len + CL - 1) / CL, t0 = min(rank * share, len), t1 = min(t0 + share, len);
   const float* w = e.weights + (size_t)u * a.cap;
   const bool staged = share <= kSelStage;
   if (staged) {
@@ -161,14 +167,13 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(PagedArgs a, 
         const uint32_t x = image(t);
         if ((x & mask) == thr) atomicAdd(&hist[(x >> shift[p]) & (bins - 1)], 1);
       }
-      if (CL > 1) cluster_sync();
-      else __syncthreads();
+      sync();
       // the digit with fewer than k images above it and at least k down to it: thread i takes the
       // i-th group of bins from the top
       const int per = bins / kSelThreads, top = bins - 1 - tid * per;
       int cnt[2] = {0, 0};
       for (int i = 0; i < per; ++i) {
-        if (CL == 1) cnt[i] = hist[top - i];
+        if (alone) cnt[i] = hist[top - i];
         else {
 #pragma unroll
           for (int r = 0; r < CL; ++r) cnt[i] += ld_cluster_s32(&hist[top - i], r);
@@ -182,8 +187,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(PagedArgs a, 
         if (lane >= o) scan += y;
       }
       if (lane == 31) wsum[warp] = scan;
-      if (CL > 1) cluster_sync();  // (the histograms are read)
-      else __syncthreads();
+      sync();  // (the histograms are read)
       const int before = lane < warp ? wsum[lane] : 0;
       const int above = scan - sum + __reduce_add_sync(0xffffffffu, before);
       if (above < k && above + sum >= k) {
@@ -214,7 +218,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(PagedArgs a, 
     }
   };
   int out = 0, ties = 0;  // certain and equal images before this CTA's tokens, then before the chunk
-  if (CL > 1) {
+  if (!alone) {
     int mk = 0, mt = 0;
     for (int base = t0; base < t1; base += kSelThreads * kSelPer) {
       uint32_t keep, tie;
@@ -265,7 +269,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(PagedArgs a, 
     ties += chunk >> 16;
     __syncthreads();
   }
-  if (CL > 1) cluster_sync();  // nobody leaves while another reads its counts
+  if (!alone) cluster_sync();  // nobody leaves while another reads its counts
 }
 
 template <int D>

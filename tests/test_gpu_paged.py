@@ -987,3 +987,22 @@ def test_the_time_of_few_queries_goes_by_the_lengths(B, hkv, G, Tq, d):
 
     tight, wide = _tight_and_wide(call)
     assert wide < 1.3 * tight, f"{wide:.1f} us, {tight:.1f} on the narrow table"
+
+
+def test_the_time_of_eviction_goes_by_the_lengths():
+    """The selection took a cluster's time for every sequence under a table for more tokens than one block of
+    threads holds, however short they were (110 us here, 11 on the narrow table)."""
+    B, hkv, n, m, page = 16, 4, 1024, 512, 64
+
+    def call(tokens):
+        c = R.Cache([n] * B, hkv, 64, page, "bf16", seed=75, width=tokens // page, spare=B * m // page)
+        p, ws, to = c.layout(hkv), None, c.free.view(B, m // page).cuda()
+        ws, weights = workspace(p), torch.rand(B, hkv, tokens, device="cuda")
+        kept, lens = torch.empty(B, hkv, m, dtype=torch.int32, device="cuda"), torch.empty(B, dtype=torch.int32, device="cuda")
+        table, n_d, after = c.table.cuda(), c.dev(c.lens), torch.empty_like(weights)
+        return lambda: dkv.dkv_paged_evict(p, c.k, c.v, table, n_d, weights, m, 4, 16, to, kept=kept, new_lens=lens,
+                                           new_weights=after, workspace=ws)
+
+    tight, wide = _microseconds(call(n)), _microseconds(call(131072))
+    zeros = B * hkv * 131072 * 4 / 3e6  # us to write the weights' tails at 3 TB/s
+    assert wide < 2 * tight + zeros, f"{wide:.1f} us, {tight:.1f} on the narrow table"
