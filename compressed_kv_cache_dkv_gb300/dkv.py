@@ -447,6 +447,12 @@ def _paged_ws(p: dkv_paged, workspace, dev: int, with_weights: bool = False) -> 
     return ws
 
 
+def _int32(what: str, *numbers: int) -> None:
+    """Refuses what an int32 argument would hold as another number."""
+    if not all(-0x80000000 <= x <= 0x7fffffff for x in numbers):
+        raise DkvError(DKV_ERR_ARG, what)
+
+
 def dkv_paged_layout(k_pages: torch.Tensor, batch: int, n_q_heads: int, max_pages: int, window: int = 0,
                      sinks: int = 0) -> dkv_paged:
     """Descriptor of a paged cache from one of its pools, fp16 or bf16 [n_pages, Hkv, page_size, d]
@@ -456,6 +462,7 @@ def dkv_paged_layout(k_pages: torch.Tensor, batch: int, n_q_heads: int, max_page
     if k_pages.dim() != 4 or k_pages.dtype not in _PAGED_DTYPES or k_pages.stride(3) != 1:
         raise DkvError(DKV_ERR_ARG, "dkv_paged_layout")
     n_pages, hkv, page, d = k_pages.shape
+    _int32("dkv_paged_layout", batch, n_q_heads, max_pages, n_pages, hkv, page, d, window, sinks)
     sp, sh, st, _ = k_pages.stride()
     p = dkv_paged(batch, n_q_heads, hkv, d, page, n_pages, max_pages, _PAGED_DTYPES[k_pages.dtype], window, sinks, sp, sh, st)
     _check(lib().dkv_paged_check(ctypes.byref(p)), "dkv_paged_layout")
@@ -645,6 +652,7 @@ def dkv_paged_evict(p: dkv_paged, k_pages: torch.Tensor, v_pages: torch.Tensor, 
         with _place(dev, stream):
             return dkv_paged_evict(p, k_pages, v_pages, page_table, lens, weights, budget, first, recent, new_table, kept,
                                    new_lens, new_weights, workspace)
+    _int32("dkv_paged_evict", budget, first, recent)
     g, width = _geometry(p), new_table.shape[-1]
     k_shape, t_shape = (g.batch, g.kv_heads, max(budget, 0)), (g.batch, width)
     if k_pages.dtype is not g.dtype or k_pages.stride() != g.strides or k_pages.shape != g.pool or k_pages.get_device() != dev:

@@ -1006,3 +1006,15 @@ def test_the_time_of_eviction_goes_by_the_lengths():
     tight, wide = _microseconds(call(n)), _microseconds(call(131072))
     zeros = B * hkv * 131072 * 4 / 3e6  # us to write the weights' tails at 3 TB/s
     assert wide < 2 * tight + zeros, f"{wide:.1f} us, {tight:.1f} on the narrow table"
+
+
+def test_eviction_refuses_numbers_past_32_bits():
+    c = R.Cache([100], 1, 64, 16, seed=76)
+    p, table = c.layout(1), c.table.cuda()
+    w = torch.rand(1, 1, c.width * 16, device="cuda")
+    before = c.k.clone()
+    for budget, first, recent in (((1 << 32) + 40, 4, 8), (40, 1 << 32, 8), (40, 4, (1 << 32) + 8), (40, 4, -(1 << 32))):
+        with pytest.raises(dkv.DkvError) as e:
+            dkv.dkv_paged_evict(p, c.k, c.v, table, c.dev([100]), w, budget, first, recent, table)
+        assert e.value.status == dkv.DKV_ERR_ARG
+    assert torch.equal(c.k.view(torch.int16), before.view(torch.int16))

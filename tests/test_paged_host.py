@@ -171,3 +171,15 @@ def test_status_reaches_python():
             dkv.dkv_paged_layout(bad, 1, 4, 2)
         assert e.value.status == dkv.DKV_ERR_ARG
     assert ctypes.sizeof(dkv.dkv_paged) == 64 and ctypes.sizeof(dkv.dkv_strides) == 24
+
+
+def test_numbers_past_32_bits_are_refused_in_python():
+    """They would arrive as others: 2^32 + 16 as 16."""
+    import torch
+    pool = torch.zeros(3, 2, 16, 64, dtype=torch.float16)
+    dkv.dkv_paged_layout(pool, 1, 4, 2, window=(1 << 31) - 1, sinks=(1 << 31) - 1)
+    for more in (dict(window=1 << 32), dict(window=(1 << 32) + 16), dict(sinks=1 << 32), dict(window=1 << 31), dict(sinks=-(1 << 32)),
+                 dict(batch=(1 << 32) + 1), dict(n_q_heads=(1 << 32) + 4), dict(max_pages=(1 << 32) + 2)):
+        with pytest.raises(dkv.DkvError) as e:
+            dkv.dkv_paged_layout(pool, **(dict(batch=1, n_q_heads=4, max_pages=2) | more))
+        assert e.value.status == dkv.DKV_ERR_ARG, more
