@@ -899,6 +899,9 @@ WIDE = [
     ("bf16", 64, 3, 1, 256, [300, 4000], [1, 100], 100, 500, 4),
     ("fp16", 128, 6, 1, 32, [1300, 600, 700], [1300, 600, 500], 1300, 0, 0),
     ("bf16", 64, 2, 1, 64, [700] * 40, None, 300, 256, 3),
+    # more units than there is room for: each walks its blocks of keys alone
+    ("fp16", 64, 1, 1, 32, [(i * 389) % 1900 for i in range(170)], [(i * 101) % 301 for i in range(170)], 300, 0, 0),
+    ("bf16", 128, 3, 1, 16, [2000 - 11 * i for i in range(160)], None, 200, 900, 300),
 ]
 
 
