@@ -102,17 +102,6 @@ __device__ inline bool named_bar_any(int id, int nthreads, bool x) {
   return any != 0;
 }
 
-// whether the phase of this parity is over (no waiting)
-__device__ inline bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // two fp32 operations in one instruction (sm_100 and up)
 __device__ inline uint64_t f2_bits(float2 x) { return *reinterpret_cast<uint64_t*>(&x); }
 __device__ inline float2 fma2(float2 x, float2 y, float2 z) {
