@@ -6,7 +6,7 @@
 // flight; the page of a piece comes from the table through the read-only cache.
 //
 // Measured: prompts of 700 to 4096 tokens in 8 sequences, 8 KV heads, d 128 (166 MB read and written):
-// 28.9 us, 5.7 TB/s.  One token for each of 16 sequences: 2.0 us in a graph, latency.
+// 29.0 us, 5.7 TB/s.  One token for each of 16 sequences: 1.9 us in a graph, latency.
 #include "paged.cuh"
 
 namespace dkv {

@@ -21,8 +21,8 @@
 // latency of the reads takes.
 //
 // Measured (d 128): 64 sequences of 300 to 8000 tokens, 8 KV heads, a window of 4096 and 4 sinks,
-// pages of 16 (841 MB): 138 us, 6.1 TB/s.  16 of 64k tokens, 2 KV heads, with their weights (1.09 GB):
-// 193 us, 5.6 TB/s.  One of 1000 tokens: 7.8 us in a graph, the latency of two launches.
+// pages of 16 (841 MB): 137 to 141 us, 6.0 TB/s.  16 of 64k tokens, 2 KV heads, with their weights (1.09 GB):
+// 193 us, 5.6 TB/s.  One of 1000 tokens: 7.4 us in a graph, the latency of two launches.
 //
 // Rows of V that the query does not see inside a tile are zeroed in shared memory
 // before the product: their weight is 0, but 0 x NaN from a slot never written would not be.

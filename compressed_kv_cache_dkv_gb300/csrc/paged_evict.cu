@@ -19,8 +19,8 @@
 // where a batch has both kinds a sequence in place writes once all rows that move have been read.
 // A CTA waits only for CTAs that started before it and that read without waiting, so every wait ends.
 //
-// Measured (d 128): 32 sequences of 2500 to 8192 tokens, 8 KV heads, cut to 4096 (1.03 GB): 177 us,
-// of which 17 the selection; 5.8 TB/s.  30000 tokens to 15000, 8 heads: 46 us; 300 to 256: 9 us (graph).
+// Measured (d 128): 32 sequences of 2500 to 8192 tokens, 8 KV heads, cut to 4096 (1.03 GB): 179 us,
+// of which 17 the selection; 5.8 TB/s.  30000 tokens to 15000, 8 heads: 43 us; 300 to 256: 8.3 us (graphs).
 #include "paged.cuh"
 
 namespace dkv {

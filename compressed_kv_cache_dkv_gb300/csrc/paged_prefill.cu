@@ -23,7 +23,7 @@
 // work for P V.  For fp16 p is scaled by 2^7 first (2^15 with the slack): weights down to e^-14 of
 // the largest keep 11 bits and smaller ones are off by 2^-32 of it at most, 2^-12 for all of the longest
 // cache's tokens together; the scale cancels in the division.  (A slack of 4 and a scale of 2^11 would
-// give them four bits more: 141 us instead of 137 for a 16k prompt under a window of 1024, 12 heads.)
+// give them four bits more, and took 3 % longer on a 16k prompt under a window of 1024, 12 heads.)
 //
 // Tiles in which some row sees a key that another does not (the diagonal, the window's edge, the
 // sinks' end) go past warp 11 first: it zeroes the V rows that no row of the CTA sees, and, since
@@ -33,10 +33,11 @@
 // Bound by the tensor cores: a 128 x 64 tile at d 128 takes 8 x 50 cycles for S (6 KB of shared
 // memory a product) and 4 x 64 for P V.
 //
-// Measured (d 128): a prompt of 8191, 32 query and 8 KV heads, pages of 16: 395 to 415 us, 1.3 to 1.4
-// PFLOP/s.  One of 16384 under a window of 1024, 12 heads: 136 us, 740 TFLOP/s; its 768 CTAs of 19 tiles
-// take five waves and a remainder, and the start and end of a CTA, which nothing overlaps, a fifth of the
-// time.  32 queries over 300 to 2000 keys: 16 us.
+// Measured (d 128): a prompt of 8191, 32 query and 8 KV heads, pages of 16: 413 to 420 us, 1.3 PFLOP/s.  One
+// of 16384 under a window of 1024, 12 heads: 137 to 139 us, 730 TFLOP/s; its 768 CTAs of 19 tiles take five
+// waves and a remainder, and the start and end of a CTA, which nothing overlaps, a fifth of the time.  At d 64
+// the same prompts take 360 and 113 us: a tile's chain of waits and its exponentials stay, half of the products go.
+// 32 queries over 300 to 2000 keys, d 64: 16.4 to 17.3 us.
 #include "paged_tc.cuh"
 
 namespace dkv {

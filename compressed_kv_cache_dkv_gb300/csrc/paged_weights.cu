@@ -13,12 +13,13 @@
 // Many queries: 256 keys stay, two warpgroups in turn to 128 of them, and the query tiles of one
 // head after the other are streamed past; a cluster of kCluster CTAs shares the queries of its keys
 // and adds the parts in rank order, since the first keys of a prompt are seen by all its queries
-// and would take many times the average.  Bound by the products and the exponentials alike (1024
-// cycles each for 256 keys x 128 queries at d 128).
+// and would take many times the average.  Products and exponentials take 1024 cycles each for 256 keys x
+// 128 queries at d 128, and both pipes are busy 55 % of the time: what bounds it is a step's chain of scores,
+// lse and exponentials, and the uneven last wave.
 //
 // Measured (d 128): the last 32 queries of 8 prompts of 2000 to 8192 tokens, 8 KV heads (92 MB): 27 us,
 // of which 14 the read, the rest the start and the end.  A prompt of 8192 with all its queries, 12
-// heads: 86 to 91 us, 1.2 PFLOP/s.
+// heads: 90 to 91 us, 1.13 PFLOP/s.
 #include "paged_tc.cuh"
 
 namespace dkv {

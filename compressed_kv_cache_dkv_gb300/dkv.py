@@ -470,6 +470,8 @@ def dkv_paged_layout(k_pages: torch.Tensor, batch: int, n_q_heads: int, max_page
 
 
 def dkv_paged_workspace_bytes(p: dkv_paged, with_weights: bool = False) -> int:
+    """Bytes of the workspace of every call below.  A call without one makes its own, and with that goes the
+    word that tells of bad lengths and pages (dkv_get_error): keep one where those have to be known."""
     return int(lib().dkv_paged_workspace_bytes(ctypes.byref(p), int(with_weights)))
 
 

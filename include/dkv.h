@@ -397,7 +397,8 @@ DKV_API int dkv_prefill_attend(int32_t batch, int32_t n_q_heads, int32_t n_kv_he
  * interleave keys and values are all taken as they are.
  *
  * Which tokens a query sees: a query at position p of its sequence (p counts
- * the sequence's tokens from 0) sees token t when
+ * the tokens that the cache holds of it from 0: after an eviction those that
+ * are left, so that window and sinks count them too) sees token t when
  *     t <= p  and  (window == 0 or t > p - window or t < sinks):
  * causal, the last `window` tokens, and the first `sinks` tokens whatever the
  * window.  Scores are c q.k with c = 1/sqrt(head_dim).  A query that sees no
@@ -421,6 +422,9 @@ DKV_API int dkv_prefill_attend(int32_t batch, int32_t n_q_heads, int32_t n_kv_he
  * of the workspace (dkv_get_error): a page index outside [0, n_pages) of a page
  * that is needed is read as a page of zeros and not written; a length outside
  * [0, max_pages * page_size] is taken as the nearest bound.
+ *
+ * The calls were added to version 5 and change none of its others: a program
+ * that loads the library at run time looks their symbols up.
  *
  * Supported: head_dim 64 or 128; 1 <= n_q_heads / n_kv_heads <= 8; page_size
  * 16, 32, 64, 128 or 256; batch <= 4096, batch * n_kv_heads <= 65535;
@@ -546,11 +550,12 @@ DKV_API int dkv_paged_weights(const dkv_paged* p, const void* q, const dkv_strid
  *                pages that hold none of the tokens being kept, or begins with
  *                the very pages of its page_table row (page_table itself with
  *                new_max_pages = max_pages, for instance): then the sequence is
- *                compacted in place.  Pages that several sequences share are
- *                read from for all of them; no page may be written for two.
- *                Where one of them is compacted in place, each other that keeps
- *                tokens of the pages written for it has to move to other pages
- *                (its rows are read before they are written over)
+ *                compacted in place, and no page stands twice in its row.  Pages
+ *                that several sequences share are read from for all of them; no
+ *                page may be written for two.  Where one of them is compacted in
+ *                place, each other that keeps tokens of the pages written for it
+ *                has to move to other pages (its rows are read before they are
+ *                written over)
  *   kept         device int32 [B][Hkv][budget]: the positions kept, ascending,
  *                -1 behind the last
  *   new_lens     device int32 [B]: min(lens, budget); may be lens itself
