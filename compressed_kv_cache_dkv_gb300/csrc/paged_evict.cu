@@ -86,7 +86,7 @@ __device__ inline void evict_order(const PagedArgs& a, const PagedEvict& e, cons
   for (int b0 = 0; b0 < a.B; b0 += kSelThreads) moving += __syncthreads_count(b0 + tid < a.B && !stays(b0 + tid));
   const bool mixed = moving > 0 && moving < a.B;
   EvictSeq* order = reinterpret_cast<EvictSeq*>(ws + kWsHeader);
-  int before = 0, to_move = 0;  // sequences that move in front of this round's; this thread's chunks
+  int before = 0, to_move = 0;  // sequences that move in front of these; this thread's chunks
   for (int b0 = 0; b0 < a.B; b0 += kSelThreads) {
     const int b = b0 + tid;
     const bool in = b < a.B, move = in && !stays(b);

@@ -447,7 +447,7 @@ def test_evict_in_place_of_pages_that_others_are_moved_from(dtype, d, hkv, page,
 
 @pytest.mark.parametrize("own_weights", [False, True])
 def test_evict_of_many_sequences_in_place_and_not(own_weights):
-    """More sequences than one round of threads puts in order."""
+    """More sequences than one block of threads puts in order at once."""
     lens = [(i * 29) % 60 for i in range(1300)]
     c = R.Cache(lens, 1, 64, 16, "bf16", seed=8, spare=2 * 1300, width=4)
     _evict_mixed(c, [n > 20 and b % 3 == 0 for b, n in enumerate(lens)], 20, 1, 5, own_weights)
