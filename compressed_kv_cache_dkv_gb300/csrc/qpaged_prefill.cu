@@ -1,0 +1,638 @@
+// dkv_qpaged_prefill: causal attention of the last tokens of each sequence over a cache held in 4 bits, with an
+// optional sliding window and sinks, on the tcgen05 tensor cores.  The sequences' queries lie one behind the other.
+//
+// A CTA owns two groups of 128 query rows that share every K and V tile: two heads of one KV head at the same
+// tokens where the group size is even, else 256 tokens of one head; up to 64 queries stand in rows of 8, 16, 32 or
+// 64 a head, so that a group holds several heads.  A grid that would leave half of the multiprocessors idle is
+// multiplied by cutting the key tiles of each CTA into parts, which a second grid joins by their references and sums.
+// Per 64-key tile j and group g
+//   S_g = Q_g K_j^T   M = 128 queries, N = 64 keys   (64 TMEM columns, two buffers a group)
+//   O_g += P_g V_j    M = 128, N = d, P from TMEM (fp16, over the first 32 columns of its S)
+//
+// Warps 0-7 hold a query row per thread: they bring Q to shared memory, and turn S into P.  Warp 8 streams the
+// tiles' bytes (bulk copies, one per page and tile) into a ring, warps 12-15 make fp16 values of them: a group's
+// values scale * code + bias are fp16 numbers exactly, so the tensor cores see the very values of the cache.
+// Warps 9 and 10 issue the products.  All operands are fp16; bf16 queries are brought into its range by a power of
+// two for each row, which goes into that row's factor of the scores (exact for values above 2^-24 of the largest).
+// Codes come out of a word in the order 0 4 1 5 2 6 3 7; Q stands in the same order, and O leaves it at the end.
+//
+// P = 2^(score - ref) is rounded once to fp16.  A row's reference lies kQpShift below a maximum and moves, with O
+// rescaled in tensor memory, only when a score exceeds that by kQpSlack (base 2): P is at most 2^15, weights down to
+// e^-14 of the largest keep 11 bits and smaller ones are off by 2^-32 of it at most.  A score is rounded by its
+// factor first, as the maximum was, and the reference taken off then: so that large scores lose nothing more.
+//
+// Values in the cache are finite.  What lies in slots that no row of the CTA sees may be anything and counts as
+// zeros; a weight of 0 takes care of what only some rows see.
+#include "paged_tc.cuh"
+#include "qpaged.cuh"
+
+namespace dkv {
+namespace {
+
+constexpr int kQpThreads = 512, kQpM = 128, kQpN = 64;
+constexpr float kQpSlack = 8.f, kQpShift = 7.f;
+constexpr float kQpLarge = 0x1p20f;  // scores (in base 2) whose rounding would show in the slack
+
+template <int D>
+struct QpSmem {
+  static constexpr int kR = 4;     // slots for K, and for V
+  static constexpr int kRaw = 3;   // tiles of bytes on their way
+  static constexpr uint32_t kQ = kQpM * D * 2;          // one group's Q
+  static constexpr uint32_t kTile = kQpN * D * 2;       // one K or V tile
+  static constexpr uint32_t kRawTile = kQpN / kQBlock * qblock_bytes(D);
+  static constexpr uint32_t kOffK = 2 * kQ;
+  static constexpr uint32_t kOffV = kOffK + kR * kTile;
+  static constexpr uint32_t kOffRaw = kOffV + kR * kTile;
+  static constexpr uint32_t kOffBar = kOffRaw + kRaw * kRawTile;
+  static constexpr uint32_t kBytes = kOffBar + 512;
+};
+
+struct QpArgs {
+  PagedArgs a;
+  PackedQuery q;
+  const uint8_t* cache;
+  void* out;
+  dkv_strides os;
+  float* lse;
+  int rows;      // query rows of a head in a group: 128, or 8, 16, 32, 64 with 128 / rows heads a group
+  int rows_shift;
+  int by_heads;  // the groups hold different heads (else two 128-token tiles of one head)
+  int heads;     // heads of a CTA
+  int per_kv;    // CTAs that share the heads of a KV head
+  int parts;     // parts of a row tile's keys at most
+  float tile_us, part_us, ratio;  // times of a key tile, and of a part; the first over the second
+  float* part_o;     // [CTA][part][256 rows][d] and
+  float2* part_stat; // [CTA][part][256 rows] reference and sum, when parts > 1
+};
+
+// Parts of `tiles` key tiles: as many as take the least time by the model, with kQpJoin us for the join, one
+// where that takes no longer.  The grid and its join have to agree, so the roundings are spelled out.
+constexpr float kQpJoin = 2.5f;
+__device__ inline int qp_parts(const QpArgs& p, int tiles) {
+  if (p.parts < 2) return 1;
+  const int parts = min(min((int)rintf(__fsqrt_rn(__fmul_rn(p.ratio, (float)tiles))), p.parts), tiles);
+  if (parts < 2) return 1;
+  const float whole = __fmul_rn(p.tile_us, (float)tiles), cut = __fadd_rn(__fmul_rn(p.tile_us, (float)((tiles + parts - 1) / parts)), __fadd_rn(__fmul_rn(p.part_us, (float)parts), kQpJoin));
+  return cut < whole ? parts : 1;
+}
+
+// The queries of a sequence: its span, and the row of its first one.
+struct QpSpan {
+  QuerySpan s;
+  int start;
+};
+__device__ inline QpSpan qp_span(const QpArgs& p, int b) {
+  QpSpan r;
+  const int s0 = __ldg(p.q.starts + b), s1 = __ldg(p.q.starts + b + 1);
+  r.s.len = paged_len(p.a, b);
+  r.start = s0;
+  r.s.n = s1 - s0;
+  if (s0 < 0 || s1 < s0 || s1 > p.q.rows || r.s.n > p.q.max_q) {
+    raise_error(p.a.err, DKV_DEVERR_INDEX);
+    r.s.n = 0;
+  }
+  r.s.off = r.s.len - r.s.n;
+  return r;
+}
+
+// Row `row` of group g of a CTA's 256: its head and token.
+struct QpRow {
+  int head, token;
+  bool live;
+};
+__device__ inline QpRow qp_row(const QpArgs& p, int kvh, int h0, int row0, int n, int g, int row) {
+  QpRow r;
+  const int h = h0 + (p.by_heads ? (g * kQpM + row) >> p.rows_shift : 0);  // within the KV head's group
+  r.head = kvh * p.a.G + h;
+  r.token = row0 + (p.by_heads ? row & (p.rows - 1) : g * kQpM + row);
+  r.live = h < p.a.G && r.token < n;
+  return r;
+}
+
+// natural log-sum-exp of a row's reference and sum (-inf for a row that sees no key)
+__device__ inline float qp_lse(float ref, float l) { return (ref + log2f(l)) * 0.6931471805599453f; }
+
+// every query at positions [p_lo, p_hi] sees every key of [k0, k0 + kQpN)
+__device__ inline bool qp_all_seen(const PagedArgs& a, int k0, int p_lo, int p_hi) {
+  return k0 + kQpN - 1 <= p_lo && (a.window == 0 || k0 > p_hi - a.window || k0 + kQpN <= a.sinks);
+}
+
+// bit c: the query at position pos sees key k0 + c
+__device__ inline unsigned long long qp_sees(const PagedArgs& a, int pos, int k0) {
+  const int hi = pos - k0, lo = a.window ? pos - a.window + 1 - k0 : 0, sk = a.sinks - k0;
+  auto below = [](int n) { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1; };
+  return below(hi + 1) & (~below(lo) | below(sk));
+}
+
+__device__ inline float2 mul2(float2 x, float2 y) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(x)), "l"(f2_bits(y)));
+  return *reinterpret_cast<float2*>(&r);
+}
+
+// Eight codes as values, in the order 0 4 1 5 2 6 3 7.  1024 + code and 1024 + 16 code are the halves whose low
+// bits are the code's; every step is exact.
+__device__ inline uint4 values8(uint32_t x, __half2 s, __half2 b) {
+  const uint32_t y = x >> 8;
+  auto half2_of = [](uint32_t w) { return *reinterpret_cast<__half2*>(&w); };
+  auto bits = [](__half2 h) { return *reinterpret_cast<uint32_t*>(&h); };
+  const __half2 base = half2_of(0x64006400u), sixteenth = half2_of(0x2c002c00u), minus64 = half2_of(0xd400d400u);
+  const __half2 c0 = __hsub2(half2_of((x & 0x000f000fu) | 0x64006400u), base);
+  const __half2 c1 = __hfma2(half2_of((x & 0x00f000f0u) | 0x64006400u), sixteenth, minus64);
+  const __half2 c2 = __hsub2(half2_of((y & 0x000f000fu) | 0x64006400u), base);
+  const __half2 c3 = __hfma2(half2_of((y & 0x00f000f0u) | 0x64006400u), sixteenth, minus64);
+  return make_uint4(bits(__hfma2(c0, s, b)), bits(__hfma2(c1, s, b)), bits(__hfma2(c2, s, b)), bits(__hfma2(c3, s, b)));
+}
+
+template <int N>
+__device__ inline void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ inline void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+// 128 registers for each of 512 threads at the start, and 2 x 168 + 80 + 96 = 4 x 128
+constexpr int kQpRegsRows = 168, kQpRegsIssue = 80, kQpRegsValues = 96;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  using S = QpSmem<D>;
+  const PagedArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
+  const QpSpan span = qp_span(p, b);
+  const QuerySpan& qs = span.s;
+  // the groups: head and first query row (of all heads the later rows, with more keys, first)
+  const int tile = (int)gridDim.z - 1 - (int)blockIdx.z;
+  const int row0 = tile * (p.by_heads ? p.rows : 2 * kQpM);
+  if (p.parts > 1) griddep_launch();  // the join; without it the next grid on the stream may be anyone's
+  if (row0 >= qs.n) return;
+  const int part = (int)blockIdx.x % p.parts, hg = (int)blockIdx.x / p.parts;
+  const int kvh = hg / p.per_kv, h0 = hg % p.per_kv * p.heads;  // h0: within the KV head's group
+  // tokens of the groups, heads of the second (0: an empty group)
+  const int tokA = min(p.by_heads ? p.rows : kQpM, qs.n - row0), tokB = p.by_heads ? tokA : max(0, min(kQpM, qs.n - row0 - kQpM));
+  const int hdB = p.by_heads ? max(0, min(kQpM / p.rows, a.G - h0 - kQpM / p.rows)) : (tokB > 0 ? 1 : 0);
+  const int p_lo = qs.off + row0, p_hi = p_lo + (p.by_heads ? tokA : tokA + tokB) - 1;
+  const KeySpan<kQpN> ks = key_span<kQpN>(a, p_lo, p_hi);
+  const int parts = qp_parts(p, ks.n);
+  if (part >= parts) return;  // fewer than a sequence of the table's length would take
+  // this part's key tiles; group A's may end a tile or two before B's
+  const int t0 = (int)((int64_t)ks.n * part / parts), t1 = (int)((int64_t)ks.n * (part + 1) / parts);
+  const int endA = p.by_heads ? ks.n : min(ks.n, max(0, ks.st + (max(0, p_lo + tokA) + kQpN - 1) / kQpN - ks.wt0));
+  const int nA = max(0, min(endA, t1) - t0), nB = hdB > 0 ? t1 - t0 : 0;
+  const int nt = max(nA, nB);
+  auto key_of = [&](int j) { return ks.key(t0 + j); };  // first key of tile j
+
+  const uint32_t sb = smem_u32(smem);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + S::kOffBar);  // [slot]
+  uint64_t* v_full = k_full + S::kR;     // [slot]
+  uint64_t* empty = v_full + S::kR;      // [slot] O_j, and so S_j, of both groups are done
+  uint64_t* raw_full = empty + S::kR;    // [stage]
+  uint64_t* raw_empty = raw_full + S::kRaw;
+  uint64_t* q_full = raw_empty + S::kRaw;  // [group]
+  uint64_t* s_full = q_full + 2;         // [group][buffer]
+  uint64_t* p_full = s_full + 4;         // [group][buffer]
+  uint64_t* o_done = p_full + 4;         // [group][buffer]
+  uint64_t* drain = o_done + 4;          // [group] after a wait that gave up
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
+  volatile uint32_t* bad_blocks = tmem_slot + 1;  // [stage] blocks on bad pages
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kR; ++i) {
+      mbar_init(&k_full[i], 4);  // a lane of each warp that makes values
+      mbar_init(&v_full[i], 4);
+      mbar_init(&empty[i], 2);  // one commit per group
+    }
+    for (int i = 0; i < S::kRaw; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 4);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], kQpM);
+      mbar_init(&o_done[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 4);
+      mbar_init(&drain[i], 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 0) tc_alloc<512>(tmem_slot);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  bool ok = true;
+
+  if (warp >= 12) {
+    // =========================== values: a thread makes half of a token's channels, of K and then of V
+    regs_dec<kQpRegsValues>();
+    const int tid = threadIdx.x - 12 * 32, tok = tid & 63, half = tid >> 6;
+    constexpr int kWords = D / 16;  // of eight codes
+    // byte of this thread's codes in a tile's bytes
+    const int g = D == 128 ? half : 0, in_g = D == 128 ? 0 : 16 * half;
+    int sl = 0, rs = 0;
+    uint32_t ph = 0, rph = 0;
+    for (int j = 0; j < nt; ++j) {
+      if (ok) ok = mbar_wait(&raw_full[rs], rph, a.err);
+      if (ok && j >= S::kR) ok = mbar_wait(&empty[sl], ph ^ 1u, a.err);
+      const int t = key_of(j) + tok;
+      const bool zero = !(t < ks.hi && (t >= ks.lo || t < a.sinks)) || (bad_blocks[rs] >> (tok / kQBlock) & 1u);
+      const uint32_t raw = sb + S::kOffRaw + rs * S::kRawTile + (uint32_t)(tok / kQBlock) * qblock_bytes(D);
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        uint32_t sbits = lds32(raw + qparam_off(D, kv, g, tok % kQBlock));
+        if (zero) sbits = 0u;
+        const __half2 sbh = *reinterpret_cast<__half2*>(&sbits), s2 = __low2half2(sbh), b2 = __high2half2(sbh);
+        const uint32_t from = raw + qcode_off(D, kv, g, tok % kQBlock) + in_g;
+        const uint32_t to = sb + (kv ? S::kOffV : S::kOffK) + sl * S::kTile;
+#pragma unroll
+        for (int x = 0; x < kWords; x += 4) {
+          const uint4 c = lds128(from + 4 * x);
+          const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) sts128(to + sw128(kQpN, tok, half * kWords + x + y), values8(w[y], s2, b2));
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(kv ? &v_full[sl] : &k_full[sl]);
+      }
+      if (lane == 0) mbar_arrive(&raw_empty[rs]);
+      if (++sl == S::kR) { sl = 0; ph ^= 1u; }
+      if (++rs == S::kRaw) { rs = 0; rph ^= 1u; }
+    }
+  } else if (warp >= 8) {
+    regs_dec<kQpRegsIssue>();
+    if (warp == 8) {
+      // =========================== the tiles' bytes
+      const uint32_t el = elect_one();
+      const int rows = min(a.page_mask + 1, kQpN), runs = kQpN / rows, bpr = rows / kQBlock;
+      int j = 0;
+      for (; j < nt; ++j) {
+        const int st = j % S::kRaw, first = key_of(j) + lane * rows;
+        // lane i < runs: its page, and the run's blocks that hold a visible token
+        int page = -1, b0 = bpr, b1 = 0;
+        bool bad = false;
+        if (lane < runs) {
+          for (int i = 0; i < bpr; ++i) {
+            const int t = first + i * kQBlock;
+            if (t < ks.hi && (t + kQBlock > ks.lo || t < a.sinks)) {
+              b0 = min(b0, i);
+              b1 = i + 1;
+            }
+          }
+          if (b0 < b1) {
+            page = paged_page(a, b, first);
+            bad = page >= a.n_pages;
+          }
+        }
+        const uint32_t none = __ballot_sync(0xffffffffu, bad);
+        const bool copies = b0 < b1 && !bad;
+        const uint32_t bytes = copies ? (uint32_t)(b1 - b0) * qblock_bytes(D) : 0u;
+        uint32_t sum = bytes;
+#pragma unroll
+        for (int o = 1; o < kQpN / kQBlock; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        sum = __shfl_sync(0xffffffffu, sum, 0);
+        const uint64_t src = reinterpret_cast<uint64_t>(p.cache) +
+                             (copies ? page * a.stride_page + kvh * a.stride_head + (int64_t)((first & a.page_mask) / kQBlock + b0) * qblock_bytes(D) : 0);
+        const uint32_t dst = sb + S::kOffRaw + st * S::kRawTile + (uint32_t)(lane * bpr + b0) * qblock_bytes(D);
+        if (j >= S::kRaw) ok = mbar_wait(&raw_empty[st], (uint32_t)((j / S::kRaw - 1) & 1), a.err);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (el) {
+          uint32_t m = 0;  // bad runs as a mask of blocks
+          for (int i = 0; i < kQpN / kQBlock; ++i) m |= (none >> (i / bpr) & 1u) << i;
+          bad_blocks[st] = m;
+          mbar_arrive_expect_tx(&raw_full[st], sum);
+        }
+        __syncwarp();
+#pragma unroll 1
+        for (int i = 0; i < runs; ++i) {
+          const uint32_t n = __shfl_sync(0xffffffffu, bytes, i), to = __shfl_sync(0xffffffffu, dst, i);
+          const uint64_t from = __shfl_sync(0xffffffffu, src, i);
+          if (n && el)
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "l"(from),
+                         "r"(n), "r"(smem_u32(&raw_full[st]))
+                         : "memory");
+        }
+      }
+      // every copy has landed before the CTA may end (also after a wait that gave up)
+      for (int x = max(0, j - S::kRaw); x < j; ++x) mbar_wait(&raw_full[x % S::kRaw], (uint32_t)((x / S::kRaw) & 1), a.err);
+    } else if (warp < 11) {
+      // =========================== products of group g
+      // The whole warp walks through here and one elected lane issues: in code that one lane runs alone the
+      // operands are not known to be uniform, and an issue took 75 to 150 cycles.
+      constexpr uint32_t id_s = tc_idesc(Num<__half>::kUmma, false, kQpN), id_o = tc_idesc(Num<__half>::kUmma, true, D);
+      const uint32_t el = elect_one();
+      const int g = warp - 9, n = g ? nB : nA, n_other = g ? nA : nB;
+      const uint32_t tg = tmem + 256u * g;
+      const uint64_t qd = tc_desc(sb + g * S::kQ, 16, 1024);
+      uint64_t* const sf = s_full + 2 * g;
+      uint64_t* const pf = p_full + 2 * g;
+      uint64_t* const od = o_done + 2 * g;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok) ok = mbar_wait(bar, parity, a.err);
+        __syncwarp();
+      };
+      int k_sl = 0, v_sl = 0;             // slots of the next K and V tile
+      uint32_t k_ph = 0, v_ph = 0;        // and their phases
+      auto scores = [&](int j) {
+        const int buf = j & 1;
+        wait(&k_full[k_sl], k_ph);
+        if (j >= 2) wait(&od[buf], (uint32_t)((j - 2) >> 1) & 1u);  // the buffer holds P_{j-2}
+        tc_fence_after();
+        const uint64_t kd = tc_desc(sb + S::kOffK + k_sl * S::kTile, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)  // 16 channels: 32 bytes of a 128-byte row, then the next 64 channels
+          tc_mma(tg + kQpN * buf, qd + (uint64_t)(((k >> 2) * kQpM * 128 + (k & 3) * 32) >> 4),
+                 kd + (uint64_t)(((k >> 2) * kQpN * 128 + (k & 3) * 32) >> 4), id_s, k > 0, el);
+        tc_commit(&sf[buf], el);
+        if (++k_sl == S::kR) { k_sl = 0; k_ph ^= 1u; }
+      };
+      if (n > 0) {
+        wait(&q_full[g], 0);
+        scores(0);
+        for (int j = 0; j < n; ++j) {
+          if (j + 1 < n) scores(j + 1);
+          const int buf = j & 1;
+          wait(&v_full[v_sl], v_ph);
+          wait(&pf[buf], (uint32_t)(j >> 1) & 1u);
+          tc_fence_after();
+          const uint64_t vd = tc_desc(sb + S::kOffV + v_sl * S::kTile, kQpN * 128, 1024);
+          const uint32_t ts = tg + kQpN * buf;
+#pragma unroll
+          for (int k = 0; k < kQpN / 16; ++k)  // 16 keys: 16 rows of 128 bytes
+            tc_mma_ta(tg + 128u, ts + 8u * k, vd + (uint64_t)(k * 16 * 128 >> 4), id_o, k > 0 ? 1u : (j > 0 ? 1u : 0u), el);
+          tc_commit(&od[buf], el);
+          // once for this group, once more where the other has no tile j
+          tc_commit(&empty[v_sl], el);
+          if (j >= n_other) tc_commit(&empty[v_sl], el);
+          if (++v_sl == S::kR) { v_sl = 0; v_ph ^= 1u; }
+        }
+      }
+      if (!__all_sync(0xffffffffu, ok)) {  // a wait gave up, and the rows may have too: no product outlives the CTA
+        tc_commit(&drain[g], el);
+        mbar_wait(&drain[g], 0, a.err);
+      }
+    }
+  } else {
+    // =========================== one query row per thread
+    regs_inc<kQpRegsRows>();
+    const int g = warp >> 2, rw = warp & 3, row = 32 * rw + lane;
+    const int n = g ? nB : nA;
+    const QpRow me = qp_row(p, kvh, h0, row0, qs.n, g, row);
+    const int pos = qs.off + me.token;
+    float slog2 = a.scale_log2;
+    if (n > 0) {  // Q to shared memory, D / 8 lanes a row
+      constexpr int L = D / 8, kAt = 32 / L, kDeep = 4;
+#pragma unroll 1
+      for (int i0 = 0; i0 < 32 / kAt; i0 += kDeep) {
+        uint4 v[kDeep];
+#pragma unroll
+        for (int x = 0; x < kDeep; ++x) {
+          const QpRow r = qp_row(p, kvh, h0, row0, qs.n, g, 32 * rw + (i0 + x) * kAt + lane / L);
+          v[x] = make_uint4(0, 0, 0, 0);
+          if (r.live)
+            v[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q.q) + (int64_t)(span.start + r.token) * p.q.qs.token +
+                                                        (int64_t)r.head * p.q.qs.head + 8 * (lane % L)));
+        }
+#pragma unroll
+        for (int x = 0; x < kDeep; ++x) {
+          float f[8];
+          const T* h = reinterpret_cast<const T*>(&v[x]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = Num<T>::to_float(h[e]);
+          if (Num<T>::kUmma == 1) {  // bf16: into fp16's range
+            float top = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+#pragma unroll
+            for (int o = 1; o < L; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int ex = max((int)(__float_as_uint(top) >> 23), 15);     // top < 2^(ex - 126)
+            const float up = __uint_as_float((uint32_t)(268 - ex) << 23);  // 2^(141 - ex): top up < 2^15
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] *= up;
+            const int mine = __shfl_sync(0xffffffffu, ex, lane % kAt * L);
+            if (lane / kAt == i0 + x) slog2 = a.scale_log2 * __uint_as_float((uint32_t)(mine - 14) << 23);  // 2^(ex - 141)
+          }
+          sts128(sb + g * S::kQ + sw128(kQpM, 32 * rw + (i0 + x) * kAt + lane / L, lane % L),
+                 make_uint4(pack_half2(f[0], f[4]), pack_half2(f[1], f[5]), pack_half2(f[2], f[6]), pack_half2(f[3], f[7])));
+        }
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[g]);
+    }
+    // positions of the group's rows (the tile is unmasked when all of them see all of it)
+    const int g_lo = p.by_heads ? p_lo : p_lo + g * kQpM, g_hi = g_lo + (g ? tokB : tokA) - 1;
+    const uint32_t tg = tmem + ((uint32_t)(32 * rw) << 16) + 256u * g, to = tg + 128u;
+    float ref = -INFINITY, l = 0.f;
+    for (int j = 0; j < n; ++j) {
+      const int buf = j & 1;
+      const uint32_t ts = tg + kQpN * buf;
+      if (ok) ok = mbar_wait(&s_full[2 * g + buf], (uint32_t)((j >> 1) & 1), a.err);
+      tc_fence_after();
+      uint32_t s[kQpN];
+#pragma unroll
+      for (int c = 0; c < kQpN / 32; ++c) tc_ld32(ts + 32 * c, s + 32 * c);
+      tc_ld_wait();
+      const int k0 = key_of(j);
+      if (!qp_all_seen(a, k0, g_lo, g_hi)) {
+        const unsigned long long sees = qp_sees(a, pos, k0);
+        if (__any_sync(0xffffffffu, sees != ~0ull)) {
+          const uint32_t half[2] = {(uint32_t)sees, (uint32_t)(sees >> 32)};
+#pragma unroll
+          for (int c = 0; c < kQpN; ++c) s[c] = half[c >> 5] >> (c & 31) & 1u ? s[c] : 0xff800000u;
+        }
+      }
+      float mx[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) mx[c] = __uint_as_float(s[c]);
+#pragma unroll
+      for (int c = 8; c < kQpN; ++c) mx[c & 7] = fmaxf(mx[c & 7], __uint_as_float(s[c]));
+      const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * slog2;
+      const bool up = top > ref + (fabsf(top) < kQpLarge ? kQpShift + kQpSlack : kQpShift);
+      const float al = up ? fast_exp2(ref - (top - kQpShift)) : 1.f;
+      if (up) ref = top - kQpShift;
+      if (j > 0 && __any_sync(0xffffffffu, up)) {  // rescale O once O_{j-1} is done
+        if (ok) ok = mbar_wait(&o_done[2 * g + (buf ^ 1)], (uint32_t)(((j - 1) >> 1) & 1), a.err);
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tc_ld32(to + 32 * c, o);
+          tc_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+          tc_st32(to + 32 * c, o);
+        }
+      }
+      const float off = ref == -INFINITY ? 0.f : -ref;
+      const float2 scale2 = make_float2(slog2, slog2), minus2 = make_float2(off, off);
+      float2 lp[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      uint32_t w[kQpN / 2];
+#pragma unroll
+      for (int e = 0; e < kQpN / 2; ++e) {
+        const float2 x = add2(mul2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), scale2), minus2);
+        const float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+        lp[e & 1] = add2(lp[e & 1], y);
+        w[e] = pack_half2(y.x, y.y);
+      }
+      tc_st32(ts, w);
+      l = fmaf(l, al, (lp[0].x + lp[1].x) + (lp[0].y + lp[1].y));
+      tc_st_wait();
+      tc_fence_before();
+      mbar_arrive(&p_full[2 * g + buf]);
+    }
+    if (n > 0 && ok) ok = mbar_wait(&o_done[2 * g + ((n - 1) & 1)], (uint32_t)(((n - 1) >> 1) & 1), a.err);
+    tc_fence_after();
+    const bool live = me.live;
+    const float il = n == 0 || l == 0.f ? 0.f : 1.f / l;  // a row that sees no key: zeros
+    // The rows go through the group's Q, which no product reads any more, so that a warp then writes
+    // whole rows of the output.
+    const uint32_t stage = sb + g * S::kQ;
+    const int64_t rec = (((int64_t)b * gridDim.z + tile) * (gridDim.x / p.parts) + hg) * p.parts + part;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t o[32];
+      if (n > 0) {
+        tc_ld32(to + 32 * c, o);
+        tc_ld_wait();
+      }
+      float f[32];  // channels in their own order
+#pragma unroll
+      for (int e = 0; e < 32; ++e) f[(e & ~7) + (e & 7) / 2 + 4 * (e & 1)] = n > 0 && l != 0.f ? __uint_as_float(o[e]) * il : 0.f;
+      if (parts > 1) {
+        if (live) {
+          float* o32 = p.part_o + (rec * 2 * kQpM + g * kQpM + row) * D + 32 * c;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(o32 + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+        }
+        continue;
+      }
+#pragma unroll
+      for (int e = 0; e < 32; e += 8)
+        sts128(stage + sw128(kQpM, row, (32 * c + e) / 8),
+               make_uint4(Num<T>::pack(f[e], f[e + 1]), Num<T>::pack(f[e + 2], f[e + 3]), Num<T>::pack(f[e + 4], f[e + 5]),
+                          Num<T>::pack(f[e + 6], f[e + 7])));
+    }
+    if (parts > 1) {
+      if (live) p.part_stat[rec * 2 * kQpM + g * kQpM + row] = make_float2(ref, l);
+    } else {
+      __syncwarp();
+      const int ch = lane % (D / 8);  // a row's piece; D / 8 lanes a row
+      T* out = static_cast<T*>(p.out) + 8 * ch;
+      auto store = [&](const QpRow& first, int r0, int n_rows) {  // rows r0 .. r0 + n_rows - 1, of one head
+        if (!first.live) return;
+        T* at = out + (int64_t)first.head * p.os.head + (int64_t)(span.start + first.token) * p.os.token;
+        const int live_rows = min(n_rows, qs.n - first.token);
+#pragma unroll 4
+        for (int r = lane / (D / 8); r < live_rows; r += 256 / D)
+          *reinterpret_cast<uint4*>(at + (int64_t)r * p.os.token) = lds128(stage + sw128(kQpM, r0 + r, ch));
+      };
+      const int step = min(p.rows, 32);
+      for (int r = 32 * rw; r < 32 * rw + 32; r += step) store(qp_row(p, kvh, h0, row0, qs.n, g, r), r, step);
+      if (live && p.lse) p.lse[(int64_t)me.head * p.q.rows + span.start + me.token] = qp_lse(ref, l);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tc_free<512>(tmem);
+}
+
+// The parts of a row joined: weights l_part 2^(ref_part - M), in part order.  A warp per row.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) qpaged_prefill_join_kernel(QpArgs p, int tiles, int hgs) {
+  constexpr int V = D / 32;  // channels of a lane
+  const PagedArgs& a = p.a;
+  griddep_wait();
+  const int b = blockIdx.z, tile = (int)blockIdx.y / hgs, hg = (int)blockIdx.y % hgs, lane = threadIdx.x & 31;
+  const int row = (int)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const QpSpan span = qp_span(p, b);
+  const QuerySpan& qs = span.s;
+  const int row0 = tile * (p.by_heads ? p.rows : 2 * kQpM), p_lo = qs.off + row0;
+  const QpRow me = qp_row(p, hg / p.per_kv, hg % p.per_kv * p.heads, row0, qs.n, row / kQpM, row % kQpM);
+  if (!me.live) return;
+  const int parts = qp_parts(p, key_span<kQpN>(a, p_lo, p_lo + min(p.by_heads ? p.rows : 2 * kQpM, qs.n - row0) - 1).n);
+  if (parts < 2) return;  // written by its one part
+  const int64_t rec = (((int64_t)b * tiles + tile) * hgs + hg) * p.parts;
+  auto at = [&](int i) { return (rec + i) * 2 * kQpM + row; };
+  float M = -INFINITY;
+  for (int i = lane; i < parts; i += 32) M = fmaxf(M, __ldcg(p.part_stat + at(i)).x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float f[V] = {}, L = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) {
+    const float2 ml = __ldcg(p.part_stat + at(i));
+    if (ml.y == 0.f) continue;  // (a NaN goes on)
+    const float w = ml.y * fast_exp2(ml.x - M);
+    L += w;
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+      const float2 o = __ldcg(reinterpret_cast<const float2*>(p.part_o + at(i) * D + V * lane + e));
+      f[e] = fmaf(w, o.x, f[e]);
+      f[e + 1] = fmaf(w, o.y, f[e + 1]);
+    }
+  }
+  const float il = L == 0.f ? 0.f : 1.f / L;
+  T* out = static_cast<T*>(p.out) + (int64_t)me.head * p.os.head + (int64_t)(span.start + me.token) * p.os.token + V * lane;
+#pragma unroll
+  for (int e = 0; e < V; e += 2) *reinterpret_cast<uint32_t*>(out + e) = Num<T>::pack(f[e] * il, f[e + 1] * il);
+  if (p.lse && lane == 0) p.lse[(int64_t)me.head * p.q.rows + span.start + me.token] = qp_lse(M, L);
+}
+
+template <typename T, int D>
+cudaError_t launch_qprefill_td(const QpArgs& p, cudaStream_t s) {
+  constexpr uint32_t smem = QpSmem<D>::kBytes;
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(qpaged_prefill_kernel<T, D>), smem);
+  if (e != cudaSuccess) return e;
+  const int tiles = (p.q.max_q + (p.by_heads ? p.rows : 2 * kQpM) - 1) / (p.by_heads ? p.rows : 2 * kQpM);
+  const int hgs = p.a.Hkv * p.per_kv;
+  qpaged_prefill_kernel<T, D><<<dim3(hgs * p.parts, p.a.B, tiles), kQpThreads, smem, s>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess || p.parts == 1) return e;
+  return launch_dependent(qpaged_prefill_join_kernel<T, D>, dim3(2 * kQpM / 8, tiles * hgs, p.a.B), 256, 0, s, p, tiles, hgs);
+}
+
+}  // namespace
+
+size_t qpaged_prefill_ws_bytes(int d) { return kWsHeader + (size_t)sm_count() * 2 * kQpM * (d + 2) * 4; }
+
+cudaError_t launch_qpaged_prefill(const PagedArgs& a, int d, int dtype, const PackedQuery& q, const uint8_t* cache,
+                                  void* out, const dkv_strides& os, float* lse, uint8_t* ws, cudaStream_t s) {
+  QpArgs p;
+  p.a = a;
+  p.q = q;
+  p.cache = cache;
+  p.out = out;
+  p.os = os;
+  p.lse = lse;
+  // Rows of a head in a group.  Up to 64 queries: a power of two, so that a group holds several heads.
+  p.rows = 8;
+  while (p.rows < q.max_q && p.rows < kQpM) p.rows *= 2;
+  p.rows_shift = 0;
+  while ((1 << p.rows_shift) < p.rows) ++p.rows_shift;
+  p.by_heads = a.G % 2 == 0 || p.rows < kQpM;
+  p.heads = p.by_heads ? 2 * kQpM / p.rows : 1;
+  p.per_kv = (a.G + p.heads - 1) / p.heads;
+  // Parts of the key tiles, when the grid would fill at most half of the multiprocessors (records for one grid of
+  // them are what the workspace holds).
+  const int tokens = p.by_heads ? p.rows : 2 * kQpM;
+  const int64_t ctas = (int64_t)a.Hkv * p.per_kv * a.B * ((q.max_q + tokens - 1) / tokens);
+  const int64_t keys = a.window > 0 && (int64_t)a.window + a.sinks + tokens < a.cap ? (int64_t)a.window + a.sinks + tokens : a.cap;
+  const int64_t fit = sm_count() / ctas;
+  p.tile_us = 0.85f;
+  p.part_us = 0.65f + 2e-6f * (float)d * (float)a.B * (float)a.Hq * (float)q.max_q;
+  p.ratio = p.tile_us / p.part_us;
+  p.parts = 1;
+  if (fit > 1) {
+    const float tiles = (float)((keys + kQpN - 1) / kQpN);
+    float parts = rintf(sqrtf(p.ratio * tiles));
+    parts = fminf(fmaxf(parts, 1.f), fminf((float)fit, tiles));
+    if (p.tile_us * ceilf(tiles / parts) + kQpJoin + p.part_us * parts < p.tile_us * tiles) p.parts = (int)parts;
+  }
+  p.part_o = reinterpret_cast<float*>(ws + kWsHeader);
+  p.part_stat = reinterpret_cast<float2*>(p.part_o + (size_t)sm_count() * 2 * kQpM * d);
+  if (dtype == DKV_BF16) return d == 128 ? launch_qprefill_td<__nv_bfloat16, 128>(p, s) : launch_qprefill_td<__nv_bfloat16, 64>(p, s);
+  return d == 128 ? launch_qprefill_td<__half, 128>(p, s) : launch_qprefill_td<__half, 64>(p, s);
+}
+
+}  // namespace dkv

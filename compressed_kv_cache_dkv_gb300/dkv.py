@@ -47,6 +47,9 @@ EXPORTED = (
     "dkv_prefill_workspace_bytes", "dkv_prefill_attend",
     "dkv_paged_check", "dkv_paged_workspace_bytes", "dkv_paged_append", "dkv_paged_decode", "dkv_paged_prefill",
     "dkv_paged_weights", "dkv_paged_evict",
+    "dkv_paged_plan_workspace_bytes", "dkv_paged_plan", "dkv_qk_norm_rope",
+    "dkv_qpaged_check", "dkv_qpaged_workspace_bytes", "dkv_qpaged_append", "dkv_qpaged_gather", "dkv_qpaged_decode",
+    "dkv_qpaged_prefill",
 )
 
 
@@ -85,6 +88,17 @@ class dkv_paged(ctypes.Structure):
 
 class dkv_strides(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("batch", "head", "token")]
+
+
+class dkv_rotate(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "n_q_heads", "n_kv_heads", "head_dim", "dtype", "norm", "rope_dims")] + [
+        ("eps", ctypes.c_float), ("rope_base", ctypes.c_double), ("inv_freq", ctypes.POINTER(ctypes.c_double))]
+
+
+class dkv_qpaged(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "n_q_heads", "n_kv_heads", "head_dim", "page_size", "n_pages", "max_pages", "dtype", "window", "sinks")] + [
+        (n, ctypes.c_int64) for n in ("stride_page", "stride_head")]
 
 
 _lib = None
@@ -141,6 +155,19 @@ def lib() -> ctypes.CDLL:
         L.dkv_paged_prefill.argtypes = [ppaged, vp, pstr, i32] + [vp] * 6 + [pstr, vp, vp, sz, vp]
         L.dkv_paged_weights.argtypes = [ppaged, vp, pstr, i32] + [vp] * 7 + [sz, vp]
         L.dkv_paged_evict.argtypes = [ppaged] + [vp] * 5 + [i32] * 3 + [vp, i32] + [vp] * 4 + [sz, vp]
+        L.dkv_paged_plan_workspace_bytes.restype = sz
+        L.dkv_paged_plan_workspace_bytes.argtypes = [i32]
+        L.dkv_paged_plan.argtypes = [i32] * 4 + [vp] * 3 + [i32, vp, vp, i32] + [vp] * 7 + [sz, vp]
+        pq = ctypes.POINTER(dkv_qpaged)
+        L.dkv_qk_norm_rope.argtypes = [ctypes.POINTER(dkv_rotate), vp, pstr, vp, pstr, vp, vp, vp, vp, pstr, vp, pstr,
+                                       ppaged, vp, pstr, vp, vp, vp, vp, sz, vp]
+        L.dkv_qpaged_check.argtypes = [pq]
+        L.dkv_qpaged_workspace_bytes.restype = sz
+        L.dkv_qpaged_workspace_bytes.argtypes = [pq]
+        L.dkv_qpaged_append.argtypes = [pq, vp, vp, pstr, i32, vp, vp, vp, sz, vp]
+        L.dkv_qpaged_gather.argtypes = [pq] + [vp] * 4 + [i32, vp, vp, pstr, vp, sz, vp]
+        L.dkv_qpaged_decode.argtypes = [pq, vp, pstr] + [vp] * 6 + [sz, vp]
+        L.dkv_qpaged_prefill.argtypes = [pq, vp, pstr, i32, i32] + [vp] * 5 + [pstr, vp, vp, sz, vp]
         _lib = L
     return _lib
 
@@ -689,6 +716,382 @@ def dkv_paged_evict(p: dkv_paged, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     if st:
         _check(st, "dkv_paged_evict")
     return kept, new_lens, new_weights
+
+
+# ---------------------------------------------------------------- pages and slots, norm and rotation
+
+_I64 = torch.int64
+
+
+def dkv_paged_plan_workspace_bytes(p) -> int:
+    """Bytes of dkv_paged_plan's workspace; p: a dkv_paged or dkv_qpaged."""
+    return int(lib().dkv_paged_plan_workspace_bytes(p.batch))
+
+
+def dkv_paged_plan(p, lens: torch.Tensor, news: torch.Tensor, free_pages: torch.Tensor, n_free: torch.Tensor,
+                   page_table: torch.Tensor, rows: int, slots: torch.Tensor | None = None,
+                   positions: torch.Tensor | None = None, starts: torch.Tensor | None = None,
+                   granted: torch.Tensor | None = None, new_lens: torch.Tensor | None = None,
+                   new_n_free: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Pages and slots of a step's new tokens: request b has lens[b] tokens and gets news[b] more (below 0:
+    drops its last ones), int32 [B] each.  Pages come off and go back to the stack free_pages[:n_free] (int32,
+    n_free int32 [1]) and into page_table int32 [B, max_pages], all in place -> (slots int64 [rows], positions
+    int32 [rows], starts int32 [B + 1], granted int32 [B], new_lens int32 [B], new_n_free int32 [1]); rows
+    behind the last token hold -1.  new_lens may be lens, new_n_free n_free.  `p`: a dkv_paged or dkv_qpaged."""
+    dev = lens.get_device()
+    if _elsewhere(lens, dev) or stream is not None:
+        with _place(dev, stream):
+            return dkv_paged_plan(p, lens, news, free_pages, n_free, page_table, rows, slots, positions, starts, granted,
+                                  new_lens, new_n_free, workspace)
+    _int32("dkv_paged_plan", rows)
+    b, width, room = p.batch, p.max_pages, max(rows, 0)
+    each, row = (b,), (room,)
+    if slots is None:
+        slots = torch.empty(row, dtype=_I64, device=dev)
+    if positions is None:
+        positions = torch.empty(row, dtype=_I32, device=dev)
+    if starts is None:
+        starts = torch.empty((b + 1,), dtype=_I32, device=dev)
+    if granted is None:
+        granted = torch.empty(each, dtype=_I32, device=dev)
+    if new_lens is None:
+        new_lens = torch.empty(each, dtype=_I32, device=dev)
+    if new_n_free is None:
+        new_n_free = torch.empty((1,), dtype=_I32, device=dev)
+    if lens.dtype is not _I32 or lens.shape != each or lens.get_device() != dev or not lens.is_contiguous():
+        _wrong("lens", lens, _I32, each, dev)
+    if news.dtype is not _I32 or news.shape != each or news.get_device() != dev or not news.is_contiguous():
+        _wrong("news", news, _I32, each, dev)
+    if free_pages.dtype is not _I32 or free_pages.dim() != 1 or free_pages.get_device() != dev or not free_pages.is_contiguous():
+        _wrong("free_pages", free_pages, _I32, (free_pages.numel(),), dev)
+    if n_free.dtype is not _I32 or n_free.shape != (1,) or n_free.get_device() != dev:
+        _wrong("n_free", n_free, _I32, (1,), dev)
+    if page_table.dtype is not _I32 or page_table.shape != (b, width) or page_table.get_device() != dev or not page_table.is_contiguous():
+        _wrong("page_table", page_table, _I32, (b, width), dev)
+    if slots.dtype is not _I64 or slots.shape != row or slots.get_device() != dev or not slots.is_contiguous():
+        _wrong("slots", slots, _I64, row, dev)
+    if positions.dtype is not _I32 or positions.shape != row or positions.get_device() != dev or not positions.is_contiguous():
+        _wrong("positions", positions, _I32, row, dev)
+    if starts.dtype is not _I32 or starts.shape != (b + 1,) or starts.get_device() != dev or not starts.is_contiguous():
+        _wrong("starts", starts, _I32, (b + 1,), dev)
+    if granted.dtype is not _I32 or granted.shape != each or granted.get_device() != dev or not granted.is_contiguous():
+        _wrong("granted", granted, _I32, each, dev)
+    if new_lens.dtype is not _I32 or new_lens.shape != each or new_lens.get_device() != dev or not new_lens.is_contiguous():
+        _wrong("new_lens", new_lens, _I32, each, dev)
+    if new_n_free.dtype is not _I32 or new_n_free.shape != (1,) or new_n_free.get_device() != dev:
+        _wrong("new_n_free", new_n_free, _I32, (1,), dev)
+    if workspace is None:
+        workspace = torch.zeros(max(dkv_paged_plan_workspace_bytes(p), 256), dtype=torch.uint8, device=dev)
+    elif workspace.get_device() != dev or not workspace.is_contiguous() or workspace.element_size() != 1:
+        raise ValueError("workspace: expected contiguous bytes on the tensors' device")
+    st = lib().dkv_paged_plan(
+        b, p.page_size, p.n_pages, width, lens.data_ptr(), news.data_ptr(), free_pages.data_ptr(), free_pages.shape[0],
+        n_free.data_ptr(), page_table.data_ptr(), rows, slots.data_ptr(), positions.data_ptr(), starts.data_ptr(),
+        granted.data_ptr(), new_lens.data_ptr(), new_n_free.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check(st, "dkv_paged_plan")
+    return slots, positions, starts, granted, new_lens, new_n_free
+
+
+@functools.lru_cache(maxsize=256)
+def _rotate(rows: int, hq: int, hkv: int, d: int, dtype: int, norm: bool, rope_dims: int, eps: float, base: float, inv_freq):
+    r = dkv_rotate(rows, hq, hkv, d, dtype, norm, rope_dims, eps, base, None)
+    if inv_freq is not None:
+        r.inv_freq = (ctypes.c_double * len(inv_freq))(*inv_freq)
+    return r, ctypes.byref(r)
+
+
+def dkv_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, rope_dims: int, rope_base: float = 1e4,
+                     inv_freq=None, q_gain: torch.Tensor | None = None, k_gain: torch.Tensor | None = None,
+                     eps: float | None = 1e-6, q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                     p: dkv_paged | None = None, v: torch.Tensor | None = None, k_pages: torch.Tensor | None = None,
+                     v_pages: torch.Tensor | None = None, slots: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, stream=None):
+    """Norm (eps None: none), gain [d] and rotation of q [rows, Hq, d] and k [rows, Hkv, d] (any strides with
+    adjacent channels) at positions int32 [rows] -> (q_out, k_out), in place where those are q and k; rows at
+    negative positions are left out (zeros in outputs allocated here).  `inv_freq`: rope_dims / 2 numbers, for
+    rope_base^(-2j / rope_dims).  With p, v [rows, Hkv, d], k_pages, v_pages and slots int64 [rows] (-1: none) the
+    rotated keys and the values also go into a 16-bit paged cache."""
+    dev = q.get_device()
+    if _elsewhere(q, dev) or stream is not None:
+        with _place(dev, stream):
+            return dkv_qk_norm_rope(q, k, positions, rope_dims, rope_base, inv_freq, q_gain, k_gain, eps, q_out, k_out, p, v,
+                                    k_pages, v_pages, slots, workspace)
+    if q.dim() != 3 or k.dim() != 3 or q.dtype not in _PAGED_DTYPES:
+        raise DkvError(DKV_ERR_ARG, "dkv_qk_norm_rope")
+    dt = q.dtype
+    rows, hq, d = q.shape
+    hkv = k.shape[1]
+    q_shape, k_shape = (rows, hq, d), (rows, hkv, d)
+    _int32("dkv_qk_norm_rope", rows, hq, hkv, d, rope_dims)
+    qs, ks = q.stride(), k.stride()
+    if qs[2] != 1:
+        _wrong_rows("q", q, dt, q_shape, dev)
+    if k.dtype is not dt or k.shape != k_shape or k.get_device() != dev or ks[2] != 1:
+        _wrong_rows("k", k, dt, k_shape, dev)
+    if positions.dtype is not _I32 or positions.shape != (rows,) or positions.get_device() != dev or not positions.is_contiguous():
+        _wrong("positions", positions, _I32, (rows,), dev)
+    for what, g in (("q_gain", q_gain), ("k_gain", k_gain)):
+        if g is not None and (g.dtype is not dt or g.shape != (d,) or g.get_device() != dev or not g.is_contiguous()):
+            _wrong(what, g, dt, (d,), dev)
+    if q_out is None:
+        q_out = torch.zeros(q_shape, dtype=dt, device=dev)
+    if k_out is None:
+        k_out = torch.zeros(k_shape, dtype=dt, device=dev)
+    qo, ko = q_out.stride(), k_out.stride()
+    if q_out.dtype is not dt or q_out.shape != q_shape or q_out.get_device() != dev or qo[2] != 1:
+        _wrong_rows("q_out", q_out, dt, q_shape, dev)
+    if k_out.dtype is not dt or k_out.shape != k_shape or k_out.get_device() != dev or ko[2] != 1:
+        _wrong_rows("k_out", k_out, dt, k_shape, dev)
+    pref = vp = vs = sp = kp = vpp = None
+    if p is not None or v is not None or k_pages is not None or v_pages is not None or slots is not None:
+        if p is None or v is None or k_pages is None or v_pages is None or slots is None:
+            raise DkvError(DKV_ERR_ARG, "dkv_qk_norm_rope")
+        g = _geometry(p)
+        s = v.stride()
+        if v.dtype is not dt or v.shape != k_shape or v.get_device() != dev or s[2] != 1:
+            _wrong_rows("v", v, dt, k_shape, dev)
+        if k_pages.dtype is not g.dtype or k_pages.stride() != g.strides or k_pages.shape != g.pool or k_pages.get_device() != dev:
+            _check_pool(g, k_pages, dev)
+        if v_pages.dtype is not g.dtype or v_pages.stride() != g.strides or v_pages.shape != g.pool or v_pages.get_device() != dev:
+            _check_pool(g, v_pages, dev)
+        if slots.dtype is not _I64 or slots.shape != (rows,) or slots.get_device() != dev or not slots.is_contiguous():
+            _wrong("slots", slots, _I64, (rows,), dev)
+        pref, vp, vs, sp, kp, vpp = g.ref, v.data_ptr(), _strides(0, s[1], s[0]), slots.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr()
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous() or workspace.element_size() != 1):
+        raise ValueError("workspace: expected contiguous bytes on the tensors' device")
+    if inv_freq is not None:
+        inv_freq = tuple(float(x) for x in inv_freq)
+        if len(inv_freq) != rope_dims // 2:
+            raise DkvError(DKV_ERR_ARG, "dkv_qk_norm_rope")
+    _, ref = _rotate(rows, hq, hkv, d, _PAGED_DTYPES[dt], eps is not None, rope_dims, 0.0 if eps is None else float(eps),
+                     float(rope_base), inv_freq)
+    st = lib().dkv_qk_norm_rope(
+        ref, q.data_ptr(), _strides(0, qs[1], qs[0]), k.data_ptr(), _strides(0, ks[1], ks[0]),
+        None if q_gain is None else q_gain.data_ptr(), None if k_gain is None else k_gain.data_ptr(), positions.data_ptr(),
+        q_out.data_ptr(), _strides(0, qo[1], qo[0]), k_out.data_ptr(), _strides(0, ko[1], ko[0]), pref, vp, vs, sp, kp, vpp,
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
+        torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check(st, "dkv_qk_norm_rope")
+    return q_out, k_out
+
+
+# ---------------------------------------------------------------- paged cache in 4 bits
+
+class _QGeometry:
+    """What the calls compare their tensors with, from a descriptor's bytes."""
+
+    __slots__ = ("key", "ref", "dtype", "pool", "strides", "batch", "heads", "kv_heads", "d", "each", "table", "q1", "lse1", "lib")
+
+    def __init__(self, p: dkv_qpaged, key: bytes):
+        self.key, self.ref = key, ctypes.byref(p)
+        self.dtype = torch.bfloat16 if p.dtype == DKV_BF16 else torch.float16
+        self.batch, self.heads, self.kv_heads, self.d = p.batch, p.n_q_heads, p.n_kv_heads, p.head_dim
+        self.pool = (p.n_pages, p.n_kv_heads, p.page_size * p.head_dim * 9 // 8)
+        self.strides = (p.stride_page, p.stride_head, 1)
+        self.each, self.table = (p.batch,), (p.batch, p.max_pages)
+        self.q1, self.lse1 = (p.batch, p.n_q_heads, p.head_dim), (p.batch, p.n_q_heads)
+        self.lib = lib()
+
+
+def _qgeometry(p: dkv_qpaged) -> _QGeometry:
+    key = bytes(p)
+    g = p.__dict__.get("_geometry")
+    if g is None or g.key != key:
+        g = p._geometry = _QGeometry(p, key)
+    return g
+
+
+def _check_cache(g: _QGeometry, t: torch.Tensor, dev: int) -> None:
+    if t.dtype is not torch.uint8 or t.shape != g.pool or t.get_device() != dev:
+        raise ValueError(f"cache: expected {torch.uint8} {g.pool} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.stride() != g.strides and any(n > 1 and a != b for n, a, b in zip(g.pool, t.stride(), g.strides)):
+        raise ValueError(f"cache: strides {t.stride()} are not the descriptor's {g.strides}")
+
+
+def _qpaged_ws(p: dkv_qpaged, workspace, dev: int) -> torch.Tensor:
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous() or workspace.element_size() != 1:
+            raise ValueError("workspace: expected contiguous bytes on the tensors' device")
+        return workspace
+    ws = torch.empty(dkv_qpaged_workspace_bytes(p), dtype=torch.uint8, device=dev)
+    ws[:256].zero_()
+    return ws
+
+
+def dkv_qpaged_layout(cache: torch.Tensor, batch: int, n_q_heads: int, head_dim: int, max_pages: int,
+                      dtype: torch.dtype = torch.float16, window: int = 0, sinks: int = 0) -> dkv_qpaged:
+    """Descriptor of a paged cache in 4 bits from its pool, uint8 [n_pages, Hkv, page_size * head_dim * 9 / 8]
+    (keys and values together; page and head strides may be any multiples of 16).  `dtype`: fp16 or bf16, of
+    rows, queries and outputs; `window`, `sinks` as in dkv_paged_layout."""
+    if cache.dim() != 3 or cache.dtype is not torch.uint8 or cache.stride(2) != 1 or dtype not in _PAGED_DTYPES or head_dim not in (64, 128):
+        raise DkvError(DKV_ERR_ARG if head_dim in (64, 128) else DKV_ERR_UNSUPPORTED, "dkv_qpaged_layout")
+    n_pages, hkv, page_bytes = cache.shape
+    if page_bytes * 8 % (9 * head_dim):
+        raise DkvError(DKV_ERR_SHAPE, "dkv_qpaged_layout")
+    page = page_bytes * 8 // (9 * head_dim)
+    _int32("dkv_qpaged_layout", batch, n_q_heads, max_pages, n_pages, hkv, page, window, sinks)
+    sp, sh, _ = cache.stride()
+    p = dkv_qpaged(batch, n_q_heads, hkv, head_dim, page, n_pages, max_pages, _PAGED_DTYPES[dtype], window, sinks, sp, sh)
+    _check(lib().dkv_qpaged_check(ctypes.byref(p)), "dkv_qpaged_layout")
+    return p
+
+
+def dkv_qpaged_workspace_bytes(p: dkv_qpaged) -> int:
+    """Bytes of the workspace of every call below; a call without one makes its own, and with that goes the
+    word that tells of bad lengths, pages, slots and values (dkv_get_error)."""
+    return int(lib().dkv_qpaged_workspace_bytes(ctypes.byref(p)))
+
+
+def dkv_qpaged_append(p: dkv_qpaged, K_new: torch.Tensor, V_new: torch.Tensor, cache: torch.Tensor, slots: torch.Tensor,
+                      workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Write rows K_new, V_new [rows, Hkv, d] (any strides with adjacent channels) in 4 bits to their slots,
+    int64 [rows] (page * page_size + place in the page, as dkv_paged_plan gives them; -1: left out)."""
+    dev = K_new.get_device()
+    if _elsewhere(K_new, dev) or stream is not None:
+        with _place(dev, stream):
+            return dkv_qpaged_append(p, K_new, V_new, cache, slots, workspace)
+    g = _qgeometry(p)
+    if K_new.stride() != V_new.stride():
+        K_new, V_new = K_new.contiguous(), V_new.contiguous()
+    rows = K_new.shape[0]
+    shape = (rows, g.kv_heads, g.d)
+    s = K_new.stride()
+    if K_new.dtype is not g.dtype or K_new.shape != shape or K_new.get_device() != dev or s[-1] != 1:
+        _wrong_rows("K_new", K_new, g.dtype, shape, dev)
+    if V_new.dtype is not g.dtype or V_new.shape != shape or V_new.get_device() != dev:
+        _wrong_rows("V_new", V_new, g.dtype, shape, dev)
+    if cache.dtype is not torch.uint8 or cache.stride() != g.strides or cache.shape != g.pool or cache.get_device() != dev:
+        _check_cache(g, cache, dev)
+    if slots.dtype is not _I64 or slots.shape != (rows,) or slots.get_device() != dev or not slots.is_contiguous():
+        _wrong("slots", slots, _I64, (rows,), dev)
+    ws = _qpaged_ws(p, workspace, dev)
+    st = g.lib.dkv_qpaged_append(g.ref, K_new.data_ptr(), V_new.data_ptr(), _strides(0, s[1], s[0]), rows, slots.data_ptr(),
+                                 cache.data_ptr(), ws.data_ptr(), ws.numel(), torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check(st, "dkv_qpaged_append")
+
+
+def dkv_qpaged_gather(p: dkv_qpaged, cache: torch.Tensor, page_table: torch.Tensor, first: torch.Tensor, K_out: torch.Tensor,
+                      V_out: torch.Tensor, counts: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                      stream=None):
+    """Read tokens back: token i < counts[b] (None: all n) from position first[b] + i of sequence b into K_out, V_out
+    [B, Hkv, n, d] (any strides with adjacent channels, both alike) -> (K_out, V_out).  Rows from counts[b] on stay."""
+    dev = cache.get_device()
+    if _elsewhere(cache, dev) or stream is not None:
+        with _place(dev, stream):
+            return dkv_qpaged_gather(p, cache, page_table, first, K_out, V_out, counts, workspace)
+    g = _qgeometry(p)
+    n = K_out.shape[2]
+    shape = (g.batch, g.kv_heads, n, g.d)
+    s = K_out.stride()
+    if K_out.dtype is not g.dtype or K_out.shape != shape or K_out.get_device() != dev or s[-1] != 1:
+        _wrong_rows("K_out", K_out, g.dtype, shape, dev)
+    if V_out.dtype is not g.dtype or V_out.shape != shape or V_out.get_device() != dev or V_out.stride() != s:
+        _wrong_rows("V_out", V_out, g.dtype, shape, dev)
+    if cache.dtype is not torch.uint8 or cache.stride() != g.strides or cache.shape != g.pool or cache.get_device() != dev:
+        _check_cache(g, cache, dev)
+    if page_table.dtype is not _I32 or page_table.shape != g.table or page_table.get_device() != dev or not page_table.is_contiguous():
+        _wrong("page_table", page_table, _I32, g.table, dev)
+    if first.dtype is not _I32 or first.shape != g.each or first.get_device() != dev or not first.is_contiguous():
+        _wrong("first", first, _I32, g.each, dev)
+    if counts is not None and (counts.dtype is not _I32 or counts.shape != g.each or counts.get_device() != dev or not counts.is_contiguous()):
+        _wrong("counts", counts, _I32, g.each, dev)
+    ws = _qpaged_ws(p, workspace, dev)
+    st = g.lib.dkv_qpaged_gather(
+        g.ref, cache.data_ptr(), page_table.data_ptr(), first.data_ptr(), None if counts is None else counts.data_ptr(), n,
+        K_out.data_ptr(), V_out.data_ptr(), _strides(s[0], s[1], s[2]), ws.data_ptr(), ws.numel(),
+        torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check(st, "dkv_qpaged_gather")
+    return K_out, V_out
+
+
+def dkv_qpaged_decode(p: dkv_qpaged, q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
+                      out: torch.Tensor | None = None, lse: torch.Tensor | bool | None = True,
+                      workspace: torch.Tensor | None = None, stream=None):
+    """One new token per sequence: q [B, Hq, d] at position lens[b] - 1 -> (out [B, Hq, d] in q's type, lse fp32
+    [B, Hq] or None)."""
+    dev = q.get_device()
+    if _elsewhere(q, dev) or stream is not None:
+        with _place(dev, stream):
+            return dkv_qpaged_decode(p, q, cache, page_table, lens, out, lse, workspace)
+    g = _qgeometry(p)
+    s = q.stride()
+    if q.dtype is not g.dtype or q.shape != g.q1 or q.get_device() != dev or s[-1] != 1:
+        _wrong_rows("q", q, g.dtype, g.q1, dev)
+    if cache.dtype is not torch.uint8 or cache.stride() != g.strides or cache.shape != g.pool or cache.get_device() != dev:
+        _check_cache(g, cache, dev)
+    if page_table.dtype is not _I32 or page_table.shape != g.table or page_table.get_device() != dev or not page_table.is_contiguous():
+        _wrong("page_table", page_table, _I32, g.table, dev)
+    if lens.dtype is not _I32 or lens.shape != g.each or lens.get_device() != dev or not lens.is_contiguous():
+        _wrong("lens", lens, _I32, g.each, dev)
+    if out is None:
+        out = torch.empty(g.q1, dtype=g.dtype, device=dev)
+    elif out.dtype is not g.dtype or out.shape != g.q1 or out.get_device() != dev or not out.is_contiguous():
+        _wrong("out", out, g.dtype, g.q1, dev)
+    if lse is True:
+        lse = torch.empty(g.lse1, dtype=_F32, device=dev)
+    elif lse is False:
+        lse = None
+    elif lse is not None and (lse.dtype is not _F32 or lse.shape != g.lse1 or lse.get_device() != dev or not lse.is_contiguous()):
+        _wrong("lse", lse, _F32, g.lse1, dev)
+    ws = _qpaged_ws(p, workspace, dev)
+    st = g.lib.dkv_qpaged_decode(
+        g.ref, q.data_ptr(), _strides(s[0], s[1], 0), cache.data_ptr(), page_table.data_ptr(), lens.data_ptr(), out.data_ptr(),
+        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check(st, "dkv_qpaged_decode")
+    return out, lse
+
+
+def dkv_qpaged_prefill(p: dkv_qpaged, q: torch.Tensor, starts: torch.Tensor, max_q: int, cache: torch.Tensor,
+                       page_table: torch.Tensor, lens: torch.Tensor, out: torch.Tensor | None = None,
+                       lse: torch.Tensor | bool | None = True, workspace: torch.Tensor | None = None, stream=None):
+    """The last tokens of each sequence, rows one behind the other: q [rows, Hq, d], sequence b's queries rows
+    starts[b] .. starts[b + 1] - 1 (int32 [B + 1]; at most max_q each), the last at position lens[b] - 1 ->
+    (out [rows, Hq, d] in q's type, lse fp32 [Hq, rows] or None).  Rows outside every span stay (zeros in outputs
+    allocated here)."""
+    dev = q.get_device()
+    if _elsewhere(q, dev) or stream is not None:
+        with _place(dev, stream):
+            return dkv_qpaged_prefill(p, q, starts, max_q, cache, page_table, lens, out, lse, workspace)
+    _int32("dkv_qpaged_prefill", max_q)
+    g, rows = _qgeometry(p), q.shape[0]
+    shape = (rows, g.heads, g.d)
+    s = q.stride()
+    if q.dtype is not g.dtype or q.shape != shape or q.get_device() != dev or s[-1] != 1:
+        _wrong_rows("q", q, g.dtype, shape, dev)
+    if starts.dtype is not _I32 or starts.shape != (g.batch + 1,) or starts.get_device() != dev or not starts.is_contiguous():
+        _wrong("starts", starts, _I32, (g.batch + 1,), dev)
+    if cache.dtype is not torch.uint8 or cache.stride() != g.strides or cache.shape != g.pool or cache.get_device() != dev:
+        _check_cache(g, cache, dev)
+    if page_table.dtype is not _I32 or page_table.shape != g.table or page_table.get_device() != dev or not page_table.is_contiguous():
+        _wrong("page_table", page_table, _I32, g.table, dev)
+    if lens.dtype is not _I32 or lens.shape != g.each or lens.get_device() != dev or not lens.is_contiguous():
+        _wrong("lens", lens, _I32, g.each, dev)
+    if out is None:
+        out = torch.zeros(shape, dtype=g.dtype, device=dev)
+    o = out.stride()
+    if out.dtype is not g.dtype or out.shape != shape or out.get_device() != dev or o[-1] != 1:
+        _wrong_rows("out", out, g.dtype, shape, dev)
+    l_shape = (g.heads, rows)
+    if lse is True:
+        lse = torch.zeros(l_shape, dtype=_F32, device=dev)
+    elif lse is False:
+        lse = None
+    elif lse is not None and (lse.dtype is not _F32 or lse.shape != l_shape or lse.get_device() != dev or not lse.is_contiguous()):
+        _wrong("lse", lse, _F32, l_shape, dev)
+    ws = _qpaged_ws(p, workspace, dev)
+    st = g.lib.dkv_qpaged_prefill(
+        g.ref, q.data_ptr(), _strides(0, s[1], s[0]), rows, max_q, starts.data_ptr(), cache.data_ptr(), page_table.data_ptr(),
+        lens.data_ptr(), out.data_ptr(), _strides(0, o[1], o[0]), None if lse is None else lse.data_ptr(), ws.data_ptr(),
+        ws.numel(), torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        _check(st, "dkv_qpaged_prefill")
+    return out, lse
 
 
 def dkv_debug_set_limits(stop_after_chunks: int = -1, wait_polls: int = 0) -> None:

@@ -568,6 +568,178 @@ DKV_API int dkv_paged_evict(const dkv_paged* p, void* k_pool, void* v_pool, cons
                             const int32_t* new_table, int32_t new_max_pages, int32_t* kept, int32_t* new_lens,
                             float* new_weights, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Pages and slots of a step's new tokens, on the GPU.
+ *
+ * Requests are sequences of a paged cache, exact or in 4 bits (below).  news[b] > 0
+ * new tokens take a page where they reach one that request b has not, from the
+ * top of the free list, request by request; news[b] < 0 drops its last -news[b]
+ * tokens (-lens[b]: all of them), and the pages that held only those go back to
+ * the list, before any is handed out.  A request is granted all of its new
+ * tokens or none: none where it and the requests before it need more pages than
+ * there are (one that needs no page goes on), or more rows than `rows`, or
+ * where it would outgrow the capacity (DKV_DEVERR_INDEX).
+ *   lens        device int32 [B]: tokens of each request
+ *   news        device int32 [B]
+ *   free_pages  device int32 [free_cap], in and out: a stack, n_free entries of it
+ *               in use; entries above the new count are not cleared
+ *   n_free      device int32 [1]
+ *   page_table  device int32 [B][max_pages], in and out: entries of pages that a
+ *               request takes are written, the others stay (those of pages given
+ *               back too).  A page given back must not be another request's
+ *   slots       device int64 [rows]: page * page_size + place in the page of each
+ *               granted token, request by request; -1 in the rows behind them
+ *   positions   device int32 [rows]: its position in its sequence; -1
+ *   starts      device int32 [B + 1]: first row of each request, and their number
+ *   granted     device int32 [B]: tokens granted (0 where news[b] < 0)
+ *   new_lens    device int32 [B], may be lens itself: lens + granted, or lens + news[b]
+ *   new_n_free  device int32 [1], may be n_free itself
+ * A page number outside [0, n_pages) gives slots of -1 and DKV_DEVERR_INDEX; so
+ * does a length outside [0, max_pages * page_size] (taken as the nearest
+ * bound), and a page given back that the list has no room for.
+ * Supported: batch <= 4096, page_size 16 to 256 (a power of two), max_pages *
+ * page_size <= 1048576, rows <= 2^30.
+ */
+DKV_API size_t dkv_paged_plan_workspace_bytes(int32_t batch);
+DKV_API int dkv_paged_plan(int32_t batch, int32_t page_size, int32_t n_pages, int32_t max_pages, const int32_t* lens,
+                           const int32_t* news, int32_t* free_pages, int32_t free_cap, const int32_t* n_free,
+                           int32_t* page_table, int32_t rows, int64_t* slots, int32_t* positions, int32_t* starts,
+                           int32_t* granted, int32_t* new_lens, int32_t* new_n_free, void* workspace, size_t ws_bytes,
+                           void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Queries and keys of a projection: each head's norm, its gain, and the rotation
+ * to the token's position, in one pass and with one rounding.
+ *   y = x / sqrt(mean of x^2 over the head's channels + eps) * gain
+ *   y_j, y_{j+h} = y_j cos - y_{j+h} sin, y_{j+h} cos + y_j sin    for j < h = rope_dims / 2,
+ * the angle position * inv_freq[j], with inv_freq[j] = rope_base^(-2j / rope_dims)
+ * where the caller gives none; channels from rope_dims on are not rotated.
+ * Squares are added in fp32 and angles held to 2^-32 of a circle at any position.
+ *   q, k        device [rows][heads][head_dim] under strides (token, head; batch is
+ *               unused): views of a fused projection's output are taken as they are
+ *   q_gain, k_gain   optional device [head_dim] in the rows' type (NULL: 1)
+ *   positions   device int32 [rows]; a row with a negative one is left out
+ *   q_out, k_out     device, under strides of their own; may be q and k themselves,
+ *               under the same strides.  k_out is optional where keys go to pages
+ *   p, v, slots, k_pool, v_pool   optional, together: keys as rotated and values v as
+ *               they are go to the slots (as dkv_paged_plan gives them; -1: none) of a
+ *               paged cache of exact rows.  No slot stands twice.  One outside the
+ *               pool is skipped and raises DKV_DEVERR_INDEX in the workspace's header
+ * The workspace (256 bytes, the header alone) is optional.
+ */
+typedef struct dkv_rotate {
+  int32_t rows;          /* tokens */
+  int32_t n_q_heads;
+  int32_t n_kv_heads;
+  int32_t head_dim;      /* 64 or 128 */
+  int32_t dtype;         /* DKV_FP16 or DKV_BF16 */
+  int32_t norm;          /* 0: neither norm nor eps */
+  int32_t rope_dims;     /* a multiple of 16 up to head_dim; 0: no rotation */
+  float eps;             /* >= 0 */
+  double rope_base;      /* > 1, finite (unused with inv_freq) */
+  const double* inv_freq;  /* optional, host [rope_dims / 2]: finite */
+} dkv_rotate;
+
+DKV_API int dkv_qk_norm_rope(const dkv_rotate* r, const void* q, const dkv_strides* qs, const void* k,
+                             const dkv_strides* ks, const void* q_gain, const void* k_gain, const int32_t* positions,
+                             void* q_out, const dkv_strides* qos, void* k_out, const dkv_strides* kos,
+                             const dkv_paged* p, const void* v, const dkv_strides* vs, const int64_t* slots,
+                             void* k_pool, void* v_pool, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Paged cache in 4 bits: 9/8 head_dim bytes a token and KV head, keys and values
+ * together, 0.28 of the 16-bit cache.
+ *
+ * One pool of bytes holds K and V: page `page` of head `head` begins at
+ * page * stride_page + head * stride_head and is a row of page_size / 16 blocks of
+ * 16 tokens, 18 d bytes each (G = d / 64 groups of 64 channels):
+ *     [K codes: G x 16 tokens x 32 bytes][V codes: the same]
+ *     [K scale, bias: 16 tokens x G x 2 fp16][V scale, bias: the same]
+ * with channel 2i of a group in the low half of byte i.  A value is
+ * scale * code + bias, as in the residual rows of the compressed cache.
+ *
+ * dkv_qpaged_append quantises each group of a row so that its values are fp16 numbers
+ * exactly: with L the group's largest magnitude and u = 2^(floor(log2(65/64 L)) - 10),
+ * at least 2^-24 (the spacing of fp16 numbers there),
+ *     b = round(min / u), n = round(max / u) - b, s = ceil(n / 15),
+ *     code = round((x / u - b) / s) in 0 .. 15,  scale = s u,  bias = b u
+ * (ties to even; s = 0 gives codes 0), all without further rounding.  A value is off by
+ * at most (max - min) / 30 + u.  fp16 holds them whatever the rows' type:
+ * values beyond +-61440 become +-61440 and NaN 0, and raise DKV_DEVERR_RANGE.
+ *
+ * Visibility, bad pages and lengths, strides of rows, batch and head limits are those
+ * of the 16-bit paged cache; a page out of range is read as one of zeros.  Scores,
+ * statistics and sums are fp32.  In front of the product with V decode holds a weight
+ * as the sum of two fp16 values (22 bits, fewer below e^-18 of the row's largest),
+ * prefill as one (relative error at most 2^-11, and weights below 2^-21 of the row's
+ * largest off by up to 2^-32 of it).  Cache values are expected to be finite (append
+ * writes no others) in the slots that a query sees; those that none sees may be anything.
+ */
+typedef struct dkv_qpaged {
+  int32_t batch;         /* sequences B */
+  int32_t n_q_heads;     /* query heads Hq */
+  int32_t n_kv_heads;    /* KV heads Hkv (Hq % Hkv == 0, Hq / Hkv <= 8) */
+  int32_t head_dim;      /* 64 or 128 */
+  int32_t page_size;     /* tokens of a page */
+  int32_t n_pages;       /* pages of the pool */
+  int32_t max_pages;     /* entries of a page-table row */
+  int32_t dtype;         /* of rows, queries and outputs: DKV_FP16 or DKV_BF16 */
+  int32_t window;        /* as in dkv_paged */
+  int32_t sinks;
+  int64_t stride_page;   /* bytes, multiples of 16, at least a page's bytes, below 2^38 */
+  int64_t stride_head;
+} dkv_qpaged;
+
+/* Check a descriptor, as dkv_paged_check does.  Host only. */
+DKV_API int dkv_qpaged_check(const dkv_qpaged* p);
+
+/* Bytes of the workspace of every call below (0 for a bad descriptor); see dkv_paged_workspace_bytes. */
+DKV_API size_t dkv_qpaged_workspace_bytes(const dkv_qpaged* p);
+
+/*
+ * Write rows K, V [rows][Hkv][head_dim] under strides `ns` (token, head; both alike)
+ * to their slots (device int64 [rows], as dkv_paged_plan gives them): -1 is left out, a
+ * slot outside the pool skipped with DKV_DEVERR_INDEX.  No slot stands twice.
+ */
+DKV_API int dkv_qpaged_append(const dkv_qpaged* p, const void* K, const void* V, const dkv_strides* ns, int32_t rows,
+                              const int64_t* slots, void* cache, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Read tokens back: token i < counts[b] (optional; NULL: n) from position first[b] + i of
+ * sequence b to K, V [B][Hkv][n][head_dim] under strides `os` (both alike), exactly in
+ * fp16, rounded in bf16: what dkv_compress_layout and dkv_append take.  Rows from
+ * counts[b] on stay; a position outside the capacity or on a bad page gives zeros and
+ * DKV_DEVERR_INDEX.
+ */
+DKV_API int dkv_qpaged_gather(const dkv_qpaged* p, const void* cache, const int32_t* page_table, const int32_t* first,
+                              const int32_t* counts, int32_t n, void* K, void* V, const dkv_strides* os, void* workspace,
+                              size_t ws_bytes, void* stream);
+
+/*
+ * Attention of one new token per sequence, at position lens[b] - 1: dkv_paged_decode over
+ * this cache.  q [B][Hq][head_dim] under strides (batch, head), out contiguous,
+ * lse optional fp32 [B][Hq].
+ */
+DKV_API int dkv_qpaged_decode(const dkv_qpaged* p, const void* q, const dkv_strides* qs, const void* cache,
+                              const int32_t* page_table, const int32_t* lens, void* out, float* lse, void* workspace,
+                              size_t ws_bytes, void* stream);
+
+/*
+ * Attention of the last tokens of each sequence, rows one behind the other: sequence b's
+ * queries are rows starts[b] .. starts[b + 1] - 1 (device int32 [B + 1], ascending, as
+ * dkv_paged_plan gives them), its last at position lens[b] - 1; negative positions
+ * see no token.  max_q: the most queries of a sequence.
+ *   q     device [rows][Hq][head_dim] under strides (token, head)
+ *   out   device, the same shape under strides `os`; rows outside every span stay
+ *   lse   optional device fp32 [Hq][rows]
+ * A sequence whose span is not in order, leaves the rows or holds more than max_q of them
+ * is left out, with DKV_DEVERR_INDEX.
+ */
+DKV_API int dkv_qpaged_prefill(const dkv_qpaged* p, const void* q, const dkv_strides* qs, int32_t rows, int32_t max_q,
+                               const int32_t* starts, const void* cache, const int32_t* page_table, const int32_t* lens,
+                               void* out, const dkv_strides* os, float* lse, void* workspace, size_t ws_bytes,
+                               void* stream);
+
 /*
  * Diagnostics for the failure path (no counterpart in the pages): from the
  * next launch on, the producer of every attention CTA of the fragment layout

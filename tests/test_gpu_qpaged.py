@@ -1,0 +1,391 @@
+"""The operators of a serving step over a paged cache in 4 bits against their definitions in 64 bits: pages and slots,
+norm and rotation, append and gather, decode and prefill; types, head layouts, page sizes, lengths from none on,
+windows, sinks, ragged batches; slots that nothing may look at hold NaN, unneeded page-table entries numbers out of
+range."""
+import math
+
+import pytest
+import torch
+
+from compressed_kv_cache_dkv_gb300 import dkv
+from tests import paged_ref as R
+from tests import qpaged_ref as Q
+
+pytestmark = pytest.mark.gpu
+
+
+def no_fault(ws):
+    assert dkv.dkv_get_error(ws) == (dkv.DKV_OK, 0)
+
+
+def workspace(p):
+    ws = torch.full((dkv.dkv_qpaged_workspace_bytes(p),), 0xFF, dtype=torch.uint8, device="cuda")
+    ws[:256] = 0  # only the header has to be zero
+    return ws
+
+
+def randn(shape, dt, seed, scale=1.0):
+    return (torch.randn(*shape, generator=torch.Generator().manual_seed(seed)) * scale).to(dt)
+
+
+# ---------------------------------------------------------------- append and gather
+
+@pytest.mark.parametrize("dtype,d,hkv,page,rows,scale", [
+    ("fp16", 128, 2, 16, 1, 1.0), ("bf16", 64, 1, 32, 37, 1.0), ("fp16", 64, 3, 256, 700, 30.0),
+    ("bf16", 128, 8, 64, 300, 1e-3), ("fp16", 128, 1, 128, 200, 3e-6), ("bf16", 128, 2, 16, 130, 4000.0)])
+def test_append_quantises_by_the_definition(dtype, d, hkv, page, rows, scale):
+    dt = Q.DT[dtype]
+    n_pages = -(-rows // page) + 2
+    cache = torch.full((n_pages, hkv, page * 9 * d // 8), 0xA5, dtype=torch.uint8, device="cuda")
+    p = dkv.dkv_qpaged_layout(cache, 1, hkv, d, n_pages, dtype=dt)
+    ws = workspace(p)
+    K, V = (randn((rows, hkv, d), dt, s, scale) for s in (1, 2))
+    K[::7, :, :64] += scale * 20          # groups far from zero
+    K[::5, :, 64:] = K[::5, :, 64:65]     # groups of one value
+    V[::3] = (V[::3] * 4 / scale).round() * scale / 4  # many ties
+    slots = torch.randperm(n_pages * page, generator=torch.Generator().manual_seed(3))[:rows]
+    if rows > 3:
+        slots[1] = -1
+    before = cache.clone()
+    dkv.dkv_qpaged_append(p, K.cuda(), V.cuda(), cache, slots.cuda(), workspace=ws)
+    large = any(bool((x[slots >= 0].double().abs() > 61440).any()) for x in (K, V))
+    assert dkv.dkv_get_error(ws)[1] == (dkv.DKV_DEVERR_RANGE if large else 0)
+    want = before.cpu()
+    blocks = want.view(n_pages, hkv, page // 16, 18 * d)
+    G = d // 64
+    for i, s in enumerate(slots.tolist()):
+        if s < 0:
+            continue
+        blk = blocks[s // page, :, s % page // 16]
+        for kv, x in enumerate((K, V)):
+            c, sc, b = Q.quantise(x[i].double())
+            c = c.to(torch.uint8)
+            for g in range(G):
+                at = kv * 8 * d + (g * 16 + s % 16) * 32
+                blk[:, at:at + 32] = c[:, g, ::2] | (c[:, g, 1::2] << 4)
+            at = (16 + kv) * d + s % 16 * G * 4
+            blk[:, at:at + 4 * G] = torch.stack([sc, b], -1).to(torch.float16).reshape(hkv, -1).view(torch.uint8)
+    assert torch.equal(cache.cpu(), want)
+
+
+def test_quantised_values_are_fp16_numbers_near_their_rows():
+    """The grid's claims: every value is an fp16 number, off by at most half a step and the grid's rounding."""
+    g = torch.Generator().manual_seed(0)
+    x = torch.randn(4000, 64, generator=g) * torch.exp(4 * torch.randn(4000, 1, generator=g)) + torch.randn(4000, 1, generator=g) * 3
+    x = x.half().double()
+    c, s, b = Q.quantise(x)
+    v = Q.values(c, s, b)
+    assert torch.equal(v.half().double(), v)
+    lo, hi = x.min(1).values, x.max(1).values
+    top = torch.maximum(lo.abs(), hi.abs())
+    u = 2.0 ** torch.clamp(torch.floor(torch.log2(top * 65 / 64)) - 10, min=-24)
+    assert bool(((v - x).abs().max(1).values <= (hi - lo) / 30 + u).all())
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_append_saturates_and_says_so(dtype):
+    dt = Q.DT[dtype]
+    cache = torch.zeros(1, 1, 16 * 144, dtype=torch.uint8, device="cuda")
+    p = dkv.dkv_qpaged_layout(cache, 1, 1, 128, 1, dtype=dt)
+    ws = workspace(p)
+    K, V = (randn((4, 1, 128), dt, s) for s in (1, 2))
+    K[0, 0, 3], K[1, 0, 70], V[2, 0, 0], V[3, 0, 64] = math.inf, -math.inf, math.nan, 65000.0
+    slots = torch.arange(4, device="cuda")
+    dkv.dkv_qpaged_append(p, K.cuda(), V.cuda(), cache, slots, workspace=ws)
+    assert dkv.dkv_get_error(ws) == (dkv.DKV_ERR_DEVICE, dkv.DKV_DEVERR_RANGE)
+    out = [torch.zeros(1, 1, 4, 128, dtype=dt, device="cuda") for _ in range(2)]
+    table, first = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    dkv.dkv_qpaged_gather(p, cache, table, first, *out, workspace=ws)
+    no_fault(ws)
+    for x, y in zip((K, V), out):
+        assert torch.equal(y[0, 0].cpu(), Q.values(*Q.quantise(x[:, 0].double())).to(dt))
+    dkv.dkv_qpaged_append(p, K.cuda() * 0, V.cuda() * 0, cache, torch.tensor([-1, 16, -2, 3], device="cuda"), workspace=ws)
+    assert dkv.dkv_get_error(ws)[1] & dkv.DKV_DEVERR_INDEX
+
+
+@pytest.mark.parametrize("dtype,d,hkv,page,lens,first,counts", [
+    ("fp16", 128, 2, 16, [40], [0], [40]), ("bf16", 64, 3, 32, [100, 1, 65], [7, 0, 3], [90, 1, 0]),
+    ("fp16", 64, 1, 256, [600, 300], [255, 17], [300, 1]), ("bf16", 128, 8, 64, [130], [63], [67])])
+def test_gather_reads_its_tokens_only(dtype, d, hkv, page, lens, first, counts):
+    c = Q.Cache(lens, hkv, d, page, dtype, seed=5, pad_head=16)
+    p = c.layout(hkv)
+    ws = workspace(p)
+    n = max(counts) + 1
+    out = [torch.full((c.B, n, hkv, d), 7.0, dtype=c.dt, device="cuda").transpose(1, 2) for _ in range(2)]
+    dkv.dkv_qpaged_gather(p, c.cache, c.table.cuda(), c.dev(first), *out, counts=c.dev(counts), workspace=ws)
+    no_fault(ws)
+    for x, rows in zip(out, (c.K, c.V)):
+        for b in range(c.B):
+            want = torch.full((hkv, n, d), 7.0, dtype=c.dt)
+            want[:, :counts[b]] = rows[b][:, first[b]:first[b] + counts[b]].to(c.dt)
+            assert torch.equal(x[b].cpu(), want)
+
+
+# ---------------------------------------------------------------- decode
+
+CASES = [
+    # dtype, d, hq, hkv, page, lens, window, sinks
+    ("fp16", 128, 12, 2, 64, [1000], 0, 0),
+    ("fp16", 64, 1, 1, 16, [1], 0, 0),
+    ("bf16", 128, 8, 1, 16, [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 0], 0, 0),
+    ("bf16", 64, 9, 3, 32, [0, 300, 0, 17, 555], 0, 0),
+    ("fp16", 128, 7, 7, 256, [5, 2049], 0, 0),
+    ("bf16", 128, 5, 1, 128, [777, 1300], 100, 0),
+    ("fp16", 128, 12, 4, 16, [50, 64, 65, 500, 1999], 64, 4),
+    ("bf16", 64, 16, 2, 64, [1500, 1, 70, 71], 70, 1),
+    ("fp16", 64, 4, 2, 32, [900, 130], 1, 0),
+    ("fp16", 128, 6, 2, 64, [1500, 333], 200, 130),
+    ("bf16", 128, 2, 1, 32, [400, 90], 1000, 5),
+]
+
+
+@pytest.mark.parametrize("dtype,d,hq,hkv,page,lens,window,sinks", CASES)
+def test_decode(dtype, d, hq, hkv, page, lens, window, sinks):
+    c = Q.Cache(lens, hkv, d, page, dtype, seed=len(lens), pad_head=32)
+    p = c.layout(hq, window, sinks)
+    ws = workspace(p)
+    q = randn((c.B, hq, d), c.dt, 7, 2.0)
+    table = c.hidden_table([n - 1 for n in lens], window, sinks)
+    out, lse = dkv.dkv_qpaged_decode(p, q.cuda(), c.cache, table, c.dev(lens), workspace=ws)
+    no_fault(ws)
+    check_decode(c, q, out, lse, lens, hq, window, sinks)
+    again, lse2 = dkv.dkv_qpaged_decode(p, q.cuda(), c.cache, table, c.dev(lens), workspace=ws)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+def check_decode(c, q, out, lse, lens, hq, window, sinks):
+    for b in range(c.B):
+        for j in range(hq):
+            ref, parts, pv = Q.attend(q[b, j:j + 1].double(), c, b, j * c.hkv // hq, torch.tensor([lens[b] - 1]), window, sinks)
+            # The products of the codes and of the biases are added up apart, as are the weights' with codes and biases.
+            # The lower half of a weight times scale (at most 2^14, the row's largest weight at 2^14) is an fp16 number: in
+            # the subnormals off by half of 2^-24, which is 2^-39 of the largest, on codes up to 15.
+            pv = pv + 2.0 ** (21 - 39) * 15 * c.q[b][1][1][j * c.hkv // hq].sum(0).repeat_interleave(64)
+            R.check_rows(out[b, j:j + 1], lse[b, j:j + 1], (ref[0], ref[1], ref[2], pv, max(ref[4], parts)), c.d, c.dt, 2.0 ** -21,
+                         f"sequence {b} head {j}")
+
+
+# ---------------------------------------------------------------- prefill
+
+PREFILL = [
+    # dtype, d, hq, hkv, page, lens, news, window, sinks
+    ("fp16", 128, 12, 2, 64, [300], [300], 0, 0),
+    ("bf16", 128, 4, 1, 16, [130, 1, 64], [130, 1, 64], 0, 0),
+    ("fp16", 64, 3, 3, 32, [65, 200], [1, 70], 0, 0),
+    ("bf16", 64, 8, 8, 32, [333, 1001], [32, 32], 0, 0),
+    ("fp16", 128, 8, 1, 256, [700], [3], 0, 0),
+    ("bf16", 128, 12, 4, 16, [600, 0, 257], [600, 0, 200], 100, 4),
+    ("fp16", 128, 2, 2, 128, [513, 100], [513, 1], 64, 0),
+    ("bf16", 64, 10, 2, 64, [400], [129], 70, 130),
+    ("fp16", 64, 5, 1, 16, [100, 90, 80], [9, 0, 17], 1, 0),
+    ("bf16", 128, 16, 2, 64, [2500], [4], 0, 0),
+    ("fp16", 128, 6, 6, 32, [520], [260], 300, 70),
+    ("fp16", 128, 4, 2, 32, [5, 40], [9, 12], 0, 0),  # more queries than tokens: the first see nothing
+]
+
+
+@pytest.mark.parametrize("dtype,d,hq,hkv,page,lens,news,window,sinks", PREFILL)
+def test_prefill(dtype, d, hq, hkv, page, lens, news, window, sinks):
+    c = Q.Cache(lens, hkv, d, page, dtype, seed=sum(lens), pad_head=16)
+    p = c.layout(hq, window, sinks)
+    ws = workspace(p)
+    gap = 3  # rows in front of the first span and behind the last belong to nobody
+    starts = [gap]
+    for n in news:
+        starts.append(starts[-1] + n)
+    rows = starts[-1] + 5
+    q = randn((rows, hq, d), c.dt, 9, 2.0)
+    table = c.hidden_table([n - m for n, m in zip(lens, news)], window, sinks)
+    fused = torch.full((rows, hq + 1, d), 7.0, dtype=c.dt, device="cuda")
+    out, lse = fused[:, :hq], torch.full((hq, rows), 7.0, device="cuda")
+    dkv.dkv_qpaged_prefill(p, q.cuda(), c.dev(starts), max(news), c.cache, table, c.dev(lens), out=out, lse=lse, workspace=ws)
+    no_fault(ws)
+    check_prefill(c, q, out, lse, lens, news, starts, hq, window, sinks)
+    mine = torch.zeros(rows, dtype=torch.bool)
+    mine[starts[0]:starts[-1]] = True
+    assert bool((fused[:, hq] == 7).all()) and bool((out[~mine.cuda()] == 7).all()) and bool((lse[:, ~mine.cuda()] == 7).all())
+
+
+def check_prefill(c, q, out, lse, lens, news, starts, hq, window, sinks):
+    for b in range(c.B):
+        if not news[b]:
+            continue
+        rows = slice(starts[b], starts[b] + news[b])
+        pos = torch.arange(lens[b] - news[b], lens[b])
+        for j in range(hq):
+            ref, parts, _ = Q.attend(q[rows, j].double(), c, b, j * c.hkv // hq, pos, window, sinks)
+            # A weight is an fp16 number, the row's largest at 2^7 or more (the reference lies 7 below a maximum, which only
+            # grows): in the subnormals it is off by half of 2^-24, 2^-32 of the largest, whatever its own size.
+            scale = ref[3] + 2.0 ** (11 - 32) * R.seen(pos, lens[b], window, sinks).double() @ c.V[b][j * c.hkv // hq].abs()
+            R.check_rows(out[rows, j], lse[j, rows], (*ref[:3], scale, max(ref[4], parts)), c.d, c.dt, 2.0 ** -11, f"sequence {b} head {j}")
+
+
+# ---------------------------------------------------------------- norm and rotation
+
+@pytest.mark.parametrize("dtype,d,hq,hkv,rope,rows,gain,eps", [
+    ("fp16", 128, 12, 2, 128, 16, True, 1e-6), ("bf16", 64, 1, 1, 64, 1, True, 1e-5), ("bf16", 128, 5, 5, 64, 33, False, 1e-6),
+    ("fp16", 64, 9, 3, 48, 7, True, None), ("fp16", 128, 32, 8, 16, 5, True, 1e-6), ("bf16", 128, 3, 1, 0, 4, True, 1e-6),
+    ("fp16", 128, 2, 1, 112, 6000, False, None)])
+def test_norm_and_rotation(dtype, d, hq, hkv, rope, rows, gain, eps):
+    dt = Q.DT[dtype]
+    qkv = randn((rows, hq + hkv, d), dt, 1, 3.0)
+    gains = [1 + randn((d,), dt, s, 0.3) for s in (2, 3)] if gain else [None, None]
+    pos = torch.randint(0, 1 << 20, (rows,), generator=torch.Generator().manual_seed(4)).int()
+    pos[0] = (1 << 31) - 1 if rows > 4 else 0
+    if rows > 2:
+        pos[2] = -1
+    fused = qkv.cuda()
+    q, k = fused[:, :hq], fused[:, hq:]
+    dkv.dkv_qk_norm_rope(q, k, pos.cuda(), rope, 1e4, q_gain=gains[0] if gains[0] is None else gains[0].cuda(),
+                         k_gain=gains[1] if gains[1] is None else gains[1].cuda(), eps=eps, q_out=q, k_out=k)
+    x = qkv.double()
+    y = x / (x.square().mean(-1, keepdim=True) + eps).sqrt() if eps is not None else x
+    if gain:
+        y = y * torch.cat([gains[0][None].expand(hq, d), gains[1][None].expand(hkv, d)]).double()
+    h = rope // 2
+    angle = pos.double()[:, None, None] * 1e4 ** (-2.0 * torch.arange(h).double() / max(rope, 1))
+    a, b = y[..., :h], y[..., h:2 * h]
+    want = torch.cat([a * angle.cos() - b * angle.sin(), b * angle.cos() + a * angle.sin(), y[..., 2 * h:]], -1)
+    size = torch.cat([a.abs() + b.abs(), a.abs() + b.abs(), y[..., 2 * h:].abs()], -1)
+    want[pos < 0] = x[pos < 0]
+    # fp32: d additions of squares, the root, three products, the angle (2^-25 of the circle, as steps of pi) and sincospi
+    # (2^-23), the last sum; angles of the definition in 64 bits are off by position 2^-52
+    f32 = (d / 4 + 24) * 2.0 ** -24 + float(pos.max()) * 2.0 ** -51
+    tol = torch.finfo(dt).eps / 2 * want.abs() + 2 * f32 * size + torch.finfo(dt).smallest_normal * torch.finfo(dt).eps
+    err = (fused.double().cpu() - want).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+
+
+def test_rotation_by_given_frequencies_and_into_pages():
+    dt, hq, hkv, d, page, rows = torch.bfloat16, 6, 2, 128, 32, 50
+    freq = [0.7 / (1 + j) for j in range(32)]
+    q, k, v = randn((rows, hq, d), dt, 1), randn((rows, hkv, d), dt, 2), randn((rows, hkv, d), dt, 3)
+    pos = torch.arange(rows).int() * 977
+    pools = [torch.full((4, page, hkv, d), 5.0, dtype=dt, device="cuda").transpose(1, 2) for _ in range(2)]
+    p = dkv.dkv_paged_layout(pools[0], 1, hq, 4)
+    slots = torch.randperm(4 * page, generator=torch.Generator().manual_seed(5))[:rows]
+    slots[3], slots[4] = -1, 4 * page
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    qo, ko = dkv.dkv_qk_norm_rope(q.cuda(), k.cuda(), pos.cuda(), 64, inv_freq=freq, p=p, v=v.cuda(), k_pages=pools[0],
+                                  v_pages=pools[1], slots=slots.cuda(), workspace=ws)
+    assert dkv.dkv_get_error(ws) == (dkv.DKV_ERR_DEVICE, dkv.DKV_DEVERR_INDEX)
+    y = k.double()
+    y = y / (y.square().mean(-1, keepdim=True) + 1e-6).sqrt()
+    angle = pos.double()[:, None, None] * torch.tensor(freq, dtype=torch.float64)
+    want = torch.cat([y[..., :32] * angle.cos() - y[..., 32:64] * angle.sin(), y[..., 32:64] * angle.cos() + y[..., :32] * angle.sin(), y[..., 64:]], -1)
+    assert bool(((ko.double().cpu() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-5).all())
+    for pool, rows_of in zip(pools, (ko.cpu(), v)):
+        expect = torch.full((4, hkv, page, d), 5.0, dtype=dt)
+        for i, s in enumerate(slots.tolist()):
+            if 0 <= s < 4 * page:
+                expect[s // page, :, s % page] = rows_of[i]
+        assert torch.equal(pool.cpu(), expect)
+
+
+# ---------------------------------------------------------------- pages and slots
+
+def plan_ref(page, n_pages, width, lens, news, free, n_free, table, rows):
+    """The definition, one request at a time, on lists."""
+    of = lambda n: -(-n // page)  # noqa: E731
+    cap = width * page
+    free, table = list(free), [list(r) for r in table]
+    lens = [min(max(n, 0), cap) for n in lens]
+    grow = [n if 0 < n <= cap - m else 0 for n, m in zip(news, lens)]
+    cut = [min(-n, m) if n < 0 else 0 for n, m in zip(news, lens)]
+    stack = free[:n_free]
+    for b in range(len(lens)):
+        for j in range(of(lens[b] - cut[b]), of(lens[b])):
+            stack.append(table[b][j])
+    back = stack[n_free:]
+    total, need_all, rows_all = len(stack), 0, 0
+    slots, positions, starts, granted, new_lens = [], [], [0], [], []
+    for b in range(len(lens)):
+        need = of(lens[b] + grow[b]) - of(lens[b])
+        need_all += need
+        rows_all += grow[b]
+        take = grow[b] if (need == 0 or need_all <= total) and rows_all <= rows else 0
+        if take:
+            for j in range(of(lens[b]), of(lens[b] + take)):
+                table[b][j] = stack.pop()
+        for t in range(lens[b], lens[b] + take):
+            pg = table[b][t // page]
+            slots.append(pg * page + t % page if 0 <= pg < n_pages else -1)
+            positions.append(t)
+        starts.append(starts[-1] + take)
+        granted.append(take)
+        new_lens.append(lens[b] - cut[b] + take)
+    for i, x in enumerate(back):
+        if n_free + i < len(free):
+            free[n_free + i] = x
+    pad = [-1] * (rows - len(slots))
+    return slots + pad, positions + pad, starts, granted, new_lens, [min(len(stack), len(free))], table, free
+
+
+def plan_case(B, page, width, seed, most, fill=1.0, share=(0.3, 0.5, 0.1)):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=g))  # noqa: E731
+    cap = width * page
+    lens, news = [], []
+    for _ in range(B):
+        kind = float(torch.rand(1, generator=g))
+        n = r(0, max(0, cap - most))
+        if kind < share[0]:
+            n, m = 0, r(0, most)
+        elif kind < share[0] + share[1]:
+            m = 1
+        elif kind < sum(share):
+            m = -n
+        else:
+            m = -r(0, n)
+        lens.append(n)
+        news.append(m)
+    used = [-(-n // page) for n in lens]
+    need = sum(max(0, -(-(n + m) // page) - u) for n, m, u in zip(lens, news, used))
+    n_free = max(0, int(need * fill))
+    n_pages = sum(used) + max(n_free, 1) + 3
+    perm = torch.randperm(n_pages, generator=g).tolist()
+    table = [[-9] * width for _ in range(B)]
+    for b, u in enumerate(used):
+        for j in range(u):
+            table[b][j] = perm.pop()
+    free = perm[:n_free] + [-5] * (n_pages - n_free)
+    return lens, news, free, n_free, n_pages, table
+
+
+@pytest.mark.parametrize("B,page,width,most,rows,fill,in_place", [
+    (1, 16, 4, 5, 8, 1.0, False), (3, 256, 2, 300, 1000, 1.0, True), (64, 16, 30, 1, 64, 1.0, True), (200, 32, 12, 100, 4000, 0.5, False),
+    (1024, 16, 4, 20, 9000, 0.9, True), (1025, 64, 8, 300, 60000, 0.7, False), (4096, 16, 6, 70, 100000, 1.2, True),
+    (300, 16, 40, 500, 2000, 1.0, False), (5, 128, 3, 200, 0, 1.0, False)])
+def test_plan(B, page, width, most, rows, fill, in_place):
+    lens, news, free, n_free, n_pages, table = plan_case(B, page, width, B, most, fill)
+    want = plan_ref(page, n_pages, width, lens, news, free, n_free, table, rows)
+    p = dkv.dkv_qpaged(B, 1, 1, 64, page, n_pages, width, 0, 0, 0, 1 << 20, 1 << 20)
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    L, F, N, T = dev(lens), dev(free), dev([n_free]), dev(table)
+    ws = torch.full((dkv.dkv_paged_plan_workspace_bytes(p),), 0xFF, dtype=torch.uint8, device="cuda")
+    ws[:256] = 0
+    got = dkv.dkv_paged_plan(p, L, dev(news), F, N, T, rows, new_lens=L if in_place else None, new_n_free=N if in_place else None,
+                             workspace=ws)
+    no_fault(ws)
+    for name, x, y in zip(("slots", "positions", "starts", "granted", "lens", "n_free", "table", "free"), (*got, T, F), want):
+        assert x.tolist() == y, name
+
+
+def test_plan_refuses_what_does_not_fit():
+    page, width = 16, 4
+    p = dkv.dkv_qpaged(5, 1, 1, 64, page, 40, width, 0, 0, 0, 1 << 20, 1 << 20)
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    ws = torch.zeros(dkv.dkv_paged_plan_workspace_bytes(p), dtype=torch.uint8, device="cuda")
+    lens, news = [60, 64, -3, 100, 16], [5, 1, 3, 0, -20]   # over the capacity twice, bad lengths twice, too many dropped
+    table = [[0, 1, 2, 3], [4, 5, 6, 7], [9] * 4, [10, 11, 12, 13], [14, 9, 9, 9]]
+    free = [20, 21, 77, -1]                                  # the top page does not exist; one place left in the list
+    want = plan_ref(page, 40, width, lens, news, free, 3, table, 20)
+    F, T = dev(free), dev(table)
+    got = dkv.dkv_paged_plan(p, dev(lens), dev(news), F, dev([3]), T, 20, workspace=ws)
+    assert dkv.dkv_get_error(ws) == (dkv.DKV_ERR_DEVICE, dkv.DKV_DEVERR_INDEX)
+    assert [x.tolist() for x in (*got, T, F)] == list(want)
+    # a list without room for a page that comes back
+    F, T = dev([20]), dev(table)
+    got = dkv.dkv_paged_plan(p, dev([16, 16, 0, 0, 0]), dev([-16, -1, 0, 0, 0]), F, dev([1]), T, 4, workspace=ws)
+    assert int(got[5]) == 1 and F.tolist() == [20] and got[4].tolist() == [0, 15, 0, 0, 0]
+    assert dkv.dkv_get_error(ws)[1] == dkv.DKV_DEVERR_INDEX
