@@ -11,23 +11,26 @@
 //                they lie, with q's channels in the same order
 //   o = C_V^T w  channels in M; two tokens' words interleaved by byte permutes give the pairs along k
 // q is brought to at most 2^15 by a power of two (bf16 queries become fp16 without loss above 2^-24 of the largest),
-// w = p s 2^(14 - E) with a running power of two E over the scales seen, as the sum of two fp16 values (22 bits).
+// w = p s 2^-E with a running power of two E over the scales seen, as the sum of two fp16 values (22 bits).
 //
-// The visible tokens of a sequence are cut into 64-token tiles, dealt out evenly to the CTAs as in the
-// 16-bit decode; a producer warp streams tiles with bulk copies (one per page, or for larger pages one per tile),
-// kQdWarps consumer warps take tiles in turn, each with its own online softmax, merged at a unit's end; units
-// that lie in several CTAs' runs leave records that a second grid joins in run order.
+// The visible tokens of a sequence are cut into 32-token tiles, dealt out evenly to the CTAs as in the 16-bit
+// decode; a CTA's warps take its tiles in turn, each with stages, copies and an online softmax of its own: a warp
+// looks up the pages of its next tiles, a lane for each, and fetches a tile with one bulk copy per page as soon as a
+// stage is free, so that no warp waits for another before a unit's end.  There the warps are merged; units that lie
+// in several CTAs' runs leave records that a second grid joins in run order.
 #include "qpaged.cuh"
 
 namespace dkv {
 namespace {
 
-constexpr int kQdTile = 64, kQdBlocks = kQdTile / kQBlock;
-constexpr int kQdWarps = 8;
-constexpr int kQdStages = 2 * kQdWarps;  // a multiple of it: a stage belongs to one warp, which so sees each of its phases
-constexpr int kQdThreads = 32 * (kQdWarps + 1);
+constexpr int kQdTile = 32, kQdBlocks = kQdTile / kQBlock;
+constexpr int kQdWarps = 16, kQdDepth = 2;  // warps, and stages of each
+constexpr int kQdThreads = 32 * kQdWarps;
 constexpr int kQdCombThreads = 512, kQdCombCols = 32;
-constexpr float kQdShift = 14.f;  // weights carry 2^14: those down to e^-18 of the largest keep 11 bits
+// Weights are 2^(score - ref).  A head's reference lies kQdShift below a maximum and moves only when a score exceeds
+// that by kQdSlack (at once where scores are so large that their rounding shows): weights are at most 2^15, and those
+// down to e^-18 of the largest keep 11 bits in the lower of the two fp16 values too.
+constexpr float kQdShift = 7.f, kQdSlack = 8.f, kQdLarge = 0x1p20f;
 
 template <int D>
 constexpr int qrec_floats() { return 16 + 8 * D; }
@@ -59,13 +62,23 @@ struct QdArgs {
 template <int D>
 struct QdSmem {
   static constexpr uint32_t kStage = kQdBlocks * qblock_bytes(D);
-  static constexpr uint32_t kOffMerge = kQdStages * kStage;                  // o [warp][D][8]
-  static constexpr uint32_t kOffStats = kOffMerge + kQdWarps * D * 32;       // m, l [warp][2][8]
-  static constexpr uint32_t kOffBar = kOffStats + kQdWarps * 64;             // full, empty [stage]
-  static constexpr uint32_t kOffBad = kOffBar + kQdStages * 16;              // [stage] blocks on bad pages
-  static constexpr uint32_t kOffPrefix = kOffBad + kQdStages * 4;            // [B + 1]
+  static constexpr uint32_t kOffMerge = kQdWarps * kQdDepth * kStage;        // o [warp][D][8]
+  static constexpr uint32_t kOffStats = kOffMerge + kQdWarps * D * 32;       // ref, l [warp][2][8]
+  static constexpr uint32_t kOffBar = kOffStats + kQdWarps * 64;             // [warp][stage]
+  static constexpr uint32_t kOffPrefix = kOffBar + kQdWarps * kQdDepth * 8;  // [B + 1]
 };
 
+// the (scale, bias) pairs of a token
+template <int G>
+__device__ inline void lds_params(uint32_t at, uint32_t (&x)[G]) {
+  if (G == 2) {
+    const uint2 y = lds64(at);
+    x[0] = y.x;
+    x[G - 1] = y.y;
+  } else {
+    x[0] = lds32(at);
+  }
+}
 __device__ inline float half_lo(uint32_t x) { return __low2float(*reinterpret_cast<__half2*>(&x)); }
 __device__ inline float half_hi(uint32_t x) { return __high2float(*reinterpret_cast<__half2*>(&x)); }
 
@@ -77,18 +90,13 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
   constexpr int G = D / 64, BB = qblock_bytes(D);
   float* merge = reinterpret_cast<float*>(smem + S::kOffMerge);
   float* stats = reinterpret_cast<float*>(smem + S::kOffStats);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kOffBar);
-  uint64_t* empty = full + kQdStages;
-  volatile uint32_t* bad_blocks = reinterpret_cast<uint32_t*>(smem + S::kOffBad);
   int* prefix = reinterpret_cast<int*>(smem + S::kOffPrefix);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t sb = smem_u32(smem);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kOffBar) + warp * kQdDepth;
+  const uint32_t stages = smem_u32(smem) + warp * kQdDepth * S::kStage;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kQdStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
-    }
+    for (int i = 0; i < kQdWarps * kQdDepth; ++i) mbar_init(reinterpret_cast<uint64_t*>(smem + S::kOffBar) + i, 1);
     fence_mbar_init();
   }
   deal_prefix(a.B, prefix, [&](int b) { return qd_span(a, b).n; });
@@ -106,78 +114,86 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
   if (c >= nc) return;
   const int x0 = deal_bound(total, nc, c), x1 = deal_bound(total, nc, c + 1);
 
-  if (warp == kQdWarps) {
-    // =========================== producer
-    const uint32_t el = elect_one();
-    const uint64_t policy = policy_evict_first();  // a cache is read once a step
-    const int rows = min(a.page_mask + 1, kQdTile), runs = kQdTile / rows, bpr = rows / kQBlock;  // a copy per run of a page
-    bool ok = true;
-    int it = 0;
-    for (int x = x0; x < x1 && ok;) {
+  // ---- the warp's tiles x0 + warp, x0 + warp + kQdWarps, ...: a lane looks after one run of slots of a page
+  const uint32_t el = elect_one();
+  const uint64_t policy = policy_evict_first();  // a cache is read once a step
+  const int rows = min(a.page_mask + 1, kQdTile), runs = kQdTile / rows, bpr = rows / kQBlock, batch = 32 / runs;
+  uint64_t src = 0;       // of the lane's run: address, bytes, place in the stage
+  uint32_t bytes = 0, to = 0, none = 0;  // none: lanes whose page is out of range
+  auto look = [&](int xb) {
+    const int x = xb + lane / runs * kQdWarps;
+    bool bad = false;
+    bytes = 0;
+    if (x < x1) {
       const DealSeg g = deal_seg(prefix, a.B, a.Hkv, x, x1);
       const QSpan s = qd_span(a, g.b);
-      for (int j = g.j0; j < g.j1; ++j, ++it) {
-        const int st = it % kQdStages, first = s.token(j) + lane * rows;
-        // lane i < runs: its page, and the run's blocks that hold a visible token
-        int page = -1, b0 = bpr, b1 = 0;
-        bool bad = false;
-        if (lane < runs) {
-          for (int i = 0; i < bpr; ++i) {
-            const int t = first + i * kQBlock;
-            if (t < s.len && (t + kQBlock > s.lo || t < a.sinks)) {
-              b0 = min(b0, i);
-              b1 = i + 1;
-            }
-          }
-          if (b0 < b1) {
-            page = paged_page(a, g.b, first);
-            bad = page >= a.n_pages;
-          }
-        }
-        const uint32_t none = __ballot_sync(0xffffffffu, bad);
-        const bool copies = b0 < b1 && !bad;
-        const uint32_t bytes = copies ? (uint32_t)(b1 - b0) * BB : 0u;
-        uint32_t sum = bytes;
-#pragma unroll
-        for (int o = 1; o < kQdBlocks; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        sum = __shfl_sync(0xffffffffu, sum, 0);
-        const uint64_t src = reinterpret_cast<uint64_t>(p.cache) +
-                             (copies ? page * a.stride_page + g.h * a.stride_head + (int64_t)((first & a.page_mask) / kQBlock + b0) * BB : 0);
-        const uint32_t dst = sb + st * S::kStage + (uint32_t)(lane * bpr + b0) * BB;
-        if (it >= kQdStages) ok = mbar_wait(&empty[st], (uint32_t)((it / kQdStages - 1) & 1), a.err);
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        if (el) {
-          uint32_t m = 0;  // bad runs as a mask of blocks
-          for (int i = 0; i < kQdBlocks; ++i) m |= (none >> (i / bpr) & 1u) << i;
-          bad_blocks[st] = m;
-          mbar_arrive_expect_tx(&full[st], sum);
-        }
-        __syncwarp();
+      const int first = s.token(g.j0) + lane % runs * rows;
+      int b0 = bpr, b1 = 0;  // blocks with a visible token
 #pragma unroll 1
-        for (int i = 0; i < runs; ++i) {
-          const uint32_t n = __shfl_sync(0xffffffffu, bytes, i), to = __shfl_sync(0xffffffffu, dst, i);
-          const uint64_t from = __shfl_sync(0xffffffffu, src, i);
-          if (n && el)
-            asm volatile(
-                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(to),
-                "l"(from), "r"(n), "r"(smem_u32(&full[st])), "l"(policy)
-                : "memory");
+      for (int i = 0; i < bpr; ++i) {
+        const int t = first + i * kQBlock;
+        if (t < s.len && (t + kQBlock > s.lo || t < a.sinks)) {
+          b0 = min(b0, i);
+          b1 = i + 1;
         }
       }
-      x += g.j1 - g.j0;
+      if (b0 < b1) {
+        const int page = paged_page(a, g.b, first);
+        bad = page >= a.n_pages;
+        if (!bad) {
+          bytes = (uint32_t)(b1 - b0) * BB;
+          src = reinterpret_cast<uint64_t>(p.cache) + page * a.stride_page + g.h * a.stride_head +
+                (int64_t)((first & a.page_mask) / kQBlock + b0) * BB;
+        }
+      }
+      to = (uint32_t)(lane % runs * bpr + b0) * BB;
     }
-    // every copy has landed before the CTA may end (also after a wait that gave up)
-    for (int i = max(0, it - kQdStages); i < it; ++i) mbar_wait(&full[i % kQdStages], (uint32_t)((i / kQdStages) & 1), a.err);
-    return;
-  }
+    none = __ballot_sync(0xffffffffu, bad);
+  };
+  bool ok = true;
+  int next = x0 + warp, slot = batch, in = 0;  // the next tile to fetch, its place in the batch, its stage
+  auto fetch = [&]() {
+    if (next >= x1 || !ok) return;
+    if (slot == batch) {
+      look(next);
+      slot = 0;
+    }
+    const uint32_t st = stages + in * S::kStage;
+    uint32_t sum = __shfl_sync(0xffffffffu, bytes, slot * runs);
+    if (runs == 2) sum += __shfl_sync(0xffffffffu, bytes, slot * 2 + 1);
+    if (el) mbar_arrive_expect_tx(&full[in], sum);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (i >= runs) break;
+      const uint32_t n = __shfl_sync(0xffffffffu, bytes, slot * runs + i), at = st + __shfl_sync(0xffffffffu, to, slot * runs + i);
+      const uint64_t from = __shfl_sync(0xffffffffu, src, slot * runs + i);
+      if (n && el)
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(at),
+            "l"(from), "r"(n), "r"(smem_u32(&full[in])), "l"(policy)
+            : "memory");
+    }
+    if (none >> (slot * runs) & (runs == 2 ? 3u : 1u)) {  // pages of zeros: no scales, no biases
+      for (int k = 0; k < kQdBlocks; ++k)
+        if (none >> (slot * runs + k / bpr) & 1u)
+          for (int i = lane; i < D / 2; i += 32)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + k * BB + 16 * D + 4 * i), "r"(0u) : "memory");
+      fence_proxy_async();
+      __syncwarp();
+    }
+    next += kQdWarps;
+    ++slot;
+    if (++in == kQdDepth) in = 0;
+  };
+  for (int i = 0; i < kQdDepth; ++i) fetch();
 
-  // =========================== consumers
   constexpr uint32_t M0 = 0x000f000fu, M1 = 0x00f000f0u;
   const int t = lane & 3, gq = lane >> 2;
   // the tokens of this lane's rows gq and gq + 8 of a block: in this order a lane's words of V lie four tokens apart
   const int r0 = (gq >> 1) + 4 * (gq & 1), r1 = r0 + 8;
-  bool ok = true;
-  int it = 0;
+  int it = 0, out = 0;       // tiles of the CTA behind us; the stage of this warp's next one
+  uint32_t phase = 0;
   for (int x = x0; x < x1;) {
     const DealSeg g = deal_seg(prefix, a.B, a.Hkv, x, x1);
     const QSpan s = qd_span(a, g.b);
@@ -224,9 +240,9 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
         for (int gg = 0; gg < G; ++gg) qs[gg][e] = __shfl_sync(0xffffffffu, sum[gg], 8 * t + 4 * e) * a.scale_log2;
       }
     }
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float ref[2] = {-INFINITY, -INFINITY}, lim[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float o[G][4][4], ob[G][2];  // products with the codes; sums of p b
-    int E[G];                    // exponent over the scales seen (as of fp32 bits)
+    int E[G];                    // scales seen are below 2^(E - 127); 0: none
 #pragma unroll
     for (int gg = 0; gg < G; ++gg) {
       E[gg] = 0;
@@ -235,12 +251,18 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
       for (int i = 0; i < 4; ++i) o[gg][i][0] = o[gg][i][1] = o[gg][i][2] = o[gg][i][3] = 0.f;
     }
 
-    for (int j = g.j0; j < g.j1; ++j, ++it) {
-      if (it % kQdWarps != warp) continue;
-      const int st = it % kQdStages, tok0 = s.token(j);
-      if (ok) ok = mbar_wait(&full[st], (uint32_t)((it / kQdStages) & 1), a.err);
-      const uint32_t tb = sb + st * S::kStage, bad = bad_blocks[st];
+    // this warp's first tile of the unit: tile i of the CTA's run is warp i % kQdWarps's
+    for (int j = g.j0 + (warp - it % kQdWarps + kQdWarps) % kQdWarps; j < g.j1; j += kQdWarps) {
+      const int tok0 = s.token(j);
+      if (ok && !__all_sync(0xffffffffu, mbar_wait(&full[out], phase, a.err))) {
+        ok = false;  // nothing more is fetched, and what is on its way has landed before the CTA may end
+        for (int i = 0; i < kQdDepth; ++i)
+          if (x + j - g.j0 + i * kQdWarps < next)
+            mbar_wait(&full[(out + i) % kQdDepth], phase ^ (out + i >= kQdDepth ? 1u : 0u), a.err);
+      }
+      const uint32_t tb = stages + out * S::kStage;
       const bool edge = !((tok0 >= s.lo && tok0 + kQdTile <= s.len) || tok0 + kQdTile <= min(a.sinks, s.len));
+      auto seen = [&](int y) { return y < s.len && (y >= s.lo || y < a.sinks); };
       // ---- scores
       float sc[kQdBlocks][4];
 #pragma unroll
@@ -257,98 +279,82 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
             mma16816(ac[gg], u0 & M1, u1 & M1, v0 & M1, v1 & M1, qb[gg][w][1][0], qb[gg][w][1][1]);
           }
         }
-        uint32_t sb0[G], sb1[G];  // scale and bias of the rows' tokens
-#pragma unroll
-        for (int gg = 0; gg < G; ++gg) {
-          sb0[gg] = lds32(kb + qparam_off(D, 0, gg, 0) + r0 * 4 * G);
-          sb1[gg] = lds32(kb + qparam_off(D, 0, gg, 0) + r1 * 4 * G);
-          if (bad >> k & 1u) sb0[gg] = sb1[gg] = 0u;  // a page of zeros
-        }
+        uint32_t sbk[2][G];  // scale and bias of the rows' tokens
+        lds_params<G>(kb + qparam_off(D, 0, 0, 0) + r0 * 4 * G, sbk[0]);
+        lds_params<G>(kb + qparam_off(D, 0, 0, 0) + r1 * 4 * G, sbk[1]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float y = 0.f, z = 0.f;
 #pragma unroll
           for (int gg = 0; gg < G; ++gg) {
-            const uint32_t sbx = e < 2 ? sb0[gg] : sb1[gg];
-            y = fmaf(half_lo(sbx), ac[gg][e], y);
-            z = fmaf(half_hi(sbx), qs[gg][e & 1], z);
+            y = fmaf(half_lo(sbk[e >> 1][gg]), ac[gg][e], y);
+            z = fmaf(half_hi(sbk[e >> 1][gg]), qs[gg][e & 1], z);
           }
           sc[k][e] = fmaf(y, kf[e & 1], z);
         }
-        if (edge) {
-          auto seen = [&](int y) { return y < s.len && (y >= s.lo || y < a.sinks); };
+      }
+      if (edge) {
+#pragma unroll
+        for (int k = 0; k < kQdBlocks; ++k) {
           const int at = tok0 + k * kQBlock;
           if (!seen(at + r0)) sc[k][0] = sc[k][1] = -INFINITY;
           if (!seen(at + r1)) sc[k][2] = sc[k][3] = -INFINITY;
         }
+        // nothing of V where a weight is 0: its scale and bias may be anything
+        if (!seen(tok0 + lane))
+#pragma unroll
+          for (int gg = 0; gg < G; ++gg)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(tb + lane / kQBlock * BB + qparam_off(D, 1, gg, lane % kQBlock)), "r"(0u) : "memory");
+        fence_proxy_async();
+        __syncwarp();
       }
-      // ---- online softmax over the tile's tokens (columns 2t, 2t + 1)
-      float al[2], ms[2];
+      // ---- references (columns 2t, 2t + 1) and the scales' power of two
+      float top[2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float y = fmaxf(sc[0][e], sc[0][e + 2]);
-#pragma unroll
-        for (int k = 1; k < kQdBlocks; ++k) y = fmaxf(y, fmaxf(sc[k][e], sc[k][e + 2]));
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
-        const float n = fmaxf(m[e], y);
-        ms[e] = n == -INFINITY ? 0.f : n;
-        al[e] = fast_exp2(m[e] - ms[e]);
-        m[e] = n;
-        l[e] *= al[e];
-      }
-      // ---- scales of V
-      uint32_t sv[kQdBlocks][2][G];
-      uint32_t most[G];
-#pragma unroll
-      for (int gg = 0; gg < G; ++gg) most[gg] = 0;
-#pragma unroll
-      for (int k = 0; k < kQdBlocks; ++k)
-#pragma unroll
-        for (int gg = 0; gg < G; ++gg)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t y = lds32(tb + k * BB + qparam_off(D, 1, gg, 0) + (e ? r1 : r0) * 4 * G);
-            // nothing of a token that is not seen (its weight is 0, its scale may be anything), zeros of a bad page
-            if (bad >> k & 1u) y = 0u;
-            if (edge) {
-              const int at = tok0 + k * kQBlock + (e ? r1 : r0);
-              if (!(at < s.len && (at >= s.lo || at < a.sinks))) y = 0u;
-            }
-            sv[k][e][gg] = y;
-            most[gg] = max(most[gg], y & 0x7fffu);
-          }
-      float inv[G];
-      bool grown = al[0] != 1.f || al[1] != 1.f;
-      float fo[G][2];
+      for (int e = 0; e < 2; ++e) top[e] = fmaxf(fmaxf(sc[0][e], sc[0][e + 2]), fmaxf(sc[1][e], sc[1][e + 2]));
+      uint32_t big[G], sbv[G];
+      lds_params<G>(tb + lane / kQBlock * BB + qparam_off(D, 1, 0, lane % kQBlock), sbv);
+      bool grown = top[0] > lim[0] || top[1] > lim[1];
 #pragma unroll
       for (int gg = 0; gg < G; ++gg) {
-        const uint32_t top = __reduce_max_sync(0xffffffffu, most[gg]);
-        const int ex = (int)(__float_as_uint(half_lo(top)) >> 23) + 1;  // scales < 2^(ex - 127)
-        float f = 1.f;
-        if (ex > E[gg]) {
-          f = E[gg] == 0 ? 0.f : __uint_as_float((uint32_t)max(127 + E[gg] - ex, 0) << 23);
-          E[gg] = ex;
-          grown = true;
-        }
-        inv[gg] = __uint_as_float((uint32_t)(254 - E[gg]) << 23);  // 2^(127 - E)
-        fo[gg][0] = al[0] * f;
-        fo[gg][1] = al[1] * f;
+        big[gg] = __reduce_max_sync(0xffffffffu, sbv[gg] & 0x7fffu);
+        grown |= (int)(__float_as_uint(half_lo(big[gg])) >> 23) >= E[gg];
       }
       if (__any_sync(0xffffffffu, grown)) {
+        float al[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float y = top[e];
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
+          al[e] = 1.f;
+          if (y > lim[e]) {
+            al[e] = fast_exp2(ref[e] - (y - kQdShift));
+            ref[e] = y - kQdShift;
+            lim[e] = ref[e] + (fabsf(y) < kQdLarge ? kQdShift + kQdSlack : kQdShift);
+          }
+          l[e] *= al[e];
+        }
 #pragma unroll
         for (int gg = 0; gg < G; ++gg) {
+          const int ex = (int)(__float_as_uint(half_lo(big[gg])) >> 23) + 1;  // scales < 2^(ex - 127)
+          float f = 1.f;
+          if (ex > E[gg]) {
+            f = __uint_as_float((uint32_t)max(127 + E[gg] - ex, 0) << 23);
+            E[gg] = ex;
+          }
           ob[gg][0] *= al[0];
           ob[gg][1] *= al[1];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            o[gg][i][0] *= fo[gg][0];
-            o[gg][i][1] *= fo[gg][1];
-            o[gg][i][2] *= fo[gg][0];
-            o[gg][i][3] *= fo[gg][1];
+            o[gg][i][0] *= al[0] * f;
+            o[gg][i][1] *= al[1] * f;
+            o[gg][i][2] *= al[0] * f;
+            o[gg][i][3] *= al[1] * f;
           }
         }
       }
+      const float off[2] = {ref[0] == -INFINITY ? 0.f : ref[0], ref[1] == -INFINITY ? 0.f : ref[1]};
       // ---- weights and the product with V's codes
 #pragma unroll
       for (int k = 0; k < kQdBlocks; ++k) {
@@ -356,16 +362,19 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
         float pr[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          // (the shift behind the difference: in front of it a large maximum would round it away)
-          pr[e] = fast_exp2((sc[k][e] - ms[e & 1]) + kQdShift);
+          pr[e] = fast_exp2(sc[k][e] - off[e & 1]);
           l[e & 1] += pr[e];
         }
+        uint32_t sv[2][G];
+        lds_params<G>(vb + qparam_off(D, 1, 0, 0) + r0 * 4 * G, sv[0]);
+        lds_params<G>(vb + qparam_off(D, 1, 0, 0) + r1 * 4 * G, sv[1]);
 #pragma unroll
         for (int gg = 0; gg < G; ++gg) {
-          const float s0 = half_lo(sv[k][0][gg]) * inv[gg], s1 = half_lo(sv[k][1][gg]) * inv[gg];
-          const float b0 = half_hi(sv[k][0][gg]), b1 = half_hi(sv[k][1][gg]);
-          ob[gg][0] += fmaf(pr[0], b0, pr[2] * b1);
-          ob[gg][1] += fmaf(pr[1], b0, pr[3] * b1);
+          const float inv = __uint_as_float((uint32_t)(254 - E[gg]) << 23);  // 2^(127 - E)
+          const float s0 = half_lo(sv[0][gg]) * inv, s1 = half_lo(sv[1][gg]) * inv;
+          const float b0 = half_hi(sv[0][gg]), b1 = half_hi(sv[1][gg]);
+          ob[gg][0] = fmaf(pr[0], b0, fmaf(pr[2], b1, ob[gg][0]));
+          ob[gg][1] = fmaf(pr[1], b0, fmaf(pr[3], b1, ob[gg][1]));
           uint32_t h0, h1, e0, e1;
           split_half2(pr[0] * s0, pr[1] * s0, h0, e0);
           split_half2(pr[2] * s1, pr[3] * s1, h1, e1);
@@ -388,8 +397,13 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
+      fetch();  // into the stage just read
+      if (++out == kQdDepth) {
+        out = 0;
+        phase ^= 1u;
+      }
     }
+    it += g.j1 - g.j0;
     x += g.j1 - g.j0;
 
     // ---- merge the warps
@@ -402,7 +416,7 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
         for (int gg = 0; gg < G; ++gg) ob[gg][e] += __shfl_xor_sync(0xffffffffu, ob[gg][e], off);
       }
     if (lane < 4) {
-      *reinterpret_cast<float2*>(stats + warp * 16 + 2 * t) = make_float2(m[0], m[1]);
+      *reinterpret_cast<float2*>(stats + warp * 16 + 2 * t) = make_float2(ref[0], ref[1]);
       *reinterpret_cast<float2*>(stats + warp * 16 + 8 + 2 * t) = make_float2(l[0], l[1]);
     }
     // o[gg][i]: channels 64 gg + 8 gq + i and + 4, stored as [gg][i, i + 4][gq][8 heads]
@@ -445,7 +459,7 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
           rec[gg] = M;
           rec[8 + gg] = L;
         } else if (gg < a.G && p.lse) {
-          p.lse[head] = (M - kQdShift + log2f(L)) * 0.6931471805599453f;
+          p.lse[head] = (M + log2f(L)) * 0.6931471805599453f;
         }
       }
     }
@@ -506,7 +520,7 @@ __global__ void __launch_bounds__(kQdCombThreads) qpaged_combine_kernel(QdArgs p
     const float L = red[8 + gg], inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
     const size_t head = (size_t)g.b * a.Hq + g.h * a.G + gg;
     static_cast<T*>(p.out)[head * D + dd] = Num<T>::from_float(v * inv);
-    if (p.lse && dd == 0) p.lse[head] = (red[gg] - kQdShift + log2f(L)) * 0.6931471805599453f;
+    if (p.lse && dd == 0) p.lse[head] = (red[gg] + log2f(L)) * 0.6931471805599453f;
   }
 }
 
