@@ -109,6 +109,11 @@ __device__ inline float2 fma2(float2 x, float2 y, float2 z) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(f2_bits(x)), "l"(f2_bits(y)), "l"(f2_bits(z)));
   return *reinterpret_cast<float2*>(&r);
 }
+__device__ inline float2 mul2(float2 x, float2 y) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(x)), "l"(f2_bits(y)));
+  return *reinterpret_cast<float2*>(&r);
+}
 __device__ inline float2 add2(float2 x, float2 y) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(x)), "l"(f2_bits(y)));

@@ -18,6 +18,7 @@
 // looks up the pages of its next tiles, a lane for each, and fetches a tile with one bulk copy per page as soon as a
 // stage is free, so that no warp waits for another before a unit's end.  There the warps are merged; units that lie
 // in several CTAs' runs leave records that a second grid joins in run order.
+#include "paged_tc.cuh"
 #include "qpaged.cuh"
 
 namespace dkv {
@@ -78,6 +79,12 @@ __device__ inline void lds_params(uint32_t at, uint32_t (&x)[G]) {
   } else {
     x[0] = lds32(at);
   }
+}
+// a product that begins a sum
+__device__ inline void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+               : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ inline float half_lo(uint32_t x) { return __low2float(*reinterpret_cast<__half2*>(&x)); }
 __device__ inline float half_hi(uint32_t x) { return __high2float(*reinterpret_cast<__half2*>(&x)); }
@@ -188,7 +195,7 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
   };
   for (int i = 0; i < kQdDepth; ++i) fetch();
 
-  constexpr uint32_t M0 = 0x000f000fu, M1 = 0x00f000f0u;
+  constexpr uint32_t M0 = 0x000f000fu, M1 = 0x00f000f0u, kOnes = 0x3c003c00u;
   const int t = lane & 3, gq = lane >> 2;
   // the tokens of this lane's rows gq and gq + 8 of a block: in this order a lane's words of V lie four tokens apart
   const int r0 = (gq >> 1) + 4 * (gq & 1), r1 = r0 + 8;
@@ -199,24 +206,21 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
     const QSpan s = qd_span(a, g.b);
     // q as B fragments: lane (gq, t) holds channels 16 t .. 16 t + 15 of each group of head gq
     uint32_t qb[G][2][2][2];      // [group][word][even, odd nibbles][b0, b1]
-    float kf[2], qs[G][2];        // per head 2t, 2t + 1: factor of the products, sums of q times scale
+    uint32_t qz;                  // the groups' sums of q, for the biases: t = 0 the fp16 value, t = 1 what it leaves
+    float2 kf;                    // factor of the products, heads 2t and 2t + 1
     {
       const bool live = gq < a.G;
       const T* row = static_cast<const T*>(p.q) + g.b * p.q_batch + (int64_t)(g.h * a.G + (live ? gq : 0)) * p.q_head + 16 * t;
-      float f[G][16], top = 0.f, sum[G];
+      float f[G][16], top = 0.f, sum[2] = {0.f, 0.f};
 #pragma unroll
       for (int gg = 0; gg < G; ++gg) {
-        sum[gg] = 0.f;
         const uint4 v[2] = {__ldg(reinterpret_cast<const uint4*>(row + 64 * gg)), __ldg(reinterpret_cast<const uint4*>(row + 64 * gg + 8))};
         const T* h = reinterpret_cast<const T*>(v);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           f[gg][e] = live ? Num<T>::to_float(h[e]) : 0.f;
           top = fmaxf(top, fabsf(f[gg][e]));
-          sum[gg] += f[gg][e];
         }
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) sum[gg] += __shfl_xor_sync(0xffffffffu, sum[gg], o);
       }
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -224,29 +228,39 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
       const float up = __uint_as_float((uint32_t)(268 - ex) << 23);  // 2^(141 - ex): top up < 2^15
       const float down = __uint_as_float((uint32_t)(ex - 14) << 23) * 0x1p24f * a.scale_log2;  // 2^(ex - 141), the codes' 2^24
 #pragma unroll
-      for (int gg = 0; gg < G; ++gg)
+      for (int gg = 0; gg < G; ++gg) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          f[gg][e] *= up;
+          sum[gg] += f[gg][e];
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) sum[gg] += __shfl_xor_sync(0xffffffffu, sum[gg], o);
+        sum[gg] *= 0x1p-10f;  // (codes carry 2^-24: the other 2^-14 follow the product, so that both parts are normal)
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const float* y = f[gg] + 8 * w;
-          qb[gg][w][0][0] = pack_half2(y[0] * up, y[4] * up);
-          qb[gg][w][0][1] = pack_half2(y[2] * up, y[6] * up);
-          qb[gg][w][1][0] = pack_half2(y[1] * up * 0.0625f, y[5] * up * 0.0625f);
-          qb[gg][w][1][1] = pack_half2(y[3] * up * 0.0625f, y[7] * up * 0.0625f);
+          qb[gg][w][0][0] = pack_half2(y[0], y[4]);
+          qb[gg][w][0][1] = pack_half2(y[2], y[6]);
+          qb[gg][w][1][0] = pack_half2(y[1] * 0.0625f, y[5] * 0.0625f);
+          qb[gg][w][1][1] = pack_half2(y[3] * 0.0625f, y[7] * 0.0625f);
         }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        kf[e] = __shfl_sync(0xffffffffu, down, 8 * t + 4 * e);
-#pragma unroll
-        for (int gg = 0; gg < G; ++gg) qs[gg][e] = __shfl_sync(0xffffffffu, sum[gg], 8 * t + 4 * e) * a.scale_log2;
       }
+      uint32_t hi, lo;
+      split_half2(sum[0], sum[1], hi, lo);
+      qz = t == 0 ? hi : t == 1 ? lo : 0u;
+      kf = make_float2(__shfl_sync(0xffffffffu, down, 8 * t), __shfl_sync(0xffffffffu, down, 8 * t + 4));
     }
-    float ref[2] = {-INFINITY, -INFINITY}, lim[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float o[G][4][4], ob[G][2];  // products with the codes; sums of p b
+    float ref[2] = {-INFINITY, -INFINITY}, lim[2] = {-INFINITY, -INFINITY};
+    float2 l = make_float2(0.f, 0.f);
+    float o[G][4][4], ow[G][4];  // products with the codes; sums of the rounded weights (the same in all rows)
+    float ob[G][2];              // sums of p (b + 8 s)
     int E[G];                    // scales seen are below 2^(E - 127); 0: none
 #pragma unroll
     for (int gg = 0; gg < G; ++gg) {
       E[gg] = 0;
       ob[gg][0] = ob[gg][1] = 0.f;
+      ow[gg][0] = ow[gg][1] = ow[gg][2] = ow[gg][3] = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[gg][i][0] = o[gg][i][1] = o[gg][i][2] = o[gg][i][3] = 0.f;
     }
@@ -264,41 +278,44 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
       const bool edge = !((tok0 >= s.lo && tok0 + kQdTile <= s.len) || tok0 + kQdTile <= min(a.sinks, s.len));
       auto seen = [&](int y) { return y < s.len && (y >= s.lo || y < a.sinks); };
       // ---- scores
-      float sc[kQdBlocks][4];
+      float2 sc[kQdBlocks][2];
 #pragma unroll
       for (int k = 0; k < kQdBlocks; ++k) {
         const uint32_t kb = tb + k * BB;
-        float ac[G][4] = {};
+        uint32_t sbk[2][G];  // scale and bias of the rows' tokens
+        lds_params<G>(kb + qparam_off(D, 0, 0, 0) + r0 * 4 * G, sbk[0]);
+        lds_params<G>(kb + qparam_off(D, 0, 0, 0) + r1 * 4 * G, sbk[1]);
+        float ac[G][4], z[4];
 #pragma unroll
         for (int gg = 0; gg < G; ++gg) {
           const uint2 y0 = lds64(kb + qcode_off(D, 0, gg, 0) + r0 * 32 + 8 * t), y1 = lds64(kb + qcode_off(D, 0, gg, 0) + r1 * 32 + 8 * t);
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             const uint32_t u0 = w ? y0.y : y0.x, u1 = w ? y1.y : y1.x, v0 = u0 >> 8, v1 = u1 >> 8;
-            mma16816(ac[gg], u0 & M0, u1 & M0, v0 & M0, v1 & M0, qb[gg][w][0][0], qb[gg][w][0][1]);
+            if (w == 0) mma16816_first(ac[gg], u0 & M0, u1 & M0, v0 & M0, v1 & M0, qb[gg][w][0][0], qb[gg][w][0][1]);
+            else mma16816(ac[gg], u0 & M0, u1 & M0, v0 & M0, v1 & M0, qb[gg][w][0][0], qb[gg][w][0][1]);
             mma16816(ac[gg], u0 & M1, u1 & M1, v0 & M1, v1 & M1, qb[gg][w][1][0], qb[gg][w][1][1]);
           }
         }
-        uint32_t sbk[2][G];  // scale and bias of the rows' tokens
-        lds_params<G>(kb + qparam_off(D, 0, 0, 0) + r0 * 4 * G, sbk[0]);
-        lds_params<G>(kb + qparam_off(D, 0, 0, 0) + r1 * 4 * G, sbk[1]);
+        // biases (of both groups) times sums of q
+        mma16816_first(z, __byte_perm(sbk[0][0], sbk[0][G - 1], 0x7632), __byte_perm(sbk[1][0], sbk[1][G - 1], 0x7632), 0u, 0u, qz, 0u);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float y = 0.f, z = 0.f;
+        for (int e = 0; e < 2; ++e) {
+          float2 y = mul2(make_float2(z[2 * e], z[2 * e + 1]), make_float2(0x1p-14f, 0x1p-14f));
 #pragma unroll
           for (int gg = 0; gg < G; ++gg) {
-            y = fmaf(half_lo(sbk[e >> 1][gg]), ac[gg][e], y);
-            z = fmaf(half_hi(sbk[e >> 1][gg]), qs[gg][e & 1], z);
+            const float f = half_lo(sbk[e][gg]);
+            y = make_float2(fmaf(f, ac[gg][2 * e], y.x), fmaf(f, ac[gg][2 * e + 1], y.y));
           }
-          sc[k][e] = fmaf(y, kf[e & 1], z);
+          sc[k][e] = mul2(y, kf);
         }
       }
       if (edge) {
 #pragma unroll
         for (int k = 0; k < kQdBlocks; ++k) {
           const int at = tok0 + k * kQBlock;
-          if (!seen(at + r0)) sc[k][0] = sc[k][1] = -INFINITY;
-          if (!seen(at + r1)) sc[k][2] = sc[k][3] = -INFINITY;
+          if (!seen(at + r0)) sc[k][0] = make_float2(-INFINITY, -INFINITY);
+          if (!seen(at + r1)) sc[k][1] = make_float2(-INFINITY, -INFINITY);
         }
         // nothing of V where a weight is 0: its scale and bias may be anything
         if (!seen(tok0 + lane))
@@ -309,9 +326,8 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
         __syncwarp();
       }
       // ---- references (columns 2t, 2t + 1) and the scales' power of two
-      float top[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) top[e] = fmaxf(fmaxf(sc[0][e], sc[0][e + 2]), fmaxf(sc[1][e], sc[1][e + 2]));
+      const float top[2] = {fmaxf(fmaxf(sc[0][0].x, sc[0][1].x), fmaxf(sc[1][0].x, sc[1][1].x)),
+                            fmaxf(fmaxf(sc[0][0].y, sc[0][1].y), fmaxf(sc[1][0].y, sc[1][1].y))};
       uint32_t big[G], sbv[G];
       lds_params<G>(tb + lane / kQBlock * BB + qparam_off(D, 1, 0, lane % kQBlock), sbv);
       bool grown = top[0] > lim[0] || top[1] > lim[1];
@@ -333,8 +349,8 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
             ref[e] = y - kQdShift;
             lim[e] = ref[e] + (fabsf(y) < kQdLarge ? kQdShift + kQdSlack : kQdShift);
           }
-          l[e] *= al[e];
         }
+        l = mul2(l, make_float2(al[0], al[1]));
 #pragma unroll
         for (int gg = 0; gg < G; ++gg) {
           const int ex = (int)(__float_as_uint(half_lo(big[gg])) >> 23) + 1;  // scales < 2^(ex - 127)
@@ -345,6 +361,8 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
           }
           ob[gg][0] *= al[0];
           ob[gg][1] *= al[1];
+          ow[gg][0] *= al[0] * f;
+          ow[gg][1] *= al[1] * f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             o[gg][i][0] *= al[0] * f;
@@ -354,16 +372,17 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
           }
         }
       }
-      const float off[2] = {ref[0] == -INFINITY ? 0.f : ref[0], ref[1] == -INFINITY ? 0.f : ref[1]};
+      const float2 off = make_float2(ref[0] == -INFINITY ? 0.f : -ref[0], ref[1] == -INFINITY ? 0.f : -ref[1]);
       // ---- weights and the product with V's codes
 #pragma unroll
       for (int k = 0; k < kQdBlocks; ++k) {
         const uint32_t vb = tb + k * BB;
-        float pr[4];
+        float2 pr[2];  // rows gq and gq + 8
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          pr[e] = fast_exp2(sc[k][e] - off[e & 1]);
-          l[e & 1] += pr[e];
+        for (int e = 0; e < 2; ++e) {
+          const float2 x = add2(sc[k][e], off);
+          pr[e] = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+          l = add2(l, pr[e]);
         }
         uint32_t sv[2][G];
         lds_params<G>(vb + qparam_off(D, 1, 0, 0) + r0 * 4 * G, sv[0]);
@@ -371,14 +390,15 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
 #pragma unroll
         for (int gg = 0; gg < G; ++gg) {
           const float inv = __uint_as_float((uint32_t)(254 - E[gg]) << 23);  // 2^(127 - E)
-          const float s0 = half_lo(sv[0][gg]) * inv, s1 = half_lo(sv[1][gg]) * inv;
-          const float b0 = half_hi(sv[0][gg]), b1 = half_hi(sv[1][gg]);
-          ob[gg][0] = fmaf(pr[0], b0, fmaf(pr[2], b1, ob[gg][0]));
-          ob[gg][1] = fmaf(pr[1], b0, fmaf(pr[3], b1, ob[gg][1]));
-          uint32_t h0, h1, e0, e1;
-          split_half2(pr[0] * s0, pr[1] * s0, h0, e0);
-          split_half2(pr[2] * s1, pr[3] * s1, h1, e1);
-          const uint32_t bh0 = movtrans(h0), bh1 = movtrans(h1), bl0 = movtrans(e0), bl1 = movtrans(e1);
+          uint32_t bw[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float sc1 = half_lo(sv[e][gg]), mid = fmaf(8.f, sc1, half_hi(sv[e][gg])), s1 = sc1 * inv;
+            ob[gg][0] = fmaf(pr[e].x, mid, ob[gg][0]);
+            ob[gg][1] = fmaf(pr[e].y, mid, ob[gg][1]);
+            bw[e] = movtrans(pack_half2(pr[e].x * s1, pr[e].y * s1));
+          }
+          mma16816(ow[gg], kOnes, kOnes, kOnes, kOnes, bw[0], bw[1]);
           uint32_t y[4], z[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) y[i] = lds32(vb + qcode_off(D, 1, gg, 0) + (4 * i + t) * 32 + 4 * gq);
@@ -391,8 +411,7 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
             uint32_t f[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) f[e] = (i < 2 ? z[e] : z[e] >> 8) & (i & 1 ? M1 : M0);
-            mma16816(o[gg][i], f[0], f[1], f[2], f[3], bh0, bh1);
-            mma16816(o[gg][i], f[0], f[1], f[2], f[3], bl0, bl1);
+            mma16816(o[gg][i], f[0], f[1], f[2], f[3], bw[0], bw[1]);
           }
         }
       }
@@ -408,26 +427,28 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
 
     // ---- merge the warps
 #pragma unroll
-    for (int off = 4; off < 32; off <<= 1)
+    for (int off = 4; off < 32; off <<= 1) {
+      l.x += __shfl_xor_sync(0xffffffffu, l.x, off);
+      l.y += __shfl_xor_sync(0xffffffffu, l.y, off);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        l[e] += __shfl_xor_sync(0xffffffffu, l[e], off);
+      for (int gg = 0; gg < G; ++gg)
 #pragma unroll
-        for (int gg = 0; gg < G; ++gg) ob[gg][e] += __shfl_xor_sync(0xffffffffu, ob[gg][e], off);
-      }
+        for (int e = 0; e < 2; ++e) ob[gg][e] += __shfl_xor_sync(0xffffffffu, ob[gg][e], off);
+    }
     if (lane < 4) {
       *reinterpret_cast<float2*>(stats + warp * 16 + 2 * t) = make_float2(ref[0], ref[1]);
-      *reinterpret_cast<float2*>(stats + warp * 16 + 8 + 2 * t) = make_float2(l[0], l[1]);
+      *reinterpret_cast<float2*>(stats + warp * 16 + 8 + 2 * t) = l;
     }
     // o[gg][i]: channels 64 gg + 8 gq + i and + 4, stored as [gg][i, i + 4][gq][8 heads]
 #pragma unroll
     for (int gg = 0; gg < G; ++gg)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float f = E[gg] == 0 ? 0.f : __uint_as_float((uint32_t)E[gg] << 23) * (i & 1 ? 0x1p20f : 0x1p24f);
-        float* ow = merge + warp * D * 8 + ((gg * 8 + i) * 8 + gq) * 8 + 2 * t;
-        *reinterpret_cast<float2*>(ow) = make_float2(fmaf(o[gg][i][0], f, ob[gg][0]), fmaf(o[gg][i][1], f, ob[gg][1]));
-        *reinterpret_cast<float2*>(ow + 4 * 64) = make_float2(fmaf(o[gg][i][2], f, ob[gg][0]), fmaf(o[gg][i][3], f, ob[gg][1]));
+        const float F = E[gg] == 0 ? 0.f : __uint_as_float((uint32_t)E[gg] << 23), f = F * (i & 1 ? 0x1p20f : 0x1p24f);
+        const float m0 = fmaf(-8.f * F, ow[gg][0], ob[gg][0]), m1 = fmaf(-8.f * F, ow[gg][1], ob[gg][1]);
+        float* at = merge + warp * D * 8 + ((gg * 8 + i) * 8 + gq) * 8 + 2 * t;
+        *reinterpret_cast<float2*>(at) = make_float2(fmaf(o[gg][i][0], f, m0), fmaf(o[gg][i][1], f, m1));
+        *reinterpret_cast<float2*>(at + 4 * 64) = make_float2(fmaf(o[gg][i][2], f, m0), fmaf(o[gg][i][3], f, m1));
       }
     named_bar_sync(1, 32 * kQdWarps);
     {

@@ -124,12 +124,6 @@ __device__ inline unsigned long long qp_sees(const PagedArgs& a, int pos, int k0
   return below(hi + 1) & (~below(lo) | below(sk));
 }
 
-__device__ inline float2 mul2(float2 x, float2 y) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(x)), "l"(f2_bits(y)));
-  return *reinterpret_cast<float2*>(&r);
-}
-
 // Eight codes as values, in the order 0 4 1 5 2 6 3 7.  1024 + code and 1024 + 16 code are the halves whose low
 // bits are the code's; every step is exact.
 __device__ inline uint4 values8(uint32_t x, __half2 s, __half2 b) {

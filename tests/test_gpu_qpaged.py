@@ -157,11 +157,13 @@ def check_decode(c, q, out, lse, lens, hq, window, sinks):
     for b in range(c.B):
         for j in range(hq):
             ref, parts, pv = Q.attend(q[b, j:j + 1].double(), c, b, j * c.hkv // hq, torch.tensor([lens[b] - 1]), window, sinks)
-            # The products of the codes and of the biases are added up apart, as are the weights' with codes and biases.
-            # The lower half of a weight times scale (at most 2^14, the row's largest weight at 2^14) is an fp16 number: in
-            # the subnormals off by half of 2^-24, which is 2^-39 of the largest, on codes up to 15.
-            pv = pv + 2.0 ** (21 - 39) * 15 * c.q[b][1][1][j * c.hkv // hq].sum(0).repeat_interleave(64)
-            R.check_rows(out[b, j:j + 1], lse[b, j:j + 1], (ref[0], ref[1], ref[2], pv, max(ref[4], parts)), c.d, c.dt, 2.0 ** -21,
+            # The products of the codes and of the biases are added up apart, in the scores and with the weights.  A weight
+            # times scale over the power of two is one fp16 number (2^-11 relative; the row's largest weight is 2^7 or more,
+            # so in the subnormals half of 2^-24 is 2^-32 of it), on codes less 8; the weights' sum and the biases are fp32.
+            s, h = c.q[b][1][1], j * c.hkv // hq
+            seen = R.seen(torch.tensor([lens[b] - 1]), lens[b], window, sinks).double()
+            pv = pv + 2.0 ** (11 - 32) * 16 * (seen @ torch.ones_like(s[h]) * (s[h] * seen[0][:, None]).amax(0) if lens[b] else s[h].sum(0)[None]).repeat_interleave(64, -1)
+            R.check_rows(out[b, j:j + 1], lse[b, j:j + 1], (ref[0], ref[1], ref[2], pv, max(ref[4], parts)), c.d, c.dt, 2.0 ** -11,
                          f"sequence {b} head {j}")
 
 
