@@ -13,11 +13,13 @@
 // q is brought to at most 2^15 by a power of two (bf16 queries become fp16 without loss above 2^-24 of the largest),
 // w = p s 2^-E with a running power of two E over the scales seen, as the sum of two fp16 values (22 bits).
 //
-// The visible tokens of a sequence are cut into 32-token tiles, dealt out evenly to the CTAs as in the 16-bit
-// decode; a CTA's warps take its tiles in turn, each with stages, copies and an online softmax of its own: a warp
-// looks up the pages of its next tiles, a lane for each, and fetches a tile with one bulk copy per page as soon as a
-// stage is free, so that no warp waits for another before a unit's end.  There the warps are merged; units that lie
-// in several CTAs' runs leave records that a second grid joins in run order.
+// The visible tokens of a sequence are cut into 32-token tiles; the tiles of all (sequence, KV head) units in a row
+// are dealt out evenly, to CTAs and in them to warps.  A warp walks its run of tiles unit by unit with stages, copies
+// and an online softmax of its own: it looks up the pages of its next tiles, a lane for each, and fetches a tile with
+// one bulk copy per page as soon as a stage is free.  A unit that lies wholly in one warp's run is finished there;
+// what lies in several is left in shared memory (a warp's last unit in its own stages, which are free by then, its
+// first one beside them) and merged once, at the CTA's end; units that lie in several CTAs' runs leave a record for
+// each, and the CTA that is last to leave one merges them in run order, so that equal calls give equal bits.
 #include "paged_tc.cuh"
 #include "qpaged.cuh"
 
@@ -27,7 +29,7 @@ namespace {
 constexpr int kQdTile = 32, kQdBlocks = kQdTile / kQBlock;
 constexpr int kQdWarps = 16, kQdDepth = 2;  // warps, and stages of each
 constexpr int kQdThreads = 32 * kQdWarps;
-constexpr int kQdCombThreads = 512, kQdCombCols = 32;
+constexpr int kQdLeast = 4;  // tiles of a CTA, as long as there are enough for all
 // Weights are 2^(score - ref).  A head's reference lies kQdShift below a maximum and moves only when a score exceeds
 // that by kQdSlack (at once where scores are so large that their rounding shows): weights are at most 2^15, and those
 // down to e^-18 of the largest keep 11 bits in the lower of the two fp16 values too.
@@ -63,11 +65,16 @@ struct QdArgs {
 template <int D>
 struct QdSmem {
   static constexpr uint32_t kStage = kQdBlocks * qblock_bytes(D);
-  static constexpr uint32_t kOffMerge = kQdWarps * kQdDepth * kStage;        // o [warp][D][8]
-  static constexpr uint32_t kOffStats = kOffMerge + kQdWarps * D * 32;       // ref, l [warp][2][8]
-  static constexpr uint32_t kOffBar = kOffStats + kQdWarps * 64;             // [warp][stage]
-  static constexpr uint32_t kOffPrefix = kOffBar + kQdWarps * kQdDepth * 8;  // [B + 1]
+  static constexpr uint32_t kOffFirst = kQdWarps * kQdDepth * kStage;        // o [warp][D][8] of first units
+  static constexpr uint32_t kOffStats = kOffFirst + kQdWarps * D * 32;       // [warp][first, last](ref [8], l [8])
+  static constexpr uint32_t kOffBar = kOffStats + kQdWarps * 128;            // [warp][stage]
+  static constexpr uint32_t kOffUnit = kOffBar + kQdWarps * kQdDepth * 8;    // [warp] its last unit; the CTA's first one
+  static constexpr uint32_t kOffPrefix = kOffUnit + (kQdWarps + 1) * 16;     // [B + 1]
+  static_assert(kQdDepth * kStage >= D * 32, "a warp's last unit fits its stages");
 };
+// Counters of the CTAs that have left a record of a unit: a byte for each CTA in which such a unit can begin, behind
+// the header's two words.  They are zero between calls (the last CTA takes its unit's away).
+constexpr int kQdMostCtas = (int)(kWsHeader - 8);
 
 // the (scale, bias) pairs of a token
 template <int G>
@@ -91,16 +98,20 @@ __device__ inline float half_hi(uint32_t x) { return __high2float(*reinterpret_c
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) {
-  extern __shared__ __align__(1024) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   using S = QdSmem<D>;
   const PagedArgs& a = p.a;
   constexpr int G = D / 64, BB = qblock_bytes(D);
-  float* merge = reinterpret_cast<float*>(smem + S::kOffMerge);
+  float* firsts = reinterpret_cast<float*>(smem + S::kOffFirst);
   float* stats = reinterpret_cast<float*>(smem + S::kOffStats);
+  int4* units = reinterpret_cast<int4*>(smem + S::kOffUnit);  // first tile, tiles, sequence, head
   int* prefix = reinterpret_cast<int*>(smem + S::kOffPrefix);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
+  // (a run of few tiles goes to every fourth of these: to warps of different schedulers)
+  const int warp = (threadIdx.x >> 5) % 4 * (kQdWarps / 4) + (threadIdx.x >> 7);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kOffBar) + warp * kQdDepth;
   const uint32_t stages = smem_u32(smem) + warp * kQdDepth * S::kStage;
+  auto lasts = [&](int w) { return reinterpret_cast<float*>(smem + w * kQdDepth * S::kStage); };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kQdWarps * kQdDepth; ++i) mbar_init(reinterpret_cast<uint64_t*>(smem + S::kOffBar) + i, 1);
@@ -108,7 +119,6 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
   }
   deal_prefix(a.B, prefix, [&](int b) { return qd_span(a, b).n; });
   __syncthreads();
-  griddep_launch();
   // sequences without a token: zeros and -inf
   for (int b = blockIdx.x; b < a.B; b += gridDim.x)
     if (prefix[b + 1] == prefix[b]) {
@@ -117,22 +127,24 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
       if (p.lse)
         for (int e = threadIdx.x; e < a.Hq; e += kQdThreads) p.lse[(size_t)b * a.Hq + e] = -INFINITY;
     }
-  const int total = prefix[a.B] * a.Hkv, nc = min((int)gridDim.x, total), c = blockIdx.x;
+  const int total = prefix[a.B] * a.Hkv, nc = min((int)gridDim.x, (total + kQdLeast - 1) / kQdLeast), c = blockIdx.x;
   if (c >= nc) return;
   const int x0 = deal_bound(total, nc, c), x1 = deal_bound(total, nc, c + 1);
+  auto bound = [&](int w) { return x0 + (x1 - x0) * w / kQdWarps; };  // of the warps' runs
+  const int y0 = bound(warp), y1 = bound(warp + 1);
 
-  // ---- the warp's tiles x0 + warp, x0 + warp + kQdWarps, ...: a lane looks after one run of slots of a page
+  // ---- the warp's tiles [y0, y1): a lane looks after one run of slots of a page
   const uint32_t el = elect_one();
   const uint64_t policy = policy_evict_first();  // a cache is read once a step
   const int rows = min(a.page_mask + 1, kQdTile), runs = kQdTile / rows, bpr = rows / kQBlock, batch = 32 / runs;
   uint64_t src = 0;       // of the lane's run: address, bytes, place in the stage
   uint32_t bytes = 0, to = 0, none = 0;  // none: lanes whose page is out of range
   auto look = [&](int xb) {
-    const int x = xb + lane / runs * kQdWarps;
+    const int x = xb + lane / runs;
     bool bad = false;
     bytes = 0;
-    if (x < x1) {
-      const DealSeg g = deal_seg(prefix, a.B, a.Hkv, x, x1);
+    if (x < y1) {
+      const DealSeg g = deal_seg(prefix, a.B, a.Hkv, x, y1);
       const QSpan s = qd_span(a, g.b);
       const int first = s.token(g.j0) + lane % runs * rows;
       int b0 = bpr, b1 = 0;  // blocks with a visible token
@@ -158,9 +170,9 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
     none = __ballot_sync(0xffffffffu, bad);
   };
   bool ok = true;
-  int next = x0 + warp, slot = batch, in = 0;  // the next tile to fetch, its place in the batch, its stage
+  int next = y0, slot = batch, in = 0;  // the next tile to fetch, its place in the batch, its stage
   auto fetch = [&]() {
-    if (next >= x1 || !ok) return;
+    if (next >= y1 || !ok) return;
     if (slot == batch) {
       look(next);
       slot = 0;
@@ -189,7 +201,7 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
       fence_proxy_async();
       __syncwarp();
     }
-    next += kQdWarps;
+    ++next;
     ++slot;
     if (++in == kQdDepth) in = 0;
   };
@@ -199,10 +211,10 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
   const int t = lane & 3, gq = lane >> 2;
   // the tokens of this lane's rows gq and gq + 8 of a block: in this order a lane's words of V lie four tokens apart
   const int r0 = (gq >> 1) + 4 * (gq & 1), r1 = r0 + 8;
-  int it = 0, out = 0;       // tiles of the CTA behind us; the stage of this warp's next one
+  int out = 0;  // the stage of the next tile
   uint32_t phase = 0;
-  for (int x = x0; x < x1;) {
-    const DealSeg g = deal_seg(prefix, a.B, a.Hkv, x, x1);
+  for (int x = y0; x < y1;) {
+    const DealSeg g = deal_seg(prefix, a.B, a.Hkv, x, y1);
     const QSpan s = qd_span(a, g.b);
     // q as B fragments: lane (gq, t) holds channels 16 t .. 16 t + 15 of each group of head gq
     uint32_t qb[G][2][2][2];      // [group][word][even, odd nibbles][b0, b1]
@@ -265,13 +277,12 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
       for (int i = 0; i < 4; ++i) o[gg][i][0] = o[gg][i][1] = o[gg][i][2] = o[gg][i][3] = 0.f;
     }
 
-    // this warp's first tile of the unit: tile i of the CTA's run is warp i % kQdWarps's
-    for (int j = g.j0 + (warp - it % kQdWarps + kQdWarps) % kQdWarps; j < g.j1; j += kQdWarps) {
+    for (int j = g.j0; j < g.j1; ++j) {
       const int tok0 = s.token(j);
       if (ok && !__all_sync(0xffffffffu, mbar_wait(&full[out], phase, a.err))) {
         ok = false;  // nothing more is fetched, and what is on its way has landed before the CTA may end
         for (int i = 0; i < kQdDepth; ++i)
-          if (x + j - g.j0 + i * kQdWarps < next)
+          if (x + j - g.j0 + i < next)
             mbar_wait(&full[(out + i) % kQdDepth], phase ^ (out + i >= kQdDepth ? 1u : 0u), a.err);
       }
       const uint32_t tb = stages + out * S::kStage;
@@ -422,10 +433,7 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
         phase ^= 1u;
       }
     }
-    it += g.j1 - g.j0;
-    x += g.j1 - g.j0;
-
-    // ---- merge the warps
+    // ---- the piece's sums: l and ob over the rows, o as [gg][i, i + 4]
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
       l.x += __shfl_xor_sync(0xffffffffu, l.x, off);
@@ -435,126 +443,187 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
 #pragma unroll
         for (int e = 0; e < 2; ++e) ob[gg][e] += __shfl_xor_sync(0xffffffffu, ob[gg][e], off);
     }
-    if (lane < 4) {
-      *reinterpret_cast<float2*>(stats + warp * 16 + 2 * t) = make_float2(ref[0], ref[1]);
-      *reinterpret_cast<float2*>(stats + warp * 16 + 8 + 2 * t) = l;
-    }
-    // o[gg][i]: channels 64 gg + 8 gq + i and + 4, stored as [gg][i, i + 4][gq][8 heads]
+    float2 v[G][8];  // channels 64 gg + 8 gq + 0 .. 7 of heads 2t, 2t + 1
 #pragma unroll
-    for (int gg = 0; gg < G; ++gg)
+    for (int gg = 0; gg < G; ++gg) {
+      const float F = E[gg] == 0 ? 0.f : __uint_as_float((uint32_t)E[gg] << 23);
+      const float m0 = fmaf(-8.f * F, ow[gg][0], ob[gg][0]), m1 = fmaf(-8.f * F, ow[gg][1], ob[gg][1]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float F = E[gg] == 0 ? 0.f : __uint_as_float((uint32_t)E[gg] << 23), f = F * (i & 1 ? 0x1p20f : 0x1p24f);
-        const float m0 = fmaf(-8.f * F, ow[gg][0], ob[gg][0]), m1 = fmaf(-8.f * F, ow[gg][1], ob[gg][1]);
-        float* at = merge + warp * D * 8 + ((gg * 8 + i) * 8 + gq) * 8 + 2 * t;
-        *reinterpret_cast<float2*>(at) = make_float2(fmaf(o[gg][i][0], f, m0), fmaf(o[gg][i][1], f, m1));
-        *reinterpret_cast<float2*>(at + 4 * 64) = make_float2(fmaf(o[gg][i][2], f, m0), fmaf(o[gg][i][3], f, m1));
+        const float f = F * (i & 1 ? 0x1p20f : 0x1p24f);
+        v[gg][i] = make_float2(fmaf(o[gg][i][0], f, m0), fmaf(o[gg][i][1], f, m1));
+        v[gg][i + 4] = make_float2(fmaf(o[gg][i][2], f, m0), fmaf(o[gg][i][3], f, m1));
       }
-    named_bar_sync(1, 32 * kQdWarps);
-    {
-      const int gg = threadIdx.x & 7;
-      float M = -INFINITY, L = 0.f, f[kQdWarps];
+    }
+    if (g.j0 == 0 && g.j1 == g.n) {
 #pragma unroll
-      for (int w = 0; w < kQdWarps; ++w) M = fmaxf(M, stats[w * 16 + gg]);
-      const float Ms = M == -INFINITY ? 0.f : M;
+      for (int e = 0; e < 2; ++e) {
+        if (2 * t + e >= a.G) continue;
+        const float L = e ? l.y : l.x, il = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);  // no weight at all: zeros; a NaN stays one
+        const size_t head = (size_t)g.b * a.Hq + g.h * a.G + 2 * t + e;
 #pragma unroll
-      for (int w = 0; w < kQdWarps; ++w) {
-        f[w] = fast_exp2(stats[w * 16 + gg] - Ms);
-        L += f[w] * stats[w * 16 + 8 + gg];
-      }
-      const bool whole = g.j0 == 0 && g.j1 == g.n;
-      const float il = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);  // no weight at all: zeros; a NaN stays one
-      float* rec = p.records + (size_t)(2 * c + (g.j0 == 0 ? 1 : 0)) * qrec_floats<D>();
-      const size_t head = (size_t)g.b * a.Hq + g.h * a.G + gg;
+        for (int gg = 0; gg < G; ++gg) {
+          uint32_t y[4];
 #pragma unroll
-      for (int dd = threadIdx.x >> 3; dd < D; dd += 4 * kQdWarps) {
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < kQdWarps; ++w) v += f[w] * merge[(w * D + dd) * 8 + gg];
-        const int ch = (dd & ~63) + 8 * (dd & 7) + (dd >> 3 & 7);
-        if (!whole) rec[16 + ch * 8 + gg] = v;
-        else if (gg < a.G) static_cast<T*>(p.out)[head * D + ch] = Num<T>::from_float(v * il);
-      }
-      if (threadIdx.x < 8) {
-        if (!whole) {
-          rec[gg] = M;
-          rec[8 + gg] = L;
-        } else if (gg < a.G && p.lse) {
-          p.lse[head] = (M + log2f(L)) * 0.6931471805599453f;
+          for (int i = 0; i < 4; ++i)
+            y[i] = Num<T>::pack((e ? v[gg][2 * i].y : v[gg][2 * i].x) * il, (e ? v[gg][2 * i + 1].y : v[gg][2 * i + 1].x) * il);
+          *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + head * D + 64 * gg + 8 * gq) = make_uint4(y[0], y[1], y[2], y[3]);
         }
+        if (p.lse && gq == 0) p.lse[head] = (ref[e] + log2f(L)) * 0.6931471805599453f;
+      }
+    } else {
+      const bool last = x + g.j1 - g.j0 == y1;
+      float* at = last ? lasts(warp) : firsts + warp * D * 8;
+      float* st = stats + warp * 32 + (last ? 16 : 0);
+      if (lane < 4) {
+        *reinterpret_cast<float2*>(st + 2 * t) = make_float2(ref[0], ref[1]);
+        *reinterpret_cast<float2*>(st + 8 + 2 * t) = l;
+      }
+#pragma unroll
+      for (int gg = 0; gg < G; ++gg)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) *reinterpret_cast<float2*>(at + ((gg * 8 + i) * 8 + gq) * 8 + 2 * t) = v[gg][i];
+    }
+    if (lane == 0) {
+      const int4 u = make_int4(x - g.j0, g.n, g.b, g.h);
+      if (x + g.j1 - g.j0 == y1) units[warp] = u;
+      if (x == x0) units[kQdWarps] = u;
+    }
+    x += g.j1 - g.j0;
+  }
+  __syncthreads();
+
+  // ---- units that lie in several warps' runs, or are cut by the CTA's
+  const int gg = threadIdx.x & 7;
+  int lastw = kQdWarps - 1;
+  while (bound(lastw) == bound(lastw + 1)) --lastw;
+  const int4 cta_first = units[kQdWarps], cta_last = units[lastw];
+  for (int w = -1; w < kQdWarps; ++w) {
+    if (w >= 0 && bound(w) == bound(w + 1)) continue;
+    const int4 u = units[w < 0 ? kQdWarps : w];
+    // each unit once: at the first warp whose last unit it is, or as the CTA's first one
+    if (w >= 0 && (bound(w) > u.x ? bound(w) > x0 || cta_first.x == u.x : cta_first.x == u.x)) continue;
+    const int xs = max(u.x, x0), xe = min(u.x + u.y, x1);
+    float M = -INFINITY;
+    uint32_t mask = 0;  // warps with a piece; those whose last unit it is
+    bool single = false;
+    for (int k = 0; k < kQdWarps; ++k) {
+      const int b0 = bound(k), b1 = bound(k + 1);
+      if (b0 >= xe || b1 <= xs || b0 == b1) continue;
+      single |= b0 <= u.x && u.x + u.y <= b1;  // written already
+      mask |= (b1 <= xe ? 0x10001u : 1u) << k;
+    }
+    if (single) continue;
+    for (uint32_t k = mask & 0xffffu; k; k &= k - 1) {
+      const int i = __ffs(k) - 1;
+      M = fmaxf(M, stats[i * 32 + (mask >> (16 + i) & 1u ? 16 : 0) + gg]);
+    }
+    const float Ms = M == -INFINITY ? 0.f : M;
+    constexpr int kEach = D * 8 / kQdThreads;
+    float L = 0.f, v[kEach] = {};
+    for (uint32_t k = mask & 0xffffu; k; k &= k - 1) {
+      const int i = __ffs(k) - 1;
+      const bool last = mask >> (16 + i) & 1u;
+      const float* st = stats + i * 32 + (last ? 16 : 0);
+      const float* from = last ? lasts(i) : firsts + i * D * 8;
+      const float f = fast_exp2(st[gg] - Ms);
+      L += f * st[8 + gg];
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) v[e] += f * from[e * kQdThreads + threadIdx.x];
+    }
+    const bool whole = u.x >= x0 && u.x + u.y <= x1;
+    const float il = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+    float* rec = p.records + (size_t)(2 * c + (u.x >= x0 ? 1 : 0)) * qrec_floats<D>();
+    const size_t head = (size_t)u.z * a.Hq + u.w * a.G + gg;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int dd = (e * kQdThreads + threadIdx.x) >> 3, ch = (dd & ~63) + 8 * (dd & 7) + (dd >> 3 & 7);
+      if (!whole) rec[16 + ch * 8 + gg] = v[e];
+      else if (gg < a.G) static_cast<T*>(p.out)[head * D + ch] = Num<T>::from_float(v[e] * il);
+    }
+    if (threadIdx.x < 8) {
+      if (!whole) {
+        rec[gg] = M;
+        rec[8 + gg] = L;
+      } else if (gg < a.G && p.lse) {
+        p.lse[head] = (M + log2f(L)) * 0.6931471805599453f;
       }
     }
-    named_bar_sync(1, 32 * kQdWarps);
   }
-}
 
-// Merge of the units that lie in several runs.  CTA (c, y) looks at the run of decode CTA c: where its last unit
-// begins in it and goes on in the next runs, it merges that unit's records (slot 1 of c, slot 0 of the following
-// CTAs) for 32 channels.
-template <typename T, int D>
-__global__ void __launch_bounds__(kQdCombThreads) qpaged_combine_kernel(QdArgs p, int ncta) {
-  const PagedArgs& a = p.a;
-  extern __shared__ float csm[];
-  constexpr int kGroups = kQdCombThreads / (8 * kQdCombCols);  // records taken side by side
-  __shared__ float part[kQdCombThreads];
-  int* prefix = reinterpret_cast<int*>(csm);
-  float* fac = csm + a.B + 1;  // [record][8]
-  float* red = fac + 8 * ncta;  // M, L [8] each
-  deal_prefix(a.B, prefix, [&](int b) { return qd_span(a, b).n; });
+  // ---- units that lie in several CTAs' runs: the last to leave its record merges them
+  __shared__ int joins[2];  // the records of the CTA's first and last unit, if it is the one
   __syncthreads();
-  griddep_wait();
-  const int total = prefix[a.B] * a.Hkv, nc = min(ncta, total), c = blockIdx.x;
-  if (c >= nc) return;
-  const int x0 = deal_bound(total, nc, c), x1 = deal_bound(total, nc, c + 1);
-  const DealSeg g = deal_seg(prefix, a.B, a.Hkv, x1 - 1, x1);  // the last tile's unit
-  const int begin = x1 - 1 - g.j0;                        // its first tile
-  if (begin < x0 || g.j0 + 1 == g.n) return;
-  const int nrec = deal_owner(total, nc, begin + g.n - 1) - c + 1;
-  auto rec = [&](int i) { return p.records + (size_t)(2 * (c + i) + (i == 0 ? 1 : 0)) * qrec_floats<D>(); };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp < 8) {
-    float M = -INFINITY, L = 0.f;
-    for (int i = lane; i < nrec; i += 32) M = fmaxf(M, __ldcg(rec(i) + warp));
-#pragma unroll
-    for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    const float Ms = M == -INFINITY ? 0.f : M;
-    for (int i = lane; i < nrec; i += 32) {
-      const float f = fast_exp2(__ldcg(rec(i) + warp) - Ms);
-      fac[i * 8 + warp] = f;
-      L += f * __ldcg(rec(i) + 8 + warp);
+  if (threadIdx.x == 0) {
+    __threadfence();
+    for (int i = 0; i < 2; ++i) {
+      const int4 u = i ? cta_last : cta_first;
+      joins[i] = 0;
+      if (u.x >= x0 && u.x + u.y <= x1) continue;
+      if (i && u.x == cta_first.x) continue;
+      const int c0 = deal_owner(total, nc, u.x), n = deal_owner(total, nc, u.x + u.y - 1) - c0 + 1, at = 8 * (c0 & 3);
+      uint32_t* word = a.err + 2 + c0 / 4;
+      if ((int)(atomicAdd(word, 1u << at) >> at & 255u) + 1 == n) {
+        atomicSub(word, (uint32_t)n << at);
+        joins[i] = n;
+      }
     }
-#pragma unroll
-    for (int off = 16; off; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-    if (lane == 0) { red[warp] = M; red[8 + warp] = L; }
+    __threadfence();
   }
   __syncthreads();
-  const int e = threadIdx.x % (8 * kQdCombCols), grp = threadIdx.x / (8 * kQdCombCols), gg = e & 7;
-  const int dd = blockIdx.y * kQdCombCols + (e >> 3);
-  float v = 0.f;
-#pragma unroll 8
-  for (int i = grp; i < nrec; i += kGroups) v += fac[i * 8 + gg] * __ldcg(rec(i) + 16 + dd * 8 + gg);
-  part[threadIdx.x] = v;
-  __syncthreads();
-  if (grp == 0 && gg < a.G) {
+  for (int k = 0; k < 2; ++k) {
+    const int n = joins[k];
+    if (n == 0) continue;
+    const int4 u = k ? cta_last : cta_first;
+    const int c0 = deal_owner(total, nc, u.x);
+    auto rec = [&](int i) { return p.records + (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * qrec_floats<D>(); };
+    float* fac = firsts;  // [record][8]
+    float* red = fac + 8 * kQdMostCtas;  // M, L [8] each
+    const int pw = threadIdx.x >> 5;
+    if (pw < 8) {
+      float M = -INFINITY, L = 0.f;
+      for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(rec(i) + pw));
 #pragma unroll
-    for (int i = 1; i < kGroups; ++i) v += part[i * 8 * kQdCombCols + e];
-    const float L = red[8 + gg], inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-    const size_t head = (size_t)g.b * a.Hq + g.h * a.G + gg;
-    static_cast<T*>(p.out)[head * D + dd] = Num<T>::from_float(v * inv);
-    if (p.lse && dd == 0) p.lse[head] = (red[gg] + log2f(L)) * 0.6931471805599453f;
+      for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+      const float Ms = M == -INFINITY ? 0.f : M;
+      for (int i = lane; i < n; i += 32) {
+        const float f = fast_exp2(__ldcg(rec(i) + pw) - Ms);
+        fac[i * 8 + pw] = f;
+        L += f * __ldcg(rec(i) + 8 + pw);
+      }
+#pragma unroll
+      for (int off = 16; off; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+      if (lane == 0) { red[pw] = M; red[8 + pw] = L; }
+    }
+    __syncthreads();
+    constexpr int kEach = D * 8 / kQdThreads;
+    float v[kEach] = {};
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const float f = fac[i * 8 + gg];
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) v[e] += f * __ldcg(rec(i) + 16 + e * kQdThreads + threadIdx.x);
+    }
+    if (gg < a.G) {
+      const float L = red[8 + gg], il = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+      const size_t head = (size_t)u.z * a.Hq + u.w * a.G + gg;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e)
+        static_cast<T*>(p.out)[head * D + ((e * kQdThreads + threadIdx.x) >> 3)] = Num<T>::from_float(v[e] * il);
+      if (p.lse && threadIdx.x < 8) p.lse[head] = (red[gg] + log2f(L)) * 0.6931471805599453f;
+    }
+    __syncthreads();
   }
 }
 
 template <typename T, int D>
 cudaError_t launch_qdecode_td(const QdArgs& p, cudaStream_t s) {
-  const int ncta = sm_count();
+  const int ncta = sm_count() < kQdMostCtas ? sm_count() : kQdMostCtas;
   const size_t smem = QdSmem<D>::kOffPrefix + ((size_t)p.a.B + 1) * 4;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(qpaged_decode_kernel<T, D>), smem);
   if (e != cudaSuccess) return e;
   qpaged_decode_kernel<T, D><<<ncta, kQdThreads, smem, s>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_dependent(qpaged_combine_kernel<T, D>, dim3(ncta, D / kQdCombCols), kQdCombThreads,
-                          ((size_t)p.a.B + 1 + 8 * ncta + 16) * 4, s, p, ncta);
+  return cudaGetLastError();
 }
 
 }  // namespace

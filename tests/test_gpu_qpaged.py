@@ -153,6 +153,49 @@ def test_decode(dtype, d, hq, hkv, page, lens, window, sinks):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("d,hkv,hq,lens", [
+    (128, 4, 8, [3] * 700 + [900, 31, 33]),     # many units of a tile: whole in a warp's run, cut by warps and by CTAs
+    (64, 1, 2, [1 + i % 150 for i in range(4096)]),
+    (128, 2, 16, [20000, 10, 15000, 1]), (64, 8, 8, [2000 + 37 * i for i in range(6)])])
+def test_decode_deals_units_to_warps(d, hkv, hq, lens):
+    page = 32
+    used = [-(-n // page) for n in lens]
+    n_pages = sum(used)
+    pool = torch.zeros(n_pages, hkv, page * 9 * d // 8, dtype=torch.uint8, device="cuda")
+    p = dkv.dkv_qpaged_layout(pool, len(lens), hq, d, max(used), dtype=torch.bfloat16)
+    ws = workspace(p)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    K, V = (torch.randn(n_pages * page, hkv, d, generator=g, device="cuda").bfloat16() for _ in range(2))
+    dkv.dkv_qpaged_append(p, K, V, pool, torch.arange(n_pages * page, device="cuda"), workspace=ws)
+    starts = torch.tensor([sum(used[:i]) for i in range(len(lens))], device="cuda")
+    table = (starts[:, None] + torch.arange(max(used), device="cuda")[None]).clamp(max=n_pages - 1).int()
+    L = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = torch.randn(len(lens), hq, d, generator=g, device="cuda").bfloat16() * 2
+    out, lse = dkv.dkv_qpaged_decode(p, q, pool, table, L, workspace=ws)
+    no_fault(ws)
+    back = [torch.zeros(1, hkv, n_pages * page, d, dtype=torch.float16, device="cuda") for _ in range(2)]
+    p16 = dkv.dkv_qpaged_layout(pool, 1, hq, d, n_pages)
+    dkv.dkv_qpaged_gather(p16, pool, torch.arange(n_pages, dtype=torch.int32, device="cuda")[None], L[:1] * 0, *back)
+    for b in range(len(lens)):
+        if len(lens) > 1000 and b % 37:
+            continue
+        at = int(starts[b]) * page
+        k, v = (x[0, :, at:at + lens[b]].double().repeat_interleave(hq // hkv, 0) for x in back)
+        s = (k @ q[b].double()[:, :, None])[..., 0] / math.sqrt(d)
+        w = s.softmax(-1)
+        want = (w[:, None] @ v)[:, 0]
+        # as in check_decode: what is added up are codes times scale and biases, and 15 scale <= 2 max + a spacing of 2^-10 max,
+        # |bias| <= max of the group's largest magnitude: at most 3.1 max each for K and V
+        size = 3.1 * (w * v.abs().amax(-1)).sum(-1, keepdim=True)
+        ds = R.score_error(d, 3.1 * float((q[b].double().abs().sum(-1) * k.abs().amax((1, 2))).max()) / math.sqrt(d))
+        tol = 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2 * ds) * (1 + 2.0 ** -8) * size + 1e-30
+        assert bool(((out[b].double() - want).abs() <= tol).all()), b
+        assert bool(((lse[b].double() - s.logsumexp(-1)).abs() <= ds + 2.0 ** -22 * s.logsumexp(-1).abs().clamp(min=1.0)).all()), b
+    for _ in range(3):  # the counters in the header are back at zero
+        again, lse2 = dkv.dkv_qpaged_decode(p, q, pool, table, L, workspace=ws)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
 def check_decode(c, q, out, lse, lens, hq, window, sinks):
     for b in range(c.B):
         for j in range(hq):
