@@ -493,37 +493,30 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
   }
   __syncthreads();
 
-  // ---- units that lie in several warps' runs, or are cut by the CTA's
-  const int gg = threadIdx.x & 7;
-  int lastw = kQdWarps - 1;
-  while (bound(lastw) == bound(lastw + 1)) --lastw;
-  const int4 cta_first = units[kQdWarps], cta_last = units[lastw];
-  for (int w = -1; w < kQdWarps; ++w) {
-    if (w >= 0 && bound(w) == bound(w + 1)) continue;
-    const int4 u = units[w < 0 ? kQdWarps : w];
-    // each unit once: at the first warp whose last unit it is, or as the CTA's first one
-    if (w >= 0 && (bound(w) > u.x ? bound(w) > x0 || cta_first.x == u.x : cta_first.x == u.x)) continue;
+  // ---- units that lie in several warps' runs, or are cut by the CTA's.  Lane w looks after warp w.
+  const int gg = threadIdx.x & 7, b0 = bound(min(lane, kQdWarps)), b1 = bound(min(lane + 1, kQdWarps));
+  const uint32_t used = __ballot_sync(0xffffffffu, b0 < b1);
+  const int4 cta_first = units[kQdWarps], cta_last = units[31 - __clz(used)];
+  // each unit once: as the CTA's first one, or with the first warp whose last unit it is
+  const int4 mine = units[min(lane, kQdWarps)];
+  const uint32_t todo = __ballot_sync(0xffffffffu, b0 < b1 && mine.x != cta_first.x && b0 <= mine.x);
+  for (uint32_t left = todo | 0x80000000u; left; left &= left - 1) {
+    const int4 u = units[min(__ffs(left) - 1, kQdWarps)];
     const int xs = max(u.x, x0), xe = min(u.x + u.y, x1);
+    const uint32_t mask = __ballot_sync(0xffffffffu, b0 < b1 && b0 < xe && b1 > xs);      // warps with a piece
+    const uint32_t ends = __ballot_sync(0xffffffffu, b1 <= xe);                           // whose last unit it is
+    if (__any_sync(0xffffffffu, b0 < b1 && b0 <= u.x && u.x + u.y <= b1)) continue;       // written already
     float M = -INFINITY;
-    uint32_t mask = 0;  // warps with a piece; those whose last unit it is
-    bool single = false;
-    for (int k = 0; k < kQdWarps; ++k) {
-      const int b0 = bound(k), b1 = bound(k + 1);
-      if (b0 >= xe || b1 <= xs || b0 == b1) continue;
-      single |= b0 <= u.x && u.x + u.y <= b1;  // written already
-      mask |= (b1 <= xe ? 0x10001u : 1u) << k;
-    }
-    if (single) continue;
-    for (uint32_t k = mask & 0xffffu; k; k &= k - 1) {
+    for (uint32_t k = mask; k; k &= k - 1) {
       const int i = __ffs(k) - 1;
-      M = fmaxf(M, stats[i * 32 + (mask >> (16 + i) & 1u ? 16 : 0) + gg]);
+      M = fmaxf(M, stats[i * 32 + (ends >> i & 1u ? 16 : 0) + gg]);
     }
     const float Ms = M == -INFINITY ? 0.f : M;
     constexpr int kEach = D * 8 / kQdThreads;
     float L = 0.f, v[kEach] = {};
-    for (uint32_t k = mask & 0xffffu; k; k &= k - 1) {
+    for (uint32_t k = mask; k; k &= k - 1) {
       const int i = __ffs(k) - 1;
-      const bool last = mask >> (16 + i) & 1u;
+      const bool last = ends >> i & 1u;
       const float* st = stats + i * 32 + (last ? 16 : 0);
       const float* from = last ? lasts(i) : firsts + i * D * 8;
       const float f = fast_exp2(st[gg] - Ms);
