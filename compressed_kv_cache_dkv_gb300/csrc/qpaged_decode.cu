@@ -507,23 +507,22 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
     const uint32_t ends = __ballot_sync(0xffffffffu, b1 <= xe);                           // whose last unit it is
     if (__any_sync(0xffffffffu, b0 < b1 && b0 <= u.x && u.x + u.y <= b1)) continue;       // written already
     float M = -INFINITY;
-    for (uint32_t k = mask; k; k &= k - 1) {
-      const int i = __ffs(k) - 1;
-      M = fmaxf(M, stats[i * 32 + (ends >> i & 1u ? 16 : 0) + gg]);
-    }
+#pragma unroll
+    for (int i = 0; i < kQdWarps; ++i)
+      if (mask >> i & 1u) M = fmaxf(M, stats[i * 32 + (ends >> i & 1u ? 16 : 0) + gg]);
     const float Ms = M == -INFINITY ? 0.f : M;
     constexpr int kEach = D * 8 / kQdThreads;
     float L = 0.f, v[kEach] = {};
-    for (uint32_t k = mask; k; k &= k - 1) {
-      const int i = __ffs(k) - 1;
-      const bool last = ends >> i & 1u;
-      const float* st = stats + i * 32 + (last ? 16 : 0);
-      const float* from = last ? lasts(i) : firsts + i * D * 8;
-      const float f = fast_exp2(st[gg] - Ms);
-      L += f * st[8 + gg];
 #pragma unroll
-      for (int e = 0; e < kEach; ++e) v[e] += f * from[e * kQdThreads + threadIdx.x];
-    }
+    for (int i = 0; i < kQdWarps; ++i)
+      if (mask >> i & 1u) {
+        const float* st = stats + i * 32 + (ends >> i & 1u ? 16 : 0);
+        const float* from = ends >> i & 1u ? lasts(i) : firsts + i * D * 8;
+        const float f = fast_exp2(st[gg] - Ms);
+        L += f * st[8 + gg];
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) v[e] += f * from[e * kQdThreads + threadIdx.x];
+      }
     const bool whole = u.x >= x0 && u.x + u.y <= x1;
     const float il = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
     float* rec = p.records + (size_t)(2 * c + (u.x >= x0 ? 1 : 0)) * qrec_floats<D>();
@@ -570,42 +569,45 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
     const int4 u = k ? cta_last : cta_first;
     const int c0 = deal_owner(total, nc, u.x);
     auto rec = [&](int i) { return p.records + (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * qrec_floats<D>(); };
-    float* fac = firsts;  // [record][8]
-    float* red = fac + 8 * kQdMostCtas;  // M, L [8] each
-    const int pw = threadIdx.x >> 5;
-    if (pw < 8) {
-      float M = -INFINITY, L = 0.f;
-      for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(rec(i) + pw));
+    constexpr int kEach = D * 8 / kQdThreads, kDeep = 8;
+    float M = -INFINITY, L = 0.f, v[kEach] = {};
+    for (int i0 = 0; i0 < n; i0 += kDeep) {
+      float m[kDeep], l[kDeep], y[kDeep][kEach];
 #pragma unroll
-      for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-      const float Ms = M == -INFINITY ? 0.f : M;
-      for (int i = lane; i < n; i += 32) {
-        const float f = fast_exp2(__ldcg(rec(i) + pw) - Ms);
-        fac[i * 8 + pw] = f;
-        L += f * __ldcg(rec(i) + 8 + pw);
+      for (int i = 0; i < kDeep; ++i) {
+        m[i] = -INFINITY;
+        if (i0 + i >= n) continue;
+        const float* from = rec(i0 + i);
+        m[i] = __ldcg(from + gg);
+        l[i] = __ldcg(from + 8 + gg);
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) y[i][e] = __ldcg(from + 16 + e * kQdThreads + threadIdx.x);
       }
+      float top = M;
 #pragma unroll
-      for (int off = 16; off; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-      if (lane == 0) { red[pw] = M; red[8 + pw] = L; }
-    }
-    __syncthreads();
-    constexpr int kEach = D * 8 / kQdThreads;
-    float v[kEach] = {};
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-      const float f = fac[i * 8 + gg];
+      for (int i = 0; i < kDeep; ++i) top = fmaxf(top, m[i]);
+      const float Ms = top == -INFINITY ? 0.f : top, al = fast_exp2(M - Ms);
+      M = top;
+      L *= al;
 #pragma unroll
-      for (int e = 0; e < kEach; ++e) v[e] += f * __ldcg(rec(i) + 16 + e * kQdThreads + threadIdx.x);
+      for (int e = 0; e < kEach; ++e) v[e] *= al;
+#pragma unroll
+      for (int i = 0; i < kDeep; ++i) {
+        if (i0 + i >= n) continue;
+        const float f = fast_exp2(m[i] - Ms);
+        L += f * l[i];
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) v[e] += f * y[i][e];
+      }
     }
     if (gg < a.G) {
-      const float L = red[8 + gg], il = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+      const float il = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
       const size_t head = (size_t)u.z * a.Hq + u.w * a.G + gg;
 #pragma unroll
       for (int e = 0; e < kEach; ++e)
         static_cast<T*>(p.out)[head * D + ((e * kQdThreads + threadIdx.x) >> 3)] = Num<T>::from_float(v[e] * il);
-      if (p.lse && threadIdx.x < 8) p.lse[head] = (red[gg] + log2f(L)) * 0.6931471805599453f;
+      if (p.lse && threadIdx.x < 8) p.lse[head] = (M + log2f(L)) * 0.6931471805599453f;
     }
-    __syncthreads();
   }
 }
 
