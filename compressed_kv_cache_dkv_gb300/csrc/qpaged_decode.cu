@@ -134,19 +134,19 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
   const int y0 = bound(warp), y1 = bound(warp + 1);
 
   // ---- the warp's tiles [y0, y1): a lane looks after one run of slots of a page
-  const uint32_t el = elect_one();
   const uint64_t policy = policy_evict_first();  // a cache is read once a step
   const int rows = min(a.page_mask + 1, kQdTile), runs = kQdTile / rows, bpr = rows / kQBlock, batch = 32 / runs;
+  const int run_shift = runs == 2 ? 1 : 0, part = lane & (runs - 1);
   uint64_t src = 0;       // of the lane's run: address, bytes, place in the stage
-  uint32_t bytes = 0, to = 0, none = 0;  // none: lanes whose page is out of range
+  uint32_t bytes = 0, to = 0, all = 0, none = 0;  // all: the tile's bytes; none: lanes whose page is out of range
   auto look = [&](int xb) {
-    const int x = xb + lane / runs;
+    const int x = xb + (lane >> run_shift);
     bool bad = false;
     bytes = 0;
     if (x < y1) {
       const DealSeg g = deal_seg(prefix, a.B, a.Hkv, x, y1);
       const QSpan s = qd_span(a, g.b);
-      const int first = s.token(g.j0) + lane % runs * rows;
+      const int first = s.token(g.j0) + part * rows;
       int b0 = bpr, b1 = 0;  // blocks with a visible token
 #pragma unroll 1
       for (int i = 0; i < bpr; ++i) {
@@ -165,9 +165,11 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
                 (int64_t)((first & a.page_mask) / kQBlock + b0) * BB;
         }
       }
-      to = (uint32_t)(lane % runs * bpr + b0) * BB;
+      to = (uint32_t)(part * bpr + b0) * BB;
     }
     none = __ballot_sync(0xffffffffu, bad);
+    all = bytes;
+    if (runs == 2) all += __shfl_xor_sync(0xffffffffu, bytes, 1);
   };
   bool ok = true;
   int next = y0, slot = batch, in = 0;  // the next tile to fetch, its place in the batch, its stage
@@ -178,24 +180,18 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
       slot = 0;
     }
     const uint32_t st = stages + in * S::kStage;
-    uint32_t sum = __shfl_sync(0xffffffffu, bytes, slot * runs);
-    if (runs == 2) sum += __shfl_sync(0xffffffffu, bytes, slot * 2 + 1);
-    if (el) mbar_arrive_expect_tx(&full[in], sum);
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (i >= runs) break;
-      const uint32_t n = __shfl_sync(0xffffffffu, bytes, slot * runs + i), at = st + __shfl_sync(0xffffffffu, to, slot * runs + i);
-      const uint64_t from = __shfl_sync(0xffffffffu, src, slot * runs + i);
-      if (n && el)
+    if (lane >> run_shift == slot) {
+      if (part == 0) mbar_arrive_expect_tx(&full[in], all);
+      if (bytes)
         asm volatile(
-            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(at),
-            "l"(from), "r"(n), "r"(smem_u32(&full[in])), "l"(policy)
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(st + to),
+            "l"(src), "r"(bytes), "r"(smem_u32(&full[in])), "l"(policy)
             : "memory");
     }
-    if (none >> (slot * runs) & (runs == 2 ? 3u : 1u)) {  // pages of zeros: no scales, no biases
+    __syncwarp();
+    if (none >> (slot << run_shift) & (runs == 2 ? 3u : 1u)) {  // pages of zeros: no scales, no biases
       for (int k = 0; k < kQdBlocks; ++k)
-        if (none >> (slot * runs + k / bpr) & 1u)
+        if (none >> ((slot << run_shift) + k / bpr) & 1u)
           for (int i = lane; i < D / 2; i += 32)
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + k * BB + 16 * D + 4 * i), "r"(0u) : "memory");
       fence_proxy_async();
@@ -500,40 +496,47 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
   // each unit once: as the CTA's first one, or with the first warp whose last unit it is
   const int4 mine = units[min(lane, kQdWarps)];
   const uint32_t todo = __ballot_sync(0xffffffffu, b0 < b1 && mine.x != cta_first.x && b0 <= mine.x);
-  for (uint32_t left = todo | 0x80000000u; left; left &= left - 1) {
-    const int4 u = units[min(__ffs(left) - 1, kQdWarps)];
+  const int n_units = __popc(todo) + 1;
+  int team = kQdWarps;  // warps of a unit: as many units side by side as there are
+  while (team > 1 && kQdWarps / team < n_units) team >>= 1;
+  for (int k = (threadIdx.x >> 5) / team; k < n_units; k += kQdWarps / team) {
+    uint32_t bits = todo;
+    for (int i = 1; i < k; ++i) bits &= bits - 1;
+    const int4 u = units[k == 0 ? kQdWarps : __ffs(bits) - 1];
     const int xs = max(u.x, x0), xe = min(u.x + u.y, x1);
     const uint32_t mask = __ballot_sync(0xffffffffu, b0 < b1 && b0 < xe && b1 > xs);      // warps with a piece
     const uint32_t ends = __ballot_sync(0xffffffffu, b1 <= xe);                           // whose last unit it is
     if (__any_sync(0xffffffffu, b0 < b1 && b0 <= u.x && u.x + u.y <= b1)) continue;       // written already
-    float M = -INFINITY;
+    float M = -INFINITY, L = 0.f, f[kQdWarps];
 #pragma unroll
-    for (int i = 0; i < kQdWarps; ++i)
-      if (mask >> i & 1u) M = fmaxf(M, stats[i * 32 + (ends >> i & 1u ? 16 : 0) + gg]);
+    for (int i = 0; i < kQdWarps; ++i) {
+      f[i] = -INFINITY;
+      if (mask >> i & 1u) f[i] = stats[i * 32 + (ends >> i & 1u ? 16 : 0) + gg];
+      M = fmaxf(M, f[i]);
+    }
     const float Ms = M == -INFINITY ? 0.f : M;
-    constexpr int kEach = D * 8 / kQdThreads;
-    float L = 0.f, v[kEach] = {};
 #pragma unroll
     for (int i = 0; i < kQdWarps; ++i)
       if (mask >> i & 1u) {
-        const float* st = stats + i * 32 + (ends >> i & 1u ? 16 : 0);
-        const float* from = ends >> i & 1u ? lasts(i) : firsts + i * D * 8;
-        const float f = fast_exp2(st[gg] - Ms);
-        L += f * st[8 + gg];
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) v[e] += f * from[e * kQdThreads + threadIdx.x];
+        f[i] = fast_exp2(f[i] - Ms);
+        L += f[i] * stats[i * 32 + (ends >> i & 1u ? 16 : 0) + 8 + gg];
       }
     const bool whole = u.x >= x0 && u.x + u.y <= x1;
     const float il = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
     float* rec = p.records + (size_t)(2 * c + (u.x >= x0 ? 1 : 0)) * qrec_floats<D>();
     const size_t head = (size_t)u.z * a.Hq + u.w * a.G + gg;
+    const int e0 = threadIdx.x % (32 * team);
+#pragma unroll 2
+    for (int e = e0; e < D * 8; e += 32 * team) {
+      float v = 0.f;
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      const int dd = (e * kQdThreads + threadIdx.x) >> 3, ch = (dd & ~63) + 8 * (dd & 7) + (dd >> 3 & 7);
-      if (!whole) rec[16 + ch * 8 + gg] = v[e];
-      else if (gg < a.G) static_cast<T*>(p.out)[head * D + ch] = Num<T>::from_float(v[e] * il);
+      for (int i = 0; i < kQdWarps; ++i)
+        if (mask >> i & 1u) v += f[i] * (ends >> i & 1u ? lasts(i) : firsts + i * D * 8)[e];
+      const int dd = e >> 3, ch = (dd & ~63) + 8 * (dd & 7) + (dd >> 3 & 7);
+      if (!whole) rec[16 + ch * 8 + gg] = v;
+      else if (gg < a.G) static_cast<T*>(p.out)[head * D + ch] = Num<T>::from_float(v * il);
     }
-    if (threadIdx.x < 8) {
+    if (e0 < 8) {
       if (!whole) {
         rec[gg] = M;
         rec[8 + gg] = L;
