@@ -10,16 +10,16 @@
 //   O_g += P_g V_j    M = 128, N = d, P from TMEM (fp16, over the first 32 columns of its S)
 //
 // Warps 0-7 hold a query row per thread: they bring Q to shared memory, and turn S into P.  Warp 8 streams the
-// tiles' bytes (bulk copies, one per page and tile) into a ring, warps 12-15 make fp16 values of them: a group's
-// values scale * code + bias are fp16 numbers exactly, so the tensor cores see the very values of the cache.
+// tiles' bytes (bulk copies, one per page and tile) into a ring, warps 12-15 and 16-19 make fp16 values of K and of V:
+// a group's values scale * code + bias are fp16 numbers exactly, so the tensor cores see the very values of the cache.
 // Warps 9 and 10 issue the products.  All operands are fp16; bf16 queries are brought into its range by a power of
 // two for each row, which goes into that row's factor of the scores (exact for values above 2^-24 of the largest).
 // Codes come out of a word in the order 0 4 1 5 2 6 3 7; Q stands in the same order, and O leaves it at the end.
 //
 // P = 2^(score - ref) is rounded once to fp16.  A row's reference lies kQpShift below a maximum and moves, with O
-// rescaled in tensor memory, only when a score exceeds that by kQpSlack (base 2): P is at most 2^15, weights down to
-// e^-14 of the largest keep 11 bits and smaller ones are off by 2^-32 of it at most.  A score is rounded by its
-// factor first, as the maximum was, and the reference taken off then: so that large scores lose nothing more.
+// rescaled in tensor memory, only when weights leave fp16's range: when a tile's sum of them exceeds 2^15, which is
+// found without a maximum.  So P is at most 2^15, weights down to e^-14 of the largest keep 11 bits and smaller ones
+// are off by 2^-32 of it at most.
 //
 // Values in the cache are finite.  What lies in slots that no row of the CTA sees may be anything and counts as
 // zeros; a weight of 0 takes care of what only some rows see.
@@ -29,9 +29,10 @@
 namespace dkv {
 namespace {
 
-constexpr int kQpThreads = 512, kQpM = 128, kQpN = 64;
-constexpr float kQpSlack = 8.f, kQpShift = 7.f;
-constexpr float kQpLarge = 0x1p20f;  // scores (in base 2) whose rounding would show in the slack
+constexpr int kQpThreads = 640, kQpM = 128, kQpN = 64;
+constexpr float kQpShift = 7.f;
+constexpr float kQpLarge = 0x1p20f;  // scores (in base 2) whose rounding would show in the range
+constexpr float kQpMost = 0x1p15f;   // of a weight
 
 template <int D>
 struct QpSmem {
@@ -138,12 +139,66 @@ __device__ inline uint4 values8(uint32_t x, __half2 s, __half2 b) {
   return make_uint4(bits(__hfma2(c0, s, b)), bits(__hfma2(c1, s, b)), bits(__hfma2(c2, s, b)), bits(__hfma2(c3, s, b)));
 }
 
+// A tile with large scores, in the loop's place (rare, so in rolled loops): the reference, and with it O and the sum,
+// moved to kQpShift below its maximum where that is higher, and P from there.  Returns reference and sum.  A score is
+// rounded by its factor before the reference is taken off, as the maximum was: an fma would leave the rounding of the
+// maximum in the exponent, 2^-4 at kQpLarge but hundreds at 2^32.
+template <int D>
+__device__ __noinline__ float2 large_tile(unsigned long long sees, uint32_t ts, uint32_t to, float slog2, float ref, float l, bool some) {
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < kQpN; c += 16) {
+    uint32_t s[16];
+    tc_ld16(ts + c, s);
+    tc_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (sees >> (c + e) & 1ull) top = fmaxf(top, __fmul_rn(__uint_as_float(s[e]), slog2));
+  }
+  const bool up = top > ref + kQpShift;
+  const float al = up ? fast_exp2(ref - (top - kQpShift)) : 1.f;
+  if (up) ref = top - kQpShift;
+  if (some && __any_sync(0xffffffffu, up)) {
+#pragma unroll 1
+    for (int c = 0; c < D; c += 16) {
+      uint32_t o[16];
+      tc_ld16(to + c, o);
+      tc_ld_wait();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+      tc_st16(to + c, o);
+    }
+  }
+  const float off = ref == -INFINITY ? 0.f : -ref;
+  l *= al;
+#pragma unroll 1
+  for (int c = 0; c < kQpN; c += 16) {  // (P's columns c / 2 .. c / 2 + 7 lie over scores that have been read)
+    uint32_t s[16], w[8];
+    tc_ld16(ts + c, s);
+    tc_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      float y[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float v = __uint_as_float(s[e + x]);
+        const float d = __fadd_rn(__fmul_rn(v, slog2), off);
+        y[x] = sees >> (c + e + x) & 1ull ? fast_exp2(d) : 0.f;
+        l += y[x];
+      }
+      w[e / 2] = pack_half2(y[0], y[1]);
+    }
+    tc_st8(ts + c / 2, w);
+  }
+  return make_float2(ref, l);
+}
+
 template <int N>
 __device__ inline void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ inline void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-// 128 registers for each of 512 threads at the start, and 2 x 168 + 80 + 96 = 4 x 128
-constexpr int kQpRegsRows = 168, kQpRegsIssue = 80, kQpRegsValues = 96;
+// 96 registers for each of 640 threads at the start, and 2 x 144 + 64 + 2 x 64 = 5 x 96
+constexpr int kQpRegsRows = 144, kQpRegsIssue = 64, kQpRegsValues = 64;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p) {
@@ -196,7 +251,7 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
     }
     for (int i = 0; i < S::kRaw; ++i) {
       mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], 4);
+      mbar_init(&raw_empty[i], 8);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
@@ -217,39 +272,43 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
   bool ok = true;
 
   if (warp >= 12) {
-    // =========================== values: a thread makes half of a token's channels, of K and then of V
+    // =========================== values, of K or of V: a thread makes half of a token's channels
     regs_dec<kQpRegsValues>();
-    const int tid = threadIdx.x - 12 * 32, tok = tid & 63, half = tid >> 6;
+    const int kv = warp >= 16, tid = (threadIdx.x - 12 * 32) & 127, tok = tid & 63, half = tid >> 6;
     constexpr int kWords = D / 16;  // of eight codes
-    // byte of this thread's codes in a tile's bytes
-    const int g = D == 128 ? half : 0, in_g = D == 128 ? 0 : 16 * half;
+    // bytes of this thread's parameters and codes in a tile's bytes, and of its values in a tile
+    const int g = D == 128 ? half : 0;
+    const uint32_t block = sb + S::kOffRaw + (uint32_t)(tok / kQBlock) * qblock_bytes(D);
+    const uint32_t param = block + (uint32_t)((16 + kv) * D + (tok % kQBlock * (D / 64) + g) * 4);
+    const uint32_t codes = block + (uint32_t)(kv * 8 * D + (g * kQBlock + tok % kQBlock) * 32 + (D == 128 ? 0 : 16 * half));
+    const uint32_t tiles = sb + (kv ? S::kOffV : S::kOffK);
+    uint64_t* const done = kv ? v_full : k_full;
     int sl = 0, rs = 0;
     uint32_t ph = 0, rph = 0;
     for (int j = 0; j < nt; ++j) {
       if (ok) ok = mbar_wait(&raw_full[rs], rph, a.err);
-      if (ok && j >= S::kR) ok = mbar_wait(&empty[sl], ph ^ 1u, a.err);
       const int t = key_of(j) + tok;
       const bool zero = !(t < ks.hi && (t >= ks.lo || t < a.sinks)) || (bad_blocks[rs] >> (tok / kQBlock) & 1u);
-      const uint32_t raw = sb + S::kOffRaw + rs * S::kRawTile + (uint32_t)(tok / kQBlock) * qblock_bytes(D);
+      uint32_t sbits = lds32(param + rs * S::kRawTile);
+      uint4 c[kWords / 4];
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        uint32_t sbits = lds32(raw + qparam_off(D, kv, g, tok % kQBlock));
-        if (zero) sbits = 0u;
-        const __half2 sbh = *reinterpret_cast<__half2*>(&sbits), s2 = __low2half2(sbh), b2 = __high2half2(sbh);
-        const uint32_t from = raw + qcode_off(D, kv, g, tok % kQBlock) + in_g;
-        const uint32_t to = sb + (kv ? S::kOffV : S::kOffK) + sl * S::kTile;
+      for (int x = 0; x < kWords / 4; ++x) c[x] = lds128(codes + rs * S::kRawTile + 16 * x);
+      if (zero) sbits = 0u;
+      const __half2 sbh = *reinterpret_cast<__half2*>(&sbits), s2 = __low2half2(sbh), b2 = __high2half2(sbh);
+      if (ok && j >= S::kR) ok = mbar_wait(&empty[sl], ph ^ 1u, a.err);
+      const uint32_t to = tiles + sl * S::kTile;
 #pragma unroll
-        for (int x = 0; x < kWords; x += 4) {
-          const uint4 c = lds128(from + 4 * x);
-          const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+      for (int x = 0; x < kWords / 4; ++x) {
+        const uint32_t w[4] = {c[x].x, c[x].y, c[x].z, c[x].w};
 #pragma unroll
-          for (int y = 0; y < 4; ++y) sts128(to + sw128(kQpN, tok, half * kWords + x + y), values8(w[y], s2, b2));
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(kv ? &v_full[sl] : &k_full[sl]);
+        for (int y = 0; y < 4; ++y) sts128(to + sw128(kQpN, tok, half * kWords + 4 * x + y), values8(w[y], s2, b2));
       }
-      if (lane == 0) mbar_arrive(&raw_empty[rs]);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&done[sl]);
+        mbar_arrive(&raw_empty[rs]);
+      }
       if (++sl == S::kR) { sl = 0; ph ^= 1u; }
       if (++rs == S::kRaw) { rs = 0; rph ^= 1u; }
     }
@@ -257,55 +316,53 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
     regs_dec<kQpRegsIssue>();
     if (warp == 8) {
       // =========================== the tiles' bytes
+      // A lane looks after one run of slots of a page (a tile has 64 / rows of them): one look at the page
+      // table for a batch of tiles.
       const uint32_t el = elect_one();
-      const int rows = min(a.page_mask + 1, kQpN), runs = kQpN / rows, bpr = rows / kQBlock;
+      const int rows = min(a.page_mask + 1, kQpN), runs = kQpN / rows, bpr = rows / kQBlock, batch = 32 / runs;
+      uint64_t src = 0;
+      uint32_t bytes = 0, dst = 0, sum = 0, none = 0;
       int j = 0;
-      for (; j < nt; ++j) {
-        const int st = j % S::kRaw, first = key_of(j) + lane * rows;
-        // lane i < runs: its page, and the run's blocks that hold a visible token
-        int page = -1, b0 = bpr, b1 = 0;
-        bool bad = false;
-        if (lane < runs) {
+      for (int in = 0; j < nt; ++j, ++in) {
+        if (j % batch == 0) {
+          in = 0;
+          const int k = j + lane / runs, r = lane % runs, first = key_of(k) + r * rows;
+          int b0 = bpr, b1 = 0;  // blocks with a visible token
           for (int i = 0; i < bpr; ++i) {
             const int t = first + i * kQBlock;
-            if (t < ks.hi && (t + kQBlock > ks.lo || t < a.sinks)) {
+            if (k < nt && t < ks.hi && (t + kQBlock > ks.lo || t < a.sinks)) {
               b0 = min(b0, i);
               b1 = i + 1;
             }
           }
-          if (b0 < b1) {
-            page = paged_page(a, b, first);
-            bad = page >= a.n_pages;
-          }
+          const int page = b0 < b1 ? paged_page(a, b, first) : 0;
+          const bool bad = page >= a.n_pages;
+          bytes = b0 < b1 && !bad ? (uint32_t)(b1 - b0) * qblock_bytes(D) : 0u;
+          if (bytes)
+            src = reinterpret_cast<uint64_t>(p.cache) + page * a.stride_page + kvh * a.stride_head +
+                  (int64_t)((first & a.page_mask) / kQBlock + b0) * qblock_bytes(D);
+          dst = (uint32_t)(r * bpr + b0) * qblock_bytes(D);
+          none = __ballot_sync(0xffffffffu, bad);
+          sum = bytes;
+          for (int o = 1; o < runs; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         }
-        const uint32_t none = __ballot_sync(0xffffffffu, bad);
-        const bool copies = b0 < b1 && !bad;
-        const uint32_t bytes = copies ? (uint32_t)(b1 - b0) * qblock_bytes(D) : 0u;
-        uint32_t sum = bytes;
-#pragma unroll
-        for (int o = 1; o < kQpN / kQBlock; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        sum = __shfl_sync(0xffffffffu, sum, 0);
-        const uint64_t src = reinterpret_cast<uint64_t>(p.cache) +
-                             (copies ? page * a.stride_page + kvh * a.stride_head + (int64_t)((first & a.page_mask) / kQBlock + b0) * qblock_bytes(D) : 0);
-        const uint32_t dst = sb + S::kOffRaw + st * S::kRawTile + (uint32_t)(lane * bpr + b0) * qblock_bytes(D);
+        const int st = j % S::kRaw;
         if (j >= S::kRaw) ok = mbar_wait(&raw_empty[st], (uint32_t)((j / S::kRaw - 1) & 1), a.err);
         if (!__all_sync(0xffffffffu, ok)) break;
+        const uint32_t all = __shfl_sync(0xffffffffu, sum, in * runs);
         if (el) {
           uint32_t m = 0;  // bad runs as a mask of blocks
-          for (int i = 0; i < kQpN / kQBlock; ++i) m |= (none >> (i / bpr) & 1u) << i;
+          if (none)
+            for (int i = 0; i < kQpN / kQBlock; ++i) m |= (none >> (in * runs + i / bpr) & 1u) << i;
           bad_blocks[st] = m;
-          mbar_arrive_expect_tx(&raw_full[st], sum);
+          mbar_arrive_expect_tx(&raw_full[st], all);
         }
         __syncwarp();
-#pragma unroll 1
-        for (int i = 0; i < runs; ++i) {
-          const uint32_t n = __shfl_sync(0xffffffffu, bytes, i), to = __shfl_sync(0xffffffffu, dst, i);
-          const uint64_t from = __shfl_sync(0xffffffffu, src, i);
-          if (n && el)
-            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "l"(from),
-                         "r"(n), "r"(smem_u32(&raw_full[st]))
-                         : "memory");
-        }
+        if (lane / runs == in && bytes)
+          asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                           sb + S::kOffRaw + st * S::kRawTile + dst),
+                       "l"(src), "r"(bytes), "r"(smem_u32(&raw_full[st]))
+                       : "memory");
       }
       // every copy has landed before the CTA may end (also after a wait that gave up)
       for (int x = max(0, j - S::kRaw); x < j; ++x) mbar_wait(&raw_full[x % S::kRaw], (uint32_t)((x / S::kRaw) & 1), a.err);
@@ -428,49 +485,65 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
       for (int c = 0; c < kQpN / 32; ++c) tc_ld32(ts + 32 * c, s + 32 * c);
       tc_ld_wait();
       const int k0 = key_of(j);
+      bool blind = false;
       if (!qp_all_seen(a, k0, g_lo, g_hi)) {
         const unsigned long long sees = qp_sees(a, pos, k0);
+        blind = sees == 0;
         if (__any_sync(0xffffffffu, sees != ~0ull)) {
           const uint32_t half[2] = {(uint32_t)sees, (uint32_t)(sees >> 32)};
 #pragma unroll
           for (int c = 0; c < kQpN; ++c) s[c] = half[c >> 5] >> (c & 31) & 1u ? s[c] : 0xff800000u;
         }
       }
-      float mx[8];
+#pragma unroll 1
+      for (bool again = false;; again = true) {
+        const float off = ref == -INFINITY ? 0.f : -ref;
+        const float2 scale2 = make_float2(slog2, slog2), minus2 = make_float2(off, off);
+        float2 lp[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        uint32_t w[kQpN / 2];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) mx[c] = __uint_as_float(s[c]);
+        for (int e = 0; e < kQpN / 2; ++e) {
+          const float2 x = fma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), scale2, minus2);
+          const float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+          lp[e & 1] = add2(lp[e & 1], y);
+          w[e] = pack_half2(y.x, y.y);
+        }
+        const float sum = (lp[0].x + lp[1].x) + (lp[0].y + lp[1].y);
+        // (no weight is above 2^15 where their sum is not; at a second try it is by a NaN)
+        const bool out = !(sum <= kQpMost) || (ref == -INFINITY && !blind) || fabsf(off) >= kQpLarge;
+        if (again || !__any_sync(0xffffffffu, out)) {
+          tc_st32(ts, w);
+          l += sum;
+          break;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 8; c < kQpN; ++c) mx[c & 7] = fmaxf(mx[c & 7], __uint_as_float(s[c]));
-      const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * slog2;
-      const bool up = top > ref + (fabsf(top) < kQpLarge ? kQpShift + kQpSlack : kQpShift);
-      const float al = up ? fast_exp2(ref - (top - kQpShift)) : 1.f;
-      if (up) ref = top - kQpShift;
-      if (j > 0 && __any_sync(0xffffffffu, up)) {  // rescale O once O_{j-1} is done
-        if (ok) ok = mbar_wait(&o_done[2 * g + (buf ^ 1)], (uint32_t)(((j - 1) >> 1) & 1), a.err);
+        for (int c = 0; c < kQpN; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * slog2;
+        if (j > 0 && ok) ok = mbar_wait(&o_done[2 * g + (buf ^ 1)], (uint32_t)(((j - 1) >> 1) & 1), a.err);
         tc_fence_after();
+        if (__any_sync(0xffffffffu, fabsf(off) >= kQpLarge || (fabsf(top) >= kQpLarge && top > -INFINITY))) {
+          const float2 rl = large_tile<D>(blind ? 0ull : qp_sees(a, pos, k0), ts, to, slog2, ref, l, j > 0);
+          ref = rl.x;
+          l = rl.y;
+          break;
+        }
+        const bool up = top > ref + kQpShift;
+        const float al = up ? fast_exp2(ref - (top - kQpShift)) : 1.f;
+        if (up) ref = top - kQpShift;
+        l *= al;
+        if (j > 0 && __any_sync(0xffffffffu, up)) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tc_ld32(to + c, o);
+            tc_ld_wait();
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tc_ld32(to + 32 * c, o);
-          tc_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-          tc_st32(to + 32 * c, o);
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+            tc_st32(to + c, o);
+          }
         }
       }
-      const float off = ref == -INFINITY ? 0.f : -ref;
-      const float2 scale2 = make_float2(slog2, slog2), minus2 = make_float2(off, off);
-      float2 lp[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      uint32_t w[kQpN / 2];
-#pragma unroll
-      for (int e = 0; e < kQpN / 2; ++e) {
-        const float2 x = add2(mul2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), scale2), minus2);
-        const float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-        lp[e & 1] = add2(lp[e & 1], y);
-        w[e] = pack_half2(y.x, y.y);
-      }
-      tc_st32(ts, w);
-      l = fmaf(l, al, (lp[0].x + lp[1].x) + (lp[0].y + lp[1].y));
       tc_st_wait();
       tc_fence_before();
       mbar_arrive(&p_full[2 * g + buf]);
