@@ -10,7 +10,7 @@
 //   O_g += P_g V_j    M = 128, N = d, P from TMEM (fp16, over the first 32 columns of its S)
 //
 // Warps 0-7 hold a query row per thread: they bring Q to shared memory, and turn S into P.  Warp 8 streams the
-// tiles' bytes (bulk copies, one per page and tile) into a ring, warps 12-15 and 16-19 make fp16 values of K and of V:
+// tiles' bytes (bulk copies, one per page and tile) into a ring, warps 12-15 make fp16 values of them:
 // a group's values scale * code + bias are fp16 numbers exactly, so the tensor cores see the very values of the cache.
 // Warps 9 and 10 issue the products.  All operands are fp16; bf16 queries are brought into its range by a power of
 // two for each row, which goes into that row's factor of the scores (exact for values above 2^-24 of the largest).
@@ -29,7 +29,7 @@
 namespace dkv {
 namespace {
 
-constexpr int kQpThreads = 640, kQpM = 128, kQpN = 64;
+constexpr int kQpThreads = 512, kQpM = 128, kQpN = 64;
 constexpr float kQpShift = 7.f;
 constexpr float kQpLarge = 0x1p20f;  // scores (in base 2) whose rounding would show in the range
 constexpr float kQpMost = 0x1p15f;   // of a weight
@@ -113,11 +113,6 @@ __device__ inline QpRow qp_row(const QpArgs& p, int kvh, int h0, int row0, int n
 // natural log-sum-exp of a row's reference and sum (-inf for a row that sees no key)
 __device__ inline float qp_lse(float ref, float l) { return (ref + log2f(l)) * 0.6931471805599453f; }
 
-// every query at positions [p_lo, p_hi] sees every key of [k0, k0 + kQpN)
-__device__ inline bool qp_all_seen(const PagedArgs& a, int k0, int p_lo, int p_hi) {
-  return k0 + kQpN - 1 <= p_lo && (a.window == 0 || k0 > p_hi - a.window || k0 + kQpN <= a.sinks);
-}
-
 // bit c: the query at position pos sees key k0 + c
 __device__ inline unsigned long long qp_sees(const PagedArgs& a, int pos, int k0) {
   const int hi = pos - k0, lo = a.window ? pos - a.window + 1 - k0 : 0, sk = a.sinks - k0;
@@ -139,56 +134,57 @@ __device__ inline uint4 values8(uint32_t x, __half2 s, __half2 b) {
   return make_uint4(bits(__hfma2(c0, s, b)), bits(__hfma2(c1, s, b)), bits(__hfma2(c2, s, b)), bits(__hfma2(c3, s, b)));
 }
 
-// A tile with large scores, in the loop's place (rare, so in rolled loops): the reference, and with it O and the sum,
-// moved to kQpShift below its maximum where that is higher, and P from there.  Returns reference and sum.  A score is
-// rounded by its factor before the reference is taken off, as the maximum was: an fma would leave the rounding of the
-// maximum in the exponent, 2^-4 at kQpLarge but hundreds at 2^32.
+// The tiles that are not all seen, and those that move a row's reference: scores once more, the reference, and with it
+// O and the sum, moved to kQpShift below the maximum where that is higher, and P from there.  Returns reference and
+// sum.  In rolled loops, apart from the plain tiles' code: with this in it that loop does not stay in the
+// instruction cache, beside the other warps' (8k causal prompt 548 us, 470 without).  A score is rounded by its
+// factor before the reference is taken off, as the maximum was: an fma would leave the rounding of the maximum in
+// the exponent, 2^-4 at kQpLarge but hundreds at 2^32.
 template <int D>
-__device__ __noinline__ float2 large_tile(unsigned long long sees, uint32_t ts, uint32_t to, float slog2, float ref, float l, bool some) {
+__device__ __noinline__ float2 other_tile(unsigned long long sees, uint32_t ts, uint32_t to, float slog2, float ref, float l, bool some) {
   float top = -INFINITY;
 #pragma unroll 1
-  for (int c = 0; c < kQpN; c += 16) {
-    uint32_t s[16];
-    tc_ld16(ts + c, s);
+  for (int c = 0; c < kQpN; c += 32) {
+    const uint32_t bits = (uint32_t)(sees >> c);
+    uint32_t s[32];
+    tc_ld32(ts + c, s);
     tc_ld_wait();
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-      if (sees >> (c + e) & 1ull) top = fmaxf(top, __fmul_rn(__uint_as_float(s[e]), slog2));
+    for (int e = 0; e < 32; ++e) top = fmaxf(top, bits >> e & 1u ? __uint_as_float(s[e]) : -INFINITY);
   }
+  top = __fmul_rn(top, slog2);
   const bool up = top > ref + kQpShift;
   const float al = up ? fast_exp2(ref - (top - kQpShift)) : 1.f;
   if (up) ref = top - kQpShift;
   if (some && __any_sync(0xffffffffu, up)) {
 #pragma unroll 1
-    for (int c = 0; c < D; c += 16) {
-      uint32_t o[16];
-      tc_ld16(to + c, o);
+    for (int c = 0; c < D; c += 32) {
+      uint32_t o[32];
+      tc_ld32(to + c, o);
       tc_ld_wait();
 #pragma unroll
-      for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-      tc_st16(to + c, o);
+      for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+      tc_st32(to + c, o);
     }
   }
   const float off = ref == -INFINITY ? 0.f : -ref;
   l *= al;
 #pragma unroll 1
-  for (int c = 0; c < kQpN; c += 16) {  // (P's columns c / 2 .. c / 2 + 7 lie over scores that have been read)
-    uint32_t s[16], w[8];
-    tc_ld16(ts + c, s);
+  for (int c = 0; c < kQpN; c += 32) {  // (P's columns c / 2 .. c / 2 + 15 lie over scores that have been read)
+    const uint32_t bits = (uint32_t)(sees >> c);
+    uint32_t s[32], w[16];
+    tc_ld32(ts + c, s);
     tc_ld_wait();
+    float2 lp = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int e = 0; e < 16; e += 2) {
-      float y[2];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const float v = __uint_as_float(s[e + x]);
-        const float d = __fadd_rn(__fmul_rn(v, slog2), off);
-        y[x] = sees >> (c + e + x) & 1ull ? fast_exp2(d) : 0.f;
-        l += y[x];
-      }
-      w[e / 2] = pack_half2(y[0], y[1]);
+    for (int e = 0; e < 32; e += 2) {
+      const float2 x = add2(mul2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), make_float2(slog2, slog2)), make_float2(off, off));
+      const float2 y = make_float2(bits >> e & 1u ? fast_exp2(x.x) : 0.f, bits >> (e + 1) & 1u ? fast_exp2(x.y) : 0.f);
+      lp = add2(lp, y);
+      w[e / 2] = pack_half2(y.x, y.y);
     }
-    tc_st8(ts + c / 2, w);
+    tc_st16(ts + c / 2, w);
+    l += lp.x + lp.y;
   }
   return make_float2(ref, l);
 }
@@ -197,8 +193,9 @@ template <int N>
 __device__ inline void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ inline void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-// 96 registers for each of 640 threads at the start, and 2 x 144 + 64 + 2 x 64 = 5 x 96
-constexpr int kQpRegsRows = 144, kQpRegsIssue = 64, kQpRegsValues = 64;
+// 128 registers for each of 512 threads at the start, and 2 x 168 + 80 + 96 = 4 x 128.  (Two warpgroups for the values
+// leave 144 to the rows, whose loop then takes 1.15 times as long.)
+constexpr int kQpRegsRows = 168, kQpRegsIssue = 80, kQpRegsValues = 96;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p) {
@@ -251,11 +248,11 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
     }
     for (int i = 0; i < S::kRaw; ++i) {
       mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], 8);
+      mbar_init(&raw_empty[i], 4);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], kQpM);
+      mbar_init(&p_full[i], 4);  // a lane of each warp
       mbar_init(&o_done[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -272,43 +269,47 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
   bool ok = true;
 
   if (warp >= 12) {
-    // =========================== values, of K or of V: a thread makes half of a token's channels
+    // =========================== values: a thread makes half of a token's channels, of K and then of V
     regs_dec<kQpRegsValues>();
-    const int kv = warp >= 16, tid = (threadIdx.x - 12 * 32) & 127, tok = tid & 63, half = tid >> 6;
+    const int tid = threadIdx.x - 12 * 32, tok = tid & 63, half = tid >> 6;
     constexpr int kWords = D / 16;  // of eight codes
-    // bytes of this thread's parameters and codes in a tile's bytes, and of its values in a tile
+    // bytes of this thread's parameters and codes (of K) in a tile's bytes
     const int g = D == 128 ? half : 0;
     const uint32_t block = sb + S::kOffRaw + (uint32_t)(tok / kQBlock) * qblock_bytes(D);
-    const uint32_t param = block + (uint32_t)((16 + kv) * D + (tok % kQBlock * (D / 64) + g) * 4);
-    const uint32_t codes = block + (uint32_t)(kv * 8 * D + (g * kQBlock + tok % kQBlock) * 32 + (D == 128 ? 0 : 16 * half));
-    const uint32_t tiles = sb + (kv ? S::kOffV : S::kOffK);
-    uint64_t* const done = kv ? v_full : k_full;
+    const uint32_t param = block + (uint32_t)qparam_off(D, 0, g, tok % kQBlock);
+    const uint32_t codes = block + (uint32_t)qcode_off(D, 0, g, tok % kQBlock) + (D == 128 ? 0 : 16 * half);
+    const uint32_t row = sb + S::kOffK + sw128(kQpN, tok, half * kWords);  // 16-byte piece c of it is at row ^ 16 c
     int sl = 0, rs = 0;
     uint32_t ph = 0, rph = 0;
     for (int j = 0; j < nt; ++j) {
       if (ok) ok = mbar_wait(&raw_full[rs], rph, a.err);
       const int t = key_of(j) + tok;
       const bool zero = !(t < ks.hi && (t >= ks.lo || t < a.sinks)) || (bad_blocks[rs] >> (tok / kQBlock) & 1u);
-      uint32_t sbits = lds32(param + rs * S::kRawTile);
-      uint4 c[kWords / 4];
+      uint32_t sbits[2];
+      uint4 c[2][kWords / 4];
 #pragma unroll
-      for (int x = 0; x < kWords / 4; ++x) c[x] = lds128(codes + rs * S::kRawTile + 16 * x);
-      if (zero) sbits = 0u;
-      const __half2 sbh = *reinterpret_cast<__half2*>(&sbits), s2 = __low2half2(sbh), b2 = __high2half2(sbh);
+      for (int kv = 0; kv < 2; ++kv) {
+        sbits[kv] = lds32(param + rs * S::kRawTile + kv * D);
+#pragma unroll
+        for (int x = 0; x < kWords / 4; ++x) c[kv][x] = lds128(codes + rs * S::kRawTile + kv * 8 * D + 16 * x);
+      }
       if (ok && j >= S::kR) ok = mbar_wait(&empty[sl], ph ^ 1u, a.err);
-      const uint32_t to = tiles + sl * S::kTile;
 #pragma unroll
-      for (int x = 0; x < kWords / 4; ++x) {
-        const uint32_t w[4] = {c[x].x, c[x].y, c[x].z, c[x].w};
+      for (int kv = 0; kv < 2; ++kv) {
+        if (zero) sbits[kv] = 0u;
+        const __half2 sbh = *reinterpret_cast<__half2*>(&sbits[kv]), s2 = __low2half2(sbh), b2 = __high2half2(sbh);
+        const uint32_t to = row + kv * (S::kOffV - S::kOffK) + sl * S::kTile;
 #pragma unroll
-        for (int y = 0; y < 4; ++y) sts128(to + sw128(kQpN, tok, half * kWords + 4 * x + y), values8(w[y], s2, b2));
+        for (int x = 0; x < kWords / 4; ++x) {
+          const uint32_t w[4] = {c[kv][x].x, c[kv][x].y, c[kv][x].z, c[kv][x].w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) sts128(to ^ (16 * (4 * x + y)), values8(w[y], s2, b2));
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(kv ? &v_full[sl] : &k_full[sl]);
       }
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&done[sl]);
-        mbar_arrive(&raw_empty[rs]);
-      }
+      if (lane == 0) mbar_arrive(&raw_empty[rs]);
       if (++sl == S::kR) { sl = 0; ph ^= 1u; }
       if (++rs == S::kRaw) { rs = 0; rph ^= 1u; }
     }
@@ -471,8 +472,12 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[g]);
     }
-    // positions of the group's rows (the tile is unmasked when all of them see all of it)
+    // tiles [plain, edges) are seen whole by all of the group's rows
     const int g_lo = p.by_heads ? p_lo : p_lo + g * kQpM, g_hi = g_lo + (g ? tokB : tokA) - 1;
+    const int first_tile = ks.wt0 - ks.st + t0;  // of the window's tiles, tile j holds keys from 64 (first_tile + j) on
+    const int plain = max(a.window ? ((max(0, g_hi - a.window + 1) + kQpN - 1) / kQpN) - first_tile : -first_tile, ks.st - t0);
+    const int edges = ((g_lo + 1) >> 6) - first_tile;
+    static_assert(kQpN == 64, "a shift by 6");
     const uint32_t tg = tmem + ((uint32_t)(32 * rw) << 16) + 256u * g, to = tg + 128u;
     float ref = -INFINITY, l = 0.f;
     for (int j = 0; j < n; ++j) {
@@ -480,25 +485,13 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
       const uint32_t ts = tg + kQpN * buf;
       if (ok) ok = mbar_wait(&s_full[2 * g + buf], (uint32_t)((j >> 1) & 1), a.err);
       tc_fence_after();
-      uint32_t s[kQpN];
+      bool other = j < plain || j >= edges;
+      if (!other) {
+        uint32_t s[kQpN];
 #pragma unroll
-      for (int c = 0; c < kQpN / 32; ++c) tc_ld32(ts + 32 * c, s + 32 * c);
-      tc_ld_wait();
-      const int k0 = key_of(j);
-      bool blind = false;
-      if (!qp_all_seen(a, k0, g_lo, g_hi)) {
-        const unsigned long long sees = qp_sees(a, pos, k0);
-        blind = sees == 0;
-        if (__any_sync(0xffffffffu, sees != ~0ull)) {
-          const uint32_t half[2] = {(uint32_t)sees, (uint32_t)(sees >> 32)};
-#pragma unroll
-          for (int c = 0; c < kQpN; ++c) s[c] = half[c >> 5] >> (c & 31) & 1u ? s[c] : 0xff800000u;
-        }
-      }
-#pragma unroll 1
-      for (bool again = false;; again = true) {
-        const float off = ref == -INFINITY ? 0.f : -ref;
-        const float2 scale2 = make_float2(slog2, slog2), minus2 = make_float2(off, off);
+        for (int c = 0; c < kQpN / 32; ++c) tc_ld32(ts + 32 * c, s + 32 * c);
+        tc_ld_wait();
+        const float2 scale2 = make_float2(slog2, slog2), minus2 = make_float2(-ref, -ref);
         float2 lp[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         uint32_t w[kQpN / 2];
 #pragma unroll
@@ -509,44 +502,24 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
           w[e] = pack_half2(y.x, y.y);
         }
         const float sum = (lp[0].x + lp[1].x) + (lp[0].y + lp[1].y);
-        // (no weight is above 2^15 where their sum is not; at a second try it is by a NaN)
-        const bool out = !(sum <= kQpMost) || (ref == -INFINITY && !blind) || fabsf(off) >= kQpLarge;
-        if (again || !__any_sync(0xffffffffu, out)) {
+        // no weight is above 2^15 where their sum is not (without a reference x, and so the sum, is infinite or NaN)
+        other = __any_sync(0xffffffffu, !(sum <= kQpMost) || !(fabsf(ref) < kQpLarge));
+        if (!other) {
           tc_st32(ts, w);
           l += sum;
-          break;
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < kQpN; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * slog2;
+      }
+      if (other) {
         if (j > 0 && ok) ok = mbar_wait(&o_done[2 * g + (buf ^ 1)], (uint32_t)(((j - 1) >> 1) & 1), a.err);
         tc_fence_after();
-        if (__any_sync(0xffffffffu, fabsf(off) >= kQpLarge || (fabsf(top) >= kQpLarge && top > -INFINITY))) {
-          const float2 rl = large_tile<D>(blind ? 0ull : qp_sees(a, pos, k0), ts, to, slog2, ref, l, j > 0);
-          ref = rl.x;
-          l = rl.y;
-          break;
-        }
-        const bool up = top > ref + kQpShift;
-        const float al = up ? fast_exp2(ref - (top - kQpShift)) : 1.f;
-        if (up) ref = top - kQpShift;
-        l *= al;
-        if (j > 0 && __any_sync(0xffffffffu, up)) {
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tc_ld32(to + c, o);
-            tc_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-            tc_st32(to + c, o);
-          }
-        }
+        const float2 rl = other_tile<D>(qp_sees(a, pos, key_of(j)), ts, to, slog2, ref, l, j > 0);
+        ref = rl.x;
+        l = rl.y;
       }
       tc_st_wait();
       tc_fence_before();
-      mbar_arrive(&p_full[2 * g + buf]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[2 * g + buf]);
     }
     if (n > 0 && ok) ok = mbar_wait(&o_done[2 * g + ((n - 1) & 1)], (uint32_t)(((n - 1) >> 1) & 1), a.err);
     tc_fence_after();
