@@ -189,6 +189,12 @@ __device__ __noinline__ float2 other_tile(unsigned long long sees, uint32_t ts, 
   return make_float2(ref, l);
 }
 
+// an arrival without a branch around it
+__device__ inline void mbar_arrive_if(uint64_t* bar, bool x) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)), "r"((uint32_t)x)
+               : "memory");
+}
+
 template <int N>
 __device__ inline void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -227,24 +233,22 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
   auto key_of = [&](int j) { return ks.key(t0 + j); };  // first key of tile j
 
   const uint32_t sb = smem_u32(smem);
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + S::kOffBar);  // [slot]
-  uint64_t* v_full = k_full + S::kR;     // [slot]
-  uint64_t* empty = v_full + S::kR;      // [slot] O_j, and so S_j, of both groups are done
-  uint64_t* raw_full = empty + S::kR;    // [stage]
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + S::kOffBar);  // [slot]
+  uint64_t* o_done = kv_full + S::kR;    // [group][slot] O_j, and so S_j, is done
+  uint64_t* raw_full = o_done + 2 * S::kR;  // [stage]
   uint64_t* raw_empty = raw_full + S::kRaw;
   uint64_t* q_full = raw_empty + S::kRaw;  // [group]
   uint64_t* s_full = q_full + 2;         // [group][buffer]
   uint64_t* p_full = s_full + 4;         // [group][buffer]
-  uint64_t* o_done = p_full + 4;         // [group][buffer]
-  uint64_t* drain = o_done + 4;          // [group] after a wait that gave up
+  uint64_t* drain = p_full + 4;          // [group] after a wait that gave up
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile uint32_t* bad_blocks = tmem_slot + 1;  // [stage] blocks on bad pages
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kR; ++i) {
-      mbar_init(&k_full[i], 4);  // a lane of each warp that makes values
-      mbar_init(&v_full[i], 4);
-      mbar_init(&empty[i], 2);  // one commit per group
+      mbar_init(&kv_full[i], 4);  // a lane of each warp that makes values
+      mbar_init(&o_done[i], 1);
+      mbar_init(&o_done[S::kR + i], 1);
     }
     for (int i = 0; i < S::kRaw; ++i) {
       mbar_init(&raw_full[i], 1);
@@ -253,7 +257,6 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);  // a lane of each warp
-      mbar_init(&o_done[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 4);
@@ -293,7 +296,8 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
 #pragma unroll
         for (int x = 0; x < kWords / 4; ++x) c[kv][x] = lds128(codes + rs * S::kRawTile + kv * 8 * D + 16 * x);
       }
-      if (ok && j >= S::kR) ok = mbar_wait(&empty[sl], ph ^ 1u, a.err);
+      if (ok && j >= S::kR && j - S::kR < nA) ok = mbar_wait(&o_done[sl], ph ^ 1u, a.err);
+      if (ok && j >= S::kR && j - S::kR < nB) ok = mbar_wait(&o_done[S::kR + sl], ph ^ 1u, a.err);
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         if (zero) sbits[kv] = 0u;
@@ -305,11 +309,11 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
 #pragma unroll
           for (int y = 0; y < 4; ++y) sts128(to ^ (16 * (4 * x + y)), values8(w[y], s2, b2));
         }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(kv ? &v_full[sl] : &k_full[sl]);
       }
-      if (lane == 0) mbar_arrive(&raw_empty[rs]);
+      fence_proxy_async();
+      __syncwarp();
+      mbar_arrive_if(&kv_full[sl], lane == 0);
+      mbar_arrive_if(&raw_empty[rs], lane == 0);
       if (++sl == S::kR) { sl = 0; ph ^= 1u; }
       if (++rs == S::kRaw) { rs = 0; rph ^= 1u; }
     }
@@ -373,50 +377,42 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
       // operands are not known to be uniform, and an issue took 75 to 150 cycles.
       constexpr uint32_t id_s = tc_idesc(Num<__half>::kUmma, false, kQpN), id_o = tc_idesc(Num<__half>::kUmma, true, D);
       const uint32_t el = elect_one();
-      const int g = warp - 9, n = g ? nB : nA, n_other = g ? nA : nB;
+      const int g = warp - 9, n = g ? nB : nA;
       const uint32_t tg = tmem + 256u * g;
       const uint64_t qd = tc_desc(sb + g * S::kQ, 16, 1024);
       uint64_t* const sf = s_full + 2 * g;
       uint64_t* const pf = p_full + 2 * g;
-      uint64_t* const od = o_done + 2 * g;
+      uint64_t* const od = o_done + S::kR * g;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (ok) ok = mbar_wait(bar, parity, a.err);
         __syncwarp();
       };
-      int k_sl = 0, v_sl = 0;             // slots of the next K and V tile
-      uint32_t k_ph = 0, v_ph = 0;        // and their phases
       auto scores = [&](int j) {
-        const int buf = j & 1;
-        wait(&k_full[k_sl], k_ph);
-        if (j >= 2) wait(&od[buf], (uint32_t)((j - 2) >> 1) & 1u);  // the buffer holds P_{j-2}
+        const int buf = j & 1, sl = j % S::kR;
+        wait(&kv_full[sl], (uint32_t)(j / S::kR) & 1u);
+        if (j >= 2) wait(&od[(j - 2) % S::kR], (uint32_t)((j - 2) / S::kR) & 1u);  // the buffer holds P_{j-2}
         tc_fence_after();
-        const uint64_t kd = tc_desc(sb + S::kOffK + k_sl * S::kTile, 16, 1024);
+        const uint64_t kd = tc_desc(sb + S::kOffK + sl * S::kTile, 16, 1024);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)  // 16 channels: 32 bytes of a 128-byte row, then the next 64 channels
           tc_mma(tg + kQpN * buf, qd + (uint64_t)(((k >> 2) * kQpM * 128 + (k & 3) * 32) >> 4),
                  kd + (uint64_t)(((k >> 2) * kQpN * 128 + (k & 3) * 32) >> 4), id_s, k > 0, el);
         tc_commit(&sf[buf], el);
-        if (++k_sl == S::kR) { k_sl = 0; k_ph ^= 1u; }
       };
       if (n > 0) {
         wait(&q_full[g], 0);
         scores(0);
         for (int j = 0; j < n; ++j) {
           if (j + 1 < n) scores(j + 1);
-          const int buf = j & 1;
-          wait(&v_full[v_sl], v_ph);
+          const int buf = j & 1, sl = j % S::kR;
           wait(&pf[buf], (uint32_t)(j >> 1) & 1u);
           tc_fence_after();
-          const uint64_t vd = tc_desc(sb + S::kOffV + v_sl * S::kTile, kQpN * 128, 1024);
+          const uint64_t vd = tc_desc(sb + S::kOffV + sl * S::kTile, kQpN * 128, 1024);
           const uint32_t ts = tg + kQpN * buf;
 #pragma unroll
           for (int k = 0; k < kQpN / 16; ++k)  // 16 keys: 16 rows of 128 bytes
             tc_mma_ta(tg + 128u, ts + 8u * k, vd + (uint64_t)(k * 16 * 128 >> 4), id_o, k > 0 ? 1u : (j > 0 ? 1u : 0u), el);
-          tc_commit(&od[buf], el);
-          // once for this group, once more where the other has no tile j
-          tc_commit(&empty[v_sl], el);
-          if (j >= n_other) tc_commit(&empty[v_sl], el);
-          if (++v_sl == S::kR) { v_sl = 0; v_ph ^= 1u; }
+          tc_commit(&od[sl], el);
         }
       }
       if (!__all_sync(0xffffffffu, ok)) {  // a wait gave up, and the rows may have too: no product outlives the CTA
@@ -510,7 +506,7 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
         }
       }
       if (other) {
-        if (j > 0 && ok) ok = mbar_wait(&o_done[2 * g + (buf ^ 1)], (uint32_t)(((j - 1) >> 1) & 1), a.err);
+        if (j > 0 && ok) ok = mbar_wait(&o_done[S::kR * g + (j - 1) % S::kR], (uint32_t)((j - 1) / S::kR) & 1u, a.err);
         tc_fence_after();
         const float2 rl = other_tile<D>(qp_sees(a, pos, key_of(j)), ts, to, slog2, ref, l, j > 0);
         ref = rl.x;
@@ -519,9 +515,9 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
       tc_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[2 * g + buf]);
+      mbar_arrive_if(&p_full[2 * g + buf], lane == 0);
     }
-    if (n > 0 && ok) ok = mbar_wait(&o_done[2 * g + ((n - 1) & 1)], (uint32_t)(((n - 1) >> 1) & 1), a.err);
+    if (n > 0 && ok) ok = mbar_wait(&o_done[S::kR * g + (n - 1) % S::kR], (uint32_t)((n - 1) / S::kR) & 1u, a.err);
     tc_fence_after();
     const bool live = me.live;
     const float il = n == 0 || l == 0.f ? 0.f : 1.f / l;  // a row that sees no key: zeros
