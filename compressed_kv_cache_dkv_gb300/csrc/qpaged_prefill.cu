@@ -288,24 +288,21 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
       if (ok) ok = mbar_wait(&raw_full[rs], rph, a.err);
       const int t = key_of(j) + tok;
       const bool zero = !(t < ks.hi && (t >= ks.lo || t < a.sinks)) || (bad_blocks[rs] >> (tok / kQBlock) & 1u);
-      uint32_t sbits[2];
-      uint4 c[2][kWords / 4];
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        sbits[kv] = lds32(param + rs * S::kRawTile + kv * D);
-#pragma unroll
-        for (int x = 0; x < kWords / 4; ++x) c[kv][x] = lds128(codes + rs * S::kRawTile + kv * 8 * D + 16 * x);
-      }
+      // (rolled: K's and V's code is the same, and short code stays in the instruction cache)
       if (ok && j >= S::kR && j - S::kR < nA) ok = mbar_wait(&o_done[sl], ph ^ 1u, a.err);
       if (ok && j >= S::kR && j - S::kR < nB) ok = mbar_wait(&o_done[S::kR + sl], ph ^ 1u, a.err);
-#pragma unroll
+#pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
-        if (zero) sbits[kv] = 0u;
-        const __half2 sbh = *reinterpret_cast<__half2*>(&sbits[kv]), s2 = __low2half2(sbh), b2 = __high2half2(sbh);
+        uint32_t sbits = lds32(param + rs * S::kRawTile + kv * D);
+        uint4 c[kWords / 4];
+#pragma unroll
+        for (int x = 0; x < kWords / 4; ++x) c[x] = lds128(codes + rs * S::kRawTile + kv * 8 * D + 16 * x);
+        if (zero) sbits = 0u;
+        const __half2 sbh = *reinterpret_cast<__half2*>(&sbits), s2 = __low2half2(sbh), b2 = __high2half2(sbh);
         const uint32_t to = row + kv * (S::kOffV - S::kOffK) + sl * S::kTile;
 #pragma unroll
         for (int x = 0; x < kWords / 4; ++x) {
-          const uint32_t w[4] = {c[kv][x].x, c[kv][x].y, c[kv][x].z, c[kv][x].w};
+          const uint32_t w[4] = {c[x].x, c[x].y, c[x].z, c[x].w};
 #pragma unroll
           for (int y = 0; y < 4; ++y) sts128(to ^ (16 * (4 * x + y)), values8(w[y], s2, b2));
         }
