@@ -7,9 +7,12 @@
 // A turn is taken as a 64-bit fraction of the circle: position * turn_j modulo 2^64 is exact however far the
 // position is, its upper 32 bits are the angle to 2^-32 of a circle, and sincospif takes it from there.
 //
-// d / 8 lanes share a row, eight channels (16 bytes) each; the partner channels of the rotation are a fixed
-// number of lanes away.  A warp keeps the cosines and sines of its token and walks the heads, kRotDepth
-// loads in flight.  Bound by memory: 4 d bytes a head, 6 d for a key that also goes into a page.
+// d / 8 lanes share a row, eight channels (16 bytes) each; the partner channels of the rotation are a fixed number of
+// lanes away, and come over as they were loaded.  Gains are folded into the cosines and sines, the norm's factor
+// into the last product.  A warp keeps these of its token and walks the heads in rounds of kRotDepth rows for each of
+// its row groups, the next round's rows on their way meanwhile.  Bound by memory: 4 d bytes a head, 6 d for a key that
+// also goes into a page.
+#include "paged_tc.cuh"
 #include "qpaged.cuh"
 
 namespace dkv {
@@ -17,15 +20,12 @@ namespace {
 
 constexpr int kRotThreads = 256, kRotDepth = 4;
 
+// channels 2 i, 2 i + 1 of a piece
 template <typename T>
-__device__ inline void load8(const uint4& v, float (&x)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const T* h = reinterpret_cast<const T*>(&w[i]);
-    x[2 * i] = Num<T>::to_float(h[0]);
-    x[2 * i + 1] = Num<T>::to_float(h[1]);
-  }
+__device__ inline float2 pair_of(const uint4& v, int i) {
+  const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+  const T* h = reinterpret_cast<const T*>(&w);
+  return make_float2(Num<T>::to_float(h[0]), Num<T>::to_float(h[1]));
 }
 
 template <typename T, int D>
@@ -37,7 +37,6 @@ __global__ void __launch_bounds__(kRotThreads) qk_norm_rope_kernel(const __grid_
   if (tok >= a.rows) return;
   const int pos = __ldg(a.positions + tok);
   if (pos < 0) return;  // a row of padding
-  const int heads = a.hq + a.hkv + (a.v ? a.hkv : 0);  // queries, keys, values to copy
   // where the token's key and value go
   int64_t page_at = -1;
   if (a.slots) {
@@ -45,72 +44,111 @@ __global__ void __launch_bounds__(kRotThreads) qk_norm_rope_kernel(const __grid_
     if (slot >= 0 && slot < a.n_slots) page_at = (slot >> a.page_shift) * a.stride_page + (slot & a.page_mask) * a.stride_token;
     else if (slot != -1 && lane == 0) raise_error(a.err, DKV_DEVERR_INDEX);
   }
-  float cs[8], sn[8];
+  // rounds of queries, of keys and of values to copy; this warp takes every parts-th
+  const int nq = (a.hq + kStep - 1) / kStep, nk = (a.hkv + kStep - 1) / kStep, rounds = nq + nk + (page_at >= 0 ? nk : 0);
+  struct Round {
+    uint4 v[kRotDepth];
+  };
+  auto fetch = [&](int r) {
+    Round x;
+    const int kind = r < nq ? 0 : r < nq + nk ? 1 : 2, heads = kind ? a.hkv : a.hq;
+    const T* src = static_cast<const T*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v);
+    const int64_t* st = kind == 0 ? a.qs : kind == 1 ? a.ks : a.vs;
+    const int h0 = (r - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * kStep + sub;
+    const T* at = src + tok * st[0] + h0 * st[1] + 8 * li;
+#pragma unroll
+    for (int i = 0; i < kRotDepth; ++i) {
+      x.v[i] = make_uint4(0, 0, 0, 0);
+      if (r < rounds && h0 + i * RPW < heads) x.v[i] = *reinterpret_cast<const uint4*>(at + (int64_t)(i * RPW) * st[1]);
+    }
+    return x;
+  };
+  int r = (int)(w % parts);
+  Round next = fetch(r);
+
   const int hl = a.half / 8;  // lanes of the first half
   const bool turns = li < 2 * hl;
-  const int partner = lane - li + (li < hl ? li + hl : turns ? li - hl : li);
+  const int other = li < hl ? li + hl : turns ? li - hl : li, partner = lane - li + other;
+  float cs[8], sn[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     cs[e] = 1.f;
     sn[e] = 0.f;
     if (!turns) continue;
-    const uint64_t f = (uint64_t)pos * a.turn[(8 * li + e) % a.half];
+    const uint64_t f = (uint64_t)pos * a.turn[(li < hl ? 8 * li : 8 * (li - hl)) + e];
     sincospif((float)(int32_t)(f >> 32) * 0x1p-31f, &sn[e], &cs[e]);
     if (li < hl) sn[e] = -sn[e];
   }
-  float qg[8], kg[8];
+  float2 A[4], B[4];  // of a row's channels, and of their partners
+  int have = -1;
+  for (; r < rounds; r += parts) {
+    const Round cur = next;
+    next = fetch(r + parts);
+    const int kind = r < nq ? 0 : r < nq + nk ? 1 : 2, heads = kind ? a.hkv : a.hq;
+    const int h0 = (r - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * kStep + sub;
+    if (kind == 2) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) qg[e] = kg[e] = 1.f;
-  if (a.q_gain) load8<T>(__ldg(static_cast<const uint4*>(a.q_gain) + li), qg);
-  if (a.k_gain) load8<T>(__ldg(static_cast<const uint4*>(a.k_gain) + li), kg);
-
-  for (int r0 = (int)(w % parts) * kStep; r0 < heads; r0 += parts * kStep) {
-    uint4 in[kRotDepth];
-#pragma unroll
-    for (int x = 0; x < kRotDepth; ++x) {
-      const int r = r0 + x * RPW + sub;
-      in[x] = make_uint4(0, 0, 0, 0);
-      if (r >= heads) continue;
-      const bool isq = r < a.hq, isk = r < a.hq + a.hkv;
-      const int h = isq ? r : isk ? r - a.hq : r - a.hq - a.hkv;
-      const T* src = static_cast<const T*>(isq ? a.q : isk ? a.k : a.v);
-      const int64_t st = isq ? a.qs[0] : isk ? a.ks[0] : a.vs[0], sh = isq ? a.qs[1] : isk ? a.ks[1] : a.vs[1];
-      in[x] = *reinterpret_cast<const uint4*>(src + tok * st + h * sh + 8 * li);
+      for (int i = 0; i < kRotDepth; ++i)
+        if (h0 + i * RPW < heads)
+          *reinterpret_cast<uint4*>(static_cast<T*>(a.v_pool) + page_at + (h0 + i * RPW) * a.stride_head + 8 * li) = cur.v[i];
+      continue;
     }
+    if (have != kind) {
+      have = kind;
+      const uint4* gain = static_cast<const uint4*>(kind ? a.k_gain : a.q_gain);
+      uint4 g = make_uint4(0, 0, 0, 0), go = g;
+      if (gain) {
+        g = __ldg(gain + li);
+        go = __ldg(gain + other);
+      }
 #pragma unroll
-    for (int x = 0; x < kRotDepth; ++x) {
-      const int r = r0 + x * RPW + sub;
-      const bool isq = r < a.hq, isk = r < a.hq + a.hkv;
-      float y[8];
-      load8<T>(in[x], y);
+      for (int e = 0; e < 4; ++e) {
+        A[e] = make_float2(cs[2 * e], cs[2 * e + 1]);
+        B[e] = make_float2(sn[2 * e], sn[2 * e + 1]);
+        if (gain) {
+          A[e] = mul2(A[e], pair_of<T>(g, e));
+          B[e] = mul2(B[e], pair_of<T>(go, e));
+        }
+      }
+    }
+    T* const out = static_cast<T*>(kind ? a.k_out : a.q_out);
+    const int64_t* st = kind ? a.kos : a.qos;
+    T* const at = out + tok * st[0] + h0 * st[1] + 8 * li;
+#pragma unroll
+    for (int i = 0; i < kRotDepth; ++i) {
+      float2 y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = pair_of<T>(cur.v[i], e);
+      float inv = 1.f;
       if (a.norm) {
-        float s = 0.f;
+        float2 s2 = mul2(y[0], y[0]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s = fmaf(y[e], y[e], s);
+        for (int e = 1; e < 4; ++e) s2 = fma2(y[e], y[e], s2);
+        float s = s2.x + s2.y;
 #pragma unroll
         for (int o = 1; o < L; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        const float inv = rsqrtf(s * (1.f / D) + a.eps);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] *= inv;
+        inv = rsqrtf(fmaf(s, 1.f / D, a.eps));
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] *= isq ? qg[e] : kg[e];
-      float o[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float z = __shfl_sync(0xffffffffu, y[e], partner);
-        o[e] = turns ? fmaf(z, sn[e], y[e] * cs[e]) : y[e];
+      uint4 z = cur.v[i];
+      if (a.half) {
+        z.x = __shfl_sync(0xffffffffu, z.x, partner);
+        z.y = __shfl_sync(0xffffffffu, z.y, partner);
+        z.z = __shfl_sync(0xffffffffu, z.z, partner);
+        z.w = __shfl_sync(0xffffffffu, z.w, partner);
       }
-      if (r >= heads) continue;
-      const uint4 out = make_uint4(Num<T>::pack(o[0], o[1]), Num<T>::pack(o[2], o[3]), Num<T>::pack(o[4], o[5]), Num<T>::pack(o[6], o[7]));
-      if (isq) {
-        *reinterpret_cast<uint4*>(static_cast<T*>(a.q_out) + tok * a.qos[0] + r * a.qos[1] + 8 * li) = out;
-      } else {
-        const int h = isk ? r - a.hq : r - a.hq - a.hkv;
-        if (isk && a.k_out) *reinterpret_cast<uint4*>(static_cast<T*>(a.k_out) + tok * a.kos[0] + h * a.kos[1] + 8 * li) = out;
-        if (page_at >= 0)
-          *reinterpret_cast<uint4*>(static_cast<T*>(isk ? a.k_pool : a.v_pool) + page_at + h * a.stride_head + 8 * li) = isk ? out : in[x];
+      if (h0 + i * RPW >= heads) continue;
+      uint32_t o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float2 x = mul2(y[e], A[e]);
+        if (turns) x = fma2(pair_of<T>(z, e), B[e], x);  // (a channel that does not turn takes nothing of an infinite one)
+        x = mul2(x, make_float2(inv, inv));
+        o[e] = Num<T>::pack(x.x, x.y);
       }
+      const uint4 res = make_uint4(o[0], o[1], o[2], o[3]);
+      if (out) *reinterpret_cast<uint4*>(at + (int64_t)(i * RPW) * st[1]) = res;
+      if (kind && page_at >= 0)
+        *reinterpret_cast<uint4*>(static_cast<T*>(a.k_pool) + page_at + (h0 + i * RPW) * a.stride_head + 8 * li) = res;
     }
   }
 }
@@ -119,7 +157,7 @@ __global__ void __launch_bounds__(kRotThreads) qk_norm_rope_kernel(const __grid_
 
 cudaError_t launch_qk_norm_rope(const RotateArgs& a, int d, int dtype, cudaStream_t s) {
   // Warps of a token: each makes the token's cosines again, so one where the tokens alone fill the GPU.
-  const int heads = a.hq + a.hkv + (a.v ? a.hkv : 0), step = 32 / (d / 8) * kRotDepth, rounds = (heads + step - 1) / step;
+  const int step = 32 / (d / 8) * kRotDepth, nk = (a.hkv + step - 1) / step, rounds = (a.hq + step - 1) / step + (a.v ? 2 : 1) * nk;
   const int64_t want = (int64_t)sm_count() * 32;
   int parts = (int)(a.rows >= want ? 1 : (want + a.rows - 1) / a.rows);
   if (parts > rounds) parts = rounds;

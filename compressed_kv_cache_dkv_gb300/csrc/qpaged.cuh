@@ -18,6 +18,20 @@ __host__ __device__ constexpr int qparam_off(int d, int kv, int g, int tok) {
   return (16 + kv) * d + (tok * (d / 64) + g) * 4;
 }
 
+// Eight codes as values, in the order 0 4 1 5 2 6 3 7.  1024 + code and 1024 + 16 code are the halves whose low
+// bits are the code's; every step is exact.
+__device__ inline uint4 qvalues8(uint32_t x, __half2 s, __half2 b) {
+  const uint32_t y = x >> 8;
+  auto half2_of = [](uint32_t w) { return *reinterpret_cast<__half2*>(&w); };
+  auto bits = [](__half2 h) { return *reinterpret_cast<uint32_t*>(&h); };
+  const __half2 base = half2_of(0x64006400u), sixteenth = half2_of(0x2c002c00u), minus64 = half2_of(0xd400d400u);
+  const __half2 c0 = __hsub2(half2_of((x & 0x000f000fu) | 0x64006400u), base);
+  const __half2 c1 = __hfma2(half2_of((x & 0x00f000f0u) | 0x64006400u), sixteenth, minus64);
+  const __half2 c2 = __hsub2(half2_of((y & 0x000f000fu) | 0x64006400u), base);
+  const __half2 c3 = __hfma2(half2_of((y & 0x00f000f0u) | 0x64006400u), sixteenth, minus64);
+  return make_uint4(bits(__hfma2(c0, s, b)), bits(__hfma2(c1, s, b)), bits(__hfma2(c2, s, b)), bits(__hfma2(c3, s, b)));
+}
+
 // In the kernels below PagedArgs holds the strides of a page and of a head in bytes.
 cudaError_t launch_qpaged_append(const PagedArgs& a, int d, int dtype, const void* K, const void* V,
                                  const dkv_strides& ns, int n_rows, const int64_t* slots, uint8_t* cache, cudaStream_t s);

@@ -14,110 +14,190 @@
 namespace dkv {
 namespace {
 
-constexpr int kQaThreads = 256, kQaVec = 4;
+constexpr int kQaThreads = 256, kQaVec = 2;
 constexpr float kQaMost = 61440.f;  // above it lo + 15 step could leave fp16
 
 __device__ inline float2 unpack2(uint32_t x, __half) { return __half22float2(*reinterpret_cast<__half2*>(&x)); }
 __device__ inline float2 unpack2(uint32_t x, __nv_bfloat16) {
   return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
 }
+// the smaller of two pairs, a NaN where either is one
+__device__ inline uint32_t min2(uint32_t x, uint32_t y, __half) {
+  const __half2 r = __hmin2_nan(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<__half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ inline uint32_t min2(uint32_t x, uint32_t y, __nv_bfloat16) {
+  const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<__nv_bfloat162*>(&x), *reinterpret_cast<__nv_bfloat162*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 
-// A lane's eight channels of a group: the word of codes, and the group's (scale, bias) as two halves.
-// `odd`: a value was not finite or too large.
+// The grid of a group between lo and hi.
+struct Grid {
+  float u, b, st;  // spacing; bias and step in its units
+};
+__device__ inline Grid grid_of(float lo, float hi) {
+  const float top = fmaxf(fabsf(lo), fabsf(hi)) * 1.015625f;
+  const int e = max((int)(__float_as_uint(top) >> 23) - 127 - 10, -24);  // u = 2^e
+  const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+  Grid g;
+  g.u = __uint_as_float((uint32_t)(127 + e) << 23);
+  g.b = rintf(lo * inv);
+  const int n = (int)(rintf(hi * inv) - g.b);
+  g.st = (float)((n + 14) / 15);
+  return g;
+}
+
+// A group with values that are not finite or too large, or with a step of at most one spacing: element by element.
 template <typename T>
-__device__ inline uint32_t quantise(const uint4& in, uint32_t* param, bool* odd) {
-  float x[8];
+__device__ __noinline__ uint32_t quantise_rare(uint4 in, uint32_t lanes, uint32_t* param, bool* odd) {
+  float x[8], lo = INFINITY, hi = -INFINITY;
   const uint32_t w[4] = {in.x, in.y, in.z, in.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack2(w[i], T());
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
-  float lo = INFINITY, hi = -INFINITY;
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    bad |= !(fabsf(x[i]) <= kQaMost);
-    x[i] = x[i] != x[i] ? 0.f : fminf(fmaxf(x[i], -kQaMost), kQaMost);
+    const float2 f = unpack2(w[i / 2], T());
+    const float y = i & 1 ? f.y : f.x;
+    bad |= !(fabsf(y) <= kQaMost);
+    x[i] = y != y ? 0.f : fminf(fmaxf(y, -kQaMost), kQaMost);
     lo = fminf(lo, x[i]);
     hi = fmaxf(hi, x[i]);
   }
   *odd = bad;
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    lo = fminf(lo, __shfl_xor_sync(lanes, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(lanes, hi, o));
   }
-  const float top = fmaxf(fabsf(lo), fabsf(hi)) * 1.015625f;
-  const int e = max((int)(__float_as_uint(top) >> 23) - 127 - 10, -24);  // u = 2^e
-  const float u = __uint_as_float((uint32_t)(127 + e) << 23), inv = __uint_as_float((uint32_t)(127 - e) << 23);
-  const float b = rintf(lo * inv);
-  const int n = (int)(rintf(hi * inv) - b), step = (n + 14) / 15;
-  const float st = (float)step, r = step > 0 ? __frcp_rn(st) : 0.f;
+  const Grid g = grid_of(lo, hi);
+  const float inv = 1.f / g.u, r = g.st > 0.f ? __frcp_rn(g.st) : 0.f;
   uint32_t codes = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float t = x[i] * inv, k = floorf((t - b) * r), border = fmaf(k + 0.5f, st, b);
+    const float t = x[i] * inv, k = floorf((t - g.b) * r), border = fmaf(k + 0.5f, g.st, g.b);
     int c = (int)k;
     c += t > border || (t == border && (c & 1));
     codes |= (uint32_t)min(max(c, 0), 15) << (4 * i);
   }
-  *param = pack_half2(st * u, b * u);
-  return step > 0 ? codes : 0u;
+  *param = pack_half2(g.st * g.u, g.b * g.u);
+  return g.st > 0.f ? codes : 0u;
 }
 
+// A lane's eight channels of a group: the word of codes, and the group's (scale, bias) as two halves.
+// `odd`: a value was not finite or too large.
+template <typename T>
+__device__ inline uint32_t quantise(const uint4& in, uint32_t* param, bool* odd) {
+  const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+  // minimum and minus the maximum, two values a register
+  const T t = T();
+  const uint32_t lo2 = min2(min2(w[0], w[1], t), min2(w[2], w[3], t), t);
+  const uint32_t hi2 = min2(min2(w[0] ^ 0x80008000u, w[1] ^ 0x80008000u, t), min2(w[2] ^ 0x80008000u, w[3] ^ 0x80008000u, t), t);
+  uint32_t m = min2(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632), t);  // (minimum, minus maximum)
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) m = min2(m, __shfl_xor_sync(0xffffffffu, m, o), t);
+  const float2 range = unpack2(m, t);
+  const float lo = range.x, hi = -range.y;
+  const Grid g = grid_of(lo, hi);
+  *odd = false;
+  // (a step of one spacing lets the largest value be half of one above code 15)
+  const bool rare = !(lo >= -kQaMost && hi <= kQaMost) || g.st <= 1.f;
+  const uint32_t lanes = __ballot_sync(0xffffffffu, rare);
+  if (rare) return quantise_rare<T>(in, lanes, param, odd);
+  // k = round(q - 1/2) of a quotient q that is off by little, as the low bits of kMagic + k; the code is k or k + 1 by
+  // the side of the border (b + (k + 1/2) st) u, which is exact, that x lies on
+  constexpr float kMagic = 12582912.f;  // 1.5 2^23
+  const float inv = 1.f / g.u, r = __frcp_rn(g.st), ri = r * inv, off = fmaf(-g.b, r, -0.5f);
+  const float su = g.st * g.u, mid = fmaf(0.5f, g.st, g.b) * g.u;
+  uint32_t z[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = unpack2(w[i / 2], t);
+    const float x = i & 1 ? f.y : f.x;
+    const float k = __fadd_rn(__fmaf_rn(x, ri, off), kMagic), border = __fmaf_rn(__fadd_rn(k, -kMagic), su, mid);
+    z[i] = __float_as_uint(k);
+    if (x > border || (x == border && (z[i] & 1u))) ++z[i];
+  }
+  // the low bytes are codes
+  const uint32_t b0 = z[1] * 16 + z[0], b1 = z[3] * 16 + z[2], b2 = z[5] * 16 + z[4], b3 = z[7] * 16 + z[6];
+  *param = pack_half2(su, g.b * g.u);
+  return __byte_perm(__byte_perm(b0, b1, 0x0040), __byte_perm(b2, b3, 0x0040), 0x5410);
+}
+
+// A thread takes eight channels of a row's key and of its value.
 template <typename T, int D>
 __global__ void __launch_bounds__(kQaThreads) qpaged_append_kernel(PagedArgs a, const uint4* __restrict__ K,
                                                                   const uint4* __restrict__ V, dkv_strides ns,
                                                                   int n_rows, const int64_t* __restrict__ slots,
                                                                   uint8_t* __restrict__ cache) {
   constexpr int R = D / 8;  // lanes of a row
-  const int64_t total = (int64_t)n_rows * a.Hkv * 2 * R, n_slots = (int64_t)a.n_pages << a.page_shift;
+  const int64_t total = (int64_t)n_rows * a.Hkv * R, n_slots = (int64_t)a.n_pages << a.page_shift;
   const int64_t base = (int64_t)blockIdx.x * (kQaThreads * kQaVec) + threadIdx.x;
-  const int c = (int)(base % R), lane8 = threadIdx.x & 7, g = c / 8;
-  const int kv = (int)(base / R & 1);  // (a step of kQaThreads is an even number of rows)
-  uint4 in[kQaVec];
-  uint8_t* block[kQaVec];
+  const int c = threadIdx.x % R, lane8 = threadIdx.x & 7, g = c / 8;
+  // row and head of the thread's first piece; the next one is kStep of them on
+  constexpr int kStep = kQaThreads / R;
+  int64_t row = base / R / a.Hkv;
+  int h = (int)(base / R - row * a.Hkv);
+  const int dr = kStep / a.Hkv, dh = kStep - dr * a.Hkv;
+  uint4 k[kQaVec], v[kQaVec];
+  uint8_t* to[kQaVec];  // of K's codes; null: nothing to write
   int tok[kQaVec];
-  bool live[kQaVec];
 #pragma unroll
-  for (int x = 0; x < kQaVec; ++x) {
-    const int64_t at = (base + x * kQaThreads) / R;  // (row, head, K or V)
-    const int h = (int)((at >> 1) % a.Hkv);
-    const int64_t row = (at >> 1) / a.Hkv;
-    live[x] = base + x * kQaThreads < total;
-    const int64_t slot = live[x] ? __ldg(slots + row) : -1;
+  for (int x = 0; x < kQaVec; ++x, row += dr, h += dh) {
+    if (h >= a.Hkv) { h -= a.Hkv; ++row; }
+    k[x] = v[x] = make_uint4(0, 0, 0, 0);
+    to[x] = nullptr;
+    tok[x] = 0;
+    if (base + x * kQaThreads >= total) continue;
+    const int64_t slot = __ldg(slots + row);
     if (slot < 0 || slot >= n_slots) {
       if (slot != -1) raise_error(a.err, DKV_DEVERR_INDEX);
-      live[x] = false;
+      continue;
     }
-    in[x] = make_uint4(0, 0, 0, 0);
-    if (!live[x]) continue;
-    in[x] = __ldg((kv ? V : K) + (row * ns.token + h * ns.head) / 8 + c);
+    const int64_t at = (row * ns.token + h * ns.head) / 8 + c;
+    k[x] = __ldg(K + at);
+    v[x] = __ldg(V + at);
     const int t = (int)slot & a.page_mask;
-    block[x] = cache + (slot >> a.page_shift) * a.stride_page + h * a.stride_head + (t / kQBlock) * qblock_bytes(D);
     tok[x] = t % kQBlock;
+    to[x] = cache + (slot >> a.page_shift) * a.stride_page + h * a.stride_head + (t / kQBlock) * qblock_bytes(D);
   }
 #pragma unroll
   for (int x = 0; x < kQaVec; ++x) {
-    uint32_t param;
-    bool odd;
-    const uint32_t codes = quantise<T>(in[x], &param, &odd);
-    if (!live[x]) continue;
-    if (odd) raise_error(a.err, DKV_DEVERR_RANGE);
-    *reinterpret_cast<uint32_t*>(block[x] + qcode_off(D, kv, g, tok[x]) + lane8 * 4) = codes;
-    if (lane8 == 0) *reinterpret_cast<uint32_t*>(block[x] + qparam_off(D, kv, g, tok[x])) = param;
+    uint32_t pk, pv;
+    bool ok, ov;
+    const uint32_t ck = quantise<T>(k[x], &pk, &ok), cv = quantise<T>(v[x], &pv, &ov);
+    if (!to[x]) continue;
+    if (ok || ov) raise_error(a.err, DKV_DEVERR_RANGE);
+    uint8_t* codes = to[x] + qcode_off(D, 0, g, tok[x]) + lane8 * 4;
+    *reinterpret_cast<uint32_t*>(codes) = ck;
+    *reinterpret_cast<uint32_t*>(codes + 8 * D) = cv;
+    if (lane8 < 2) *reinterpret_cast<uint32_t*>(to[x] + qparam_off(D, lane8, g, tok[x])) = lane8 ? pv : pk;
   }
 }
 
+// Eight codes as values in order: fp16 ones, exactly; bf16 ones are their roundings.
+template <typename T>
+__device__ inline uint4 values_of(uint32_t w, uint32_t param) {
+  const uint4 v = qvalues8(w, __low2half2(*reinterpret_cast<__half2*>(&param)), __high2half2(*reinterpret_cast<__half2*>(&param)));
+  uint4 o = make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.x, v.y, 0x7632),
+                       __byte_perm(v.z, v.w, 0x7632));
+  if (Num<T>::kUmma == 1) {
+    uint32_t* p = &o.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpack2(p[i], __half());
+      p[i] = Num<T>::pack(f.x, f.y);
+    }
+  }
+  return o;
+}
+
+// A thread takes eight channels of a token's key and of its value.
 template <typename T, int D>
 __global__ void __launch_bounds__(kQaThreads) qpaged_gather_kernel(PagedArgs a, const uint8_t* __restrict__ cache,
                                                                   const int32_t* __restrict__ first,
                                                                   const int32_t* __restrict__ counts, int n, uint4* K,
                                                                   uint4* V, dkv_strides os) {
   constexpr int R = D / 8;
-  const int b = blockIdx.y, hv = (int)(blockIdx.x % (2u * a.Hkv)), h = hv >> 1, kv = hv & 1;
+  const int b = blockIdx.y, h = (int)(blockIdx.x % (unsigned)a.Hkv);
   int cnt = n;
   if (counts) {
     cnt = __ldg(counts + b);
@@ -127,30 +207,36 @@ __global__ void __launch_bounds__(kQaThreads) qpaged_gather_kernel(PagedArgs a, 
     }
   }
   const int64_t p0 = __ldg(first + b);
-  uint4* dst = kv ? V : K;
-  const int c = threadIdx.x % R;
+  const int c = threadIdx.x % R, i0 = (int)(blockIdx.x / (unsigned)a.Hkv) * kQaVec * (kQaThreads / R) + threadIdx.x / R;
+  if (i0 >= cnt) return;
+  uint32_t wk[kQaVec], wv[kQaVec], sk[kQaVec], sv[kQaVec];
 #pragma unroll
   for (int x = 0; x < kQaVec; ++x) {
-    const int i = ((int)(blockIdx.x / (2u * a.Hkv)) * kQaVec + x) * (kQaThreads / R) + threadIdx.x / R;
-    if (i >= cnt) return;
+    const int i = i0 + x * (kQaThreads / R);
     const int64_t t = p0 + i;
-    uint32_t w = 0, sb = 0;
+    wk[x] = wv[x] = sk[x] = sv[x] = 0;
+    if (i >= cnt) continue;
     if (t < 0 || t >= a.cap) {
       raise_error(a.err, DKV_DEVERR_INDEX);
-    } else {
-      const int page = paged_page(a, b, (int)t), tok = (int)t & a.page_mask;
-      if (page < a.n_pages) {
-        const uint8_t* block = cache + page * a.stride_page + h * a.stride_head + (tok / kQBlock) * qblock_bytes(D);
-        w = __ldg(reinterpret_cast<const uint32_t*>(block + qcode_off(D, kv, c / 8, tok % kQBlock) + 4 * (c & 7)));
-        sb = __ldg(reinterpret_cast<const uint32_t*>(block + qparam_off(D, kv, c / 8, tok % kQBlock)));
-      }
+      continue;
     }
-    const float2 f = __half22float2(*reinterpret_cast<__half2*>(&sb));
-    uint32_t o[4];
+    const int page = paged_page(a, b, (int)t), tok = (int)t & a.page_mask;
+    if (page >= a.n_pages) continue;
+    const uint8_t* block = cache + page * a.stride_page + h * a.stride_head + (tok / kQBlock) * qblock_bytes(D);
+    const uint32_t* code = reinterpret_cast<const uint32_t*>(block + qcode_off(D, 0, c / 8, tok % kQBlock) + 4 * (c & 7));
+    const uint32_t* param = reinterpret_cast<const uint32_t*>(block + qparam_off(D, 0, c / 8, tok % kQBlock));
+    wk[x] = __ldg(code);
+    wv[x] = __ldg(code + 2 * D);
+    sk[x] = __ldg(param);
+    sv[x] = __ldg(param + D / 4);
+  }
+  const int64_t at = (b * os.batch + h * os.head) / 8 + c;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      o[e] = Num<T>::pack(fmaf((float)(w >> (8 * e) & 15u), f.x, f.y), fmaf((float)(w >> (8 * e + 4) & 15u), f.x, f.y));
-    dst[(b * os.batch + h * os.head + i * os.token) / 8 + c] = make_uint4(o[0], o[1], o[2], o[3]);
+  for (int x = 0; x < kQaVec; ++x) {
+    const int i = i0 + x * (kQaThreads / R);
+    if (i >= cnt) return;
+    K[at + i * os.token / 8] = values_of<T>(wk[x], sk[x]);
+    V[at + i * os.token / 8] = values_of<T>(wv[x], sv[x]);
   }
 }
 
@@ -158,7 +244,7 @@ __global__ void __launch_bounds__(kQaThreads) qpaged_gather_kernel(PagedArgs a, 
 
 cudaError_t launch_qpaged_append(const PagedArgs& a, int d, int dtype, const void* K, const void* V,
                                  const dkv_strides& ns, int n_rows, const int64_t* slots, uint8_t* cache, cudaStream_t s) {
-  const int64_t per = kQaThreads * kQaVec, pieces = (int64_t)n_rows * a.Hkv * 2 * (d / 8);
+  const int64_t per = kQaThreads * kQaVec, pieces = (int64_t)n_rows * a.Hkv * (d / 8);
   auto go = [&](auto kernel) {
     kernel<<<(unsigned)((pieces + per - 1) / per), kQaThreads, 0, s>>>(a, static_cast<const uint4*>(K), static_cast<const uint4*>(V),
                                                                        ns, n_rows, slots, cache);
@@ -172,7 +258,7 @@ cudaError_t launch_qpaged_gather(const PagedArgs& a, int d, int dtype, const uin
                                  const int32_t* counts, int n, void* K, void* V, const dkv_strides& os, cudaStream_t s) {
   const int per = kQaThreads / (d / 8) * kQaVec;
   auto go = [&](auto kernel) {
-    kernel<<<dim3((unsigned)((n + per - 1) / per) * (2u * a.Hkv), a.B), kQaThreads, 0, s>>>(a, cache, first, counts, n, static_cast<uint4*>(K),
+    kernel<<<dim3((unsigned)((n + per - 1) / per) * (unsigned)a.Hkv, a.B), kQaThreads, 0, s>>>(a, cache, first, counts, n, static_cast<uint4*>(K),
                                                                           static_cast<uint4*>(V), os);
   };
   if (dtype == DKV_BF16) d == 128 ? go(qpaged_gather_kernel<__nv_bfloat16, 128>) : go(qpaged_gather_kernel<__nv_bfloat16, 64>);

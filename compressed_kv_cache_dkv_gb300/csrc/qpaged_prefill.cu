@@ -120,20 +120,6 @@ __device__ inline unsigned long long qp_sees(const PagedArgs& a, int pos, int k0
   return below(hi + 1) & (~below(lo) | below(sk));
 }
 
-// Eight codes as values, in the order 0 4 1 5 2 6 3 7.  1024 + code and 1024 + 16 code are the halves whose low
-// bits are the code's; every step is exact.
-__device__ inline uint4 values8(uint32_t x, __half2 s, __half2 b) {
-  const uint32_t y = x >> 8;
-  auto half2_of = [](uint32_t w) { return *reinterpret_cast<__half2*>(&w); };
-  auto bits = [](__half2 h) { return *reinterpret_cast<uint32_t*>(&h); };
-  const __half2 base = half2_of(0x64006400u), sixteenth = half2_of(0x2c002c00u), minus64 = half2_of(0xd400d400u);
-  const __half2 c0 = __hsub2(half2_of((x & 0x000f000fu) | 0x64006400u), base);
-  const __half2 c1 = __hfma2(half2_of((x & 0x00f000f0u) | 0x64006400u), sixteenth, minus64);
-  const __half2 c2 = __hsub2(half2_of((y & 0x000f000fu) | 0x64006400u), base);
-  const __half2 c3 = __hfma2(half2_of((y & 0x00f000f0u) | 0x64006400u), sixteenth, minus64);
-  return make_uint4(bits(__hfma2(c0, s, b)), bits(__hfma2(c1, s, b)), bits(__hfma2(c2, s, b)), bits(__hfma2(c3, s, b)));
-}
-
 // The tiles that are not all seen, and those that move a row's reference: scores once more, the reference, and with it
 // O and the sum, moved to kQpShift below the maximum where that is higher, and P from there.  Returns reference and
 // sum.  In rolled loops, apart from the plain tiles' code: with this in it that loop does not stay in the
@@ -304,7 +290,7 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
         for (int x = 0; x < kWords / 4; ++x) {
           const uint32_t w[4] = {c[x].x, c[x].y, c[x].z, c[x].w};
 #pragma unroll
-          for (int y = 0; y < 4; ++y) sts128(to ^ (16 * (4 * x + y)), values8(w[y], s2, b2));
+          for (int y = 0; y < 4; ++y) sts128(to ^ (16 * (4 * x + y)), qvalues8(w[y], s2, b2));
         }
       }
       fence_proxy_async();
