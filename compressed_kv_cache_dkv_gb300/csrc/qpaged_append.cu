@@ -9,6 +9,7 @@
 // quotient only proposes k, and x / u is compared with the border lo + (k + 1/2) step, a multiple of 1/2.
 //
 // Bound by memory: 4 d bytes in and 9/8 d out a row and head (the gather the other way round).
+#include "paged_tc.cuh"
 #include "qpaged.cuh"
 
 namespace dkv {
@@ -31,25 +32,44 @@ __device__ inline uint32_t min2(uint32_t x, uint32_t y, __nv_bfloat16) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+constexpr float kMagic = 12582912.f;  // 1.5 2^23: x + kMagic - kMagic is x rounded to a whole number, ties to even
+
+__device__ inline uint32_t max2(uint32_t x, uint32_t y, __half) {
+  const __half2 r = __hmax2_nan(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<__half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ inline uint32_t max2(uint32_t x, uint32_t y, __nv_bfloat16) {
+  const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<__nv_bfloat162*>(&x), *reinterpret_cast<__nv_bfloat162*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // The grid of a group between lo and hi.
 struct Grid {
-  float u, b, st;  // spacing; bias and step in its units
+  float u, inv;  // spacing, and one over it
+  float b, st;   // bias and step in spacings
 };
 __device__ inline Grid grid_of(float lo, float hi) {
   const float top = fmaxf(fabsf(lo), fabsf(hi)) * 1.015625f;
-  const int e = max((int)(__float_as_uint(top) >> 23) - 127 - 10, -24);  // u = 2^e
-  const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+  // u = 2^e, e = max(exponent of top - 10, -24), in place
+  const uint32_t e = max(__float_as_uint(top) & 0x7f800000u, 113u << 23) - (10u << 23);
   Grid g;
-  g.u = __uint_as_float((uint32_t)(127 + e) << 23);
-  g.b = rintf(lo * inv);
-  const int n = (int)(rintf(hi * inv) - g.b);
-  g.st = (float)((n + 14) / 15);
+  g.u = __uint_as_float(e);
+  g.inv = __uint_as_float((254u << 23) - e);
+  g.b = __fadd_rn(__fmaf_rn(lo, g.inv, kMagic), -kMagic);
+  const float n = __fadd_rn(__fadd_rn(__fmaf_rn(hi, g.inv, kMagic), -kMagic), -g.b);
+  // (n + 14) / 15 without its remainder: that is at most 14/15, in the middle of which it is rounded
+  g.st = __fadd_rn(__fadd_rn(__fmaf_rn(n + 14.f, 1.f / 15.f, -7.f / 15.f), kMagic), -kMagic);
   return g;
 }
 
+struct Quantised {
+  uint32_t codes, param;  // of a lane's eight channels, and of the group: (scale, bias) as two halves
+  bool odd;               // a value was not finite or too large
+};
+
 // A group with values that are not finite or too large, or with a step of at most one spacing: element by element.
 template <typename T>
-__device__ __noinline__ uint32_t quantise_rare(uint4 in, uint32_t lanes, uint32_t* param, bool* odd) {
+__device__ __noinline__ Quantised quantise_rare(uint4 in, uint32_t lanes) {
   float x[8], lo = INFINITY, hi = -INFINITY;
   const uint32_t w[4] = {in.x, in.y, in.z, in.w};
   bool bad = false;
@@ -62,14 +82,13 @@ __device__ __noinline__ uint32_t quantise_rare(uint4 in, uint32_t lanes, uint32_
     lo = fminf(lo, x[i]);
     hi = fmaxf(hi, x[i]);
   }
-  *odd = bad;
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) {
     lo = fminf(lo, __shfl_xor_sync(lanes, lo, o));
     hi = fmaxf(hi, __shfl_xor_sync(lanes, hi, o));
   }
   const Grid g = grid_of(lo, hi);
-  const float inv = 1.f / g.u, r = g.st > 0.f ? __frcp_rn(g.st) : 0.f;
+  const float inv = g.inv, r = g.st > 0.f ? 1.f / g.st : 0.f;
   uint32_t codes = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -78,48 +97,47 @@ __device__ __noinline__ uint32_t quantise_rare(uint4 in, uint32_t lanes, uint32_
     c += t > border || (t == border && (c & 1));
     codes |= (uint32_t)min(max(c, 0), 15) << (4 * i);
   }
-  *param = pack_half2(g.st * g.u, g.b * g.u);
-  return g.st > 0.f ? codes : 0u;
+  return {g.st > 0.f ? codes : 0u, pack_half2(g.st * g.u, g.b * g.u), bad};
 }
 
-// A lane's eight channels of a group: the word of codes, and the group's (scale, bias) as two halves.
-// `odd`: a value was not finite or too large.
+// A lane's eight channels of a group.
 template <typename T>
-__device__ inline uint32_t quantise(const uint4& in, uint32_t* param, bool* odd) {
+__device__ inline Quantised quantise(const uint4& in) {
   const uint32_t w[4] = {in.x, in.y, in.z, in.w};
   // minimum and minus the maximum, two values a register
   const T t = T();
-  const uint32_t lo2 = min2(min2(w[0], w[1], t), min2(w[2], w[3], t), t);
-  const uint32_t hi2 = min2(min2(w[0] ^ 0x80008000u, w[1] ^ 0x80008000u, t), min2(w[2] ^ 0x80008000u, w[3] ^ 0x80008000u, t), t);
-  uint32_t m = min2(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632), t);  // (minimum, minus maximum)
+  const uint32_t lo2 = min2(min2(w[0], w[1], t), min2(w[2], w[3], t), t), hi2 = max2(max2(w[0], w[1], t), max2(w[2], w[3], t), t);
+  uint32_t m = min2(__byte_perm(lo2, hi2, 0x5410) ^ 0x80000000u, __byte_perm(lo2, hi2, 0x7632) ^ 0x80000000u, t);
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) m = min2(m, __shfl_xor_sync(0xffffffffu, m, o), t);
   const float2 range = unpack2(m, t);
   const float lo = range.x, hi = -range.y;
   const Grid g = grid_of(lo, hi);
-  *odd = false;
   // (a step of one spacing lets the largest value be half of one above code 15)
   const bool rare = !(lo >= -kQaMost && hi <= kQaMost) || g.st <= 1.f;
   const uint32_t lanes = __ballot_sync(0xffffffffu, rare);
-  if (rare) return quantise_rare<T>(in, lanes, param, odd);
+  if (rare) return quantise_rare<T>(in, lanes);
   // k = round(q - 1/2) of a quotient q that is off by little, as the low bits of kMagic + k; the code is k or k + 1 by
-  // the side of the border (b + (k + 1/2) st) u, which is exact, that x lies on
-  constexpr float kMagic = 12582912.f;  // 1.5 2^23
-  const float inv = 1.f / g.u, r = __frcp_rn(g.st), ri = r * inv, off = fmaf(-g.b, r, -0.5f);
-  const float su = g.st * g.u, mid = fmaf(0.5f, g.st, g.b) * g.u;
+  // the side of the border (b + (k + 1/2) st) u, which is exact, that x lies on: k + 1 above it, and on it if k is odd
+  // (a difference of 0 less one has the sign bit)
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(g.st));
+  const float ri = r * g.inv, off = fmaf(-g.b, r, -0.5f), su = g.st * g.u, mid = fmaf(0.5f, g.st, g.b) * g.u;
   uint32_t z[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 f = unpack2(w[i / 2], t);
-    const float x = i & 1 ? f.y : f.x;
-    const float k = __fadd_rn(__fmaf_rn(x, ri, off), kMagic), border = __fmaf_rn(__fadd_rn(k, -kMagic), su, mid);
-    z[i] = __float_as_uint(k);
-    if (x > border || (x == border && (z[i] & 1u))) ++z[i];
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = unpack2(w[i], t);
+    const float2 k = add2(fma2(x, make_float2(ri, ri), make_float2(off, off)), make_float2(kMagic, kMagic));
+    const float2 border = fma2(add2(k, make_float2(-kMagic, -kMagic)), make_float2(su, su), make_float2(mid, mid));
+    const float2 d = add2(border, make_float2(-x.x, -x.y));
+    z[2 * i] = __float_as_uint(k.x);
+    z[2 * i + 1] = __float_as_uint(k.y);
+    z[2 * i] += (__float_as_uint(d.x) - (z[2 * i] & 1u)) >> 31;
+    z[2 * i + 1] += (__float_as_uint(d.y) - (z[2 * i + 1] & 1u)) >> 31;
   }
   // the low bytes are codes
   const uint32_t b0 = z[1] * 16 + z[0], b1 = z[3] * 16 + z[2], b2 = z[5] * 16 + z[4], b3 = z[7] * 16 + z[6];
-  *param = pack_half2(su, g.b * g.u);
-  return __byte_perm(__byte_perm(b0, b1, 0x0040), __byte_perm(b2, b3, 0x0040), 0x5410);
+  return {__byte_perm(__byte_perm(b0, b1, 0x0040), __byte_perm(b2, b3, 0x0040), 0x5410), pack_half2(su, g.b * g.u), false};
 }
 
 // A thread takes eight channels of a row's key and of its value.
@@ -129,13 +147,13 @@ __global__ void __launch_bounds__(kQaThreads) qpaged_append_kernel(PagedArgs a, 
                                                                   int n_rows, const int64_t* __restrict__ slots,
                                                                   uint8_t* __restrict__ cache) {
   constexpr int R = D / 8;  // lanes of a row
-  const int64_t total = (int64_t)n_rows * a.Hkv * R, n_slots = (int64_t)a.n_pages << a.page_shift;
-  const int64_t base = (int64_t)blockIdx.x * (kQaThreads * kQaVec) + threadIdx.x;
+  const int64_t n_slots = (int64_t)a.n_pages << a.page_shift;
   const int c = threadIdx.x % R, lane8 = threadIdx.x & 7, g = c / 8;
   // row and head of the thread's first piece; the next one is kStep of them on
   constexpr int kStep = kQaThreads / R;
-  int64_t row = base / R / a.Hkv;
-  int h = (int)(base / R - row * a.Hkv);
+  const uint32_t pair = blockIdx.x * (kStep * kQaVec) + threadIdx.x / R;
+  uint32_t row = pair / (uint32_t)a.Hkv;
+  int h = (int)(pair - row * (uint32_t)a.Hkv);
   const int dr = kStep / a.Hkv, dh = kStep - dr * a.Hkv;
   uint4 k[kQaVec], v[kQaVec];
   uint8_t* to[kQaVec];  // of K's codes; null: nothing to write
@@ -146,7 +164,7 @@ __global__ void __launch_bounds__(kQaThreads) qpaged_append_kernel(PagedArgs a, 
     k[x] = v[x] = make_uint4(0, 0, 0, 0);
     to[x] = nullptr;
     tok[x] = 0;
-    if (base + x * kQaThreads >= total) continue;
+    if (row >= (uint32_t)n_rows) continue;
     const int64_t slot = __ldg(slots + row);
     if (slot < 0 || slot >= n_slots) {
       if (slot != -1) raise_error(a.err, DKV_DEVERR_INDEX);
@@ -161,15 +179,13 @@ __global__ void __launch_bounds__(kQaThreads) qpaged_append_kernel(PagedArgs a, 
   }
 #pragma unroll
   for (int x = 0; x < kQaVec; ++x) {
-    uint32_t pk, pv;
-    bool ok, ov;
-    const uint32_t ck = quantise<T>(k[x], &pk, &ok), cv = quantise<T>(v[x], &pv, &ov);
+    const Quantised qk = quantise<T>(k[x]), qv = quantise<T>(v[x]);
     if (!to[x]) continue;
-    if (ok || ov) raise_error(a.err, DKV_DEVERR_RANGE);
+    if (qk.odd || qv.odd) raise_error(a.err, DKV_DEVERR_RANGE);
     uint8_t* codes = to[x] + qcode_off(D, 0, g, tok[x]) + lane8 * 4;
-    *reinterpret_cast<uint32_t*>(codes) = ck;
-    *reinterpret_cast<uint32_t*>(codes + 8 * D) = cv;
-    if (lane8 < 2) *reinterpret_cast<uint32_t*>(to[x] + qparam_off(D, lane8, g, tok[x])) = lane8 ? pv : pk;
+    *reinterpret_cast<uint32_t*>(codes) = qk.codes;
+    *reinterpret_cast<uint32_t*>(codes + 8 * D) = qv.codes;
+    if (lane8 < 2) *reinterpret_cast<uint32_t*>(to[x] + qparam_off(D, lane8, g, tok[x])) = lane8 ? qv.param : qk.param;
   }
 }
 

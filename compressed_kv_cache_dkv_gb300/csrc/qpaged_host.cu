@@ -216,7 +216,7 @@ int dkv_qpaged_append(const dkv_qpaged* p, const void* K, const void* V, const d
   if (rows < 0) return DKV_ERR_ARG;
   if (rows == 0) return DKV_OK;
   if (!K || !V || !slots || !cache) return DKV_ERR_ARG;
-  if (rows > (1 << 30) || (int64_t)rows * p->n_kv_heads > (int64_t(1) << 34)) return DKV_ERR_UNSUPPORTED;
+  if (rows > (1 << 30) || (int64_t)rows * p->n_kv_heads > (int64_t(1) << 31)) return DKV_ERR_UNSUPPORTED;
   if ((st = check_rows(ns, 1, p->n_kv_heads, rows, p->head_dim)) != DKV_OK) return st;
   if (!aligned(K, 16) || !aligned(V, 16) || !aligned(cache, 16) || !aligned(slots, 8)) return DKV_ERR_ALIGN;
   const PagedArgs a = make_args(p, nullptr, nullptr, workspace);
