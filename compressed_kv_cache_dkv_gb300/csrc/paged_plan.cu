@@ -14,6 +14,7 @@ namespace dkv {
 namespace {
 
 constexpr int kPlanThreads = 1024, kPlanMost = 4;  // requests of a thread at most: 4096 in all
+constexpr int kPlanFew = 256;                      // threads for as many requests and their rows
 constexpr int kPlanRows = 4;                       // rows of a thread
 constexpr int kPlanAlone = 8192;                   // rows that one CTA takes
 
@@ -31,6 +32,7 @@ struct Plan {
   PlanArgs a;
   PlanSums s;
   int n_free, top;  // of the list, without and with the pages given back
+  bool vec;         // slots and positions begin on 16-byte boundaries
 
   __device__ int pages_of(int n) const { return (n >> a.page_shift) + ((n & ((1 << a.page_shift) - 1)) != 0); }
   // the request whose span of `cum` holds x < cum[B]
@@ -72,6 +74,13 @@ struct Plan {
       if (pg >= 0 && pg < a.n_pages) slot[x] = ((int64_t)pg << a.page_shift) + (t & ((1 << a.page_shift) - 1));
       else raise_error(a.err, DKV_DEVERR_INDEX);
     }
+    if (vec && i0 + kPlanRows <= a.rows) {
+      static_assert(kPlanRows == 4, "two 16-byte stores of slots, one of positions");
+      *reinterpret_cast<longlong2*>(a.slots + i0) = make_longlong2(slot[0], slot[1]);
+      *reinterpret_cast<longlong2*>(a.slots + i0 + 2) = make_longlong2(slot[2], slot[3]);
+      *reinterpret_cast<int4*>(a.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      return;
+    }
 #pragma unroll
     for (int x = 0; x < kPlanRows; ++x)
       if (i0 + x < a.rows) {
@@ -93,10 +102,11 @@ struct Plan {
   }
 };
 
-// exclusive prefix sums over the CTA of up to three values a thread, and their totals
-template <int N>
+// exclusive prefix sums over a CTA of THREADS of N values a thread, and their totals
+template <int THREADS, int N>
 __device__ inline void block_sums(int64_t (&v)[N], int64_t (&total)[N]) {
-  __shared__ int64_t part[N][32];
+  constexpr int kWarps = THREADS / 32;
+  __shared__ int64_t part[N][kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t x[N];
 #pragma unroll
@@ -111,39 +121,44 @@ __device__ inline void block_sums(int64_t (&v)[N], int64_t (&total)[N]) {
   }
   __syncthreads();
   if (warp < N) {
-    int64_t y = part[warp][lane];
+    int64_t y = lane < kWarps ? part[warp][lane] : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
+    for (int o = 1; o < kWarps; o <<= 1) {
       const int64_t z = __shfl_up_sync(0xffffffffu, y, o);
       if (lane >= o) y += z;
     }
-    part[warp][lane] = y;
+    if (lane < kWarps) part[warp][lane] = y;
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     v[i] = x[i] - v[i] + (warp ? part[i][warp - 1] : 0);
-    total[i] = part[i][31];
+    total[i] = part[i][kWarps - 1];
   }
-  __syncthreads();
 }
+// two counts in one sum (each stays below 2^31: 4096 requests of at most 65536 pages, 2^30 rows)
+__device__ inline int64_t both(int hi, int lo) { return ((int64_t)hi << 32) | (uint32_t)lo; }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, int* ws, int alone) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) plan_kernel(PlanArgs a, int* ws, int alone, bool vec) {
   extern __shared__ int sums[];
+  constexpr int kMost = THREADS == kPlanThreads ? kPlanMost : 1;
+  if (!alone) griddep_launch();  // the grid that writes
   Plan p;
   p.a = a;
+  p.vec = vec;
   p.s = plan_sums(alone ? sums : ws, a.B);
-  const int per = (a.B + kPlanThreads - 1) / kPlanThreads, b0 = threadIdx.x * per;
+  const int per = (a.B + THREADS - 1) / THREADS, b0 = threadIdx.x * per;
   const int cap = a.max_pages << a.page_shift;
   int n_free = __ldcg(a.n_free);
   if (n_free < 0 || n_free > a.free_cap) {
     if (threadIdx.x == 0) raise_error(a.err, DKV_DEVERR_INDEX);
     n_free = min(max(n_free, 0), a.free_cap);
   }
-  int len[kPlanMost], cut[kPlanMost], grow[kPlanMost];
-  int64_t v[3] = {0, 0, 0}, all[3];  // pages given back, pages needed, tokens
+  int len[kMost], cut[kMost], grow[kMost];
+  int64_t v[2] = {0, 0}, all[2];  // pages given back and pages needed; tokens
 #pragma unroll
-  for (int i = 0; i < kPlanMost; ++i) {
+  for (int i = 0; i < kMost; ++i) {
     const int b = b0 + i;
     len[i] = cut[i] = grow[i] = 0;
     if (i >= per || b >= a.B) continue;
@@ -153,58 +168,62 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, int* ws,
     if (m < 0) cut[i] = m < -len[i] ? len[i] : -m;
     else if (fits) grow[i] = m;
     if (n != len[i] || !fits || m < -len[i]) raise_error(a.err, DKV_DEVERR_INDEX);
-    v[0] += p.pages_of(len[i]) - p.pages_of(len[i] - cut[i]);
-    v[1] += p.pages_of(len[i] + grow[i]) - p.pages_of(len[i]);
-    v[2] += grow[i];
+    v[0] += both(p.pages_of(len[i]) - p.pages_of(len[i] - cut[i]), p.pages_of(len[i] + grow[i]) - p.pages_of(len[i]));
+    v[1] += grow[i];
   }
-  block_sums(v, all);
+  block_sums<THREADS>(v, all);
+  const int all_back = (int)(all[0] >> 32);
   p.n_free = n_free;
-  p.top = n_free + (int)all[0];
-  int give[kPlanMost];  // tokens granted
-  int64_t back = v[0], asked = v[1], rows = v[2], w[2] = {0, 0}, sum[2];
+  p.top = n_free + all_back;
+  int give[kMost];  // tokens granted
+  int back = (int)(v[0] >> 32), asked = (int)v[0];
+  int64_t rows = v[1], w[1] = {0}, sum[1];
 #pragma unroll
-  for (int i = 0; i < kPlanMost; ++i) {
+  for (int i = 0; i < kMost; ++i) {
     const int need = p.pages_of(len[i] + grow[i]) - p.pages_of(len[i]);
     asked += need;
     rows += grow[i];
     give[i] = (need == 0 || asked <= p.top) && rows <= a.rows ? grow[i] : 0;
-    w[0] += give[i];
-    w[1] += give[i] ? need : 0;
+    w[0] += both(give[i], give[i] ? need : 0);
   }
-  block_sums(w, sum);
+  __syncthreads();
+  block_sums<THREADS>(w, sum);
+  const int all_rows = (int)(sum[0] >> 32), all_need = (int)sum[0];
+  int start = (int)(w[0] >> 32), taken = (int)w[0];
 #pragma unroll
-  for (int i = 0; i < kPlanMost; ++i) {
+  for (int i = 0; i < kMost; ++i) {
     const int b = b0 + i;
     if (i >= per || b >= a.B) continue;
-    p.s.starts[b] = (int)w[0];
-    p.s.need[b] = (int)w[1];
-    p.s.back[b] = (int)back;
+    p.s.starts[b] = start;
+    p.s.need[b] = taken;
+    p.s.back[b] = back;
     p.s.lens[b] = len[i];
-    a.starts[b] = (int)w[0];
+    a.starts[b] = start;
     a.granted[b] = give[i];
     a.new_lens[b] = len[i] - cut[i] + give[i];
-    w[0] += give[i];
-    w[1] += p.pages_of(len[i] + give[i]) - p.pages_of(len[i]);
+    start += give[i];
+    taken += p.pages_of(len[i] + give[i]) - p.pages_of(len[i]);
     back += p.pages_of(len[i]) - p.pages_of(len[i] - cut[i]);
   }
   if (threadIdx.x == 0) {
-    p.s.starts[a.B] = a.starts[a.B] = (int)sum[0];
-    p.s.need[a.B] = (int)sum[1];
-    p.s.back[a.B] = (int)all[0];
+    p.s.starts[a.B] = a.starts[a.B] = all_rows;
+    p.s.need[a.B] = all_need;
+    p.s.back[a.B] = all_back;
     p.s.lens[a.B] = n_free;
-    *a.new_n_free = min(p.top - (int)sum[1], a.free_cap);
+    *a.new_n_free = min(p.top - all_need, a.free_cap);
   }
   __syncthreads();
-  if (alone) p.write(threadIdx.x, kPlanThreads);
+  if (alone) p.write(threadIdx.x, THREADS);
 }
 
-__global__ void __launch_bounds__(256) plan_write_kernel(PlanArgs a, const int* ws) {
+__global__ void __launch_bounds__(256) plan_write_kernel(PlanArgs a, const int* ws, bool vec) {
   extern __shared__ int sums[];
   griddep_wait();
   for (int i = threadIdx.x; i < plan_ints(a.B); i += blockDim.x) sums[i] = __ldcg(ws + i);
   __syncthreads();
   Plan p;
   p.a = a;
+  p.vec = vec;
   p.s = plan_sums(sums, a.B);
   p.n_free = p.s.lens[a.B];
   p.top = p.n_free + p.s.back[a.B];
@@ -218,14 +237,16 @@ size_t plan_ws_bytes(int B) { return kWsHeader + round_up((size_t)plan_ints(B) *
 cudaError_t launch_paged_plan(const PlanArgs& a, uint8_t* ws, cudaStream_t s) {
   int* sums = reinterpret_cast<int*>(ws + kWsHeader);
   const size_t smem = (size_t)plan_ints(a.B) * 4;
-  const bool alone = a.rows <= kPlanAlone;
-  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(plan_kernel), smem);
+  const bool alone = a.rows <= kPlanAlone, few = a.B <= kPlanFew && a.rows <= kPlanFew * kPlanRows;
+  const bool vec = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) & 15u) == 0;
+  cudaError_t e = ensure_smem_limit(few ? reinterpret_cast<const void*>(plan_kernel<kPlanFew>) : reinterpret_cast<const void*>(plan_kernel<kPlanThreads>), smem);
   if (e != cudaSuccess) return e;
-  plan_kernel<<<1, kPlanThreads, smem, s>>>(a, sums, alone);
+  if (few) plan_kernel<kPlanFew><<<1, kPlanFew, smem, s>>>(a, sums, alone, vec);
+  else plan_kernel<kPlanThreads><<<1, kPlanThreads, smem, s>>>(a, sums, alone, vec);
   if ((e = cudaGetLastError()) != cudaSuccess || alone) return e;
   if ((e = ensure_smem_limit(reinterpret_cast<const void*>(plan_write_kernel), smem)) != cudaSuccess) return e;
   const int64_t most = ((int64_t)a.rows + 256 * kPlanRows - 1) / (256 * kPlanRows);
-  return launch_dependent(plan_write_kernel, dim3((unsigned)(most < 4 * sm_count() ? most : 4 * sm_count())), 256, smem, s, a, (const int*)sums);
+  return launch_dependent(plan_write_kernel, dim3((unsigned)(most < 4 * sm_count() ? most : 4 * sm_count())), 256, smem, s, a, (const int*)sums, vec);
 }
 
 }  // namespace dkv
