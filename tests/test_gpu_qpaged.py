@@ -434,3 +434,408 @@ def test_plan_refuses_what_does_not_fit():
     got = dkv.dkv_paged_plan(p, dev([16, 16, 0, 0, 0]), dev([-16, -1, 0, 0, 0]), F, dev([1]), T, 4, workspace=ws)
     assert int(got[5]) == 1 and F.tolist() == [20] and got[4].tolist() == [0, 15, 0, 0, 0]
     assert dkv.dkv_get_error(ws)[1] == dkv.DKV_DEVERR_INDEX
+
+
+# ---------------------------------------------------------------- places and numbers at their limits
+
+def filled(d, hkv, page, n_pages, dt, seed=1, scale=1.0, head_pad=0):
+    """A pool of random rows, page i holding tokens i * page and up of one long row, and those rows as they are held (fp64)."""
+    store = torch.full((n_pages, hkv, page * 9 * d // 8 + head_pad), 0xFF, dtype=torch.uint8, device="cuda")
+    pool = store[..., :page * 9 * d // 8]
+    p = dkv.dkv_qpaged_layout(pool, 1, hkv, d, n_pages, dtype=dt)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    K, V = ((torch.randn(n_pages * page, hkv, d, generator=g, device="cuda") * scale).to(dt) for _ in range(2))
+    dkv.dkv_qpaged_append(p, K, V, pool, torch.arange(n_pages * page, device="cuda"))
+    back = [torch.zeros(1, hkv, n_pages * page, d, dtype=torch.float16, device="cuda") for _ in range(2)]
+    p16 = dkv.dkv_qpaged_layout(pool, 1, hkv, d, n_pages)
+    dkv.dkv_qpaged_gather(p16, pool, torch.arange(n_pages, dtype=torch.int32, device="cuda")[None],
+                          torch.zeros(1, dtype=torch.int32, device="cuda"), *back)
+    return pool, back[0][0].double(), back[1][0].double()
+
+
+def exact_rows(q, k, v):
+    """q [m, d], k, v [n, d] fp64 -> (out, lse, bounds of the parts) of rows that see everything."""
+    s = (q @ k.T) / math.sqrt(q.shape[1])
+    w = s.softmax(-1)
+    size = 3.1 * (w * v.abs().amax(-1)).sum(-1, keepdim=True)
+    ds = R.score_error(q.shape[1], 3.1 * float(q.abs().sum(-1).max() * k.abs().max()) / math.sqrt(q.shape[1]))
+    return w @ v, s.logsumexp(-1), size, ds
+
+
+def near(out, lse, ref, dt, p_eps=2.0 ** -11):
+    want, want_lse, size, ds = ref
+    tol = torch.finfo(dt).eps / 2 * want.abs() + (p_eps + 2 * ds) * (1 + 2.0 ** -8) * size + 1e-30
+    assert bool(((out.double() - want).abs() <= tol).all())
+    assert bool(((lse.double() - want_lse).abs() <= ds + 2.0 ** -22 * want_lse.abs().clamp(min=1.0)).all())
+
+
+def test_most_sequences_that_a_call_takes():
+    B, d, page = 4096, 128, 16
+    pool, k, v = filled(d, 1, page, 64, torch.float16)
+    p = dkv.dkv_qpaged_layout(pool, B, 8, d, 2)
+    ws = workspace(p)
+    lens = torch.arange(B, dtype=torch.int32, device="cuda") % 33
+    table = torch.stack([torch.arange(B) % 63, torch.arange(B) % 63 + 1], 1).int().cuda()
+    q = randn((B, 8, d), torch.float16, 3, 2.0).cuda()
+    out, lse = dkv.dkv_qpaged_decode(p, q, pool, table, lens, workspace=ws)
+    no_fault(ws)
+    for b in (0, 1, 32, 33, 100, 2047, 4095):
+        n, at = int(lens[b]), b % 63 * page
+        if n == 0:
+            assert not out[b].any() and bool((lse[b] == -math.inf).all())
+        else:
+            near(out[b], lse[b], exact_rows(q[b].double(), k[0, at:at + n], v[0, at:at + n]), torch.float16)
+    starts = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    out2, lse2 = dkv.dkv_qpaged_prefill(p, q, starts, 1, pool, table, lens, workspace=ws)
+    no_fault(ws)
+    some = lens > 0
+    assert bool(((out2[some].double() - out[some].double()).abs() <= 2.0 ** -8 * v.abs().max()).all())
+
+
+def test_offsets_past_32_bits():
+    d, hkv, page, n_pages = 128, 2, 256, 64
+    wide = 140 << 20  # bytes from page to page: 8.75 GB in all
+    store = torch.empty(n_pages * wide, dtype=torch.uint8, device="cuda")
+    bytes_of = page * 9 * d // 8
+    pool = store.as_strided((n_pages, hkv, bytes_of), (wide, wide // 2, 1))
+    dt = torch.bfloat16
+    p = dkv.dkv_qpaged_layout(pool, 1, 4, d, n_pages, dtype=dt)
+    ws = workspace(p)
+    n = n_pages * page
+    K, V = (randn((n, hkv, d), dt, s).cuda() for s in (1, 2))
+    table = torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device="cuda")[None].contiguous()
+    t = torch.arange(n, device="cuda")
+    dkv.dkv_qpaged_append(p, K, V, pool, table[0].long()[t // page] * page + t % page, workspace=ws)
+    back = [torch.zeros(1, hkv, n, d, dtype=dt, device="cuda") for _ in range(2)]
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dkv.dkv_qpaged_gather(p, pool, table, zero, *back, workspace=ws)
+    for x, y in zip((K, V), back):
+        want = Q.values(*Q.quantise(x[-300:].double().cpu())).to(dt)
+        assert torch.equal(y[0, :, -300:].cpu(), want.transpose(0, 1))
+    q = randn((1, 4, d), dt, 3, 2.0).cuda()
+    L = torch.tensor([n], dtype=torch.int32, device="cuda")
+    out, lse = dkv.dkv_qpaged_decode(p, q, pool, table, L, workspace=ws)
+    out2, lse2 = dkv.dkv_qpaged_prefill(p, q, torch.tensor([0, 1], dtype=torch.int32, device="cuda"), 1, pool, table, L, workspace=ws)
+    no_fault(ws)
+    exact = dkv.dkv_qpaged_layout(pool, 1, 4, d, n_pages)
+    back = [torch.zeros(1, hkv, n, d, dtype=torch.float16, device="cuda") for _ in range(2)]
+    dkv.dkv_qpaged_gather(exact, pool, table, zero, *back, workspace=ws)
+    for h in range(hkv):
+        ref = exact_rows(q[0, 2 * h:2 * h + 2].double(), back[0][0, h].double(), back[1][0, h].double())
+        near(out[0, 2 * h:2 * h + 2], lse[0, 2 * h:2 * h + 2], ref, dt)
+        near(out2[0, 2 * h:2 * h + 2], lse2[2 * h:2 * h + 2, 0], ref, dt)
+
+
+@pytest.mark.parametrize("page", [16, 64, 128])
+def test_pages_and_lengths_out_of_range(page):
+    d, hkv, n_pages, dt = 128, 2, 12, torch.float16
+    pool, k, v = filled(d, hkv, page, n_pages, dt, seed=page)
+    width = 300 // page + 1
+    p = dkv.dkv_qpaged_layout(pool, 3, 4, d, width)
+    ws = workspace(p)
+    table = torch.zeros(3, width, dtype=torch.int32)
+    for b in range(3):
+        table[b] = (torch.arange(width) * 5 + b) % n_pages
+    bad = min(1, width - 1)
+    table[0, bad] = n_pages
+    table[2, 0] = -1
+    lens = torch.tensor([280, 1 << 20, -4], dtype=torch.int32)  # as they are, the capacity, none
+    real = [280, width * page, 0]
+    q = randn((3, 4, d), dt, 5, 2.0).cuda()
+    out, lse = dkv.dkv_qpaged_decode(p, q, pool, table.cuda(), lens.cuda(), workspace=ws)
+    assert dkv.dkv_get_error(ws) == (dkv.DKV_ERR_DEVICE, dkv.DKV_DEVERR_INDEX)
+    out2, lse2 = dkv.dkv_qpaged_prefill(p, q, torch.arange(4, dtype=torch.int32, device="cuda"), 1, pool, table.cuda(), lens.cuda(), workspace=ws)
+    assert dkv.dkv_get_error(ws) == (dkv.DKV_ERR_DEVICE, dkv.DKV_DEVERR_INDEX)
+    for b in range(2):
+        t = torch.arange(real[b])
+        pg = table[b].long()[t // page]
+        ok = ((pg >= 0) & (pg < n_pages)).cuda()
+        at = (pg.clamp(0, n_pages - 1) * page + t % page).cuda()
+        for h in range(hkv):
+            K, V = (torch.where(ok[:, None], x[h][at], 0.0) for x in (k, v))
+            ref = exact_rows(q[b, 2 * h:2 * h + 2].double(), K, V)
+            near(out[b, 2 * h:2 * h + 2], lse[b, 2 * h:2 * h + 2], ref, dt)
+            near(out2[b, 2 * h:2 * h + 2], lse2[2 * h:2 * h + 2, b], ref, dt)
+    assert not out[2].any() and bool((lse[2] == -math.inf).all()) and not out2[2].any() and bool((lse2[:, 2] == -math.inf).all())
+    back = [torch.full((3, hkv, 20, d), 7.0, dtype=dt, device="cuda") for _ in range(2)]
+    first = torch.tensor([page - 4, real[1] - 10, -3], dtype=torch.int32, device="cuda")
+    dkv.dkv_qpaged_gather(p, pool, table.cuda(), first, *back, counts=torch.tensor([8, 20, 5], dtype=torch.int32, device="cuda"), workspace=ws)
+    assert dkv.dkv_get_error(ws)[1] == dkv.DKV_DEVERR_INDEX
+    for x, rows in zip(back, (k, v)):
+        at = int(table[0, 0]) * page + page - 4
+        assert torch.equal(x[0, :, :4].double(), rows[:, at:at + 4]) and not x[0, :, 4:8].any()
+        assert not x[1, :, 10:].any() and not x[2, :, :3].any() and bool((x[0, :, 8:] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("power", [10, 20, 24, 30])
+def test_scores_of_any_size(dtype, power):
+    """Scores around 2^power: the heaviest key takes all, and nothing overflows."""
+    dt, d, n, page = Q.DT[dtype], 128, 700, 64
+    pool = torch.zeros(11, 1, page * 144, dtype=torch.uint8, device="cuda")
+    p = dkv.dkv_qpaged_layout(pool, 1, 8, d, 11, dtype=dt)
+    ws = workspace(p)
+    size = 2.0 ** (power / 2)
+    K = torch.zeros(n, 1, d)
+    K[:, 0, 0] = torch.randperm(n, generator=torch.Generator().manual_seed(power)).double().div(n).mul(2).sub(1) * min(size, 4e4)
+    K, V = K.to(dt).cuda(), randn((n, 1, d), dt, 2).cuda()
+    dkv.dkv_qpaged_append(p, K, V, pool, torch.arange(n, device="cuda"), workspace=ws)
+    q = torch.zeros(1, 8, d)
+    q[0, :, 0] = torch.linspace(0.5, 1, 8) * min(size * math.sqrt(d), 6e4)  # (an fp16 query of 2^15 sqrt(d) would be infinite)
+    q = q.to(dt).cuda()
+    table, L = torch.arange(11, dtype=torch.int32, device="cuda")[None].contiguous(), torch.tensor([n], dtype=torch.int32, device="cuda")
+    out, lse = dkv.dkv_qpaged_decode(p, q, pool, table, L, workspace=ws)
+    out2, lse2 = dkv.dkv_qpaged_prefill(p, q.expand(40, 8, d).contiguous(), torch.tensor([0, 40], dtype=torch.int32, device="cuda"), 40, pool, table, L, workspace=ws)
+    no_fault(ws)
+    back = [torch.zeros(1, 1, n, d, dtype=torch.float16, device="cuda") for _ in range(2)]
+    dkv.dkv_qpaged_gather(dkv.dkv_qpaged_layout(pool, 1, 8, d, 11), pool, table, L * 0, *back, workspace=ws)
+    k, v = (x[0, 0].double() for x in back)
+    for j in range(8):
+        s = (k @ q[0, j].double()) / math.sqrt(d)
+        ds = R.score_error(d, 3.1 * float(s.abs().max()))
+        for o, l, pos in [(out[0, j], lse[0, j], n - 1), (out2[0, j], lse2[j, 0], n - 40), (out2[39, j], lse2[j, 39], n - 1), (out2[17, j], lse2[j, 17], n - 23)]:
+            t = s[:pos + 1]
+            assert bool(torch.isfinite(o).all()) and bool(torch.isfinite(l))
+            assert abs(float(l) - float(t.logsumexp(0))) <= ds + 1e-4 + 2.0 ** -22 * float(t.abs().max())
+            # what is out of reach of the scores' errors has no weight; the output lies within the others' values
+            close = v[:pos + 1][t >= t.max() - 2 * ds - 20]
+            assert bool((o.double() <= close.amax(0) + 2.0 ** -7 * 5).all()) and bool((o.double() >= close.amin(0) - 2.0 ** -7 * 5).all())
+
+
+def test_a_query_that_is_not_finite_stays_alone():
+    d, dt, page = 128, torch.bfloat16, 32
+    pool, k, v = filled(d, 1, page, 20, dt)
+    p = dkv.dkv_qpaged_layout(pool, 2, 8, d, 10, dtype=dt)
+    ws = workspace(p)
+    table = torch.arange(20, dtype=torch.int32, device="cuda").view(2, 10)
+    L = torch.tensor([320, 300], dtype=torch.int32, device="cuda")
+    q = randn((2, 8, d), dt, 3).cuda()
+    clean, lse = dkv.dkv_qpaged_decode(p, q, pool, table, L, workspace=ws)
+    q2 = q.clone()
+    q2[0, 3, 5], q2[1, 0, 0] = math.nan, math.inf
+    out, lse2 = dkv.dkv_qpaged_decode(p, q2, pool, table, L, workspace=ws)
+    hit = torch.zeros(2, 8, dtype=torch.bool, device="cuda")
+    hit[0, 3] = hit[1, 0] = True
+    assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse2[~hit], lse[~hit]) and not bool(torch.isfinite(out[hit]).all())
+    rows = randn((200, 8, d), dt, 4).cuda()
+    starts = torch.tensor([0, 150, 200], dtype=torch.int32, device="cuda")
+    clean, _ = dkv.dkv_qpaged_prefill(p, rows, starts, 150, pool, table, L, workspace=ws)
+    bad = rows.clone()
+    bad[70, 2, 1], bad[180, 7, 127] = math.inf, math.nan
+    out, _ = dkv.dkv_qpaged_prefill(p, bad, starts, 150, pool, table, L, workspace=ws)
+    hit = torch.zeros(200, 8, dtype=torch.bool, device="cuda")
+    hit[70, 2] = hit[180, 7] = True
+    # (rows of one warp move their references together: the same values but for a rounding of the weights)
+    assert bool(((out[~hit].double() - clean[~hit].double()).abs() <= 2.0 ** -8 * v.abs().max() * 2).all())
+    assert not bool(torch.isfinite(out[hit]).all())
+    zeros, lz = dkv.dkv_qpaged_decode(p, q * 0, pool, table, L, workspace=ws)
+    assert bool(((zeros[0, 0].double() - v[0, :320].mean(0)).abs() <= 2.0 ** -7).all())
+    assert abs(float(lz[0, 0]) - math.log(320)) < 1e-5
+    no_fault(ws)
+
+
+def test_prefill_spans_out_of_order():
+    d, dt, page = 64, torch.float16, 16
+    pool, k, v = filled(d, 2, page, 30, dt)
+    p = dkv.dkv_qpaged_layout(pool, 4, 4, d, 7)
+    ws = workspace(p)
+    table = torch.arange(28, dtype=torch.int32, device="cuda").view(4, 7)
+    L = torch.tensor([100, 90, 80, 70], dtype=torch.int32, device="cuda")
+    q = randn((60, 4, d), dt, 3).cuda()
+    good, _ = dkv.dkv_qpaged_prefill(p, q, torch.tensor([0, 20, 40, 50, 60], dtype=torch.int32, device="cuda"), 20, pool, table, L, workspace=ws)
+    no_fault(ws)
+    for starts, left_out in (([0, 20, 40, 50, 61], [3]), ([0, 20, 40, 39, 60], [2, 3]), ([-1, 20, 40, 50, 60], [0])):
+        out, _ = dkv.dkv_qpaged_prefill(p, q, torch.tensor(starts, dtype=torch.int32, device="cuda"), 20, pool, table, L, workspace=ws)
+        assert dkv.dkv_get_error(ws) == (dkv.DKV_ERR_DEVICE, dkv.DKV_DEVERR_INDEX)
+        for b, (lo, hi) in enumerate(((0, 20), (20, 40), (40, 50), (50, 60))):
+            if b not in left_out:
+                assert torch.equal(out[lo:hi], good[lo:hi])
+    out, _ = dkv.dkv_qpaged_prefill(p, q, torch.tensor([0, 20, 40, 50, 60], dtype=torch.int32, device="cuda"), 19, pool, table, L, workspace=ws)
+    assert dkv.dkv_get_error(ws)[1] == dkv.DKV_DEVERR_INDEX and not out[:40].any() and torch.equal(out[40:], good[40:])
+
+
+def test_few_queries_under_a_wide_table():
+    """The keys of few queries are cut into parts; a table many times as wide as the sequences takes the same path."""
+    d, dt, page = 128, torch.bfloat16, 64
+    pool, k, v = filled(d, 2, page, 80, dt)
+    for width in (40, 2000):
+        p = dkv.dkv_qpaged_layout(pool, 2, 12, d, width, dtype=dt)
+        ws = workspace(p)
+        table = torch.full((2, width), -1, dtype=torch.int32)
+        table[0, :40], table[1, :40] = torch.arange(40), torch.arange(40, 80)
+        L = torch.tensor([2560, 1500], dtype=torch.int32, device="cuda")
+        starts = torch.tensor([0, 9, 14], dtype=torch.int32, device="cuda")
+        q = randn((14, 12, d), dt, 5, 2.0).cuda()
+        out, lse = dkv.dkv_qpaged_prefill(p, q, starts, 9, pool, table.cuda(), L, workspace=ws)
+        no_fault(ws)
+        for row, n in ((0, 2552), (8, 2560), (9, 1496), (13, 1500)):
+            at = 0 if row < 9 else 2560
+            for h in range(2):
+                ref = exact_rows(q[row, 6 * h:6 * h + 6].double(), k[h, at:at + n], v[h, at:at + n])
+                near(out[row, 6 * h:6 * h + 6], lse[6 * h:6 * h + 6, row], ref, dt)
+
+
+# ---------------------------------------------------------------- streams, graphs, a run of them together
+
+class Server:
+    """A decoding loop as a program would write it: plan, rotate, append, attend."""
+
+    def __init__(self, B=3, hq=6, hkv=2, d=64, page=16, width=12, dt=torch.bfloat16, rows=64, window=0, sinks=0):
+        self.B, self.hq, self.hkv, self.d, self.page, self.rows, self.dt = B, hq, hkv, d, page, rows, dt
+        n_pages = B * width
+        dev = lambda *x: torch.zeros(*x, dtype=torch.int32, device="cuda")  # noqa: E731
+        self.pool = torch.full((n_pages, hkv, page * 9 * d // 8), 0xFF, dtype=torch.uint8, device="cuda")
+        self.p = dkv.dkv_qpaged_layout(self.pool, B, hq, d, width, dtype=dt, window=window, sinks=sinks)
+        self.table, self.lens, self.news = dev(B, width) - 1, dev(B), dev(B)
+        self.free = torch.randperm(n_pages, generator=torch.Generator().manual_seed(1)).int().cuda()
+        self.n_free = dev(1) + n_pages
+        self.ws = workspace(self.p)
+        self.pws = torch.zeros(dkv.dkv_paged_plan_workspace_bytes(self.p), dtype=torch.uint8, device="cuda")
+        self.slots, self.positions = torch.zeros(rows, dtype=torch.int64, device="cuda"), dev(rows)
+        self.starts, self.granted = dev(B + 1), dev(B)
+        self.gain = (1 + randn((d,), dt, 5, 0.1)).cuda()
+        self.q, self.k = (torch.zeros(rows, n, d, dtype=dt, device="cuda") for n in (hq, hkv))
+        self.qkv = torch.zeros(rows, hq + 2 * hkv, d, dtype=dt, device="cuda")
+        self.out, self.lse = torch.zeros(rows, hq, d, dtype=dt, device="cuda"), torch.zeros(hq, rows, device="cuda")
+        self.out1, self.lse1 = torch.zeros(B, hq, d, dtype=dt, device="cuda"), torch.zeros(B, hq, device="cuda")
+
+    def step(self, max_q, stream=None):
+        dkv.dkv_paged_plan(self.p, self.lens, self.news, self.free, self.n_free, self.table, self.rows, slots=self.slots,
+                           positions=self.positions, starts=self.starts, granted=self.granted, new_lens=self.lens,
+                           new_n_free=self.n_free, workspace=self.pws, stream=stream)
+        q, k, v = self.qkv.split([self.hq, self.hkv, self.hkv], 1)
+        dkv.dkv_qk_norm_rope(q, k, self.positions, 64, 1e4, q_gain=self.gain, k_gain=self.gain, q_out=self.q, k_out=self.k, stream=stream)
+        dkv.dkv_qpaged_append(self.p, self.k, v, self.pool, self.slots, workspace=self.ws, stream=stream)
+        if max_q == 1:  # every sequence has one new token: row b is sequence b's
+            dkv.dkv_qpaged_decode(self.p, self.q[:self.B], self.pool, self.table, self.lens, out=self.out1, lse=self.lse1, workspace=self.ws,
+                                  stream=stream)
+        dkv.dkv_qpaged_prefill(self.p, self.q, self.starts, max_q, self.pool, self.table, self.lens, out=self.out, lse=self.lse,
+                               workspace=self.ws, stream=stream)
+
+
+def run_server(s, steps, launch, window=0, sinks=0):
+    """steps: new tokens of each sequence (below 0: dropped); every step's outputs against attention over the rows that went in."""
+    kept = [[[], []] for _ in range(s.B)]
+    g = torch.Generator().manual_seed(9)
+    for news in steps:
+        s.news.copy_(torch.tensor(news, dtype=torch.int32))
+        s.qkv.copy_((torch.randn(*s.qkv.shape, generator=g) * 1.5).to(s.dt))
+        launch(max(max(news), 1))
+        torch.cuda.synchronize()
+        assert s.granted.tolist() == [max(n, 0) for n in news]
+        starts = s.starts.tolist()
+        q, k, v = s.q.cpu(), s.k.cpu(), s.qkv[:, s.hq + s.hkv:].cpu()
+        for b, n in enumerate(news):
+            if n < 0:
+                for x in kept[b]:
+                    del x[len(x) + n:]
+            for i in range(starts[b], starts[b + 1]):
+                assert int(s.positions[i]) == len(kept[b][0])
+                kept[b][0].append(Q.values(*Q.quantise(k[i].double())))
+                kept[b][1].append(Q.values(*Q.quantise(v[i].double())))
+            assert int(s.lens[b]) == len(kept[b][0])
+            if n <= 0:
+                continue
+            K, V = (torch.stack(x, 1) for x in kept[b])          # [hkv][tokens][d]
+            pos = torch.arange(K.shape[1] - n, K.shape[1])
+            for j in range(s.hq):
+                h = j * s.hkv // s.hq
+                rows = slice(starts[b], starts[b + 1])
+                ref = R.attend(q[rows, j].double(), K[h], V[h], pos, window, sinks)
+                size = 3.1 * (ref[2] * V[h].abs().amax(-1)).sum(-1, keepdim=True).expand(-1, s.d)
+                parts = 3.1 * float(q[rows, j].double().abs().sum(-1).max() * K[h].abs().max()) / math.sqrt(s.d)
+                size = size + 2.0 ** (11 - 32) * 3.1 * V[h].abs().amax(-1).sum()  # weights in fp16's subnormals
+                R.check_rows(s.out[rows, j], s.lse[j, rows], (*ref[:3], size, parts), s.d, s.dt, 2.0 ** -11, f"step {news} sequence {b} head {j}")
+                if max(news) == 1:
+                    assert news == [1] * s.B
+                    R.check_rows(s.out1[b:b + 1, j], s.lse1[b:b + 1, j], (*ref[:3], size, parts), s.d, s.dt, 2.0 ** -11, f"decode {b} head {j}")
+    no_fault(s.ws)
+    no_fault(s.pws)
+
+
+def test_run_of_them_together():
+    s = Server()
+    run_server(s, [[20, 5, 33], [1, 1, 1], [1, 1, 1], [0, 30, -33], [7, -20, 16], [1, 1, 1], [-28, 40, 12], [1, 1, 1]], s.step)
+    assert int(s.n_free) + sum(-(-n // s.page) for n in s.lens.tolist()) == s.B * 12
+    s = Server(window=17, sinks=2)
+    run_server(s, [[20, 5, 33], [1, 1, 1], [0, 30, 0], [1, 1, 1]], s.step, window=17, sinks=2)
+
+
+def test_run_on_another_stream_and_in_a_graph():
+    s = Server()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def on_side(max_q):
+        side.wait_stream(torch.cuda.current_stream())
+        s.step(max_q, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    run_server(s, [[20, 5, 33], [1, 1, 1], [3, 0, 2]], on_side)
+
+    s = Server()
+    s.step(1)  # (kernels are loaded before the capture; no sequence grows)
+    torch.cuda.synchronize()
+    graphs = {}
+    for max_q in (1, 64):
+        graphs[max_q] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graphs[max_q]):
+            s.step(max_q)
+    run_server(s, [[20, 5, 33], [1, 1, 1], [0, 30, -33], [7, -20, 16], [1, 1, 1], [1, 1, 1]], lambda n: graphs[1 if n == 1 else 64].replay())
+
+
+def test_outputs_allocated_in_the_given_stream():
+    d, dt, page = 128, torch.float16, 32
+    pool, k, v = filled(d, 2, page, 40, dt)
+    p = dkv.dkv_qpaged_layout(pool, 1, 8, d, 40)
+    table = torch.arange(40, dtype=torch.int32, device="cuda")[None].contiguous()
+    L = torch.tensor([1280], dtype=torch.int32, device="cuda")
+    q = randn((1, 8, d), dt, 5).cuda()
+    want, want_lse = dkv.dkv_qpaged_decode(p, q, pool, table, L)
+    starts = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    want2, _ = dkv.dkv_qpaged_prefill(p, q, starts, 1, pool, table, L)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(20):
+        busy = torch.randn(2048, 2048, device="cuda")
+        busy = busy @ busy                                  # the current stream is behind
+        out, lse = dkv.dkv_qpaged_decode(p, q, pool, table, L, stream=side)
+        out2, _ = dkv.dkv_qpaged_prefill(p, q, starts, 1, pool, table, L, stream=side)
+        side.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, want_lse) and torch.equal(out2, want2)
+
+
+def test_two_calls_at_once():
+    """Two streams, a workspace each, over one pool."""
+    d, dt, page = 128, torch.bfloat16, 64
+    pool, k, v = filled(d, 4, page, 200, dt)
+    p = dkv.dkv_qpaged_layout(pool, 2, 8, d, 100, dtype=dt)
+    table = torch.arange(200, dtype=torch.int32, device="cuda").view(2, 100)
+    L = torch.tensor([6400, 3000], dtype=torch.int32, device="cuda")
+    qs = [randn((2, 8, d), dt, s).cuda() for s in (1, 2)]
+    ws = [workspace(p) for _ in range(2)]
+    want = [dkv.dkv_qpaged_decode(p, q, pool, table, L, workspace=ws[0]) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        got = [dkv.dkv_qpaged_decode(p, q, pool, table, L, workspace=w, stream=s) for q, w, s in zip(qs, ws, streams)]
+        torch.cuda.synchronize()
+        for (a, b), (c, e) in zip(got, want):
+            assert torch.equal(a, c) and torch.equal(b, e)
+    for w in ws:
+        no_fault(w)
+
+
+def test_rows_go_on_to_the_compressed_cache():
+    """Tokens of the 4-bit pages, read back, are what the compressed cache is made of."""
+    d, hkv, page, n = 64, 2, 64, 3 * 256 + 100
+    pool, k, v = filled(d, hkv, page, 14, torch.float16)
+    p = dkv.dkv_qpaged_layout(pool, 1, 4, d, 14)
+    K, V = (torch.zeros(1, hkv, n, d, dtype=torch.float16, device="cuda") for _ in range(2))
+    dkv.dkv_qpaged_gather(p, pool, torch.arange(14, dtype=torch.int32, device="cuda")[None].contiguous(), torch.zeros(1, dtype=torch.int32, device="cuda"), K, V)
+    desc = dkv.dkv_layout(1, 4, hkv, d, 3, 100, 16, 32)
+    cache = dkv.dkv_compress_layout(desc, K, V)
+    q = randn((1, 4, d), torch.float16, 3).cuda()
+    out, lse, _ = dkv.dkv_decode_attend(desc, q, cache, 3)
+    exact, _ = dkv.dkv_qpaged_decode(dkv.dkv_qpaged_layout(pool, 1, 4, d, 14), q, pool, torch.arange(14, dtype=torch.int32, device="cuda")[None].contiguous(),
+                                     torch.tensor([n], dtype=torch.int32, device="cuda"))
+    assert bool(torch.isfinite(out).all()) and tuple(out.shape) == (1, 4, d) and tuple(exact.shape) == (1, 4, d)
