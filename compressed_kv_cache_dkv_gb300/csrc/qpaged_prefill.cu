@@ -411,41 +411,46 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
     const QpRow me = qp_row(p, kvh, h0, row0, qs.n, g, row);
     const int pos = qs.off + me.token;
     float slog2 = a.scale_log2;
-    if (n > 0) {  // Q to shared memory, D / 8 lanes a row
-      constexpr int L = D / 8, kAt = 32 / L, kDeep = 4;
-#pragma unroll 1
-      for (int i0 = 0; i0 < 32 / kAt; i0 += kDeep) {
-        uint4 v[kDeep];
-#pragma unroll
-        for (int x = 0; x < kDeep; ++x) {
-          const QpRow r = qp_row(p, kvh, h0, row0, qs.n, g, 32 * rw + (i0 + x) * kAt + lane / L);
-          v[x] = make_uint4(0, 0, 0, 0);
-          if (r.live)
-            v[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q.q) + (int64_t)(span.start + r.token) * p.q.qs.token +
-                                                        (int64_t)r.head * p.q.qs.head + 8 * (lane % L)));
+    if (n > 0) {
+      // Q to shared memory, D / 8 lanes a row; there each thread brings its row into the order of the codes, and into
+      // fp16's range.  (Not unrolled further: straight code that runs once for a CTA waits for its instructions.)
+      constexpr int L = D / 8, kAt = 32 / L;
+      const uint32_t to = sb + g * S::kQ;
+#pragma unroll 4
+      for (int i = 0; i < L; ++i) {
+        const int x = 32 * rw + i * kAt + lane / L;
+        const QpRow r = qp_row(p, kvh, h0, row0, qs.n, g, x);
+        const T* from = static_cast<const T*>(p.q.q) + 8 * (lane % L);
+        if (r.live) from += (int64_t)(span.start + r.token) * p.q.qs.token + (int64_t)r.head * p.q.qs.head;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + sw128(kQpM, x, lane % L)), "l"(from), "r"(r.live ? 16 : 0) : "memory");
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+      float up = 1.f;
+      if (Num<T>::kUmma == 1) {
+        uint32_t top = 0;  // the row's largest magnitudes, by their bits
+#pragma unroll 4
+        for (int c = 0; c < L; ++c) {
+          const uint4 v = lds128(to + sw128(kQpM, row, c));
+          top = __vmaxu2(__vmaxu2(top, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
+          top = __vmaxu2(__vmaxu2(top, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
         }
+        const int ex = max((int)(max(top & 0xffffu, top >> 16) >> 7), 15);  // all < 2^(ex - 126)
+        up = __uint_as_float((uint32_t)(268 - ex) << 23);                    // 2^(141 - ex): below 2^15 then
+        slog2 *= __uint_as_float((uint32_t)(ex - 14) << 23);                 // 2^(ex - 141)
+      }
+#pragma unroll 4
+      for (int c = 0; c < L; ++c) {
+        const uint32_t at = to + sw128(kQpM, row, c);
+        const uint4 v = lds128(at);
+        uint32_t w[4] = {__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632)};
+        if (Num<T>::kUmma == 1)
 #pragma unroll
-        for (int x = 0; x < kDeep; ++x) {
-          float f[8];
-          const T* h = reinterpret_cast<const T*>(&v[x]);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = Num<T>::to_float(h[e]);
-          if (Num<T>::kUmma == 1) {  // bf16: into fp16's range
-            float top = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
-#pragma unroll
-            for (int o = 1; o < L; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const int ex = max((int)(__float_as_uint(top) >> 23), 15);     // top < 2^(ex - 126)
-            const float up = __uint_as_float((uint32_t)(268 - ex) << 23);  // 2^(141 - ex): top up < 2^15
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] *= up;
-            const int mine = __shfl_sync(0xffffffffu, ex, lane % kAt * L);
-            if (lane / kAt == i0 + x) slog2 = a.scale_log2 * __uint_as_float((uint32_t)(mine - 14) << 23);  // 2^(ex - 141)
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = mul2(make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u)), make_float2(up, up));
+            w[e] = pack_half2(f.x, f.y);
           }
-          sts128(sb + g * S::kQ + sw128(kQpM, 32 * rw + (i0 + x) * kAt + lane / L, lane % L),
-                 make_uint4(pack_half2(f[0], f[4]), pack_half2(f[1], f[5]), pack_half2(f[2], f[6]), pack_half2(f[3], f[7])));
-        }
+        sts128(at, make_uint4(w[0], w[1], w[2], w[3]));
       }
       fence_proxy_async();
       __syncwarp();
@@ -508,7 +513,7 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
     // whole rows of the output.
     const uint32_t stage = sb + g * S::kQ;
     const int64_t rec = (((int64_t)b * gridDim.z + tile) * (gridDim.x / p.parts) + hg) * p.parts + part;
-#pragma unroll
+#pragma unroll 1  // (short code, as above)
     for (int c = 0; c < D / 32; ++c) {
       uint32_t o[32];
       if (n > 0) {
