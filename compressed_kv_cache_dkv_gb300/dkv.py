@@ -743,9 +743,10 @@ def dkv_paged_plan(p, lens: torch.Tensor, news: torch.Tensor, free_pages: torch.
         with _place(dev, stream):
             return dkv_paged_plan(p, lens, news, free_pages, n_free, page_table, rows, slots, positions, starts, granted,
                                   new_lens, new_n_free, workspace)
-    _int32("dkv_paged_plan", rows)
-    b, width, room = p.batch, p.max_pages, max(rows, 0)
-    each, row = (b,), (room,)
+    if not -0x80000000 <= rows <= 0x7fffffff:
+        raise DkvError(DKV_ERR_ARG, "dkv_paged_plan")
+    b, width = p.batch, p.max_pages
+    each, row = (b,), (rows if rows > 0 else 0,)
     if slots is None:
         slots = torch.empty(row, dtype=_I64, device=dev)
     if positions is None:
@@ -824,7 +825,8 @@ def dkv_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, 
     rows, hq, d = q.shape
     hkv = k.shape[1]
     q_shape, k_shape = (rows, hq, d), (rows, hkv, d)
-    _int32("dkv_qk_norm_rope", rows, hq, hkv, d, rope_dims)
+    if not (rows <= 0x7fffffff and -0x80000000 <= rope_dims <= 0x7fffffff):
+        raise DkvError(DKV_ERR_ARG, "dkv_qk_norm_rope")
     qs, ks = q.stride(), k.stride()
     if qs[2] != 1:
         _wrong_rows("q", q, dt, q_shape, dev)
@@ -832,9 +834,10 @@ def dkv_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, 
         _wrong_rows("k", k, dt, k_shape, dev)
     if positions.dtype is not _I32 or positions.shape != (rows,) or positions.get_device() != dev or not positions.is_contiguous():
         _wrong("positions", positions, _I32, (rows,), dev)
-    for what, g in (("q_gain", q_gain), ("k_gain", k_gain)):
-        if g is not None and (g.dtype is not dt or g.shape != (d,) or g.get_device() != dev or not g.is_contiguous()):
-            _wrong(what, g, dt, (d,), dev)
+    if q_gain is not None and (q_gain.dtype is not dt or q_gain.shape != (d,) or q_gain.get_device() != dev or not q_gain.is_contiguous()):
+        _wrong("q_gain", q_gain, dt, (d,), dev)
+    if k_gain is not None and (k_gain.dtype is not dt or k_gain.shape != (d,) or k_gain.get_device() != dev or not k_gain.is_contiguous()):
+        _wrong("k_gain", k_gain, dt, (d,), dev)
     if q_out is None:
         q_out = torch.zeros(q_shape, dtype=dt, device=dev)
     if k_out is None:
@@ -1058,7 +1061,8 @@ def dkv_qpaged_prefill(p: dkv_qpaged, q: torch.Tensor, starts: torch.Tensor, max
     if _elsewhere(q, dev) or stream is not None:
         with _place(dev, stream):
             return dkv_qpaged_prefill(p, q, starts, max_q, cache, page_table, lens, out, lse, workspace)
-    _int32("dkv_qpaged_prefill", max_q)
+    if not -0x80000000 <= max_q <= 0x7fffffff:
+        raise DkvError(DKV_ERR_ARG, "dkv_qpaged_prefill")
     g, rows = _qgeometry(p), q.shape[0]
     shape = (rows, g.heads, g.d)
     s = q.stride()
