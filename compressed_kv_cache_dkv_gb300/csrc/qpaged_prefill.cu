@@ -230,29 +230,73 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile uint32_t* bad_blocks = tmem_slot + 1;  // [stage] blocks on bad pages
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < S::kR; ++i) {
-      mbar_init(&kv_full[i], 4);  // a lane of each warp that makes values
-      mbar_init(&o_done[i], 1);
-      mbar_init(&o_done[S::kR + i], 1);
+  // Warps 8-15 set up what all wait on, and look up the first pages; meanwhile the others send for their queries.
+  constexpr int kQLanes = D / 8, kQAt = 32 / kQLanes;  // lanes of a query row, rows at once
+  const int rows = min(a.page_mask + 1, kQpN), runs = kQpN / rows, bpr = rows / kQBlock, batch = 32 / runs;
+  uint64_t src = 0;  // warp 8: a lane looks after one run of slots of a page (a tile has 64 / rows of them), one look for a batch of tiles
+  uint32_t bytes = 0, dst = 0, sum = 0, none = 0;
+  auto look = [&](int j) {
+    const int k = j + lane / runs, r = lane % runs, first = key_of(k) + r * rows;
+    int b0 = bpr, b1 = 0;  // blocks with a visible token
+    for (int i = 0; i < bpr; ++i) {
+      const int t = first + i * kQBlock;
+      if (k < nt && t < ks.hi && (t + kQBlock > ks.lo || t < a.sinks)) {
+        b0 = min(b0, i);
+        b1 = i + 1;
+      }
     }
-    for (int i = 0; i < S::kRaw; ++i) {
-      mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], 4);
+    const int page = b0 < b1 ? paged_page(a, b, first) : 0;
+    const bool bad = page >= a.n_pages;
+    bytes = b0 < b1 && !bad ? (uint32_t)(b1 - b0) * qblock_bytes(D) : 0u;
+    if (bytes)
+      src = reinterpret_cast<uint64_t>(p.cache) + page * a.stride_page + kvh * a.stride_head +
+            (int64_t)((first & a.page_mask) / kQBlock + b0) * qblock_bytes(D);
+    dst = (uint32_t)(r * bpr + b0) * qblock_bytes(D);
+    none = __ballot_sync(0xffffffffu, bad);
+    sum = bytes;
+    for (int o = 1; o < runs; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  };
+  if (warp >= 8) {
+    if (threadIdx.x == 9 * 32) {
+      for (int i = 0; i < S::kR; ++i) {
+        mbar_init(&kv_full[i], 4);  // a lane of each warp that makes values
+        mbar_init(&o_done[i], 1);
+        mbar_init(&o_done[S::kR + i], 1);
+      }
+      for (int i = 0; i < S::kRaw; ++i) {
+        mbar_init(&raw_full[i], 1);
+        mbar_init(&raw_empty[i], 4);
+      }
+      for (int i = 0; i < 4; ++i) {
+        mbar_init(&s_full[i], 1);
+        mbar_init(&p_full[i], 4);  // a lane of each warp
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&q_full[i], 4);
+        mbar_init(&drain[i], 1);
+      }
+      fence_mbar_init();
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);  // a lane of each warp
+    if (warp == 11) tc_alloc<512>(tmem_slot);
+    if (warp == 8) look(0);
+    tc_fence_before();
+    named_bar_sync(1, kQpThreads / 2);
+    asm volatile("barrier.cta.arrive 2, %0;" ::"n"(kQpThreads) : "memory");
+  } else {
+    const int g = warp >> 2;
+    if ((g ? nB : nA) > 0) {
+#pragma unroll 4
+      for (int i = 0; i < kQLanes; ++i) {
+        const int x = 32 * (warp & 3) + i * kQAt + lane / kQLanes;
+        const QpRow r = qp_row(p, kvh, h0, row0, qs.n, g, x);
+        const T* from = static_cast<const T*>(p.q.q) + 8 * (lane % kQLanes);
+        if (r.live) from += (int64_t)(span.start + r.token) * p.q.qs.token + (int64_t)r.head * p.q.qs.head;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sb + g * S::kQ + sw128(kQpM, x, lane % kQLanes)), "l"(from), "r"(r.live ? 16 : 0)
+                     : "memory");
+      }
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 4);
-      mbar_init(&drain[i], 1);
-    }
-    fence_mbar_init();
+    named_bar_sync(2, kQpThreads);
   }
-  if (warp == 0) tc_alloc<512>(tmem_slot);
-  tc_fence_before();
-  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   bool ok = true;
@@ -304,35 +348,12 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
     regs_dec<kQpRegsIssue>();
     if (warp == 8) {
       // =========================== the tiles' bytes
-      // A lane looks after one run of slots of a page (a tile has 64 / rows of them): one look at the page
-      // table for a batch of tiles.
       const uint32_t el = elect_one();
-      const int rows = min(a.page_mask + 1, kQpN), runs = kQpN / rows, bpr = rows / kQBlock, batch = 32 / runs;
-      uint64_t src = 0;
-      uint32_t bytes = 0, dst = 0, sum = 0, none = 0;
       int j = 0;
       for (int in = 0; j < nt; ++j, ++in) {
-        if (j % batch == 0) {
+        if (in == batch) {
+          look(j);
           in = 0;
-          const int k = j + lane / runs, r = lane % runs, first = key_of(k) + r * rows;
-          int b0 = bpr, b1 = 0;  // blocks with a visible token
-          for (int i = 0; i < bpr; ++i) {
-            const int t = first + i * kQBlock;
-            if (k < nt && t < ks.hi && (t + kQBlock > ks.lo || t < a.sinks)) {
-              b0 = min(b0, i);
-              b1 = i + 1;
-            }
-          }
-          const int page = b0 < b1 ? paged_page(a, b, first) : 0;
-          const bool bad = page >= a.n_pages;
-          bytes = b0 < b1 && !bad ? (uint32_t)(b1 - b0) * qblock_bytes(D) : 0u;
-          if (bytes)
-            src = reinterpret_cast<uint64_t>(p.cache) + page * a.stride_page + kvh * a.stride_head +
-                  (int64_t)((first & a.page_mask) / kQBlock + b0) * qblock_bytes(D);
-          dst = (uint32_t)(r * bpr + b0) * qblock_bytes(D);
-          none = __ballot_sync(0xffffffffu, bad);
-          sum = bytes;
-          for (int o = 1; o < runs; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         }
         const int st = j % S::kRaw;
         if (j >= S::kRaw) ok = mbar_wait(&raw_empty[st], (uint32_t)((j / S::kRaw - 1) & 1), a.err);
@@ -412,18 +433,10 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
     const int pos = qs.off + me.token;
     float slog2 = a.scale_log2;
     if (n > 0) {
-      // Q to shared memory, D / 8 lanes a row; there each thread brings its row into the order of the codes, and into
-      // fp16's range.  (Not unrolled further: straight code that runs once for a CTA waits for its instructions.)
-      constexpr int L = D / 8, kAt = 32 / L;
+      // Each thread brings its row of Q into the order of the codes, and into fp16's range.  (Not unrolled further:
+      // straight code that runs once for a CTA waits for its instructions.)
+      constexpr int L = kQLanes;
       const uint32_t to = sb + g * S::kQ;
-#pragma unroll 4
-      for (int i = 0; i < L; ++i) {
-        const int x = 32 * rw + i * kAt + lane / L;
-        const QpRow r = qp_row(p, kvh, h0, row0, qs.n, g, x);
-        const T* from = static_cast<const T*>(p.q.q) + 8 * (lane % L);
-        if (r.live) from += (int64_t)(span.start + r.token) * p.q.qs.token + (int64_t)r.head * p.q.qs.head;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + sw128(kQpM, x, lane % L)), "l"(from), "r"(r.live ? 16 : 0) : "memory");
-      }
       asm volatile("cp.async.wait_all;" ::: "memory");
       __syncwarp();
       float up = 1.f;
@@ -559,7 +572,7 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 0) tc_free<512>(tmem);
+  if (warp == 11) tc_free<512>(tmem);
 }
 
 // The parts of a row joined: weights l_part 2^(ref_part - M), in part order.  A warp per row.
