@@ -12,6 +12,10 @@
 // into the last product.  A warp keeps these of its token and walks the heads in rounds of kRotDepth rows for each of
 // its row groups, the next round's rows on their way meanwhile.  Bound by memory: 4 d bytes a head, 6 d for a key that
 // also goes into a page.
+//
+// Measured: 16384 tokens of 32 query and 8 KV heads, d 128, bf16, keys and values into pages too (436 MB): 82 us, 5.3
+// TB/s, 0.79 of the measured copy rate (146 without the next round on its way, gains and norm as products of their
+// own).  16 tokens of 12 and 2 heads: 4.3 us in a graph.
 #include "paged_tc.cuh"
 #include "qpaged.cuh"
 

@@ -8,13 +8,19 @@
 // exact in fp32 (integers below 2^12, powers of two), and a code is round((x / u - lo) / step) without error: the
 // quotient only proposes k, and x / u is compared with the border lo + (k + 1/2) step, a multiple of 1/2.
 //
-// Bound by memory: 4 d bytes in and 9/8 d out a row and head (the gather the other way round).
+// Bound by instructions, 180 for a warp's 256 values (append: 0.78 of the issue slots), at 0.4 to 0.5 of the memory's
+// rate: 4 d bytes in and 9/8 d out a row and head, the gather the other way round.  Minima and maxima are taken on
+// pairs, the grid without conversions, quotient and border two at a time.
+//
+// Measured: 8 prompts of 700 to 4096 tokens, 8 KV heads, d 128, bf16: 33 us in (106 MB; 66 with a quotient, a floor
+// and conversions for each value), 21 us back.  One token of 64 sequences: 5.4 us for both in a graph.
 #include "paged_tc.cuh"
 #include "qpaged.cuh"
 
 namespace dkv {
 namespace {
 
+// (four pieces a thread: 60 us for both calls on the prompts, 55 with two)
 constexpr int kQaThreads = 256, kQaVec = 2;
 constexpr float kQaMost = 61440.f;  // above it lo + 15 step could leave fp16
 

@@ -10,8 +10,11 @@
 //   S = C_K q    mma.sync m16n8k16, tokens in M, heads in N; a token's 32 bytes a group are a lane's operand as
 //                they lie, with q's channels in the same order
 //   o = C_V^T w  channels in M; two tokens' words interleaved by byte permutes give the pairs along k
-// q is brought to at most 2^15 by a power of two (bf16 queries become fp16 without loss above 2^-24 of the largest),
-// w = p s 2^-E with a running power of two E over the scales seen, as the sum of two fp16 values (22 bits).
+// q is brought to at most 2^15 by a power of two, so that it is an fp16 operand whatever its type (channels above 2^-25
+// of the largest without loss).  w = p s 2^-E, with a running power of two E over the scales seen, is rounded once to
+// fp16 (relative error 2^-11).  That rounding falls on codes less 8 (the sum of the rounded weights, times 8, goes
+// off again, and the bias is b + 8 s), so that it is one of about the size of the values, as in the 16-bit prefill; a
+// second fp16 value for what the first leaves took 9 % longer (16 of 64k: 77.8 us, 71.6 without).
 //
 // The visible tokens of a sequence are cut into 32-token tiles; the tiles of all (sequence, KV head) units in a row
 // are dealt out evenly, to CTAs and in them to warps.  A warp walks its run of tiles unit by unit with stages, copies
@@ -20,6 +23,15 @@
 // what lies in several is left in shared memory (a warp's last unit in its own stages, which are free by then, its
 // first one beside them) and merged once, at the CTA's end; units that lie in several CTAs' runs leave a record for
 // each, and the CTA that is last to leave one merges them in run order, so that equal calls give equal bits.
+//
+// Bound: memory at 9/8 d bytes a token and KV head; right beside it the instructions that cut codes out of words and
+// scale weights (290 a warp for 16 tokens; 0.56 of the issue slots, 0.5 of the integer pipe).  What it took, on 16
+// sequences of 64k tokens, 2 KV heads, d 128 (302 MB, floor 45 us): one producer warp with a page look-up for each
+// tile 157 us; a look-up for a batch of tiles 96; every warp its own tiles and copies, sixteen warps 78; one fp16
+// weight, biases by a product, packed arithmetic 72; one merge a CTA, the join in the same grid 68.  The loop
+// streams at 5.8 TB/s (0.87 of the measured copy rate); 4 us at the start (lengths, then the page table, then
+// the first copies) and 6 at the end (uneven finish, merge, join) are what is left.  64 sequences of 300 to 8000
+// under a window of 4096, 8 KV heads, pages of 16 (237 MB): 65 us.  One of 1000 tokens: 9.9 us in a graph.
 #include "paged_tc.cuh"
 #include "qpaged.cuh"
 
@@ -32,7 +44,7 @@ constexpr int kQdThreads = 32 * kQdWarps;
 constexpr int kQdLeast = 4;  // tiles of a CTA, as long as there are enough for all
 // Weights are 2^(score - ref).  A head's reference lies kQdShift below a maximum and moves only when a score exceeds
 // that by kQdSlack (at once where scores are so large that their rounding shows): weights are at most 2^15, and those
-// down to e^-18 of the largest keep 11 bits in the lower of the two fp16 values too.
+// down to e^-14 of the largest keep 11 bits.
 constexpr float kQdShift = 7.f, kQdSlack = 8.f, kQdLarge = 0x1p20f;
 
 template <int D>
