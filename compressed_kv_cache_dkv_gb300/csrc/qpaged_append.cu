@@ -1,6 +1,6 @@
 // dkv_qpaged_append: new K and V rows into pages in 4 bits; dkv_qpaged_gather: rows of the cache back in 16 bits.
 //
-// Eight lanes share a group of 64 channels, eight channels (16 bytes in, a 32-bit word of codes out) each.
+// Four lanes share a group of 64 channels, sixteen channels (32 bytes in, two 32-bit words of codes out) each.
 // The grid u of a group: fp16 numbers are u = 2^(e - 10) apart below 2^(e + 1), e the exponent of 65/64 of the
 // group's largest magnitude L.  With lo = round(min / u), n = round(max / u) - lo, step = ceil(n / 15) every
 // value (lo + code * step) u lies on that grid, and below 2^(e + 1): lo + 15 step <= L / u + 1/2 + 15 and
@@ -8,20 +8,22 @@
 // exact in fp32 (integers below 2^12, powers of two), and a code is round((x / u - lo) / step) without error: the
 // quotient only proposes k, and x / u is compared with the border lo + (k + 1/2) step, a multiple of 1/2.
 //
-// Bound by instructions, 180 for a warp's 256 values (append: 0.78 of the issue slots), at 0.4 to 0.5 of the memory's
-// rate: 4 d bytes in and 9/8 d out a row and head, the gather the other way round.  Minima and maxima are taken on
-// pairs, the grid without conversions, quotient and border two at a time.
+// Bound by instructions, 122 for 256 values (append: 0.66 of the issue slots), at 0.6 of the memory's rate: 4 d bytes in
+// and 9/8 d out a row and head, the gather the other way round.  Minima and maxima are taken on pairs, the grid
+// without conversions, quotient and border two at a time.
 //
-// Measured: 8 prompts of 700 to 4096 tokens, 8 KV heads, d 128, bf16: 33 us in (106 MB; 66 with a quotient, a floor
-// and conversions for each value), 21 us back.  One token of 64 sequences: 5.4 us for both in a graph.
+// Measured: 8 prompts of 700 to 4096 tokens, 8 KV heads, d 128, bf16: 27 us in (106 MB; 66 with a quotient, a floor
+// and conversions for each value, 33 with eight lanes a group), 21 us back.  One token of 64 sequences: 5.4 us for
+// both in a graph.
 #include "paged_tc.cuh"
 #include "qpaged.cuh"
 
 namespace dkv {
 namespace {
 
-// (four pieces a thread: 60 us for both calls on the prompts, 55 with two)
-constexpr int kQaThreads = 256, kQaVec = 2;
+// Two rows a thread take 39 us instead of 27 to write the prompts above (89 registers).  Read back, two tokens of eight
+// channels a thread take 21 us; sixteen channels, whose stores then leave gaps, 26.
+constexpr int kQaThreads = 256, kQgVec = 2;
 constexpr float kQaMost = 61440.f;  // above it lo + 15 step could leave fp16
 
 __device__ inline float2 unpack2(uint32_t x, __half) { return __half22float2(*reinterpret_cast<__half2*>(&x)); }
@@ -68,54 +70,70 @@ __device__ inline Grid grid_of(float lo, float hi) {
   return g;
 }
 
+struct Rows16 {
+  uint32_t w[8];  // sixteen channels
+};
 struct Quantised {
-  uint32_t codes, param;  // of a lane's eight channels, and of the group: (scale, bias) as two halves
-  bool odd;               // a value was not finite or too large
+  uint32_t codes[2], param;  // of a lane's sixteen channels, and of the group: (scale, bias) as two halves
+  bool odd;                  // a value was not finite or too large
 };
 
 // A group with values that are not finite or too large, or with a step of at most one spacing: element by element.
 template <typename T>
-__device__ __noinline__ Quantised quantise_rare(uint4 in, uint32_t lanes) {
-  float x[8], lo = INFINITY, hi = -INFINITY;
-  const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+__device__ __noinline__ Quantised quantise_rare(Rows16 in, uint32_t lanes) {
+  float lo = INFINITY, hi = -INFINITY;
   bool bad = false;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 f = unpack2(w[i / 2], T());
+  auto value = [&](int i) {
+    const float2 f = unpack2(in.w[i / 2], T());
     const float y = i & 1 ? f.y : f.x;
     bad |= !(fabsf(y) <= kQaMost);
-    x[i] = y != y ? 0.f : fminf(fmaxf(y, -kQaMost), kQaMost);
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
+    return y != y ? 0.f : fminf(fmaxf(y, -kQaMost), kQaMost);
+  };
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float x = value(i);
+    lo = fminf(lo, x);
+    hi = fmaxf(hi, x);
   }
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
+  for (int o = 1; o < 4; o <<= 1) {
     lo = fminf(lo, __shfl_xor_sync(lanes, lo, o));
     hi = fmaxf(hi, __shfl_xor_sync(lanes, hi, o));
   }
   const Grid g = grid_of(lo, hi);
-  const float inv = g.inv, r = g.st > 0.f ? 1.f / g.st : 0.f;
-  uint32_t codes = 0;
+  const float r = g.st > 0.f ? 1.f / g.st : 0.f;
+  Quantised q;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float t = x[i] * inv, k = floorf((t - g.b) * r), border = fmaf(k + 0.5f, g.st, g.b);
-    int c = (int)k;
-    c += t > border || (t == border && (c & 1));
-    codes |= (uint32_t)min(max(c, 0), 15) << (4 * i);
+  for (int w = 0; w < 2; ++w) {
+    q.codes[w] = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float t = value(8 * w + i) * g.inv, k = floorf((t - g.b) * r), border = fmaf(k + 0.5f, g.st, g.b);
+      int c = (int)k;
+      c += t > border || (t == border && (c & 1));
+      q.codes[w] |= (uint32_t)min(max(c, 0), 15) << (4 * i);
+    }
+    if (g.st == 0.f) q.codes[w] = 0;
   }
-  return {g.st > 0.f ? codes : 0u, pack_half2(g.st * g.u, g.b * g.u), bad};
+  q.param = pack_half2(g.st * g.u, g.b * g.u);
+  q.odd = bad;
+  return q;
 }
 
-// A lane's eight channels of a group.
+// A lane's sixteen channels of a group.
 template <typename T>
-__device__ inline Quantised quantise(const uint4& in) {
-  const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+__device__ inline Quantised quantise(const Rows16& in) {
   // minimum and minus the maximum, two values a register
   const T t = T();
-  const uint32_t lo2 = min2(min2(w[0], w[1], t), min2(w[2], w[3], t), t), hi2 = max2(max2(w[0], w[1], t), max2(w[2], w[3], t), t);
+  uint32_t lo2 = in.w[0], hi2 = in.w[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    lo2 = min2(lo2, in.w[i], t);
+    hi2 = max2(hi2, in.w[i], t);
+  }
   uint32_t m = min2(__byte_perm(lo2, hi2, 0x5410) ^ 0x80000000u, __byte_perm(lo2, hi2, 0x7632) ^ 0x80000000u, t);
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) m = min2(m, __shfl_xor_sync(0xffffffffu, m, o), t);
+  for (int o = 1; o < 4; o <<= 1) m = min2(m, __shfl_xor_sync(0xffffffffu, m, o), t);
   const float2 range = unpack2(m, t);
   const float lo = range.x, hi = -range.y;
   const Grid g = grid_of(lo, hi);
@@ -129,70 +147,68 @@ __device__ inline Quantised quantise(const uint4& in) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(g.st));
   const float ri = r * g.inv, off = fmaf(-g.b, r, -0.5f), su = g.st * g.u, mid = fmaf(0.5f, g.st, g.b) * g.u;
-  uint32_t z[8];
+  Quantised q;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 x = unpack2(w[i], t);
-    const float2 k = add2(fma2(x, make_float2(ri, ri), make_float2(off, off)), make_float2(kMagic, kMagic));
-    const float2 border = fma2(add2(k, make_float2(-kMagic, -kMagic)), make_float2(su, su), make_float2(mid, mid));
-    const float2 d = add2(border, make_float2(-x.x, -x.y));
-    z[2 * i] = __float_as_uint(k.x);
-    z[2 * i + 1] = __float_as_uint(k.y);
-    z[2 * i] += (__float_as_uint(d.x) - (z[2 * i] & 1u)) >> 31;
-    z[2 * i + 1] += (__float_as_uint(d.y) - (z[2 * i + 1] & 1u)) >> 31;
+  for (int w = 0; w < 2; ++w) {
+    uint32_t z[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = unpack2(in.w[4 * w + i], t);
+      const float2 k = add2(fma2(x, make_float2(ri, ri), make_float2(off, off)), make_float2(kMagic, kMagic));
+      const float2 border = fma2(add2(k, make_float2(-kMagic, -kMagic)), make_float2(su, su), make_float2(mid, mid));
+      const float2 d = add2(border, make_float2(-x.x, -x.y));
+      z[2 * i] = __float_as_uint(k.x);
+      z[2 * i + 1] = __float_as_uint(k.y);
+      z[2 * i] += (__float_as_uint(d.x) - (z[2 * i] & 1u)) >> 31;
+      z[2 * i + 1] += (__float_as_uint(d.y) - (z[2 * i + 1] & 1u)) >> 31;
+    }
+    // the low bytes are codes
+    const uint32_t b0 = z[1] * 16 + z[0], b1 = z[3] * 16 + z[2], b2 = z[5] * 16 + z[4], b3 = z[7] * 16 + z[6];
+    q.codes[w] = __byte_perm(__byte_perm(b0, b1, 0x0040), __byte_perm(b2, b3, 0x0040), 0x5410);
   }
-  // the low bytes are codes
-  const uint32_t b0 = z[1] * 16 + z[0], b1 = z[3] * 16 + z[2], b2 = z[5] * 16 + z[4], b3 = z[7] * 16 + z[6];
-  return {__byte_perm(__byte_perm(b0, b1, 0x0040), __byte_perm(b2, b3, 0x0040), 0x5410), pack_half2(su, g.b * g.u), false};
+  q.param = pack_half2(su, g.b * g.u);
+  q.odd = false;
+  return q;
+}
+__device__ inline Rows16 load16(const uint4* at) {
+  const uint4 x = __ldg(at), y = __ldg(at + 1);
+  return {{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w}};
 }
 
-// A thread takes eight channels of a row's key and of its value.
+// A thread takes sixteen channels of a row's key and of its value.
 template <typename T, int D>
 __global__ void __launch_bounds__(kQaThreads) qpaged_append_kernel(PagedArgs a, const uint4* __restrict__ K,
                                                                   const uint4* __restrict__ V, dkv_strides ns,
                                                                   int n_rows, const int64_t* __restrict__ slots,
                                                                   uint8_t* __restrict__ cache) {
-  constexpr int R = D / 8;  // lanes of a row
+  constexpr int R = D / 16;  // lanes of a row
   const int64_t n_slots = (int64_t)a.n_pages << a.page_shift;
-  const int c = threadIdx.x % R, lane8 = threadIdx.x & 7, g = c / 8;
-  // row and head of the thread's first piece; the next one is kStep of them on
-  constexpr int kStep = kQaThreads / R;
-  const uint32_t pair = blockIdx.x * (kStep * kQaVec) + threadIdx.x / R;
-  uint32_t row = pair / (uint32_t)a.Hkv;
-  int h = (int)(pair - row * (uint32_t)a.Hkv);
-  const int dr = kStep / a.Hkv, dh = kStep - dr * a.Hkv;
-  uint4 k[kQaVec], v[kQaVec];
-  uint8_t* to[kQaVec];  // of K's codes; null: nothing to write
-  int tok[kQaVec];
-#pragma unroll
-  for (int x = 0; x < kQaVec; ++x, row += dr, h += dh) {
-    if (h >= a.Hkv) { h -= a.Hkv; ++row; }
-    k[x] = v[x] = make_uint4(0, 0, 0, 0);
-    to[x] = nullptr;
-    tok[x] = 0;
-    if (row >= (uint32_t)n_rows) continue;
+  const int c = threadIdx.x % R, lane4 = threadIdx.x & 3, g = c / 4;
+  const uint32_t pair = blockIdx.x * (kQaThreads / R) + threadIdx.x / R, row = pair / (uint32_t)a.Hkv;
+  const int h = (int)(pair - row * (uint32_t)a.Hkv);
+  Rows16 k = {}, v = {};
+  uint8_t* to = nullptr;  // the block; null: nothing to write
+  int tok = 0;
+  if (row < (uint32_t)n_rows) {
     const int64_t slot = __ldg(slots + row);
-    if (slot < 0 || slot >= n_slots) {
-      if (slot != -1) raise_error(a.err, DKV_DEVERR_INDEX);
-      continue;
+    if (slot >= 0 && slot < n_slots) {
+      const int64_t at = (row * ns.token + h * ns.head) / 8 + 2 * c;
+      k = load16(K + at);
+      v = load16(V + at);
+      const int t = (int)slot & a.page_mask;
+      tok = t % kQBlock;
+      to = cache + (slot >> a.page_shift) * a.stride_page + h * a.stride_head + (t / kQBlock) * qblock_bytes(D);
+    } else if (slot != -1) {
+      raise_error(a.err, DKV_DEVERR_INDEX);
     }
-    const int64_t at = (row * ns.token + h * ns.head) / 8 + c;
-    k[x] = __ldg(K + at);
-    v[x] = __ldg(V + at);
-    const int t = (int)slot & a.page_mask;
-    tok[x] = t % kQBlock;
-    to[x] = cache + (slot >> a.page_shift) * a.stride_page + h * a.stride_head + (t / kQBlock) * qblock_bytes(D);
   }
-#pragma unroll
-  for (int x = 0; x < kQaVec; ++x) {
-    const Quantised qk = quantise<T>(k[x]), qv = quantise<T>(v[x]);
-    if (!to[x]) continue;
-    if (qk.odd || qv.odd) raise_error(a.err, DKV_DEVERR_RANGE);
-    uint8_t* codes = to[x] + qcode_off(D, 0, g, tok[x]) + lane8 * 4;
-    *reinterpret_cast<uint32_t*>(codes) = qk.codes;
-    *reinterpret_cast<uint32_t*>(codes + 8 * D) = qv.codes;
-    if (lane8 < 2) *reinterpret_cast<uint32_t*>(to[x] + qparam_off(D, lane8, g, tok[x])) = lane8 ? qv.param : qk.param;
-  }
+  const Quantised qk = quantise<T>(k), qv = quantise<T>(v);
+  if (!to) return;
+  if (qk.odd || qv.odd) raise_error(a.err, DKV_DEVERR_RANGE);
+  uint8_t* codes = to + qcode_off(D, 0, g, tok) + lane4 * 8;
+  *reinterpret_cast<uint2*>(codes) = make_uint2(qk.codes[0], qk.codes[1]);
+  *reinterpret_cast<uint2*>(codes + 8 * D) = make_uint2(qv.codes[0], qv.codes[1]);
+  if (lane4 < 2) *reinterpret_cast<uint32_t*>(to + qparam_off(D, lane4, g, tok)) = lane4 ? qv.param : qk.param;
 }
 
 // Eight codes as values in order: fp16 ones, exactly; bf16 ones are their roundings.
@@ -229,11 +245,11 @@ __global__ void __launch_bounds__(kQaThreads) qpaged_gather_kernel(PagedArgs a, 
     }
   }
   const int64_t p0 = __ldg(first + b);
-  const int c = threadIdx.x % R, i0 = (int)(blockIdx.x / (unsigned)a.Hkv) * kQaVec * (kQaThreads / R) + threadIdx.x / R;
+  const int c = threadIdx.x % R, i0 = (int)(blockIdx.x / (unsigned)a.Hkv) * kQgVec * (kQaThreads / R) + threadIdx.x / R;
   if (i0 >= cnt) return;
-  uint32_t wk[kQaVec], wv[kQaVec], sk[kQaVec], sv[kQaVec];
+  uint32_t wk[kQgVec], wv[kQgVec], sk[kQgVec], sv[kQgVec];
 #pragma unroll
-  for (int x = 0; x < kQaVec; ++x) {
+  for (int x = 0; x < kQgVec; ++x) {
     const int i = i0 + x * (kQaThreads / R);
     const int64_t t = p0 + i;
     wk[x] = wv[x] = sk[x] = sv[x] = 0;
@@ -254,7 +270,7 @@ __global__ void __launch_bounds__(kQaThreads) qpaged_gather_kernel(PagedArgs a, 
   }
   const int64_t at = (b * os.batch + h * os.head) / 8 + c;
 #pragma unroll
-  for (int x = 0; x < kQaVec; ++x) {
+  for (int x = 0; x < kQgVec; ++x) {
     const int i = i0 + x * (kQaThreads / R);
     if (i >= cnt) return;
     K[at + i * os.token / 8] = values_of<T>(wk[x], sk[x]);
@@ -266,7 +282,7 @@ __global__ void __launch_bounds__(kQaThreads) qpaged_gather_kernel(PagedArgs a, 
 
 cudaError_t launch_qpaged_append(const PagedArgs& a, int d, int dtype, const void* K, const void* V,
                                  const dkv_strides& ns, int n_rows, const int64_t* slots, uint8_t* cache, cudaStream_t s) {
-  const int64_t per = kQaThreads * kQaVec, pieces = (int64_t)n_rows * a.Hkv * (d / 8);
+  const int64_t per = kQaThreads, pieces = (int64_t)n_rows * a.Hkv * (d / 16);
   auto go = [&](auto kernel) {
     kernel<<<(unsigned)((pieces + per - 1) / per), kQaThreads, 0, s>>>(a, static_cast<const uint4*>(K), static_cast<const uint4*>(V),
                                                                        ns, n_rows, slots, cache);
@@ -278,7 +294,7 @@ cudaError_t launch_qpaged_append(const PagedArgs& a, int d, int dtype, const voi
 
 cudaError_t launch_qpaged_gather(const PagedArgs& a, int d, int dtype, const uint8_t* cache, const int32_t* first,
                                  const int32_t* counts, int n, void* K, void* V, const dkv_strides& os, cudaStream_t s) {
-  const int per = kQaThreads / (d / 8) * kQaVec;
+  const int per = kQaThreads / (d / 8) * kQgVec;
   auto go = [&](auto kernel) {
     kernel<<<dim3((unsigned)((n + per - 1) / per) * (unsigned)a.Hkv, a.B), kQaThreads, 0, s>>>(a, cache, first, counts, n, static_cast<uint4*>(K),
                                                                           static_cast<uint4*>(V), os);
