@@ -240,7 +240,7 @@ size_t plan_ws_bytes(int B) { return kWsHeader + round_up((size_t)plan_ints(B) *
 cudaError_t launch_paged_plan(const PlanArgs& a, uint8_t* ws, cudaStream_t s) {
   int* sums = reinterpret_cast<int*>(ws + kWsHeader);
   const size_t smem = (size_t)plan_ints(a.B) * 4;
-  const bool alone = a.rows <= kPlanAlone, few = a.B <= kPlanFew && a.rows <= kPlanFew * kPlanRows;
+  const bool alone = a.rows <= kPlanAlone, few = a.B <= kPlanFew && (!alone || a.rows <= kPlanFew * kPlanRows);
   const bool vec = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) & 15u) == 0;
   cudaError_t e = ensure_smem_limit(few ? reinterpret_cast<const void*>(plan_kernel<kPlanFew>) : reinterpret_cast<const void*>(plan_kernel<kPlanThreads>), smem);
   if (e != cudaSuccess) return e;
