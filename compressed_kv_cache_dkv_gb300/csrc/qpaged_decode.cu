@@ -31,7 +31,9 @@
 // weight, biases by a product, packed arithmetic 72; one merge a CTA, the join in the same grid 68.  The loop
 // streams at 5.8 TB/s (0.87 of the measured copy rate); 4 us at the start (lengths, then the page table, then
 // the first copies) and 6 at the end (uneven finish, merge, join) are what is left.  64 sequences of 300 to 8000
-// under a window of 4096, 8 KV heads, pages of 16 (237 MB): 65 us.  One of 1000 tokens: 9.9 us in a graph.
+// under a window of 4096, 8 KV heads, pages of 16 (237 MB): 65 us.  One of 1000 tokens: 9.9 us in a graph.  The join
+// of many records with all loads in flight: one sequence of 65536 tokens, 2 KV heads 19.7 us (23.8 with eight at a
+// time, merged as they came).
 #include "paged_tc.cuh"
 #include "qpaged.cuh"
 
@@ -41,7 +43,15 @@ namespace {
 constexpr int kQdTile = 32, kQdBlocks = kQdTile / kQBlock;
 constexpr int kQdWarps = 16, kQdDepth = 2;  // warps, and stages of each
 constexpr int kQdThreads = 32 * kQdWarps;
-constexpr int kQdLeast = 4;  // tiles of a CTA, as long as there are enough for all
+// Tiles of a CTA, as long as there are enough for all.  In a graph: one sequence of 100 tokens, 8 KV heads 7.9 us
+// (with 8: 8.7, with 12: 13.6), of 2000, 2 KV heads 11.4 (11.3, 12.1), 16 of 200, 8 KV heads 9.0 (12.6, 13.8).
+constexpr int kQdLeast = 4;
+// Sequences of one length (one alone, or all beyond their window) get a number of CTAs that cuts units at equal parts,
+// so that no CTA has to join two units one after the other, as long as that adds fewer than so many tiles to a run: one
+// sequence of 9000 tokens, 2 KV heads, in a graph 15.0 us (19.9 without), 16 of 200, 8 KV heads, 9.4 (13.1), 10 of
+// 1600 15.6 (17.1; below 24 they gained, and 4 of 16000 lost 0.2 of 27.7).  With uneven lengths the whole grid is
+// better: 10 of 100 to 1500 14.1 us, 17.3 so.
+constexpr int64_t kQdEven = 24;
 // Weights are 2^(score - ref).  A head's reference lies kQdShift below a maximum and moves only when a score exceeds
 // that by kQdSlack (at once where scores are so large that their rounding shows): weights are at most 2^15, and those
 // down to e^-14 of the largest keep 11 bits.
@@ -86,7 +96,7 @@ struct QdSmem {
 };
 // Counters of the CTAs that have left a record of a unit: a byte for each CTA in which such a unit can begin, behind
 // the header's two words.  They are zero between calls (the last CTA takes its unit's away).
-constexpr int kQdMostCtas = (int)(kWsHeader - 8);
+constexpr int kQdMostCtas = 160;
 
 // the (scale, bias) pairs of a token
 template <int G>
@@ -139,7 +149,14 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
       if (p.lse)
         for (int e = threadIdx.x; e < a.Hq; e += kQdThreads) p.lse[(size_t)b * a.Hq + e] = -INFINITY;
     }
-  const int total = prefix[a.B] * a.Hkv, nc = min((int)gridDim.x, (total + kQdLeast - 1) / kQdLeast), c = blockIdx.x;
+  const int total = prefix[a.B] * a.Hkv, c = blockIdx.x;
+  int nc = min((int)gridDim.x, (total + kQdLeast - 1) / kQdLeast);
+  bool even = true;
+  for (int b = threadIdx.x; b < a.B; b += kQdThreads) even = even && prefix[b + 1] - prefix[b] == prefix[1];
+  if (__syncthreads_and(even)) {
+    const int64_t fewer = nc / (a.B * a.Hkv) * (a.B * a.Hkv);
+    if ((int64_t)total * (nc - fewer) < kQdEven * nc * fewer) nc = (int)fewer;
+  }
   if (c >= nc) return;
   const int x0 = deal_bound(total, nc, c), x1 = deal_bound(total, nc, c + 1);
   auto bound = [&](int w) { return x0 + (x1 - x0) * w / kQdWarps; };  // of the warps' runs
@@ -578,50 +595,89 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
     __threadfence();
   }
   __syncthreads();
-  for (int k = 0; k < 2; ++k) {
-    const int n = joins[k];
-    if (n == 0) continue;
+  if (joins[0] | joins[1]) {  // with both, each has half the warps
+    const bool both = joins[0] && joins[1];
+    const int threads = both ? kQdThreads / 2 : kQdThreads, tid = threadIdx.x & (threads - 1);
+    const int k = both ? threadIdx.x >> 8 : joins[1] ? 1 : 0, n = joins[k];
+    auto sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + k), "r"(threads) : "memory"); };
     const int4 u = k ? cta_last : cta_first;
     const int c0 = deal_owner(total, nc, u.x);
-    auto rec = [&](int i) { return p.records + (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * qrec_floats<D>(); };
-    constexpr int kEach = D * 8 / kQdThreads, kDeep = 8;
-    float M = -INFINITY, L = 0.f, v[kEach] = {};
-    for (int i0 = 0; i0 < n; i0 += kDeep) {
-      float m[kDeep], l[kDeep], y[kDeep][kEach];
+    constexpr int kStep = 2 * qrec_floats<D>();  // from a CTA's record to the next one's; the first is a CTA's second
+    auto rec = [&](int i) { return p.records + (size_t)(c0 + i) * kStep + (i == 0 ? kStep / 2 : 0); };
+    // Eight warps turn a head's references into factors each while the first records are on their way; groups of
+    // threads take records in turn, four values a thread (loads that wait for one another cost a microsecond each).
+    // The sums are over every kParts-th record, whichever threads make them.
+    constexpr int kDeep = 8, kQuads = D * 2, kParts = kQdThreads / kQuads, kStats = (kQdMostCtas + 31) / 32;
+    constexpr int kRoom = 8 * kQdMostCtas + 16 > 4 * kQdThreads ? 8 * kQdMostCtas + 16 : 4 * kQdThreads;
+    static_assert(2 * kRoom <= kQdWarps * D * 8, "the factors of two units");
+    float* fac = firsts + k * kRoom;                           // [record][8]
+    float* red = fac + 8 * kQdMostCtas;                        // M, L [8] each
+    float* part = reinterpret_cast<float*>(smem) + k * kRoom;  // [kParts][D][8]
+    const int groups = threads / kQuads, pw = tid >> 5, grp = tid / kQuads;
+    const int at = tid % kQuads;  // heads 4 (at % 2) .. + 3 of a channel
+    const int n4 = 4 * (at & 1) < a.G ? n : 0;                              // (those that are not there are not read)
+    float4 y[kDeep], sum = make_float4(0.f, 0.f, 0.f, 0.f), odd = sum;
+    auto fetch = [&](int i0) {
+      const float4* from = reinterpret_cast<const float4*>(rec(i0) + 16) + at;
 #pragma unroll
-      for (int i = 0; i < kDeep; ++i) {
-        m[i] = -INFINITY;
-        if (i0 + i >= n) continue;
-        const float* from = rec(i0 + i);
-        m[i] = __ldcg(from + gg);
-        l[i] = __ldcg(from + 8 + gg);
+      for (int i = 0; i < kDeep; ++i)
+        if (i0 + i * groups < n4) y[i] = __ldcg(from + i * (groups * kStep / 4) - (i && i0 == 0 ? kStep / 8 : 0));
+    };
+    float m[kStats], l[kStats];
+    if (pw < 8) {
 #pragma unroll
-        for (int e = 0; e < kEach; ++e) y[i][e] = __ldcg(from + 16 + e * kQdThreads + threadIdx.x);
-      }
-      float top = M;
-#pragma unroll
-      for (int i = 0; i < kDeep; ++i) top = fmaxf(top, m[i]);
-      const float Ms = top == -INFINITY ? 0.f : top, al = fast_exp2(M - Ms);
-      M = top;
-      L *= al;
-#pragma unroll
-      for (int e = 0; e < kEach; ++e) v[e] *= al;
-#pragma unroll
-      for (int i = 0; i < kDeep; ++i) {
-        if (i0 + i >= n) continue;
-        const float f = fast_exp2(m[i] - Ms);
-        L += f * l[i];
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) v[e] += f * y[i][e];
+      for (int i = 0; i < kStats; ++i) {
+        const bool is = lane + 32 * i < n;
+        m[i] = is ? __ldcg(rec(lane + 32 * i) + pw) : -INFINITY;
+        l[i] = is ? __ldcg(rec(lane + 32 * i) + 8 + pw) : 0.f;
       }
     }
-    if (gg < a.G) {
-      const float il = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-      const size_t head = (size_t)u.z * a.Hq + u.w * a.G + gg;
+    fetch(grp);
+    if (pw < 8) {
+      float M = m[0], L = 0.f;
 #pragma unroll
-      for (int e = 0; e < kEach; ++e)
-        static_cast<T*>(p.out)[head * D + ((e * kQdThreads + threadIdx.x) >> 3)] = Num<T>::from_float(v[e] * il);
-      if (p.lse && threadIdx.x < 8) p.lse[head] = (M + log2f(L)) * 0.6931471805599453f;
+      for (int i = 1; i < kStats; ++i) M = fmaxf(M, m[i]);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float Ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int i = 0; i < kStats; ++i) {
+        const float f = fast_exp2(m[i] - Ms);
+        if (lane + 32 * i < n) fac[(lane + 32 * i) * 8 + pw] = f;
+        L += f * l[i];
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+      if (lane == 0) {
+        red[pw] = M;
+        red[8 + pw] = L;
+      }
+    }
+    sync();
+    for (int i0 = grp;;) {
+#pragma unroll
+      for (int i = 0; i < kDeep; ++i) {
+        if (i0 + i * groups >= n4) continue;
+        const float4 f = reinterpret_cast<const float4*>(fac + (i0 + i * groups) * 8)[at & 1];
+        float4& to = both && i % 2 ? odd : sum;
+        to = make_float4(fmaf(f.x, y[i].x, to.x), fmaf(f.y, y[i].y, to.y), fmaf(f.z, y[i].z, to.z), fmaf(f.w, y[i].w, to.w));
+      }
+      if ((i0 += kDeep * groups) >= n4) break;
+      fetch(i0);
+    }
+    reinterpret_cast<float4*>(part)[tid] = sum;
+    if (both) reinterpret_cast<float4*>(part)[threads + tid] = odd;
+    sync();
+    const float M = red[gg], L = red[8 + gg], il = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+    const size_t head = (size_t)u.z * a.Hq + u.w * a.G + gg;
+    if (gg < a.G) {
+      for (int e = tid; e < D * 8; e += threads) {
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) v += part[i * D * 8 + e];
+        static_cast<T*>(p.out)[head * D + (e >> 3)] = Num<T>::from_float(v * il);
+      }
+      if (p.lse && tid < 8) p.lse[head] = (M + log2f(L)) * 0.6931471805599453f;
     }
   }
 }

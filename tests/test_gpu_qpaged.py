@@ -156,7 +156,10 @@ def test_decode(dtype, d, hq, hkv, page, lens, window, sinks):
 @pytest.mark.parametrize("d,hkv,hq,lens", [
     (128, 4, 8, [3] * 700 + [900, 31, 33]),     # many units of a tile: whole in a warp's run, cut by warps and by CTAs
     (64, 1, 2, [1 + i % 150 for i in range(4096)]),
-    (128, 2, 16, [20000, 10, 15000, 1]), (64, 8, 8, [2000 + 37 * i for i in range(6)])])
+    (128, 2, 16, [20000, 10, 15000, 1]), (64, 8, 8, [2000 + 37 * i for i in range(6)]),
+    # a CTA that holds the end of one long unit and the start of the next may be last at both; equal lengths cut evenly
+    (128, 2, 8, [4000, 3900]), (64, 2, 2, [4100, 3970, 2000]), (128, 3, 18, [2100, 2000, 1900]), (64, 1, 8, [5000, 4900]),
+    (128, 2, 12, [9000]), (64, 8, 16, [200] * 16), (128, 4, 4, [700] * 5)])
 def test_decode_deals_units_to_warps(d, hkv, hq, lens):
     page = 32
     used = [-(-n // page) for n in lens]
@@ -191,7 +194,7 @@ def test_decode_deals_units_to_warps(d, hkv, hq, lens):
         tol = 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2 * ds) * (1 + 2.0 ** -8) * size + 1e-30
         assert bool(((out[b].double() - want).abs() <= tol).all()), b
         assert bool(((lse[b].double() - s.logsumexp(-1)).abs() <= ds + 2.0 ** -22 * s.logsumexp(-1).abs().clamp(min=1.0)).all()), b
-    for _ in range(3):  # the counters in the header are back at zero
+    for _ in range(20):  # the counters in the header are back at zero, and it is the same whoever comes last
         again, lse2 = dkv.dkv_qpaged_decode(p, q, pool, table, L, workspace=ws)
         assert torch.equal(out, again) and torch.equal(lse, lse2)
 
