@@ -678,6 +678,59 @@ def test_few_queries_under_a_wide_table():
                 near(out[row, 6 * h:6 * h + 6], lse[6 * h:6 * h + 6, row], ref, dt)
 
 
+@pytest.mark.parametrize("dtype,d,hq,hkv,page,B,cached,most,window,sinks", [
+    ("fp16", 128, 6, 2, 16, 40, 200, 300, 0, 0),      # groups of 128 tokens of one head, the second often short or empty
+    ("bf16", 64, 16, 8, 64, 50, 300, 200, 40, 3),     # groups of two heads
+    ("bf16", 128, 4, 1, 32, 400, 20, 40, 0, 0),       # hardly a tile for each CTA; requests without a token
+    ("fp16", 64, 5, 1, 128, 100, 0, 300, 100, 0),     # five heads: whole prompts
+    ("bf16", 128, 10, 5, 16, 200, 1000, 6, 0, 0),     # a few queries of many sequences, three of five groups' heads idle
+    ("fp16", 128, 12, 2, 64, 1, 100, 8000, 0, 0)])
+def test_prefill_of_more_tiles_than_multiprocessors(dtype, d, hq, hkv, page, B, cached, most, window, sinks):
+    """A CTA then goes on with the places of others: every row as alone, and equal calls equal."""
+    dt, rnd = Q.DT[dtype], torch.Generator().manual_seed(d + B)
+    news = torch.randint(0, most + 1, (B,), generator=rnd).tolist() if B > 1 else [most]
+    lens = [n + int(torch.randint(0, cached + 1, (1,), generator=rnd)) for n in news]
+    used = [-(-n // page) for n in lens]
+    n_pages = sum(used) + 1
+    pool, k, v = filled(d, hkv, page, n_pages, dt, seed=B)
+    p = dkv.dkv_qpaged_layout(pool, B, hq, d, max(used), dtype=dt, window=window, sinks=sinks)
+    ws = workspace(p)
+    at = [sum(used[:b]) for b in range(B)]
+    table = (torch.tensor(at)[:, None] + torch.arange(max(used))[None]).clamp(max=n_pages - 1).int().cuda()
+    starts = [0]
+    for n in news:
+        starts.append(starts[-1] + n)
+    rows = starts[-1] + 2
+    q = randn((rows, hq, d), dt, 5, 2.0).cuda()
+    out, lse = torch.full((rows, hq, d), 7.0, dtype=dt, device="cuda"), torch.full((hq, rows), 7.0, device="cuda")
+    call = lambda o, x: dkv.dkv_qpaged_prefill(p, q, torch.tensor(starts, dtype=torch.int32, device="cuda"), most, pool, table,  # noqa: E731
+                                               torch.tensor(lens, dtype=torch.int32, device="cuda"), out=o, lse=x, workspace=ws)
+    call(out, lse)
+    no_fault(ws)
+    assert bool((out[-2:] == 7).all()) and bool((lse[:, -2:] == 7).all())
+    for b in range(B):
+        n, m = lens[b], news[b]
+        if m == 0:
+            continue
+        pos, t = torch.arange(n - m, n, device="cuda")[:, None], torch.arange(n, device="cuda")[None]
+        sees = t <= pos
+        if window:
+            sees &= (t > pos - window) | (t < sinks)
+        for h in range(hq) if B > 1 else (0, hq - 1):
+            kk, vv = (x[h * hkv // hq, at[b] * page:at[b] * page + n] for x in (k, v))
+            x = q[starts[b]:starts[b] + m, h].double()
+            s = ((x @ kk.T) / math.sqrt(d)).masked_fill(~sees, -math.inf)
+            w, big = s.softmax(-1), vv.abs().amax(-1)
+            # weights below 2^-24 of fp16's unit are off by 2^-32 of the largest, beside 2^-11 of themselves (as in check_prefill)
+            size = 3.1 * ((w * big).sum(-1) + 2.0 ** (11 - 32) * sees.double() @ big)[:, None]
+            ds = R.score_error(d, 3.1 * float(x.abs().sum(-1).max() * kk.abs().max()) / math.sqrt(d))
+            near(out[starts[b]:starts[b] + m, h], lse[h, starts[b]:starts[b] + m], (w @ vv, s.logsumexp(-1), size, ds), dt)
+    for _ in range(3):
+        out2, lse2 = torch.full_like(out, 7.0), torch.full_like(lse, 7.0)
+        call(out2, lse2)
+        assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
 # ---------------------------------------------------------------- streams, graphs, a run of them together
 
 class Server:
