@@ -10,14 +10,15 @@
 // multiprocessors, which writes 12 bytes for each.
 //
 // Measured: one token for each of 64 requests 4.3 us in a graph; 256 requests into a million rows (12.6 MB, most of them
-// padding) 14.3 us, of which the sums 5 and the second grid's start and shared copy of the sums 3.
+// padding) 12.4 us, 10.8 in a graph, of which the sums 4 and the second grid's start and shared copy of the sums 3 (14.2 with
+// 1024 threads for the sums).
 #include "qpaged.cuh"
 
 namespace dkv {
 namespace {
 
 constexpr int kPlanThreads = 1024, kPlanMost = 4;  // requests of a thread at most: 4096 in all
-constexpr int kPlanFew = 256;                      // threads for as many requests and their rows
+constexpr int kPlanFew = 256;                      // threads for as many requests, and for their rows where one CTA writes them
 constexpr int kPlanRows = 4;                       // rows of a thread
 constexpr int kPlanAlone = 8192;                   // rows that one CTA takes
 

@@ -40,7 +40,8 @@
 // causal prompt 446 us in a graph (465 without), 16k under a window of 1024 139 (147), 8 prompts of 700 to 4096 507
 // (537).  A place is taken when the loading warp has sent off the unit's last tile: taken at a unit's start, places
 // wait for busy CTAs while others run out (8k causal 465).  The second group's start put off by three tiles, to have
-// the groups' ends apart, cost 2 us.
+// the groups' ends apart, cost 2 us.  Edge tiles without a new maximum in a third function: 498 for the 8 prompts, and 142
+// under the window.
 //
 // Measured (d 128): a prompt of 8191, 32 query and 8 KV heads, pages of 16: 451 us, 1.22 PFLOP/s.  One of 16384
 // under a window of 1024, 12 heads: 143 us.  32 queries over 300 to 2000 keys, d 64: 16.4 us in a graph.
@@ -696,7 +697,7 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
       // whole rows of the output.
       const uint32_t stage = sb + g * S::kQ;
       const int64_t rec = (((int64_t)u.b * gridDim.z + u.tile) * (gridDim.x / p.parts) + u.hg) * p.parts + u.part;
-#pragma unroll 1  // (short code, as above)
+#pragma unroll 2  // (short code, as above: all four at once, with the next load on its way, 150 us under the window)
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
         if (n > 0) {
