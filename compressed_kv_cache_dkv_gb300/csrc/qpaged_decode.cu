@@ -51,7 +51,7 @@ constexpr int kQdLeast = 4;
 // sequence of 9000 tokens, 2 KV heads, in a graph 15.0 us (19.9 without), 16 of 200, 8 KV heads, 9.4 (13.1), 10 of
 // 1600 15.6 (17.1; below 24 they gained, and 4 of 16000 lost 0.2 of 27.7).  With uneven lengths the whole grid is
 // better: 10 of 100 to 1500 14.1 us, 17.3 so.
-constexpr int64_t kQdEven = 24;
+constexpr int kQdEven = 24;
 // Weights are 2^(score - ref).  A head's reference lies kQdShift below a maximum and moves only when a score exceeds
 // that by kQdSlack (at once where scores are so large that their rounding shows): weights are at most 2^15, and those
 // down to e^-14 of the largest keep 11 bits.
@@ -151,11 +151,10 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
     }
   const int total = prefix[a.B] * a.Hkv, c = blockIdx.x;
   int nc = min((int)gridDim.x, (total + kQdLeast - 1) / kQdLeast);
-  bool even = true;
-  for (int b = threadIdx.x; b < a.B; b += kQdThreads) even = even && prefix[b + 1] - prefix[b] == prefix[1];
-  if (__syncthreads_and(even)) {
-    const int64_t fewer = nc / (a.B * a.Hkv) * (a.B * a.Hkv);
-    if ((int64_t)total * (nc - fewer) < kQdEven * nc * fewer) nc = (int)fewer;
+  const int one = prefix[1];  // of one length: a look at the middle and the end will do (all of them took 1 us more)
+  if (prefix[a.B] == (int64_t)a.B * one && prefix[a.B / 2] == (int64_t)(a.B / 2) * one) {
+    const int units = a.B * a.Hkv, fewer = nc - nc % units;
+    if ((float)total * (float)(nc - fewer) < (float)kQdEven * (float)nc * (float)fewer) nc = fewer;
   }
   if (c >= nc) return;
   const int x0 = deal_bound(total, nc, c), x1 = deal_bound(total, nc, c + 1);
