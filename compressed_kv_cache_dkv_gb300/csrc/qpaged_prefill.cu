@@ -566,7 +566,8 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
       for (int i = 1;; ++i) {
         if (i >= 2) ok = mbar_wait(&unit_empty[i & 1], (uint32_t)((i - 2) >> 1) & 1u, a.err);
         // (not before this CTA comes to its end: who takes early leaves others idle)
-        if (ok) ok = mbar_wait(unit_sent, (uint32_t)(i - 1) & 1u, a.err);
+        // This wait is as long as a unit (1e6 tokens 15 ms): 20 s at most.  The loading warp arrives if its waits give up, too.
+        if (ok) ok = mbar_wait(unit_sent, (uint32_t)(i - 1) & 1u, a.err, 16 * kWaitLimit);
         if (!__all_sync(0xffffffffu, ok)) break;
         if (el) {
           mbar_arrive_expect_tx(taken_full, 16);

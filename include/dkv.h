@@ -694,7 +694,8 @@ typedef struct dkv_qpaged {
 /* Check a descriptor, as dkv_paged_check does.  Host only. */
 DKV_API int dkv_qpaged_check(const dkv_qpaged* p);
 
-/* Bytes of the workspace of every call below (0 for a bad descriptor); see dkv_paged_workspace_bytes. */
+/* Bytes of the workspace of every call below (0 for a bad descriptor); see dkv_paged_workspace_bytes.  The header also
+ * holds counters of dkv_qpaged_decode, zero before and after every call. */
 DKV_API size_t dkv_qpaged_workspace_bytes(const dkv_qpaged* p);
 
 /*
