@@ -293,7 +293,8 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
   uint64_t* s_full = q_full + 2;         // [group][buffer]
   uint64_t* p_full = s_full + 4;         // [group][buffer]
   uint64_t* drain = p_full + 4;          // [group] after a wait that gave up
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
+  uint64_t* rows_through = drain + 2;    // [group] the rows of a group that falls idle have seen the end of its last product
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rows_through + 2);
   volatile uint32_t* bad_blocks = tmem_slot + 1;  // [stage] blocks on bad pages
   uint64_t* unit_full = reinterpret_cast<uint64_t*>(tmem_slot + 4);  // [2]
   uint64_t* unit_empty = unit_full + 2;                              // [2]
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
   uint64_t* unit_sent = taken_full + 1;  // a unit's copies are on their way
   void* taken = taken_full + 2;                                      // 16 bytes
   QpUnit* units = reinterpret_cast<QpUnit*>(taken_full + 4);         // [2]
-  static_assert(320 + 2 * sizeof(QpUnit) <= 768, "the units fit");
+  static_assert(336 + 2 * sizeof(QpUnit) <= 768, "the units fit");
 
   bool ok = true;
   const QpUnit first = qp_unit(p, blockIdx.x, blockIdx.y, blockIdx.z);
@@ -383,6 +384,7 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
       for (int i = 0; i < 2; ++i) {
         mbar_init(&q_full[i], 4);
         mbar_init(&drain[i], 1);
+        mbar_init(&rows_through[i], 4);
         mbar_init(&unit_full[i], 1);
         mbar_init(&unit_empty[i], 15);  // all warps but the one that fills them
       }
@@ -513,8 +515,9 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
         if (ok) ok = mbar_wait(bar, parity, a.err);
         __syncwarp();
       };
-      uint32_t it = 0, c = 0, qph = 0;  // tiles so far, and those of this group: slots go by the first, buffers by the second
+      uint32_t it = 0, c = 0, qph = 0, tph = 0;  // tiles so far, and those of this group: slots go by the first, buffers by the second
       int un = 0;
+      bool busy = false;  // the group's last unit with tiles had rows
       do {
         const QpUnit u = kOn ? units[un & 1] : first;
         left(un);
@@ -531,7 +534,15 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
                    kd + (uint64_t)(((k >> 2) * kQpN * 128 + (k & 3) * 32) >> 4), id_s, k > 0, el);
           tc_commit(&sf[buf], el);
         };
+        // In a unit where the group is empty nothing holds this warp, and its arrivals would take the barrier that the rows
+        // wait on for the last product, four tiles earlier, through another phase: not before all of them have seen that one.
+        if (kOn && n == 0 && u.nt > 0 && busy) {
+          wait(&rows_through[g], tph);
+          tph ^= 1u;
+          busy = false;
+        }
         if (n > 0) {
+          busy = true;
           wait(&q_full[g], qph);  // (the rows have read the last unit's O by then)
           qph ^= 1u;
           scores(0);
@@ -593,6 +604,7 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
     const int g = warp >> 2, rw = warp & 3, row = 32 * rw + lane;
     uint32_t it = 0, cc = 0;  // tiles so far, and those of this group
     int un = 0;
+    bool busy = false;  // as the products'
     do {
       const QpUnit u = kOn ? units[un & 1] : first;
       left(un);
@@ -601,6 +613,10 @@ __global__ void __launch_bounds__(kQpThreads, 1) qpaged_prefill_kernel(QpArgs p)
       const QuerySpan& qs = u.qs;
       const KeySpan<kQpN>& ks = u.ks;
       const int n = g ? u.nB : u.nA, parts = u.parts, p_lo = u.p_lo, t0 = u.t0;
+      if (kOn) {  // (the warp is together here: all of it has seen the last unit's end)
+        mbar_arrive_if(&rows_through[g], lane == 0 && n == 0 && u.nt > 0 && busy);
+        busy = n > 0 || (busy && u.nt == 0);
+      }
       const QpRow me = qp_row(p, u.kvh, u.h0, u.row0, qs.n, g, row);
       const int pos = qs.off + me.token;
       float slog2 = a.scale_log2;

@@ -731,6 +731,54 @@ def test_prefill_of_more_tiles_than_multiprocessors(dtype, d, hq, hkv, page, B, 
         assert torch.equal(out, out2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("dtype,d,hq,hkv,page,news,cached,window,sinks", [
+    ("fp16", 128, 3, 3, 32, [256, 100], [600, 700], 0, 0),         # 256 tokens of a head a unit: both groups, the first alone
+    ("bf16", 64, 1, 1, 16, [384, 1, 300, 128], [900, 64], 0, 0),
+    ("fp16", 64, 5, 1, 64, [256, 128, 90], [1000], 500, 70),
+    ("bf16", 128, 6, 1, 64, [64, 40, 1], [800, 320], 0, 0),        # four heads of six, then two: the second group without a head
+    ("fp16", 128, 10, 2, 128, [30, 17], [1500, 640], 900, 3)])
+def test_prefill_where_a_group_has_rows_in_some_units_only(dtype, d, hq, hkv, page, news, cached, window, sinks):
+    """A CTA goes from units of two groups of rows to units whose second group is empty, and back."""
+    dt, B = Q.DT[dtype], 240
+    news = [news[b % len(news)] for b in range(B)]
+    lens = [n + cached[b % len(cached)] for b, n in enumerate(news)]
+    n_pages = -(-max(lens) // page)
+    pool, k, v = filled(d, hkv, page, n_pages, dt, seed=hq)
+    p = dkv.dkv_qpaged_layout(pool, B, hq, d, n_pages, dtype=dt, window=window, sinks=sinks)
+    ws = workspace(p)
+    table = torch.arange(n_pages, dtype=torch.int32, device="cuda").repeat(B, 1)    # one row of tokens for all
+    starts = [0]
+    for n in news:
+        starts.append(starts[-1] + n)
+    rows = starts[-1]
+    q = randn((rows, hq, d), dt, 6, 2.0).cuda()
+    pos = torch.cat([torch.arange(n - m, n) for n, m in zip(lens, news)]).cuda()[:, None]
+    t = torch.arange(max(lens), device="cuda")[None]
+    sees = t <= pos
+    if window:
+        sees &= (t > pos - window) | (t < sinks)
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    refs = []
+    for h in range(hq):
+        kk, vv = (x[h * hkv // hq, :max(lens)] for x in (k, v))
+        x = q[:, h].double()
+        s = ((x @ kk.T) / math.sqrt(d)).masked_fill(~sees, -math.inf)
+        w, big = s.softmax(-1), vv.abs().amax(-1)
+        # weights below 2^-24 of fp16's unit are off by 2^-32 of the largest, beside 2^-11 of themselves (as in check_prefill)
+        size = 3.1 * ((w * big).sum(-1) + 2.0 ** (11 - 32) * sees.double() @ big)[:, None]
+        refs.append((w @ vv, s.logsumexp(-1), size, R.score_error(d, 3.1 * float(x.abs().sum(-1).max() * kk.abs().max()) / math.sqrt(d))))
+    first = None
+    for _ in range(10):
+        out, lse = torch.full((rows, hq, d), 7.0, dtype=dt, device="cuda"), torch.full((hq, rows), 7.0, device="cuda")
+        dkv.dkv_qpaged_prefill(p, q, dev(starts), max(news), pool, table, dev(lens), out=out, lse=lse, workspace=ws)
+        no_fault(ws)
+        if first is None:
+            first = out, lse
+            for h in range(hq):
+                near(out[:, h], lse[h], refs[h], dt)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
 # ---------------------------------------------------------------- streams, graphs, a run of them together
 
 class Server:
