@@ -11,8 +11,8 @@
 //                they lie, with q's channels in the same order
 //   o = C_V^T w  channels in M; two tokens' words interleaved by byte permutes give the pairs along k
 // q is brought to at most 2^15 by a power of two, so that it is an fp16 operand whatever its type (channels above 2^-25
-// of the largest without loss).  w = p s 2^-E, with a running power of two E over the scales seen, is rounded once to
-// fp16 (relative error 2^-11).  That rounding falls on codes less 8 (the sum of the rounded weights, times 8, goes
+// of the largest without loss).  w = p s 2^-E, with a running power of two E for each head and group, is rounded once to
+// fp16 (relative error 2^-11, or 2^-32 of the head's largest product).  That rounding falls on codes less 8 (the sum of the rounded weights, times 8, goes
 // off again, and the bias is b + 8 s), so that it is one of about the size of the values, as in the 16-bit prefill; a
 // second fp16 value for what the first leaves took 9 % longer (16 of 64k: 77.8 us, 71.6 without).
 //
@@ -56,6 +56,13 @@ constexpr int kQdEven = 24;
 // that by kQdSlack (at once where scores are so large that their rounding shows): weights are at most 2^15, and those
 // down to e^-14 of the largest keep 11 bits.
 constexpr float kQdShift = 7.f, kQdSlack = 8.f, kQdLarge = 0x1p20f;
+// A weight times its token's scale is held times 2^-E as a half.  E, of each head and group of channels, lies 7 below a
+// product's exponent, goes with the reference, and moves when a product is above 2^15 (kQdMost, a half's bits).  It follows
+// the products, not the scales: with E from the largest scale a token of no weight with values 2^27 times the others'
+// left these 4 bits.  -E goes up to 96: products below 2^-89, a weight being 2^7 at least, are off by 2^-121.
+constexpr uint32_t kQdMost = 0x7800u;
+constexpr float kQdFinest = 0x1p96f;
+__device__ inline float qd_one_over(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }  // x a power of two
 
 template <int D>
 constexpr int qrec_floats() { return 16 + 8 * D; }
@@ -290,12 +297,12 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
     float ref[2] = {-INFINITY, -INFINITY}, lim[2] = {-INFINITY, -INFINITY};
     float2 l = make_float2(0.f, 0.f);
     float o[G][4][4], ow[G][4];  // products with the codes; sums of the rounded weights (the same in all rows)
-    float ob[G][2];              // sums of p (b + 8 s)
-    int E[G];                    // scales seen are below 2^(E - 127); 0: none
+    float2 ob[G];                // sums of p (b + 8 s)
+    float2 inv[G];               // 2^-E
 #pragma unroll
     for (int gg = 0; gg < G; ++gg) {
-      E[gg] = 0;
-      ob[gg][0] = ob[gg][1] = 0.f;
+      inv[gg] = make_float2(kQdFinest, kQdFinest);
+      ob[gg] = make_float2(0.f, 0.f);
       ow[gg][0] = ow[gg][1] = ow[gg][2] = ow[gg][3] = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[gg][i][0] = o[gg][i][1] = o[gg][i][2] = o[gg][i][3] = 0.f;
@@ -360,19 +367,11 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
         fence_proxy_async();
         __syncwarp();
       }
-      // ---- references (columns 2t, 2t + 1) and the scales' power of two
+      // ---- references (columns 2t, 2t + 1)
       const float top[2] = {fmaxf(fmaxf(sc[0][0].x, sc[0][1].x), fmaxf(sc[1][0].x, sc[1][1].x)),
                             fmaxf(fmaxf(sc[0][0].y, sc[0][1].y), fmaxf(sc[1][0].y, sc[1][1].y))};
-      uint32_t big[G], sbv[G];
-      lds_params<G>(tb + lane / kQBlock * BB + qparam_off(D, 1, 0, lane % kQBlock), sbv);
-      bool grown = top[0] > lim[0] || top[1] > lim[1];
-#pragma unroll
-      for (int gg = 0; gg < G; ++gg) {
-        big[gg] = __reduce_max_sync(0xffffffffu, sbv[gg] & 0x7fffu);
-        grown |= (int)(__float_as_uint(half_lo(big[gg])) >> 23) >= E[gg];
-      }
-      if (__any_sync(0xffffffffu, grown)) {
-        float al[2];
+      if (__any_sync(0xffffffffu, top[0] > lim[0] || top[1] > lim[1])) {
+        float al[2], up[2];  // up: a power of two, al up in [1, 2)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float y = top[e];
@@ -384,55 +383,95 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
             ref[e] = y - kQdShift;
             lim[e] = ref[e] + (fabsf(y) < kQdLarge ? kQdShift + kQdSlack : kQdShift);
           }
+          up[e] = __uint_as_float((254u << 23) - (__float_as_uint(al[e]) & 0x7f800000u));
         }
         l = mul2(l, make_float2(al[0], al[1]));
 #pragma unroll
-        for (int gg = 0; gg < G; ++gg) {
-          const int ex = (int)(__float_as_uint(half_lo(big[gg])) >> 23) + 1;  // scales < 2^(ex - 127)
-          float f = 1.f;
-          if (ex > E[gg]) {
-            f = __uint_as_float((uint32_t)max(127 + E[gg] - ex, 0) << 23);
-            E[gg] = ex;
-          }
-          ob[gg][0] *= al[0];
-          ob[gg][1] *= al[1];
-          ow[gg][0] *= al[0] * f;
-          ow[gg][1] *= al[1] * f;
+        for (int gg = 0; gg < G; ++gg) {  // the products' power of two goes with the reference
+          const float2 to = make_float2(fminf(inv[gg].x * up[0], kQdFinest), fminf(inv[gg].y * up[1], kQdFinest));
+          const float f0 = al[0] * (to.x * qd_one_over(inv[gg].x)), f1 = al[1] * (to.y * qd_one_over(inv[gg].y));
+          inv[gg] = to;
+          ob[gg] = mul2(ob[gg], make_float2(al[0], al[1]));
+          ow[gg][0] *= f0;
+          ow[gg][1] *= f1;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            o[gg][i][0] *= al[0] * f;
-            o[gg][i][1] *= al[1] * f;
-            o[gg][i][2] *= al[0] * f;
-            o[gg][i][3] *= al[1] * f;
+            o[gg][i][0] *= f0;
+            o[gg][i][1] *= f1;
+            o[gg][i][2] *= f0;
+            o[gg][i][3] *= f1;
           }
         }
       }
       const float2 off = make_float2(ref[0] == -INFINITY ? 0.f : -ref[0], ref[1] == -INFINITY ? 0.f : -ref[1]);
-      // ---- weights and the product with V's codes
+      // ---- weights p, and p s 2^-E as halves
+      uint32_t wt[kQdBlocks][2][G], most = 0;
+#pragma unroll
+      for (int k = 0; k < kQdBlocks; ++k) {
+        uint32_t sv[2][G];
+        lds_params<G>(tb + k * BB + qparam_off(D, 1, 0, 0) + r0 * 4 * G, sv[0]);
+        lds_params<G>(tb + k * BB + qparam_off(D, 1, 0, 0) + r1 * 4 * G, sv[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {  // rows gq and gq + 8
+          const float2 x = add2(sc[k][e], off);
+          sc[k][e] = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+          l = add2(l, sc[k][e]);
+#pragma unroll
+          for (int gg = 0; gg < G; ++gg) {
+            const float s1 = half_lo(sv[e][gg]), mid = fmaf(8.f, s1, half_hi(sv[e][gg]));
+            ob[gg] = fma2(sc[k][e], make_float2(mid, mid), ob[gg]);
+            const float2 w = mul2(sc[k][e], mul2(inv[gg], make_float2(s1, s1)));
+            wt[k][e][gg] = pack_half2(w.x, w.y);
+            most = __vmaxu2(most, wt[k][e][gg]);
+          }
+        }
+      }
+      if (__any_sync(0xffffffffu, (most & 0xffffu) > kQdMost || most >> 16 > kQdMost)) {  // E follows the largest product
+#pragma unroll
+        for (int gg = 0; gg < G; ++gg) {
+          float2 m = make_float2(0.f, 0.f);
+          float s1[kQdBlocks][2];
+#pragma unroll
+          for (int k = 0; k < kQdBlocks; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              s1[k][e] = half_lo(lds32(tb + k * BB + qparam_off(D, 1, gg, 0) + (e ? r1 : r0) * 4 * G));
+              const float2 w = mul2(sc[k][e], mul2(inv[gg], make_float2(s1[k][e], s1[k][e])));
+              m = make_float2(fmaxf(m.x, w.x), fmaxf(m.y, w.y));
+            }
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1)
+            m = make_float2(fmaxf(m.x, __shfl_xor_sync(0xffffffffu, m.x, off)), fmaxf(m.y, __shfl_xor_sync(0xffffffffu, m.y, off)));
+          // (each head by its own products alone; the factor brings the largest into [2^7, 2^8))
+          const uint32_t h = pack_half2(m.x, m.y);
+          const float f0 = (h & 0xffffu) > kQdMost ? __uint_as_float((261u << 23) - (__float_as_uint(m.x) & 0x7f800000u)) : 1.f;
+          const float f1 = h >> 16 > kQdMost ? __uint_as_float((261u << 23) - (__float_as_uint(m.y) & 0x7f800000u)) : 1.f;
+          inv[gg] = mul2(inv[gg], make_float2(f0, f1));
+          ow[gg][0] *= f0;
+          ow[gg][1] *= f1;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            o[gg][i][0] *= f0;
+            o[gg][i][1] *= f1;
+            o[gg][i][2] *= f0;
+            o[gg][i][3] *= f1;
+          }
+#pragma unroll
+          for (int k = 0; k < kQdBlocks; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 w = mul2(sc[k][e], mul2(inv[gg], make_float2(s1[k][e], s1[k][e])));
+              wt[k][e][gg] = pack_half2(w.x, w.y);
+            }
+        }
+      }
+      // ---- the product with V's codes
 #pragma unroll
       for (int k = 0; k < kQdBlocks; ++k) {
         const uint32_t vb = tb + k * BB;
-        float2 pr[2];  // rows gq and gq + 8
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float2 x = add2(sc[k][e], off);
-          pr[e] = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-          l = add2(l, pr[e]);
-        }
-        uint32_t sv[2][G];
-        lds_params<G>(vb + qparam_off(D, 1, 0, 0) + r0 * 4 * G, sv[0]);
-        lds_params<G>(vb + qparam_off(D, 1, 0, 0) + r1 * 4 * G, sv[1]);
 #pragma unroll
         for (int gg = 0; gg < G; ++gg) {
-          const float inv = __uint_as_float((uint32_t)(254 - E[gg]) << 23);  // 2^(127 - E)
-          uint32_t bw[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float sc1 = half_lo(sv[e][gg]), mid = fmaf(8.f, sc1, half_hi(sv[e][gg])), s1 = sc1 * inv;
-            ob[gg][0] = fmaf(pr[e].x, mid, ob[gg][0]);
-            ob[gg][1] = fmaf(pr[e].y, mid, ob[gg][1]);
-            bw[e] = movtrans(pack_half2(pr[e].x * s1, pr[e].y * s1));
-          }
+          const uint32_t bw[2] = {movtrans(wt[k][0][gg]), movtrans(wt[k][1][gg])};
           mma16816(ow[gg], kOnes, kOnes, kOnes, kOnes, bw[0], bw[1]);
           uint32_t y[4], z[4];
 #pragma unroll
@@ -463,20 +502,21 @@ __global__ void __launch_bounds__(kQdThreads, 1) qpaged_decode_kernel(QdArgs p) 
       l.x += __shfl_xor_sync(0xffffffffu, l.x, off);
       l.y += __shfl_xor_sync(0xffffffffu, l.y, off);
 #pragma unroll
-      for (int gg = 0; gg < G; ++gg)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) ob[gg][e] += __shfl_xor_sync(0xffffffffu, ob[gg][e], off);
+      for (int gg = 0; gg < G; ++gg) {
+        ob[gg].x += __shfl_xor_sync(0xffffffffu, ob[gg].x, off);
+        ob[gg].y += __shfl_xor_sync(0xffffffffu, ob[gg].y, off);
+      }
     }
     float2 v[G][8];  // channels 64 gg + 8 gq + 0 .. 7 of heads 2t, 2t + 1
 #pragma unroll
     for (int gg = 0; gg < G; ++gg) {
-      const float F = E[gg] == 0 ? 0.f : __uint_as_float((uint32_t)E[gg] << 23);
-      const float m0 = fmaf(-8.f * F, ow[gg][0], ob[gg][0]), m1 = fmaf(-8.f * F, ow[gg][1], ob[gg][1]);
+      const float F0 = qd_one_over(inv[gg].x), F1 = qd_one_over(inv[gg].y);  // 2^E
+      const float m0 = fmaf(-8.f * F0, ow[gg][0], ob[gg].x), m1 = fmaf(-8.f * F1, ow[gg][1], ob[gg].y);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float f = F * (i & 1 ? 0x1p20f : 0x1p24f);
-        v[gg][i] = make_float2(fmaf(o[gg][i][0], f, m0), fmaf(o[gg][i][1], f, m1));
-        v[gg][i + 4] = make_float2(fmaf(o[gg][i][2], f, m0), fmaf(o[gg][i][3], f, m1));
+        const float f0 = F0 * (i & 1 ? 0x1p20f : 0x1p24f), f1 = F1 * (i & 1 ? 0x1p20f : 0x1p24f);
+        v[gg][i] = make_float2(fmaf(o[gg][i][0], f0, m0), fmaf(o[gg][i][1], f1, m1));
+        v[gg][i + 4] = make_float2(fmaf(o[gg][i][2], f0, m0), fmaf(o[gg][i][3], f1, m1));
       }
     }
     if (g.j0 == 0 && g.j1 == g.n) {

@@ -213,6 +213,54 @@ def check_decode(c, q, out, lse, lens, hq, window, sinks):
                          f"sequence {b} head {j}")
 
 
+@pytest.mark.parametrize("dtype,d,hkv,B,n,page,rising", [
+    ("bf16", 128, 1, 1, 40, 16, False), ("fp16", 64, 2, 3, 700, 32, False), ("bf16", 64, 2, 64, 4096, 64, True),
+    ("fp16", 128, 2, 60, 4090, 32, True), ("fp16", 128, 1, 2, 9000, 256, False)])
+def test_decode_values_far_from_the_heaviest_tokens(dtype, d, hkv, B, n, page, rising):
+    """Tokens of hardly any weight with values 2^27 times the others': the others keep their bits.  Rising: they have
+    weight when they come, until a later token outweighs them by e^30."""
+    dt, G, n_pages = Q.DT[dtype], 4, -(-n // page)
+    pool = torch.zeros(n_pages, hkv, page * 9 * d // 8, dtype=torch.uint8, device="cuda")
+    p = dkv.dkv_qpaged_layout(pool, B, hkv * G, d, n_pages, dtype=dt)
+    ws = workspace(p)
+    t = torch.arange(n)
+    heavy = n // 2 // 256 * 256 + 32 * 7 + 11 if rising else 7
+    odd = (t // 32 % 8 == 6) & (t % 32 == 5) if rising else (t == 3) | (t == n // 2) | (t == n - 1)
+    score = torch.zeros(n)
+    score[odd] = 0.0 if rising else -30.0
+    score[heavy] = 30.0 if rising else 12.0
+    K, V = randn((n, hkv, d), dt, 1).double(), randn((n, hkv, d), dt, 2).double() * 2.0 ** -13
+    K[:, :, 0] = (score * math.sqrt(d) / 16)[:, None]
+    V[odd] = randn((int(odd.sum()), hkv, d), dt, 3).double() * 2.0 ** 13
+    dkv.dkv_qpaged_append(p, K.to(dt).cuda(), V.to(dt).cuda(), pool, t.cuda(), workspace=ws)
+    table = torch.arange(n_pages, dtype=torch.int32, device="cuda").repeat(B, 1)
+    L = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    q = randn((B, hkv * G, d), dt, 4, 0.1)
+    q[..., 0] = 16.0
+    q = q.cuda()
+    out, lse = dkv.dkv_qpaged_decode(p, q, pool, table, L, workspace=ws)
+    no_fault(ws)
+    back = [torch.zeros(1, hkv, n, d, dtype=torch.float16, device="cuda") for _ in range(2)]
+    dkv.dkv_qpaged_gather(dkv.dkv_qpaged_layout(pool, 1, hkv * G, d, n_pages), pool, table[:1].contiguous(), L[:1] * 0, *back)
+    for h in range(hkv):
+        k, v = (x[0, h].double() for x in back)
+        x = q[:, h * G:(h + 1) * G].double().flatten(0, 1)
+        s = (x @ k.T) / math.sqrt(d)
+        w = s.softmax(-1)
+        # a weight times scale, on codes less 8, is off by 2^-11 of itself and 2^-32 of the row's largest one; 8 scale is
+        # below 3.1 times the largest magnitude (as in exact_rows)
+        part = w * v.abs().amax(-1)
+        ds = R.score_error(d, 3.1 * float((x.abs() @ k.abs().T).max()) / math.sqrt(d))
+        size = 3.1 * (part.sum(-1) + 2.0 ** (11 - 32) * n * part.amax(-1))[:, None]
+        want = w @ v
+        # (half of fp16's smallest step)
+        tol = torch.finfo(dt).eps / 2 * want.abs() + (2.0 ** -11 + 2 * ds) * (1 + 2.0 ** -8) * size + 2.0 ** -25 * (dt == torch.float16)
+        err = (out[:, h * G:(h + 1) * G].double().flatten(0, 1) - want).abs()
+        assert bool((err <= tol).all()), float((err / tol).max())
+        z = s.logsumexp(-1)
+        assert bool(((lse[:, h * G:(h + 1) * G].double().flatten() - z).abs() <= ds + 2.0 ** -22 * z.abs().clamp(min=1.0)).all())
+
+
 # ---------------------------------------------------------------- prefill
 
 PREFILL = [
