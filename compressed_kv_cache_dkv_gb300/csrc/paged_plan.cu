@@ -99,7 +99,9 @@ struct Plan {
       a.table[(int64_t)b * a.max_pages + pages_of(s.lens[b]) + k - s.need[b]] = page((int)k);
     }
     for (int64_t r = tid; r < s.back[a.B]; r += n) {
-      if (n_free + r < a.free_cap) a.free_pages[n_free + r] = returned((int)r);
+      const int pg = returned((int)r);
+      if (pg < 0 || pg >= a.n_pages) raise_error(a.err, DKV_DEVERR_INDEX);
+      if (n_free + r < a.free_cap) a.free_pages[n_free + r] = pg;
       else if (n_free + r < top - s.need[a.B]) raise_error(a.err, DKV_DEVERR_INDEX);  // no room for it in the list
     }
     for (int64_t i = tid * kPlanRows; i < a.rows; i += n * kPlanRows) fill(i);

@@ -594,9 +594,10 @@ DKV_API int dkv_paged_evict(const dkv_paged* p, void* k_pool, void* v_pool, cons
  *   granted     device int32 [B]: tokens granted (0 where news[b] < 0)
  *   new_lens    device int32 [B], may be lens itself: lens + granted, or lens + news[b]
  *   new_n_free  device int32 [1], may be n_free itself
- * A page number outside [0, n_pages) gives slots of -1 and DKV_DEVERR_INDEX; so
- * does a length outside [0, max_pages * page_size] (taken as the nearest
- * bound), and a page given back that the list has no room for.
+ * A page number outside [0, n_pages) gives slots of -1 and DKV_DEVERR_INDEX; one
+ * that is given back raises it then, and goes to the list like any other.  So
+ * do a length outside [0, max_pages * page_size] (taken as the nearest bound)
+ * and a page given back that the list has no room for.
  * Supported: batch <= 4096, page_size 16 to 256 (a power of two), max_pages *
  * page_size <= 1048576, rows <= 2^30.
  */

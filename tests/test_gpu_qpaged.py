@@ -487,6 +487,24 @@ def test_plan_refuses_what_does_not_fit():
     assert dkv.dkv_get_error(ws)[1] == dkv.DKV_DEVERR_INDEX
 
 
+@pytest.mark.parametrize("rows", [8, 9000])
+@pytest.mark.parametrize("bad", [-1, 40, 1 << 30])
+def test_plan_tells_of_pages_given_back_that_do_not_exist(rows, bad):
+    """When they come back, not when another request takes them."""
+    page, width = 16, 4
+    p = dkv.dkv_qpaged(3, 1, 1, 64, page, 40, width, 0, 0, 0, 1 << 20, 1 << 20)
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    ws = torch.zeros(dkv.dkv_paged_plan_workspace_bytes(p), dtype=torch.uint8, device="cuda")
+    lens, news = [64, 40, 10], [-30, 5, 2]     # two pages back, none taken
+    for there in (7, bad):
+        table, free = [[0, 1, 2, there], [4, 5, 6, -9], [8, -9, -9, -9]], [20, 21, -5, -5]
+        want = plan_ref(page, 40, width, lens, news, free, 2, table, rows)
+        F, T = dev(free), dev(table)
+        got = dkv.dkv_paged_plan(p, dev(lens), dev(news), F, dev([2]), T, rows, workspace=ws)
+        assert dkv.dkv_get_error(ws)[1] == (0 if there == 7 else dkv.DKV_DEVERR_INDEX)
+        assert [x.tolist() for x in (*got, T, F)] == list(want)
+
+
 # ---------------------------------------------------------------- places and numbers at their limits
 
 def filled(d, hkv, page, n_pages, dt, seed=1, scale=1.0, head_pad=0):
