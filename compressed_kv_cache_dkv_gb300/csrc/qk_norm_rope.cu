@@ -4,8 +4,10 @@
 //   y = x / sqrt(mean(x^2) + eps) * gain        over the d channels of a head, in fp32
 //   (y_j, y_{j+h}) turned by position * f_j     for j < h, rounded once, at the end
 //
-// A turn is taken as a 64-bit fraction of the circle: position * turn_j modulo 2^64 is exact however far the
-// position is, its upper 32 bits are the angle to 2^-32 of a circle, and sincospif takes it from there.
+// A turn is taken as a 64-bit fraction of the circle: position * turn_j modulo 2^64 is exact however far the position
+// is.  turn_j is not: it comes of a double, off by 2^-54 of a circle for a frequency up to 1 (three roundings, of the
+// power, of 1 / 2 pi and of their product, of 2^-53 each, and those of the exponent: (3 + ln 1 / f) f / 2 pi of 2^-53), so
+// that position 2^31 is off by 2^-23.  The upper 32 bits go to sincospif as fp32: 2^-26 of a circle more.
 //
 // d / 8 lanes share a row, eight channels (16 bytes) each; the partner channels of the rotation are a fixed number of
 // lanes away, and come over as they were loaded.  Gains are folded into the cosines and sines, the norm's factor

@@ -615,7 +615,8 @@ DKV_API int dkv_paged_plan(int32_t batch, int32_t page_size, int32_t n_pages, in
  *   y_j, y_{j+h} = y_j cos - y_{j+h} sin, y_{j+h} cos + y_j sin    for j < h = rope_dims / 2,
  * the angle position * inv_freq[j], with inv_freq[j] = rope_base^(-2j / rope_dims)
  * where the caller gives none; channels from rope_dims on are not rotated.
- * Squares are added in fp32 and angles held to 2^-32 of a circle at any position.
+ * Squares are added in fp32.  An angle is off by less than 2^-25 of a circle (it ends in
+ * fp32), and by position * 2^-54 * max(1, inv_freq[j]) of one (the frequency is a double).
  *   q, k        device [rows][heads][head_dim] under strides (token, head; batch is
  *               unused): views of a fused projection's output are taken as they are
  *   q_gain, k_gain   optional device [head_dim] in the rows' type (NULL: 1)

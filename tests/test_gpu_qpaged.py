@@ -3,6 +3,7 @@ norm and rotation, append and gather, decode and prefill; types, head layouts, p
 windows, sinks, ragged batches; slots that nothing may look at hold NaN, unneeded page-table entries numbers out of
 range."""
 import math
+from fractions import Fraction
 
 import pytest
 import torch
@@ -376,6 +377,40 @@ def test_rotation_by_given_frequencies_and_into_pages():
             if 0 <= s < 4 * page:
                 expect[s // page, :, s % page] = rows_of[i]
         assert torch.equal(pool.cpu(), expect)
+
+
+PI = Fraction(314159265358979323846264338327950288419716939937510582097494, 10 ** 59)
+
+
+@pytest.mark.parametrize("base", [None, 65536.0])
+def test_angles_are_as_exact_as_the_header_says(base):
+    """Pairs that turn to almost nothing, so that the angle's error is what is left; the angle itself in whole numbers."""
+    h, d = 32, 64
+    freq = [65536.0 ** (-j / h) if base else [1.0, 0.7310585786300049, 1e-3, 1.7e-6, 3.7, 1 / 3, 0.9999999, 20.0][j % 8] / (1 + j // 8) for j in range(h)]
+    keep = [j for j in range(h) if not base or j % 2 == 0]    # (frequencies that are powers of two: their definition is exact)
+    pos = [0, 1, 1000, 65535, (1 << 20) - 1, (1 << 24) + 1, (1 << 30) + 12345, (1 << 31) - 1]
+    x, want, tol = torch.zeros(len(pos), 1, d), torch.zeros(len(pos), h, dtype=torch.float64), torch.zeros(len(pos), h, dtype=torch.float64)
+    n = torch.arange(1, 2049).double()
+    for i, p in enumerate(pos):
+        for j in keep:
+            turns = Fraction(p) * Fraction(freq[j]) / (2 * PI)
+            a = 2 * math.pi * float(turns - math.floor(turns))
+            c, s = math.cos(a), math.sin(a)
+            m = (n * (s / c if abs(s) < abs(c) else c / s)).round()
+            r = (m * c - n * s if abs(s) < abs(c) else n * c - m * s).abs()
+            at = int(r.argmin())
+            lo, hi = (float(m[at]), float(n[at])) if abs(s) < abs(c) else (float(n[at]), float(m[at]))
+            x[i, 0, j], x[i, 0, j + h] = lo, hi
+            want[i, j] = lo * c - hi * s
+            # fp32: cosine and sine off by 2^-23 (two units), a product and a sum by 2^-24 of what they give
+            tol[i, j] = 2.0 ** -11 * abs(want[i, j]) + 2.0 ** -25 + (abs(lo) + abs(hi)) * (2.0 ** -23 + 2.0 ** -24 + 2.0 ** -24) + \
+                2 * math.pi * math.hypot(lo, hi) * (2.0 ** -25 + p * 2.0 ** -54 * max(1.0, freq[j]))
+    x = x.half().cuda()
+    q, k = dkv.dkv_qk_norm_rope(x, x, torch.tensor(pos, dtype=torch.int32, device="cuda"), d, rope_base=base or 1e4,
+                                inv_freq=None if base else freq, eps=None)
+    for y in (q, k):
+        err = (y[:, 0, :h].double().cpu() - want)[:, keep].abs()
+        assert bool((err <= tol[:, keep]).all()), float((err / tol[:, keep]).max())
 
 
 # ---------------------------------------------------------------- pages and slots
