@@ -413,6 +413,26 @@ def test_angles_are_as_exact_as_the_header_says(base):
         assert bool((err <= tol[:, keep]).all()), float((err / tol[:, keep]).max())
 
 
+def test_keys_into_pages_alone():
+    """The C call without k_out: queries out, keys and values into pages only, the same bits as with it."""
+    dt, hq, hkv, d, page, rows = torch.float16, 8, 4, 64, 16, 70
+    q, k, v = (randn((rows, n, d), dt, s).cuda() for s, n in ((1, hq), (2, hkv), (3, hkv)))
+    pos, slots = torch.arange(rows, dtype=torch.int32, device="cuda"), torch.randperm(80, generator=torch.Generator().manual_seed(4))[:rows].cuda()
+    pools = [[torch.full((5, hkv, page, d), 5.0, dtype=dt, device="cuda") for _ in range(2)] for _ in range(2)]
+    p = dkv.dkv_paged_layout(pools[0][0], 1, hq, 5)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    want, _ = dkv.dkv_qk_norm_rope(q, k, pos, d, p=p, v=v, k_pages=pools[0][0], v_pages=pools[0][1], slots=slots, workspace=ws)
+    out = torch.zeros_like(want)
+    r = dkv.dkv_rotate(rows, hq, hkv, d, dkv.DKV_FP16, 1, d, 1e-6, 1e4, None)
+    qs, ks = dkv.dkv_strides(0, d, hq * d), dkv.dkv_strides(0, d, hkv * d)
+    st = dkv.lib().dkv_qk_norm_rope(r, q.data_ptr(), qs, k.data_ptr(), ks, None, None, pos.data_ptr(), out.data_ptr(), qs, None, None, p,
+                                    v.data_ptr(), ks, slots.data_ptr(), pools[1][0].data_ptr(), pools[1][1].data_ptr(), ws.data_ptr(),
+                                    ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert st == dkv.DKV_OK
+    no_fault(ws)
+    assert torch.equal(out, want) and torch.equal(pools[1][0], pools[0][0]) and torch.equal(pools[1][1], pools[0][1])
+
+
 # ---------------------------------------------------------------- pages and slots
 
 def plan_ref(page, n_pages, width, lens, news, free, n_free, table, rows):
@@ -520,6 +540,26 @@ def test_plan_refuses_what_does_not_fit():
     got = dkv.dkv_paged_plan(p, dev([16, 16, 0, 0, 0]), dev([-16, -1, 0, 0, 0]), F, dev([1]), T, 4, workspace=ws)
     assert int(got[5]) == 1 and F.tolist() == [20] and got[4].tolist() == [0, 15, 0, 0, 0]
     assert dkv.dkv_get_error(ws)[1] == dkv.DKV_DEVERR_INDEX
+
+
+@pytest.mark.parametrize("B,page,width,most,rows,fill,shift", [
+    (256, 16, 30, 200, 9001, 0.7, 0), (7, 64, 200, 9000, 30003, 1.0, 0), (100, 32, 40, 500, 20000, 0.5, 1),  # few requests, two grids
+    (40, 16, 12, 60, 1000, 1.0, 1), (64, 128, 9, 300, 8192, 0.8, 1), (1000, 16, 8, 60, 12345, 0.9, 1)])      # rows off 16 bytes
+def test_plan_of_few_requests_and_of_rows_anywhere(B, page, width, most, rows, fill, shift):
+    lens, news, free, n_free, n_pages, table = plan_case(B, page, width, B + 1, most, fill)
+    want = plan_ref(page, n_pages, width, lens, news, free, n_free, table, rows)
+    p = dkv.dkv_qpaged(B, 1, 1, 64, page, n_pages, width, 0, 0, 0, 1 << 20, 1 << 20)
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    L, F, N, T = dev(lens), dev(free), dev([n_free]), dev(table)
+    ws = torch.zeros(dkv.dkv_paged_plan_workspace_bytes(p), dtype=torch.uint8, device="cuda")
+    around = [torch.full((rows + 8,), 77, dtype=t, device="cuda") for t in (torch.int64, torch.int32)]
+    slots, positions = (x[shift:shift + rows] for x in around)
+    got = dkv.dkv_paged_plan(p, L, dev(news), F, N, T, rows, slots=slots, positions=positions, workspace=ws)
+    no_fault(ws)
+    for name, x, y in zip(("slots", "positions", "starts", "granted", "lens", "n_free", "table", "free"), (*got, T, F), want):
+        assert x.tolist() == y, name
+    for x in around:
+        assert bool((x[:shift] == 77).all()) and bool((x[shift + rows:] == 77).all())
 
 
 @pytest.mark.parametrize("rows", [8, 9000])
@@ -1044,3 +1084,31 @@ def test_rows_go_on_to_the_compressed_cache():
     exact, _ = dkv.dkv_qpaged_decode(dkv.dkv_qpaged_layout(pool, 1, 4, d, 14), q, pool, torch.arange(14, dtype=torch.int32, device="cuda")[None].contiguous(),
                                      torch.tensor([n], dtype=torch.int32, device="cuda"))
     assert bool(torch.isfinite(out).all()) and tuple(out.shape) == (1, 4, d) and tuple(exact.shape) == (1, 4, d)
+
+
+def test_rows_that_go_on_are_the_rows_that_went_in():
+    """Gathered keys and values are the quantised rows of their tokens and heads, the compressed cache made of them is the
+    one made of those rows, and the attention over the pages is theirs."""
+    d, hkv, page, n, dt = 64, 2, 64, 3 * 256 + 100, torch.float16
+    n_pages = -(-n // page)
+    pool = torch.zeros(n_pages, hkv, page * 9 * d // 8, dtype=torch.uint8, device="cuda")
+    p = dkv.dkv_qpaged_layout(pool, 1, 4, d, n_pages)
+    rows = [randn((n, hkv, d), dt, s) for s in (1, 2)]
+    order = torch.randperm(n_pages, generator=torch.Generator().manual_seed(3))
+    t = torch.arange(n)
+    dkv.dkv_qpaged_append(p, *(x.cuda() for x in rows), pool, (order[t // page] * page + t % page).cuda())
+    table, zero = order.int()[None].cuda(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    back = [torch.zeros(1, hkv, n, d, dtype=dt, device="cuda") for _ in range(2)]
+    dkv.dkv_qpaged_gather(p, pool, table, zero, *back)
+    held = [Q.values(*Q.quantise(x.transpose(0, 1).double())) for x in rows]
+    for x, y in zip(back, held):
+        assert torch.equal(x[0].double().cpu(), y)
+    q = randn((1, 4, d), dt, 3).cuda()
+    desc = dkv.dkv_layout(1, 4, hkv, d, 3, 100, 16, 32)
+    got, want = (dkv.dkv_decode_attend(desc, q, dkv.dkv_compress_layout(desc, *kv), 3)
+                 for kv in (back, [x.to(dt)[None].contiguous().cuda() for x in held]))
+    assert all(torch.equal(x, y) for x, y in zip(got, want)) and bool(torch.isfinite(got[0]).all())
+    out, lse = dkv.dkv_qpaged_decode(p, q, pool, table, zero + n)
+    for h in range(hkv):
+        at = slice(2 * h, 2 * h + 2)
+        near(out[0, at], lse[0, at], exact_rows(q[0, at].double(), *(x[h].cuda() for x in held)), dt)
