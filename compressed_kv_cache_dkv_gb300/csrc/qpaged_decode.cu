@@ -10,11 +10,13 @@
 //   S = C_K q    mma.sync m16n8k16, tokens in M, heads in N; a token's 32 bytes a group are a lane's operand as
 //                they lie, with q's channels in the same order
 //   o = C_V^T w  channels in M; two tokens' words interleaved by byte permutes give the pairs along k
-// q is brought to at most 2^15 by a power of two, so that it is an fp16 operand whatever its type (channels above 2^-25
+// q is brought to at most 2^15 by a power of two, so that it is an fp16 operand whatever its type (channels above 2^-24
 // of the largest without loss).  w = p s 2^-E, with a running power of two E for each head and group, is rounded once to
-// fp16 (relative error 2^-11, or 2^-32 of the head's largest product).  That rounding falls on codes less 8 (the sum of the rounded weights, times 8, goes
-// off again, and the bias is b + 8 s), so that it is one of about the size of the values, as in the 16-bit prefill; a
-// second fp16 value for what the first leaves took 9 % longer (16 of 64k: 77.8 us, 71.6 without).
+// fp16 (relative error 2^-11, or 2^-32 of the head's largest product).  That rounding falls on codes less 8 (the sum of
+// the rounded weights, times 8, goes off again, and the bias is b + 8 s), so that it is one of about the size of the
+// values, as in the 16-bit prefill.  One value is a choice: a second one for what the first leaves took 9 % longer (16
+// of 64k: 77.8 us, 71.6 without), and with one the outputs are as far from the definition (2.1e-4 in fp16, 1.7e-3 in
+// bf16, root mean square) as a plain form's with fp32 weights.
 //
 // The visible tokens of a sequence are cut into 32-token tiles; the tiles of all (sequence, KV head) units in a row
 // are dealt out evenly, to CTAs and in them to warps.  A warp walks its run of tiles unit by unit with stages, copies
@@ -25,14 +27,14 @@
 // each, and the CTA that is last to leave one merges them in run order, so that equal calls give equal bits.
 //
 // Bound: memory at 9/8 d bytes a token and KV head; right beside it the instructions that cut codes out of words and
-// scale weights (290 a warp for 16 tokens; 0.56 of the issue slots, 0.5 of the integer pipe).  What it took, on 16
+// scale weights (317 a warp for 16 tokens, start and end among them; 0.54 of the issue slots, 0.52 of the integer pipe).  What it took, on 16
 // sequences of 64k tokens, 2 KV heads, d 128 (302 MB, floor 45 us): one producer warp with a page look-up for each
 // tile 157 us; a look-up for a batch of tiles 96; every warp its own tiles and copies, sixteen warps 78; one fp16
 // weight, biases by a product, packed arithmetic 72; one merge a CTA, the join in the same grid 68.  The loop
 // streams at 5.8 TB/s (0.87 of the measured copy rate); 4 us at the start (lengths, then the page table, then
 // the first copies) and 6 at the end (uneven finish, merge, join) are what is left.  64 sequences of 300 to 8000
-// under a window of 4096, 8 KV heads, pages of 16 (237 MB): 65 us.  One of 1000 tokens: 9.9 us in a graph.  The join
-// of many records with all loads in flight: one sequence of 65536 tokens, 2 KV heads 19.7 us (23.8 with eight at a
+// under a window of 4096, 8 KV heads, pages of 16 (237 MB): 65 us.  One of 1000 tokens: 11.3 us in a graph.  The join
+// of many records with all loads in flight: one sequence of 65536 tokens, 2 KV heads 18.9 us (23.8 with eight at a
 // time, merged as they came).
 #include "paged_tc.cuh"
 #include "qpaged.cuh"
@@ -59,7 +61,10 @@ constexpr float kQdShift = 7.f, kQdSlack = 8.f, kQdLarge = 0x1p20f;
 // A weight times its token's scale is held times 2^-E as a half.  E, of each head and group of channels, lies 7 below a
 // product's exponent, goes with the reference, and moves when a product is above 2^15 (kQdMost, a half's bits).  It follows
 // the products, not the scales: with E from the largest scale a token of no weight with values 2^27 times the others'
-// left these 4 bits.  -E goes up to 96: products below 2^-89, a weight being 2^7 at least, are off by 2^-121.
+// left these 4 bits.  A piece's first tile always moves it: 0.3 us of a short call (one of 1000 tokens, 12 / 2 heads, in a
+// graph 11.3 us, 11.0 with the scales'), 49.7 us for 512 sequences of 10 to 200 tokens, 8 KV heads (46.9), nothing of long
+// ones.  A start by the first tile's largest scale, checked against the products: 48.9 of the 512, but 66.3 us for 16 of
+// 64k, 65.8 without.  -E goes up to 96: products below 2^-89, a weight being 2^7 at least, are off by 2^-121.
 constexpr uint32_t kQdMost = 0x7800u;
 constexpr float kQdFinest = 0x1p96f;
 __device__ inline float qd_one_over(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }  // x a power of two

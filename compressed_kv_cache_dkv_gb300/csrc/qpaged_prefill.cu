@@ -19,7 +19,9 @@
 // P = 2^(score - ref) is rounded once to fp16.  A row's reference lies kQpShift below a maximum and moves, with O
 // rescaled in tensor memory, only when weights leave fp16's range: when a tile's sum of them exceeds 2^15, which is
 // found without a maximum.  So P is at most 2^15, weights down to e^-14 of the largest keep 11 bits and smaller ones
-// are off by 2^-32 of it at most.
+// are off by 2^-32 of it at most.  One fp16 value is a choice: an operand has 16 bits, and a second P V product for what
+// the first leaves would be 512 more of a tile's 1312 cycles of products; fp16 outputs are 2.3e-4 from the definition (root
+// mean square, the prompt under a window below), a plain form's with fp32 weights 2.1e-4, bf16 ones both 1.7e-3.
 //
 // Values in the cache are finite.  What lies in slots that no row of the CTA sees may be anything and counts as
 // zeros; a weight of 0 takes care of what only some rows see.
@@ -37,14 +39,15 @@
 // control): warp 11 asks for it, works out its rows and tiles for all warps, and the next tiles' bytes and values are
 // made while the last rows leave.  That leaves 6.6 us from a unit's last tile to the next one's first (product's end
 // 0.7, output 2.3, next unit 0.4, queries sent for 1.1, there 0.65, converted 0.8 to 1.4, first scores 0.65): the 8k
-// causal prompt 446 us in a graph (465 without), 16k under a window of 1024 139 (147), 8 prompts of 700 to 4096 507
+// causal prompt 446 us in a graph (465 without), 16k under a window of 1024 141 (147), 8 prompts of 700 to 4096 507
 // (537).  A place is taken when the loading warp has sent off the unit's last tile: taken at a unit's start, places
 // wait for busy CTAs while others run out (8k causal 465).  The second group's start put off by three tiles, to have
-// the groups' ends apart, cost 2 us.  Edge tiles without a new maximum in a third function: 498 for the 8 prompts, and 142
+// the groups' ends apart, cost 2 us.  A group that falls idle in the next unit waits for its rows there; a
+// wait in every unit cost the windowed prompt 6 us.  Edge tiles without a new maximum in a third function: 498 for the 8 prompts, and 142
 // under the window.
 //
 // Measured (d 128): a prompt of 8191, 32 query and 8 KV heads, pages of 16: 451 us, 1.22 PFLOP/s.  One of 16384
-// under a window of 1024, 12 heads: 143 us.  32 queries over 300 to 2000 keys, d 64: 16.4 us in a graph.
+// under a window of 1024, 12 heads: 144 us.  32 queries over 300 to 2000 keys, d 64: 16.4 us in a graph.
 #include "paged_tc.cuh"
 #include "qpaged.cuh"
 

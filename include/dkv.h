@@ -673,10 +673,13 @@ DKV_API int dkv_qk_norm_rope(const dkv_rotate* r, const void* q, const dkv_strid
  * of the 16-bit paged cache; a page out of range is read as one of zeros.  Scores,
  * statistics and sums are fp32.  In front of the product with V a weight (decode: times
  * its token's scale, in each group of 64 channels) is one fp16 value: its relative error is
- * at most 2^-11, and those below 2^-21 of the row's largest are off by up to 2^-32 of it.  Queries are brought
- * into fp16's range by a power of two for each row and head (prefill: those in bf16);
- * channels below 2^-25 of the row's largest lose bits.  Cache values are expected to be finite (append writes no
- * others) in the slots that a query sees; those that none sees may be anything.
+ * at most 2^-11, and those below 2^-21 of the row's largest are off by up to 2^-32 of it.
+ * Queries are brought into fp16's range by a power of two for each row and head (prefill:
+ * those in bf16); channels below 2^-24 of the row's largest lose bits.  Cache values are
+ * expected to be finite (append writes no others) in the slots that a query sees; those that
+ * none sees may be anything.  Equal calls give equal bits; a sequence's bits may differ with
+ * the others that it is called with, which decide where its keys are cut and when the rows of
+ * a warp move their references.
  */
 typedef struct dkv_qpaged {
   int32_t batch;         /* sequences B */
